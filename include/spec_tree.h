@@ -81,6 +81,8 @@ enum {
                                    fp16, so a V value beyond fp16's range (|v| > 65504) among
                                    the keys the row sees (cache rows below kv_len, its tree
                                    ancestors) gives this, as do non-finite inputs there. */
+#define SPEC_DEV_BADPAGE  0x40u /* a page table entry that was needed is outside [0, n_pages) */
+#define SPEC_DEV_BADTOK   0x80u /* a drafted token is outside [0, V) (it is refused) */
 
 enum { SPEC_IO_F32 = 0, SPEC_IO_BF16 = 1 };
 
@@ -474,6 +476,145 @@ int attn_tree_verify_noalloc(const spec_cfg *cfg, const spec_tree *tree, const v
                              const void *k_tree, const void *v_tree, const void *k_cache,
                              const void *v_cache, const int32_t *kv_len, void *o,
                              uint32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------------
+ * Chain drafts over a paged cache: the serving step beside the tree step.  A
+ * step of B requests appends the rows of its new tokens (the pending bonus
+ * token and any drafts) to a paged key/value cache (kv_page_append), attends
+ * from them (attn_decode_paged), and verifies the drafts against the target's
+ * logits (draft_verify_sampled), which advances kv_len over what was kept;
+ * rows of refused drafts are written over by the next step.
+ */
+enum {
+    SPEC_KV_IO = 0,      /* cache rows in the I/O type */
+    SPEC_KV_E4M3 = 1     /* cache rows as e4m3 codes with one fp32 scale per row and head */
+};
+
+#define SPEC_MIN_PAGE 16
+#define SPEC_MAX_PAGE 1024
+#define SPEC_MAX_PAGED_B 4096
+
+/* Shape of the paged calls.  Limits (else ST_EINVAL): 1 <= B <= 4096;
+ * 1 <= T <= 2^20 (attn_decode_paged: T <= 128); Hq % Hkv == 0; D in {64, 128};
+ * page a power of two in [16, 1024]; n_pages, max_pages >= 1;
+ * max_pages * page <= 2^30; B * max(Hq, Hkv) <= 2^24. */
+typedef struct spec_paged_cfg {
+    int32_t B;               /* requests */
+    int32_t T;               /* rows of the new-token tensors per request */
+    int32_t Hq, Hkv, D;
+    int32_t page;            /* cache rows per page */
+    int32_t n_pages;         /* pages in the pool */
+    int32_t max_pages;       /* page table columns per request */
+    int32_t io_dtype;        /* SPEC_IO_BF16 or SPEC_IO_F32 */
+    int32_t kv_dtype;        /* SPEC_KV_IO or SPEC_KV_E4M3 */
+} spec_paged_cfg;
+
+/* A paged cache.  Row r of request b lives in page page_table[b][r / page],
+ * slot r % page.  Pages are head-major, so that the rows of one head in one
+ * page are contiguous.  Requests may share pages that none of them appends to. */
+typedef struct spec_paged_kv {
+    void *k_pages, *v_pages;    /* [n_pages][Hkv][page][D] io, or uint8 e4m3 codes */
+    float *k_scale, *v_scale;   /* [n_pages][Hkv][page] (SPEC_KV_E4M3; else ignored) */
+    const int32_t *page_table;  /* [B][max_pages] */
+    const int32_t *kv_len;      /* [B] committed rows */
+} spec_paged_kv;
+
+/* Bytes of workspace of the paged calls (0 on an invalid cfg), zero-filled once
+ * like the tree calls' workspace, which it does not replace.  num_sms: the SM
+ * count to lay it out for; 0 asks the current device (0 when there is none). */
+size_t spec_paged_workspace_bytes(const spec_paged_cfg *cfg, int num_sms);
+
+/*
+ * kv_page_append -- write the new tokens' rows behind the committed ones.
+ * Row i < n_new[b] of k_new / v_new goes to cache row kv_len[b] + i.  With
+ * SPEC_KV_E4M3 each row x of one head becomes
+ *   scale = max(amax |x| / 448, 2^-100)  (1 for a row of zeros),
+ *   code  = e4m3(x / scale)   (round to nearest even),
+ * and stands for code * scale; a row with a non-finite value gets a NaN scale
+ * and NaN codes.  kv_len is not changed.
+ *   k_new, v_new [B][T][Hkv][D] io     n_new  NULL (T each) or [B], in [0, T]
+ *          (else clamped, SPEC_DEV_BADREQ)
+ * A request with kv_len < 0 or kv_len + n_new > max_pages * page is left
+ * unwritten (SPEC_DEV_OVERFLOW); a row whose page is outside the pool too
+ * (SPEC_DEV_BADPAGE).  Two rows of one call must not share a slot.
+ */
+int kv_page_append(const spec_paged_cfg *cfg, const spec_paged_kv *kv, const void *k_new,
+                   const void *v_new, const int32_t *n_new, void *ws, void *stream);
+
+/*
+ * kv_page_read -- the committed rows as the contiguous cache attn_tree_verify
+ * takes: row r < kv_len[b] of k_out / v_out is the value cache row r stands
+ * for (code * scale in fp32, rounded once to io); later rows are left as they
+ * were, as are rows whose page is outside the pool (SPEC_DEV_BADPAGE).
+ * kv_len outside [0, min(Lmax, max_pages * page)] is clamped
+ * (SPEC_DEV_OVERFLOW).  cfg->T is not used.
+ *   k_out, v_out [B][Lmax][Hkv][D] io, 1 <= Lmax <= 2^30
+ */
+int kv_page_read(const spec_paged_cfg *cfg, const spec_paged_kv *kv, int Lmax, void *k_out,
+                 void *v_out, void *ws, void *stream);
+
+/*
+ * attn_decode_paged -- attention of the new tokens over the paged cache (one
+ * layer), after their rows were appended.  Row i < n_new[b], q-head h (kv-head
+ * h / (Hq/Hkv)) sees cache rows [0, kv_len[b] + i]:
+ * o = softmax(q K^T / sqrt(D)) V, fp32 accumulation; rows i >= n_new[b] get 0.
+ * Cache rows a row does not see never reach it, whatever they hold.  Rows in
+ * pages outside the pool are not seen (SPEC_DEV_BADPAGE); kv_len outside
+ * [0, max_pages * page - n_new[b]] is clamped to the table
+ * (SPEC_DEV_OVERFLOW); a row that sees nothing gets 0; an output that is not
+ * finite raises SPEC_DEV_RANGE.
+ *   q, o [B][T][Hq][D] io     n_new as for kv_page_append     T <= 128
+ */
+int attn_decode_paged(const spec_paged_cfg *cfg, const spec_paged_kv *kv, const void *q,
+                      const int32_t *n_new, void *o, void *ws, void *stream);
+
+/* Shape of the chain verification: N drafts per request in [0, 127], V >= 1,
+ * 1 <= B <= 65535, temperature > 0 and finite, reserved 0 (else ST_EINVAL). */
+typedef struct spec_draft_cfg {
+    int32_t B, N, V;
+    int32_t io_dtype;        /* of the logits */
+    float temperature;
+    uint32_t reserved;
+} spec_draft_cfg;
+
+typedef struct spec_draft_out {
+    int32_t *accept_len;     /* [B] tau in [1, n_draft + 1]: drafts kept + 1 */
+    int32_t *out_tok;        /* [B][N+1] kept drafts, then the drawn token, -1 beyond tau */
+    float *target_prob;      /* [B][N] p_i of draft i (0 beyond n_draft); NULL when N = 0 */
+} spec_draft_out;
+
+/* Workspace of draft_verify_sampled, as spec_paged_workspace_bytes. */
+size_t spec_draft_workspace_bytes(const spec_draft_cfg *cfg, int num_sms);
+
+/*
+ * draft_verify_sampled -- verification of a drafted chain from given random
+ * numbers.  Speculative-decoding tutorial (mlqm.cn), section 2.3: a draft x
+ * with draft probability q(x) is kept with probability min(1, p(x)/q(x)),
+ * else a token is drawn from max(0, p - q) renormalised; the output follows
+ * the target's p exactly.
+ *   p_i = softmax(logits[b][i][:] / temperature), i = 0..n_draft[b];
+ *   draft i is kept while u[b][i] q_i(x_i) < p_i(x_i) (i = 0, 1, ... in turn);
+ *   at the first draft j that is not kept the token is
+ *     argmax_v max(0, p_j(v) - q_j(v)) / e[b][v],
+ *   with every draft kept argmax_v p_n(v) / e[b][v]  (lowest v on ties; where
+ *   p_j <= q_j everywhere in fp32, p_j / e decides).
+ * With u uniform on [0, 1) and e standard exponential, independent, the argmax
+ * draws v with its weight's share.  N = 0 is plain sampling of one token.
+ *   draft_tok [B][N] int32, draft_prob NULL (drafts are point masses, q = 1) or
+ *   [B][N][V] float >= 0, u [B][N] float (these may be NULL when N = 0);
+ *   n_draft NULL (N each) or [B], in [0, N] (else clamped, SPEC_DEV_BADREQ);
+ *   logits [B][N+1][V] io (rows beyond n_draft are not read);
+ *   e [B][V] float > 0;
+ *   kv_len, root_tok  NULL, or [B]: advanced by tau / replaced by the drawn token.
+ * A draft outside [0, V) is refused (SPEC_DEV_BADTOK).  A row whose
+ * probabilities are not finite (NaN or +inf logits, or all -inf) refuses its
+ * draft and draws token 0 (SPEC_DEV_BADLOGIT).  Decisions within fp32 rounding
+ * of a tie can differ from a float64 evaluation.
+ */
+int draft_verify_sampled(const spec_draft_cfg *cfg, const int32_t *draft_tok,
+                         const int32_t *n_draft, const float *draft_prob, const void *logits,
+                         const float *u, const float *e, const spec_draft_out *out,
+                         int32_t *kv_len, int32_t *root_tok, void *ws, void *stream);
 
 #ifdef __cplusplus
 }

@@ -22,15 +22,20 @@ ST_OK, ST_EINVAL, ST_EUNSUPPORTED, ST_ECUDA, ST_EOVERFLOW, ST_TIMEOUT, ST_ESCRAT
 NOALLOC_SCRATCH_BYTES = 8 << 20
 SPEC_DEV_OVERFLOW, SPEC_DEV_BADLAT, SPEC_DEV_TIMEOUT, SPEC_DEV_BADREQ = 0x1, 0x2, 0x4, 0x8
 SPEC_DEV_BADLOGIT, SPEC_DEV_RANGE = 0x10, 0x20
+SPEC_DEV_BADPAGE, SPEC_DEV_BADTOK = 0x40, 0x80
 SPEC_IO_F32, SPEC_IO_BF16 = 0, 1
+SPEC_KV_IO, SPEC_KV_E4M3 = 0, 1
 EXPORTS = ("spec_workspace_bytes", "spec_workspace_bytes_for_sms", "spec_tree_build", "gdn_tree_verify", "attn_tree_verify",
            "accept_and_commit", "spec_verify_step", "spec_status_read", "spec_status_clear",
            "spec_status_string", "spec_abi_version", "attn_tree_verify_noalloc",
            "spec_wait_probe", "spec_step_launches", "spec_tree_build_ragged",
            "spec_verify_step_ragged", "spec_tree_build_markov", "spec_verify_step_markov",
            "accept_and_commit_sampled", "spec_verify_step_sampled",
-           "spec_verify_step_persistent", "spec_step_launches_persistent")
+           "spec_verify_step_persistent", "spec_step_launches_persistent",
+           "spec_paged_workspace_bytes", "kv_page_append", "kv_page_read", "attn_decode_paged",
+           "spec_draft_workspace_bytes", "draft_verify_sampled")
 SAMPLE_CHUNK = 4096
+_STATUS_BYTES = 256          # the status word and its reserve, at the head of a workspace
 
 _lock = threading.Lock()
 _lib = None
@@ -70,6 +75,25 @@ class SpecAccept(ctypes.Structure):
 class SpecSampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("reserved", ctypes.c_uint32),
                 ("seed", ctypes.c_uint64)]
+
+
+class SpecPagedCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "B", "T", "Hq", "Hkv", "D", "page", "n_pages", "max_pages", "io_dtype", "kv_dtype")]
+
+
+class SpecPagedKV(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k_pages", "v_pages", "k_scale", "v_scale", "page_table", "kv_len")]
+
+
+class SpecDraftCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "N", "V", "io_dtype")] + [
+        ("temperature", ctypes.c_float), ("reserved", ctypes.c_uint32)]
+
+
+class SpecDraftOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("accept_len", "out_tok", "target_prob")]
 
 
 def load(path: Optional[str] = None) -> ctypes.CDLL:
@@ -128,6 +152,20 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
             lib.attn_tree_verify_noalloc.argtypes = [cfgp, ctypes.POINTER(SpecTree)] + [vp] * 9
             lib.spec_wait_probe.argtypes = [ctypes.c_uint32, ctypes.c_int, vp, vp]
             lib.spec_step_launches.argtypes = [cfgp]
+            pcfgp, pkvp = ctypes.POINTER(SpecPagedCfg), ctypes.POINTER(SpecPagedKV)
+            dcfgp = ctypes.POINTER(SpecDraftCfg)
+            lib.spec_paged_workspace_bytes.argtypes = [pcfgp, ctypes.c_int]
+            lib.spec_paged_workspace_bytes.restype = ctypes.c_size_t
+            lib.spec_draft_workspace_bytes.argtypes = [dcfgp, ctypes.c_int]
+            lib.spec_draft_workspace_bytes.restype = ctypes.c_size_t
+            lib.kv_page_append.argtypes = [pcfgp, pkvp] + [vp] * 5
+            lib.kv_page_read.argtypes = [pcfgp, pkvp, ctypes.c_int] + [vp] * 4
+            lib.attn_decode_paged.argtypes = [pcfgp, pkvp] + [vp] * 5
+            lib.draft_verify_sampled.argtypes = [dcfgp] + [vp] * 6 + [
+                ctypes.POINTER(SpecDraftOut)] + [vp] * 4
+            for n in ("kv_page_append", "kv_page_read", "attn_decode_paged",
+                      "draft_verify_sampled"):
+                getattr(lib, n).restype = ctypes.c_int
             for n in ("spec_tree_build", "gdn_tree_verify", "attn_tree_verify",
                       "attn_tree_verify_noalloc", "spec_wait_probe", "spec_step_launches",
                       "spec_tree_build_ragged", "spec_verify_step_ragged", "spec_tree_build_markov",
@@ -436,3 +474,206 @@ def spec_wait_probe(limit_us: int, satisfy: bool, ws, stream=None):
 
 def spec_status_clear(ws, stream=None):
     _check("spec_status_clear", load().spec_status_clear(_ptr(ws, name="ws"), _stream(stream)))
+
+
+# ------------------------------------------- paged cache, decode, drafted chain
+
+_IO = {"bf16": (SPEC_IO_BF16, torch.bfloat16), "f32": (SPEC_IO_F32, torch.float32)}
+_KV = {"io": SPEC_KV_IO, "e4m3": SPEC_KV_E4M3}
+
+
+def paged_cfg(B, T, Hq, Hkv, D, page, n_pages, max_pages, io="bf16", kv="io") -> SpecPagedCfg:
+    """Shape of the paged calls; io "bf16" or "f32", kv "io" or "e4m3"."""
+    return SpecPagedCfg(B, T, Hq, Hkv, D, page, n_pages, max_pages, _IO[io][0], _KV[kv])
+
+
+def draft_cfg(B, N, V, io="bf16", temperature=1.0) -> SpecDraftCfg:
+    """Shape of draft_verify_sampled; io is the logits' type."""
+    return SpecDraftCfg(B, N, V, _IO[io][0], float(temperature), 0)
+
+
+def _arg(t, dtype, shape, name, device):
+    """Data pointer of a contiguous CUDA tensor of that type and shape on the
+    current device (None passes: an argument that may be absent)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    return t.data_ptr()
+
+
+def _workspace(ws, need, device):
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous CUDA tensor")
+    if ws.get_device() != device:
+        raise ValueError(f"ws is on cuda:{ws.get_device()}, the current device is cuda:{device}")
+    if ws.nbytes < need:
+        raise ValueError(f"ws holds {ws.nbytes} bytes, {need} are needed")
+    return ws.data_ptr()
+
+
+def _required(t, name):
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t
+
+
+def spec_paged_workspace_bytes(cfg: SpecPagedCfg, num_sms: int = 0) -> int:
+    """Workspace bytes of the paged calls (num_sms 0: the current device's)."""
+    n = load().spec_paged_workspace_bytes(ctypes.byref(cfg), int(num_sms))
+    if n == 0:
+        raise SpecError("spec_paged_workspace_bytes", ST_EINVAL,
+                        "invalid configuration (or no CUDA device visible)")
+    return int(n)
+
+
+def spec_draft_workspace_bytes(cfg: SpecDraftCfg, num_sms: int = 0) -> int:
+    """Workspace bytes of draft_verify_sampled (num_sms 0: the current device's)."""
+    n = load().spec_draft_workspace_bytes(ctypes.byref(cfg), int(num_sms))
+    if n == 0:
+        raise SpecError("spec_draft_workspace_bytes", ST_EINVAL,
+                        "invalid configuration (or no CUDA device visible)")
+    return int(n)
+
+
+def alloc_paged_workspace(cfg: SpecPagedCfg, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of spec_paged_workspace_bytes(cfg) bytes."""
+    return torch.zeros((spec_paged_workspace_bytes(cfg),), dtype=torch.uint8, device=device)
+
+
+def alloc_draft_workspace(cfg: SpecDraftCfg, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of spec_draft_workspace_bytes(cfg) bytes."""
+    return torch.zeros((spec_draft_workspace_bytes(cfg),), dtype=torch.uint8, device=device)
+
+
+class PagedKV:
+    """A paged cache's tensors, checked once against a SpecPagedCfg.
+
+    k_pages, v_pages [n_pages][Hkv][page][D] (io type; float8_e4m3fn with
+    kv="e4m3"), k_scale, v_scale [n_pages][Hkv][page] fp32 (e4m3 only),
+    page_table [B][max_pages] and kv_len [B] int32.  The tensors are fixed for
+    the object's life; their contents are the caller's.
+    """
+
+    def __init__(self, cfg: SpecPagedCfg, k_pages, v_pages, page_table, kv_len, k_scale=None,
+                 v_scale=None):
+        q8 = cfg.kv_dtype == SPEC_KV_E4M3
+        dt = torch.float8_e4m3fn if q8 else _io_dtype(cfg)
+        dev = torch.cuda.current_device()
+        pool = (cfg.n_pages, cfg.Hkv, cfg.page, cfg.D)
+        i32, f32 = torch.int32, torch.float32
+        if not q8 and (k_scale is not None or v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to a cache in 8 bits")
+        sc = [_arg(_required(t, n), f32, pool[:3], n, dev) if q8 else None
+              for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
+        self._c = SpecPagedKV(
+            _arg(_required(k_pages, "k_pages"), dt, pool, "k_pages", dev),
+            _arg(_required(v_pages, "v_pages"), dt, pool, "v_pages", dev), *sc,
+            _arg(_required(page_table, "page_table"), i32, (cfg.B, cfg.max_pages), "page_table",
+                 dev),
+            _arg(_required(kv_len, "kv_len"), i32, (cfg.B,), "kv_len", dev))
+        self._t = (k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
+        self.key = (pool, cfg.B, cfg.max_pages, cfg.kv_dtype, dt, dev)
+
+    k_pages, v_pages, k_scale, v_scale, page_table, kv_len = (
+        property(lambda self, i=i: self._t[i]) for i in range(6))
+
+    @classmethod
+    def empty(cls, cfg: SpecPagedCfg, device="cuda") -> "PagedKV":
+        """Zero-filled pool, a page table that owns no page (-1) and kv_len 0."""
+        q8 = cfg.kv_dtype == SPEC_KV_E4M3
+        dt = torch.float8_e4m3fn if q8 else _io_dtype(cfg)
+        pool = (cfg.n_pages, cfg.Hkv, cfg.page, cfg.D)
+        sc = [torch.ones(pool[:3], dtype=torch.float32, device=device) if q8 else None
+              for _ in range(2)]
+        return cls(cfg, torch.zeros(pool, dtype=dt, device=device),
+                   torch.zeros(pool, dtype=dt, device=device),
+                   torch.full((cfg.B, cfg.max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros((cfg.B,), dtype=torch.int32, device=device), *sc)
+
+    def c(self, cfg: SpecPagedCfg) -> SpecPagedKV:
+        pool = (cfg.n_pages, cfg.Hkv, cfg.page, cfg.D)
+        if self.key[:4] != (pool, cfg.B, cfg.max_pages, cfg.kv_dtype) or (
+                cfg.kv_dtype == SPEC_KV_IO and self.key[4] != _io_dtype(cfg)):
+            raise ValueError("the cache was made for another configuration")
+        if self.key[5] != torch.cuda.current_device():
+            raise ValueError(f"the cache is on cuda:{self.key[5]}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        return self._c
+
+
+def kv_page_append(cfg: SpecPagedCfg, kv: PagedKV, k_new, v_new, ws, n_new=None, stream=None):
+    """Write the new tokens' rows (k_new, v_new [B][T][Hkv][D] io) behind the
+    committed ones; n_new: None or CUDA int32 [B]."""
+    dt, dev = _io_dtype(cfg), torch.cuda.current_device()
+    shape = (cfg.B, cfg.T, cfg.Hkv, cfg.D)
+    _check("kv_page_append", load().kv_page_append(
+        ctypes.byref(cfg), ctypes.byref(kv.c(cfg)), _arg(k_new, dt, shape, "k_new", dev),
+        _arg(v_new, dt, shape, "v_new", dev), _arg(n_new, torch.int32, (cfg.B,), "n_new", dev),
+        _workspace(ws, _STATUS_BYTES, dev), _stream(stream)))
+
+
+def kv_page_read(cfg: SpecPagedCfg, kv: PagedKV, k_out, v_out, ws, stream=None):
+    """The committed rows as a contiguous cache [B][Lmax][Hkv][D] io (rows at
+    or past kv_len are left as they were)."""
+    dt, dev = _io_dtype(cfg), torch.cuda.current_device()
+    Lmax = k_out.shape[1] if isinstance(k_out, torch.Tensor) and k_out.dim() == 4 else 0
+    shape = (cfg.B, Lmax, cfg.Hkv, cfg.D)
+    _check("kv_page_read", load().kv_page_read(
+        ctypes.byref(cfg), ctypes.byref(kv.c(cfg)), Lmax, _arg(k_out, dt, shape, "k_out", dev),
+        _arg(v_out, dt, shape, "v_out", dev), _workspace(ws, _STATUS_BYTES, dev),
+        _stream(stream)))
+
+
+def attn_decode_paged(cfg: SpecPagedCfg, kv: PagedKV, q, o, ws, n_new=None, stream=None):
+    """Attention of the new tokens (q, o [B][T][Hq][D] io) over the paged cache."""
+    dt, dev = _io_dtype(cfg), torch.cuda.current_device()
+    shape = (cfg.B, cfg.T, cfg.Hq, cfg.D)
+    _check("attn_decode_paged", load().attn_decode_paged(
+        ctypes.byref(cfg), ctypes.byref(kv.c(cfg)), _arg(q, dt, shape, "q", dev),
+        _arg(n_new, torch.int32, (cfg.B,), "n_new", dev), _arg(o, dt, shape, "o", dev),
+        _workspace(ws, load().spec_paged_workspace_bytes(ctypes.byref(cfg), 0), dev),
+        _stream(stream)))
+
+
+class DraftBuffers:
+    """Outputs of draft_verify_sampled."""
+
+    def __init__(self, cfg: SpecDraftCfg, device="cuda"):
+        B, N = cfg.B, cfg.N
+        self.accept_len = torch.empty((B,), dtype=torch.int32, device=device)
+        self.out_tok = torch.empty((B, N + 1), dtype=torch.int32, device=device)
+        self.target_prob = torch.empty((B, N), dtype=torch.float32, device=device)
+
+
+def draft_verify_sampled(cfg: SpecDraftCfg, draft_tok, draft_prob, logits, u, e,
+                         out: DraftBuffers, ws, n_draft=None, kv_len=None, root_tok=None,
+                         stream=None):
+    """Verify drafted chains from given random numbers: draft_tok int32 [B][N],
+    draft_prob f32 [B][N][V] or None (point masses), logits io [B][N+1][V], u
+    f32 [B][N], e f32 [B][V]; kv_len / root_tok are advanced when given.  With
+    N = 0 (plain sampling) draft_tok, draft_prob and u are not read."""
+    dev, f32, i32 = torch.cuda.current_device(), torch.float32, torch.int32
+    B, N, V = cfg.B, cfg.N, cfg.V
+    if N == 0:
+        draft_tok = draft_prob = u = None
+    co = SpecDraftOut(_arg(out.accept_len, i32, (B,), "accept_len", dev),
+                      _arg(out.out_tok, i32, (B, N + 1), "out_tok", dev),
+                      _arg(out.target_prob, f32, (B, N), "target_prob", dev) if N else None)
+    _check("draft_verify_sampled", load().draft_verify_sampled(
+        ctypes.byref(cfg), _arg(draft_tok, i32, (B, N), "draft_tok", dev),
+        _arg(n_draft, i32, (B,), "n_draft", dev),
+        _arg(draft_prob, f32, (B, N, V), "draft_prob", dev),
+        _arg(logits, _io_dtype(cfg), (B, N + 1, V), "logits", dev), _arg(u, f32, (B, N), "u", dev),
+        _arg(e, f32, (B, V), "e", dev), ctypes.byref(co), _arg(kv_len, i32, (B,), "kv_len", dev),
+        _arg(root_tok, i32, (B,), "root_tok", dev),
+        _workspace(ws, load().spec_draft_workspace_bytes(ctypes.byref(cfg), 0), dev),
+        _stream(stream)))

@@ -1,0 +1,136 @@
+// paged.cuh -- shapes, checks and addressing shared by the paged-cache kernels
+// (paged_cache.cu, attn_paged.cu) and the chain verification (draft_verify.cu).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "checks.h"
+#include "common.cuh"
+
+namespace spec {
+
+inline int check_paged_cfg(const spec_paged_cfg* c) {
+    if (!c) return ST_EINVAL;
+    if (c->B < 1 || c->B > SPEC_MAX_PAGED_B || c->T < 1 || c->T > (1 << 20)) return ST_EINVAL;
+    if (c->Hq < 1 || c->Hkv < 1 || c->Hq % c->Hkv != 0) return ST_EINVAL;
+    if ((int64_t)c->B * c->Hq > (1 << 24)) return ST_EINVAL;
+    if (c->D != 64 && c->D != 128) return ST_EINVAL;
+    if (c->page < SPEC_MIN_PAGE || c->page > SPEC_MAX_PAGE || (c->page & (c->page - 1)))
+        return ST_EINVAL;
+    if (c->n_pages < 1 || c->max_pages < 1 || (int64_t)c->max_pages * c->page > (1 << 30))
+        return ST_EINVAL;
+    if (c->io_dtype != SPEC_IO_F32 && c->io_dtype != SPEC_IO_BF16) return ST_EUNSUPPORTED;
+    if (c->kv_dtype != SPEC_KV_IO && c->kv_dtype != SPEC_KV_E4M3) return ST_EUNSUPPORTED;
+    return ST_OK;
+}
+
+inline int check_paged_kv(const spec_paged_cfg& c, const spec_paged_kv* kv) {
+    if (!kv || !al16(kv->k_pages) || !al16(kv->v_pages) || !al16(kv->page_table) ||
+        !al16(kv->kv_len))
+        return ST_EINVAL;
+    if (c.kv_dtype == SPEC_KV_E4M3 && (!al16(kv->k_scale) || !al16(kv->v_scale))) return ST_EINVAL;
+    return ST_OK;
+}
+
+inline int check_draft_cfg(const spec_draft_cfg* c) {
+    if (!c) return ST_EINVAL;
+    if (c->B < 1 || c->B > 65535 || c->N < 0 || c->N + 1 > SPEC_MAX_ROWS || c->V < 1)
+        return ST_EINVAL;
+    if (!(c->temperature > 0.0f && c->temperature <= 3.0e38f) || c->reserved != 0u)
+        return ST_EINVAL;
+    if (c->io_dtype != SPEC_IO_F32 && c->io_dtype != SPEC_IO_BF16) return ST_EUNSUPPORTED;
+    return ST_OK;
+}
+
+struct PagedWs {
+    size_t total;
+};
+
+inline PagedWs paged_ws_layout(const spec_paged_cfg&, int) {
+    PagedWs w{};
+    w.total = 256;                       // status word + reserve
+    return w;
+}
+
+struct DraftWs {
+    size_t total;
+};
+
+inline DraftWs draft_ws_layout(const spec_draft_cfg&, int) {
+    DraftWs w{};
+    w.total = 256;                       // status word + reserve
+    return w;
+}
+
+cudaError_t launch_page_append(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* k_new,
+                               const void* v_new, const int32_t* n_new, void* ws, cudaStream_t st);
+cudaError_t launch_page_read(const spec_paged_cfg& c, const spec_paged_kv& kv, int Lmax,
+                             void* k_out, void* v_out, void* ws, cudaStream_t st);
+cudaError_t launch_attn_paged(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
+                              const int32_t* n_new, void* o, void* ws, cudaStream_t st);
+cudaError_t launch_draft_verify(const spec_draft_cfg& c, const int32_t* draft_tok,
+                                const int32_t* n_draft, const float* draft_prob,
+                                const void* logits, const float* u, const float* e,
+                                const spec_draft_out& out, int32_t* kv_len, int32_t* root_tok,
+                                void* ws, cudaStream_t st);
+
+// fn<IO, KV, D>(...) for the configuration `c` in scope
+#define SPEC_PAGED_DISPATCH(fn, ...)                                                   \
+    do {                                                                               \
+        const bool d128 = c.D == 128, q8 = c.kv_dtype == SPEC_KV_E4M3;                 \
+        if (c.io_dtype == SPEC_IO_BF16) {                                              \
+            if (q8)                                                                    \
+                return d128 ? fn<SPEC_IO_BF16, SPEC_KV_E4M3, 128>(__VA_ARGS__)         \
+                            : fn<SPEC_IO_BF16, SPEC_KV_E4M3, 64>(__VA_ARGS__);         \
+            return d128 ? fn<SPEC_IO_BF16, SPEC_KV_IO, 128>(__VA_ARGS__)               \
+                        : fn<SPEC_IO_BF16, SPEC_KV_IO, 64>(__VA_ARGS__);               \
+        }                                                                              \
+        if (q8)                                                                        \
+            return d128 ? fn<SPEC_IO_F32, SPEC_KV_E4M3, 128>(__VA_ARGS__)              \
+                        : fn<SPEC_IO_F32, SPEC_KV_E4M3, 64>(__VA_ARGS__);              \
+        return d128 ? fn<SPEC_IO_F32, SPEC_KV_IO, 128>(__VA_ARGS__)                    \
+                    : fn<SPEC_IO_F32, SPEC_KV_IO, 64>(__VA_ARGS__);                    \
+    } while (0)
+
+// ---- device side ------------------------------------------------------------------
+
+// Element of a cache row: the I/O type, or an e4m3 code.
+template <int IO, int KV> struct kv_t { using T = typename io_t<IO>::T; };
+template <int IO> struct kv_t<IO, SPEC_KV_E4M3> { using T = uint8_t; };
+
+// What a paged kernel needs to find a row, by value.
+struct PageMap {
+    const int32_t* table;
+    const int32_t* kv_len;
+    int max_pages, n_pages, sh;          // page = 1 << sh
+    int Hkv;
+    __device__ __forceinline__ int cap() const { return max_pages << sh; }
+    // index of (row, head) among the pool's rows, or -1 when the page is not in the pool
+    __device__ __forceinline__ int64_t row(int b, int pos, int h) const {
+        const int p = table[(size_t)b * max_pages + (pos >> sh)];
+        if ((unsigned)p >= (unsigned)n_pages) return -1;
+        return ((((int64_t)p * Hkv + h) << sh) | (pos & ((1 << sh) - 1)));
+    }
+};
+
+inline PageMap page_map(const spec_paged_cfg& c, const spec_paged_kv& kv) {
+    PageMap m{kv.page_table, kv.kv_len, c.max_pages, c.n_pages, 0, c.Hkv};
+    while ((1 << m.sh) < c.page) ++m.sh;
+    return m;
+}
+
+// New rows of request b: n_new[b] (NULL: T) clamped to [0, T]; raises
+// SPEC_DEV_BADREQ through `bits`.
+__device__ __forceinline__ int new_rows(const int32_t* n_new, int b, int T, uint32_t& bits) {
+    if (!n_new) return T;
+    const int n = n_new[b];
+    if (n < 0 || n > T) bits |= SPEC_DEV_BADREQ;
+    return n < 0 ? 0 : (n > T ? T : n);
+}
+
+__device__ __forceinline__ float e4m3_to_float(uint8_t x) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(x, __NV_E4M3);
+    return __half2float(__half(h));
+}
+
+}  // namespace spec

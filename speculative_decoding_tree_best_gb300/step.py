@@ -243,3 +243,61 @@ class HostStep:
         if self.graph is None:
             self.capture()
         self.graph.replay()
+
+
+class ChainStep:
+    """Buffers and calls of a serving step over a paged cache with a chain of
+    drafts: per attention layer the new tokens' rows are appended and attended
+    from (attend), then the drafts are verified (verify), which advances kv_len
+    over what was kept.  A step of request b has n_draft[b] + 1 new tokens: the
+    pending token and its drafts; with n_draft 0 it is a plain decode step.
+
+    The layers share one page table, kv_len and root_tok, which the caller
+    owns the contents of (page_table names the pages of each request; a page
+    id is good for every layer's pool).  Rows of refused drafts are written
+    over by the next step.
+    """
+
+    def __init__(self, pcfg: binding.SpecPagedCfg, dcfg: binding.SpecDraftCfg, n_layers: int,
+                 device="cuda"):
+        if pcfg.T != dcfg.N + 1 or pcfg.B != dcfg.B or pcfg.io_dtype != dcfg.io_dtype:
+            raise ValueError("a step needs T = N + 1 and the same B and I/O type on both sides")
+        self.pcfg, self.dcfg = pcfg, dcfg
+        first = binding.PagedKV.empty(pcfg, device)
+        self.page_table, self.kv_len = first.page_table, first.kv_len
+        self.caches = [first]
+        for _ in range(n_layers - 1):
+            e = binding.PagedKV.empty(pcfg, device)
+            self.caches.append(binding.PagedKV(pcfg, e.k_pages, e.v_pages, self.page_table,
+                                               self.kv_len, e.k_scale, e.v_scale))
+        i32 = dict(dtype=torch.int32, device=device)
+        self.root_tok = torch.zeros((pcfg.B,), **i32)
+        self.n_draft = torch.full((pcfg.B,), dcfg.N, **i32)
+        self._n_new = torch.empty((pcfg.B,), **i32)
+        dt = torch.bfloat16 if pcfg.io_dtype == binding.SPEC_IO_BF16 else torch.float32
+        self.attn_o = torch.empty((n_layers, pcfg.B, pcfg.T, pcfg.Hq, pcfg.D), dtype=dt,
+                                  device=device)
+        self.out = binding.DraftBuffers(dcfg, device)
+        self.paged_ws = binding.alloc_paged_workspace(pcfg, device)
+        self.draft_ws = binding.alloc_draft_workspace(dcfg, device)
+
+    def attend(self, layer: int, q, k_new, v_new):
+        """Append layer `layer`'s rows and attend from them: [B][T][Hq][D]."""
+        torch.add(self.n_draft, 1, out=self._n_new)
+        o = self.attn_o[layer]
+        kv = self.caches[layer]
+        binding.kv_page_append(self.pcfg, kv, k_new, v_new, self.paged_ws, n_new=self._n_new)
+        binding.attn_decode_paged(self.pcfg, kv, q, o, self.paged_ws, n_new=self._n_new)
+        return o
+
+    def verify(self, logits, draft_tok, draft_prob, u, e) -> binding.DraftBuffers:
+        """Verify the drafts, advance kv_len and root_tok."""
+        binding.draft_verify_sampled(self.dcfg, draft_tok, draft_prob, logits, u, e, self.out,
+                                     self.draft_ws, n_draft=self.n_draft, kv_len=self.kv_len,
+                                     root_tok=self.root_tok)
+        return self.out
+
+    def status(self) -> int:
+        """SPEC_DEV_* bits of the calls so far."""
+        return (binding.spec_status_read(self.paged_ws)
+                | binding.spec_status_read(self.draft_ws))
