@@ -1,93 +1,1095 @@
 // attn_paged.cu -- attention of a step's new tokens over the paged cache.
 //
-// One warp per (request, new token, q-head): one pass over the row's keys with
-// the running maximum and sum of the softmax, the head dimension split over
-// the lanes.
+// Mathematics.  Row r = (new token i, q-head h of the kv-head's group) of a
+// request sees keys [0, kv_len + i]:  o = sum_k w_k v_k / sum_k w_k with
+// w_k = 2^(x_k - m), x_k = q.k log2(e) / sqrt(D), m the running maximum: one
+// pass, kept per warp and joined at the end (the maxima, sums and outputs of
+// two parts a, b join as m = max(m_a, m_b), o = o_a 2^(m_a - m) + o_b 2^(m_b - m)).
+// In an 8-bit cache a value is code * scale per row: the key's scale multiplies
+// the score; the value's scale goes into the weight's exponent,
+// w'_k = 2^(x_k + log2 scale_k - m) with m the maximum over x_k + log2 scale_k,
+// so that the weights that meet the codes are at most 1 whatever the scales.
+//
+// What bounds it: reading the cache, 2 D values a key and kv-head against
+// 4 D G T flops (G = Hq / Hkv), 2 G T flops a byte in bf16: far below the
+// tensor cores' rate up to G T of about 100.  So the products run on
+// mma.sync with the KEYS as the 16-row operand and the rows as its 8 columns
+// (S^T = K Q^T, O^T = V^T W^T): a decode step's few rows then fill the
+// instruction (4 rows of 8 at G = 4; tcgen05's smallest tile would hold 64 or
+// 128 rows), the softmax's statistics stay with the thread that holds the
+// column in both products, and W^T gets from the first product's layout to
+// the second's by movmatrix alone.
+//
+// Data flow.  The cache is cut into granules of 16 rows (a page holds whole
+// granules).  The granules of all (request, kv-head, row group) segments in a
+// row are dealt out evenly to one CTA per SM, so lengths need not match; a
+// segment cut between CTAs leaves parts in the workspace, and the CTA that
+// finishes last (a ticket per segment) joins them in their order.  In a CTA
+// one warp issues TMA copies (16 rows x 128 bytes, 128-byte swizzle) into a ring of
+// 64-key stages, and W warps take granules from it in turn.  A row's 16-byte
+// chunks go to lanes so that the products need no transposition of K, and of
+// V only byte permutes; the row order below makes every 128-bit shared load
+// free of bank conflicts under the swizzle.
+#include <cuda.h>
 #include <math.h>
 
 #include "paged.cuh"
+#include "tc_util.cuh"
 
 namespace spec {
 
 namespace {
 
-constexpr int WARPS = 4;
+using tc::mbar_wait;
+using tc::smem_u32;
 
-template <int IO, int KV, int D>
-__global__ void __launch_bounds__(32 * WARPS)
-attn_rows(PageMap pm, int B, int T, int Hq, const typename io_t<IO>::T* __restrict__ q,
-          const void* __restrict__ k_pages, const void* __restrict__ v_pages,
-          const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-          const int32_t* __restrict__ n_new, typename io_t<IO>::T* __restrict__ o, float qk_scale,
-          void* ws) {
-    constexpr int E = D / 32;
-    const int64_t w = (int64_t)blockIdx.x * WARPS + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    if (w >= (int64_t)B * T * Hq) return;
-    const int h = (int)(w % Hq);
-    const int b = (int)(w / Hq / T), i = (int)(w / Hq % T);
-    const int hk = h / (Hq / pm.Hkv);
-    uint32_t bits = 0;
-    const int n = new_rows(n_new, b, T, bits);
-    int L = pm.kv_len[b];
-    if (L < 0 || L > pm.cap() - n) {
+constexpr int GK = 16;                 // keys per granule
+constexpr int SG = 4;                  // granules per stage
+constexpr int SK = GK * SG;            // keys per stage
+
+// ---- instruction wrappers -------------------------------------------------------------
+
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32_1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 8x8 transpose of 16-bit elements across the warp
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+// two e4m3 codes (the low or high half of x) as f16x2: exact
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t x) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t packh(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t packb(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float lo_b(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_b(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ uint32_t tf32_rna(float x) {
+    uint32_t y;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+    return y;
+}
+// x = hi + lo to 2^-22: two tf32 parts; an infinity stays in hi
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = tf32_rna(x);
+    if ((hi & 0x7fffffffu) == 0x7f800000u) hi = __float_as_uint(x) & 0xffffe000u;
+    const float h = __uint_as_float(hi);
+    lo = h == x ? 0u : tf32_rna(x - h);
+}
+
+// ---- layout of the operands -----------------------------------------------------------
+
+template <int IO, int KV, int D> struct At {
+    static constexpr bool Q8 = KV == SPEC_KV_E4M3;
+    static constexpr bool F32 = !Q8 && IO == SPEC_IO_F32;
+    static constexpr int EB = Q8 ? 1 : (IO == SPEC_IO_F32 ? 4 : 2);   // bytes of a cached value
+    static constexpr int ROWB = D * EB;
+    static constexpr int SW = ROWB < 128 ? ROWB : 128;  // bytes of a row in one swizzled block
+    static constexpr int NB = ROWB / SW;                // blocks per row
+    static constexpr int KCH = ROWB / 64;               // 16-byte chunks of a K row per lane
+    static constexpr int EPC = 16 / EB;                 // values per chunk
+    static constexpr int VL = ROWB / 8 < 16 ? 1 : ROWB / 128;   // V loads per row and lane
+    static constexpr int RL = Q8 ? D / 8 : EPC;         // consecutive values of a lane in a row
+    static constexpr int NRUN = D / 8 / RL;
+    static constexpr int NT = D / 16;                   // 16-value tiles of O^T
+    static constexpr int QT = (Q8 && IO == SPEC_IO_F32) || F32 ? 2 : 1;   // parts of a Q value
+    static constexpr int QR = Q8 ? 8 : 4;               // Q registers per chunk and part
+    static constexpr int PT = (Q8 && IO == SPEC_IO_BF16) ? 1 : 2;   // parts of a weight
+    static constexpr int STAGE_KV = SK * ROWB;          // bytes of K (or V) in a stage
+    static constexpr int STAGE = 2 * STAGE_KV;
+};
+
+// byte offset of 16-byte chunk c of key row r in a stage's K (or V) region
+template <class A> __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
+    constexpr int CPB = A::SW / 16;
+    const int blk = c / CPB, cc = c % CPB;
+    const int x = A::SW == 128 ? (r & 7) : ((r >> 1) & 3);
+    return (uint32_t)(blk * SK * A::SW + r * A::SW + ((cc ^ x) << 4));
+}
+
+struct AttnParams {
+    PageMap pm;
+    const void* q;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* n_new;
+    void* o;
+    void* ws;
+    uint32_t* tickets;
+    float4* part_o;
+    float4* part_ml;
+    int B, T, Hq, G;
+    int rtc, rtg;            // row tiles per CTA, row groups per (request, kv-head)
+    int stages;
+    int min_granules;        // per CTA
+    float qk_scale;          // log2(e) / sqrt(D)
+};
+
+// One request's lengths.
+struct Req {
+    int L, n, ng;            // committed rows, new rows, granules
+};
+__device__ __forceinline__ Req request(const AttnParams& p, int b, uint32_t& bits) {
+    Req r;
+    r.n = new_rows(p.n_new, b, p.T, bits);
+    r.L = p.pm.kv_len[b];
+    const int cap = p.pm.cap();
+    if (r.L < 0 || r.L > cap - r.n) {
         bits |= SPEC_DEV_OVERFLOW;
-        L = L < 0 ? 0 : min(L, pm.cap());
+        r.L = r.L < 0 ? 0 : min(r.L, cap);
     }
-    const int end = i < n ? min(L + i + 1, pm.cap()) : 0;
-    float qr[E], acc[E], m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-        qr[j] = io_t<IO>::ld(q, w * D + lane * E + j) * qk_scale;
-        acc[j] = 0.0f;
+    const int end = r.n > 0 ? min(r.L + r.n, cap) : 0;
+    r.ng = max(1, (end + GK - 1) / GK);
+    return r;
+}
+
+// One pass over the segments of a CTA's granule range, in order.
+struct Walk {
+    int b, seg, pos;         // request, segment in the request, granule in the segment
+    long long left;
+    Req rq;
+    __device__ __forceinline__ int count() const {
+        return (int)min((long long)(rq.ng - pos), left);
     }
-    using KT = typename kv_t<IO, KV>::T;
-    const KT* kp = static_cast<const KT*>(k_pages);
-    const KT* vp = static_cast<const KT*>(v_pages);
-    for (int pos = 0; pos < end; ++pos) {
-        const int64_t r = pm.row(b, pos, hk);
-        if (r < 0) {
-            bits |= SPEC_DEV_BADPAGE;
-            continue;
+    // past `c` granules of the present segment
+    __device__ __forceinline__ void next(const AttnParams& p, int hr, int c) {
+        left -= c;
+        pos += c;
+        if (pos < rq.ng || left <= 0) return;
+        pos = 0;
+        if (++seg == hr) {
+            seg = 0;
+            ++b;
+            uint32_t bits = 0;
+            rq = request(p, b, bits);
         }
-        float s = 0.0f, v[E];
+    }
+};
+
+// The CTA that owns granule u of `units` dealt to `n` CTAs (CTA c starts at c units / n).
+__device__ __forceinline__ int owner(long long u, long long units, int n) {
+    return (int)(((u + 1) * n - 1) / units);
+}
+
+template <int IO, int KV, int D, int NR, int W>
+__global__ void __launch_bounds__(32 * (W + 1), 1)
+attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+           const __grid_constant__ AttnParams p) {
+    using A = At<IO, KV, D>;
+    constexpr int NTH = 32 * (W + 1);
+    constexpr int MAXST = 16;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[MAXST], empty[MAXST];
+    __shared__ uint32_t flags[MAXST];
+    __shared__ long long wsum[W + 1];
+    __shared__ long long first_off;
+    __shared__ int first_b;
+    __shared__ volatile int abort_flag;
+    __shared__ int last_flag;
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int hr = p.pm.Hkv * p.rtg;
+    uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float* scales = reinterpret_cast<float*>(ring + (size_t)p.stages * A::STAGE);
+    float4* buf = reinterpret_cast<float4*>(scales + (A::Q8 ? p.stages * 2 * SK : 0));
+
+    // ---- this CTA's share of the granules
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < p.stages; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&empty[s], W);
+        }
+        tc::fence_mbar_init();
+    }
+    const int per = (p.B + NTH - 1) / NTH;
+    long long mine = 0;
+    uint32_t bits = 0;
+    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b)
+        mine += (long long)request(p, b, bits).ng * hr;
+    if (bits && blockIdx.x == 0) raise_status(p.ws, bits);
+    long long incl = mine;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            if constexpr (KV == SPEC_KV_E4M3) {
-                s += qr[j] * e4m3_to_float(kp[r * D + lane * E + j]);
-                v[j] = e4m3_to_float(vp[r * D + lane * E + j]) * v_scale[r];
-            } else {
-                s += qr[j] * io_t<IO>::ld(kp, r * D + lane * E + j);
-                v[j] = io_t<IO>::ld(vp, r * D + lane * E + j);
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    long long before = 0, units = 0;
+#pragma unroll 1
+    for (int w = 0; w <= W; ++w) {
+        if (w < warp) before += wsum[w];
+        units += wsum[w];
+    }
+    const int n_cta = (int)min((long long)gridDim.x, (units + p.min_granules - 1) / p.min_granules);
+    if ((int)blockIdx.x >= n_cta) return;
+    const long long g0 = units * blockIdx.x / n_cta, g1 = units * (blockIdx.x + 1) / n_cta;
+    {
+        const long long lo = before + incl - mine;
+        if (g0 >= lo && g0 < lo + mine) {
+            long long at = lo;
+            for (int b = tid * per;; ++b) {
+                uint32_t ignore = 0;
+                const long long c = (long long)request(p, b, ignore).ng * hr;
+                if (g0 < at + c) {
+                    first_b = b;
+                    first_off = g0 - at;
+                    break;
+                }
+                at += c;
             }
         }
-        s = warp_sum(s);
-        if constexpr (KV == SPEC_KV_E4M3) s *= k_scale[r];
-        const float nm = fmaxf(m, s), base = nm == -INFINITY ? 0.0f : nm;
-        const float f = expf(m - base), p = expf(s - base);
-        l = l * f + p;
-#pragma unroll
-        for (int j = 0; j < E; ++j) acc[j] = acc[j] * f + p * v[j];
-        m = nm;
     }
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-        const float x = l == 0.0f ? 0.0f : acc[j] / l;
-        if (!(fabsf(x) <= 3.4028234663852886e38f)) bits |= SPEC_DEV_RANGE;
-        io_t<IO>::st(o, w * D + lane * E + j, x);
+    __syncthreads();
+    Walk wk;
+    wk.b = first_b;
+    wk.left = g1 - g0;
+    {
+        uint32_t ignore = 0;
+        wk.rq = request(p, wk.b, ignore);
+        wk.seg = (int)(first_off / wk.rq.ng);
+        wk.pos = (int)(first_off % wk.rq.ng);
     }
-    if (bits) raise_status(ws, bits);
+    const int rows_tile = 8 * NR;
+    const int cap = p.pm.cap();
+
+    if (warp == W) {
+        // ---- producer: page ids for eight stages at once, one granule per lane
+        int st = 0, use = 0, issued = 0;
+        bool ok = true;
+        uint32_t bad = 0;
+        while (wk.left > 0 && ok) {
+            const int hk = wk.seg / p.rtg, rg = wk.seg % p.rtg;
+            const int r0 = rg * p.rtc * rows_tile;
+            int end = 0;
+            if (r0 < wk.rq.n * p.G) {
+                const int last = min(r0 + p.rtc * rows_tile, wk.rq.n * p.G) - 1;
+                end = min(wk.rq.L + last / p.G + 1, cap);
+            }
+            const int cnt = wk.count();
+            for (int base = 0; base < cnt && ok; base += 32) {
+                const int gi = base + lane;
+                const int key = (wk.pos + gi) * GK;
+                int64_t row = -1;
+                if (gi < cnt && key < end) {
+                    row = p.pm.row(wk.b, key, hk);
+                    if (row < 0) bad = SPEC_DEV_BADPAGE;
+                }
+                const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+                const int64_t prow = (int64_t)p.pm.Hkv << p.pm.sh;      // rows per page
+                const int page = row >= 0 ? (int)(row / prow) : 0;
+                const int prel = row >= 0 ? (int)(row % prow) : 0;
+                for (int u = 0; u < 8 && base + 4 * u < cnt; ++u) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (use & 1) ^ 1,
+                                                           &abort_flag));
+                    if (!ok) break;
+                    const uint32_t m4 = (have >> (4 * u)) & 15u;
+                    if (lane == 0) {
+                        flags[st] = m4;
+                        tc::mbar_arrive_expect_tx(
+                            &full[st], __popc(m4) * (2 * GK * A::ROWB + (A::Q8 ? 8 * GK : 0)));
+                    }
+                    __syncwarp();
+                    if (lane / 4 == u && row >= 0) {
+                        uint8_t* kd = ring + (size_t)st * A::STAGE + (lane % 4) * GK * A::SW;
+#pragma unroll
+                        for (int nb = 0; nb < A::NB; ++nb) {
+                            tc::tma_load_3d(kd + nb * SK * A::SW, &mk, &full[st], nb * A::SW, prel,
+                                            page);
+                            tc::tma_load_3d(kd + A::STAGE_KV + nb * SK * A::SW, &mv, &full[st],
+                                            nb * A::SW, prel, page);
+                        }
+                        if constexpr (A::Q8) {
+                            float* sd = scales + st * 2 * SK + (lane % 4) * GK;
+#pragma unroll
+                            for (int v = 0; v < 2; ++v)
+                                asm volatile(
+                                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::"
+                                    "bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(sd + v * SK)),
+                                    "l"((v ? p.v_scale : p.k_scale) + row), "r"(4 * GK),
+                                    "r"(smem_u32(&full[st]))
+                                    : "memory");
+                        }
+                    }
+                    ++issued;
+                    if (++st == p.stages) {
+                        st = 0;
+                        ++use;
+                    }
+                }
+            }
+            wk.next(p, hr, cnt);
+        }
+        if (__any_sync(0xffffffffu, bad != 0) && lane == 0) raise_status(p.ws, SPEC_DEV_BADPAGE);
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) raise_status(p.ws, SPEC_DEV_TIMEOUT);
+            // copies in flight land before the CTA's shared memory is released
+            for (int j = max(0, issued - p.stages); j < issued; ++j)
+                mbar_wait(&full[j % p.stages], (j / p.stages) & 1, nullptr);
+        }
+        return;
+    }
+
+    // ---- consumers
+    const int rt = warp % p.rtc, kw = warp / p.rtc, KW = W / p.rtc;
+    const int g = lane / 4, t = lane % 4;
+    const int kr = g ^ ((g & 1) << 2);                       // key row of fragment row g
+    const int va = 2 * t, vb = (2 * t + 1) ^ 4;              // key rows of fragment columns 2t, 2t+1
+    int st = 0, use = 0;
+
+    float o[NR][A::NT][4];
+    float m[NR][2], l[NR][2], rowf[NR][2];
+    int lim[NR][2];
+    uint32_t qf[NR][A::QT][A::KCH][A::QR];
+
+    auto clear = [&]() {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            m[nr][0] = m[nr][1] = -INFINITY;
+            l[nr][0] = l[nr][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < A::NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nr][i][e] = 0.0f;
+        }
+    };
+    // join (m2, l2) and outputs read by `get(nr, i)` into the own ones
+    auto join = [&](const float (&m2)[NR][2], const float (&l2)[NR][2], auto get) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            float f1[2], f2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float nm = fmaxf(m[nr][e], m2[nr][e]);
+                const float base = nm == -INFINITY ? 0.0f : nm;
+                f1[e] = ex2(m[nr][e] - base);
+                f2[e] = ex2(m2[nr][e] - base);
+                m[nr][e] = nm;
+                l[nr][e] = l[nr][e] * f1[e] + l2[nr][e] * f2[e];
+            }
+#pragma unroll
+            for (int i = 0; i < A::NT; ++i) {
+                const float4 x = get(nr, i);
+                o[nr][i][0] = o[nr][i][0] * f1[0] + x.x * f2[0];
+                o[nr][i][1] = o[nr][i][1] * f1[1] + x.y * f2[1];
+                o[nr][i][2] = o[nr][i][2] * f1[0] + x.z * f2[0];
+                o[nr][i][3] = o[nr][i][3] * f1[1] + x.w * f2[1];
+            }
+        }
+    };
+    auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
+    // join the key warps' results into key warp 0's, by halves
+    auto join_warps = [&]() {
+        constexpr int SLOT = NR * (A::NT + 1) * 32;
+        for (int n = KW; n > 1; n = (n + 1) / 2) {
+            const int h = (n + 1) / 2;
+            if (kw >= h && kw < n) {
+                float4* d = buf + ((kw - h) * p.rtc + rt) * SLOT + lane;
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    d[(nr * (A::NT + 1)) * 32] = make_float4(m[nr][0], m[nr][1], l[nr][0], l[nr][1]);
+#pragma unroll
+                    for (int i = 0; i < A::NT; ++i)
+                        d[(nr * (A::NT + 1) + 1 + i) * 32] =
+                            make_float4(o[nr][i][0], o[nr][i][1], o[nr][i][2], o[nr][i][3]);
+                }
+            }
+            bar();
+            if (kw < n - h) {
+                const float4* s = buf + (kw * p.rtc + rt) * SLOT + lane;
+                float m2[NR][2], l2[NR][2];
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    const float4 x = s[(nr * (A::NT + 1)) * 32];
+                    m2[nr][0] = x.x;
+                    m2[nr][1] = x.y;
+                    l2[nr][0] = x.z;
+                    l2[nr][1] = x.w;
+                }
+                join(m2, l2, [&](int nr, int i) { return s[(nr * (A::NT + 1) + 1 + i) * 32]; });
+            }
+            bar();
+        }
+    };
+
+    // one granule: keys [kb, kb + 16) in slot rows [16 sl, 16 sl + 16) of stage `st`
+    auto granule = [&](int kb, int sl, int lim_min, int lim_max) {
+        const uint32_t ks = smem_u32(ring + (size_t)st * A::STAGE);
+        const uint32_t vs = ks + A::STAGE_KV;
+        const int rk = sl * GK + kr;
+        float s[NR][4];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) s[nr][0] = s[nr][1] = s[nr][2] = s[nr][3] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < A::KCH; ++j) {
+            const uint4 k0 = lds128(ks + chunk_off<A>(rk, t + 4 * j));
+            const uint4 k1 = lds128(ks + chunk_off<A>(rk + 8, t + 4 * j));
+            if constexpr (A::Q8) {
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a[4] = {e4m3x2(w0[i]), e4m3x2(w1[i]), e4m3x2(w0[i] >> 16),
+                                           e4m3x2(w1[i] >> 16)};
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int q = 0; q < A::QT; ++q)
+                            mma_f16_16816(s[nr], a, qf[nr][q][j][2 * i], qf[nr][q][j][2 * i + 1]);
+                }
+            } else if constexpr (A::F32) {
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t ah[4], al[4];
+                    split_tf32(__uint_as_float(w0[2 * i]), ah[0], al[0]);
+                    split_tf32(__uint_as_float(w1[2 * i]), ah[1], al[1]);
+                    split_tf32(__uint_as_float(w0[2 * i + 1]), ah[2], al[2]);
+                    split_tf32(__uint_as_float(w1[2 * i + 1]), ah[3], al[3]);
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        mma_tf32_1688(s[nr], ah, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
+                        mma_tf32_1688(s[nr], ah, qf[nr][1][j][2 * i], qf[nr][1][j][2 * i + 1]);
+                        mma_tf32_1688(s[nr], al, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
+                    }
+                }
+            } else {
+                const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    mma_bf16_16816(s[nr], a0, qf[nr][0][j][0], qf[nr][0][j][1]);
+                    mma_bf16_16816(s[nr], a1, qf[nr][0][j][2], qf[nr][0][j][3]);
+                }
+            }
+        }
+        // scores in log2 units; a = what the V weights go by
+        const bool masked = kb + GK > lim_min;
+        float lv[2] = {0.0f, 0.0f}, kf[2] = {1.0f, 1.0f};
+        if constexpr (A::Q8) {
+            const float* sc = scales + st * 2 * SK + rk;
+            kf[0] = sc[0];
+            kf[1] = sc[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float y = sc[SK + 8 * k];
+                lv[k] = y >= 0.0f && y < 0x1p-126f ? -126.0f : __log2f(y);   // a scale of 0
+            }
+        }
+        float x[NR][4];
+        bool grow = false;
+        float nm[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[nr][e] = s[nr][e] * (A::Q8 ? rowf[nr][e & 1] * kf[e >> 1] : rowf[nr][e & 1]);
+                if (masked && kb + kr + 8 * (e >> 1) >= lim[nr][e & 1]) x[nr][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float y;
+                if constexpr (A::Q8) {
+                    // a masked key's scale may be anything
+                    const float a0 = x[nr][e] == -INFINITY ? -INFINITY : x[nr][e] + lv[0];
+                    const float a1 = x[nr][2 + e] == -INFINITY ? -INFINITY : x[nr][2 + e] + lv[1];
+                    y = fmaxf(a0, a1);
+                } else {
+                    y = fmaxf(x[nr][e], x[nr][2 + e]);
+                }
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                nm[nr][e] = fmaxf(m[nr][e], y);
+                grow |= nm[nr][e] > m[nr][e];
+            }
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = ex2(m[nr][e] - (nm[nr][e] == -INFINITY ? 0.0f : nm[nr][e]));
+                    m[nr][e] = nm[nr][e];
+                    l[nr][e] *= f;
+#pragma unroll
+                    for (int i = 0; i < A::NT; ++i) {
+                        o[nr][i][e] *= f;
+                        o[nr][i][2 + e] *= f;
+                    }
+                }
+            }
+        }
+        // weights, their sum, and the second product's B operand
+        uint32_t wb[NR][A::PT][A::F32 ? 4 : 2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float base = m[nr][e & 1] == -INFINITY ? 0.0f : m[nr][e & 1];
+                const float d = x[nr][e] - base;
+                const float pl = ex2(d);
+                l[nr][e & 1] += pl;
+                if constexpr (A::Q8)
+                    w[e] = x[nr][e] == -INFINITY ? 0.0f : ex2(d + lv[e >> 1]);
+                else
+                    w[e] = pl;
+            }
+            if constexpr (A::F32) {
+                // 32-bit transposes as two 16-bit ones; columns = keys va, vb (+ 8)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t a = __float_as_uint(w[2 * k]), c = __float_as_uint(w[2 * k + 1]);
+                    const uint32_t th = movm(__byte_perm(a, c, 0x7632));
+                    const uint32_t tl = movm(__byte_perm(a, c, 0x5410));
+                    split_tf32(__uint_as_float(__byte_perm(tl, th, 0x5410)), wb[nr][0][2 * k],
+                               wb[nr][1][2 * k]);
+                    split_tf32(__uint_as_float(__byte_perm(tl, th, 0x7632)), wb[nr][0][2 * k + 1],
+                               wb[nr][1][2 * k + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if constexpr (A::Q8) {
+                        const uint32_t h = packh(w[2 * k], w[2 * k + 1]);
+                        wb[nr][0][k] = movm(h);
+                        if constexpr (A::PT == 2) {
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                            wb[nr][A::PT - 1][k] = movm(packh(w[2 * k] - b.x, w[2 * k + 1] - b.y));
+                        }
+                    } else {
+                        const uint32_t h = packb(w[2 * k], w[2 * k + 1]);
+                        wb[nr][0][k] = movm(h);
+                        wb[nr][A::PT - 1][k] = movm(packb(w[2 * k] - lo_b(h), w[2 * k + 1] - hi_b(h)));
+                    }
+                }
+            }
+        }
+        // O^T += V^T W^T.  cut: key rows of the granule from there on count as
+        // zeros (their weights are 0, but 0 x inf is not).  only >= 0: just the
+        // rows whose limit is `only`.
+        auto pv = [&](int cut, int only) {
+            const bool z0 = va >= cut, z1 = vb >= cut, z2 = va + 8 >= cut, z3 = vb + 8 >= cut;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            auto acc = [&](int nr, int i, const uint32_t (&a)[4], int k, int part) {
+                if constexpr (A::F32) {
+                    mma_tf32_1688(o[nr][i], a, wb[nr][part][2 * k], wb[nr][part][2 * k + 1]);
+                } else if constexpr (A::Q8) {
+                    mma_f16_16816(o[nr][i], a, wb[nr][part][0], wb[nr][part][1]);
+                } else {
+                    mma_bf16_16816(o[nr][i], a, wb[nr][part][0], wb[nr][part][1]);
+                }
+            };
+            float keep[NR][4];
+            auto tile = [&](int i, const uint32_t (&a)[4], const uint32_t (&a2)[4],
+                            const uint32_t (&al)[4], const uint32_t (&a2l)[4]) {
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    if (only >= 0) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) keep[nr][e] = o[nr][i][e];
+                    }
+                    if constexpr (A::F32) {
+                        acc(nr, i, a, 0, 0);
+                        acc(nr, i, a, 0, 1);
+                        acc(nr, i, al, 0, 0);
+                        acc(nr, i, a2, 1, 0);
+                        acc(nr, i, a2, 1, 1);
+                        acc(nr, i, a2l, 1, 0);
+                    } else {
+                        acc(nr, i, a, 0, 0);
+                        if constexpr (A::PT == 2) acc(nr, i, a, 0, 1);
+                    }
+                    if (only >= 0) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (lim[nr][e & 1] != only) o[nr][i][e] = keep[nr][e];
+                    }
+                }
+            };
+            const int rv = sl * GK;
+#pragma unroll
+            for (int j = 0; j < A::VL; ++j) {
+                uint4 v0, v1, v2, v3;
+                if constexpr (A::ROWB == 64) {
+                    // 8 bytes per lane and row
+                    const uint32_t h8 = (g & 1) * 8;
+                    const uint2 u0 = lds64(vs + chunk_off<A>(rv + va, g >> 1) + h8);
+                    const uint2 u1 = lds64(vs + chunk_off<A>(rv + vb, g >> 1) + h8);
+                    const uint2 u2 = lds64(vs + chunk_off<A>(rv + va + 8, g >> 1) + h8);
+                    const uint2 u3 = lds64(vs + chunk_off<A>(rv + vb + 8, g >> 1) + h8);
+                    v0 = make_uint4(u0.x, u0.y, 0, 0);
+                    v1 = make_uint4(u1.x, u1.y, 0, 0);
+                    v2 = make_uint4(u2.x, u2.y, 0, 0);
+                    v3 = make_uint4(u3.x, u3.y, 0, 0);
+                } else {
+                    v0 = lds128(vs + chunk_off<A>(rv + va, g + 8 * j));
+                    v1 = lds128(vs + chunk_off<A>(rv + vb, g + 8 * j));
+                    v2 = lds128(vs + chunk_off<A>(rv + va + 8, g + 8 * j));
+                    v3 = lds128(vs + chunk_off<A>(rv + vb + 8, g + 8 * j));
+                }
+                if (cut < GK) {
+                    if (z0) v0 = zero;
+                    if (z1) v1 = zero;
+                    if (z2) v2 = zero;
+                    if (z3) v3 = zero;
+                }
+                const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
+                const uint32_t x2[4] = {v2.x, v2.y, v2.z, v2.w}, x3[4] = {v3.x, v3.y, v3.z, v3.w};
+                if constexpr (A::F32) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t a[4], al[4], c[4], cl[4];
+                        split_tf32(__uint_as_float(x0[2 * r]), a[0], al[0]);
+                        split_tf32(__uint_as_float(x0[2 * r + 1]), a[1], al[1]);
+                        split_tf32(__uint_as_float(x1[2 * r]), a[2], al[2]);
+                        split_tf32(__uint_as_float(x1[2 * r + 1]), a[3], al[3]);
+                        split_tf32(__uint_as_float(x2[2 * r]), c[0], cl[0]);
+                        split_tf32(__uint_as_float(x2[2 * r + 1]), c[1], cl[1]);
+                        split_tf32(__uint_as_float(x3[2 * r]), c[2], cl[2]);
+                        split_tf32(__uint_as_float(x3[2 * r + 1]), c[3], cl[3]);
+                        tile(j * 2 + r, a, c, al, cl);
+                    }
+                } else if constexpr (A::Q8) {
+                    constexpr int NW = A::ROWB == 64 ? 2 : 4;
+#pragma unroll
+                    for (int i = 0; i < NW; ++i) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t sel = h ? 0x7362 : 0x5140;
+                            const uint32_t c0 = __byte_perm(x0[i], x1[i], sel);
+                            const uint32_t c1 = __byte_perm(x2[i], x3[i], sel);
+                            const uint32_t a[4] = {e4m3x2(c0), e4m3x2(c0 >> 16), e4m3x2(c1),
+                                                   e4m3x2(c1 >> 16)};
+                            tile(2 * i + h, a, a, a, a);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a[4] = {
+                            __byte_perm(x0[i], x1[i], 0x5410), __byte_perm(x0[i], x1[i], 0x7632),
+                            __byte_perm(x2[i], x3[i], 0x5410), __byte_perm(x2[i], x3[i], 0x7632)};
+                        tile(4 * j + i, a, a, a, a);
+                    }
+                }
+            }
+        };
+        if (!masked) {
+            pv(GK, -1);
+            return;
+        }
+        // keys that some rows see and some do not must not reach the latter:
+        // where one of them holds a value that is not finite, the rows of
+        // each limit are taken by themselves
+        bool bad = false;
+#pragma unroll 1
+        for (int c = lane; c < GK * (A::ROWB / 16); c += 32) {
+            const int r = c % GK;
+            if (kb + r < lim_min || kb + r >= lim_max) continue;
+            const uint4 v = lds128(vs + chunk_off<A>(sl * GK + r, c / GK));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (A::F32) {
+                    bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
+                } else if constexpr (A::Q8) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) bad |= ((w[i] >> (8 * y)) & 0x7fu) == 0x7fu;
+                } else {
+                    bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+                }
+            }
+        }
+        if (!__any_sync(0xffffffffu, bad)) {
+            pv(lim_max - kb, -1);
+        } else {
+#pragma unroll 1
+            for (int c = lim_min; c <= lim_max; ++c) pv(c - kb, c);
+        }
+    };
+
+    // the outputs of the key warp that holds them
+    auto write_out = [&](int hk, int row0) {
+        using T = typename io_t<IO>::T;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nr][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const int r = row0 + nr * 8 + 2 * t + e;
+                const int i = r / p.G;
+                if (i >= p.T) continue;
+                const bool real = i < wk.rq.n && sum != 0.0f;
+                T* dst = static_cast<T*>(p.o) +
+                         (((size_t)wk.b * p.T + i) * p.Hq + hk * p.G + r % p.G) * D;
+                const float inv = real ? 1.0f / sum : 0.0f;
+#pragma unroll
+                for (int run = 0; run < A::NRUN; ++run) {
+                    float y[A::RL];
+#pragma unroll
+                    for (int k = 0; k < A::RL; ++k) {
+                        y[k] = real ? o[nr][run * (A::RL / 2) + k / 2][(k & 1) * 2 + e] * inv : 0.0f;
+                        if (!(fabsf(y[k]) <= 3.4028234663852886e38f)) bits = SPEC_DEV_RANGE;
+                    }
+                    const int d0 = run * 8 * A::RL + g * A::RL;
+                    if constexpr (IO == SPEC_IO_F32) {
+#pragma unroll
+                        for (int k = 0; k < A::RL; k += 4)
+                            *reinterpret_cast<float4*>(dst + d0 + k) =
+                                make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < A::RL; k += 8)
+                            *reinterpret_cast<uint4*>(dst + d0 + k) =
+                                make_uint4(packb(y[k], y[k + 1]), packb(y[k + 2], y[k + 3]),
+                                           packb(y[k + 4], y[k + 5]), packb(y[k + 6], y[k + 7]));
+                    }
+                }
+            }
+        if (bits) raise_status(p.ws, bits);
+    };
+
+    long long gpos = g0;                 // global index of the present granule
+    while (wk.left > 0) {
+        const int hk = wk.seg / p.rtg, rg = wk.seg % p.rtg;
+        const int row0 = (rg * p.rtc + rt) * rows_tile;
+        const int cnt = wk.count();
+        // ---- limits and Q of this warp's rows
+        int lim_min = 0, lim_max = 0;
+        if (row0 < wk.rq.n * p.G) {
+            const int last = min(row0 + rows_tile, wk.rq.n * p.G) - 1;
+            lim_min = min(wk.rq.L + row0 / p.G + 1, cap);
+            lim_max = min(wk.rq.L + last / p.G + 1, cap);
+        }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = (row0 + nr * 8 + 2 * t + e) / p.G;
+                lim[nr][e] = i < wk.rq.n ? min(wk.rq.L + i + 1, cap) : 0x7fffffff;
+            }
+            const int r = row0 + nr * 8 + g;
+            const int i = r / p.G;
+            const bool real = i < wk.rq.n;
+            const size_t qo = real ? (((size_t)wk.b * p.T + i) * p.Hq + hk * p.G + r % p.G) * D : 0;
+            if constexpr (!A::Q8 && !A::F32) {
+                const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + qo;
+#pragma unroll
+                for (int j = 0; j < A::KCH; ++j) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (real) u = *reinterpret_cast<const uint4*>(qp + (t + 4 * j) * 8);
+                    qf[nr][0][j][0] = u.x;
+                    qf[nr][0][j][1] = u.y;
+                    qf[nr][0][j][2] = u.z;
+                    qf[nr][0][j][3] = u.w;
+                }
+                rowf[nr][0] = rowf[nr][1] = p.qk_scale;
+            } else if constexpr (A::F32) {
+                const float* qp = static_cast<const float*>(p.q) + qo;
+#pragma unroll
+                for (int j = 0; j < A::KCH; ++j) {
+                    float4 u = make_float4(0, 0, 0, 0);
+                    if (real) u = *reinterpret_cast<const float4*>(qp + (t + 4 * j) * 4);
+                    split_tf32(u.x, qf[nr][0][j][0], qf[nr][1][j][0]);
+                    split_tf32(u.y, qf[nr][0][j][1], qf[nr][1][j][1]);
+                    split_tf32(u.z, qf[nr][0][j][2], qf[nr][1][j][2]);
+                    split_tf32(u.w, qf[nr][0][j][3], qf[nr][1][j][3]);
+                }
+                rowf[nr][0] = rowf[nr][1] = p.qk_scale;
+            } else {
+                // fp16 with the row scaled by a power of two so that its largest
+                // value is in [2^14, 2^15): bf16 values down to 2^-28 of it keep
+                // every bit, fp32 ones go in two parts
+                float y[A::KCH][16], amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < A::KCH; ++j) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[j][k] = 0.0f;
+                    if (real) {
+                        if constexpr (IO == SPEC_IO_BF16) {
+                            const uint4* qp = reinterpret_cast<const uint4*>(
+                                static_cast<const __nv_bfloat16*>(p.q) + qo + (t + 4 * j) * 16);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint4 u = qp[c];
+                                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    y[j][8 * c + 2 * k] = lo_b(w[k]);
+                                    y[j][8 * c + 2 * k + 1] = hi_b(w[k]);
+                                }
+                            }
+                        } else {
+                            const float4* qp = reinterpret_cast<const float4*>(
+                                static_cast<const float*>(p.q) + qo + (t + 4 * j) * 16);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const float4 u = qp[c];
+                                y[j][4 * c] = u.x;
+                                y[j][4 * c + 1] = u.y;
+                                y[j][4 * c + 2] = u.z;
+                                y[j][4 * c + 3] = u.w;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(y[j][k]));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // 2^(14 - exponent), within what fp32 holds (0 and inf: 1)
+                int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+                if (!(amax > 0.0f) || ex == 128) ex = 14;
+                ex = max(ex, -100);
+                const float f = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+                const float fi = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+#pragma unroll
+                for (int j = 0; j < A::KCH; ++j)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float a = y[j][2 * k] * f, c = y[j][2 * k + 1] * f;
+                        const uint32_t h = packh(a, c);
+                        qf[nr][0][j][k] = h;
+                        if constexpr (A::QT == 2) {
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                            qf[nr][A::QT - 1][j][k] = packh(a - b.x, c - b.y);
+                        }
+                    }
+                // lane (g, t) made row g; it needs rows 2t and 2t + 1
+                rowf[nr][0] = p.qk_scale * __shfl_sync(0xffffffffu, fi, 8 * t);
+                rowf[nr][1] = p.qk_scale * __shfl_sync(0xffffffffu, fi, 8 * t + 4);
+            }
+        }
+        clear();
+        // ---- the granules
+        for (int base = 0; base < cnt; base += SG) {
+            if (!mbar_wait(&full[st], use & 1, &abort_flag)) {
+                abort_flag = 1;
+                if (lane == 0) raise_status(p.ws, SPEC_DEV_TIMEOUT);
+            }
+            __syncwarp();
+            const uint32_t have = flags[st];
+#pragma unroll 1
+            for (int sl = 0; sl < SG; ++sl) {
+                const int gi = base + sl;
+                if (gi % KW != kw || gi >= cnt || !((have >> sl) & 1u)) continue;
+                const int kb = (wk.pos + gi) * GK;
+                if (kb < lim_max) granule(kb, sl, lim_min, lim_max);
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&empty[st]);
+            if (++st == p.stages) {
+                st = 0;
+                ++use;
+            }
+        }
+        // ---- the segment's end
+        join_warps();
+        if (cnt == wk.rq.ng) {
+            if (kw == 0) write_out(hk, row0);
+        } else {
+            constexpr int PO = NR * A::NT * 32, PM = NR * 32;
+            const long long s0 = gpos - wk.pos, s1 = s0 + wk.rq.ng;
+            const int c0 = owner(s0, units, n_cta), c1 = owner(s1 - 1, units, n_cta);
+            const long long start0 = units * c0 / n_cta;
+            auto slot = [&](int c) { return 2 * c + (c == c0 && s0 > start0 ? 1 : 0); };
+            // lanes whose rows the tile does not have write and read nothing
+            bool in[NR];
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) in[nr] = row0 + nr * 8 + 2 * t < wk.rq.n * p.G;
+            if (kw == 0) {
+                const size_t at = (size_t)slot(blockIdx.x) * p.rtc + rt;
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    if (!in[nr]) continue;
+                    __stcg(p.part_ml + at * PM + nr * 32 + lane,
+                           make_float4(m[nr][0], m[nr][1], l[nr][0], l[nr][1]));
+#pragma unroll
+                    for (int i = 0; i < A::NT; ++i)
+                        __stcg(p.part_o + at * PO + (nr * A::NT + i) * 32 + lane,
+                               make_float4(o[nr][i][0], o[nr][i][1], o[nr][i][2], o[nr][i][3]));
+                }
+                __threadfence();
+            }
+            bar();
+            if (tid == 0) {
+                uint32_t* tk = p.tickets + (size_t)wk.b * hr + wk.seg;
+                const uint32_t n = (uint32_t)(c1 - c0 + 1);
+                const bool last = atomicAdd(tk, 1u) == n - 1;
+                if (last) *tk = 0;                       // for the next call
+                last_flag = last;
+                __threadfence();
+            }
+            bar();
+            if (last_flag) {
+                clear();
+                for (int c = c0 + kw; c <= c1; c += KW) {
+                    const size_t at = (size_t)slot(c) * p.rtc + rt;
+                    float m2[NR][2], l2[NR][2];
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        float4 x = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+                        if (in[nr]) x = __ldcg(p.part_ml + at * PM + nr * 32 + lane);
+                        m2[nr][0] = x.x;
+                        m2[nr][1] = x.y;
+                        l2[nr][0] = x.z;
+                        l2[nr][1] = x.w;
+                    }
+                    join(m2, l2, [&](int nr, int i) {
+                        return in[nr] ? __ldcg(p.part_o + at * PO + (nr * A::NT + i) * 32 + lane)
+                                      : make_float4(0, 0, 0, 0);
+                    });
+                }
+                join_warps();
+                if (kw == 0) write_out(hk, row0);
+            }
+            bar();                                       // last_flag and buf are free again
+        }
+        gpos += cnt;
+        wk.next(p, hr, cnt);
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// A pool as bytes [n_pages][Hkv page][row bytes], boxes of 16 rows.
+template <class A> bool pool_map(CUtensorMap* m, const spec_paged_cfg& c, const void* base) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t rows = (cuuint64_t)c.Hkv * c.page;
+    const cuuint64_t dims[3] = {(cuuint64_t)A::ROWB, rows, (cuuint64_t)c.n_pages};
+    const cuuint64_t str[2] = {(cuuint64_t)A::ROWB, rows * A::ROWB};
+    const cuuint32_t box[3] = {(cuuint32_t)A::SW, (cuuint32_t)GK, 1}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               A::SW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int SMEM_MAX = 226 * 1024;
+
+template <int IO, int KV, int D, int NR, int W>
+cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
+                        const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
+    using A = At<IO, KV, D>;
+    const int sms = device_sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const PagedWs w = paged_ws_layout(c, sms);
+    CUtensorMap mk, mv;
+    if (!pool_map<A>(&mk, c, kv.k_pages) || !pool_map<A>(&mv, c, kv.v_pages))
+        return cudaErrorInvalidValue;
+    AttnParams p{};
+    p.pm = page_map(c, kv);
+    p.q = q;
+    p.k_scale = kv.k_scale;
+    p.v_scale = kv.v_scale;
+    p.n_new = n_new;
+    p.o = o;
+    p.ws = ws;
+    p.tickets = ws_ptr<uint32_t>(ws, w.ticket_off);
+    p.part_o = ws_ptr<float4>(ws, w.part_o_off);
+    p.part_ml = ws_ptr<float4>(ws, w.part_ml_off);
+    p.B = c.B;
+    p.T = c.T;
+    p.Hq = c.Hq;
+    p.G = c.Hq / c.Hkv;
+    p.rtc = w.rtc;
+    p.rtg = w.rtg;
+    p.min_granules = 8;
+    p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
+    const int fixed = 1024 + W / 2 * NR * (A::NT + 1) * 32 * 16;
+    const int per_stage = A::STAGE + (A::Q8 ? 2 * SK * 4 : 0);
+    p.stages = (SMEM_MAX - fixed) / per_stage;
+    if (p.stages > 16) p.stages = 16;
+    const int smem = fixed + p.stages * per_stage;
+    auto kern = attn_paged<IO, KV, D, NR, W>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // at most every granule of a full table
+    const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * (((int64_t)c.max_pages * c.page) / GK);
+    const int grid = (int)(most < sms ? most : sms);
+    return launch_k(false, kern, dim3(grid), dim3(32 * (W + 1)), smem, st, mk, mv, p);
 }
 
 template <int IO, int KV, int D>
 cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
                    const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
-    using T = typename io_t<IO>::T;
-    const int64_t ctas = ((int64_t)c.B * c.T * c.Hq + WARPS - 1) / WARPS;
-    return launch_k(false, attn_rows<IO, KV, D>, dim3((unsigned)ctas), dim3(32 * WARPS), 0, st,
-                    page_map(c, kv), c.B, c.T, c.Hq, static_cast<const T*>(q), kv.k_pages,
-                    kv.v_pages, kv.k_scale, kv.v_scale, n_new, static_cast<T*>(o),
-                    1.0f / sqrtf((float)D), ws);
+    // one more warp issues the copies: 16 or 8 in all share the registers
+    // evenly (128 or 255 each); row tiles in a CTA must divide the warps
+    constexpr bool wide = IO == SPEC_IO_BF16;
+    if (paged_row_tiles(c).nr == 1)
+        return attn_launch<IO, KV, D, 1, wide ? 15 : 7>(c, kv, q, n_new, o, ws, st);
+    return attn_launch<IO, KV, D, 2, 8>(c, kv, q, n_new, o, ws, st);
 }
 
 }  // namespace

@@ -42,13 +42,42 @@ inline int check_draft_cfg(const spec_draft_cfg* c) {
     return ST_OK;
 }
 
-struct PagedWs {
-    size_t total;
+// How the decode attention's rows (T tokens x Hq/Hkv heads of a kv-head) are
+// tiled: nr columns of 8 rows per warp, rtc row tiles per CTA, rtg row groups.
+struct RowTiles {
+    int nr, rtc, rtg;
 };
 
-inline PagedWs paged_ws_layout(const spec_paged_cfg&, int) {
+inline RowTiles paged_row_tiles(const spec_paged_cfg& c) {
+    const int64_t rows = (int64_t)c.T * (c.Hq / c.Hkv);
+    RowTiles r{};
+    r.nr = rows <= 8 ? 1 : 2;
+    const int64_t tiles = (rows + 8 * r.nr - 1) / (8 * r.nr);
+    r.rtc = tiles <= 1 ? 1 : (tiles <= 2 ? 2 : 4);
+    r.rtg = (int)((tiles + r.rtc - 1) / r.rtc);
+    return r;
+}
+
+// Status word; a ticket per (request, kv-head, row group); two parts per CTA
+// (a CTA's first and last segment may be shared with its neighbours):
+// fp32 outputs in the warps' register order, and (max, max, sum, sum) per lane.
+struct PagedWs {
+    size_t ticket_off, part_o_off, part_ml_off, total;
+    int rtc, rtg;
+};
+
+inline PagedWs paged_ws_layout(const spec_paged_cfg& c, int num_sms) {
     PagedWs w{};
-    w.total = 256;                       // status word + reserve
+    w.total = 256;
+    w.ticket_off = w.total;
+    if (c.T > SPEC_MAX_ROWS) return w;       // no attention with so many rows
+    const RowTiles r = paged_row_tiles(c);
+    w.rtc = r.rtc;
+    w.rtg = r.rtg;
+    const size_t tiles = (size_t)2 * num_sms * r.rtc * r.nr;
+    w.part_o_off = align_up(w.ticket_off + sizeof(uint32_t) * (size_t)c.B * c.Hkv * r.rtg, 256);
+    w.part_ml_off = align_up(w.part_o_off + tiles * 8 * c.D * sizeof(float), 256);
+    w.total = align_up(w.part_ml_off + tiles * 32 * 16, 256);
     return w;
 }
 
