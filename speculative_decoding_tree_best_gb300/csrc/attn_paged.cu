@@ -26,7 +26,7 @@
 // segment cut between CTAs leaves parts in the workspace, and the CTA that
 // finishes last (a ticket per segment) joins them in their order.  In a CTA
 // one warp issues TMA copies (16 rows x 128 bytes, 128-byte swizzle) into a ring of
-// 64-key stages, and W warps take granules from it in turn.  A row's 16-byte
+// granules, and W warps take them in turn.  A row's 16-byte
 // chunks go to lanes so that the products need no transposition of K, and of
 // V only byte permutes; the row order below makes every 128-bit shared load
 // free of bank conflicts under the swizzle.
@@ -44,8 +44,7 @@ using tc::mbar_wait;
 using tc::smem_u32;
 
 constexpr int GK = 16;                 // keys per granule
-constexpr int SG = 4;                  // granules per stage
-constexpr int SK = GK * SG;            // keys per stage
+constexpr int MAX_SLOTS = 64;          // granules in a CTA's ring, at most
 
 // ---- instruction wrappers -------------------------------------------------------------
 
@@ -142,16 +141,16 @@ template <int IO, int KV, int D> struct At {
     static constexpr int QT = (Q8 && IO == SPEC_IO_F32) || F32 ? 2 : 1;   // parts of a Q value
     static constexpr int QR = Q8 ? 8 : 4;               // Q registers per chunk and part
     static constexpr int PT = (Q8 && IO == SPEC_IO_BF16) ? 1 : 2;   // parts of a weight
-    static constexpr int STAGE_KV = SK * ROWB;          // bytes of K (or V) in a stage
-    static constexpr int STAGE = 2 * STAGE_KV;
+    static constexpr int SLOT_KV = GK * ROWB;           // bytes of K (or V) of a granule
+    static constexpr int SLOT = 2 * SLOT_KV;
 };
 
-// byte offset of 16-byte chunk c of key row r in a stage's K (or V) region
+// byte offset of 16-byte chunk c of key row r in a slot's K (or V) region
 template <class A> __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
     constexpr int CPB = A::SW / 16;
     const int blk = c / CPB, cc = c % CPB;
     const int x = A::SW == 128 ? (r & 7) : ((r >> 1) & 3);
-    return (uint32_t)(blk * SK * A::SW + r * A::SW + ((cc ^ x) << 4));
+    return (uint32_t)(blk * GK * A::SW + r * A::SW + ((cc ^ x) << 4));
 }
 
 struct AttnParams {
@@ -167,7 +166,7 @@ struct AttnParams {
     float4* part_ml;
     int B, T, Hq, G;
     int rtc, rtg;            // row tiles per CTA, row groups per (request, kv-head)
-    int stages;
+    int slots;
     int min_granules;        // per CTA
     float qk_scale;          // log2(e) / sqrt(D)
 };
@@ -224,10 +223,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
            const __grid_constant__ AttnParams p) {
     using A = At<IO, KV, D>;
     constexpr int NTH = 32 * (W + 1);
-    constexpr int MAXST = 16;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[MAXST], empty[MAXST];
-    __shared__ uint32_t flags[MAXST];
+    __shared__ uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
+    __shared__ uint32_t flags[MAX_SLOTS];
     __shared__ long long wsum[W + 1];
     __shared__ long long first_off;
     __shared__ int first_b;
@@ -237,15 +235,15 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int hr = p.pm.Hkv * p.rtg;
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    float* scales = reinterpret_cast<float*>(ring + (size_t)p.stages * A::STAGE);
-    float4* buf = reinterpret_cast<float4*>(scales + (A::Q8 ? p.stages * 2 * SK : 0));
+    float* scales = reinterpret_cast<float*>(ring + (size_t)p.slots * A::SLOT);
+    float4* buf = reinterpret_cast<float4*>(scales + (A::Q8 ? p.slots * 2 * GK : 0));
 
     // ---- this CTA's share of the granules
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < p.stages; ++s) {
+        for (int s = 0; s < p.slots; ++s) {
             tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&empty[s], W);
+            tc::mbar_init(&empty[s], p.rtc);
         }
         tc::fence_mbar_init();
     }
@@ -302,8 +300,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     const int cap = p.pm.cap();
 
     if (warp == W) {
-        // ---- producer: page ids for eight stages at once, one granule per lane
-        int st = 0, use = 0, issued = 0;
+        // ---- producer: one granule per lane, four lanes at a time; the page
+        // ids of 32 granules are fetched at once
+        int slot0 = 0, use0 = 0;         // of the batch's first granule
         bool ok = true;
         uint32_t bad = 0;
         while (wk.left > 0 && ok) {
@@ -318,52 +317,76 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             for (int base = 0; base < cnt && ok; base += 32) {
                 const int gi = base + lane;
                 const int key = (wk.pos + gi) * GK;
-                int64_t row = -1;
+                int page = -1;
                 if (gi < cnt && key < end) {
-                    row = p.pm.row(wk.b, key, hk);
-                    if (row < 0) bad = SPEC_DEV_BADPAGE;
+                    page = p.pm.table[(size_t)wk.b * p.pm.max_pages + (key >> p.pm.sh)];
+                    if ((unsigned)page >= (unsigned)p.pm.n_pages) {
+                        bad = SPEC_DEV_BADPAGE;
+                        page = -1;
+                    }
                 }
-                const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
-                const int64_t prow = (int64_t)p.pm.Hkv << p.pm.sh;      // rows per page
-                const int page = row >= 0 ? (int)(row / prow) : 0;
-                const int prel = row >= 0 ? (int)(row % prow) : 0;
-                for (int u = 0; u < 8 && base + 4 * u < cnt; ++u) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], (use & 1) ^ 1,
-                                                           &abort_flag));
+                const int prow = (hk << p.pm.sh) | (key & ((1 << p.pm.sh) - 1));
+                int slot = slot0 + lane, use = use0;
+                while (slot >= p.slots) {
+                    slot -= p.slots;
+                    ++use;
+                }
+                int n = 0;                   // granules of this batch under way
+                for (; n < 32 && base + n < cnt; n += 4) {
+                    const bool turn = lane / 4 == n / 4 && gi < cnt;
+                    bool got = true;
+                    if (turn) got = mbar_wait(&empty[slot], (use & 1) ^ 1, &abort_flag);
+                    ok = __all_sync(0xffffffffu, got);
                     if (!ok) break;
-                    const uint32_t m4 = (have >> (4 * u)) & 15u;
-                    if (lane == 0) {
-                        flags[st] = m4;
+                    if (turn) {
+                        flags[slot] = page >= 0;
                         tc::mbar_arrive_expect_tx(
-                            &full[st], __popc(m4) * (2 * GK * A::ROWB + (A::Q8 ? 8 * GK : 0)));
+                            &full[slot], page >= 0 ? A::SLOT + (A::Q8 ? 8 * GK : 0) : 0);
+                        if (page >= 0) {
+                            uint8_t* kd = ring + (size_t)slot * A::SLOT;
+#pragma unroll
+                            for (int nb = 0; nb < A::NB; ++nb) {
+                                tc::tma_load_3d(kd + nb * GK * A::SW, &mk, &full[slot], nb * A::SW,
+                                                prow, page);
+                                tc::tma_load_3d(kd + A::SLOT_KV + nb * GK * A::SW, &mv, &full[slot],
+                                                nb * A::SW, prow, page);
+                            }
+                            if constexpr (A::Q8) {
+                                const int64_t row =
+                                    (((int64_t)page * p.pm.Hkv) << p.pm.sh) + prow;
+                                float* sd = scales + slot * 2 * GK;
+#pragma unroll
+                                for (int v = 0; v < 2; ++v)
+                                    asm volatile(
+                                        "cp.async.bulk.shared::cluster.global.mbarrier::"
+                                        "complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                            smem_u32(sd + v * GK)),
+                                        "l"((v ? p.v_scale : p.k_scale) + row), "r"(4 * GK),
+                                        "r"(smem_u32(&full[slot]))
+                                        : "memory");
+                            }
+                        }
                     }
                     __syncwarp();
-                    if (lane / 4 == u && row >= 0) {
-                        uint8_t* kd = ring + (size_t)st * A::STAGE + (lane % 4) * GK * A::SW;
-#pragma unroll
-                        for (int nb = 0; nb < A::NB; ++nb) {
-                            tc::tma_load_3d(kd + nb * SK * A::SW, &mk, &full[st], nb * A::SW, prel,
-                                            page);
-                            tc::tma_load_3d(kd + A::STAGE_KV + nb * SK * A::SW, &mv, &full[st],
-                                            nb * A::SW, prel, page);
+                }
+                if (!ok) {
+                    // copies in flight land before the CTA's shared memory is
+                    // released: each slot's last issued phase
+                    if (lane < n) mbar_wait(&full[slot], use & 1, nullptr);
+                    for (int k = lane; k < p.slots; k += 32) {
+                        int s = slot0 + n + k, v = use0 - 1;   // the slots before them
+                        while (s >= p.slots) {
+                            s -= p.slots;
+                            ++v;
                         }
-                        if constexpr (A::Q8) {
-                            float* sd = scales + st * 2 * SK + (lane % 4) * GK;
-#pragma unroll
-                            for (int v = 0; v < 2; ++v)
-                                asm volatile(
-                                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::"
-                                    "bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(sd + v * SK)),
-                                    "l"((v ? p.v_scale : p.k_scale) + row), "r"(4 * GK),
-                                    "r"(smem_u32(&full[st]))
-                                    : "memory");
-                        }
+                        if (v >= 0 && k < p.slots - n) mbar_wait(&full[s], v & 1, nullptr);
                     }
-                    ++issued;
-                    if (++st == p.stages) {
-                        st = 0;
-                        ++use;
-                    }
+                    break;
+                }
+                slot0 += min(32, cnt - base);
+                while (slot0 >= p.slots) {
+                    slot0 -= p.slots;
+                    ++use0;
                 }
             }
             wk.next(p, hr, cnt);
@@ -372,9 +395,6 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         if (!ok) {
             abort_flag = 1;
             if (lane == 0) raise_status(p.ws, SPEC_DEV_TIMEOUT);
-            // copies in flight land before the CTA's shared memory is released
-            for (int j = max(0, issued - p.stages); j < issued; ++j)
-                mbar_wait(&full[j % p.stages], (j / p.stages) & 1, nullptr);
         }
         return;
     }
@@ -384,7 +404,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     const int g = lane / 4, t = lane % 4;
     const int kr = g ^ ((g & 1) << 2);                       // key row of fragment row g
     const int va = 2 * t, vb = (2 * t + 1) ^ 4;              // key rows of fragment columns 2t, 2t+1
-    int st = 0, use = 0;
+    int slot0 = 0, use0 = 0;             // of the segment portion's first granule
 
     float o[NR][A::NT][4];
     float m[NR][2], l[NR][2], rowf[NR][2];
@@ -461,18 +481,17 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
 
-    // one granule: keys [kb, kb + 16) in slot rows [16 sl, 16 sl + 16) of stage `st`
-    auto granule = [&](int kb, int sl, int lim_min, int lim_max) {
-        const uint32_t ks = smem_u32(ring + (size_t)st * A::STAGE);
-        const uint32_t vs = ks + A::STAGE_KV;
-        const int rk = sl * GK + kr;
+    // one granule: keys [kb, kb + 16) in ring slot `slot`
+    auto granule = [&](int kb, int slot, int lim_min, int lim_max) {
+        const uint32_t ks = smem_u32(ring + (size_t)slot * A::SLOT);
+        const uint32_t vs = ks + A::SLOT_KV;
         float s[NR][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) s[nr][0] = s[nr][1] = s[nr][2] = s[nr][3] = 0.0f;
 #pragma unroll
         for (int j = 0; j < A::KCH; ++j) {
-            const uint4 k0 = lds128(ks + chunk_off<A>(rk, t + 4 * j));
-            const uint4 k1 = lds128(ks + chunk_off<A>(rk + 8, t + 4 * j));
+            const uint4 k0 = lds128(ks + chunk_off<A>(kr, t + 4 * j));
+            const uint4 k1 = lds128(ks + chunk_off<A>(kr + 8, t + 4 * j));
             if constexpr (A::Q8) {
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -514,12 +533,12 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const bool masked = kb + GK > lim_min;
         float lv[2] = {0.0f, 0.0f}, kf[2] = {1.0f, 1.0f};
         if constexpr (A::Q8) {
-            const float* sc = scales + st * 2 * SK + rk;
+            const float* sc = scales + slot * 2 * GK + kr;
             kf[0] = sc[0];
             kf[1] = sc[8];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float y = sc[SK + 8 * k];
+                const float y = sc[GK + 8 * k];
                 lv[k] = y >= 0.0f && y < 0x1p-126f ? -126.0f : __log2f(y);   // a scale of 0
             }
         }
@@ -654,26 +673,25 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     }
                 }
             };
-            const int rv = sl * GK;
 #pragma unroll
             for (int j = 0; j < A::VL; ++j) {
                 uint4 v0, v1, v2, v3;
                 if constexpr (A::ROWB == 64) {
                     // 8 bytes per lane and row
                     const uint32_t h8 = (g & 1) * 8;
-                    const uint2 u0 = lds64(vs + chunk_off<A>(rv + va, g >> 1) + h8);
-                    const uint2 u1 = lds64(vs + chunk_off<A>(rv + vb, g >> 1) + h8);
-                    const uint2 u2 = lds64(vs + chunk_off<A>(rv + va + 8, g >> 1) + h8);
-                    const uint2 u3 = lds64(vs + chunk_off<A>(rv + vb + 8, g >> 1) + h8);
+                    const uint2 u0 = lds64(vs + chunk_off<A>(va, g >> 1) + h8);
+                    const uint2 u1 = lds64(vs + chunk_off<A>(vb, g >> 1) + h8);
+                    const uint2 u2 = lds64(vs + chunk_off<A>(va + 8, g >> 1) + h8);
+                    const uint2 u3 = lds64(vs + chunk_off<A>(vb + 8, g >> 1) + h8);
                     v0 = make_uint4(u0.x, u0.y, 0, 0);
                     v1 = make_uint4(u1.x, u1.y, 0, 0);
                     v2 = make_uint4(u2.x, u2.y, 0, 0);
                     v3 = make_uint4(u3.x, u3.y, 0, 0);
                 } else {
-                    v0 = lds128(vs + chunk_off<A>(rv + va, g + 8 * j));
-                    v1 = lds128(vs + chunk_off<A>(rv + vb, g + 8 * j));
-                    v2 = lds128(vs + chunk_off<A>(rv + va + 8, g + 8 * j));
-                    v3 = lds128(vs + chunk_off<A>(rv + vb + 8, g + 8 * j));
+                    v0 = lds128(vs + chunk_off<A>(va, g + 8 * j));
+                    v1 = lds128(vs + chunk_off<A>(vb, g + 8 * j));
+                    v2 = lds128(vs + chunk_off<A>(va + 8, g + 8 * j));
+                    v3 = lds128(vs + chunk_off<A>(vb + 8, g + 8 * j));
                 }
                 if (cut < GK) {
                     if (z0) v0 = zero;
@@ -734,7 +752,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         for (int c = lane; c < GK * (A::ROWB / 16); c += 32) {
             const int r = c % GK;
             if (kb + r < lim_min || kb + r >= lim_max) continue;
-            const uint4 v = lds128(vs + chunk_off<A>(sl * GK + r, c / GK));
+            const uint4 v = lds128(vs + chunk_off<A>(r, c / GK));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -912,27 +930,34 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         clear();
-        // ---- the granules
-        for (int base = 0; base < cnt; base += SG) {
-            if (!mbar_wait(&full[st], use & 1, &abort_flag)) {
+        // ---- the granules: every KW-th one
+        int slot = slot0 + kw, use = use0;
+        for (int gi = kw; gi < cnt; gi += KW, slot += KW) {
+            while (slot >= p.slots) {
+                slot -= p.slots;
+                ++use;
+            }
+            // The slot's granule before this one may be another warp's and may
+            // land later than this warp's last one: a wait for this use's copy
+            // is only good once that use is over, or its parity is the one
+            // of two uses ago.
+            bool got = use == 0 || mbar_wait(&empty[slot], (use - 1) & 1, &abort_flag);
+            got = got && mbar_wait(&full[slot], use & 1, &abort_flag);
+            if (!got) {
                 abort_flag = 1;
                 if (lane == 0) raise_status(p.ws, SPEC_DEV_TIMEOUT);
             }
             __syncwarp();
-            const uint32_t have = flags[st];
-#pragma unroll 1
-            for (int sl = 0; sl < SG; ++sl) {
-                const int gi = base + sl;
-                if (gi % KW != kw || gi >= cnt || !((have >> sl) & 1u)) continue;
-                const int kb = (wk.pos + gi) * GK;
-                if (kb < lim_max) granule(kb, sl, lim_min, lim_max);
-            }
+            const int kb = (wk.pos + gi) * GK;
+            if (flags[slot] && kb < lim_max) granule(kb, slot, lim_min, lim_max);
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&empty[st]);
-            if (++st == p.stages) {
-                st = 0;
-                ++use;
-            }
+            if (lane == 0) tc::mbar_arrive(&empty[slot]);
+        }
+        slot0 += cnt % p.slots;
+        use0 += cnt / p.slots;
+        if (slot0 >= p.slots) {
+            slot0 -= p.slots;
+            ++use0;
         }
         // ---- the segment's end
         join_warps();
@@ -1068,10 +1093,10 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.min_granules = 8;
     p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
     const int fixed = 1024 + W / 2 * NR * (A::NT + 1) * 32 * 16;
-    const int per_stage = A::STAGE + (A::Q8 ? 2 * SK * 4 : 0);
-    p.stages = (SMEM_MAX - fixed) / per_stage;
-    if (p.stages > 16) p.stages = 16;
-    const int smem = fixed + p.stages * per_stage;
+    const int per_slot = A::SLOT + (A::Q8 ? 2 * GK * 4 : 0);
+    p.slots = (SMEM_MAX - fixed) / per_slot;
+    if (p.slots > MAX_SLOTS) p.slots = MAX_SLOTS;
+    const int smem = fixed + p.slots * per_slot;
     auto kern = attn_paged<IO, KV, D, NR, W>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

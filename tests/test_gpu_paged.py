@@ -269,6 +269,17 @@ def test_one_long_request(kv):
     x.check(x.attend())
 
 
+@pytest.mark.parametrize("io,kv,D", [("bf16", "e4m3", 128), ("bf16", "io", 64), ("bf16", "io", 128),
+                                     ("f32", "io", 64)])
+def test_many_granules_per_cta(io, kv, D):
+    """Long enough that each CTA goes around its ring of copies many times."""
+    x = Case([33000, 9001, 16000], T=1, Hq=8, Hkv=8, D=D, page=64, io=io, kv=kv, seed=61)
+    x.check(x.attend())
+    x = Case([9001, 6000], T=6, Hq=24, Hkv=8, D=D, page=16, io=io, kv=kv, seed=62)
+    x.check(x.attend())
+    assert x.status() == 0
+
+
 def test_scales_of_very_different_rows():
     """Weights and scales far apart: a large key scale, tiny and huge values."""
     x = Case([500, 700], Hq=8, Hkv=2, D=128, page=32, kv="e4m3", seed=7, spread=4.0)
