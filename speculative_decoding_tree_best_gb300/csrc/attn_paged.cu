@@ -43,7 +43,8 @@ namespace {
 using tc::mbar_wait;
 using tc::smem_u32;
 
-constexpr int GK = 16;                 // keys per granule
+constexpr int SUB = 16;                // keys per product tile: the smallest page
+constexpr int GK = 32;                 // keys per granule
 constexpr int MAX_SLOTS = 64;          // granules in a CTA's ring, at most
 
 // ---- instruction wrappers -------------------------------------------------------------
@@ -95,10 +96,18 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
     return v;
 }
-// two e4m3 codes (the low or high half of x) as f16x2: exact
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t x) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// four e4m3 codes as two f16x2 (codes 0, 1 and 2, 3): exact
+__device__ __forceinline__ void e4m3x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+// log2 of a scale; 0 counts as 2^-126, a NaN stays
+__device__ __forceinline__ float log2_scale(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00800000;\n\tlg2.approx.f32 %0, %0;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ uint32_t packh(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -167,6 +176,7 @@ struct AttnParams {
     int B, T, Hq, G;
     int rtc, rtg;            // row tiles per CTA, row groups per (request, kv-head)
     int slots;
+    int box;                 // rows per copy: GK, or SUB where pages are that small
     int min_granules;        // per CTA
     float qk_scale;          // log2(e) / sqrt(D)
 };
@@ -317,15 +327,22 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             for (int base = 0; base < cnt && ok; base += 32) {
                 const int gi = base + lane;
                 const int key = (wk.pos + gi) * GK;
-                int page = -1;
-                if (gi < cnt && key < end) {
-                    page = p.pm.table[(size_t)wk.b * p.pm.max_pages + (key >> p.pm.sh)];
-                    if ((unsigned)page >= (unsigned)p.pm.n_pages) {
-                        bad = SPEC_DEV_BADPAGE;
-                        page = -1;
+                int page[2] = {-1, -1};
+                if (gi < cnt) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int at = key + h * SUB;
+                        if (at >= end) continue;
+                        page[h] = p.pm.table[(size_t)wk.b * p.pm.max_pages + (at >> p.pm.sh)];
+                        if ((unsigned)page[h] >= (unsigned)p.pm.n_pages) {
+                            bad = SPEC_DEV_BADPAGE;
+                            page[h] = -1;
+                        }
                     }
+                    // a copy of GK rows brings the whole granule
+                    if (p.box == GK) page[1] = page[0];
                 }
-                const int prow = (hk << p.pm.sh) | (key & ((1 << p.pm.sh) - 1));
+                const uint32_t have = (page[0] >= 0 ? 1u : 0u) | (page[1] >= 0 ? 2u : 0u);
                 int slot = slot0 + lane, use = use0;
                 while (slot >= p.slots) {
                     slot -= p.slots;
@@ -339,29 +356,34 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     ok = __all_sync(0xffffffffu, got);
                     if (!ok) break;
                     if (turn) {
-                        flags[slot] = page >= 0;
+                        flags[slot] = have;
                         tc::mbar_arrive_expect_tx(
-                            &full[slot], page >= 0 ? A::SLOT + (A::Q8 ? 8 * GK : 0) : 0);
-                        if (page >= 0) {
-                            uint8_t* kd = ring + (size_t)slot * A::SLOT;
+                            &full[slot],
+                            __popc(have) * (A::SLOT / 2 + (A::Q8 ? 8 * SUB : 0)));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (page[h] < 0 || (h == 1 && p.box == GK)) continue;
+                            const int prow =
+                                (hk << p.pm.sh) | ((key + h * SUB) & ((1 << p.pm.sh) - 1));
+                            uint8_t* kd = ring + (size_t)slot * A::SLOT + h * SUB * A::SW;
 #pragma unroll
                             for (int nb = 0; nb < A::NB; ++nb) {
                                 tc::tma_load_3d(kd + nb * GK * A::SW, &mk, &full[slot], nb * A::SW,
-                                                prow, page);
+                                                prow, page[h]);
                                 tc::tma_load_3d(kd + A::SLOT_KV + nb * GK * A::SW, &mv, &full[slot],
-                                                nb * A::SW, prow, page);
+                                                nb * A::SW, prow, page[h]);
                             }
                             if constexpr (A::Q8) {
                                 const int64_t row =
-                                    (((int64_t)page * p.pm.Hkv) << p.pm.sh) + prow;
-                                float* sd = scales + slot * 2 * GK;
+                                    (((int64_t)page[h] * p.pm.Hkv) << p.pm.sh) + prow;
+                                float* sd = scales + slot * 2 * GK + h * SUB;
 #pragma unroll
                                 for (int v = 0; v < 2; ++v)
                                     asm volatile(
                                         "cp.async.bulk.shared::cluster.global.mbarrier::"
                                         "complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                             smem_u32(sd + v * GK)),
-                                        "l"((v ? p.v_scale : p.k_scale) + row), "r"(4 * GK),
+                                        "l"((v ? p.v_scale : p.k_scale) + row), "r"(4 * p.box),
                                         "r"(smem_u32(&full[slot]))
                                         : "memory");
                             }
@@ -400,6 +422,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     }
 
     // ---- consumers
+    // key warp kw of KW, row tile rt; warps beyond KW rtc only keep the barriers
     const int rt = warp % p.rtc, kw = warp / p.rtc, KW = W / p.rtc;
     const int g = lane / 4, t = lane % 4;
     const int kr = g ^ ((g & 1) << 2);                       // key row of fragment row g
@@ -481,94 +504,111 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
 
-    // one granule: keys [kb, kb + 16) in ring slot `slot`
-    auto granule = [&](int kb, int slot, int lim_min, int lim_max) {
+    // one granule: keys [kb, kb + GK) in ring slot `slot`; have: its halves in the pool
+    auto granule = [&](int kb, int slot, uint32_t have, int lim_min, int lim_max) {
         const uint32_t ks = smem_u32(ring + (size_t)slot * A::SLOT);
         const uint32_t vs = ks + A::SLOT_KV;
-        float s[NR][4];
+        constexpr int NS = GK / SUB;
+        float x[NR][NS][4];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) s[nr][0] = s[nr][1] = s[nr][2] = s[nr][3] = 0.0f;
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int h = 0; h < NS; ++h) x[nr][h][0] = x[nr][h][1] = x[nr][h][2] = x[nr][h][3] = 0.0f;
 #pragma unroll
         for (int j = 0; j < A::KCH; ++j) {
-            const uint4 k0 = lds128(ks + chunk_off<A>(kr, t + 4 * j));
-            const uint4 k1 = lds128(ks + chunk_off<A>(kr + 8, t + 4 * j));
-            if constexpr (A::Q8) {
+#pragma unroll
+            for (int h = 0; h < NS; ++h) {
+                const uint4 k0 = lds128(ks + chunk_off<A>(h * SUB + kr, t + 4 * j));
+                const uint4 k1 = lds128(ks + chunk_off<A>(h * SUB + kr + 8, t + 4 * j));
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+                if constexpr (A::Q8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a[4] = {e4m3x2(w0[i]), e4m3x2(w1[i]), e4m3x2(w0[i] >> 16),
-                                           e4m3x2(w1[i] >> 16)};
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a[4];
+                        e4m3x4(w0[i], a[0], a[2]);
+                        e4m3x4(w1[i], a[1], a[3]);
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
+                        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int q = 0; q < A::QT; ++q)
-                            mma_f16_16816(s[nr], a, qf[nr][q][j][2 * i], qf[nr][q][j][2 * i + 1]);
-                }
-            } else if constexpr (A::F32) {
-                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+                            for (int q = 0; q < A::QT; ++q)
+                                mma_f16_16816(x[nr][h], a, qf[nr][q][j][2 * i],
+                                              qf[nr][q][j][2 * i + 1]);
+                    }
+                } else if constexpr (A::F32) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t ah[4], al[4];
-                    split_tf32(__uint_as_float(w0[2 * i]), ah[0], al[0]);
-                    split_tf32(__uint_as_float(w1[2 * i]), ah[1], al[1]);
-                    split_tf32(__uint_as_float(w0[2 * i + 1]), ah[2], al[2]);
-                    split_tf32(__uint_as_float(w1[2 * i + 1]), ah[3], al[3]);
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t ah[4], al[4];
+                        split_tf32(__uint_as_float(w0[2 * i]), ah[0], al[0]);
+                        split_tf32(__uint_as_float(w1[2 * i]), ah[1], al[1]);
+                        split_tf32(__uint_as_float(w0[2 * i + 1]), ah[2], al[2]);
+                        split_tf32(__uint_as_float(w1[2 * i + 1]), ah[3], al[3]);
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) {
+                            mma_tf32_1688(x[nr][h], ah, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
+                            mma_tf32_1688(x[nr][h], ah, qf[nr][1][j][2 * i], qf[nr][1][j][2 * i + 1]);
+                            mma_tf32_1688(x[nr][h], al, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
+                        }
+                    }
+                } else {
+                    const uint32_t a0[4] = {w0[0], w1[0], w0[1], w1[1]};
+                    const uint32_t a1[4] = {w0[2], w1[2], w0[3], w1[3]};
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr) {
-                        mma_tf32_1688(s[nr], ah, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
-                        mma_tf32_1688(s[nr], ah, qf[nr][1][j][2 * i], qf[nr][1][j][2 * i + 1]);
-                        mma_tf32_1688(s[nr], al, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
+                        mma_bf16_16816(x[nr][h], a0, qf[nr][0][j][0], qf[nr][0][j][1]);
+                        mma_bf16_16816(x[nr][h], a1, qf[nr][0][j][2], qf[nr][0][j][3]);
                     }
                 }
-            } else {
-                const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y}, a1[4] = {k0.z, k1.z, k0.w, k1.w};
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    mma_bf16_16816(s[nr], a0, qf[nr][0][j][0], qf[nr][0][j][1]);
-                    mma_bf16_16816(s[nr], a1, qf[nr][0][j][2], qf[nr][0][j][3]);
-                }
             }
         }
-        // scores in log2 units; a = what the V weights go by
-        const bool masked = kb + GK > lim_min;
-        float lv[2] = {0.0f, 0.0f}, kf[2] = {1.0f, 1.0f};
-        if constexpr (A::Q8) {
-            const float* sc = scales + slot * 2 * GK + kr;
-            kf[0] = sc[0];
-            kf[1] = sc[8];
+        // scores in log2 units, -inf where the row does not see the key
+        const bool masked = kb + GK > lim_min || have != 3u;
+        float lv[NS][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float y = sc[GK + 8 * k];
-                lv[k] = y >= 0.0f && y < 0x1p-126f ? -126.0f : __log2f(y);   // a scale of 0
+        for (int h = 0; h < NS; ++h) {
+            float kf[2] = {1.0f, 1.0f};
+            if constexpr (A::Q8) {
+                const float* sc = scales + slot * 2 * GK + h * SUB + kr;
+                kf[0] = sc[0];
+                kf[1] = sc[8];
+                lv[h][0] = log2_scale(sc[GK]);
+                lv[h][1] = log2_scale(sc[GK + 8]);
             }
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[nr][h][e] *= A::Q8 ? rowf[nr][e & 1] * kf[e >> 1] : rowf[nr][e & 1];
         }
-        float x[NR][4];
+        if (masked) {
+#pragma unroll
+            for (int h = 0; h < NS; ++h)
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (kb + h * SUB + kr + 8 * (e >> 1) >= lim[nr][e & 1] || !((have >> h) & 1u))
+                            x[nr][h][e] = -INFINITY;
+        }
+        // the running maximum of what the V weights go by (fmaxf passes over a NaN)
         bool grow = false;
         float nm[NR][2];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[nr][e] = s[nr][e] * (A::Q8 ? rowf[nr][e & 1] * kf[e >> 1] : rowf[nr][e & 1]);
-                if (masked && kb + kr + 8 * (e >> 1) >= lim[nr][e & 1]) x[nr][e] = -INFINITY;
-            }
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float y;
-                if constexpr (A::Q8) {
-                    // a masked key's scale may be anything
-                    const float a0 = x[nr][e] == -INFINITY ? -INFINITY : x[nr][e] + lv[0];
-                    const float a1 = x[nr][2 + e] == -INFINITY ? -INFINITY : x[nr][2 + e] + lv[1];
-                    y = fmaxf(a0, a1);
-                } else {
-                    y = fmaxf(x[nr][e], x[nr][2 + e]);
+                float y = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < NS; ++h) {
+                    if constexpr (A::Q8)
+                        y = fmaxf(y, fmaxf(x[nr][h][e] + lv[h][0], x[nr][h][2 + e] + lv[h][1]));
+                    else
+                        y = fmaxf(y, fmaxf(x[nr][h][e], x[nr][h][2 + e]));
                 }
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
                 nm[nr][e] = fmaxf(m[nr][e], y);
                 grow |= nm[nr][e] > m[nr][e];
             }
-        }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
@@ -586,191 +626,191 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         // weights, their sum, and the second product's B operand
-        uint32_t wb[NR][A::PT][A::F32 ? 4 : 2];
+        uint32_t wb[NR][NS][A::PT][A::F32 ? 4 : 2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            float w[4];
+            const float b0 = m[nr][0] == -INFINITY ? 0.0f : m[nr][0];
+            const float b1 = m[nr][1] == -INFINITY ? 0.0f : m[nr][1];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float base = m[nr][e & 1] == -INFINITY ? 0.0f : m[nr][e & 1];
-                const float d = x[nr][e] - base;
-                const float pl = ex2(d);
-                l[nr][e & 1] += pl;
-                if constexpr (A::Q8)
-                    w[e] = x[nr][e] == -INFINITY ? 0.0f : ex2(d + lv[e >> 1]);
-                else
-                    w[e] = pl;
-            }
-            if constexpr (A::F32) {
-                // 32-bit transposes as two 16-bit ones; columns = keys va, vb (+ 8)
+            for (int h = 0; h < NS; ++h) {
+                float w[4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t a = __float_as_uint(w[2 * k]), c = __float_as_uint(w[2 * k + 1]);
-                    const uint32_t th = movm(__byte_perm(a, c, 0x7632));
-                    const uint32_t tl = movm(__byte_perm(a, c, 0x5410));
-                    split_tf32(__uint_as_float(__byte_perm(tl, th, 0x5410)), wb[nr][0][2 * k],
-                               wb[nr][1][2 * k]);
-                    split_tf32(__uint_as_float(__byte_perm(tl, th, 0x7632)), wb[nr][0][2 * k + 1],
-                               wb[nr][1][2 * k + 1]);
+                for (int e = 0; e < 4; ++e) {
+                    const float d = x[nr][h][e] - ((e & 1) ? b1 : b0);
+                    const float pl = ex2(d);
+                    l[nr][e & 1] += pl;
+                    w[e] = A::Q8 ? ex2(d + lv[h][e >> 1]) : pl;
+                    // the scale of a key that is not seen may be anything
+                    if (A::Q8 && masked && x[nr][h][e] == -INFINITY) w[e] = 0.0f;
                 }
-            } else {
+                if constexpr (A::F32) {
+                    // 32-bit transposes as two 16-bit ones; columns = keys va, vb (+ 8)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if constexpr (A::Q8) {
-                        const uint32_t h = packh(w[2 * k], w[2 * k + 1]);
-                        wb[nr][0][k] = movm(h);
-                        if constexpr (A::PT == 2) {
-                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                            wb[nr][A::PT - 1][k] = movm(packh(w[2 * k] - b.x, w[2 * k + 1] - b.y));
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t a = __float_as_uint(w[2 * k]);
+                        const uint32_t c = __float_as_uint(w[2 * k + 1]);
+                        const uint32_t th = movm(__byte_perm(a, c, 0x7632));
+                        const uint32_t tl = movm(__byte_perm(a, c, 0x5410));
+                        split_tf32(__uint_as_float(__byte_perm(tl, th, 0x5410)),
+                                   wb[nr][h][0][2 * k], wb[nr][h][1][2 * k]);
+                        split_tf32(__uint_as_float(__byte_perm(tl, th, 0x7632)),
+                                   wb[nr][h][0][2 * k + 1], wb[nr][h][1][2 * k + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if constexpr (A::Q8) {
+                            const uint32_t c = packh(w[2 * k], w[2 * k + 1]);
+                            wb[nr][h][0][k] = movm(c);
+                            if constexpr (A::PT == 2) {
+                                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&c));
+                                wb[nr][h][A::PT - 1][k] =
+                                    movm(packh(w[2 * k] - b.x, w[2 * k + 1] - b.y));
+                            }
+                        } else {
+                            const uint32_t c = packb(w[2 * k], w[2 * k + 1]);
+                            wb[nr][h][0][k] = movm(c);
+                            wb[nr][h][A::PT - 1][k] =
+                                movm(packb(w[2 * k] - lo_b(c), w[2 * k + 1] - hi_b(c)));
                         }
-                    } else {
-                        const uint32_t h = packb(w[2 * k], w[2 * k + 1]);
-                        wb[nr][0][k] = movm(h);
-                        wb[nr][A::PT - 1][k] = movm(packb(w[2 * k] - lo_b(h), w[2 * k + 1] - hi_b(h)));
                     }
                 }
             }
         }
-        // O^T += V^T W^T.  cut: key rows of the granule from there on count as
-        // zeros (their weights are 0, but 0 x inf is not).  only >= 0: just the
-        // rows whose limit is `only`.
-        auto pv = [&](int cut, int only) {
-            const bool z0 = va >= cut, z1 = vb >= cut, z2 = va + 8 >= cut, z3 = vb + 8 >= cut;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            auto acc = [&](int nr, int i, const uint32_t (&a)[4], int k, int part) {
-                if constexpr (A::F32) {
-                    mma_tf32_1688(o[nr][i], a, wb[nr][part][2 * k], wb[nr][part][2 * k + 1]);
-                } else if constexpr (A::Q8) {
-                    mma_f16_16816(o[nr][i], a, wb[nr][part][0], wb[nr][part][1]);
-                } else {
-                    mma_bf16_16816(o[nr][i], a, wb[nr][part][0], wb[nr][part][1]);
+        // Keys that no row sees must not reach O (their weights are 0, but
+        // 0 x inf is not): their V counts as zeros.  Of the keys that some rows
+        // see and some do not, a value that is not finite must not reach the
+        // latter: then the rows of each limit are taken by themselves.
+        bool slow = false;
+        if (masked && lim_min < lim_max) {
+            bool bad = false;
+#pragma unroll 1
+            for (int c = lane; c < GK * (A::ROWB / 16); c += 32) {
+                const int r = c % GK;
+                if (kb + r < lim_min || kb + r >= lim_max || !((have >> (r / SUB)) & 1u)) continue;
+                const uint4 v = lds128(vs + chunk_off<A>(r, c / GK));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (A::F32) {
+                        bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
+                    } else if constexpr (A::Q8) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) bad |= ((w[i] >> (8 * y)) & 0x7fu) == 0x7fu;
+                    } else {
+                        bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+                    }
                 }
+            }
+            slow = __any_sync(0xffffffffu, bad);
+        }
+        int cut = slow ? lim_min : lim_max;
+#pragma unroll 1
+        for (;;) {
+            float keep[NR][A::NT][4];
+            if (slow) {
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int i = 0; i < A::NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) keep[nr][i][e] = o[nr][i][e];
+            }
+            // O^T += V^T W^T
+            auto mma_o = [&](int nr, int i, const uint32_t (&a)[4], int h, int k, int part) {
+                if constexpr (A::F32)
+                    mma_tf32_1688(o[nr][i], a, wb[nr][h][part][2 * k], wb[nr][h][part][2 * k + 1]);
+                else if constexpr (A::Q8)
+                    mma_f16_16816(o[nr][i], a, wb[nr][h][part][0], wb[nr][h][part][1]);
+                else
+                    mma_bf16_16816(o[nr][i], a, wb[nr][h][part][0], wb[nr][h][part][1]);
             };
-            float keep[NR][4];
-            auto tile = [&](int i, const uint32_t (&a)[4], const uint32_t (&a2)[4],
-                            const uint32_t (&al)[4], const uint32_t (&a2l)[4]) {
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    if (only >= 0) {
+            for (int h = 0; h < NS; ++h) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) keep[nr][e] = o[nr][i][e];
+                for (int j = 0; j < A::VL; ++j) {
+                    uint32_t v[4][4];
+                    const int row[4] = {va, vb, va + 8, vb + 8};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = h * SUB + row[k];
+                        if constexpr (A::ROWB == 64) {        // 8 bytes per lane and row
+                            const uint2 u = lds64(vs + chunk_off<A>(r, g >> 1) + (g & 1) * 8);
+                            v[k][0] = u.x;
+                            v[k][1] = u.y;
+                            v[k][2] = v[k][3] = 0;
+                        } else {
+                            const uint4 u = lds128(vs + chunk_off<A>(r, g + 8 * j));
+                            v[k][0] = u.x;
+                            v[k][1] = u.y;
+                            v[k][2] = u.z;
+                            v[k][3] = u.w;
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (kb + h * SUB + row[k] >= cut || !((have >> h) & 1u))
+                                v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0;
                     }
                     if constexpr (A::F32) {
-                        acc(nr, i, a, 0, 0);
-                        acc(nr, i, a, 0, 1);
-                        acc(nr, i, al, 0, 0);
-                        acc(nr, i, a2, 1, 0);
-                        acc(nr, i, a2, 1, 1);
-                        acc(nr, i, a2l, 1, 0);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t a[4], al[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    split_tf32(__uint_as_float(v[2 * k + i / 2][2 * r + i % 2]), a[i],
+                                               al[i]);
+#pragma unroll
+                                for (int nr = 0; nr < NR; ++nr) {
+                                    mma_o(nr, j * 2 + r, a, h, k, 0);
+                                    mma_o(nr, j * 2 + r, a, h, k, 1);
+                                    mma_o(nr, j * 2 + r, al, h, k, 0);
+                                }
+                            }
+                        }
+                    } else if constexpr (A::Q8) {
+                        constexpr int NW = A::ROWB == 64 ? 2 : 4;
+#pragma unroll
+                        for (int i = 0; i < NW; ++i) {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t sel = y ? 0x7362 : 0x5140;
+                                uint32_t a[4];
+                                e4m3x4(__byte_perm(v[0][i], v[1][i], sel), a[0], a[1]);
+                                e4m3x4(__byte_perm(v[2][i], v[3][i], sel), a[2], a[3]);
+#pragma unroll
+                                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                                    for (int q = 0; q < A::PT; ++q) mma_o(nr, 2 * i + y, a, h, 0, q);
+                            }
+                        }
                     } else {
-                        acc(nr, i, a, 0, 0);
-                        if constexpr (A::PT == 2) acc(nr, i, a, 0, 1);
-                    }
-                    if (only >= 0) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (lim[nr][e & 1] != only) o[nr][i][e] = keep[nr][e];
-                    }
-                }
-            };
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a[4] = {__byte_perm(v[0][i], v[1][i], 0x5410),
+                                                   __byte_perm(v[0][i], v[1][i], 0x7632),
+                                                   __byte_perm(v[2][i], v[3][i], 0x5410),
+                                                   __byte_perm(v[2][i], v[3][i], 0x7632)};
 #pragma unroll
-            for (int j = 0; j < A::VL; ++j) {
-                uint4 v0, v1, v2, v3;
-                if constexpr (A::ROWB == 64) {
-                    // 8 bytes per lane and row
-                    const uint32_t h8 = (g & 1) * 8;
-                    const uint2 u0 = lds64(vs + chunk_off<A>(va, g >> 1) + h8);
-                    const uint2 u1 = lds64(vs + chunk_off<A>(vb, g >> 1) + h8);
-                    const uint2 u2 = lds64(vs + chunk_off<A>(va + 8, g >> 1) + h8);
-                    const uint2 u3 = lds64(vs + chunk_off<A>(vb + 8, g >> 1) + h8);
-                    v0 = make_uint4(u0.x, u0.y, 0, 0);
-                    v1 = make_uint4(u1.x, u1.y, 0, 0);
-                    v2 = make_uint4(u2.x, u2.y, 0, 0);
-                    v3 = make_uint4(u3.x, u3.y, 0, 0);
-                } else {
-                    v0 = lds128(vs + chunk_off<A>(va, g + 8 * j));
-                    v1 = lds128(vs + chunk_off<A>(vb, g + 8 * j));
-                    v2 = lds128(vs + chunk_off<A>(va + 8, g + 8 * j));
-                    v3 = lds128(vs + chunk_off<A>(vb + 8, g + 8 * j));
-                }
-                if (cut < GK) {
-                    if (z0) v0 = zero;
-                    if (z1) v1 = zero;
-                    if (z2) v2 = zero;
-                    if (z3) v3 = zero;
-                }
-                const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
-                const uint32_t x2[4] = {v2.x, v2.y, v2.z, v2.w}, x3[4] = {v3.x, v3.y, v3.z, v3.w};
-                if constexpr (A::F32) {
+                            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        uint32_t a[4], al[4], c[4], cl[4];
-                        split_tf32(__uint_as_float(x0[2 * r]), a[0], al[0]);
-                        split_tf32(__uint_as_float(x0[2 * r + 1]), a[1], al[1]);
-                        split_tf32(__uint_as_float(x1[2 * r]), a[2], al[2]);
-                        split_tf32(__uint_as_float(x1[2 * r + 1]), a[3], al[3]);
-                        split_tf32(__uint_as_float(x2[2 * r]), c[0], cl[0]);
-                        split_tf32(__uint_as_float(x2[2 * r + 1]), c[1], cl[1]);
-                        split_tf32(__uint_as_float(x3[2 * r]), c[2], cl[2]);
-                        split_tf32(__uint_as_float(x3[2 * r + 1]), c[3], cl[3]);
-                        tile(j * 2 + r, a, c, al, cl);
-                    }
-                } else if constexpr (A::Q8) {
-                    constexpr int NW = A::ROWB == 64 ? 2 : 4;
-#pragma unroll
-                    for (int i = 0; i < NW; ++i) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t sel = h ? 0x7362 : 0x5140;
-                            const uint32_t c0 = __byte_perm(x0[i], x1[i], sel);
-                            const uint32_t c1 = __byte_perm(x2[i], x3[i], sel);
-                            const uint32_t a[4] = {e4m3x2(c0), e4m3x2(c0 >> 16), e4m3x2(c1),
-                                                   e4m3x2(c1 >> 16)};
-                            tile(2 * i + h, a, a, a, a);
+                                for (int q = 0; q < A::PT; ++q) mma_o(nr, 4 * j + i, a, h, 0, q);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a[4] = {
-                            __byte_perm(x0[i], x1[i], 0x5410), __byte_perm(x0[i], x1[i], 0x7632),
-                            __byte_perm(x2[i], x3[i], 0x5410), __byte_perm(x2[i], x3[i], 0x7632)};
-                        tile(4 * j + i, a, a, a, a);
-                    }
                 }
             }
-        };
-        if (!masked) {
-            pv(GK, -1);
-            return;
-        }
-        // keys that some rows see and some do not must not reach the latter:
-        // where one of them holds a value that is not finite, the rows of
-        // each limit are taken by themselves
-        bool bad = false;
-#pragma unroll 1
-        for (int c = lane; c < GK * (A::ROWB / 16); c += 32) {
-            const int r = c % GK;
-            if (kb + r < lim_min || kb + r >= lim_max) continue;
-            const uint4 v = lds128(vs + chunk_off<A>(r, c / GK));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (!slow) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (A::F32) {
-                    bad |= (w[i] & 0x7f800000u) == 0x7f800000u;
-                } else if constexpr (A::Q8) {
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) bad |= ((w[i] >> (8 * y)) & 0x7fu) == 0x7fu;
-                } else {
-                    bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-                }
-            }
-        }
-        if (!__any_sync(0xffffffffu, bad)) {
-            pv(lim_max - kb, -1);
-        } else {
-#pragma unroll 1
-            for (int c = lim_min; c <= lim_max; ++c) pv(c - kb, c);
+                for (int i = 0; i < A::NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (lim[nr][e & 1] != cut) o[nr][i][e] = keep[nr][i][e];
+            if (++cut > lim_max) break;
         }
     };
 
@@ -932,7 +972,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         clear();
         // ---- the granules: every KW-th one
         int slot = slot0 + kw, use = use0;
-        for (int gi = kw; gi < cnt; gi += KW, slot += KW) {
+        for (int gi = kw; gi < cnt && kw < KW; gi += KW, slot += KW) {
             while (slot >= p.slots) {
                 slot -= p.slots;
                 ++use;
@@ -949,7 +989,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
             __syncwarp();
             const int kb = (wk.pos + gi) * GK;
-            if (flags[slot] && kb < lim_max) granule(kb, slot, lim_min, lim_max);
+            const uint32_t have = flags[slot];
+            if (have != 0 && kb < lim_max) granule(kb, slot, have, lim_min, lim_max);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[slot]);
         }
@@ -999,7 +1040,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             bar();
             if (last_flag) {
                 clear();
-                for (int c = c0 + kw; c <= c1; c += KW) {
+                for (int c = c0 + kw; c <= c1 && kw < KW; c += KW) {
                     const size_t at = (size_t)slot(c) * p.rtc + rt;
                     float m2[NR][2], l2[NR][2];
 #pragma unroll
@@ -1046,14 +1087,15 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// A pool as bytes [n_pages][Hkv page][row bytes], boxes of 16 rows.
+// A pool as bytes [n_pages][Hkv page][row bytes], boxes of a granule's rows.
 template <class A> bool pool_map(CUtensorMap* m, const spec_paged_cfg& c, const void* base) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t rows = (cuuint64_t)c.Hkv * c.page;
     const cuuint64_t dims[3] = {(cuuint64_t)A::ROWB, rows, (cuuint64_t)c.n_pages};
     const cuuint64_t str[2] = {(cuuint64_t)A::ROWB, rows * A::ROWB};
-    const cuuint32_t box[3] = {(cuuint32_t)A::SW, (cuuint32_t)GK, 1}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)A::SW, (cuuint32_t)(c.page >= GK ? GK : SUB), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE,
                A::SW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -1061,7 +1103,11 @@ template <class A> bool pool_map(CUtensorMap* m, const spec_paged_cfg& c, const 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int SMEM_MAX = 226 * 1024;
+#ifndef SPEC_AP_W1
+#define SPEC_AP_W1 7
+#define SPEC_AP_W2 7
+#endif
+constexpr int SMEM_MAX = 225 * 1024;     // of 227 KB, beside the static variables
 
 template <int IO, int KV, int D, int NR, int W>
 cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
@@ -1090,18 +1136,20 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.G = c.Hq / c.Hkv;
     p.rtc = w.rtc;
     p.rtg = w.rtg;
-    p.min_granules = 8;
+    p.min_granules = 4;
+    p.box = c.page >= GK ? GK : SUB;
     p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
-    const int fixed = 1024 + W / 2 * NR * (A::NT + 1) * 32 * 16;
-    const int per_slot = A::SLOT + (A::Q8 ? 2 * GK * 4 : 0);
-    p.slots = (SMEM_MAX - fixed) / per_slot;
-    if (p.slots > MAX_SLOTS) p.slots = MAX_SLOTS;
+    constexpr int fixed = 1024 + W / 2 * NR * (A::NT + 1) * 32 * 16;
+    constexpr int per_slot = A::SLOT + (A::Q8 ? 2 * GK * 4 : 0);
+    constexpr int fit = (SMEM_MAX - fixed) / per_slot;
+    static_assert(fit >= W && fit >= 4, "the ring's waits need a slot per key warp");
+    p.slots = fit < MAX_SLOTS ? fit : MAX_SLOTS;
     const int smem = fixed + p.slots * per_slot;
     auto kern = attn_paged<IO, KV, D, NR, W>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // at most every granule of a full table
-    const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * (((int64_t)c.max_pages * c.page) / GK);
+    const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * (((int64_t)c.max_pages * c.page + GK - 1) / GK);
     const int grid = (int)(most < sms ? most : sms);
     return launch_k(false, kern, dim3(grid), dim3(32 * (W + 1)), smem, st, mk, mv, p);
 }
@@ -1111,10 +1159,10 @@ cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void*
                    const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
     // one more warp issues the copies: 16 or 8 in all share the registers
     // evenly (128 or 255 each); row tiles in a CTA must divide the warps
-    constexpr bool wide = IO == SPEC_IO_BF16;
+    constexpr bool big = At<IO, KV, D>::SLOT > 16384;
     if (paged_row_tiles(c).nr == 1)
-        return attn_launch<IO, KV, D, 1, wide ? 15 : 7>(c, kv, q, n_new, o, ws, st);
-    return attn_launch<IO, KV, D, 2, 8>(c, kv, q, n_new, o, ws, st);
+        return attn_launch<IO, KV, D, 1, big ? 6 : SPEC_AP_W1>(c, kv, q, n_new, o, ws, st);
+    return attn_launch<IO, KV, D, 2, big ? 6 : SPEC_AP_W2>(c, kv, q, n_new, o, ws, st);
 }
 
 }  // namespace

@@ -53,8 +53,8 @@ inline RowTiles paged_row_tiles(const spec_paged_cfg& c) {
     RowTiles r{};
     r.nr = rows <= 8 ? 1 : 2;
     const int64_t tiles = (rows + 8 * r.nr - 1) / (8 * r.nr);
-    r.rtc = tiles <= 1 ? 1 : (tiles <= 2 ? 2 : 4);
-    r.rtg = (int)((tiles + r.rtc - 1) / r.rtc);
+    r.rtg = (int)((tiles + 2) / 3);
+    r.rtc = (int)((tiles + r.rtg - 1) / r.rtg);
     return r;
 }
 

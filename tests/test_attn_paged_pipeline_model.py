@@ -137,8 +137,8 @@ def portions_of(rnd):
     return [rnd.choice([1, 3, 7, 17, 40, 70]) for _ in range(rnd.randint(1, 4))]
 
 
-@pytest.mark.parametrize("slots,kws,rtc", [(24, 15, 1), (44, 15, 1), (13, 7, 1), (64, 15, 1),
-                                           (22, 8, 1), (40, 4, 2), (40, 2, 4), (15, 15, 1)])
+@pytest.mark.parametrize("slots,kws,rtc", [(13, 7, 1), (25, 7, 1), (51, 7, 1), (6, 6, 1),
+                                           (24, 11, 1), (11, 11, 1), (13, 3, 2), (13, 2, 3)])
 def test_ring(slots, kws, rtc):
     for seed in range(25):
         run(portions_of(random.Random(seed)), slots, kws, rtc, seed)
