@@ -65,14 +65,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_tf32_1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // 8x8 transpose of 16-bit elements across the warp
 __device__ __forceinline__ uint32_t movm(uint32_t x) {
     uint32_t y;
@@ -103,6 +95,7 @@ __device__ __forceinline__ void e4m3x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
         : "=r"(lo), "=r"(hi)
         : "r"(x));
 }
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 // log2 of a scale; 0 counts as 2^-126, a NaN stays
 __device__ __forceinline__ float log2_scale(float x) {
     float y;
@@ -119,17 +112,25 @@ __device__ __forceinline__ uint32_t packb(float lo, float hi) {
 }
 __device__ __forceinline__ float lo_b(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_b(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-__device__ __forceinline__ uint32_t tf32_rna(float x) {
-    uint32_t y;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
-    return y;
+// x = sum of three bf16 parts, by cutting off 8 bits at a time: exact for
+// normal numbers; an infinity or NaN stays in the first part.  Parts come as
+// fp32 bit patterns whose low half is zero.
+__device__ __forceinline__ void split3(float x, uint32_t (&p)[3]) {
+    p[0] = __float_as_uint(x) & 0xffff0000u;
+    const float h = __uint_as_float(p[0]);
+    const float r = h == x ? 0.0f : x - h;
+    p[1] = __float_as_uint(r) & 0xffff0000u;
+    p[2] = __float_as_uint(r - __uint_as_float(p[1]));     // its low half is never looked at
 }
-// x = hi + lo to 2^-22: two tf32 parts; an infinity stays in hi
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = tf32_rna(x);
-    if ((hi & 0x7fffffffu) == 0x7f800000u) hi = __float_as_uint(x) & 0xffffe000u;
-    const float h = __uint_as_float(hi);
-    lo = h == x ? 0u : tf32_rna(x - h);
+// the same parts of x and y as three bf16 pairs
+__device__ __forceinline__ void split3x2(float x, float y, uint32_t& p0, uint32_t& p1,
+                                         uint32_t& p2) {
+    uint32_t a[3], b[3];
+    split3(x, a);
+    split3(y, b);
+    p0 = __byte_perm(a[0], b[0], 0x7632);
+    p1 = __byte_perm(a[1], b[1], 0x7632);
+    p2 = __byte_perm(a[2], b[2], 0x7632);
 }
 
 // ---- layout of the operands -----------------------------------------------------------
@@ -145,11 +146,10 @@ template <int IO, int KV, int D> struct At {
     static constexpr int EPC = 16 / EB;                 // values per chunk
     static constexpr int VL = ROWB / 8 < 16 ? 1 : ROWB / 128;   // V loads per row and lane
     static constexpr int RL = Q8 ? D / 8 : EPC;         // consecutive values of a lane in a row
-    static constexpr int NRUN = D / 8 / RL;
     static constexpr int NT = D / 16;                   // 16-value tiles of O^T
-    static constexpr int QT = (Q8 && IO == SPEC_IO_F32) || F32 ? 2 : 1;   // parts of a Q value
-    static constexpr int QR = Q8 ? 8 : 4;               // Q registers per chunk and part
-    static constexpr int PT = (Q8 && IO == SPEC_IO_BF16) ? 1 : 2;   // parts of a weight
+    static constexpr int QT = F32 ? 3 : (Q8 && IO == SPEC_IO_F32 ? 2 : 1);  // parts of a Q value
+    static constexpr int QR = EPC / 2;                  // Q registers per chunk and part
+    static constexpr int PT = F32 ? 3 : (Q8 && IO == SPEC_IO_BF16 ? 1 : 2); // parts of a weight
     static constexpr int SLOT_KV = GK * ROWB;           // bytes of K (or V) of a granule
     static constexpr int SLOT = 2 * SLOT_KV;
 };
@@ -177,8 +177,13 @@ struct AttnParams {
     int rtc, rtg;            // row tiles per CTA, row groups per (request, kv-head)
     int slots;
     int box;                 // rows per copy: GK, or SUB where pages are that small
-    int min_granules;        // per CTA
+    int min_sh;              // a CTA takes at least 2^min_sh granules of a long segment
+    unsigned long long g_mul;   // ceil(2^32 / G)
     float qk_scale;          // log2(e) / sqrt(D)
+    // row / G, exact for the rows there can be (at most 2^16)
+    __device__ __forceinline__ int tok(int r) const { return (int)(((unsigned long long)r * g_mul) >> 32); }
+    __device__ __forceinline__ int hk(int seg) const { return rtg == 1 ? seg : seg / rtg; }
+    __device__ __forceinline__ int rg(int seg) const { return rtg == 1 ? 0 : seg % rtg; }
 };
 
 // One request's lengths.
@@ -222,10 +227,24 @@ struct Walk {
     }
 };
 
+// a b / c; 32-bit where a is small (b, c: CTA counts or indexes)
+__device__ __forceinline__ long long muldiv(long long a, int b, int c) {
+    if (a < (1 << 20) && b < (1 << 11)) return (uint32_t)a * (uint32_t)b / (uint32_t)c;
+    return a * b / c;
+}
 // The CTA that owns granule u of `units` dealt to `n` CTAs (CTA c starts at c units / n).
 __device__ __forceinline__ int owner(long long u, long long units, int n) {
+    if (units < (1 << 20) && n < (1 << 11))
+        return (int)(((uint32_t)(u + 1) * (uint32_t)n - 1) / (uint32_t)units);
     return (int)(((u + 1) * n - 1) / units);
 }
+
+// A segment that this CTA shares with others: what joining its parts needs.
+struct Pend {
+    int b, seg, n;           // request, segment in it, new rows
+    int c0, c1, shift;       // its CTAs (c1 < 0: none); 1: the part of c0 is that CTA's second
+    int last;                // this CTA's part was the last one to be written
+};
 
 template <int IO, int KV, int D, int NR, int W>
 __global__ void __launch_bounds__(32 * (W + 1), 1)
@@ -239,8 +258,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     __shared__ long long wsum[W + 1];
     __shared__ long long first_off;
     __shared__ int first_b;
+    __shared__ Req first_rq;
     __shared__ volatile int abort_flag;
-    __shared__ int last_flag;
+    __shared__ Pend pend[2];
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int hr = p.pm.Hkv * p.rtg;
@@ -251,17 +271,23 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     // ---- this CTA's share of the granules
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < p.slots; ++s) {
-            tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&empty[s], p.rtc);
-        }
+        pend[0].c1 = pend[1].c1 = -1;
+        pend[0].last = pend[1].last = 0;
+    }
+    if (warp == W && lane < 2) tc::tma_prefetch_desc(lane ? &mv : &mk);
+    for (int s = tid; s < p.slots; s += NTH) {
+        tc::mbar_init(&full[s], 1);
+        tc::mbar_init(&empty[s], p.rtc);
         tc::fence_mbar_init();
     }
     const int per = (p.B + NTH - 1) / NTH;
     long long mine = 0;
     uint32_t bits = 0;
-    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b)
-        mine += (long long)request(p, b, bits).ng * hr;
+    Req rq0{};
+    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
+        rq0 = request(p, b, bits);
+        mine += (long long)rq0.ng * hr;
+    }
     if (bits && blockIdx.x == 0) raise_status(p.ws, bits);
     long long incl = mine;
 #pragma unroll
@@ -272,24 +298,31 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
     long long before = 0, units = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w <= W; ++w) {
-        if (w < warp) before += wsum[w];
-        units += wsum[w];
+        const long long x = wsum[w];
+        if (w < warp) before += x;
+        units += x;
     }
-    const int n_cta = (int)min((long long)gridDim.x, (units + p.min_granules - 1) / p.min_granules);
+    // a CTA per segment, and per 2^min_sh granules of longer ones
+    const int n_cta = (int)min((long long)gridDim.x,
+                               max((units + (1 << p.min_sh) - 1) >> p.min_sh,
+                                   (long long)p.B * hr));
     if ((int)blockIdx.x >= n_cta) return;
-    const long long g0 = units * blockIdx.x / n_cta, g1 = units * (blockIdx.x + 1) / n_cta;
+    const long long g0 = muldiv(units, blockIdx.x, n_cta);
+    const long long g1 = muldiv(units, blockIdx.x + 1, n_cta);
     {
         const long long lo = before + incl - mine;
         if (g0 >= lo && g0 < lo + mine) {
             long long at = lo;
             for (int b = tid * per;; ++b) {
                 uint32_t ignore = 0;
-                const long long c = (long long)request(p, b, ignore).ng * hr;
+                if (per > 1) rq0 = request(p, b, ignore);
+                const long long c = (long long)rq0.ng * hr;
                 if (g0 < at + c) {
                     first_b = b;
                     first_off = g0 - at;
+                    first_rq = rq0;
                     break;
                 }
                 at += c;
@@ -300,9 +333,11 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     Walk wk;
     wk.b = first_b;
     wk.left = g1 - g0;
-    {
-        uint32_t ignore = 0;
-        wk.rq = request(p, wk.b, ignore);
+    wk.rq = first_rq;
+    if (first_off < 0x7fffffff) {
+        wk.seg = (int)((uint32_t)first_off / (uint32_t)wk.rq.ng);
+        wk.pos = (int)((uint32_t)first_off % (uint32_t)wk.rq.ng);
+    } else {
         wk.seg = (int)(first_off / wk.rq.ng);
         wk.pos = (int)(first_off % wk.rq.ng);
     }
@@ -316,12 +351,12 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         bool ok = true;
         uint32_t bad = 0;
         while (wk.left > 0 && ok) {
-            const int hk = wk.seg / p.rtg, rg = wk.seg % p.rtg;
+            const int hk = p.hk(wk.seg), rg = p.rg(wk.seg);
             const int r0 = rg * p.rtc * rows_tile;
             int end = 0;
             if (r0 < wk.rq.n * p.G) {
                 const int last = min(r0 + p.rtc * rows_tile, wk.rq.n * p.G) - 1;
-                end = min(wk.rq.L + last / p.G + 1, cap);
+                end = min(wk.rq.L + p.tok(last) + 1, cap);
             }
             const int cnt = wk.count();
             for (int base = 0; base < cnt && ok; base += 32) {
@@ -470,38 +505,94 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
     auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
-    // join the key warps' results into key warp 0's, by halves
-    auto join_warps = [&]() {
-        constexpr int SLOT = NR * (A::NT + 1) * 32;
-        for (int n = KW; n > 1; n = (n + 1) / 2) {
-            const int h = (n + 1) / 2;
-            if (kw >= h && kw < n) {
-                float4* d = buf + ((kw - h) * p.rtc + rt) * SLOT + lane;
+    // The key warps' results meet in shared memory, (max, max, sum, sum) and the
+    // tiles of O^T in register order, and the tiles are then shared out to the
+    // warps: each joins its tiles over the key warps, and writes them to the
+    // output (whole) or to part `at` of the workspace.
+    constexpr int JW = NR * (A::NT + 1) * 32;            // float4 of a warp
+    constexpr int PO = NR * A::NT * 32, PM = NR * 32;    // float4 of a part's row tile
+    constexpr int TPR = NR * A::NT;                      // tiles of a row tile
+    auto finish = [&](int b, int seg, int n, bool whole, size_t at) {
+        bar();                                           // everyone is done with buf
+        if (kw < KW) {
+            float4* d = buf + warp * JW + lane;
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    d[(nr * (A::NT + 1)) * 32] = make_float4(m[nr][0], m[nr][1], l[nr][0], l[nr][1]);
+            for (int nr = 0; nr < NR; ++nr) {
+                d[nr * (A::NT + 1) * 32] = make_float4(m[nr][0], m[nr][1], l[nr][0], l[nr][1]);
 #pragma unroll
-                    for (int i = 0; i < A::NT; ++i)
-                        d[(nr * (A::NT + 1) + 1 + i) * 32] =
-                            make_float4(o[nr][i][0], o[nr][i][1], o[nr][i][2], o[nr][i][3]);
-                }
+                for (int i = 0; i < A::NT; ++i)
+                    d[(nr * (A::NT + 1) + 1 + i) * 32] =
+                        make_float4(o[nr][i][0], o[nr][i][1], o[nr][i][2], o[nr][i][3]);
             }
-            bar();
-            if (kw < n - h) {
-                const float4* s = buf + (kw * p.rtc + rt) * SLOT + lane;
-                float m2[NR][2], l2[NR][2];
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    const float4 x = s[(nr * (A::NT + 1)) * 32];
-                    m2[nr][0] = x.x;
-                    m2[nr][1] = x.y;
-                    l2[nr][0] = x.z;
-                    l2[nr][1] = x.w;
-                }
-                join(m2, l2, [&](int nr, int i) { return s[(nr * (A::NT + 1) + 1 + i) * 32]; });
-            }
-            bar();
         }
+        bar();
+        using T = typename io_t<IO>::T;
+        uint32_t bits = 0;
+#pragma unroll 1
+        for (int task = warp; task < p.rtc * TPR; task += W) {
+            const int rt2 = task / TPR, nr = task % TPR / A::NT, i = task % A::NT;
+            const float4* s = buf + rt2 * JW + nr * (A::NT + 1) * 32 + lane;
+            const int step = p.rtc * JW;
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float4 x = s[min(k, KW - 1) * step];
+                m0 = fmaxf(m0, x.x);
+                m1 = fmaxf(m1, x.y);
+            }
+            const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const int at = min(k, KW - 1) * step;
+                const float4 x = s[at], z = s[at + (1 + i) * 32];
+                const float f0 = k < KW ? ex2(x.x - b0) : 0.0f;
+                const float f1 = k < KW ? ex2(x.y - b1) : 0.0f;
+                if (k >= KW) continue;               // 0 x inf
+                l0 += x.z * f0;
+                l1 += x.w * f1;
+                y.x += z.x * f0;
+                y.y += z.y * f1;
+                y.z += z.z * f0;
+                y.w += z.w * f1;
+            }
+            const int r0 = ((p.rg(seg) * p.rtc + rt2) * NR + nr) * 8 + 2 * t;
+            if (!whole) {
+                // lanes whose rows the step does not have write nothing
+                if (r0 >= n * p.G) continue;
+                const size_t pt = at * p.rtc + rt2;
+                __stcg(p.part_o + pt * PO + (nr * A::NT + i) * 32 + lane, y);
+                if (i == 0)
+                    __stcg(p.part_ml + pt * PM + nr * 32 + lane, make_float4(m0, m1, l0, l1));
+                continue;
+            }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+            }
+            const int hk = p.hk(seg);
+            const int d0 = (i / (A::RL / 2) * 8 + g) * A::RL + 2 * (i % (A::RL / 2));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int tok = p.tok(r0 + e);
+                if (tok >= p.T) continue;
+                const float sum = e ? l1 : l0;
+                const bool real = tok < n && sum != 0.0f;
+                const float inv = real ? 1.0f / sum : 0.0f;
+                const float u = real ? (e ? y.y : y.x) * inv : 0.0f;
+                const float v = real ? (e ? y.w : y.z) * inv : 0.0f;
+                if (!(fabsf(u) <= 3.4028234663852886e38f && fabsf(v) <= 3.4028234663852886e38f))
+                    bits = SPEC_DEV_RANGE;
+                T* dst = static_cast<T*>(p.o) +
+                         (((size_t)b * p.T + tok) * p.Hq + hk * p.G + r0 + e - tok * p.G) * D + d0;
+                if constexpr (IO == SPEC_IO_F32)
+                    *reinterpret_cast<float2*>(dst) = make_float2(u, v);
+                else
+                    *reinterpret_cast<uint32_t*>(dst) = packb(u, v);
+            }
+        }
+        if (bits) raise_status(p.ws, bits);
     };
 
     // one granule: keys [kb, kb + GK) in ring slot `slot`; have: its halves in the pool
@@ -535,20 +626,18 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                                               qf[nr][q][j][2 * i + 1]);
                     }
                 } else if constexpr (A::F32) {
+                    uint32_t a[3][4];
+                    split3x2(__uint_as_float(w0[0]), __uint_as_float(w0[1]), a[0][0], a[1][0], a[2][0]);
+                    split3x2(__uint_as_float(w1[0]), __uint_as_float(w1[1]), a[0][1], a[1][1], a[2][1]);
+                    split3x2(__uint_as_float(w0[2]), __uint_as_float(w0[3]), a[0][2], a[1][2], a[2][2]);
+                    split3x2(__uint_as_float(w1[2]), __uint_as_float(w1[3]), a[0][3], a[1][3], a[2][3]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t ah[4], al[4];
-                        split_tf32(__uint_as_float(w0[2 * i]), ah[0], al[0]);
-                        split_tf32(__uint_as_float(w1[2 * i]), ah[1], al[1]);
-                        split_tf32(__uint_as_float(w0[2 * i + 1]), ah[2], al[2]);
-                        split_tf32(__uint_as_float(w1[2 * i + 1]), ah[3], al[3]);
+                    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr) {
-                            mma_tf32_1688(x[nr][h], ah, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
-                            mma_tf32_1688(x[nr][h], ah, qf[nr][1][j][2 * i], qf[nr][1][j][2 * i + 1]);
-                            mma_tf32_1688(x[nr][h], al, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
-                        }
-                    }
+                        for (int q = 2; q >= 0; --q)           // parts i + q <= 2: 2^-24 is left
+#pragma unroll
+                            for (int i = 2 - q; i >= 0; --i)
+                                mma_bf16_16816(x[nr][h], a[i], qf[nr][q][j][0], qf[nr][q][j][1]);
                 } else {
                     const uint32_t a0[4] = {w0[0], w1[0], w0[1], w1[1]};
                     const uint32_t a1[4] = {w0[2], w1[2], w0[3], w1[3]};
@@ -626,7 +715,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         // weights, their sum, and the second product's B operand
-        uint32_t wb[NR][NS][A::PT][A::F32 ? 4 : 2];
+        uint32_t wb[NR][NS][A::PT][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             const float b0 = m[nr][0] == -INFINITY ? 0.0f : m[nr][0];
@@ -644,17 +733,12 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     if (A::Q8 && masked && x[nr][h][e] == -INFINITY) w[e] = 0.0f;
                 }
                 if constexpr (A::F32) {
-                    // 32-bit transposes as two 16-bit ones; columns = keys va, vb (+ 8)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint32_t a = __float_as_uint(w[2 * k]);
-                        const uint32_t c = __float_as_uint(w[2 * k + 1]);
-                        const uint32_t th = movm(__byte_perm(a, c, 0x7632));
-                        const uint32_t tl = movm(__byte_perm(a, c, 0x5410));
-                        split_tf32(__uint_as_float(__byte_perm(tl, th, 0x5410)),
-                                   wb[nr][h][0][2 * k], wb[nr][h][1][2 * k]);
-                        split_tf32(__uint_as_float(__byte_perm(tl, th, 0x7632)),
-                                   wb[nr][h][0][2 * k + 1], wb[nr][h][1][2 * k + 1]);
+                        uint32_t c[3];
+                        split3x2(w[2 * k], w[2 * k + 1], c[0], c[1], c[2]);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) wb[nr][h][q][k] = movm(c[q]);
                     }
                 } else {
 #pragma unroll
@@ -717,10 +801,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                         for (int e = 0; e < 4; ++e) keep[nr][i][e] = o[nr][i][e];
             }
             // O^T += V^T W^T
-            auto mma_o = [&](int nr, int i, const uint32_t (&a)[4], int h, int k, int part) {
-                if constexpr (A::F32)
-                    mma_tf32_1688(o[nr][i], a, wb[nr][h][part][2 * k], wb[nr][h][part][2 * k + 1]);
-                else if constexpr (A::Q8)
+            auto mma_o = [&](int nr, int i, const uint32_t (&a)[4], int h, int part) {
+                if constexpr (A::Q8)
                     mma_f16_16816(o[nr][i], a, wb[nr][h][part][0], wb[nr][h][part][1]);
                 else
                     mma_bf16_16816(o[nr][i], a, wb[nr][h][part][0], wb[nr][h][part][1]);
@@ -756,20 +838,19 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     if constexpr (A::F32) {
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
+                            uint32_t a[3][4];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t a[4], al[4];
+                            for (int i = 0; i < 4; ++i)       // columns va, vb, then + 8
+                                split3x2(__uint_as_float(v[i / 2 * 2][2 * r + i % 2]),
+                                         __uint_as_float(v[i / 2 * 2 + 1][2 * r + i % 2]), a[0][i],
+                                         a[1][i], a[2][i]);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    split_tf32(__uint_as_float(v[2 * k + i / 2][2 * r + i % 2]), a[i],
-                                               al[i]);
+                            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                for (int nr = 0; nr < NR; ++nr) {
-                                    mma_o(nr, j * 2 + r, a, h, k, 0);
-                                    mma_o(nr, j * 2 + r, a, h, k, 1);
-                                    mma_o(nr, j * 2 + r, al, h, k, 0);
-                                }
-                            }
+                                for (int q = 2; q >= 0; --q)
+#pragma unroll
+                                    for (int i = 2 - q; i >= 0; --i)
+                                        mma_o(nr, j * 2 + r, a[i], h, q);
                         }
                     } else if constexpr (A::Q8) {
                         constexpr int NW = A::ROWB == 64 ? 2 : 4;
@@ -784,7 +865,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                    for (int q = 0; q < A::PT; ++q) mma_o(nr, 2 * i + y, a, h, 0, q);
+                                    for (int q = 0; q < A::PT; ++q) mma_o(nr, 2 * i + y, a, h, q);
                             }
                         }
                     } else {
@@ -797,7 +878,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                for (int q = 0; q < A::PT; ++q) mma_o(nr, 4 * j + i, a, h, 0, q);
+                                for (int q = 0; q < A::PT; ++q) mma_o(nr, 4 * j + i, a, h, q);
                         }
                     }
                 }
@@ -814,95 +895,47 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
 
-    // the outputs of the key warp that holds them
-    auto write_out = [&](int hk, int row0) {
-        using T = typename io_t<IO>::T;
-        uint32_t bits = 0;
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float sum = l[nr][e];
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const int r = row0 + nr * 8 + 2 * t + e;
-                const int i = r / p.G;
-                if (i >= p.T) continue;
-                const bool real = i < wk.rq.n && sum != 0.0f;
-                T* dst = static_cast<T*>(p.o) +
-                         (((size_t)wk.b * p.T + i) * p.Hq + hk * p.G + r % p.G) * D;
-                const float inv = real ? 1.0f / sum : 0.0f;
-#pragma unroll
-                for (int run = 0; run < A::NRUN; ++run) {
-                    float y[A::RL];
-#pragma unroll
-                    for (int k = 0; k < A::RL; ++k) {
-                        y[k] = real ? o[nr][run * (A::RL / 2) + k / 2][(k & 1) * 2 + e] * inv : 0.0f;
-                        if (!(fabsf(y[k]) <= 3.4028234663852886e38f)) bits = SPEC_DEV_RANGE;
-                    }
-                    const int d0 = run * 8 * A::RL + g * A::RL;
-                    if constexpr (IO == SPEC_IO_F32) {
-#pragma unroll
-                        for (int k = 0; k < A::RL; k += 4)
-                            *reinterpret_cast<float4*>(dst + d0 + k) =
-                                make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < A::RL; k += 8)
-                            *reinterpret_cast<uint4*>(dst + d0 + k) =
-                                make_uint4(packb(y[k], y[k + 1]), packb(y[k + 2], y[k + 3]),
-                                           packb(y[k + 4], y[k + 5]), packb(y[k + 6], y[k + 7]));
-                    }
-                }
-            }
-        if (bits) raise_status(p.ws, bits);
-    };
-
-    long long gpos = g0;                 // global index of the present granule
-    while (wk.left > 0) {
-        const int hk = wk.seg / p.rtg, rg = wk.seg % p.rtg;
-        const int row0 = (rg * p.rtc + rt) * rows_tile;
-        const int cnt = wk.count();
-        // ---- limits and Q of this warp's rows
-        int lim_min = 0, lim_max = 0;
-        if (row0 < wk.rq.n * p.G) {
-            const int last = min(row0 + rows_tile, wk.rq.n * p.G) - 1;
-            lim_min = min(wk.rq.L + row0 / p.G + 1, cap);
-            lim_max = min(wk.rq.L + last / p.G + 1, cap);
-        }
+    // A warp's Q rows as they are in memory, 16 bytes at a time (rows the step
+    // does not have: zeros)
+    constexpr int QB = IO == SPEC_IO_F32 ? 4 : 2;
+    constexpr int RAW = D * QB / 64;                     // 16-byte pieces of a row per lane
+    auto load_q = [&](const Walk& w, uint4 (&raw)[NR][RAW]) {
+        const int hk = p.hk(w.seg), row0 = (p.rg(w.seg) * p.rtc + rt) * rows_tile;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
+            const int r = row0 + nr * 8 + g, i = p.tok(r);
+            const bool real = i < p.T;
+            const uint4* qp = reinterpret_cast<const uint4*>(
+                static_cast<const uint8_t*>(p.q) +
+                (real ? (((size_t)w.b * p.T + i) * p.Hq + hk * p.G + r - i * p.G) * D * QB : 0));
+            constexpr int PC = RAW / A::KCH;             // pieces per cache chunk
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = (row0 + nr * 8 + 2 * t + e) / p.G;
-                lim[nr][e] = i < wk.rq.n ? min(wk.rq.L + i + 1, cap) : 0x7fffffff;
-            }
-            const int r = row0 + nr * 8 + g;
-            const int i = r / p.G;
-            const bool real = i < wk.rq.n;
-            const size_t qo = real ? (((size_t)wk.b * p.T + i) * p.Hq + hk * p.G + r % p.G) * D : 0;
+            for (int k = 0; k < RAW; ++k)
+                raw[nr][k] = real ? __ldg(qp + (t + 4 * (k / PC)) * PC + k % PC)
+                                  : make_uint4(0, 0, 0, 0);
+        }
+    };
+    // and as the first product's operand
+    auto make_q = [&](const uint4 (&raw)[NR][RAW]) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
             if constexpr (!A::Q8 && !A::F32) {
-                const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + qo;
 #pragma unroll
                 for (int j = 0; j < A::KCH; ++j) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (real) u = *reinterpret_cast<const uint4*>(qp + (t + 4 * j) * 8);
-                    qf[nr][0][j][0] = u.x;
-                    qf[nr][0][j][1] = u.y;
-                    qf[nr][0][j][2] = u.z;
-                    qf[nr][0][j][3] = u.w;
+                    qf[nr][0][j][0] = raw[nr][j].x;
+                    qf[nr][0][j][1] = raw[nr][j].y;
+                    qf[nr][0][j][2] = raw[nr][j].z;
+                    qf[nr][0][j][3] = raw[nr][j].w;
                 }
                 rowf[nr][0] = rowf[nr][1] = p.qk_scale;
             } else if constexpr (A::F32) {
-                const float* qp = static_cast<const float*>(p.q) + qo;
 #pragma unroll
                 for (int j = 0; j < A::KCH; ++j) {
-                    float4 u = make_float4(0, 0, 0, 0);
-                    if (real) u = *reinterpret_cast<const float4*>(qp + (t + 4 * j) * 4);
-                    split_tf32(u.x, qf[nr][0][j][0], qf[nr][1][j][0]);
-                    split_tf32(u.y, qf[nr][0][j][1], qf[nr][1][j][1]);
-                    split_tf32(u.z, qf[nr][0][j][2], qf[nr][1][j][2]);
-                    split_tf32(u.w, qf[nr][0][j][3], qf[nr][1][j][3]);
+                    const uint32_t w[4] = {raw[nr][j].x, raw[nr][j].y, raw[nr][j].z, raw[nr][j].w};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        split3x2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]),
+                                 qf[nr][0][j][k], qf[nr][1][j][k], qf[nr][2][j][k]);
                 }
                 rowf[nr][0] = rowf[nr][1] = p.qk_scale;
             } else {
@@ -912,32 +945,18 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 float y[A::KCH][16], amax = 0.0f;
 #pragma unroll
                 for (int j = 0; j < A::KCH; ++j) {
+                    constexpr int PC = RAW / A::KCH;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[j][k] = 0.0f;
-                    if (real) {
-                        if constexpr (IO == SPEC_IO_BF16) {
-                            const uint4* qp = reinterpret_cast<const uint4*>(
-                                static_cast<const __nv_bfloat16*>(p.q) + qo + (t + 4 * j) * 16);
+                    for (int c = 0; c < PC; ++c) {
+                        const uint4 u = raw[nr][j * PC + c];
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const uint4 u = qp[c];
-                                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    y[j][8 * c + 2 * k] = lo_b(w[k]);
-                                    y[j][8 * c + 2 * k + 1] = hi_b(w[k]);
-                                }
-                            }
-                        } else {
-                            const float4* qp = reinterpret_cast<const float4*>(
-                                static_cast<const float*>(p.q) + qo + (t + 4 * j) * 16);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const float4 u = qp[c];
-                                y[j][4 * c] = u.x;
-                                y[j][4 * c + 1] = u.y;
-                                y[j][4 * c + 2] = u.z;
-                                y[j][4 * c + 3] = u.w;
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (IO == SPEC_IO_BF16) {
+                                y[j][8 * c + 2 * k] = lo_b(w[k]);
+                                y[j][8 * c + 2 * k + 1] = hi_b(w[k]);
+                            } else {
+                                y[j][4 * c + k] = __uint_as_float(w[k]);
                             }
                         }
                     }
@@ -969,7 +988,41 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 rowf[nr][1] = p.qk_scale * __shfl_sync(0xffffffffu, fi, 8 * t + 4);
             }
         }
+    };
+
+    long long gpos = g0;                 // global index of the present granule
+    uint4 raw[NR][RAW];
+    // one row tile: the next segment's Q rows are fetched during this one
+    constexpr bool AHEAD = NR == 1 && IO == SPEC_IO_BF16;
+    if (AHEAD) load_q(wk, raw);
+    bool counted = false;                // this CTA's parts are in
+    for (;;) {
+        int b, seg, n;
+        bool whole = true;
+        size_t at = 0;
         clear();
+        if (wk.left > 0) {
+        const int row0 = (p.rg(wk.seg) * p.rtc + rt) * rows_tile;
+        const int cnt = wk.count();
+        // ---- limits and Q of this warp's rows
+        int lim_min = 0, lim_max = 0;
+        if (row0 < wk.rq.n * p.G) {
+            const int last = min(row0 + rows_tile, wk.rq.n * p.G) - 1;
+            lim_min = min(wk.rq.L + p.tok(row0) + 1, cap);
+            lim_max = min(wk.rq.L + p.tok(last) + 1, cap);
+        }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = p.tok(row0 + nr * 8 + 2 * t + e);
+                lim[nr][e] = i < wk.rq.n ? min(wk.rq.L + i + 1, cap) : 0x7fffffff;
+            }
+        if (!AHEAD) load_q(wk, raw);
+        make_q(raw);
+        Walk nx = wk;
+        nx.next(p, hr, cnt);
+        if (AHEAD && nx.left > 0) load_q(nx, raw);
         // ---- the granules: every KW-th one
         int slot = slot0 + kw, use = use0;
         for (int gi = kw; gi < cnt && kw < KW; gi += KW, slot += KW) {
@@ -1001,69 +1054,81 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             ++use0;
         }
         // ---- the segment's end
-        join_warps();
-        if (cnt == wk.rq.ng) {
-            if (kw == 0) write_out(hk, row0);
-        } else {
-            constexpr int PO = NR * A::NT * 32, PM = NR * 32;
+        b = wk.b;
+        seg = wk.seg;
+        n = wk.rq.n;
+        whole = cnt == wk.rq.ng;
+        if (!whole) {
             const long long s0 = gpos - wk.pos, s1 = s0 + wk.rq.ng;
             const int c0 = owner(s0, units, n_cta), c1 = owner(s1 - 1, units, n_cta);
-            const long long start0 = units * c0 / n_cta;
-            auto slot = [&](int c) { return 2 * c + (c == c0 && s0 > start0 ? 1 : 0); };
-            // lanes whose rows the tile does not have write and read nothing
-            bool in[NR];
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) in[nr] = row0 + nr * 8 + 2 * t < wk.rq.n * p.G;
-            if (kw == 0) {
-                const size_t at = (size_t)slot(blockIdx.x) * p.rtc + rt;
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    if (!in[nr]) continue;
-                    __stcg(p.part_ml + at * PM + nr * 32 + lane,
-                           make_float4(m[nr][0], m[nr][1], l[nr][0], l[nr][1]));
-#pragma unroll
-                    for (int i = 0; i < A::NT; ++i)
-                        __stcg(p.part_o + at * PO + (nr * A::NT + i) * 32 + lane,
-                               make_float4(o[nr][i][0], o[nr][i][1], o[nr][i][2], o[nr][i][3]));
-                }
-                __threadfence();
-            }
-            bar();
+            const int shift = s0 > muldiv(units, c0, n_cta);
+            at = 2 * blockIdx.x + ((int)blockIdx.x == c0 ? shift : 0);
             if (tid == 0) {
-                uint32_t* tk = p.tickets + (size_t)wk.b * hr + wk.seg;
-                const uint32_t n = (uint32_t)(c1 - c0 + 1);
-                const bool last = atomicAdd(tk, 1u) == n - 1;
-                if (last) *tk = 0;                       // for the next call
-                last_flag = last;
-                __threadfence();
+                Pend& pe = pend[gpos != g0];
+                pe.b = b;
+                pe.seg = seg;
+                pe.n = n;
+                pe.c0 = c0;
+                pe.c1 = c1;
+                pe.shift = shift;
             }
-            bar();
-            if (last_flag) {
-                clear();
-                for (int c = c0 + kw; c <= c1 && kw < KW; c += KW) {
-                    const size_t at = (size_t)slot(c) * p.rtc + rt;
-                    float m2[NR][2], l2[NR][2];
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) {
-                        float4 x = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
-                        if (in[nr]) x = __ldcg(p.part_ml + at * PM + nr * 32 + lane);
-                        m2[nr][0] = x.x;
-                        m2[nr][1] = x.y;
-                        l2[nr][0] = x.z;
-                        l2[nr][1] = x.w;
-                    }
-                    join(m2, l2, [&](int nr, int i) {
-                        return in[nr] ? __ldcg(p.part_o + at * PO + (nr * A::NT + i) * 32 + lane)
-                                      : make_float4(0, 0, 0, 0);
-                    });
-                }
-                join_warps();
-                if (kw == 0) write_out(hk, row0);
-            }
-            bar();                                       // last_flag and buf are free again
         }
         gpos += cnt;
-        wk.next(p, hr, cnt);
+        wk = nx;
+        } else {
+            // ---- out of granules: count this CTA's parts in (each warp that
+            // wrote some, once for both segments it may share), and join the
+            // segments whose last part was this CTA's
+            const int writers = min(W, p.rtc * TPR);
+            if (!counted) {
+                counted = true;
+                bar();                                   // pend is there
+                if (warp < writers) {
+                    fence_gpu();
+                    __syncwarp();
+                    if (lane < 2 && pend[lane].c1 >= 0) {
+                        Pend& pe = pend[lane];
+                        uint32_t* tk = p.tickets + (size_t)pe.b * hr + pe.seg;
+                        if (atomicAdd(tk, 1u) == (uint32_t)((pe.c1 - pe.c0 + 1) * writers - 1)) {
+                            *tk = 0;                     // for the next call
+                            pe.last = 1;
+                        }
+                    }
+                }
+                bar();
+            }
+            const int k = pend[0].last == 1 ? 0 : (pend[1].last == 1 ? 1 : 2);
+            if (k == 2) break;
+            const Pend pe = pend[k];
+            bar();
+            if (tid == 0) pend[k].last = 2;
+            fence_gpu();
+            b = pe.b;
+            seg = pe.seg;
+            n = pe.n;
+            const int row0 = (p.rg(seg) * p.rtc + rt) * rows_tile;
+#pragma unroll 2
+            for (int c = pe.c0 + kw; c <= pe.c1 && kw < KW; c += KW) {
+                const size_t pt = (size_t)(2 * c + (c == pe.c0 ? pe.shift : 0)) * p.rtc + rt;
+                float m2[NR][2], l2[NR][2];
+                bool in[NR];
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    in[nr] = row0 + nr * 8 + 2 * t < n * p.G;
+                    float4 x = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+                    if (in[nr]) x = __ldcg(p.part_ml + pt * PM + nr * 32 + lane);
+                    m2[nr][0] = x.x;
+                    m2[nr][1] = x.y;
+                    l2[nr][0] = x.z;
+                    l2[nr][1] = x.w;
+                }
+                join(m2, l2, [&](int nr, int i) {
+                    return in[nr] ? __ldcg(p.part_o + pt * PO + (nr * A::NT + i) * 32 + lane)
+                                  : make_float4(0, 0, 0, 0);
+                });
+            }
+        }
+        finish(b, seg, n, whole, at);
     }
 }
 
@@ -1134,12 +1199,13 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.T = c.T;
     p.Hq = c.Hq;
     p.G = c.Hq / c.Hkv;
+    p.g_mul = ((1ull << 32) + p.G - 1) / p.G;
     p.rtc = w.rtc;
     p.rtg = w.rtg;
-    p.min_granules = 4;
+    p.min_sh = 2;
     p.box = c.page >= GK ? GK : SUB;
     p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
-    constexpr int fixed = 1024 + W / 2 * NR * (A::NT + 1) * 32 * 16;
+    constexpr int fixed = 1024 + W * NR * (A::NT + 1) * 32 * 16;
     constexpr int per_slot = A::SLOT + (A::Q8 ? 2 * GK * 4 : 0);
     constexpr int fit = (SMEM_MAX - fixed) / per_slot;
     static_assert(fit >= W && fit >= 4, "the ring's waits need a slot per key warp");
@@ -1162,7 +1228,7 @@ cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void*
     constexpr bool big = At<IO, KV, D>::SLOT > 16384;
     if (paged_row_tiles(c).nr == 1)
         return attn_launch<IO, KV, D, 1, big ? 6 : SPEC_AP_W1>(c, kv, q, n_new, o, ws, st);
-    return attn_launch<IO, KV, D, 2, big ? 6 : SPEC_AP_W2>(c, kv, q, n_new, o, ws, st);
+    return attn_launch<IO, KV, D, 2, big ? 5 : SPEC_AP_W2>(c, kv, q, n_new, o, ws, st);
 }
 
 }  // namespace
