@@ -495,9 +495,11 @@ enum {
 #define SPEC_MAX_PAGED_B 4096
 
 /* Shape of the paged calls.  Limits (else ST_EINVAL): 1 <= B <= 4096;
- * 1 <= T <= 2^20 (attn_decode_paged: T <= 128 and T Hq / Hkv <= 65536); Hq % Hkv == 0; D in {64, 128};
+ * 1 <= T <= 2^20; Hq % Hkv == 0; D in {64, 128};
  * page a power of two in [16, 1024]; n_pages, max_pages >= 1;
- * max_pages * page <= 2^30; B * max(Hq, Hkv) <= 2^24. */
+ * max_pages * page <= 2^30; B * max(Hq, Hkv) <= 2^24.  attn_decode_paged:
+ * T <= 128, R = T Hq / Hkv <= 65536, and B Hkv ceil(R / 48) (max_pages page / 32)
+ * < 2^31. */
 typedef struct spec_paged_cfg {
     int32_t B;               /* requests */
     int32_t T;               /* rows of the new-token tensors per request */

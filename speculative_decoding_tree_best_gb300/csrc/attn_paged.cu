@@ -177,6 +177,7 @@ struct AttnParams {
     int rtc, rtg;            // row tiles per CTA, row groups per (request, kv-head)
     int slots;
     int box;                 // rows per copy: GK, or SUB where pages are that small
+    size_t table_lines, q_lines;   // 128-byte lines of the page table and of Q
     int min_sh;              // a CTA takes at least 2^min_sh granules of a long segment
     unsigned long long g_mul;   // ceil(2^32 / G)
     float qk_scale;          // log2(e) / sqrt(D)
@@ -207,11 +208,9 @@ __device__ __forceinline__ Req request(const AttnParams& p, int b, uint32_t& bit
 // One pass over the segments of a CTA's granule range, in order.
 struct Walk {
     int b, seg, pos;         // request, segment in the request, granule in the segment
-    long long left;
+    int left;
     Req rq;
-    __device__ __forceinline__ int count() const {
-        return (int)min((long long)(rq.ng - pos), left);
-    }
+    __device__ __forceinline__ int count() const { return min(rq.ng - pos, left); }
     // past `c` granules of the present segment
     __device__ __forceinline__ void next(const AttnParams& p, int hr, int c) {
         left -= c;
@@ -227,17 +226,19 @@ struct Walk {
     }
 };
 
-// a b / c; 32-bit where a is small (b, c: CTA counts or indexes)
-__device__ __forceinline__ long long muldiv(long long a, int b, int c) {
-    if (a < (1 << 20) && b < (1 << 11)) return (uint32_t)a * (uint32_t)b / (uint32_t)c;
-    return a * b / c;
-}
-// The CTA that owns granule u of `units` dealt to `n` CTAs (CTA c starts at c units / n).
-__device__ __forceinline__ int owner(long long u, long long units, int n) {
-    if (units < (1 << 20) && n < (1 << 11))
-        return (int)(((uint32_t)(u + 1) * (uint32_t)n - 1) / (uint32_t)units);
-    return (int)(((u + 1) * n - 1) / units);
-}
+// `units` granules (below 2^31) dealt to n CTAs: the first r get q + 1, the others q.
+struct Deal {
+    int q, r;
+    Deal() = default;
+    __device__ __forceinline__ Deal(int units, int n)
+        : q((int)((uint32_t)units / (uint32_t)n)), r(units - q * n) {}
+    __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
+    __device__ __forceinline__ int owner(int u) const {
+        const int big = r * (q + 1);
+        return u < big ? (int)((uint32_t)u / (uint32_t)(q + 1))
+                       : r + (int)((uint32_t)(u - big) / (uint32_t)q);
+    }
+};
 
 // A segment that this CTA shares with others: what joining its parts needs.
 struct Pend {
@@ -255,9 +256,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
     __shared__ uint32_t flags[MAX_SLOTS];
-    __shared__ long long wsum[W + 1];
-    __shared__ long long first_off;
-    __shared__ int first_b;
+    __shared__ int wsum[W + 1];
+    __shared__ int first_off, first_b;
     __shared__ Req first_rq;
     __shared__ volatile int abort_flag;
     __shared__ Pend pend[2];
@@ -280,45 +280,108 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         tc::mbar_init(&empty[s], p.rtc);
         tc::fence_mbar_init();
     }
-    const int per = (p.B + NTH - 1) / NTH;
-    long long mine = 0;
+    // what comes after the lengths: the page table and Q, on their way to L2
+    // while the lengths are read (a line per thread of the grid)
+    for (size_t k = blockIdx.x * NTH + tid; k < p.table_lines + p.q_lines;
+         k += (size_t)gridDim.x * NTH)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            k < p.table_lines
+                ? reinterpret_cast<const char*>(p.pm.table) + k * 128
+                : static_cast<const char*>(p.q) + (k - p.table_lines) * 128));
+    // How the granules are dealt out.  Up to 32 requests every warp reads all
+    // lengths, one per lane; beyond, the block does, some per thread.
+    //   whole:   short segments (a warp takes two granules at most), one to a
+    //            CTA, when there are CTAs enough;
+    //   aligned: few long segments: each gets CTAs of its own, by its length
+    //            (no CTA then works, and joins, in two segments);
+    //   else     the row of all granules is cut evenly, at least 2^min_sh each.
+    Walk wk;
+    Deal deal;
+    int g0 = 0, n_cta, units;
+    int own_c0 = -1, own_c1 = -1;        // aligned: the segment's CTAs
     uint32_t bits = 0;
-    Req rq0{};
-    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
-        rq0 = request(p, b, bits);
-        mine += (long long)rq0.ng * hr;
-    }
-    if (bits && blockIdx.x == 0) raise_status(p.ws, bits);
-    long long incl = mine;
+    const int nseg = p.B * hr, cta = blockIdx.x;
+    if (p.B <= 32) {
+        Req rq{0, 0, 0};
+        if (lane < p.B) rq = request(p, lane, bits);
+        units = __reduce_add_sync(0xffffffffu, rq.ng) * hr;
+        const int longest = __reduce_max_sync(0xffffffffu, rq.ng);
+        const bool whole = nseg <= (int)gridDim.x && longest <= 2 * (W / p.rtc);
+        n_cta = whole ? nseg : min((int)gridDim.x, (units + (1 << p.min_sh) - 1) >> p.min_sh);
+        const bool aligned = !whole && 4 * nseg <= n_cta && units < (1 << 22);
+        // CTAs per segment of the lane's request, or granules of the request
+        int k = whole ? 1 : rq.ng;
+        if (aligned) k = 1 + (n_cta - nseg) * rq.ng / units;
+        if (lane >= p.B) k = 0;
+        int incl = k * hr;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    long long before = 0, units = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        deal = Deal(units, n_cta);
+        g0 = deal.start(cta);
+        const int want = whole || aligned ? cta : g0;
+        const uint32_t hit = __ballot_sync(0xffffffffu, want < incl);
+        if (hit == 0 || cta >= n_cta) return;
+        const int b = __ffs(hit) - 1;
+        wk.b = b;
+        wk.rq.L = __shfl_sync(0xffffffffu, rq.L, b);
+        wk.rq.n = __shfl_sync(0xffffffffu, rq.n, b);
+        wk.rq.ng = __shfl_sync(0xffffffffu, rq.ng, b);
+        k = __shfl_sync(0xffffffffu, k, b);
+        const int off = want - (__shfl_sync(0xffffffffu, incl, b) - k * hr);
+        wk.seg = (int)((uint32_t)off / (uint32_t)k);
+        const int rest = off - wk.seg * k;
+        if (whole) {
+            wk.pos = 0;
+            wk.left = wk.rq.ng;
+        } else if (aligned) {
+            const Deal d(wk.rq.ng, k);
+            wk.pos = d.start(rest);
+            wk.left = d.start(rest + 1) - wk.pos;
+            own_c0 = cta - rest;
+            own_c1 = own_c0 + k - 1;
+        } else {
+            wk.pos = rest;
+            wk.left = deal.start(cta + 1) - g0;
+        }
+        __syncthreads();
+    } else {
+        const int per = (p.B + NTH - 1) / NTH;
+        int mine = 0;
+        Req rq0{};
+        for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
+            rq0 = request(p, b, bits);
+            mine += rq0.ng * hr;
+        }
+        int incl = mine;
 #pragma unroll
-    for (int w = 0; w <= W; ++w) {
-        const long long x = wsum[w];
-        if (w < warp) before += x;
-        units += x;
-    }
-    // a CTA per segment, and per 2^min_sh granules of longer ones
-    const int n_cta = (int)min((long long)gridDim.x,
-                               max((units + (1 << p.min_sh) - 1) >> p.min_sh,
-                                   (long long)p.B * hr));
-    if ((int)blockIdx.x >= n_cta) return;
-    const long long g0 = muldiv(units, blockIdx.x, n_cta);
-    const long long g1 = muldiv(units, blockIdx.x + 1, n_cta);
-    {
-        const long long lo = before + incl - mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        int before = 0;
+        units = 0;
+#pragma unroll
+        for (int w = 0; w <= W; ++w) {
+            const int x = wsum[w];
+            if (w < warp) before += x;
+            units += x;
+        }
+        n_cta = min((int)gridDim.x, (units + (1 << p.min_sh) - 1) >> p.min_sh);
+        if (cta >= n_cta) return;
+        deal = Deal(units, n_cta);
+        g0 = deal.start(cta);
+        const int lo = before + incl - mine;
         if (g0 >= lo && g0 < lo + mine) {
-            long long at = lo;
+            int at = lo;
             for (int b = tid * per;; ++b) {
                 uint32_t ignore = 0;
                 if (per > 1) rq0 = request(p, b, ignore);
-                const long long c = (long long)rq0.ng * hr;
+                const int c = rq0.ng * hr;
                 if (g0 < at + c) {
                     first_b = b;
                     first_off = g0 - at;
@@ -328,19 +391,14 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 at += c;
             }
         }
-    }
-    __syncthreads();
-    Walk wk;
-    wk.b = first_b;
-    wk.left = g1 - g0;
-    wk.rq = first_rq;
-    if (first_off < 0x7fffffff) {
+        __syncthreads();
+        wk.b = first_b;
+        wk.rq = first_rq;
+        wk.left = deal.start(cta + 1) - g0;
         wk.seg = (int)((uint32_t)first_off / (uint32_t)wk.rq.ng);
-        wk.pos = (int)((uint32_t)first_off % (uint32_t)wk.rq.ng);
-    } else {
-        wk.seg = (int)(first_off / wk.rq.ng);
-        wk.pos = (int)(first_off % wk.rq.ng);
+        wk.pos = first_off - wk.seg * wk.rq.ng;
     }
+    if (bits && cta == 0) raise_status(p.ws, bits);
     const int rows_tile = 8 * NR;
     const int cap = p.pm.cap();
 
@@ -480,38 +538,14 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 for (int e = 0; e < 4; ++e) o[nr][i][e] = 0.0f;
         }
     };
-    // join (m2, l2) and outputs read by `get(nr, i)` into the own ones
-    auto join = [&](const float (&m2)[NR][2], const float (&l2)[NR][2], auto get) {
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            float f1[2], f2[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float nm = fmaxf(m[nr][e], m2[nr][e]);
-                const float base = nm == -INFINITY ? 0.0f : nm;
-                f1[e] = ex2(m[nr][e] - base);
-                f2[e] = ex2(m2[nr][e] - base);
-                m[nr][e] = nm;
-                l[nr][e] = l[nr][e] * f1[e] + l2[nr][e] * f2[e];
-            }
-#pragma unroll
-            for (int i = 0; i < A::NT; ++i) {
-                const float4 x = get(nr, i);
-                o[nr][i][0] = o[nr][i][0] * f1[0] + x.x * f2[0];
-                o[nr][i][1] = o[nr][i][1] * f1[1] + x.y * f2[1];
-                o[nr][i][2] = o[nr][i][2] * f1[0] + x.z * f2[0];
-                o[nr][i][3] = o[nr][i][3] * f1[1] + x.w * f2[1];
-            }
-        }
-    };
     auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
-    // The key warps' results meet in shared memory, (max, max, sum, sum) and the
-    // tiles of O^T in register order, and the tiles are then shared out to the
-    // warps: each joins its tiles over the key warps, and writes them to the
-    // output (whole) or to part `at` of the workspace.
     constexpr int JW = NR * (A::NT + 1) * 32;            // float4 of a warp
     constexpr int PO = NR * A::NT * 32, PM = NR * 32;    // float4 of a part's row tile
     constexpr int TPR = NR * A::NT;                      // tiles of a row tile
+    // The end of a segment portion (or of the joining of parts): the key warps'
+    // results meet in shared memory, (max, max, sum, sum) and the tiles of O^T in
+    // register order; the tiles are shared out to the warps by twos, joined over
+    // the key warps, and go to the output (whole) or to part `at` of the workspace.
     auto finish = [&](int b, int seg, int n, bool whole, size_t at) {
         bar();                                           // everyone is done with buf
         if (kw < KW) {
@@ -526,42 +560,48 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         bar();
-        using T = typename io_t<IO>::T;
-        uint32_t bits = 0;
 #pragma unroll 1
-        for (int task = warp; task < p.rtc * TPR; task += W) {
-            const int rt2 = task / TPR, nr = task % TPR / A::NT, i = task % A::NT;
+        for (int task = warp; task < p.rtc * TPR / 2; task += W) {
+            const int rt2 = task / (TPR / 2), q = task % (TPR / 2);
+            const int nr = q / (A::NT / 2), i = q % (A::NT / 2) * 2;
             const float4* s = buf + rt2 * JW + nr * (A::NT + 1) * 32 + lane;
             const int step = p.rtc * JW;
+            float4 x[W];
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const float4 x = s[min(k, KW - 1) * step];
-                m0 = fmaxf(m0, x.x);
-                m1 = fmaxf(m1, x.y);
-            }
-            const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
-            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k = 0; k < W; ++k) x[k] = s[min(k, KW - 1) * step];
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                const int at = min(k, KW - 1) * step;
-                const float4 x = s[at], z = s[at + (1 + i) * 32];
-                const float f0 = k < KW ? ex2(x.x - b0) : 0.0f;
-                const float f1 = k < KW ? ex2(x.y - b1) : 0.0f;
-                if (k >= KW) continue;               // 0 x inf
-                l0 += x.z * f0;
-                l1 += x.w * f1;
-                y.x += z.x * f0;
-                y.y += z.y * f1;
-                y.z += z.z * f0;
-                y.w += z.w * f1;
+                m0 = fmaxf(m0, x[k].x);
+                m1 = fmaxf(m1, x[k].y);
+            }
+            const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+            float4 y[2];
+            y[0] = y[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float f0 = ex2(x[k].x - b0), f1 = ex2(x[k].y - b1);
+                const float4 z0 = s[min(k, KW - 1) * step + (1 + i) * 32];
+                const float4 z1 = s[min(k, KW - 1) * step + (2 + i) * 32];
+                if (k >= KW) continue;
+                l0 += x[k].z * f0;
+                l1 += x[k].w * f1;
+                y[0].x += z0.x * f0;
+                y[0].y += z0.y * f1;
+                y[0].z += z0.z * f0;
+                y[0].w += z0.w * f1;
+                y[1].x += z1.x * f0;
+                y[1].y += z1.y * f1;
+                y[1].z += z1.z * f0;
+                y[1].w += z1.w * f1;
             }
             const int r0 = ((p.rg(seg) * p.rtc + rt2) * NR + nr) * 8 + 2 * t;
             if (!whole) {
                 // lanes whose rows the step does not have write nothing
                 if (r0 >= n * p.G) continue;
                 const size_t pt = at * p.rtc + rt2;
-                __stcg(p.part_o + pt * PO + (nr * A::NT + i) * 32 + lane, y);
+                __stcg(p.part_o + pt * PO + (nr * A::NT + i) * 32 + lane, y[0]);
+                __stcg(p.part_o + pt * PO + (nr * A::NT + i + 1) * 32 + lane, y[1]);
                 if (i == 0)
                     __stcg(p.part_ml + pt * PM + nr * 32 + lane, make_float4(m0, m1, l0, l1));
                 continue;
@@ -571,8 +611,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 l0 += __shfl_xor_sync(0xffffffffu, l0, d);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, d);
             }
+            using T = typename io_t<IO>::T;
             const int hk = p.hk(seg);
-            const int d0 = (i / (A::RL / 2) * 8 + g) * A::RL + 2 * (i % (A::RL / 2));
+            bool bad = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int tok = p.tok(r0 + e);
@@ -580,19 +621,24 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 const float sum = e ? l1 : l0;
                 const bool real = tok < n && sum != 0.0f;
                 const float inv = real ? 1.0f / sum : 0.0f;
-                const float u = real ? (e ? y.y : y.x) * inv : 0.0f;
-                const float v = real ? (e ? y.w : y.z) * inv : 0.0f;
-                if (!(fabsf(u) <= 3.4028234663852886e38f && fabsf(v) <= 3.4028234663852886e38f))
-                    bits = SPEC_DEV_RANGE;
                 T* dst = static_cast<T*>(p.o) +
-                         (((size_t)b * p.T + tok) * p.Hq + hk * p.G + r0 + e - tok * p.G) * D + d0;
-                if constexpr (IO == SPEC_IO_F32)
-                    *reinterpret_cast<float2*>(dst) = make_float2(u, v);
-                else
-                    *reinterpret_cast<uint32_t*>(dst) = packb(u, v);
+                         (((size_t)b * p.T + tok) * p.Hq + hk * p.G + r0 + e - tok * p.G) * D;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int d0 = ((i + k) / (A::RL / 2) * 8 + g) * A::RL +
+                                   2 * ((i + k) % (A::RL / 2));
+                    const float u = real ? (e ? y[k].y : y[k].x) * inv : 0.0f;
+                    const float v = real ? (e ? y[k].w : y[k].z) * inv : 0.0f;
+                    bad |= !(fabsf(u) <= 3.4028234663852886e38f &&
+                             fabsf(v) <= 3.4028234663852886e38f);
+                    if constexpr (IO == SPEC_IO_F32)
+                        *reinterpret_cast<float2*>(dst + d0) = make_float2(u, v);
+                    else
+                        *reinterpret_cast<uint32_t*>(dst + d0) = packb(u, v);
+                }
             }
+            if (bad) raise_status(p.ws, SPEC_DEV_RANGE);
         }
-        if (bits) raise_status(p.ws, bits);
     };
 
     // one granule: keys [kb, kb + GK) in ring slot `slot`; have: its halves in the pool
@@ -605,48 +651,65 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int h = 0; h < NS; ++h) x[nr][h][0] = x[nr][h][1] = x[nr][h][2] = x[nr][h][3] = 0.0f;
+        // consecutive products go to different accumulators: the halves in turn
 #pragma unroll
         for (int j = 0; j < A::KCH; ++j) {
+            uint32_t w0[NS][4], w1[NS][4];
 #pragma unroll
             for (int h = 0; h < NS; ++h) {
                 const uint4 k0 = lds128(ks + chunk_off<A>(h * SUB + kr, t + 4 * j));
                 const uint4 k1 = lds128(ks + chunk_off<A>(h * SUB + kr + 8, t + 4 * j));
-                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-                if constexpr (A::Q8) {
+                w0[h][0] = k0.x, w0[h][1] = k0.y, w0[h][2] = k0.z, w0[h][3] = k0.w;
+                w1[h][0] = k1.x, w1[h][1] = k1.y, w1[h][2] = k1.z, w1[h][3] = k1.w;
+            }
+            if constexpr (A::Q8) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t a[4];
-                        e4m3x4(w0[i], a[0], a[2]);
-                        e4m3x4(w1[i], a[1], a[3]);
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a[NS][4];
+#pragma unroll
+                    for (int h = 0; h < NS; ++h) {
+                        e4m3x4(w0[h][i], a[h][0], a[h][2]);
+                        e4m3x4(w1[h][i], a[h][1], a[h][3]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < A::QT; ++q)
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                            for (int q = 0; q < A::QT; ++q)
-                                mma_f16_16816(x[nr][h], a, qf[nr][q][j][2 * i],
+                            for (int h = 0; h < NS; ++h)
+                                mma_f16_16816(x[nr][h], a[h], qf[nr][q][j][2 * i],
                                               qf[nr][q][j][2 * i + 1]);
+                }
+            } else if constexpr (A::F32) {
+                uint32_t a[NS][3][4];
+#pragma unroll
+                for (int h = 0; h < NS; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t* w = k % 2 ? w1[h] : w0[h];
+                        split3x2(__uint_as_float(w[k / 2 * 2]), __uint_as_float(w[k / 2 * 2 + 1]),
+                                 a[h][0][k], a[h][1][k], a[h][2][k]);
                     }
-                } else if constexpr (A::F32) {
-                    uint32_t a[3][4];
-                    split3x2(__uint_as_float(w0[0]), __uint_as_float(w0[1]), a[0][0], a[1][0], a[2][0]);
-                    split3x2(__uint_as_float(w1[0]), __uint_as_float(w1[1]), a[0][1], a[1][1], a[2][1]);
-                    split3x2(__uint_as_float(w0[2]), __uint_as_float(w0[3]), a[0][2], a[1][2], a[2][2]);
-                    split3x2(__uint_as_float(w1[2]), __uint_as_float(w1[3]), a[0][3], a[1][3], a[2][3]);
+#pragma unroll
+                for (int q = 2; q >= 0; --q)                  // parts i + q <= 2: 2^-24 is left
+#pragma unroll
+                    for (int i = 2 - q; i >= 0; --i)
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                            for (int h = 0; h < NS; ++h)
+                                mma_bf16_16816(x[nr][h], a[h][i], qf[nr][q][j][0], qf[nr][q][j][1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int q = 2; q >= 0; --q)           // parts i + q <= 2: 2^-24 is left
-#pragma unroll
-                            for (int i = 2 - q; i >= 0; --i)
-                                mma_bf16_16816(x[nr][h], a[i], qf[nr][q][j][0], qf[nr][q][j][1]);
-                } else {
-                    const uint32_t a0[4] = {w0[0], w1[0], w0[1], w1[1]};
-                    const uint32_t a1[4] = {w0[2], w1[2], w0[3], w1[3]};
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) {
-                        mma_bf16_16816(x[nr][h], a0, qf[nr][0][j][0], qf[nr][0][j][1]);
-                        mma_bf16_16816(x[nr][h], a1, qf[nr][0][j][2], qf[nr][0][j][3]);
-                    }
-                }
+                        for (int h = 0; h < NS; ++h) {
+                            const uint32_t a[4] = {w0[h][2 * i], w1[h][2 * i], w0[h][2 * i + 1],
+                                                   w1[h][2 * i + 1]};
+                            mma_bf16_16816(x[nr][h], a, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
+                        }
             }
         }
         // scores in log2 units, -inf where the row does not see the key
@@ -835,51 +898,57 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                             if (kb + h * SUB + row[k] >= cut || !((have >> h) & 1u))
                                 v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0;
                     }
+                    // consecutive products go to different tiles
                     if constexpr (A::F32) {
+                        uint32_t a[2][3][4];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            uint32_t a[3][4];
+                        for (int r = 0; r < 2; ++r)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)       // columns va, vb, then + 8
                                 split3x2(__uint_as_float(v[i / 2 * 2][2 * r + i % 2]),
-                                         __uint_as_float(v[i / 2 * 2 + 1][2 * r + i % 2]), a[0][i],
-                                         a[1][i], a[2][i]);
+                                         __uint_as_float(v[i / 2 * 2 + 1][2 * r + i % 2]),
+                                         a[r][0][i], a[r][1][i], a[r][2][i]);
 #pragma unroll
-                            for (int nr = 0; nr < NR; ++nr)
+                        for (int q = 2; q >= 0; --q)
 #pragma unroll
-                                for (int q = 2; q >= 0; --q)
+                            for (int i = 2 - q; i >= 0; --i)
 #pragma unroll
-                                    for (int i = 2 - q; i >= 0; --i)
-                                        mma_o(nr, j * 2 + r, a[i], h, q);
-                        }
+                                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) mma_o(nr, j * 2 + r, a[r][i], h, q);
                     } else if constexpr (A::Q8) {
                         constexpr int NW = A::ROWB == 64 ? 2 : 4;
 #pragma unroll
                         for (int i = 0; i < NW; ++i) {
+                            uint32_t a[2][4];
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const uint32_t sel = y ? 0x7362 : 0x5140;
-                                uint32_t a[4];
-                                e4m3x4(__byte_perm(v[0][i], v[1][i], sel), a[0], a[1]);
-                                e4m3x4(__byte_perm(v[2][i], v[3][i], sel), a[2], a[3]);
+                                e4m3x4(__byte_perm(v[0][i], v[1][i], sel), a[y][0], a[y][1]);
+                                e4m3x4(__byte_perm(v[2][i], v[3][i], sel), a[y][2], a[y][3]);
+                            }
+#pragma unroll
+                            for (int q = 0; q < A::PT; ++q)
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                    for (int q = 0; q < A::PT; ++q) mma_o(nr, 2 * i + y, a, h, q);
-                            }
+                                    for (int y = 0; y < 2; ++y) mma_o(nr, 2 * i + y, a[y], h, q);
                         }
                     } else {
+                        uint32_t a[4][4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t a[4] = {__byte_perm(v[0][i], v[1][i], 0x5410),
-                                                   __byte_perm(v[0][i], v[1][i], 0x7632),
-                                                   __byte_perm(v[2][i], v[3][i], 0x5410),
-                                                   __byte_perm(v[2][i], v[3][i], 0x7632)};
+                            a[i][0] = __byte_perm(v[0][i], v[1][i], 0x5410);
+                            a[i][1] = __byte_perm(v[0][i], v[1][i], 0x7632);
+                            a[i][2] = __byte_perm(v[2][i], v[3][i], 0x5410);
+                            a[i][3] = __byte_perm(v[2][i], v[3][i], 0x7632);
+                        }
+#pragma unroll
+                        for (int q = 0; q < A::PT; ++q)
 #pragma unroll
                             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                for (int q = 0; q < A::PT; ++q) mma_o(nr, 4 * j + i, a, h, q);
-                        }
+                                for (int i = 0; i < 4; ++i) mma_o(nr, 4 * j + i, a[i], h, q);
                     }
                 }
             }
@@ -990,7 +1059,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
 
-    long long gpos = g0;                 // global index of the present granule
+    int gpos = g0;                       // global index of the present granule
     uint4 raw[NR][RAW];
     // one row tile: the next segment's Q rows are fetched during this one
     constexpr bool AHEAD = NR == 1 && IO == SPEC_IO_BF16;
@@ -1059,10 +1128,14 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         n = wk.rq.n;
         whole = cnt == wk.rq.ng;
         if (!whole) {
-            const long long s0 = gpos - wk.pos, s1 = s0 + wk.rq.ng;
-            const int c0 = owner(s0, units, n_cta), c1 = owner(s1 - 1, units, n_cta);
-            const int shift = s0 > muldiv(units, c0, n_cta);
-            at = 2 * blockIdx.x + ((int)blockIdx.x == c0 ? shift : 0);
+            int c0 = own_c0, c1 = own_c1, shift = 0;
+            if (c0 < 0) {
+                const int s0 = gpos - wk.pos;
+                c0 = deal.owner(s0);
+                c1 = deal.owner(s0 + wk.rq.ng - 1);
+                shift = s0 > deal.start(c0);
+            }
+            at = 2 * cta + (cta == c0 ? shift : 0);
             if (tid == 0) {
                 Pend& pe = pend[gpos != g0];
                 pe.b = b;
@@ -1079,7 +1152,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             // ---- out of granules: count this CTA's parts in (each warp that
             // wrote some, once for both segments it may share), and join the
             // segments whose last part was this CTA's
-            const int writers = min(W, p.rtc * TPR);
+            const int writers = min(W, p.rtc * TPR / 2);
             if (!counted) {
                 counted = true;
                 bar();                                   // pend is there
@@ -1107,25 +1180,54 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             seg = pe.seg;
             n = pe.n;
             const int row0 = (p.rg(seg) * p.rtc + rt) * rows_tile;
-#pragma unroll 2
-            for (int c = pe.c0 + kw; c <= pe.c1 && kw < KW; c += KW) {
-                const size_t pt = (size_t)(2 * c + (c == pe.c0 ? pe.shift : 0)) * p.rtc + rt;
-                float m2[NR][2], l2[NR][2];
-                bool in[NR];
+            constexpr int STEP = NR == 1 ? 3 : 1;        // parts under way at once
+#pragma unroll 1
+            for (int c = pe.c0 + kw; c <= pe.c1 && kw < KW; c += KW * STEP) {
+                float4 x[STEP][NR], z[STEP][NR][A::NT];
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    in[nr] = row0 + nr * 8 + 2 * t < n * p.G;
-                    float4 x = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
-                    if (in[nr]) x = __ldcg(p.part_ml + pt * PM + nr * 32 + lane);
-                    m2[nr][0] = x.x;
-                    m2[nr][1] = x.y;
-                    l2[nr][0] = x.z;
-                    l2[nr][1] = x.w;
+                for (int j = 0; j < STEP; ++j) {
+                    const int cc = c + j * KW;
+                    const size_t pt = (size_t)(2 * cc + (cc == pe.c0 ? pe.shift : 0)) * p.rtc + rt;
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        // lanes whose rows the step does not have read nothing
+                        const bool in = cc <= pe.c1 && row0 + nr * 8 + 2 * t < n * p.G;
+                        x[j][nr] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+                        if (in) x[j][nr] = __ldcg(p.part_ml + pt * PM + nr * 32 + lane);
+#pragma unroll
+                        for (int i = 0; i < A::NT; ++i) {
+                            z[j][nr][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (in)
+                                z[j][nr][i] =
+                                    __ldcg(p.part_o + pt * PO + (nr * A::NT + i) * 32 + lane);
+                        }
+                    }
                 }
-                join(m2, l2, [&](int nr, int i) {
-                    return in[nr] ? __ldcg(p.part_o + pt * PO + (nr * A::NT + i) * 32 + lane)
-                                  : make_float4(0, 0, 0, 0);
-                });
+#pragma unroll
+                for (int j = 0; j < STEP; ++j)
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        float f1[2], f2[2];
+                        const float m2[2] = {x[j][nr].x, x[j][nr].y};
+                        const float l2[2] = {x[j][nr].z, x[j][nr].w};
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float nm = fmaxf(m[nr][e], m2[e]);
+                            const float base = nm == -INFINITY ? 0.0f : nm;
+                            f1[e] = ex2(m[nr][e] - base);
+                            f2[e] = ex2(m2[e] - base);
+                            m[nr][e] = nm;
+                            l[nr][e] = l[nr][e] * f1[e] + l2[e] * f2[e];
+                        }
+#pragma unroll
+                        for (int i = 0; i < A::NT; ++i) {
+                            const float4 y = z[j][nr][i];
+                            o[nr][i][0] = o[nr][i][0] * f1[0] + y.x * f2[0];
+                            o[nr][i][1] = o[nr][i][1] * f1[1] + y.y * f2[1];
+                            o[nr][i][2] = o[nr][i][2] * f1[0] + y.z * f2[0];
+                            o[nr][i][3] = o[nr][i][3] * f1[1] + y.w * f2[1];
+                        }
+                    }
             }
         }
         finish(b, seg, n, whole, at);
@@ -1203,6 +1305,8 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.rtc = w.rtc;
     p.rtg = w.rtg;
     p.min_sh = 2;
+    p.table_lines = ((size_t)c.B * c.max_pages * 4 + 127) / 128;
+    p.q_lines = ((size_t)c.B * c.T * c.Hq * D * (IO == SPEC_IO_F32 ? 4 : 2) + 127) / 128;
     p.box = c.page >= GK ? GK : SUB;
     p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
     constexpr int fixed = 1024 + W * NR * (A::NT + 1) * 32 * 16;
