@@ -497,17 +497,21 @@ def _arg(t, dtype, shape, name, device):
     current device (None passes: an argument that may be absent)."""
     if t is None:
         return None
+    try:
+        if (t.dtype is dtype and t.get_device() == device and t.shape == shape
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if t.get_device() != device:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _workspace(ws, need, device):
@@ -518,6 +522,44 @@ def _workspace(ws, need, device):
     if ws.nbytes < need:
         raise ValueError(f"ws holds {ws.nbytes} bytes, {need} are needed")
     return ws.data_ptr()
+
+
+class _Plan:
+    """What the calls of one configuration on one device need to know: the
+    shapes and types of their arguments and the workspace's size."""
+    __slots__ = ("new", "q", "b", "dt", "need")
+
+    def __init__(self, cfg):
+        if isinstance(cfg, SpecPagedCfg):
+            self.new = (cfg.B, cfg.T, cfg.Hkv, cfg.D)
+            self.q = (cfg.B, cfg.T, cfg.Hq, cfg.D)
+            self.need = int(load().spec_paged_workspace_bytes(ctypes.byref(cfg), 0))
+        else:
+            self.new = (cfg.B, cfg.N)
+            self.q = (cfg.B, cfg.N + 1, cfg.V)
+            self.need = int(load().spec_draft_workspace_bytes(ctypes.byref(cfg), 0))
+        self.b = (cfg.B,)
+        self.dt = _io_dtype(cfg)
+
+
+_plans = {}
+
+
+def _plan(cfg, device) -> _Plan:
+    key = (type(cfg), bytes(cfg), device)
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) >= 1024:
+            _plans.clear()
+        p = _plans[key] = _Plan(cfg)
+    return p
+
+
+def _raw_stream(stream, device):
+    """_stream as an integer; the current stream without making an object."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _required(t, name):
@@ -582,6 +624,7 @@ class PagedKV:
             _arg(_required(kv_len, "kv_len"), i32, (cfg.B,), "kv_len", dev))
         self._t = (k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
         self.key = (pool, cfg.B, cfg.max_pages, cfg.kv_dtype, dt, dev)
+        self._fits = set()
 
     k_pages, v_pages, k_scale, v_scale, page_table, kv_len = (
         property(lambda self, i=i: self._t[i]) for i in range(6))
@@ -599,49 +642,54 @@ class PagedKV:
                    torch.full((cfg.B, cfg.max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros((cfg.B,), dtype=torch.int32, device=device), *sc)
 
-    def c(self, cfg: SpecPagedCfg) -> SpecPagedKV:
-        pool = (cfg.n_pages, cfg.Hkv, cfg.page, cfg.D)
-        if self.key[:4] != (pool, cfg.B, cfg.max_pages, cfg.kv_dtype) or (
-                cfg.kv_dtype == SPEC_KV_IO and self.key[4] != _io_dtype(cfg)):
-            raise ValueError("the cache was made for another configuration")
-        if self.key[5] != torch.cuda.current_device():
+    def c(self, cfg: SpecPagedCfg, device: int) -> SpecPagedKV:
+        if device != self.key[5]:
             raise ValueError(f"the cache is on cuda:{self.key[5]}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+                             f"cuda:{device}")
+        fits = bytes(cfg)
+        if fits not in self._fits:                 # T and Hq may differ from call to call
+            pool = (cfg.n_pages, cfg.Hkv, cfg.page, cfg.D)
+            if self.key[:4] != (pool, cfg.B, cfg.max_pages, cfg.kv_dtype) or (
+                    cfg.kv_dtype == SPEC_KV_IO and self.key[4] != _io_dtype(cfg)):
+                raise ValueError("the cache was made for another configuration")
+            if len(self._fits) >= 64:
+                self._fits.clear()
+            self._fits.add(fits)
         return self._c
 
 
 def kv_page_append(cfg: SpecPagedCfg, kv: PagedKV, k_new, v_new, ws, n_new=None, stream=None):
     """Write the new tokens' rows (k_new, v_new [B][T][Hkv][D] io) behind the
     committed ones; n_new: None or CUDA int32 [B]."""
-    dt, dev = _io_dtype(cfg), torch.cuda.current_device()
-    shape = (cfg.B, cfg.T, cfg.Hkv, cfg.D)
-    _check("kv_page_append", load().kv_page_append(
-        ctypes.byref(cfg), ctypes.byref(kv.c(cfg)), _arg(k_new, dt, shape, "k_new", dev),
-        _arg(v_new, dt, shape, "v_new", dev), _arg(n_new, torch.int32, (cfg.B,), "n_new", dev),
-        _workspace(ws, _STATUS_BYTES, dev), _stream(stream)))
+    dev = torch.cuda.current_device()
+    p = _plan(cfg, dev)
+    _check("kv_page_append", (_lib or load()).kv_page_append(
+        ctypes.byref(cfg), ctypes.byref(kv.c(cfg, dev)), _arg(k_new, p.dt, p.new, "k_new", dev),
+        _arg(v_new, p.dt, p.new, "v_new", dev), _arg(n_new, torch.int32, p.b, "n_new", dev),
+        _workspace(ws, _STATUS_BYTES, dev), _raw_stream(stream, dev)))
 
 
 def kv_page_read(cfg: SpecPagedCfg, kv: PagedKV, k_out, v_out, ws, stream=None):
     """The committed rows as a contiguous cache [B][Lmax][Hkv][D] io (rows at
     or past kv_len are left as they were)."""
-    dt, dev = _io_dtype(cfg), torch.cuda.current_device()
+    dev = torch.cuda.current_device()
+    p = _plan(cfg, dev)
     Lmax = k_out.shape[1] if isinstance(k_out, torch.Tensor) and k_out.dim() == 4 else 0
     shape = (cfg.B, Lmax, cfg.Hkv, cfg.D)
-    _check("kv_page_read", load().kv_page_read(
-        ctypes.byref(cfg), ctypes.byref(kv.c(cfg)), Lmax, _arg(k_out, dt, shape, "k_out", dev),
-        _arg(v_out, dt, shape, "v_out", dev), _workspace(ws, _STATUS_BYTES, dev),
-        _stream(stream)))
+    _check("kv_page_read", (_lib or load()).kv_page_read(
+        ctypes.byref(cfg), ctypes.byref(kv.c(cfg, dev)), Lmax, _arg(k_out, p.dt, shape, "k_out", dev),
+        _arg(v_out, p.dt, shape, "v_out", dev), _workspace(ws, _STATUS_BYTES, dev),
+        _raw_stream(stream, dev)))
 
 
 def attn_decode_paged(cfg: SpecPagedCfg, kv: PagedKV, q, o, ws, n_new=None, stream=None):
     """Attention of the new tokens (q, o [B][T][Hq][D] io) over the paged cache."""
-    dt, dev = _io_dtype(cfg), torch.cuda.current_device()
-    shape = (cfg.B, cfg.T, cfg.Hq, cfg.D)
-    _check("attn_decode_paged", load().attn_decode_paged(
-        ctypes.byref(cfg), ctypes.byref(kv.c(cfg)), _arg(q, dt, shape, "q", dev),
-        _arg(n_new, torch.int32, (cfg.B,), "n_new", dev), _arg(o, dt, shape, "o", dev),
-        _workspace(ws, load().spec_paged_workspace_bytes(ctypes.byref(cfg), 0), dev),
-        _stream(stream)))
+    dev = torch.cuda.current_device()
+    p = _plan(cfg, dev)
+    _check("attn_decode_paged", (_lib or load()).attn_decode_paged(
+        ctypes.byref(cfg), ctypes.byref(kv.c(cfg, dev)), _arg(q, p.dt, p.q, "q", dev),
+        _arg(n_new, torch.int32, p.b, "n_new", dev), _arg(o, p.dt, p.q, "o", dev),
+        _workspace(ws, p.need, dev), _raw_stream(stream, dev)))
 
 
 class DraftBuffers:
@@ -662,18 +710,18 @@ def draft_verify_sampled(cfg: SpecDraftCfg, draft_tok, draft_prob, logits, u, e,
     f32 [B][N], e f32 [B][V]; kv_len / root_tok are advanced when given.  With
     N = 0 (plain sampling) draft_tok, draft_prob and u are not read."""
     dev, f32, i32 = torch.cuda.current_device(), torch.float32, torch.int32
-    B, N, V = cfg.B, cfg.N, cfg.V
+    p = _plan(cfg, dev)
+    N, V = p.new[1], p.q[2]
     if N == 0:
         draft_tok = draft_prob = u = None
-    co = SpecDraftOut(_arg(out.accept_len, i32, (B,), "accept_len", dev),
-                      _arg(out.out_tok, i32, (B, N + 1), "out_tok", dev),
-                      _arg(out.target_prob, f32, (B, N), "target_prob", dev) if N else None)
-    _check("draft_verify_sampled", load().draft_verify_sampled(
-        ctypes.byref(cfg), _arg(draft_tok, i32, (B, N), "draft_tok", dev),
-        _arg(n_draft, i32, (B,), "n_draft", dev),
-        _arg(draft_prob, f32, (B, N, V), "draft_prob", dev),
-        _arg(logits, _io_dtype(cfg), (B, N + 1, V), "logits", dev), _arg(u, f32, (B, N), "u", dev),
-        _arg(e, f32, (B, V), "e", dev), ctypes.byref(co), _arg(kv_len, i32, (B,), "kv_len", dev),
-        _arg(root_tok, i32, (B,), "root_tok", dev),
-        _workspace(ws, load().spec_draft_workspace_bytes(ctypes.byref(cfg), 0), dev),
-        _stream(stream)))
+    co = SpecDraftOut(_arg(out.accept_len, i32, p.b, "accept_len", dev),
+                      _arg(out.out_tok, i32, p.q[:2], "out_tok", dev),
+                      _arg(out.target_prob, f32, p.new, "target_prob", dev) if N else None)
+    _check("draft_verify_sampled", (_lib or load()).draft_verify_sampled(
+        ctypes.byref(cfg), _arg(draft_tok, i32, p.new, "draft_tok", dev),
+        _arg(n_draft, i32, p.b, "n_draft", dev),
+        _arg(draft_prob, f32, p.new + (V,), "draft_prob", dev),
+        _arg(logits, p.dt, p.q, "logits", dev), _arg(u, f32, p.new, "u", dev),
+        _arg(e, f32, p.b + (V,), "e", dev), ctypes.byref(co), _arg(kv_len, i32, p.b, "kv_len", dev),
+        _arg(root_tok, i32, p.b, "root_tok", dev), _workspace(ws, p.need, dev),
+        _raw_stream(stream, dev)))

@@ -33,6 +33,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "paged.cuh"
 #include "tc_util.cuh"
 
@@ -1316,8 +1318,17 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.slots = fit < MAX_SLOTS ? fit : MAX_SLOTS;
     const int smem = fixed + p.slots * per_slot;
     auto kern = attn_paged<IO, KV, D, NR, W>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // once per device and kernel (the size is a constant of the kernel)
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     // at most every granule of a full table
     const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * (((int64_t)c.max_pages * c.page + GK - 1) / GK);
     const int grid = (int)(most < sms ? most : sms);

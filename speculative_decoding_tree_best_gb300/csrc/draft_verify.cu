@@ -14,10 +14,9 @@
 // Two launches, the second under the first's tail:
 //   1. row_mass: every needed logits row in `splits` segments, a CTA each:
 //      (max, sum of 2^((x - max) k)), k = log2(e) / temperature, 16-byte loads,
-//      four in flight per thread.  Rows are V elements apart, so a row may
-//      start inside a 16-byte group: segments are cut at groups, and the
-//      elements of a row's first and last group that are not its own count as
-//      -inf.
+//      eight in flight per thread.  Rows are V elements apart, so a row may
+//      start inside a 16-byte group: the few elements beside its whole groups
+//      are taken one by one.
 //   2. race: each CTA decides its request's chain from the segments' masses
 //      (a warp per row), then scans a slice of the vocabulary at the row where
 //      the chain ended; the request's last CTA (a ticket) joins the slices and
@@ -92,7 +91,7 @@ template <int IO>
 __global__ void __launch_bounds__(NT)
 row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
          const typename io_t<IO>::T* __restrict__ logits, float k, float2* part, int splits) {
-    constexpr int VEC = grp<IO>::VEC, U = 4;
+    constexpr int VEC = grp<IO>::VEC, U = 8;
     __shared__ float sm[NT / 32], ss[NT / 32];
     const int row = blockIdx.x / splits, seg = blockIdx.x % splits;
     const int b = row / (c.N + 1), i = row % (c.N + 1);
@@ -100,47 +99,63 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
     // the second launch may start: it waits for this one's results
     pdl_trigger();
     if (i > new_rows(n_draft, b, c.N, ignore)) return;
+    // the row's own 16-byte groups [g0, g1), and the elements beside them
     const int64_t r0 = (int64_t)row * c.V, r1 = r0 + c.V;
-    const int64_t total = (int64_t)c.B * (c.N + 1) * c.V;
-    const int64_t g0 = r0 / VEC;
-    const int groups = (int)((r1 + VEC - 1) / VEC - g0);
+    const int64_t g0 = (r0 + VEC - 1) / VEC, g1 = r1 / VEC;
+    const int groups = g1 > g0 ? (int)(g1 - g0) : 0;
     const int per = (groups + splits - 1) / splits;
     const int lo = seg * per, hi = min(groups, lo + per);
     const uint4* src = reinterpret_cast<const uint4*>(logits) + g0;
     float m = -INFINITY, s = 0.0f;
     for (int e0 = lo + threadIdx.x; e0 < hi; e0 += U * NT) {
-        float x[U][VEC];
+        uint4 u[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int e = e0 + j * NT;
-            const int64_t at = (g0 + e) * VEC;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (e < hi && at + VEC <= total) u = __ldg(src + e);
-            grp<IO>::unpack(u, x[j]);
-            // the tensor's last elements, beyond its last whole group
-            if (e < hi && at + VEC > total)
-                for (int v = 0; v < VEC; ++v) x[j][v] = at + v < total ? io_t<IO>::ld(logits, at + v) : 0.0f;
-            // a row's edges
-            if (e >= hi || at < r0 || at + VEC > r1)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    if (e >= hi || at + v < r0 || at + v >= r1) x[j][v] = -INFINITY;
+            const uint32_t none = IO == SPEC_IO_F32 ? 0xff800000u : 0xff80ff80u;   // -inf
+            u[j] = make_uint4(none, none, none, none);
+            if (e0 + j * NT < hi) u[j] = __ldg(src + e0 + j * NT);
         }
         float nm = m;
+        if constexpr (IO == SPEC_IO_F32) {
 #pragma unroll
-        for (int j = 0; j < U; ++j)
+            for (int j = 0; j < U; ++j) {
+                float x[VEC];
+                grp<IO>::unpack(u[j], x);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) nm = fmaxf(nm, x[j][v]);
+                for (int v = 0; v < VEC; ++v) nm = fmaxf(nm, x[v]);
+            }
+        } else {
+            __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&u[0].x);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&u[j]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) h = __hmax2(h, p[v]);
+            }
+            nm = fmaxf(nm, fmaxf(__low2float(h), __high2float(h)));   // a NaN is passed over
+        }
         if (m != nm) s *= ex2((m - nm) * k);
         m = nm;
         const float base = m == -INFINITY ? 0.0f : m;      // a NaN beside -inf stays
-        float part_s[U] = {};
+        float ps[4] = {};
 #pragma unroll
-        for (int v = 0; v < VEC; ++v)
+        for (int j = 0; j < U; ++j) {
+            float x[VEC];
+            grp<IO>::unpack(u[j], x);
 #pragma unroll
-            for (int j = 0; j < U; ++j) part_s[j] += ex2((x[j][v] - base) * k);
-#pragma unroll
-        for (int j = 0; j < U; ++j) s += part_s[j];
+            for (int v = 0; v < VEC; ++v) ps[v % 4] += ex2((x[v] - base) * k);
+        }
+        s += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+    }
+    if (seg == 0) {
+        // the elements of the row in groups that it shares with its neighbours
+        const int64_t head = min(g0 * VEC, r1), tail = max(g1 * VEC, head);
+        const int64_t at = threadIdx.x < head - r0 ? r0 + threadIdx.x
+                                                   : tail + (threadIdx.x - (head - r0));
+        if (at < r1 && (at < head || at >= tail)) {
+            const float x = io_t<IO>::ld(logits, at);
+            merge(m, s, x, x == -INFINITY ? 0.0f : x - x + 1.0f, k);   // NaN, +inf: NaN
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -172,7 +187,7 @@ struct RaceArgs {
     int32_t* root_tok;
     void* ws;
     const float2* part;
-    float4* cand;            // [B][slices]: (score, token) of max(0, p - q) and of p
+    float2* cand;            // [B][slices]: (score, token)
     uint32_t* tickets;       // [B]
     int splits, slices, per; // per: tokens of a slice
     float k;                 // log2(e) / temperature
@@ -184,14 +199,16 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     using T = typename io_t<IO>::T;
     constexpr int VEC = 8;
     __shared__ float row_m[SPEC_MAX_ROWS], row_s[SPEC_MAX_ROWS];
-    __shared__ int keep[SPEC_MAX_ROWS];
+    __shared__ float tok_x[SPEC_MAX_ROWS], tok_q[SPEC_MAX_ROWS];
+    __shared__ int keep[SPEC_MAX_ROWS], draft[SPEC_MAX_ROWS];
     __shared__ Cand sh[NT / 32];
     __shared__ int last_cta;
     const int b = blockIdx.y, N = c.N, V = c.V, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const T* logits = static_cast<const T*>(a.logits);
     const int lo = blockIdx.x * a.per, hi = min(V, lo + a.per);
     const float* e = a.e + (size_t)b * V;
-    // what does not depend on the decision: this slice's first exponentials
+    // ---- what does not depend on the masses: this slice's first exponentials,
+    // the drafts and what the target and the drafter say of them
     const bool vec = V % VEC == 0;
     float ev[VEC];
     const int v0 = lo + tid * VEC;
@@ -201,9 +218,19 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     }
     uint32_t bits = 0;
     const int n = new_rows(a.n_draft, b, N, bits);
+    if (tid < n) {
+        const int x = a.draft_tok[(size_t)b * N + tid];
+        const bool in = x >= 0 && x < V;
+        if (!in) bits |= SPEC_DEV_BADTOK;
+        draft[tid] = x;
+        tok_x[tid] = in ? io_t<IO>::ld(logits, ((size_t)b * (N + 1) + tid) * V + x) : 0.0f;
+        const float q = in && a.draft_prob ? a.draft_prob[((size_t)b * N + tid) * V + x] : 1.0f;
+        tok_q[tid] = a.u[(size_t)b * N + tid] * q;
+    }
+    if (bits && blockIdx.x == 0) raise_status(a.ws, bits);
     pdl_wait();
 
-    // ---- the chain: a warp per row
+    // ---- the rows' masses (a warp per row) and the chain
     for (int i = warp; i <= n; i += NT / 32) {
         const size_t row = (size_t)b * (N + 1) + i;
         float m = -INFINITY, s = 0.0f;
@@ -218,47 +245,38 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
             merge(m, s, om, os, a.k);
         }
         if (lane == 0) {
-            const bool fine = s > 0.0f && s <= 3.0e38f;     // else NaN, +inf or no mass
             row_m[i] = m;
-            row_s[i] = fine ? s : 0.0f;
-            int ok = 0;
-            if (i < n) {
-                const int x = a.draft_tok[(size_t)b * N + i];
-                const bool in = x >= 0 && x < V;
-                float p = 0.0f;
-                if (!in) bits |= SPEC_DEV_BADTOK;
-                if (in && fine) {
-                    p = expf((io_t<IO>::ld(logits, row * V + x) - m) / c.temperature) / s;
-                    const float q = a.draft_prob ? a.draft_prob[((size_t)b * N + i) * V + x] : 1.0f;
-                    ok = a.u[(size_t)b * N + i] * q < p;
-                }
-                if (blockIdx.x == 0) a.out.target_prob[(size_t)b * N + i] = p;
-            }
-            keep[i] = ok;
+            row_s[i] = s > 0.0f && s <= 3.0e38f ? s : 0.0f;   // else NaN, +inf or no mass
         }
     }
-    if (blockIdx.x == 0) {
-        for (int j = n + tid; j < N; j += NT) a.out.target_prob[(size_t)b * N + j] = 0.0f;
-        if (bits) raise_status(a.ws, bits);
+    __syncthreads();
+    if (tid < N) {
+        float p = 0.0f;
+        const bool in = tid < n && draft[tid] >= 0 && draft[tid] < V;
+        if (in && row_s[tid] > 0.0f)
+            p = expf((tok_x[tid] - row_m[tid]) / c.temperature) / row_s[tid];
+        if (tid < n) keep[tid] = in && tok_q[tid] < p;
+        if (blockIdx.x == 0) a.out.target_prob[(size_t)b * N + tid] = p;
     }
     __syncthreads();
     int kept = 0;
     while (kept < n && keep[kept]) ++kept;
 
     // ---- the race over this slice of the row where the chain ended
-    const size_t row = (size_t)b * (N + 1) + kept;
     const float m = row_m[kept], s = row_s[kept], inv = 1.0f / s;
-    const T* lp = logits + row * V;
+    const T* lp = logits + ((size_t)b * (N + 1) + kept) * V;
     const float* qp = kept < n && a.draft_prob ? a.draft_prob + ((size_t)b * N + kept) * V : nullptr;
-    const int point = kept < n && !a.draft_prob ? a.draft_tok[(size_t)b * N + kept] : -1;
-    Cand rest{-INFINITY, NONE}, all{-INFINITY, NONE};
+    const int point = kept < n && !a.draft_prob ? draft[kept] : -1;
+    Cand best{-INFINITY, NONE};
+    float bar = 0.0f;                    // a little under the best score so far
     auto score = [&](float x, float q, float ex, int v) {
-        const float p = ex2((x - m) * a.k) * inv;
-        if (p > 0.0f) take(all, p / ex, v);
-        const float w = p - q;
-        if (w > 0.0f) take(rest, w / ex, v);
+        const float w = ex2((x - m) * a.k) * inv - q;
+        if (w > bar * ex) {              // seldom: the division is not for every token
+            take(best, w / ex, v);
+            bar = best.s * (1.0f - 0x1p-20f);
+        }
     };
-    if (s > 0.0f) {
+    auto scan = [&]() {
         if (vec) {
             for (int v = v0; v < hi; v += NT * VEC) {
                 float x[VEC], q[VEC];
@@ -290,31 +308,36 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
             for (int v = lo + tid; v < hi; v += NT)
                 score(io_t<IO>::ld(lp, v), qp ? qp[v] : (v == point ? 1.0f : 0.0f), e[v], v);
         }
-    }
-    rest = block_best(rest, sh);
-    all = block_best(all, sh);
+    };
+    if (s > 0.0f) scan();
+    best = block_best(best, sh);
     if (tid == 0) {
         __stcg(a.cand + (size_t)b * a.slices + blockIdx.x,
-               make_float4(rest.s, __int_as_float(rest.i), all.s, __int_as_float(all.i)));
-        __threadfence();
+               make_float2(best.s, __int_as_float(best.i)));
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
         last_cta = atomicAdd(a.tickets + b, 1u) == (uint32_t)a.slices - 1;
-        __threadfence();
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
     }
     __syncthreads();
     if (!last_cta) return;
-    rest = all = Cand{-INFINITY, NONE};
+    best = Cand{-INFINITY, NONE};
     for (int k = tid; k < a.slices; k += NT) {
-        const float4 x = __ldcg(a.cand + (size_t)b * a.slices + k);
-        take(rest, x.x, __float_as_int(x.y));
-        take(all, x.z, __float_as_int(x.w));
+        const float2 x = __ldcg(a.cand + (size_t)b * a.slices + k);
+        take(best, x.x, __float_as_int(x.y));
     }
-    rest = block_best(rest, sh);
-    all = block_best(all, sh);
-    const Cand best = kept < n && rest.i != NONE ? rest : all;
+    best = block_best(best, sh);
+    if (best.i == NONE && s > 0.0f && kept < n) {
+        // p <= q everywhere in fp32 (a refusal at a rounding's distance): p decides
+        Cand again{-INFINITY, NONE};
+        for (int v = tid; v < V; v += NT) {
+            const float w = ex2((io_t<IO>::ld(lp, v) - m) * a.k) * inv;
+            if (w > 0.0f) take(again, w / e[v], v);
+        }
+        best = block_best(again, sh);
+    }
     const int tok = best.i != NONE ? best.i : 0;
     for (int j = tid; j <= N; j += NT)
-        a.out.out_tok[(size_t)b * (N + 1) + j] =
-            j < kept ? a.draft_tok[(size_t)b * N + j] : (j == kept ? tok : -1);
+        a.out.out_tok[(size_t)b * (N + 1) + j] = j < kept ? draft[j] : (j == kept ? tok : -1);
     if (tid == 0) {
         a.tickets[b] = 0;                                // for the next call
         a.out.accept_len[b] = kept + 1;
@@ -346,7 +369,7 @@ cudaError_t launch_draft_verify(const spec_draft_cfg& c, const int32_t* draft_to
     if (sms < 1) return cudaErrorInvalidDevice;
     const DraftWs w = draft_ws_layout(c, sms);
     RaceArgs a{draft_tok, n_draft, draft_prob, logits, u, e, out, kv_len, root_tok, ws,
-               ws_ptr<const float2>(ws, w.part_off), ws_ptr<float4>(ws, w.cand_off),
+               ws_ptr<const float2>(ws, w.part_off), ws_ptr<float2>(ws, w.cand_off),
                ws_ptr<uint32_t>(ws, w.ticket_off), w.splits, w.slices, w.per,
                1.4426950408889634f / c.temperature};
     return c.io_dtype == SPEC_IO_BF16 ? verify_t<SPEC_IO_BF16>(c, n_draft, logits, a, w, st)
