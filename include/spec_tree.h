@@ -493,9 +493,10 @@ enum {
 #define SPEC_MIN_PAGE 16
 #define SPEC_MAX_PAGE 1024
 #define SPEC_MAX_PAGED_B 4096
+#define SPEC_MAX_HKV 1024
 
 /* Shape of the paged calls.  Limits (else ST_EINVAL): 1 <= B <= 4096;
- * 1 <= T <= 2^20; Hq % Hkv == 0; D in {64, 128};
+ * 1 <= T <= 2^20; Hkv <= 1024; Hq % Hkv == 0; D in {64, 128};
  * page a power of two in [16, 1024]; n_pages, max_pages >= 1;
  * max_pages * page <= 2^30; B * max(Hq, Hkv) <= 2^24.  attn_decode_paged:
  * T <= 128, R = T Hq / Hkv <= 65536, and B Hkv ceil(R / 48) (max_pages page / 32)

@@ -104,10 +104,11 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
     const int64_t g0 = (r0 + VEC - 1) / VEC, g1 = r1 / VEC;
     const int groups = g1 > g0 ? (int)(g1 - g0) : 0;
     const int per = (groups + splits - 1) / splits;
-    const int lo = seg * per, hi = min(groups, lo + per);
+    const int lo = seg * per, hi = min(groups, lo + per), left = hi - lo;
     const uint4* src = reinterpret_cast<const uint4*>(logits) + g0;
     float m = -INFINITY, s = 0.0f;
-    for (int e0 = lo + threadIdx.x; e0 < hi; e0 += U * NT) {
+    for (int at = 0; at < left; at += U * NT) {
+        const int e0 = lo + at + threadIdx.x;
         uint4 u[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
@@ -136,16 +137,21 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
         }
         if (m != nm) s *= ex2((m - nm) * k);
         m = nm;
+        // 2^((x - base) k) as 2^(x k - c), c = fl(base k): the sum of a product
+        // and a constant is rounded once, and what c is off by, base k - c (a
+        // fused multiply-add gives it exactly), is the same factor for all
         const float base = m == -INFINITY ? 0.0f : m;      // a NaN beside -inf stays
+        const float c0 = -base * k;
         float ps[4] = {};
 #pragma unroll
         for (int j = 0; j < U; ++j) {
+            if (at + j * NT >= left) break;                // the same for all threads
             float x[VEC];
             grp<IO>::unpack(u[j], x);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) ps[v % 4] += ex2((x[v] - base) * k);
+            for (int v = 0; v < VEC; ++v) ps[v % 4] += ex2(fmaf(x[v], k, c0));
         }
-        s += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        s += ((ps[0] + ps[1]) + (ps[2] + ps[3])) * ex2(-fmaf(base, k, c0));
     }
     if (seg == 0) {
         // the elements of the row in groups that it shares with its neighbours
@@ -197,7 +203,9 @@ template <int IO>
 __global__ void __launch_bounds__(NT)
 race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     using T = typename io_t<IO>::T;
-    constexpr int VEC = 8;
+    // tokens per group, groups under way at once: 2 and 64 registers, so that
+    // three CTAs share an SM (24 requests 22.1 us; 1: 23.4, 4 on two CTAs: 28)
+    constexpr int VEC = 8, U = 2;
     __shared__ float row_m[SPEC_MAX_ROWS], row_s[SPEC_MAX_ROWS];
     __shared__ float tok_x[SPEC_MAX_ROWS], tok_q[SPEC_MAX_ROWS];
     __shared__ int keep[SPEC_MAX_ROWS], draft[SPEC_MAX_ROWS];
@@ -210,12 +218,20 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     // ---- what does not depend on the masses: this slice's first exponentials,
     // the drafts and what the target and the drafter say of them
     const bool vec = V % VEC == 0;
-    float ev[VEC];
-    const int v0 = lo + tid * VEC;
-    if (vec && v0 < hi) {
-        *reinterpret_cast<float4*>(ev) = __ldg(reinterpret_cast<const float4*>(e + v0));
-        *reinterpret_cast<float4*>(ev + 4) = __ldg(reinterpret_cast<const float4*>(e + v0 + 4));
-    }
+    float ev[U][VEC];
+    auto load_e = [&](int v0) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int v = v0 + j * NT * VEC;
+            if (v < hi) {
+                *reinterpret_cast<float4*>(ev[j]) = __ldg(reinterpret_cast<const float4*>(e + v));
+                *reinterpret_cast<float4*>(ev[j] + 4) =
+                    __ldg(reinterpret_cast<const float4*>(e + v + 4));
+            }
+        }
+    };
+    const int first = lo + tid * VEC;
+    if (vec) load_e(first);
     uint32_t bits = 0;
     const int n = new_rows(a.n_draft, b, N, bits);
     if (tid < n) {
@@ -276,40 +292,43 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
             bar = best.s * (1.0f - 0x1p-20f);
         }
     };
-    auto scan = [&]() {
-        if (vec) {
-            for (int v = v0; v < hi; v += NT * VEC) {
-                float x[VEC], q[VEC];
-                if constexpr (IO == SPEC_IO_BF16) {
-                    grp<IO>::unpack(__ldg(reinterpret_cast<const uint4*>(lp + v)), x);
-                } else {
-                    *reinterpret_cast<float4*>(x) = __ldg(reinterpret_cast<const float4*>(lp + v));
-                    *reinterpret_cast<float4*>(x + 4) =
-                        __ldg(reinterpret_cast<const float4*>(lp + v + 4));
-                }
+    if (s > 0.0f && vec) {
+        for (int v0 = first; v0 < hi; v0 += U * NT * VEC) {
+            if (v0 != first) load_e(v0);
+            uint4 xu[U][IO == SPEC_IO_F32 ? 2 : 1];
+            float q[U][VEC];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int v = v0 + j * NT * VEC;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) q[j][i] = v + i == point ? 1.0f : 0.0f;
+                if (v >= hi) continue;
+                const uint4* src = reinterpret_cast<const uint4*>(lp + v);
+                xu[j][0] = __ldg(src);
+                if constexpr (IO == SPEC_IO_F32) xu[j][1] = __ldg(src + 1);
                 if (qp) {
-                    *reinterpret_cast<float4*>(q) = __ldg(reinterpret_cast<const float4*>(qp + v));
-                    *reinterpret_cast<float4*>(q + 4) =
+                    *reinterpret_cast<float4*>(q[j]) = __ldg(reinterpret_cast<const float4*>(qp + v));
+                    *reinterpret_cast<float4*>(q[j] + 4) =
                         __ldg(reinterpret_cast<const float4*>(qp + v + 4));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) q[j] = v + j == point ? 1.0f : 0.0f;
                 }
-                if (v != v0) {
-                    *reinterpret_cast<float4*>(ev) = __ldg(reinterpret_cast<const float4*>(e + v));
-                    *reinterpret_cast<float4*>(ev + 4) =
-                        __ldg(reinterpret_cast<const float4*>(e + v + 4));
-                }
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) score(x[j], q[j], ev[j], v + j);
             }
-        } else {
-#pragma unroll 4
-            for (int v = lo + tid; v < hi; v += NT)
-                score(io_t<IO>::ld(lp, v), qp ? qp[v] : (v == point ? 1.0f : 0.0f), e[v], v);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int v = v0 + j * NT * VEC;
+                if (v >= hi) break;
+                float x[VEC];
+                grp<IO>::unpack(xu[j][0], reinterpret_cast<float(&)[grp<IO>::VEC]>(x[0]));
+                if constexpr (IO == SPEC_IO_F32)
+                    grp<IO>::unpack(xu[j][1], reinterpret_cast<float(&)[grp<IO>::VEC]>(x[4]));
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) score(x[i], q[j][i], ev[j][i], v + i);
+            }
         }
-    };
-    if (s > 0.0f) scan();
+    } else if (s > 0.0f) {
+#pragma unroll 4
+        for (int v = lo + tid; v < hi; v += NT)
+            score(io_t<IO>::ld(lp, v), qp ? qp[v] : (v == point ? 1.0f : 0.0f), e[v], v);
+    }
     best = block_best(best, sh);
     if (tid == 0) {
         __stcg(a.cand + (size_t)b * a.slices + blockIdx.x,

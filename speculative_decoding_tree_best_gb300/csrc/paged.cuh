@@ -12,7 +12,7 @@ namespace spec {
 inline int check_paged_cfg(const spec_paged_cfg* c) {
     if (!c) return ST_EINVAL;
     if (c->B < 1 || c->B > SPEC_MAX_PAGED_B || c->T < 1 || c->T > (1 << 20)) return ST_EINVAL;
-    if (c->Hq < 1 || c->Hkv < 1 || c->Hq % c->Hkv != 0) return ST_EINVAL;
+    if (c->Hq < 1 || c->Hkv < 1 || c->Hkv > SPEC_MAX_HKV || c->Hq % c->Hkv != 0) return ST_EINVAL;
     if ((int64_t)c->B * c->Hq > (1 << 24)) return ST_EINVAL;
     if (c->D != 64 && c->D != 128) return ST_EINVAL;
     if (c->page < SPEC_MIN_PAGE || c->page > SPEC_MAX_PAGE || (c->page & (c->page - 1)))
@@ -85,10 +85,6 @@ inline PagedWs paged_ws_layout(const spec_paged_cfg& c, int num_sms) {
 // `per` tokens for the race.  About eight CTAs per SM over all rows, and three
 // over the requests' races, but no segment under 4096 and no slice under 2048
 // tokens (a load per thread).
-#ifndef SPEC_DV_A
-#define SPEC_DV_A 8LL
-#define SPEC_DV_B 3LL
-#endif
 struct DraftWs {
     size_t part_off, cand_off, ticket_off, total;
     int splits, slices, per;
@@ -100,8 +96,8 @@ inline DraftWs draft_ws_layout(const spec_draft_cfg& c, int num_sms) {
     auto clamp = [](int64_t want, int64_t most) {
         return (int)(want < 1 ? 1 : (want > most ? most : want));
     };
-    w.splits = clamp((SPEC_DV_A * num_sms + rows - 1) / rows, ((int64_t)c.V + 4095) / 4096);
-    w.slices = clamp((SPEC_DV_B * num_sms + c.B - 1) / c.B, ((int64_t)c.V + 2047) / 2048);
+    w.splits = clamp((8LL * num_sms + rows - 1) / rows, ((int64_t)c.V + 4095) / 4096);
+    w.slices = clamp((3LL * num_sms + c.B - 1) / c.B, ((int64_t)c.V + 2047) / 2048);
     w.per = (int)((((int64_t)c.V + w.slices - 1) / w.slices + 7) / 8 * 8);
     w.slices = (int)(((int64_t)c.V + w.per - 1) / w.per);
     w.part_off = 256;

@@ -1,8 +1,8 @@
 // paged_cache.cu -- the paged key/value cache written and read back.
 //
-// A row (one token's key or value of one head, D values) is handled by the
-// lanes of one half- or quarter-warp group, 16 bytes of the I/O type per lane,
-// so that its maximum is a few shuffles and its codes leave in one piece.
+// A row (one token's key or value of one head, D values) belongs to 8, 16 or
+// 32 lanes, 16 bytes of the I/O type each, so that its maximum is a few shuffles
+// and its codes leave in one piece.
 //
 // Written with 8 bits: scale = max(amax / 448, 2^-100), code = e4m3(x / scale).
 // 448 is e4m3's largest value, so the row's largest value keeps all three
@@ -47,142 +47,228 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The rows of one request, (token, head) in memory order, are cut into blocks of
+// RPC rows, one to a CTA; a thread has UNR rows of its block, all under way
+// at once.
+constexpr int UNR = 4;
+
+template <int IO, int D> struct rows_of {
+    static constexpr int PER = NT / geo<IO, D>::LPR;     // rows per pass of the block
+    static constexpr int RPC = UNR * PER;
+};
+
+struct RowArgs {
+    PageMap pm;
+    int T;                   // tokens per request in the flat tensors
+    int blocks;              // CTAs per request
+    uint32_t h_mul;          // ceil(2^32 / Hkv), 0 for Hkv = 1
+    // x / Hkv for x < Hkv + 2^12
+    __device__ __forceinline__ int token(int x) const { return h_mul ? __umulhi(x, h_mul) : x; }
+};
+
 template <int IO, int KV, int D>
 __global__ void __launch_bounds__(NT)
-append_rows(PageMap pm, int B, int T, const uint4* __restrict__ k_new,
+append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
             const uint4* __restrict__ v_new, const int32_t* __restrict__ n_new, void* k_pages,
             void* v_pages, float* k_scale, float* v_scale, void* ws) {
     using G = geo<IO, D>;
-    const int64_t rows = (int64_t)B * T * pm.Hkv;
-    const int64_t r = ((int64_t)blockIdx.x * NT + threadIdx.x) / G::LPR;
-    const int lane = threadIdx.x % G::LPR;
+    using R = rows_of<IO, D>;
+    const PageMap& pm = a.pm;
+    const int b = blockIdx.x / a.blocks, row0 = (blockIdx.x - b * a.blocks) * R::RPC;
+    const int lane = threadIdx.x % G::LPR, mine = threadIdx.x / G::LPR;
     const bool is_v = blockIdx.y != 0;
-    if (r >= rows) return;                         // whole row groups leave together
-    const int h = (int)(r % pm.Hkv);
-    const int64_t bi = r / pm.Hkv;
-    const int b = (int)(bi / T), i = (int)(bi % T);
+    const int tok0 = row0 / pm.Hkv, h0 = row0 - tok0 * pm.Hkv;
     uint32_t bits = 0;
-    const int n = new_rows(n_new, b, T, bits);
+    const int n = new_rows(n_new, b, a.T, bits);
     const int L = pm.kv_len[b];
     if (L < 0 || L > pm.cap() - n) bits |= SPEC_DEV_OVERFLOW;
-    if (bits && lane == 0 && i == 0 && h == 0) raise_status(ws, bits);
-    if ((bits & SPEC_DEV_OVERFLOW) || i >= n) return;
-    const int64_t dst = pm.row(b, L + i, h);
-    if (dst < 0) {
-        if (lane == 0) raise_status(ws, SPEC_DEV_BADPAGE);
-        return;
+    if (bits && row0 == 0 && threadIdx.x == 0) raise_status(ws, bits);
+    if ((bits & SPEC_DEV_OVERFLOW) || tok0 >= n) return;
+    const uint4* src = (is_v ? v_new : k_new) + ((size_t)b * a.T * pm.Hkv + row0) * G::LPR;
+    uint4 u[UNR];
+    int64_t dst[UNR];
+#pragma unroll
+    for (int j = 0; j < UNR; ++j) {
+        const int r = j * R::PER + mine, dt = a.token(h0 + r);
+        const int i = tok0 + dt, h = h0 + r - dt * pm.Hkv;
+        dst[j] = -1;
+        u[j] = make_uint4(0, 0, 0, 0);
+        if (i < n) {
+            u[j] = __ldg(src + r * G::LPR + lane);
+            dst[j] = pm.row(b, L + i, h);
+            if (dst[j] < 0 && lane == 0) raise_status(ws, SPEC_DEV_BADPAGE);
+        }
     }
-    const uint4 u = (is_v ? v_new : k_new)[r * G::LPR + lane];
     void* pages = is_v ? v_pages : k_pages;
-    if constexpr (KV == SPEC_KV_IO) {
-        reinterpret_cast<uint4*>(pages)[dst * G::LPR + lane] = u;
-    } else {
-        float x[G::VEC], amax = 0.0f, bad = 0.0f;
-        unpack<IO>(u, x);
 #pragma unroll
-        for (int j = 0; j < G::VEC; ++j) {
-            amax = fmaxf(amax, fabsf(x[j]));
-            bad += x[j] - x[j];                    // NaN for a non-finite value, else 0
-        }
-        const unsigned grp = G::LPR == 32 ? 0xffffffffu
-                                          : ((1u << (G::LPR & 31)) - 1u)
-                                                << ((threadIdx.x & 31) & ~(G::LPR - 1));
+    for (int j = 0; j < UNR; ++j) {
+        if constexpr (KV == SPEC_KV_IO) {
+            if (dst[j] >= 0) reinterpret_cast<uint4*>(pages)[dst[j] * G::LPR + lane] = u[j];
+        } else {
+            // the row's largest magnitude as an integer: bit patterns of
+            // magnitudes order like the numbers, infinities and NaN on top
+            uint32_t top;
+            const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+            if constexpr (IO == SPEC_IO_F32) {
+                top = max(max(w[0] & 0x7fffffffu, w[1] & 0x7fffffffu),
+                          max(w[2] & 0x7fffffffu, w[3] & 0x7fffffffu));
+            } else {
+                const uint32_t y = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                            __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                top = max(y << 16, y & 0xffff0000u);
+            }
 #pragma unroll
-        for (int o = G::LPR / 2; o > 0; o >>= 1) {
-            amax = fmaxf(amax, __shfl_xor_sync(grp, amax, o));
-            bad += __shfl_xor_sync(grp, bad, o);
-        }
-        float scale = amax == 0.0f ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-100f);
-        if (bad != 0.0f) scale = __int_as_float(0x7fffffff);   // bad is 0 or NaN
-        uint32_t w[G::VEC / 4];
+            for (int o = G::LPR / 2; o > 0; o >>= 1)
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float amax = __uint_as_float(top);
+            float scale = top == 0u ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-100f);
+            if (top >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
+            // x / scale: quotient by the rounded reciprocal, then one Newton step
+            // on its remainder (Markstein 1990), which rounds it correctly; where
+            // the remainder underflows the code is 0 whatever it is
+            const float inv = __frcp_rn(scale);
+            float x[G::VEC];
+            unpack<IO>(u[j], x);
 #pragma unroll
-        for (int j = 0; j < G::VEC / 4; ++j) {
-            const float2 a = make_float2(__fdiv_rn(x[4 * j], scale), __fdiv_rn(x[4 * j + 1], scale));
-            const float2 c = make_float2(__fdiv_rn(x[4 * j + 2], scale),
-                                         __fdiv_rn(x[4 * j + 3], scale));
-            w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
-                   ((uint32_t)__nv_cvt_float2_to_fp8x2(c, __NV_SATFINITE, __NV_E4M3) << 16);
+            for (int k = 0; k < G::VEC; ++k) {
+                const float q = x[k] * inv;
+                x[k] = fmaf(fmaf(-q, scale, x[k]), inv, q);
+            }
+            uint32_t c[G::VEC / 4];
+#pragma unroll
+            for (int k = 0; k < G::VEC / 4; ++k)
+                c[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[4 * k], x[4 * k + 1]),
+                                                          __NV_SATFINITE, __NV_E4M3) |
+                       ((uint32_t)__nv_cvt_float2_to_fp8x2(
+                            make_float2(x[4 * k + 2], x[4 * k + 3]), __NV_SATFINITE, __NV_E4M3)
+                        << 16);
+            if (dst[j] >= 0) {
+                if constexpr (G::VEC == 8)
+                    reinterpret_cast<uint2*>(pages)[dst[j] * G::LPR + lane] = make_uint2(c[0], c[1]);
+                else
+                    reinterpret_cast<uint32_t*>(pages)[dst[j] * G::LPR + lane] = c[0];
+                if (lane == 0) (is_v ? v_scale : k_scale)[dst[j]] = scale;
+            }
         }
-        if constexpr (G::VEC == 8)
-            reinterpret_cast<uint2*>(pages)[dst * G::LPR + lane] = make_uint2(w[0], w[1]);
-        else
-            reinterpret_cast<uint32_t*>(pages)[dst * G::LPR + lane] = w[0];
-        if (lane == 0) (is_v ? v_scale : k_scale)[dst] = scale;
     }
 }
 
 template <int IO, int KV, int D>
 __global__ void __launch_bounds__(NT)
-read_rows(PageMap pm, int B, int Lmax, const void* __restrict__ k_pages,
+read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
           const void* __restrict__ v_pages, const float* __restrict__ k_scale,
           const float* __restrict__ v_scale, uint4* __restrict__ k_out, uint4* __restrict__ v_out,
           void* ws) {
     using G = geo<IO, D>;
-    const int64_t rows = (int64_t)B * Lmax * pm.Hkv;
-    const int64_t r = ((int64_t)blockIdx.x * NT + threadIdx.x) / G::LPR;
-    const int lane = threadIdx.x % G::LPR;
+    using R = rows_of<IO, D>;
+    const PageMap& pm = a.pm;
+    const int b = blockIdx.x / a.blocks, row0 = (blockIdx.x - b * a.blocks) * R::RPC;
+    const int lane = threadIdx.x % G::LPR, mine = threadIdx.x / G::LPR;
     const bool is_v = blockIdx.y != 0;
-    if (r >= rows) return;
-    const int h = (int)(r % pm.Hkv);
-    const int64_t bi = r / pm.Hkv;
-    const int b = (int)(bi / Lmax), i = (int)(bi % Lmax);
+    const int tok0 = row0 / pm.Hkv, h0 = row0 - tok0 * pm.Hkv;
     int L = pm.kv_len[b];
-    const int most = min(Lmax, pm.cap());
+    const int most = min(a.T, pm.cap());
     if (L < 0 || L > most) {
-        if (lane == 0 && i == 0 && h == 0) raise_status(ws, SPEC_DEV_OVERFLOW);
+        if (row0 == 0 && threadIdx.x == 0) raise_status(ws, SPEC_DEV_OVERFLOW);
         L = L < 0 ? 0 : most;
     }
-    if (i >= L) return;
-    const int64_t src = pm.row(b, i, h);
-    if (src < 0) {
-        if (lane == 0) raise_status(ws, SPEC_DEV_BADPAGE);
-        return;
-    }
+    if (tok0 >= L) return;
     const void* pages = is_v ? v_pages : k_pages;
-    uint4 u;
-    if constexpr (KV == SPEC_KV_IO) {
-        u = reinterpret_cast<const uint4*>(pages)[src * G::LPR + lane];
-    } else {
-        const float scale = (is_v ? v_scale : k_scale)[src];
-        const uint8_t* cp = reinterpret_cast<const uint8_t*>(pages) + src * D + lane * G::VEC;
-        uint32_t w[G::VEC / 4];
+    constexpr int NW = KV == SPEC_KV_E4M3 ? G::VEC / 4 : 4;   // 32-bit words of a lane's piece
+    uint32_t w[UNR][NW];
+    float scale[UNR];
+    bool have[UNR];
 #pragma unroll
-        for (int j = 0; j < G::VEC / 4; ++j) w[j] = reinterpret_cast<const uint32_t*>(cp)[j];
-        float x[G::VEC];
-#pragma unroll
-        for (int j = 0; j < G::VEC; ++j)
-            x[j] = e4m3_to_float((uint8_t)(w[j / 4] >> (8 * (j % 4)))) * scale;
-        if constexpr (IO == SPEC_IO_F32)
-            u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                           __float_as_uint(x[3]));
-        else
-            u = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                           pack_bf16(x[6], x[7]));
+    for (int j = 0; j < UNR; ++j) {
+        const int r = j * R::PER + mine, dt = a.token(h0 + r);
+        const int i = tok0 + dt, h = h0 + r - dt * pm.Hkv;
+        have[j] = i < L;
+        if (!have[j]) continue;
+        const int64_t src = pm.row(b, i, h);
+        have[j] = src >= 0;
+        if (src < 0) {
+            if (lane == 0) raise_status(ws, SPEC_DEV_BADPAGE);
+            continue;
+        }
+        if constexpr (KV == SPEC_KV_E4M3) {
+            scale[j] = __ldg((is_v ? v_scale : k_scale) + src);
+            if constexpr (NW == 2) {
+                const uint2 y = __ldg(reinterpret_cast<const uint2*>(pages) + src * G::LPR + lane);
+                w[j][0] = y.x;
+                w[j][1] = y.y;
+            } else {
+                w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(pages) + src * G::LPR + lane);
+            }
+        } else {
+            const uint4 y = __ldg(reinterpret_cast<const uint4*>(pages) + src * G::LPR + lane);
+            w[j][0] = y.x;
+            w[j][1] = y.y;
+            w[j][NW - 2] = y.z;
+            w[j][NW - 1] = y.w;
+        }
     }
-    (is_v ? v_out : k_out)[r * G::LPR + lane] = u;
+    uint4* dst = (is_v ? v_out : k_out) + ((size_t)b * a.T * pm.Hkv + row0) * G::LPR + lane;
+#pragma unroll
+    for (int j = 0; j < UNR; ++j) {
+        if (!have[j]) continue;
+        uint4 u;
+        if constexpr (KV == SPEC_KV_IO) {
+            u = make_uint4(w[j][0], w[j][1], w[j][NW - 2], w[j][NW - 1]);
+        } else {
+            float x[G::VEC];
+#pragma unroll
+            for (int k = 0; k < G::VEC / 2; ++k) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)(w[j][k / 2] >> (16 * (k % 2))), __NV_E4M3);
+                const float2 f = __half22float2(__half2(h));
+                x[2 * k] = f.x * scale[j];
+                x[2 * k + 1] = f.y * scale[j];
+            }
+            if constexpr (IO == SPEC_IO_F32)
+                u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                               __float_as_uint(x[3]));
+            else
+                u = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                               pack_bf16(x[G::VEC - 4], x[G::VEC - 3]),
+                               pack_bf16(x[G::VEC - 2], x[G::VEC - 1]));
+        }
+        dst[(j * R::PER + mine) * G::LPR] = u;
+    }
+}
+
+// cudaErrorInvalidConfiguration when the launch would need too many CTAs.
+template <int IO, int D>
+cudaError_t row_args(const spec_paged_cfg& c, const spec_paged_kv& kv, int64_t T, RowArgs& a) {
+    const int64_t rows = T * c.Hkv;
+    const int64_t blocks = (rows + rows_of<IO, D>::RPC - 1) / rows_of<IO, D>::RPC;
+    if (rows > 0x7fffffff - 4096 || blocks * c.B > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    a.pm = page_map(c, kv);
+    a.T = (int)T;
+    a.blocks = (int)blocks;
+    a.h_mul = c.Hkv == 1 ? 0u : (uint32_t)(((1ull << 32) + c.Hkv - 1) / c.Hkv);
+    return cudaSuccess;
 }
 
 template <int IO, int KV, int D>
 cudaError_t append_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* k_new,
                      const void* v_new, const int32_t* n_new, void* ws, cudaStream_t st) {
-    const int64_t lanes = (int64_t)c.B * c.T * c.Hkv * geo<IO, D>::LPR;
-    const int64_t ctas = (lanes + NT - 1) / NT;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_k(false, append_rows<IO, KV, D>, dim3((unsigned)ctas, 2), dim3(NT), 0, st,
-                    page_map(c, kv), c.B, c.T, static_cast<const uint4*>(k_new),
-                    static_cast<const uint4*>(v_new), n_new, kv.k_pages, kv.v_pages, kv.k_scale,
-                    kv.v_scale, ws);
+    RowArgs a;
+    const cudaError_t e = row_args<IO, D>(c, kv, c.T, a);
+    if (e != cudaSuccess) return e;
+    return launch_k(false, append_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT), 0,
+                    st, a, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), n_new,
+                    kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, ws);
 }
 
 template <int IO, int KV, int D>
 cudaError_t read_t(const spec_paged_cfg& c, const spec_paged_kv& kv, int Lmax, void* k_out,
                    void* v_out, void* ws, cudaStream_t st) {
-    const int64_t lanes = (int64_t)c.B * Lmax * c.Hkv * geo<IO, D>::LPR;
-    const int64_t ctas = (lanes + NT - 1) / NT;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_k(false, read_rows<IO, KV, D>, dim3((unsigned)ctas, 2), dim3(NT), 0, st,
-                    page_map(c, kv), c.B, Lmax, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale,
-                    static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), ws);
+    RowArgs a;
+    const cudaError_t e = row_args<IO, D>(c, kv, Lmax, a);
+    if (e != cudaSuccess) return e;
+    return launch_k(false, read_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT), 0, st,
+                    a, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, static_cast<uint4*>(k_out),
+                    static_cast<uint4*>(v_out), ws);
 }
 
 }  // namespace
