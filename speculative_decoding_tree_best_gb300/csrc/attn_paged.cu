@@ -47,6 +47,10 @@ using tc::smem_u32;
 
 constexpr int SUB = 16;                // keys per product tile: the smallest page
 constexpr int GK = 32;                 // keys per granule
+#ifndef SPEC_AP_AL
+#define SPEC_AP_AL 4
+#endif
+constexpr int MAX_RTC = 3;             // row tiles per CTA, at most (paged_row_tiles)
 constexpr int MAX_SLOTS = 64;          // granules in a CTA's ring, at most
 
 // ---- instruction wrappers -------------------------------------------------------------
@@ -245,11 +249,13 @@ struct Deal {
 // A segment that this CTA shares with others: what joining its parts needs.
 struct Pend {
     int b, seg, n;           // request, segment in it, new rows
-    int c0, c1, shift;       // its CTAs (c1 < 0: none); 1: the part of c0 is that CTA's second
+    int c0, c1, shift;       // its CTAs; 1: the part of c0 is that CTA's second
     int last;                // this CTA's part was the last one to be written
 };
 
-template <int IO, int KV, int D, int NR, int W>
+// NR column tiles of 8 rows per warp, W key warps times row tiles, NS halves of a
+// granule at a time, QS: Q in shared memory instead of registers
+template <int IO, int KV, int D, int NR, int W, int NS, bool QS>
 __global__ void __launch_bounds__(32 * (W + 1), 1)
 attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
            const __grid_constant__ AttnParams p) {
@@ -273,7 +279,6 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     // ---- this CTA's share of the granules
     if (tid == 0) {
         abort_flag = 0;
-        pend[0].c1 = pend[1].c1 = -1;
         pend[0].last = pend[1].last = 0;
     }
     if (warp == W && lane < 2) tc::tma_prefetch_desc(lane ? &mv : &mk);
@@ -310,7 +315,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const int longest = __reduce_max_sync(0xffffffffu, rq.ng);
         const bool whole = nseg <= (int)gridDim.x && longest <= 2 * (W / p.rtc);
         n_cta = whole ? nseg : min((int)gridDim.x, (units + (1 << p.min_sh) - 1) >> p.min_sh);
-        const bool aligned = !whole && 4 * nseg <= n_cta && units < (1 << 22);
+        const bool aligned = !whole && SPEC_AP_AL * nseg <= n_cta && units < (1 << 22);
         // CTAs per segment of the lane's request, or granules of the request
         int k = whole ? 1 : rq.ng;
         if (aligned) k = 1 + (n_cta - nseg) * rq.ng / units;
@@ -525,9 +530,13 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     int slot0 = 0, use0 = 0;             // of the segment portion's first granule
 
     float o[NR][A::NT][4];
-    float m[NR][2], l[NR][2], rowf[NR][2];
-    int lim[NR][2];
-    uint32_t qf[NR][A::QT][A::KCH][A::QR];
+    float m[NR][2], l[NR][2], rowf[NR][2] = {};  // rowf: not used with QS
+    // Q^T, the first product's B operand: in registers, or with four column
+    // tiles in shared memory, [rt][nr][chunk][pair][lane]
+    static_assert(!QS || A::QT == 1, "Q in shared memory is in one part");
+    uint32_t qf[NR][A::QT][A::KCH][A::QR] = {};  // not used with QS
+    uint2* qs = reinterpret_cast<uint2*>(buf + W * (A::NT + 1) * 32);
+    float* qsf = reinterpret_cast<float*>(qs + (QS ? p.rtc * NR * A::KCH * (A::QR / 2) * 32 : 0));
 
     auto clear = [&]() {
 #pragma unroll
@@ -541,32 +550,33 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
     auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
-    constexpr int JW = NR * (A::NT + 1) * 32;            // float4 of a warp
+    constexpr int JW = (A::NT + 1) * 32;                 // float4 of a warp's column tile
     constexpr int PO = NR * A::NT * 32, PM = NR * 32;    // float4 of a part's row tile
-    constexpr int TPR = NR * A::NT;                      // tiles of a row tile
-    // The end of a segment portion (or of the joining of parts): the key warps'
-    // results meet in shared memory, (max, max, sum, sum) and the tiles of O^T in
-    // register order; the tiles are shared out to the warps by twos, joined over
-    // the key warps, and go to the output (whole) or to part `at` of the workspace.
+    // The end of a segment portion (or of the joining of parts), column tile by
+    // column tile: the key warps' results meet in shared memory, (max, max, sum,
+    // sum) and the tiles of O^T in register order; the tiles are shared out to the
+    // warps by twos, joined over the key warps, and go to the output (whole) or
+    // to part `at` of the workspace.
     auto finish = [&](int b, int seg, int n, bool whole, size_t at) {
+#pragma unroll 1
+      for (int nr = 0; nr < NR; ++nr) {
         bar();                                           // everyone is done with buf
         if (kw < KW) {
             float4* d = buf + warp * JW + lane;
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-                d[nr * (A::NT + 1) * 32] = make_float4(m[nr][0], m[nr][1], l[nr][0], l[nr][1]);
+            for (int c = 0; c < NR; ++c) {
+                if (c != nr) continue;
+                d[0] = make_float4(m[c][0], m[c][1], l[c][0], l[c][1]);
 #pragma unroll
                 for (int i = 0; i < A::NT; ++i)
-                    d[(nr * (A::NT + 1) + 1 + i) * 32] =
-                        make_float4(o[nr][i][0], o[nr][i][1], o[nr][i][2], o[nr][i][3]);
+                    d[(1 + i) * 32] = make_float4(o[c][i][0], o[c][i][1], o[c][i][2], o[c][i][3]);
             }
         }
         bar();
 #pragma unroll 1
-        for (int task = warp; task < p.rtc * TPR / 2; task += W) {
-            const int rt2 = task / (TPR / 2), q = task % (TPR / 2);
-            const int nr = q / (A::NT / 2), i = q % (A::NT / 2) * 2;
-            const float4* s = buf + rt2 * JW + nr * (A::NT + 1) * 32 + lane;
+        for (int task = warp; task < p.rtc * (A::NT / 2); task += W) {
+            const int rt2 = task / (A::NT / 2), i = task % (A::NT / 2) * 2;
+            const float4* s = buf + rt2 * JW + lane;
             const int step = p.rtc * JW;
             float4 x[W];
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
@@ -641,26 +651,48 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
             if (bad) raise_status(p.ws, SPEC_DEV_RANGE);
         }
+      }
+    };
+
+    // Keys that rows 2t, 2t + 1 of column tile nr see: [0, limit); rows that are
+    // not the step's: all, and what comes of them is dropped.
+    auto limit = [&](int nr, int e) {
+        const int i = p.tok((p.rg(wk.seg) * p.rtc + rt) * rows_tile + nr * 8 + 2 * t + e);
+        return i < wk.rq.n ? min(wk.rq.L + i + 1, cap) : 0x7fffffff;
+    };
+    auto row_factor = [&](int nr, int e) {
+        if constexpr (QS)
+            return qsf[(rt * NR + nr) * 8 + 2 * t + e];
+        else
+            return rowf[nr][e];
     };
 
     // one granule: keys [kb, kb + GK) in ring slot `slot`; have: its halves in the pool
     auto granule = [&](int kb, int slot, uint32_t have, int lim_min, int lim_max) {
         const uint32_t ks = smem_u32(ring + (size_t)slot * A::SLOT);
         const uint32_t vs = ks + A::SLOT_KV;
-        constexpr int NS = GK / SUB;
+#pragma unroll 1
+      for (int h0 = 0; h0 < GK / SUB; h0 += NS) {
+        if (NS < GK / SUB && (!((have >> h0) & 1u) || kb + h0 * SUB >= lim_max)) continue;
         float x[NR][NS][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int h = 0; h < NS; ++h) x[nr][h][0] = x[nr][h][1] = x[nr][h][2] = x[nr][h][3] = 0.0f;
         // consecutive products go to different accumulators: the halves in turn
+        auto q_of = [&](int nr, int q, int j, int i) {
+            if constexpr (QS)
+                return qs[(((rt * NR + nr) * A::KCH + j) * (A::QR / 2) + i) * 32 + lane];
+            else
+                return make_uint2(qf[nr][q][j][2 * i], qf[nr][q][j][2 * i + 1]);
+        };
 #pragma unroll
         for (int j = 0; j < A::KCH; ++j) {
             uint32_t w0[NS][4], w1[NS][4];
 #pragma unroll
             for (int h = 0; h < NS; ++h) {
-                const uint4 k0 = lds128(ks + chunk_off<A>(h * SUB + kr, t + 4 * j));
-                const uint4 k1 = lds128(ks + chunk_off<A>(h * SUB + kr + 8, t + 4 * j));
+                const uint4 k0 = lds128(ks + chunk_off<A>((h0 + h) * SUB + kr, t + 4 * j));
+                const uint4 k1 = lds128(ks + chunk_off<A>((h0 + h) * SUB + kr + 8, t + 4 * j));
                 w0[h][0] = k0.x, w0[h][1] = k0.y, w0[h][2] = k0.z, w0[h][3] = k0.w;
                 w1[h][0] = k1.x, w1[h][1] = k1.y, w1[h][2] = k1.z, w1[h][3] = k1.w;
             }
@@ -676,11 +708,11 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                     for (int q = 0; q < A::QT; ++q)
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
+                        for (int nr = 0; nr < NR; ++nr) {
+                            const uint2 b = q_of(nr, q, j, i);
 #pragma unroll
-                            for (int h = 0; h < NS; ++h)
-                                mma_f16_16816(x[nr][h], a[h], qf[nr][q][j][2 * i],
-                                              qf[nr][q][j][2 * i + 1]);
+                            for (int h = 0; h < NS; ++h) mma_f16_16816(x[nr][h], a[h], b.x, b.y);
+                        }
                 }
             } else if constexpr (A::F32) {
                 uint32_t a[NS][3][4];
@@ -699,29 +731,33 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                            for (int h = 0; h < NS; ++h)
-                                mma_bf16_16816(x[nr][h], a[h][i], qf[nr][q][j][0], qf[nr][q][j][1]);
+                            for (int h = 0; h < NS; ++h) {
+                                const uint2 b = q_of(nr, q, j, 0);
+                                mma_bf16_16816(x[nr][h], a[h][i], b.x, b.y);
+                            }
             } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
+                    for (int nr = 0; nr < NR; ++nr) {
+                        const uint2 b = q_of(nr, 0, j, i);
 #pragma unroll
                         for (int h = 0; h < NS; ++h) {
                             const uint32_t a[4] = {w0[h][2 * i], w1[h][2 * i], w0[h][2 * i + 1],
                                                    w1[h][2 * i + 1]};
-                            mma_bf16_16816(x[nr][h], a, qf[nr][0][j][2 * i], qf[nr][0][j][2 * i + 1]);
+                            mma_bf16_16816(x[nr][h], a, b.x, b.y);
                         }
+                    }
             }
         }
         // scores in log2 units, -inf where the row does not see the key
-        const bool masked = kb + GK > lim_min || have != 3u;
+        const bool masked = kb + (h0 + NS) * SUB > lim_min || (NS == GK / SUB && have != 3u);
         float lv[NS][2];
 #pragma unroll
         for (int h = 0; h < NS; ++h) {
             float kf[2] = {1.0f, 1.0f};
             if constexpr (A::Q8) {
-                const float* sc = scales + slot * 2 * GK + h * SUB + kr;
+                const float* sc = scales + slot * 2 * GK + (h0 + h) * SUB + kr;
                 kf[0] = sc[0];
                 kf[1] = sc[8];
                 lv[h][0] = log2_scale(sc[GK]);
@@ -731,7 +767,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    x[nr][h][e] *= A::Q8 ? rowf[nr][e & 1] * kf[e >> 1] : rowf[nr][e & 1];
+                    x[nr][h][e] *= A::Q8 ? row_factor(nr, e & 1) * kf[e >> 1] : p.qk_scale;
         }
         if (masked) {
 #pragma unroll
@@ -740,7 +776,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (kb + h * SUB + kr + 8 * (e >> 1) >= lim[nr][e & 1] || !((have >> h) & 1u))
+                        if (kb + (h0 + h) * SUB + kr + 8 * (e >> 1) >= limit(nr, e & 1) ||
+                            !((have >> (h0 + h)) & 1u))
                             x[nr][h][e] = -INFINITY;
         }
         // the running maximum of what the V weights go by (fmaxf passes over a NaN)
@@ -779,52 +816,24 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 }
             }
         }
-        // weights, their sum, and the second product's B operand
-        uint32_t wb[NR][NS][A::PT][2];
+        // the weights, in place of the scores, and their sum
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             const float b0 = m[nr][0] == -INFINITY ? 0.0f : m[nr][0];
             const float b1 = m[nr][1] == -INFINITY ? 0.0f : m[nr][1];
 #pragma unroll
-            for (int h = 0; h < NS; ++h) {
-                float w[4];
+            for (int h = 0; h < NS; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float d = x[nr][h][e] - ((e & 1) ? b1 : b0);
                     const float pl = ex2(d);
                     l[nr][e & 1] += pl;
-                    w[e] = A::Q8 ? ex2(d + lv[h][e >> 1]) : pl;
                     // the scale of a key that is not seen may be anything
-                    if (A::Q8 && masked && x[nr][h][e] == -INFINITY) w[e] = 0.0f;
+                    if (A::Q8 && masked && x[nr][h][e] == -INFINITY)
+                        x[nr][h][e] = 0.0f;
+                    else
+                        x[nr][h][e] = A::Q8 ? ex2(d + lv[h][e >> 1]) : pl;
                 }
-                if constexpr (A::F32) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t c[3];
-                        split3x2(w[2 * k], w[2 * k + 1], c[0], c[1], c[2]);
-#pragma unroll
-                        for (int q = 0; q < 3; ++q) wb[nr][h][q][k] = movm(c[q]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if constexpr (A::Q8) {
-                            const uint32_t c = packh(w[2 * k], w[2 * k + 1]);
-                            wb[nr][h][0][k] = movm(c);
-                            if constexpr (A::PT == 2) {
-                                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&c));
-                                wb[nr][h][A::PT - 1][k] =
-                                    movm(packh(w[2 * k] - b.x, w[2 * k + 1] - b.y));
-                            }
-                        } else {
-                            const uint32_t c = packb(w[2 * k], w[2 * k + 1]);
-                            wb[nr][h][0][k] = movm(c);
-                            wb[nr][h][A::PT - 1][k] =
-                                movm(packb(w[2 * k] - lo_b(c), w[2 * k + 1] - hi_b(c)));
-                        }
-                    }
-                }
-            }
         }
         // Keys that no row sees must not reach O (their weights are 0, but
         // 0 x inf is not): their V counts as zeros.  Of the keys that some rows
@@ -834,10 +843,10 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         if (masked && lim_min < lim_max) {
             bool bad = false;
 #pragma unroll 1
-            for (int c = lane; c < GK * (A::ROWB / 16); c += 32) {
-                const int r = c % GK;
+            for (int c = lane; c < NS * SUB * (A::ROWB / 16); c += 32) {
+                const int r = h0 * SUB + c % (NS * SUB);
                 if (kb + r < lim_min || kb + r >= lim_max || !((have >> (r / SUB)) & 1u)) continue;
-                const uint4 v = lds128(vs + chunk_off<A>(r, c / GK));
+                const uint4 v = lds128(vs + chunk_off<A>(r, c / (NS * SUB)));
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -856,7 +865,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         int cut = slow ? lim_min : lim_max;
 #pragma unroll 1
         for (;;) {
-            float keep[NR][A::NT][4];
+            // volatile: in local memory, not in registers that the usual way needs
+            volatile float keep[NR][A::NT][4];
             if (slow) {
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
@@ -865,22 +875,46 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                         for (int e = 0; e < 4; ++e) keep[nr][i][e] = o[nr][i][e];
             }
-            // O^T += V^T W^T
-            auto mma_o = [&](int nr, int i, const uint32_t (&a)[4], int h, int part) {
-                if constexpr (A::Q8)
-                    mma_f16_16816(o[nr][i], a, wb[nr][h][part][0], wb[nr][h][part][1]);
-                else
-                    mma_bf16_16816(o[nr][i], a, wb[nr][h][part][0], wb[nr][h][part][1]);
-            };
 #pragma unroll
             for (int h = 0; h < NS; ++h) {
+                // the half's weights as the second product's B operand, in parts
+                uint32_t wb[NR][A::PT][2];
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float u = x[nr][h][2 * k], v = x[nr][h][2 * k + 1];
+                        if constexpr (A::F32) {
+                            uint32_t c[3];
+                            split3x2(u, v, c[0], c[1], c[2]);
+#pragma unroll
+                            for (int q = 0; q < 3; ++q) wb[nr][q][k] = movm(c[q]);
+                        } else if constexpr (A::Q8) {
+                            const uint32_t c = packh(u, v);
+                            wb[nr][0][k] = movm(c);
+                            if constexpr (A::PT == 2) {
+                                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&c));
+                                wb[nr][A::PT - 1][k] = movm(packh(u - b.x, v - b.y));
+                            }
+                        } else {
+                            const uint32_t c = packb(u, v);
+                            wb[nr][0][k] = movm(c);
+                            wb[nr][A::PT - 1][k] = movm(packb(u - lo_b(c), v - hi_b(c)));
+                        }
+                    }
+                auto mma_o = [&](int nr, int i, const uint32_t (&a)[4], int part) {
+                    if constexpr (A::Q8)
+                        mma_f16_16816(o[nr][i], a, wb[nr][part][0], wb[nr][part][1]);
+                    else
+                        mma_bf16_16816(o[nr][i], a, wb[nr][part][0], wb[nr][part][1]);
+                };
 #pragma unroll
                 for (int j = 0; j < A::VL; ++j) {
                     uint32_t v[4][4];
                     const int row[4] = {va, vb, va + 8, vb + 8};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int r = h * SUB + row[k];
+                        const int r = (h0 + h) * SUB + row[k];
                         if constexpr (A::ROWB == 64) {        // 8 bytes per lane and row
                             const uint2 u = lds64(vs + chunk_off<A>(r, g >> 1) + (g & 1) * 8);
                             v[k][0] = u.x;
@@ -897,7 +931,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     if (masked) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (kb + h * SUB + row[k] >= cut || !((have >> h) & 1u))
+                            if (kb + (h0 + h) * SUB + row[k] >= cut || !((have >> (h0 + h)) & 1u))
                                 v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0;
                     }
                     // consecutive products go to different tiles
@@ -917,7 +951,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                    for (int r = 0; r < 2; ++r) mma_o(nr, j * 2 + r, a[r][i], h, q);
+                                    for (int r = 0; r < 2; ++r) mma_o(nr, j * 2 + r, a[r][i], q);
                     } else if constexpr (A::Q8) {
                         constexpr int NW = A::ROWB == 64 ? 2 : 4;
 #pragma unroll
@@ -934,7 +968,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                    for (int y = 0; y < 2; ++y) mma_o(nr, 2 * i + y, a[y], h, q);
+                                    for (int y = 0; y < 2; ++y) mma_o(nr, 2 * i + y, a[y], q);
                         }
                     } else {
                         uint32_t a[4][4];
@@ -950,7 +984,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) mma_o(nr, 4 * j + i, a[i], h, q);
+                                for (int i = 0; i < 4; ++i) mma_o(nr, 4 * j + i, a[i], q);
                     }
                 }
             }
@@ -961,114 +995,102 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 for (int i = 0; i < A::NT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (lim[nr][e & 1] != cut) o[nr][i][e] = keep[nr][i][e];
+                        if (limit(nr, e & 1) != cut) o[nr][i][e] = keep[nr][i][e];
             if (++cut > lim_max) break;
         }
+      }
     };
 
-    // A warp's Q rows as they are in memory, 16 bytes at a time (rows the step
-    // does not have: zeros)
+    // A column tile's Q rows (tile: in the CTA's row group) as they are in memory,
+    // 16 bytes at a time (rows the step does not have: zeros)
     constexpr int QB = IO == SPEC_IO_F32 ? 4 : 2;
     constexpr int RAW = D * QB / 64;                     // 16-byte pieces of a row per lane
-    auto load_q = [&](const Walk& w, uint4 (&raw)[NR][RAW]) {
-        const int hk = p.hk(w.seg), row0 = (p.rg(w.seg) * p.rtc + rt) * rows_tile;
+    auto load_q = [&](const Walk& w, int tile, uint4 (&raw)[RAW]) {
+        const int r = (p.rg(w.seg) * p.rtc * NR + tile) * 8 + g, i = p.tok(r);
+        const bool real = i < p.T;
+        const uint4* qp = reinterpret_cast<const uint4*>(
+            static_cast<const uint8_t*>(p.q) +
+            (real ? (((size_t)w.b * p.T + i) * p.Hq + p.hk(w.seg) * p.G + r - i * p.G) * D * QB : 0));
+        constexpr int PC = RAW / A::KCH;                 // pieces per cache chunk
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            const int r = row0 + nr * 8 + g, i = p.tok(r);
-            const bool real = i < p.T;
-            const uint4* qp = reinterpret_cast<const uint4*>(
-                static_cast<const uint8_t*>(p.q) +
-                (real ? (((size_t)w.b * p.T + i) * p.Hq + hk * p.G + r - i * p.G) * D * QB : 0));
-            constexpr int PC = RAW / A::KCH;             // pieces per cache chunk
-#pragma unroll
-            for (int k = 0; k < RAW; ++k)
-                raw[nr][k] = real ? __ldg(qp + (t + 4 * (k / PC)) * PC + k % PC)
-                                  : make_uint4(0, 0, 0, 0);
-        }
+        for (int k = 0; k < RAW; ++k)
+            raw[k] = real ? __ldg(qp + (t + 4 * (k / PC)) * PC + k % PC) : make_uint4(0, 0, 0, 0);
     };
     // and as the first product's operand
-    auto make_q = [&](const uint4 (&raw)[NR][RAW]) {
+    auto make_q = [&](const uint4 (&raw)[RAW], uint32_t (&qr)[A::QT][A::KCH][A::QR], float& row) {
+        row = p.qk_scale;
+        if constexpr (!A::Q8 && !A::F32) {
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            if constexpr (!A::Q8 && !A::F32) {
-#pragma unroll
-                for (int j = 0; j < A::KCH; ++j) {
-                    qf[nr][0][j][0] = raw[nr][j].x;
-                    qf[nr][0][j][1] = raw[nr][j].y;
-                    qf[nr][0][j][2] = raw[nr][j].z;
-                    qf[nr][0][j][3] = raw[nr][j].w;
-                }
-                rowf[nr][0] = rowf[nr][1] = p.qk_scale;
-            } else if constexpr (A::F32) {
-#pragma unroll
-                for (int j = 0; j < A::KCH; ++j) {
-                    const uint32_t w[4] = {raw[nr][j].x, raw[nr][j].y, raw[nr][j].z, raw[nr][j].w};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        split3x2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]),
-                                 qf[nr][0][j][k], qf[nr][1][j][k], qf[nr][2][j][k]);
-                }
-                rowf[nr][0] = rowf[nr][1] = p.qk_scale;
-            } else {
-                // fp16 with the row scaled by a power of two so that its largest
-                // value is in [2^14, 2^15): bf16 values down to 2^-28 of it keep
-                // every bit, fp32 ones go in two parts
-                float y[A::KCH][16], amax = 0.0f;
-#pragma unroll
-                for (int j = 0; j < A::KCH; ++j) {
-                    constexpr int PC = RAW / A::KCH;
-#pragma unroll
-                    for (int c = 0; c < PC; ++c) {
-                        const uint4 u = raw[nr][j * PC + c];
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if constexpr (IO == SPEC_IO_BF16) {
-                                y[j][8 * c + 2 * k] = lo_b(w[k]);
-                                y[j][8 * c + 2 * k + 1] = hi_b(w[k]);
-                            } else {
-                                y[j][4 * c + k] = __uint_as_float(w[k]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(y[j][k]));
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // 2^(14 - exponent), within what fp32 holds (0 and inf: 1)
-                int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-                if (!(amax > 0.0f) || ex == 128) ex = 14;
-                ex = max(ex, -100);
-                const float f = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-                const float fi = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-#pragma unroll
-                for (int j = 0; j < A::KCH; ++j)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float a = y[j][2 * k] * f, c = y[j][2 * k + 1] * f;
-                        const uint32_t h = packh(a, c);
-                        qf[nr][0][j][k] = h;
-                        if constexpr (A::QT == 2) {
-                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                            qf[nr][A::QT - 1][j][k] = packh(a - b.x, c - b.y);
-                        }
-                    }
-                // lane (g, t) made row g; it needs rows 2t and 2t + 1
-                rowf[nr][0] = p.qk_scale * __shfl_sync(0xffffffffu, fi, 8 * t);
-                rowf[nr][1] = p.qk_scale * __shfl_sync(0xffffffffu, fi, 8 * t + 4);
+            for (int j = 0; j < A::KCH; ++j) {
+                qr[0][j][0] = raw[j].x;
+                qr[0][j][1] = raw[j].y;
+                qr[0][j][2] = raw[j].z;
+                qr[0][j][3] = raw[j].w;
             }
+        } else if constexpr (A::F32) {
+#pragma unroll
+            for (int j = 0; j < A::KCH; ++j) {
+                const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    split3x2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]), qr[0][j][k],
+                             qr[1][j][k], qr[2][j][k]);
+            }
+        } else {
+            // fp16 with the row scaled by a power of two so that its largest
+            // value is in [2^14, 2^15): bf16 values down to 2^-28 of it keep
+            // every bit, fp32 ones go in two parts
+            float y[A::KCH][16], amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < A::KCH; ++j) {
+                constexpr int PC = RAW / A::KCH;
+#pragma unroll
+                for (int c = 0; c < PC; ++c) {
+                    const uint4 u = raw[j * PC + c];
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (IO == SPEC_IO_BF16) {
+                            y[j][8 * c + 2 * k] = lo_b(w[k]);
+                            y[j][8 * c + 2 * k + 1] = hi_b(w[k]);
+                        } else {
+                            y[j][4 * c + k] = __uint_as_float(w[k]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(y[j][k]));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^(14 - exponent), within what fp32 holds (0 and inf: 1)
+            int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+            if (!(amax > 0.0f) || ex == 128) ex = 14;
+            ex = max(ex, -100);
+            const float f = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+            row *= __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+#pragma unroll
+            for (int j = 0; j < A::KCH; ++j)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float a = y[j][2 * k] * f, c = y[j][2 * k + 1] * f;
+                    const uint32_t h = packh(a, c);
+                    qr[0][j][k] = h;
+                    if constexpr (A::QT == 2) {
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                        qr[A::QT - 1][j][k] = packh(a - b.x, c - b.y);
+                    }
+                }
         }
     };
 
     int gpos = g0;                       // global index of the present granule
-    uint4 raw[NR][RAW];
+    uint4 raw[RAW];
     // one row tile: the next segment's Q rows are fetched during this one
     constexpr bool AHEAD = NR == 1 && IO == SPEC_IO_BF16;
-    if (AHEAD) load_q(wk, raw);
-    bool counted = false;                // this CTA's parts are in
+    if (AHEAD) load_q(wk, rt, raw);
     for (;;) {
-        int b, seg, n;
+        int b, seg, n, c0 = 0, c1 = 0, which = 0;
         bool whole = true;
         size_t at = 0;
         clear();
@@ -1082,18 +1104,37 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             lim_min = min(wk.rq.L + p.tok(row0) + 1, cap);
             lim_max = min(wk.rq.L + p.tok(last) + 1, cap);
         }
+        if constexpr (QS) {
+            // the warps make a column tile each (they are past the last
+            // segment's products: its joining had barriers)
+            for (int tile = warp; tile < p.rtc * NR; tile += W) {
+                float row;
+                uint32_t qt[A::QT][A::KCH][A::QR];
+                load_q(wk, tile, raw);
+                make_q(raw, qt, row);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+                for (int j = 0; j < A::KCH; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = p.tok(row0 + nr * 8 + 2 * t + e);
-                lim[nr][e] = i < wk.rq.n ? min(wk.rq.L + i + 1, cap) : 0x7fffffff;
+                    for (int i = 0; i < A::QR / 2; ++i)
+                        qs[((tile * A::KCH + j) * (A::QR / 2) + i) * 32 + lane] =
+                            make_uint2(qt[0][j][2 * i], qt[0][j][2 * i + 1]);
+                if (t == 0) qsf[tile * 8 + g] = row;
             }
-        if (!AHEAD) load_q(wk, raw);
-        make_q(raw);
+            bar();
+        } else {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                float row;
+                if (!AHEAD) load_q(wk, rt * NR + nr, raw);
+                make_q(raw, qf[nr], row);
+                // lane (g, t) made row g; it needs rows 2t and 2t + 1
+                rowf[nr][0] = __shfl_sync(0xffffffffu, row, 8 * t);
+                rowf[nr][1] = __shfl_sync(0xffffffffu, row, 8 * t + 4);
+            }
+        }
         Walk nx = wk;
         nx.next(p, hr, cnt);
-        if (AHEAD && nx.left > 0) load_q(nx, raw);
+        if (AHEAD && nx.left > 0) load_q(nx, rt, raw);
         // ---- the granules: every KW-th one
         int slot = slot0 + kw, use = use0;
         for (int gi = kw; gi < cnt && kw < KW; gi += KW, slot += KW) {
@@ -1130,7 +1171,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         n = wk.rq.n;
         whole = cnt == wk.rq.ng;
         if (!whole) {
-            int c0 = own_c0, c1 = own_c1, shift = 0;
+            c0 = own_c0, c1 = own_c1;
+            int shift = 0;
             if (c0 < 0) {
                 const int s0 = gpos - wk.pos;
                 c0 = deal.owner(s0);
@@ -1138,8 +1180,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 shift = s0 > deal.start(c0);
             }
             at = 2 * cta + (cta == c0 ? shift : 0);
+            which = gpos != g0;
             if (tid == 0) {
-                Pend& pe = pend[gpos != g0];
+                Pend& pe = pend[which];
                 pe.b = b;
                 pe.seg = seg;
                 pe.n = n;
@@ -1151,27 +1194,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         gpos += cnt;
         wk = nx;
         } else {
-            // ---- out of granules: count this CTA's parts in (each warp that
-            // wrote some, once for both segments it may share), and join the
-            // segments whose last part was this CTA's
-            const int writers = min(W, p.rtc * TPR / 2);
-            if (!counted) {
-                counted = true;
-                bar();                                   // pend is there
-                if (warp < writers) {
-                    fence_gpu();
-                    __syncwarp();
-                    if (lane < 2 && pend[lane].c1 >= 0) {
-                        Pend& pe = pend[lane];
-                        uint32_t* tk = p.tickets + (size_t)pe.b * hr + pe.seg;
-                        if (atomicAdd(tk, 1u) == (uint32_t)((pe.c1 - pe.c0 + 1) * writers - 1)) {
-                            *tk = 0;                     // for the next call
-                            pe.last = 1;
-                        }
-                    }
-                }
-                bar();
-            }
+            // ---- out of granules: the segments whose last part was this CTA's
+            bar();                                       // pend is there
             const int k = pend[0].last == 1 ? 0 : (pend[1].last == 1 ? 1 : 2);
             if (k == 2) break;
             const Pend pe = pend[k];
@@ -1233,6 +1257,22 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         finish(b, seg, n, whole, at);
+        if (!whole && warp < min(W, p.rtc * (A::NT / 2))) {
+            // each warp that wrote of the part counts itself in; the segment is
+            // joined, when its CTA has no more granules, by who comes last.  (A
+            // CTA's first part is counted in while it works on: the neighbour
+            // then joins that segment, and no CTA is left with two.)
+            fence_gpu();
+            __syncwarp();
+            if (lane == 0) {
+                uint32_t* tk = p.tickets + (size_t)b * hr + seg;
+                const uint32_t all = (uint32_t)(c1 - c0 + 1) * min(W, p.rtc * (A::NT / 2));
+                if (atomicAdd(tk, 1u) == all - 1) {
+                    *tk = 0;                             // for the next call
+                    pend[which].last = 1;
+                }
+            }
+        }
     }
 }
 
@@ -1272,13 +1312,9 @@ template <class A> bool pool_map(CUtensorMap* m, const spec_paged_cfg& c, const 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-#ifndef SPEC_AP_W1
-#define SPEC_AP_W1 7
-#define SPEC_AP_W2 7
-#endif
 constexpr int SMEM_MAX = 225 * 1024;     // of 227 KB, beside the static variables
 
-template <int IO, int KV, int D, int NR, int W>
+template <int IO, int KV, int D, int NR, int W, int NS, bool QS>
 cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
                         const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
     using A = At<IO, KV, D>;
@@ -1311,13 +1347,14 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.q_lines = ((size_t)c.B * c.T * c.Hq * D * (IO == SPEC_IO_F32 ? 4 : 2) + 127) / 128;
     p.box = c.page >= GK ? GK : SUB;
     p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
-    constexpr int fixed = 1024 + W * NR * (A::NT + 1) * 32 * 16;
+    constexpr int fixed = 1024 + W * (A::NT + 1) * 32 * 16 +
+                          (QS ? MAX_RTC * NR * (A::KCH * A::QR * 128 + 32) : 0);
     constexpr int per_slot = A::SLOT + (A::Q8 ? 2 * GK * 4 : 0);
     constexpr int fit = (SMEM_MAX - fixed) / per_slot;
     static_assert(fit >= W && fit >= 4, "the ring's waits need a slot per key warp");
     p.slots = fit < MAX_SLOTS ? fit : MAX_SLOTS;
     const int smem = fixed + p.slots * per_slot;
-    auto kern = attn_paged<IO, KV, D, NR, W>;
+    auto kern = attn_paged<IO, KV, D, NR, W, NS, QS>;
     // once per device and kernel (the size is a constant of the kernel)
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
@@ -1341,9 +1378,30 @@ cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void*
     // one more warp issues the copies: 16 or 8 in all share the registers
     // evenly (128 or 255 each); row tiles in a CTA must divide the warps
     constexpr bool big = At<IO, KV, D>::SLOT > 16384;
-    if (paged_row_tiles(c).nr == 1)
-        return attn_launch<IO, KV, D, 1, big ? 6 : SPEC_AP_W1>(c, kv, q, n_new, o, ws, st);
-    return attn_launch<IO, KV, D, 2, big ? 5 : SPEC_AP_W2>(c, kv, q, n_new, o, ws, st);
+    const int nr = paged_row_tiles(c).nr;
+#ifndef SPEC_AP_1W
+#define SPEC_AP_1W 7
+#define SPEC_AP_1N 2
+#endif
+    if (nr == 1) {
+        if constexpr (IO == SPEC_IO_BF16 && KV == SPEC_KV_E4M3)
+            return attn_launch<IO, KV, D, 1, SPEC_AP_1W, SPEC_AP_1N, false>(c, kv, q, n_new, o, ws, st);
+        else
+            return attn_launch<IO, KV, D, 1, big ? 6 : 7, 2, false>(c, kv, q, n_new, o, ws, st);
+    }
+#ifdef SPEC_AP_4
+    if constexpr (IO == SPEC_IO_BF16)
+        if (nr == 4) return attn_launch<IO, KV, D, 4, 7, 1, true>(c, kv, q, n_new, o, ws, st);
+#endif
+#ifndef SPEC_AP_2W
+#define SPEC_AP_2W 7
+#define SPEC_AP_2N 2
+#define SPEC_AP_2Q false
+#endif
+    if constexpr (IO == SPEC_IO_BF16 && KV == SPEC_KV_E4M3)
+        return attn_launch<IO, KV, D, 2, SPEC_AP_2W, SPEC_AP_2N, SPEC_AP_2Q>(c, kv, q, n_new, o, ws, st);
+    else
+        return attn_launch<IO, KV, D, 2, big ? 6 : 7, 2, false>(c, kv, q, n_new, o, ws, st);
 }
 
 }  // namespace
