@@ -46,10 +46,6 @@ using tc::mbar_wait;
 using tc::smem_u32;
 
 constexpr int SUB = 16;                // keys per product tile: the smallest page
-constexpr int GK = 32;                 // keys per granule
-#ifndef SPEC_AP_AL
-#define SPEC_AP_AL 4
-#endif
 constexpr int MAX_RTC = 3;             // row tiles per CTA, at most (paged_row_tiles)
 constexpr int MAX_SLOTS = 64;          // granules in a CTA's ring, at most
 
@@ -156,6 +152,10 @@ template <int IO, int KV, int D> struct At {
     static constexpr int QT = F32 ? 3 : (Q8 && IO == SPEC_IO_F32 ? 2 : 1);  // parts of a Q value
     static constexpr int QR = EPC / 2;                  // Q registers per chunk and part
     static constexpr int PT = F32 ? 3 : (Q8 && IO == SPEC_IO_BF16 ? 1 : 2); // parts of a weight
+    // Keys per granule: about 16 KB of K and V at D = 128, so that issuing its
+    // copies (about 40 cycles each, two to four of them) keeps ahead of memory
+    static constexpr int GK = Q8 ? 64 : 32;
+    static constexpr int NSUB = GK / SUB;
     static constexpr int SLOT_KV = GK * ROWB;           // bytes of K (or V) of a granule
     static constexpr int SLOT = 2 * SLOT_KV;
 };
@@ -165,7 +165,7 @@ template <class A> __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
     constexpr int CPB = A::SW / 16;
     const int blk = c / CPB, cc = c % CPB;
     const int x = A::SW == 128 ? (r & 7) : ((r >> 1) & 3);
-    return (uint32_t)(blk * GK * A::SW + r * A::SW + ((cc ^ x) << 4));
+    return (uint32_t)(blk * A::GK * A::SW + r * A::SW + ((cc ^ x) << 4));
 }
 
 struct AttnParams {
@@ -182,7 +182,8 @@ struct AttnParams {
     int B, T, Hq, G;
     int rtc, rtg;            // row tiles per CTA, row groups per (request, kv-head)
     int slots;
-    int box;                 // rows per copy: GK, or SUB where pages are that small
+    int gk_sh;               // log2 of a granule's keys
+    int box;                 // rows per copy: a granule's, or a page's where that is less
     size_t table_lines, q_lines;   // 128-byte lines of the page table and of Q
     int min_sh;              // a CTA takes at least 2^min_sh granules of a long segment
     unsigned long long g_mul;   // ceil(2^32 / G)
@@ -207,7 +208,7 @@ __device__ __forceinline__ Req request(const AttnParams& p, int b, uint32_t& bit
         r.L = r.L < 0 ? 0 : min(r.L, cap);
     }
     const int end = r.n > 0 ? min(r.L + r.n, cap) : 0;
-    r.ng = max(1, (end + GK - 1) / GK);
+    r.ng = max(1, (end + (1 << p.gk_sh) - 1) >> p.gk_sh);
     return r;
 }
 
@@ -253,9 +254,9 @@ struct Pend {
     int last;                // this CTA's part was the last one to be written
 };
 
-// NR column tiles of 8 rows per warp, W key warps times row tiles, NS halves of a
-// granule at a time, QS: Q in shared memory instead of registers
-template <int IO, int KV, int D, int NR, int W, int NS, bool QS>
+// NR column tiles of 8 rows per warp; W key warps times row tiles; QS: Q in shared
+// memory instead of registers
+template <int IO, int KV, int D, int NR, int W, bool QS>
 __global__ void __launch_bounds__(32 * (W + 1), 1)
 attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
            const __grid_constant__ AttnParams p) {
@@ -270,11 +271,12 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     __shared__ volatile int abort_flag;
     __shared__ Pend pend[2];
 
+    constexpr int GK = A::GK, NS = 2;    // keys per granule, sub-tiles taken together
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int hr = p.pm.Hkv * p.rtg;
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float* scales = reinterpret_cast<float*>(ring + (size_t)p.slots * A::SLOT);
-    float4* buf = reinterpret_cast<float4*>(scales + (A::Q8 ? p.slots * 2 * GK : 0));
+    float4* buf = reinterpret_cast<float4*>(scales + (A::Q8 ? p.slots * 2 * A::GK : 0));
 
     // ---- this CTA's share of the granules
     if (tid == 0) {
@@ -297,7 +299,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 : static_cast<const char*>(p.q) + (k - p.table_lines) * 128));
     // How the granules are dealt out.  Up to 32 requests every warp reads all
     // lengths, one per lane; beyond, the block does, some per thread.
-    //   whole:   short segments (a warp takes two granules at most), one to a
+    //   whole:   short segments (64 keys a warp at most), one to a
     //            CTA, when there are CTAs enough;
     //   aligned: few long segments: each gets CTAs of its own, by its length
     //            (no CTA then works, and joins, in two segments);
@@ -313,9 +315,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         if (lane < p.B) rq = request(p, lane, bits);
         units = __reduce_add_sync(0xffffffffu, rq.ng) * hr;
         const int longest = __reduce_max_sync(0xffffffffu, rq.ng);
-        const bool whole = nseg <= (int)gridDim.x && longest <= 2 * (W / p.rtc);
+        const bool whole = nseg <= (int)gridDim.x && longest <= 64 / GK * (W / p.rtc);
         n_cta = whole ? nseg : min((int)gridDim.x, (units + (1 << p.min_sh) - 1) >> p.min_sh);
-        const bool aligned = !whole && SPEC_AP_AL * nseg <= n_cta && units < (1 << 22);
+        const bool aligned = !whole && 4 * nseg <= n_cta && units < (1 << 22);
         // CTAs per segment of the lane's request, or granules of the request
         int k = whole ? 1 : rq.ng;
         if (aligned) k = 1 + (n_cta - nseg) * rq.ng / units;
@@ -410,8 +412,13 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     const int cap = p.pm.cap();
 
     if (warp == W) {
-        // ---- producer: one granule per lane, four lanes at a time; the page
-        // ids of 32 granules are fetched at once
+        // ---- producer: one granule per lane, SB lanes at a time; the page ids of 32
+        // granules are fetched at once.  Issuing costs this warp some 200 cycles
+        // a group and 40 a copy; a large group waits for as many free slots.
+        // (2.2 GB of 8-bit cache: 32 keys a granule, groups of 1, 2, 4, 8: 621,
+        // 452, 366, 334 us; 64 keys, groups of 1, 2, 4: 391, 329, 342.  bf16, 24
+        // requests, groups of 1, 2, 4, 8: 79, 77, 75.8, 78.8 us.)
+        constexpr int SB = A::Q8 ? 2 : 4;
         int slot0 = 0, use0 = 0;         // of the batch's first granule
         bool ok = true;
         uint32_t bad = 0;
@@ -427,30 +434,32 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             for (int base = 0; base < cnt && ok; base += 32) {
                 const int gi = base + lane;
                 const int key = (wk.pos + gi) * GK;
-                int page[2] = {-1, -1};
-                if (gi < cnt) {
+                int page[A::NSUB];
+                uint32_t have = 0;           // sub-tiles whose rows are in the pool
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int at = key + h * SUB;
-                        if (at >= end) continue;
+                for (int h = 0; h < A::NSUB; ++h) {
+                    const int at = key + h * SUB;
+                    page[h] = -1;
+                    // rows that come with an earlier copy of this granule
+                    if (h > 0 && (h * SUB) % p.box != 0) {
+                        page[h] = page[h - 1];
+                    } else if (gi < cnt && at < end) {
                         page[h] = p.pm.table[(size_t)wk.b * p.pm.max_pages + (at >> p.pm.sh)];
                         if ((unsigned)page[h] >= (unsigned)p.pm.n_pages) {
                             bad = SPEC_DEV_BADPAGE;
                             page[h] = -1;
                         }
                     }
-                    // a copy of GK rows brings the whole granule
-                    if (p.box == GK) page[1] = page[0];
+                    have |= (page[h] >= 0 ? 1u : 0u) << h;
                 }
-                const uint32_t have = (page[0] >= 0 ? 1u : 0u) | (page[1] >= 0 ? 2u : 0u);
                 int slot = slot0 + lane, use = use0;
                 while (slot >= p.slots) {
                     slot -= p.slots;
                     ++use;
                 }
                 int n = 0;                   // granules of this batch under way
-                for (; n < 32 && base + n < cnt; n += 4) {
-                    const bool turn = lane / 4 == n / 4 && gi < cnt;
+                for (; n < 32 && base + n < cnt; n += SB) {
+                    const bool turn = lane / SB == n / SB && gi < cnt;
                     bool got = true;
                     if (turn) got = mbar_wait(&empty[slot], (use & 1) ^ 1, &abort_flag);
                     ok = __all_sync(0xffffffffu, got);
@@ -459,10 +468,10 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                         flags[slot] = have;
                         tc::mbar_arrive_expect_tx(
                             &full[slot],
-                            __popc(have) * (A::SLOT / 2 + (A::Q8 ? 8 * SUB : 0)));
+                            __popc(have) * (A::SLOT / A::NSUB + (A::Q8 ? 8 * SUB : 0)));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (page[h] < 0 || (h == 1 && p.box == GK)) continue;
+                        for (int h = 0; h < A::NSUB; ++h) {
+                            if (page[h] < 0 || (h * SUB) % p.box != 0) continue;
                             const int prow =
                                 (hk << p.pm.sh) | ((key + h * SUB) & ((1 << p.pm.sh) - 1));
                             uint8_t* kd = ring + (size_t)slot * A::SLOT + h * SUB * A::SW;
@@ -672,8 +681,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const uint32_t ks = smem_u32(ring + (size_t)slot * A::SLOT);
         const uint32_t vs = ks + A::SLOT_KV;
 #pragma unroll 1
-      for (int h0 = 0; h0 < GK / SUB; h0 += NS) {
-        if (NS < GK / SUB && (!((have >> h0) & 1u) || kb + h0 * SUB >= lim_max)) continue;
+      for (int h0 = 0; h0 < A::NSUB; h0 += NS) {
+        const uint32_t part = (have >> h0) & ((1u << NS) - 1u);
+        if (part == 0 || kb + h0 * SUB >= lim_max) continue;
         float x[NR][NS][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
@@ -751,7 +761,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         // scores in log2 units, -inf where the row does not see the key
-        const bool masked = kb + (h0 + NS) * SUB > lim_min || (NS == GK / SUB && have != 3u);
+        const bool masked = kb + (h0 + NS) * SUB > lim_min || part != (1u << NS) - 1u;
         float lv[NS][2];
 #pragma unroll
         for (int h = 0; h < NS; ++h) {
@@ -1303,7 +1313,7 @@ template <class A> bool pool_map(CUtensorMap* m, const spec_paged_cfg& c, const 
     const cuuint64_t rows = (cuuint64_t)c.Hkv * c.page;
     const cuuint64_t dims[3] = {(cuuint64_t)A::ROWB, rows, (cuuint64_t)c.n_pages};
     const cuuint64_t str[2] = {(cuuint64_t)A::ROWB, rows * A::ROWB};
-    const cuuint32_t box[3] = {(cuuint32_t)A::SW, (cuuint32_t)(c.page >= GK ? GK : SUB), 1};
+    const cuuint32_t box[3] = {(cuuint32_t)A::SW, (cuuint32_t)(c.page < A::GK ? c.page : A::GK), 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1314,7 +1324,7 @@ template <class A> bool pool_map(CUtensorMap* m, const spec_paged_cfg& c, const 
 
 constexpr int SMEM_MAX = 225 * 1024;     // of 227 KB, beside the static variables
 
-template <int IO, int KV, int D, int NR, int W, int NS, bool QS>
+template <int IO, int KV, int D, int NR, int W, bool QS>
 cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
                         const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
     using A = At<IO, KV, D>;
@@ -1342,19 +1352,20 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.g_mul = ((1ull << 32) + p.G - 1) / p.G;
     p.rtc = w.rtc;
     p.rtg = w.rtg;
-    p.min_sh = 2;
+    p.min_sh = A::Q8 ? 1 : 2;            // 128 keys
+    p.gk_sh = A::Q8 ? 6 : 5;
     p.table_lines = ((size_t)c.B * c.max_pages * 4 + 127) / 128;
     p.q_lines = ((size_t)c.B * c.T * c.Hq * D * (IO == SPEC_IO_F32 ? 4 : 2) + 127) / 128;
-    p.box = c.page >= GK ? GK : SUB;
+    p.box = c.page < A::GK ? c.page : A::GK;
     p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
     constexpr int fixed = 1024 + W * (A::NT + 1) * 32 * 16 +
                           (QS ? MAX_RTC * NR * (A::KCH * A::QR * 128 + 32) : 0);
-    constexpr int per_slot = A::SLOT + (A::Q8 ? 2 * GK * 4 : 0);
+    constexpr int per_slot = A::SLOT + (A::Q8 ? 2 * A::GK * 4 : 0);
     constexpr int fit = (SMEM_MAX - fixed) / per_slot;
     static_assert(fit >= W && fit >= 4, "the ring's waits need a slot per key warp");
     p.slots = fit < MAX_SLOTS ? fit : MAX_SLOTS;
     const int smem = fixed + p.slots * per_slot;
-    auto kern = attn_paged<IO, KV, D, NR, W, NS, QS>;
+    auto kern = attn_paged<IO, KV, D, NR, W, QS>;
     // once per device and kernel (the size is a constant of the kernel)
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
@@ -1367,7 +1378,7 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     // at most every granule of a full table
-    const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * (((int64_t)c.max_pages * c.page + GK - 1) / GK);
+    const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * (((int64_t)c.max_pages * c.page + A::GK - 1) / A::GK);
     const int grid = (int)(most < sms ? most : sms);
     return launch_k(false, kern, dim3(grid), dim3(32 * (W + 1)), smem, st, mk, mv, p);
 }
@@ -1377,31 +1388,17 @@ cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void*
                    const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
     // one more warp issues the copies: 16 or 8 in all share the registers
     // evenly (128 or 255 each); row tiles in a CTA must divide the warps
+    // Up to eight rows: seven key warps and the producer with up to 255 registers
+    // each.  More: ten with 168, Q in shared memory (8 requests x 32 rows, 8-bit
+    // cache: 49.7 us; seven with 255: 59.9).  In fp32 a granule at D = 128 is 32
+    // KB, and the ring must have a slot per key warp.
     constexpr bool big = At<IO, KV, D>::SLOT > 16384;
-    const int nr = paged_row_tiles(c).nr;
-#ifndef SPEC_AP_1W
-#define SPEC_AP_1W 7
-#define SPEC_AP_1N 2
-#endif
-    if (nr == 1) {
-        if constexpr (IO == SPEC_IO_BF16 && KV == SPEC_KV_E4M3)
-            return attn_launch<IO, KV, D, 1, SPEC_AP_1W, SPEC_AP_1N, false>(c, kv, q, n_new, o, ws, st);
-        else
-            return attn_launch<IO, KV, D, 1, big ? 6 : 7, 2, false>(c, kv, q, n_new, o, ws, st);
-    }
-#ifdef SPEC_AP_4
+    if (paged_row_tiles(c).nr == 1)
+        return attn_launch<IO, KV, D, 1, big ? 6 : 7, false>(c, kv, q, n_new, o, ws, st);
     if constexpr (IO == SPEC_IO_BF16)
-        if (nr == 4) return attn_launch<IO, KV, D, 4, 7, 1, true>(c, kv, q, n_new, o, ws, st);
-#endif
-#ifndef SPEC_AP_2W
-#define SPEC_AP_2W 7
-#define SPEC_AP_2N 2
-#define SPEC_AP_2Q false
-#endif
-    if constexpr (IO == SPEC_IO_BF16 && KV == SPEC_KV_E4M3)
-        return attn_launch<IO, KV, D, 2, SPEC_AP_2W, SPEC_AP_2N, SPEC_AP_2Q>(c, kv, q, n_new, o, ws, st);
+        return attn_launch<IO, KV, D, 2, 10, true>(c, kv, q, n_new, o, ws, st);
     else
-        return attn_launch<IO, KV, D, 2, big ? 6 : 7, 2, false>(c, kv, q, n_new, o, ws, st);
+        return attn_launch<IO, KV, D, 2, big ? 6 : 7, false>(c, kv, q, n_new, o, ws, st);
 }
 
 }  // namespace

@@ -48,15 +48,10 @@ struct RowTiles {
     int nr, rtc, rtg;
 };
 
-#ifdef SPEC_AP_4
-#define SPEC_AP_N 4
-#else
-#define SPEC_AP_N 2
-#endif
 inline RowTiles paged_row_tiles(const spec_paged_cfg& c) {
     const int64_t rows = (int64_t)c.T * (c.Hq / c.Hkv);
     RowTiles r{};
-    r.nr = rows <= 8 ? 1 : (rows <= 16 || c.io_dtype == SPEC_IO_F32 ? 2 : SPEC_AP_N);
+    r.nr = rows <= 8 ? 1 : 2;
     const int64_t tiles = (rows + 8 * r.nr - 1) / (8 * r.nr);
     r.rtg = (int)((tiles + 2) / 3);
     r.rtc = (int)((tiles + r.rtg - 1) / r.rtg);

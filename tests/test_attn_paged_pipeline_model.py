@@ -1,5 +1,5 @@
 """A CPU model of the ring protocol of the decode attention (csrc/attn_paged.cu):
-one producer that issues granule copies in order, four at a time, into a ring
+one producer that issues granule copies in order, a few at a time, into a ring
 of slots, and key warps that take the granules in turn (granule i of a segment
 portion by warp i mod KW; with several row tiles, one warp of each).  Copies
 land and warps work for random times, and mbarrier waits have the hardware's
@@ -47,7 +47,7 @@ class Bar:
         return ok
 
 
-def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1):
+def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1, group=4):
     rnd = random.Random(seed)
     full, empty = [Bar(1) for _ in range(slots)], [Bar(rtc) for _ in range(slots)]
     content, readers = [None] * slots, [0] * slots
@@ -64,13 +64,13 @@ def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1):
     def producer():
         i = 0
         for cnt in portions:
-            for b in range(0, cnt, 4):
-                group = range(i + b, i + min(b + 4, cnt))
-                for k in group:
+            for b in range(0, cnt, group):
+                batch = range(i + b, i + min(b + group, cnt))
+                for k in batch:
                     phase = k // slots - 1
                     while phase >= 0 and not empty[k % slots].passed(phase):
                         yield 1
-                for k in group:
+                for k in batch:
                     s = k % slots
                     if readers[s]:
                         raise Broken("a slot is written while it is read")
@@ -137,11 +137,12 @@ def portions_of(rnd):
     return [rnd.choice([1, 3, 7, 17, 40, 70]) for _ in range(rnd.randint(1, 4))]
 
 
-@pytest.mark.parametrize("slots,kws,rtc", [(13, 7, 1), (25, 7, 1), (51, 7, 1), (6, 6, 1),
-                                           (24, 11, 1), (11, 11, 1), (13, 3, 2), (13, 2, 3)])
-def test_ring(slots, kws, rtc):
+@pytest.mark.parametrize("slots,kws,rtc,group", [
+    (12, 7, 1, 4), (11, 7, 1, 2), (23, 7, 1, 2), (24, 7, 1, 4), (6, 6, 1, 4), (10, 10, 1, 2),
+    (10, 5, 2, 2), (10, 3, 3, 4), (13, 3, 2, 4)])
+def test_ring(slots, kws, rtc, group):
     for seed in range(25):
-        run(portions_of(random.Random(seed)), slots, kws, rtc, seed)
+        run(portions_of(random.Random(seed)), slots, kws, rtc, seed, group=group)
 
 
 def test_a_wait_for_the_copy_alone_is_caught():
