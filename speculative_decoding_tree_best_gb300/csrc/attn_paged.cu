@@ -185,7 +185,7 @@ struct AttnParams {
     int gk_sh;               // log2 of a granule's keys
     int box;                 // rows per copy: a granule's, or a page's where that is less
     size_t table_lines, q_lines;   // 128-byte lines of the page table and of Q
-    int min_sh;              // a CTA takes at least 2^min_sh granules of a long segment
+    int min_sh;              // aligned: a CTA takes at least 2^min_sh granules
     unsigned long long g_mul;   // ceil(2^32 / G)
     float qk_scale;          // log2(e) / sqrt(D)
     // row / G, exact for the rows there can be (at most 2^16)
@@ -212,18 +212,28 @@ __device__ __forceinline__ Req request(const AttnParams& p, int b, uint32_t& bit
     return r;
 }
 
-// One pass over the segments of a CTA's granule range, in order.
+// What a segment costs a CTA beside its granules (Q, joining, a part): about so
+// many granules' time.  Each segment is dealt out as if it began with them (24
+// requests, 8-bit cache, 1, 4, 6, 8, 12: 51.7, 48.9, 47.3, 47.2, 47.4 us).
+constexpr int OVERHEAD = 8;
+
+// One pass over the segments of a CTA's share, in order.
 struct Walk {
-    int b, seg, pos;         // request, segment in the request, granule in the segment
-    int left;
+    int b, seg;              // request, segment in the request
+    int at;                  // place in the segment, of its ov + rq.ng
+    int left;                // of the share
+    int ov;
     Req rq;
-    __device__ __forceinline__ int count() const { return min(rq.ng - pos, left); }
-    // past `c` granules of the present segment
-    __device__ __forceinline__ void next(const AttnParams& p, int hr, int c) {
+    __device__ __forceinline__ int take() const { return min(ov + rq.ng - at, left); }
+    // the granules of this portion: [pos, pos + count)
+    __device__ __forceinline__ int pos() const { return max(0, at - ov); }
+    __device__ __forceinline__ int count() const { return max(0, at + take() - ov) - pos(); }
+    __device__ __forceinline__ void next(const AttnParams& p, int hr) {
+        const int c = take();
         left -= c;
-        pos += c;
-        if (pos < rq.ng || left <= 0) return;
-        pos = 0;
+        at += c;
+        if (at < ov + rq.ng || left <= 0) return;
+        at = 0;
         if (++seg == hr) {
             seg = 0;
             ++b;
@@ -233,7 +243,7 @@ struct Walk {
     }
 };
 
-// `units` granules (below 2^31) dealt to n CTAs: the first r get q + 1, the others q.
+// `units` (below 2^31) dealt to n CTAs: the first r get q + 1, the others q.
 struct Deal {
     int q, r;
     Deal() = default;
@@ -246,6 +256,12 @@ struct Deal {
                        : r + (int)((uint32_t)(u - big) / (uint32_t)q);
     }
 };
+
+// CTAs to deal to: as many as there are, but a segment is not cut to less than
+// twice its overhead.
+__device__ __forceinline__ int cta_count(int units, int nseg, int most) {
+    return min(most, max(nseg, units / (2 * OVERHEAD)));
+}
 
 // A segment that this CTA shares with others: what joining its parts needs.
 struct Pend {
@@ -303,7 +319,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     //            CTA, when there are CTAs enough;
     //   aligned: few long segments: each gets CTAs of its own, by its length
     //            (no CTA then works, and joins, in two segments);
-    //   else     the row of all granules is cut evenly, at least 2^min_sh each.
+    //   else     the row of all segments, overheads included, is cut evenly.
     Walk wk;
     Deal deal;
     int g0 = 0, n_cta, units;
@@ -313,14 +329,18 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     if (p.B <= 32) {
         Req rq{0, 0, 0};
         if (lane < p.B) rq = request(p, lane, bits);
-        units = __reduce_add_sync(0xffffffffu, rq.ng) * hr;
+        const int granules = __reduce_add_sync(0xffffffffu, rq.ng) * hr;
         const int longest = __reduce_max_sync(0xffffffffu, rq.ng);
         const bool whole = nseg <= (int)gridDim.x && longest <= 64 / GK * (W / p.rtc);
-        n_cta = whole ? nseg : min((int)gridDim.x, (units + (1 << p.min_sh) - 1) >> p.min_sh);
-        const bool aligned = !whole && 4 * nseg <= n_cta && units < (1 << 22);
-        // CTAs per segment of the lane's request, or granules of the request
-        int k = whole ? 1 : rq.ng;
-        if (aligned) k = 1 + (n_cta - nseg) * rq.ng / units;
+        n_cta = min((int)gridDim.x, (granules + (1 << p.min_sh) - 1) >> p.min_sh);
+        const bool aligned = !whole && 4 * nseg <= n_cta && granules < (1 << 22);
+        units = granules + nseg * OVERHEAD;
+        // CTAs per segment of the lane's request, or its segment's units
+        int k = whole ? 1 : rq.ng + OVERHEAD;
+        if (aligned)
+            k = 1 + (n_cta - nseg) * rq.ng / granules;
+        else
+            n_cta = whole ? nseg : cta_count(units, nseg, gridDim.x);
         if (lane >= p.B) k = 0;
         int incl = k * hr;
 #pragma unroll
@@ -342,17 +362,18 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const int off = want - (__shfl_sync(0xffffffffu, incl, b) - k * hr);
         wk.seg = (int)((uint32_t)off / (uint32_t)k);
         const int rest = off - wk.seg * k;
+        wk.ov = whole || aligned ? 0 : OVERHEAD;
         if (whole) {
-            wk.pos = 0;
+            wk.at = 0;
             wk.left = wk.rq.ng;
         } else if (aligned) {
             const Deal d(wk.rq.ng, k);
-            wk.pos = d.start(rest);
-            wk.left = d.start(rest + 1) - wk.pos;
+            wk.at = d.start(rest);
+            wk.left = d.start(rest + 1) - wk.at;
             own_c0 = cta - rest;
             own_c1 = own_c0 + k - 1;
         } else {
-            wk.pos = rest;
+            wk.at = rest;
             wk.left = deal.start(cta + 1) - g0;
         }
         __syncthreads();
@@ -362,7 +383,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         Req rq0{};
         for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
             rq0 = request(p, b, bits);
-            mine += rq0.ng * hr;
+            mine += (rq0.ng + OVERHEAD) * hr;
         }
         int incl = mine;
 #pragma unroll
@@ -380,7 +401,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             if (w < warp) before += x;
             units += x;
         }
-        n_cta = min((int)gridDim.x, (units + (1 << p.min_sh) - 1) >> p.min_sh);
+        n_cta = cta_count(units, nseg, gridDim.x);
         if (cta >= n_cta) return;
         deal = Deal(units, n_cta);
         g0 = deal.start(cta);
@@ -390,7 +411,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             for (int b = tid * per;; ++b) {
                 uint32_t ignore = 0;
                 if (per > 1) rq0 = request(p, b, ignore);
-                const int c = rq0.ng * hr;
+                const int c = (rq0.ng + OVERHEAD) * hr;
                 if (g0 < at + c) {
                     first_b = b;
                     first_off = g0 - at;
@@ -404,8 +425,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         wk.b = first_b;
         wk.rq = first_rq;
         wk.left = deal.start(cta + 1) - g0;
-        wk.seg = (int)((uint32_t)first_off / (uint32_t)wk.rq.ng);
-        wk.pos = first_off - wk.seg * wk.rq.ng;
+        wk.ov = OVERHEAD;
+        wk.seg = (int)((uint32_t)first_off / (uint32_t)(wk.rq.ng + OVERHEAD));
+        wk.at = first_off - wk.seg * (wk.rq.ng + OVERHEAD);
     }
     if (bits && cta == 0) raise_status(p.ws, bits);
     const int rows_tile = 8 * NR;
@@ -430,10 +452,10 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 const int last = min(r0 + p.rtc * rows_tile, wk.rq.n * p.G) - 1;
                 end = min(wk.rq.L + p.tok(last) + 1, cap);
             }
-            const int cnt = wk.count();
+            const int first = wk.pos(), cnt = wk.count();
             for (int base = 0; base < cnt && ok; base += 32) {
                 const int gi = base + lane;
-                const int key = (wk.pos + gi) * GK;
+                const int key = (first + gi) * GK;
                 int page[A::NSUB];
                 uint32_t have = 0;           // sub-tiles whose rows are in the pool
 #pragma unroll
@@ -520,7 +542,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     ++use0;
                 }
             }
-            wk.next(p, hr, cnt);
+            wk.next(p, hr);
         }
         if (__any_sync(0xffffffffu, bad != 0) && lane == 0) raise_status(p.ws, SPEC_DEV_BADPAGE);
         if (!ok) {
@@ -1094,7 +1116,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
 
-    int gpos = g0;                       // global index of the present granule
+    int gpos = g0;                       // where this CTA is among all units
     uint4 raw[RAW];
     // one row tile: the next segment's Q rows are fetched during this one
     constexpr bool AHEAD = NR == 1 && IO == SPEC_IO_BF16;
@@ -1106,7 +1128,13 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         clear();
         if (wk.left > 0) {
         const int row0 = (p.rg(wk.seg) * p.rtc + rt) * rows_tile;
-        const int cnt = wk.count();
+        const int first = wk.pos(), cnt = wk.count();
+        if (cnt == 0) {                      // a segment's overhead alone
+            gpos += wk.take();
+            wk.next(p, hr);
+            if (AHEAD && wk.left > 0) load_q(wk, rt, raw);
+            continue;
+        }
         // ---- limits and Q of this warp's rows
         int lim_min = 0, lim_max = 0;
         if (row0 < wk.rq.n * p.G) {
@@ -1143,7 +1171,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         Walk nx = wk;
-        nx.next(p, hr, cnt);
+        nx.next(p, hr);
         if (AHEAD && nx.left > 0) load_q(nx, rt, raw);
         // ---- the granules: every KW-th one
         int slot = slot0 + kw, use = use0;
@@ -1163,7 +1191,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 if (lane == 0) raise_status(p.ws, SPEC_DEV_TIMEOUT);
             }
             __syncwarp();
-            const int kb = (wk.pos + gi) * GK;
+            const int kb = (first + gi) * GK;
             const uint32_t have = flags[slot];
             if (have != 0 && kb < lim_max) granule(kb, slot, have, lim_min, lim_max);
             __syncwarp();
@@ -1184,9 +1212,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             c0 = own_c0, c1 = own_c1;
             int shift = 0;
             if (c0 < 0) {
-                const int s0 = gpos - wk.pos;
-                c0 = deal.owner(s0);
-                c1 = deal.owner(s0 + wk.rq.ng - 1);
+                const int s0 = gpos - wk.at;
+                c0 = deal.owner(s0 + wk.ov);
+                c1 = deal.owner(s0 + wk.ov + wk.rq.ng - 1);
                 shift = s0 > deal.start(c0);
             }
             at = 2 * cta + (cta == c0 ? shift : 0);
@@ -1201,7 +1229,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 pe.shift = shift;
             }
         }
-        gpos += cnt;
+        gpos += wk.take();
         wk = nx;
         } else {
             // ---- out of granules: the segments whose last part was this CTA's
