@@ -137,7 +137,7 @@ __device__ __forceinline__ void split3x2(float x, float y, uint32_t& p0, uint32_
 
 // ---- layout of the operands -----------------------------------------------------------
 
-template <int IO, int KV, int D> struct At {
+template <int IO, int KV, int D, int NR> struct At {
     static constexpr bool Q8 = KV == SPEC_KV_E4M3;
     static constexpr bool F32 = !Q8 && IO == SPEC_IO_F32;
     static constexpr int EB = Q8 ? 1 : (IO == SPEC_IO_F32 ? 4 : 2);   // bytes of a cached value
@@ -152,9 +152,10 @@ template <int IO, int KV, int D> struct At {
     static constexpr int QT = F32 ? 3 : (Q8 && IO == SPEC_IO_F32 ? 2 : 1);  // parts of a Q value
     static constexpr int QR = EPC / 2;                  // Q registers per chunk and part
     static constexpr int PT = F32 ? 3 : (Q8 && IO == SPEC_IO_BF16 ? 1 : 2); // parts of a weight
-    // Keys per granule: about 16 KB of K and V at D = 128, so that issuing its
-    // copies (about 40 cycles each, two to four of them) keeps ahead of memory
-    static constexpr int GK = Q8 ? 64 : 32;
+    // Keys per granule.  With few rows memory is the bound: 64 keys in 8 bits, so
+    // that issuing a granule's copies (about 40 cycles each, four of them) keeps
+    // ahead of it.  With more rows the products are, and 32 keys spread better.
+    static constexpr int GK = Q8 && NR == 1 ? 64 : 32;
     static constexpr int NSUB = GK / SUB;
     static constexpr int SLOT_KV = GK * ROWB;           // bytes of K (or V) of a granule
     static constexpr int SLOT = 2 * SLOT_KV;
@@ -276,7 +277,7 @@ template <int IO, int KV, int D, int NR, int W, bool QS>
 __global__ void __launch_bounds__(32 * (W + 1), 1)
 attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
            const __grid_constant__ AttnParams p) {
-    using A = At<IO, KV, D>;
+    using A = At<IO, KV, D, NR>;
     constexpr int NTH = 32 * (W + 1);
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
@@ -566,7 +567,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     // tiles in shared memory, [rt][nr][chunk][pair][lane]
     static_assert(!QS || A::QT == 1, "Q in shared memory is in one part");
     uint32_t qf[NR][A::QT][A::KCH][A::QR] = {};  // not used with QS
-    uint2* qs = reinterpret_cast<uint2*>(buf + W * (A::NT + 1) * 32);
+    uint2* qs = reinterpret_cast<uint2*>(buf + W * NR * (A::NT + 1) * 32);
     float* qsf = reinterpret_cast<float*>(qs + (QS ? p.rtc * NR * A::KCH * (A::QR / 2) * 32 : 0));
 
     auto clear = [&]() {
@@ -581,33 +582,32 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
     };
     auto bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
-    constexpr int JW = (A::NT + 1) * 32;                 // float4 of a warp's column tile
+    constexpr int JW = NR * (A::NT + 1) * 32;            // float4 of a warp
+    constexpr int TPR = NR * A::NT / 2;                  // pairs of tiles of a row tile
     constexpr int PO = NR * A::NT * 32, PM = NR * 32;    // float4 of a part's row tile
-    // The end of a segment portion (or of the joining of parts), column tile by
-    // column tile: the key warps' results meet in shared memory, (max, max, sum,
-    // sum) and the tiles of O^T in register order; the tiles are shared out to the
-    // warps by twos, joined over the key warps, and go to the output (whole) or
-    // to part `at` of the workspace.
+    // The end of a segment portion (or of the joining of parts): the key warps'
+    // results meet in shared memory, (max, max, sum, sum) and the tiles of O^T in
+    // register order; the tiles are shared out to the warps by twos, joined over
+    // the key warps, and go to the output (whole) or to part `at` of the workspace.
     auto finish = [&](int b, int seg, int n, bool whole, size_t at) {
-#pragma unroll 1
-      for (int nr = 0; nr < NR; ++nr) {
         bar();                                           // everyone is done with buf
         if (kw < KW) {
             float4* d = buf + warp * JW + lane;
 #pragma unroll
-            for (int c = 0; c < NR; ++c) {
-                if (c != nr) continue;
-                d[0] = make_float4(m[c][0], m[c][1], l[c][0], l[c][1]);
+            for (int nr = 0; nr < NR; ++nr) {
+                d[nr * (A::NT + 1) * 32] = make_float4(m[nr][0], m[nr][1], l[nr][0], l[nr][1]);
 #pragma unroll
                 for (int i = 0; i < A::NT; ++i)
-                    d[(1 + i) * 32] = make_float4(o[c][i][0], o[c][i][1], o[c][i][2], o[c][i][3]);
+                    d[(nr * (A::NT + 1) + 1 + i) * 32] =
+                        make_float4(o[nr][i][0], o[nr][i][1], o[nr][i][2], o[nr][i][3]);
             }
         }
         bar();
 #pragma unroll 1
-        for (int task = warp; task < p.rtc * (A::NT / 2); task += W) {
-            const int rt2 = task / (A::NT / 2), i = task % (A::NT / 2) * 2;
-            const float4* s = buf + rt2 * JW + lane;
+        for (int task = warp; task < p.rtc * TPR; task += W) {
+            const int rt2 = task / TPR, nr = task % TPR / (A::NT / 2);
+            const int i = task % (A::NT / 2) * 2;
+            const float4* s = buf + rt2 * JW + nr * (A::NT + 1) * 32 + lane;
             const int step = p.rtc * JW;
             float4 x[W];
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
@@ -682,7 +682,6 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
             if (bad) raise_status(p.ws, SPEC_DEV_RANGE);
         }
-      }
     };
 
     // Keys that rows 2t, 2t + 1 of column tile nr see: [0, limit); rows that are
@@ -1295,7 +1294,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         finish(b, seg, n, whole, at);
-        if (!whole && warp < min(W, p.rtc * (A::NT / 2))) {
+        if (!whole && warp < min(W, p.rtc * TPR)) {
             // each warp that wrote of the part counts itself in; the segment is
             // joined, when its CTA has no more granules, by who comes last.  (A
             // CTA's first part is counted in while it works on: the neighbour
@@ -1304,7 +1303,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             __syncwarp();
             if (lane == 0) {
                 uint32_t* tk = p.tickets + (size_t)b * hr + seg;
-                const uint32_t all = (uint32_t)(c1 - c0 + 1) * min(W, p.rtc * (A::NT / 2));
+                const uint32_t all = (uint32_t)(c1 - c0 + 1) * min(W, p.rtc * TPR);
                 if (atomicAdd(tk, 1u) == all - 1) {
                     *tk = 0;                             // for the next call
                     pend[which].last = 1;
@@ -1355,7 +1354,7 @@ constexpr int SMEM_MAX = 225 * 1024;     // of 227 KB, beside the static variabl
 template <int IO, int KV, int D, int NR, int W, bool QS>
 cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
                         const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
-    using A = At<IO, KV, D>;
+    using A = At<IO, KV, D, NR>;
     const int sms = device_sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
     const PagedWs w = paged_ws_layout(c, sms);
@@ -1380,13 +1379,13 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.g_mul = ((1ull << 32) + p.G - 1) / p.G;
     p.rtc = w.rtc;
     p.rtg = w.rtg;
-    p.min_sh = A::Q8 ? 1 : 2;            // 128 keys
-    p.gk_sh = A::Q8 ? 6 : 5;
+    p.gk_sh = A::GK == 64 ? 6 : 5;
+    p.min_sh = 7 - p.gk_sh;              // 128 keys
     p.table_lines = ((size_t)c.B * c.max_pages * 4 + 127) / 128;
     p.q_lines = ((size_t)c.B * c.T * c.Hq * D * (IO == SPEC_IO_F32 ? 4 : 2) + 127) / 128;
     p.box = c.page < A::GK ? c.page : A::GK;
     p.qk_scale = 1.4426950408889634f / sqrtf((float)D);
-    constexpr int fixed = 1024 + W * (A::NT + 1) * 32 * 16 +
+    constexpr int fixed = 1024 + W * NR * (A::NT + 1) * 32 * 16 +
                           (QS ? MAX_RTC * NR * (A::KCH * A::QR * 128 + 32) : 0);
     constexpr int per_slot = A::SLOT + (A::Q8 ? 2 * A::GK * 4 : 0);
     constexpr int fit = (SMEM_MAX - fixed) / per_slot;
@@ -1420,13 +1419,14 @@ cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void*
     // each.  More: ten with 168, Q in shared memory (8 requests x 32 rows, 8-bit
     // cache: 49.7 us; seven with 255: 59.9).  In fp32 a granule at D = 128 is 32
     // KB, and the ring must have a slot per key warp.
-    constexpr bool big = At<IO, KV, D>::SLOT > 16384;
+    constexpr bool big = At<IO, KV, D, 1>::SLOT > 16384;
     if (paged_row_tiles(c).nr == 1)
         return attn_launch<IO, KV, D, 1, big ? 6 : 7, false>(c, kv, q, n_new, o, ws, st);
     if constexpr (IO == SPEC_IO_BF16)
-        return attn_launch<IO, KV, D, 2, 10, true>(c, kv, q, n_new, o, ws, st);
+        return attn_launch<IO, KV, D, 2, At<IO, KV, D, 2>::SLOT < 16384 ? 10 : 7, true>(
+            c, kv, q, n_new, o, ws, st);
     else
-        return attn_launch<IO, KV, D, 2, big ? 6 : 7, false>(c, kv, q, n_new, o, ws, st);
+        return attn_launch<IO, KV, D, 2, big ? 5 : 7, false>(c, kv, q, n_new, o, ws, st);
 }
 
 }  // namespace
