@@ -45,6 +45,16 @@ __device__ __forceinline__ void merge(float& m, float& s, float om, float os, fl
     m = nm;
 }
 
+// The warp's (m, s), in every lane.
+__device__ __forceinline__ void warp_mass(float& m, float& s, float k) {
+    float nm = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, o));
+    if (m != nm) s *= ex2((m - nm) * k);
+    m = nm;
+    s = warp_sum(s);
+}
+
 struct Cand {
     float s;          // w / e of the best token, -inf when there is none
     int i;
@@ -163,21 +173,17 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
             merge(m, s, x, x == -INFINITY ? 0.0f : x - x + 1.0f, k);   // NaN, +inf: NaN
         }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float om = __shfl_xor_sync(0xffffffffu, m, o);
-        const float os = __shfl_xor_sync(0xffffffffu, s, o);
-        merge(m, s, om, os, k);
-    }
+    warp_mass(m, s, k);
     if (threadIdx.x % 32 == 0) {
         sm[threadIdx.x / 32] = m;
         ss[threadIdx.x / 32] = s;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int w = 1; w < NT / 32; ++w) merge(m, s, sm[w], ss[w], k);
-        part[(size_t)row * splits + seg] = make_float2(m, s);
+    if (threadIdx.x < 32) {
+        m = threadIdx.x < NT / 32 ? sm[threadIdx.x] : -INFINITY;
+        s = threadIdx.x < NT / 32 ? ss[threadIdx.x] : 0.0f;
+        warp_mass(m, s, k);
+        if (threadIdx.x == 0) part[(size_t)row * splits + seg] = make_float2(m, s);
     }
 }
 
@@ -254,12 +260,7 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
             const float2 x = __ldcg(a.part + row * a.splits + k);
             merge(m, s, x.x, x.y, a.k);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, o);
-            const float os = __shfl_xor_sync(0xffffffffu, s, o);
-            merge(m, s, om, os, a.k);
-        }
+        warp_mass(m, s, a.k);
         if (lane == 0) {
             row_m[i] = m;
             row_s[i] = s > 0.0f && s <= 3.0e38f ? s : 0.0f;   // else NaN, +inf or no mass
@@ -283,13 +284,25 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     const T* lp = logits + ((size_t)b * (N + 1) + kept) * V;
     const float* qp = kept < n && a.draft_prob ? a.draft_prob + ((size_t)b * N + kept) * V : nullptr;
     const int point = kept < n && !a.draft_prob ? draft[kept] : -1;
-    Cand best{-INFINITY, NONE};
-    float bar = 0.0f;                    // a little under the best score so far
+    // Scores w / e by the approximate reciprocal; the thread keeps the weight and
+    // exponential of its best, and where two scores are nearer than that
+    // reciprocal tells apart, the quotients decide.  (A division per token made
+    // the race 45 instructions a token.)
+    float top_lo = 0.0f, top_hi = 0.0f, top_w = 0.0f, top_e = 1.0f;
+    int top_i = NONE;
     auto score = [&](float x, float q, float ex, int v) {
-        const float w = ex2((x - m) * a.k) * inv - q;
-        if (w > bar * ex) {              // seldom: the division is not for every token
-            take(best, w / ex, v);
-            bar = best.s * (1.0f - 0x1p-20f);
+        const float w = fmaf(ex2((x - m) * a.k), inv, -q);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex));
+        const float s = w * r;
+        bool more = s > top_hi;
+        if (!more && s > top_lo) more = w / ex > top_w / top_e;      // seldom
+        if (more) {
+            top_lo = s * (1.0f - 0x1p-20f);
+            top_hi = s * (1.0f + 0x1p-20f);
+            top_w = w;
+            top_e = ex;
+            top_i = v;
         }
     };
     if (s > 0.0f && vec) {
@@ -329,6 +342,7 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
         for (int v = lo + tid; v < hi; v += NT)
             score(io_t<IO>::ld(lp, v), qp ? qp[v] : (v == point ? 1.0f : 0.0f), e[v], v);
     }
+    Cand best{top_i == NONE ? -INFINITY : top_w / top_e, top_i};
     best = block_best(best, sh);
     if (tid == 0) {
         __stcg(a.cand + (size_t)b * a.slices + blockIdx.x,

@@ -47,6 +47,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// x / y from r, 1 / y rounded: one Newton step on the quotient's remainder, which
+// rounds it correctly (Markstein 1990).
+__device__ __forceinline__ float quotient(float x, float y, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, y, x), r, q);
+}
+
 // The rows of one request, (token, head) in memory order, are cut into blocks of
 // RPC rows, one to a CTA; a thread has UNR rows of its block, all under way
 // at once.
@@ -121,19 +128,14 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
             for (int o = G::LPR / 2; o > 0; o >>= 1)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float amax = __uint_as_float(top);
-            float scale = top == 0u ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-100f);
+            float scale = top == 0u ? 1.0f : fmaxf(quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-100f);
             if (top >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
-            // x / scale: quotient by the rounded reciprocal, then one Newton step
-            // on its remainder (Markstein 1990), which rounds it correctly; where
-            // the remainder underflows the code is 0 whatever it is
+            // where the remainder underflows the code is 0 whatever it is
             const float inv = __frcp_rn(scale);
             float x[G::VEC];
             unpack<IO>(u[j], x);
 #pragma unroll
-            for (int k = 0; k < G::VEC; ++k) {
-                const float q = x[k] * inv;
-                x[k] = fmaf(fmaf(-q, scale, x[k]), inv, q);
-            }
+            for (int k = 0; k < G::VEC; ++k) x[k] = quotient(x[k], scale, inv);
             uint32_t c[G::VEC / 4];
 #pragma unroll
             for (int k = 0; k < G::VEC / 4; ++k)
