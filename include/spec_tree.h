@@ -499,7 +499,7 @@ enum {
  * 1 <= T <= 2^20; Hkv <= 1024; Hq % Hkv == 0; D in {64, 128};
  * page a power of two in [16, 1024]; n_pages, max_pages >= 1;
  * max_pages * page <= 2^30; B * max(Hq, Hkv) <= 2^24.  attn_decode_paged:
- * T <= 128, R = T Hq / Hkv <= 65536, and B Hkv ceil(R / 48) (max_pages page / 32)
+ * T <= 128, R = T Hq / Hkv <= 65536, and B Hkv ceil(R / 48) (max_pages page / 32 + 9)
  * < 2^31. */
 typedef struct spec_paged_cfg {
     int32_t B;               /* requests */
@@ -561,11 +561,13 @@ int kv_page_read(const spec_paged_cfg *cfg, const spec_paged_kv *kv, int Lmax, v
  * layer), after their rows were appended.  Row i < n_new[b], q-head h (kv-head
  * h / (Hq/Hkv)) sees cache rows [0, kv_len[b] + i]:
  * o = softmax(q K^T / sqrt(D)) V, fp32 accumulation; rows i >= n_new[b] get 0.
- * Cache rows a row does not see never reach it, whatever they hold.  Rows in
+ * Cache rows a row does not see never reach it, whatever they hold; of those it
+ * sees, a value that is not finite may make all of it not finite.  Rows in
  * pages outside the pool are not seen (SPEC_DEV_BADPAGE); kv_len outside
  * [0, max_pages * page - n_new[b]] is clamped to the table
  * (SPEC_DEV_OVERFLOW); a row that sees nothing gets 0; an output that is not
- * finite raises SPEC_DEV_RANGE.
+ * finite raises SPEC_DEV_RANGE.  Scales are >= 0.  The result does not depend
+ * on the order in which CTAs finish.
  *   q, o [B][T][Hq][D] io     n_new as for kv_page_append     T <= 128
  */
 int attn_decode_paged(const spec_paged_cfg *cfg, const spec_paged_kv *kv, const void *q,

@@ -60,7 +60,7 @@ int attn_decode_paged(const spec_paged_cfg* cfg, const spec_paged_kv* kv, const 
     // granules are counted in 32 bits
     const int64_t per_req = ((int64_t)cfg->max_pages * cfg->page + 31) / 32;
     const int64_t segs = (int64_t)cfg->Hkv * spec::paged_row_tiles(*cfg).rtg;
-    if (cfg->B * per_req > 0x7fffffff / segs) return ST_EINVAL;
+    if (cfg->B * (per_req + 8) > 0x7fffffff / segs) return ST_EINVAL;
 
     if (!al16(q) || !al16(o) || !al16(ws) || (n_new && !al16(n_new))) return ST_EINVAL;
     return cuda_rc(spec::launch_attn_paged(*cfg, *kv, q, n_new, o, ws,

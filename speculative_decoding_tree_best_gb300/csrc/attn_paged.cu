@@ -20,16 +20,29 @@
 // column in both products, and W^T gets from the first product's layout to
 // the second's by movmatrix alone.
 //
-// Data flow.  The cache is cut into granules of 16 rows (a page holds whole
-// granules).  The granules of all (request, kv-head, row group) segments in a
-// row are dealt out evenly to one CTA per SM, so lengths need not match; a
-// segment cut between CTAs leaves parts in the workspace, and the CTA that
-// finishes last (a ticket per segment) joins them in their order.  In a CTA
-// one warp issues TMA copies (16 rows x 128 bytes, 128-byte swizzle) into a ring of
-// granules, and W warps take them in turn.  A row's 16-byte
-// chunks go to lanes so that the products need no transposition of K, and of
-// V only byte permutes; the row order below makes every 128-bit shared load
-// free of bank conflicts under the swizzle.
+// Data flow.  The cache is cut into granules of 32 or 64 rows.  The granules of
+// all (request, kv-head, row group) segments are dealt out to one CTA per SM by
+// their number, so lengths need not match; a segment cut between CTAs leaves
+// parts in the workspace, and the CTA whose part is the last one (a ticket per
+// segment) joins them, in their order.  In a CTA one warp issues TMA copies (up
+// to 64 rows x 128 bytes, 128-byte swizzle) into a ring of granules, and W warps
+// take them in turn.  A row's 16-byte chunks go to lanes so that the products
+// need no transposition of K, and of V only byte permutes; the row order below
+// keeps 128-bit shared loads free of bank conflicts under the swizzle.
+//
+// Rounding.  Scores, weights, sums and outputs are fp32.  What the tensor cores
+// take is exact (cached values; bf16 q) or in parts: weights as two bf16 parts
+// (2^-16) over a bf16 cache, as one fp16 part over an 8-bit cache with bf16
+// outputs (2^-11, an eighth of the output's own rounding; they are at most 1),
+// two fp16 parts with fp32 outputs (2^-22), and an fp32 cache, q and weights as
+// three bf16 parts each (2^-24).
+//
+// Measured (graph replays, bytes of K, V and scales over time): 8 x 131072 keys,
+// 8 kv-heads, 8 bits 326 us, 6.8 TB/s, the rate of a plain copy; 24 requests of
+// 1024-8192 keys bf16 72 us (6.2 TB/s), 8 bits 47 us (4.9 TB/s: two or three
+// segments a CTA, some 5000 cycles each of ends, joins and imbalance); one
+// request of 4096 keys bf16 10 us, of which reading is 2.5: launch, lengths,
+// page ids and copies follow one another, then parts are joined.
 #include <cuda.h>
 #include <math.h>
 
@@ -190,7 +203,9 @@ struct AttnParams {
     unsigned long long g_mul;   // ceil(2^32 / G)
     float qk_scale;          // log2(e) / sqrt(D)
     // row / G, exact for the rows there can be (at most 2^16)
-    __device__ __forceinline__ int tok(int r) const { return (int)(((unsigned long long)r * g_mul) >> 32); }
+    __device__ __forceinline__ int tok(int r) const {
+        return (int)(((unsigned long long)r * g_mul) >> 32);
+    }
     __device__ __forceinline__ int hk(int seg) const { return rtg == 1 ? seg : seg / rtg; }
     __device__ __forceinline__ int rg(int seg) const { return rtg == 1 ? 0 : seg % rtg; }
 };
@@ -307,13 +322,13 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         tc::fence_mbar_init();
     }
     // what comes after the lengths: the page table and Q, on their way to L2
-    // while the lengths are read (a line per thread of the grid)
-    for (size_t k = blockIdx.x * NTH + tid; k < p.table_lines + p.q_lines;
-         k += (size_t)gridDim.x * NTH)
+    // while the lengths are read (a line per thread of the grid, no more)
+    const size_t line = (size_t)blockIdx.x * NTH + tid;
+    if (line < p.table_lines + p.q_lines)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            k < p.table_lines
-                ? reinterpret_cast<const char*>(p.pm.table) + k * 128
-                : static_cast<const char*>(p.q) + (k - p.table_lines) * 128));
+            line < p.table_lines
+                ? reinterpret_cast<const char*>(p.pm.table) + line * 128
+                : static_cast<const char*>(p.q) + (line - p.table_lines) * 128));
     // How the granules are dealt out.  Up to 32 requests every warp reads all
     // lengths, one per lane; beyond, the block does, some per thread.
     //   whole:   short segments (64 keys a warp at most), one to a
@@ -558,13 +573,13 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     const int rt = warp % p.rtc, kw = warp / p.rtc, KW = W / p.rtc;
     const int g = lane / 4, t = lane % 4;
     const int kr = g ^ ((g & 1) << 2);                       // key row of fragment row g
-    const int va = 2 * t, vb = (2 * t + 1) ^ 4;              // key rows of fragment columns 2t, 2t+1
+    const int va = 2 * t, vb = (2 * t + 1) ^ 4;              // of fragment columns 2t, 2t + 1
     int slot0 = 0, use0 = 0;             // of the segment portion's first granule
 
     float o[NR][A::NT][4];
     float m[NR][2], l[NR][2], rowf[NR][2] = {};  // rowf: not used with QS
-    // Q^T, the first product's B operand: in registers, or with four column
-    // tiles in shared memory, [rt][nr][chunk][pair][lane]
+    // Q^T, the first product's B operand: in registers, or (QS) in shared memory
+    // as [rt][nr][chunk][pair][lane]
     static_assert(!QS || A::QT == 1, "Q in shared memory is in one part");
     uint32_t qf[NR][A::QT][A::KCH][A::QR] = {};  // not used with QS
     uint2* qs = reinterpret_cast<uint2*>(buf + W * NR * (A::NT + 1) * 32);
@@ -697,19 +712,20 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             return rowf[nr][e];
     };
 
-    // one granule: keys [kb, kb + GK) in ring slot `slot`; have: its halves in the pool
-    auto granule = [&](int kb, int slot, uint32_t have, int lim_min, int lim_max) {
+    // NS sub-tiles of a granule, from its h0-th on: keys [kb + 16 h0, ..) in ring
+    // slot `slot`; have: a bit per sub-tile that is in the pool
+    auto products = [&](int kb, int h0, int slot, uint32_t have, int lim_min, int lim_max) {
+        const uint32_t part = (have >> h0) & ((1u << NS) - 1u);
+        if (part == 0 || kb + h0 * SUB >= lim_max) return;
         const uint32_t ks = smem_u32(ring + (size_t)slot * A::SLOT);
         const uint32_t vs = ks + A::SLOT_KV;
-#pragma unroll 1
-      for (int h0 = 0; h0 < A::NSUB; h0 += NS) {
-        const uint32_t part = (have >> h0) & ((1u << NS) - 1u);
-        if (part == 0 || kb + h0 * SUB >= lim_max) continue;
         float x[NR][NS][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int h = 0; h < NS; ++h) x[nr][h][0] = x[nr][h][1] = x[nr][h][2] = x[nr][h][3] = 0.0f;
+            for (int h = 0; h < NS; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[nr][h][e] = 0.0f;
         // consecutive products go to different accumulators: the halves in turn
         auto q_of = [&](int nr, int q, int j, int i) {
             if constexpr (QS)
@@ -924,7 +940,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                             const uint32_t c = packh(u, v);
                             wb[nr][0][k] = movm(c);
                             if constexpr (A::PT == 2) {
-                                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&c));
+                                const float2 b =
+                                    __half22float2(*reinterpret_cast<const __half2*>(&c));
                                 wb[nr][A::PT - 1][k] = movm(packh(u - b.x, v - b.y));
                             }
                         } else {
@@ -1029,7 +1046,6 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                         if (limit(nr, e & 1) != cut) o[nr][i][e] = keep[nr][i][e];
             if (++cut > lim_max) break;
         }
-      }
     };
 
     // A column tile's Q rows (tile: in the CTA's row group) as they are in memory,
@@ -1041,7 +1057,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const bool real = i < p.T;
         const uint4* qp = reinterpret_cast<const uint4*>(
             static_cast<const uint8_t*>(p.q) +
-            (real ? (((size_t)w.b * p.T + i) * p.Hq + p.hk(w.seg) * p.G + r - i * p.G) * D * QB : 0));
+            (real ? (((size_t)w.b * p.T + i) * p.Hq + p.hk(w.seg) * p.G + r - i * p.G) * D * QB
+                  : 0));
         constexpr int PC = RAW / A::KCH;                 // pieces per cache chunk
 #pragma unroll
         for (int k = 0; k < RAW; ++k)
@@ -1126,110 +1143,112 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         size_t at = 0;
         clear();
         if (wk.left > 0) {
-        const int row0 = (p.rg(wk.seg) * p.rtc + rt) * rows_tile;
-        const int first = wk.pos(), cnt = wk.count();
-        if (cnt == 0) {                      // a segment's overhead alone
+            const int row0 = (p.rg(wk.seg) * p.rtc + rt) * rows_tile;
+            const int first = wk.pos(), cnt = wk.count();
+            if (cnt == 0) {                      // a segment's overhead alone
+                gpos += wk.take();
+                wk.next(p, hr);
+                if (AHEAD && wk.left > 0) load_q(wk, rt, raw);
+                continue;
+            }
+            // ---- limits and Q of this warp's rows
+            int lim_min = 0, lim_max = 0;
+            if (row0 < wk.rq.n * p.G) {
+                const int last = min(row0 + rows_tile, wk.rq.n * p.G) - 1;
+                lim_min = min(wk.rq.L + p.tok(row0) + 1, cap);
+                lim_max = min(wk.rq.L + p.tok(last) + 1, cap);
+            }
+            if constexpr (QS) {
+                // the warps make a column tile each (they are past the last
+                // segment's products: its joining had barriers)
+                for (int tile = warp; tile < p.rtc * NR; tile += W) {
+                    float row;
+                    uint32_t qt[A::QT][A::KCH][A::QR];
+                    load_q(wk, tile, raw);
+                    make_q(raw, qt, row);
+#pragma unroll
+                    for (int j = 0; j < A::KCH; ++j)
+#pragma unroll
+                        for (int i = 0; i < A::QR / 2; ++i)
+                            qs[((tile * A::KCH + j) * (A::QR / 2) + i) * 32 + lane] =
+                                make_uint2(qt[0][j][2 * i], qt[0][j][2 * i + 1]);
+                    if (t == 0) qsf[tile * 8 + g] = row;
+                }
+                bar();
+            } else {
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    float row;
+                    if (!AHEAD) load_q(wk, rt * NR + nr, raw);
+                    make_q(raw, qf[nr], row);
+                    // lane (g, t) made row g; it needs rows 2t and 2t + 1
+                    rowf[nr][0] = __shfl_sync(0xffffffffu, row, 8 * t);
+                    rowf[nr][1] = __shfl_sync(0xffffffffu, row, 8 * t + 4);
+                }
+            }
+            Walk nx = wk;
+            nx.next(p, hr);
+            if (AHEAD && nx.left > 0) load_q(nx, rt, raw);
+            // ---- the granules: every KW-th one
+            int slot = slot0 + kw, use = use0;
+            for (int gi = kw; gi < cnt && kw < KW; gi += KW, slot += KW) {
+                while (slot >= p.slots) {
+                    slot -= p.slots;
+                    ++use;
+                }
+                // The slot's granule before this one may be another warp's and may
+                // land later than this warp's last one: a wait for this use's copy
+                // is only good once that use is over, or its parity is the one
+                // of two uses ago.
+                bool got = use == 0 || mbar_wait(&empty[slot], (use - 1) & 1, &abort_flag);
+                got = got && mbar_wait(&full[slot], use & 1, &abort_flag);
+                if (!got) {
+                    abort_flag = 1;
+                    if (lane == 0) raise_status(p.ws, SPEC_DEV_TIMEOUT);
+                }
+                __syncwarp();
+                const int kb = (first + gi) * GK;
+                const uint32_t have = flags[slot];
+#pragma unroll 1
+                for (int h0 = 0; h0 < A::NSUB; h0 += NS)
+                    products(kb, h0, slot, have, lim_min, lim_max);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&empty[slot]);
+            }
+            slot0 += cnt % p.slots;
+            use0 += cnt / p.slots;
+            if (slot0 >= p.slots) {
+                slot0 -= p.slots;
+                ++use0;
+            }
+            // ---- the segment's end
+            b = wk.b;
+            seg = wk.seg;
+            n = wk.rq.n;
+            whole = cnt == wk.rq.ng;
+            if (!whole) {
+                c0 = own_c0, c1 = own_c1;
+                int shift = 0;
+                if (c0 < 0) {
+                    const int s0 = gpos - wk.at;
+                    c0 = deal.owner(s0 + wk.ov);
+                    c1 = deal.owner(s0 + wk.ov + wk.rq.ng - 1);
+                    shift = s0 > deal.start(c0);
+                }
+                at = 2 * cta + (cta == c0 ? shift : 0);
+                which = gpos != g0;
+                if (tid == 0) {
+                    Pend& pe = pend[which];
+                    pe.b = b;
+                    pe.seg = seg;
+                    pe.n = n;
+                    pe.c0 = c0;
+                    pe.c1 = c1;
+                    pe.shift = shift;
+                }
+            }
             gpos += wk.take();
-            wk.next(p, hr);
-            if (AHEAD && wk.left > 0) load_q(wk, rt, raw);
-            continue;
-        }
-        // ---- limits and Q of this warp's rows
-        int lim_min = 0, lim_max = 0;
-        if (row0 < wk.rq.n * p.G) {
-            const int last = min(row0 + rows_tile, wk.rq.n * p.G) - 1;
-            lim_min = min(wk.rq.L + p.tok(row0) + 1, cap);
-            lim_max = min(wk.rq.L + p.tok(last) + 1, cap);
-        }
-        if constexpr (QS) {
-            // the warps make a column tile each (they are past the last
-            // segment's products: its joining had barriers)
-            for (int tile = warp; tile < p.rtc * NR; tile += W) {
-                float row;
-                uint32_t qt[A::QT][A::KCH][A::QR];
-                load_q(wk, tile, raw);
-                make_q(raw, qt, row);
-#pragma unroll
-                for (int j = 0; j < A::KCH; ++j)
-#pragma unroll
-                    for (int i = 0; i < A::QR / 2; ++i)
-                        qs[((tile * A::KCH + j) * (A::QR / 2) + i) * 32 + lane] =
-                            make_uint2(qt[0][j][2 * i], qt[0][j][2 * i + 1]);
-                if (t == 0) qsf[tile * 8 + g] = row;
-            }
-            bar();
-        } else {
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-                float row;
-                if (!AHEAD) load_q(wk, rt * NR + nr, raw);
-                make_q(raw, qf[nr], row);
-                // lane (g, t) made row g; it needs rows 2t and 2t + 1
-                rowf[nr][0] = __shfl_sync(0xffffffffu, row, 8 * t);
-                rowf[nr][1] = __shfl_sync(0xffffffffu, row, 8 * t + 4);
-            }
-        }
-        Walk nx = wk;
-        nx.next(p, hr);
-        if (AHEAD && nx.left > 0) load_q(nx, rt, raw);
-        // ---- the granules: every KW-th one
-        int slot = slot0 + kw, use = use0;
-        for (int gi = kw; gi < cnt && kw < KW; gi += KW, slot += KW) {
-            while (slot >= p.slots) {
-                slot -= p.slots;
-                ++use;
-            }
-            // The slot's granule before this one may be another warp's and may
-            // land later than this warp's last one: a wait for this use's copy
-            // is only good once that use is over, or its parity is the one
-            // of two uses ago.
-            bool got = use == 0 || mbar_wait(&empty[slot], (use - 1) & 1, &abort_flag);
-            got = got && mbar_wait(&full[slot], use & 1, &abort_flag);
-            if (!got) {
-                abort_flag = 1;
-                if (lane == 0) raise_status(p.ws, SPEC_DEV_TIMEOUT);
-            }
-            __syncwarp();
-            const int kb = (first + gi) * GK;
-            const uint32_t have = flags[slot];
-            if (have != 0 && kb < lim_max) granule(kb, slot, have, lim_min, lim_max);
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&empty[slot]);
-        }
-        slot0 += cnt % p.slots;
-        use0 += cnt / p.slots;
-        if (slot0 >= p.slots) {
-            slot0 -= p.slots;
-            ++use0;
-        }
-        // ---- the segment's end
-        b = wk.b;
-        seg = wk.seg;
-        n = wk.rq.n;
-        whole = cnt == wk.rq.ng;
-        if (!whole) {
-            c0 = own_c0, c1 = own_c1;
-            int shift = 0;
-            if (c0 < 0) {
-                const int s0 = gpos - wk.at;
-                c0 = deal.owner(s0 + wk.ov);
-                c1 = deal.owner(s0 + wk.ov + wk.rq.ng - 1);
-                shift = s0 > deal.start(c0);
-            }
-            at = 2 * cta + (cta == c0 ? shift : 0);
-            which = gpos != g0;
-            if (tid == 0) {
-                Pend& pe = pend[which];
-                pe.b = b;
-                pe.seg = seg;
-                pe.n = n;
-                pe.c0 = c0;
-                pe.c1 = c1;
-                pe.shift = shift;
-            }
-        }
-        gpos += wk.take();
-        wk = nx;
+            wk = nx;
         } else {
             // ---- out of granules: the segments whose last part was this CTA's
             bar();                                       // pend is there
@@ -1405,7 +1424,8 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     // at most every granule of a full table
-    const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * (((int64_t)c.max_pages * c.page + A::GK - 1) / A::GK);
+    const int64_t per_seg = ((int64_t)c.max_pages * c.page + A::GK - 1) / A::GK;
+    const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * per_seg;
     const int grid = (int)(most < sms ? most : sms);
     return launch_k(false, kern, dim3(grid), dim3(32 * (W + 1)), smem, st, mk, mv, p);
 }
@@ -1413,8 +1433,6 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
 template <int IO, int KV, int D>
 cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
                    const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
-    // one more warp issues the copies: 16 or 8 in all share the registers
-    // evenly (128 or 255 each); row tiles in a CTA must divide the warps
     // Up to eight rows: seven key warps and the producer with up to 255 registers
     // each.  More: ten with 168, Q in shared memory (8 requests x 32 rows, 8-bit
     // cache: 49.7 us; seven with 255: 59.9).  In fp32 a granule at D = 128 is 32

@@ -282,7 +282,8 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     // ---- the race over this slice of the row where the chain ended
     const float m = row_m[kept], s = row_s[kept], inv = 1.0f / s;
     const T* lp = logits + ((size_t)b * (N + 1) + kept) * V;
-    const float* qp = kept < n && a.draft_prob ? a.draft_prob + ((size_t)b * N + kept) * V : nullptr;
+    const float* qp =
+        kept < n && a.draft_prob ? a.draft_prob + ((size_t)b * N + kept) * V : nullptr;
     const int point = kept < n && !a.draft_prob ? draft[kept] : -1;
     // Scores w / e by the approximate reciprocal; the thread keeps the weight and
     // exponential of its best, and where two scores are nearer than that
@@ -320,7 +321,8 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
                 xu[j][0] = __ldg(src);
                 if constexpr (IO == SPEC_IO_F32) xu[j][1] = __ldg(src + 1);
                 if (qp) {
-                    *reinterpret_cast<float4*>(q[j]) = __ldg(reinterpret_cast<const float4*>(qp + v));
+                    *reinterpret_cast<float4*>(q[j]) =
+                        __ldg(reinterpret_cast<const float4*>(qp + v));
                     *reinterpret_cast<float4*>(q[j] + 4) =
                         __ldg(reinterpret_cast<const float4*>(qp + v + 4));
                 }
@@ -385,7 +387,8 @@ cudaError_t verify_t(const spec_draft_cfg& c, const int32_t* n_draft, const void
                      RaceArgs a, const DraftWs& w, cudaStream_t st) {
     const int64_t ctas = (int64_t)c.B * (c.N + 1) * w.splits;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch_k(false, row_mass<IO>, dim3((unsigned)ctas), dim3(NT), 0, st, c, n_draft, static_cast<const typename io_t<IO>::T*>(logits), a.k,
+    cudaError_t e = launch_k(false, row_mass<IO>, dim3((unsigned)ctas), dim3(NT), 0, st, c,
+                             n_draft, static_cast<const typename io_t<IO>::T*>(logits), a.k,
                              ws_ptr<float2>(a.ws, w.part_off), w.splits);
     if (e != cudaSuccess) return e;
     return launch_k(true, race<IO>, dim3(w.slices, c.B), dim3(NT), 0, st, c, a);

@@ -26,7 +26,8 @@ template <int IO, int D> struct geo {
 };
 
 template <int IO>
-__device__ __forceinline__ void unpack(const uint4& u, float (&x)[16 / sizeof(typename io_t<IO>::T)]) {
+__device__ __forceinline__ void unpack(const uint4& u,
+                                       float (&x)[16 / sizeof(typename io_t<IO>::T)]) {
     if constexpr (IO == SPEC_IO_F32) {
         x[0] = __uint_as_float(u.x);
         x[1] = __uint_as_float(u.y);
@@ -128,7 +129,8 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
             for (int o = G::LPR / 2; o > 0; o >>= 1)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float amax = __uint_as_float(top);
-            float scale = top == 0u ? 1.0f : fmaxf(quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-100f);
+            float scale = fmaxf(quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-100f);
+            if (top == 0u) scale = 1.0f;
             if (top >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
             // where the remainder underflows the code is 0 whatever it is
             const float inv = __frcp_rn(scale);
@@ -146,7 +148,8 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
                         << 16);
             if (dst[j] >= 0) {
                 if constexpr (G::VEC == 8)
-                    reinterpret_cast<uint2*>(pages)[dst[j] * G::LPR + lane] = make_uint2(c[0], c[1]);
+                    reinterpret_cast<uint2*>(pages)[dst[j] * G::LPR + lane] =
+                        make_uint2(c[0], c[1]);
                 else
                     reinterpret_cast<uint32_t*>(pages)[dst[j] * G::LPR + lane] = c[0];
                 if (lane == 0) (is_v ? v_scale : k_scale)[dst[j]] = scale;
@@ -257,9 +260,9 @@ cudaError_t append_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const voi
     RowArgs a;
     const cudaError_t e = row_args<IO, D>(c, kv, c.T, a);
     if (e != cudaSuccess) return e;
-    return launch_k(false, append_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT), 0,
-                    st, a, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), n_new,
-                    kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, ws);
+    return launch_k(false, append_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT),
+                    0, st, a, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
+                    n_new, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, ws);
 }
 
 template <int IO, int KV, int D>
@@ -268,8 +271,8 @@ cudaError_t read_t(const spec_paged_cfg& c, const spec_paged_kv& kv, int Lmax, v
     RowArgs a;
     const cudaError_t e = row_args<IO, D>(c, kv, Lmax, a);
     if (e != cudaSuccess) return e;
-    return launch_k(false, read_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT), 0, st,
-                    a, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, static_cast<uint4*>(k_out),
+    return launch_k(false, read_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT), 0,
+                    st, a, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, static_cast<uint4*>(k_out),
                     static_cast<uint4*>(v_out), ws);
 }
 

@@ -32,7 +32,7 @@ def calls(lib, cfg, kv=None, n_new=None, x=P, ws=P, Lmax=8):
 
 
 @pytest.mark.parametrize("field,value", [
-    ("B", 0), ("B", 4097), ("T", 0), ("T", 1 << 21), ("Hq", 7), ("Hkv", 0), ("D", 96), ("D", 256),
+    ("B", 0), ("B", 4097), ("Hkv", 2048), ("T", 0), ("T", 1 << 21), ("Hq", 7), ("Hkv", 0), ("D", 96), ("D", 256),
     ("page", 8), ("page", 48), ("page", 2048), ("n_pages", 0), ("max_pages", 0),
     ("max_pages", 1 << 26), ("io_dtype", 5), ("kv_dtype", 2)])
 def test_paged_shapes_are_refused(lib, field, value):
@@ -55,9 +55,11 @@ def test_paged_pointers_are_refused(lib):
     assert calls(lib, cfg, Lmax=0)[1] == binding.ST_EINVAL
     n = calls(lib, cfg, n_new=ctypes.c_void_p(4))
     assert n[0] == n[2] == binding.ST_EINVAL
-    long = binding.paged_cfg(**dict(GOOD, T=129))
-    assert lib.attn_decode_paged(ctypes.byref(long), ctypes.byref(binding.SpecPagedKV(*([16] * 6))),
-                                 P, None, P, P, None) == binding.ST_EINVAL
+    kv = ctypes.byref(binding.SpecPagedKV(*([16] * 6)))
+    for bad in (dict(T=129), dict(T=128, Hq=2048, Hkv=2),         # rows of a kv-head
+                dict(B=4096, Hq=1024, Hkv=1024, max_pages=1 << 20)):   # granules in 32 bits
+        long = binding.paged_cfg(**dict(GOOD, **bad))
+        assert lib.attn_decode_paged(ctypes.byref(long), kv, P, None, P, P, None) == binding.ST_EINVAL
 
 
 def test_workspace_sizes_are_host_only(lib):

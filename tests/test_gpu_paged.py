@@ -269,6 +269,43 @@ def test_one_long_request(kv):
     x.check(x.attend())
 
 
+@pytest.mark.parametrize("B", [33, 300, 600])
+@pytest.mark.parametrize("kv", ["e4m3", "io"])
+def test_many_requests(B, kv):
+    """Beyond 32 requests the block finds its share (several lengths per thread
+    beyond its threads); some requests have no new row."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 90, B).tolist()
+    lens[B // 2] = 700
+    x = Case(lens, T=2, Hq=4, Hkv=2, D=64, page=16, kv=kv, seed=B, max_pages=45,
+             n_new=rng.integers(0, 3, B).tolist())
+    x.check(x.attend())
+    assert x.status() == 0
+
+
+def test_the_most_new_tokens_and_the_largest_pages():
+    x = Case([900, 3], T=128, Hq=6, Hkv=2, D=64, page=1024, kv="e4m3", seed=63, n_new=[128, 100])
+    x.check(x.attend())
+    x = Case([5, 1023, 1024, 2000], T=1, Hq=16, Hkv=1, D=128, page=1024, kv="io", seed=64)
+    x.check(x.attend())
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each with its own workspace; the results are those of one after the other."""
+    xs = [Case([3000, 50], T=1, Hq=8, Hkv=8, D=128, page=64, kv="e4m3", seed=70 + i) for i in range(2)]
+    want = [x.attend() for x in xs]
+    qs, ns = [x.dev(x.q) for x in xs], [x.n_dev() for x in xs]
+    outs = [torch.zeros_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, q, n, o, st in zip(xs, qs, ns, outs, streams):
+            binding.attn_decode_paged(x.cfg, x.kv, q, o, x.ws, n_new=n, stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
 @pytest.mark.parametrize("io,kv,D", [("bf16", "e4m3", 128), ("bf16", "io", 64), ("bf16", "io", 128),
                                      ("f32", "io", 64)])
 def test_many_granules_per_cta(io, kv, D):
