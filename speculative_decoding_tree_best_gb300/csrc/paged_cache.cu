@@ -55,6 +55,12 @@ __device__ __forceinline__ float quotient(float x, float y, float r) {
     return fmaf(fmaf(-q, y, x), r, q);
 }
 
+// two quotients by the same y
+__device__ __forceinline__ float2 quotients(float2 x, float y, float r) {
+    const float2 r2 = make_float2(r, r), q = __fmul2_rn(x, r2);
+    return __ffma2_rn(__ffma2_rn(q, make_float2(-y, -y), x), r2, q);
+}
+
 // The rows of one request, (token, head) in memory order, are cut into blocks of
 // RPC rows, one to a CTA; a thread has UNR rows of its block, all under way
 // at once.
@@ -108,51 +114,67 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
         }
     }
     void* pages = is_v ? v_pages : k_pages;
+    if constexpr (KV == SPEC_KV_IO) {
 #pragma unroll
-    for (int j = 0; j < UNR; ++j) {
-        if constexpr (KV == SPEC_KV_IO) {
+        for (int j = 0; j < UNR; ++j)
             if (dst[j] >= 0) reinterpret_cast<uint4*>(pages)[dst[j] * G::LPR + lane] = u[j];
-        } else {
-            // the row's largest magnitude as an integer: bit patterns of
-            // magnitudes order like the numbers, infinities and NaN on top
-            uint32_t top;
+    } else {
+        // the largest magnitudes as integers: bit patterns of magnitudes order
+        // like the numbers, infinities and NaN on top
+        uint32_t top[UNR];
+#pragma unroll
+        for (int j = 0; j < UNR; ++j) {
             const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
             if constexpr (IO == SPEC_IO_F32) {
-                top = max(max(w[0] & 0x7fffffffu, w[1] & 0x7fffffffu),
-                          max(w[2] & 0x7fffffffu, w[3] & 0x7fffffffu));
+                top[j] = max(max(w[0] & 0x7fffffffu, w[1] & 0x7fffffffu),
+                             max(w[2] & 0x7fffffffu, w[3] & 0x7fffffffu));
             } else {
                 const uint32_t y = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                                             __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-                top = max(y << 16, y & 0xffff0000u);
+                top[j] = max(y << 16, y & 0xffff0000u);
             }
+        }
+        // The thread's four rows are reduced together: lanes whose number ends in
+        // binary 00, 10, 01, 11 keep rows 0 to 3, so that one exchange serves two
+        // rows and every lane makes one scale instead of four.
+        static_assert(UNR == 4);
+        const bool o1 = lane & 1, o2 = lane & 2;
+        uint32_t k0 = o1 ? top[2] : top[0], k1 = o1 ? top[3] : top[1];
+        k0 = max(k0, __shfl_xor_sync(0xffffffffu, o1 ? top[0] : top[2], 1));
+        k1 = max(k1, __shfl_xor_sync(0xffffffffu, o1 ? top[1] : top[3], 1));
+        uint32_t most = max(o2 ? k1 : k0, __shfl_xor_sync(0xffffffffu, o2 ? k0 : k1, 2));
 #pragma unroll
-            for (int o = G::LPR / 2; o > 0; o >>= 1)
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float amax = __uint_as_float(top);
-            float scale = fmaxf(quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-100f);
-            if (top == 0u) scale = 1.0f;
-            if (top >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
-            // where the remainder underflows the code is 0 whatever it is
-            const float inv = __frcp_rn(scale);
+        for (int o = 4; o < G::LPR; o <<= 1)
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const float amax = __uint_as_float(most);
+        float scale = fmaxf(quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-100f);
+        if (most == 0u) scale = 1.0f;
+        if (most >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
+        const int64_t at = o1 ? (o2 ? dst[3] : dst[2]) : (o2 ? dst[1] : dst[0]);
+        if (lane < 4 && at >= 0) (is_v ? v_scale : k_scale)[at] = scale;
+        // where the remainder underflows the code is 0 whatever it is
+        const float inv = __frcp_rn(scale);
+#pragma unroll
+        for (int j = 0; j < UNR; ++j) {
+            const int from = 2 * (j & 1) + j / 2;
+            const float sj = __shfl_sync(0xffffffffu, scale, from, G::LPR);
+            const float rj = __shfl_sync(0xffffffffu, inv, from, G::LPR);
             float x[G::VEC];
             unpack<IO>(u[j], x);
-#pragma unroll
-            for (int k = 0; k < G::VEC; ++k) x[k] = quotient(x[k], scale, inv);
             uint32_t c[G::VEC / 4];
 #pragma unroll
-            for (int k = 0; k < G::VEC / 4; ++k)
-                c[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[4 * k], x[4 * k + 1]),
-                                                          __NV_SATFINITE, __NV_E4M3) |
-                       ((uint32_t)__nv_cvt_float2_to_fp8x2(
-                            make_float2(x[4 * k + 2], x[4 * k + 3]), __NV_SATFINITE, __NV_E4M3)
-                        << 16);
+            for (int k = 0; k < G::VEC / 4; ++k) {
+                const float2 lo = quotients(make_float2(x[4 * k], x[4 * k + 1]), sj, rj);
+                const float2 hi = quotients(make_float2(x[4 * k + 2], x[4 * k + 3]), sj, rj);
+                c[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                       ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
+            }
             if (dst[j] >= 0) {
                 if constexpr (G::VEC == 8)
                     reinterpret_cast<uint2*>(pages)[dst[j] * G::LPR + lane] =
                         make_uint2(c[0], c[1]);
                 else
                     reinterpret_cast<uint32_t*>(pages)[dst[j] * G::LPR + lane] = c[0];
-                if (lane == 0) (is_v ? v_scale : k_scale)[dst[j]] = scale;
             }
         }
     }
