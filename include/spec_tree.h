@@ -499,7 +499,7 @@ enum {
  * 1 <= T <= 2^20; Hkv <= 1024; Hq % Hkv == 0; D in {64, 128};
  * page a power of two in [16, 1024]; n_pages, max_pages >= 1;
  * max_pages * page <= 2^30; B * max(Hq, Hkv) <= 2^24.  attn_decode_paged:
- * T <= 128, R = T Hq / Hkv <= 65536, and B Hkv ceil(R / 48) (max_pages page / 32 + 9)
+ * T <= 128, R = T Hq / Hkv <= 65536, and B Hkv ceil(R / 48) (3 max_pages page / 32 + 27)
  * < 2^31. */
 typedef struct spec_paged_cfg {
     int32_t B;               /* requests */

@@ -57,11 +57,10 @@ int attn_decode_paged(const spec_paged_cfg* cfg, const spec_paged_kv* kv, const 
     if (rc) return rc;
     if ((rc = spec::check_paged_kv(*cfg, kv))) return rc;
     if (cfg->T > SPEC_MAX_ROWS || (int64_t)cfg->T * (cfg->Hq / cfg->Hkv) > 65536) return ST_EINVAL;
-    // granules are counted in 32 bits
-    const int64_t per_req = ((int64_t)cfg->max_pages * cfg->page + 31) / 32;
+    // granules, each as often as a row group has tiles, are counted in 32 bits
+    const int64_t per_req = ((int64_t)cfg->max_pages * cfg->page + 31) / 32 * 3;
     const int64_t segs = (int64_t)cfg->Hkv * spec::paged_row_tiles(*cfg).rtg;
-    if (cfg->B * (per_req + 8) > 0x7fffffff / segs) return ST_EINVAL;
-
+    if (cfg->B * (per_req + 24) > 0x7fffffff / segs) return ST_EINVAL;
     if (!al16(q) || !al16(o) || !al16(ws) || (n_new && !al16(n_new))) return ST_EINVAL;
     return cuda_rc(spec::launch_attn_paged(*cfg, *kv, q, n_new, o, ws,
                                            static_cast<cudaStream_t>(stream)));

@@ -111,6 +111,10 @@ __device__ __forceinline__ void e4m3x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
         : "r"(x));
 }
 __device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+__device__ __forceinline__ void arrive_n(uint64_t* bar, int n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+                 : "memory");
+}
 // log2 of a scale; 0 counts as 2^-126, a NaN stays
 __device__ __forceinline__ float log2_scale(float x) {
     float y;
@@ -208,6 +212,16 @@ struct AttnParams {
     }
     __device__ __forceinline__ int hk(int seg) const { return rtg == 1 ? seg : seg / rtg; }
     __device__ __forceinline__ int rg(int seg) const { return rtg == 1 ? 0 : seg % rtg; }
+    // a segment's row tiles that have rows, with n new tokens; at least one
+    template <int NR> __device__ __forceinline__ int live(int n, int seg) const {
+        if constexpr (NR == 1) return 1;
+        const int rows = n * G - rg(seg) * rtc * 8 * NR;
+        return min(max((rows + 8 * NR - 1) / (8 * NR), 1), rtc);
+    }
+    // what a granule of such a request costs, in granules of one row tile
+    template <int NR> __device__ __forceinline__ int weight(int n) const {
+        return rtg == 1 ? live<NR>(n, 0) : 1;
+    }
 };
 
 // One request's lengths.
@@ -228,33 +242,45 @@ __device__ __forceinline__ Req request(const AttnParams& p, int b, uint32_t& bit
     return r;
 }
 
-// What a segment costs a CTA beside its granules (Q, joining, a part): about so
-// many granules' time.  Each segment is dealt out as if it began with them (24
-// requests, 8-bit cache, 1, 4, 6, 8, 12: 51.7, 48.9, 47.3, 47.2, 47.4 us).
-constexpr int OVERHEAD = 8;
+// What a segment costs a CTA beside its granules (Q, the warps' wait for the last
+// one, joining, a part), in units: each segment is dealt out as if it began
+// with them.  Up to eight rows, 24 requests, 8-bit cache, 1, 4, 6, 8, 12: 51.7,
+// 48.9, 47.3, 47.2, 47.4 us.  More rows, 8 requests of 4096-8192 keys, 8, 16, 20,
+// 26, 32: 42.6, 41.4, 41.2, 40.2, 40.5 us; of 256-1024 keys 8, 16, 24: 21.1, 22.9,
+// 24.8 us (segments are then cut to fewer CTAs), so that it goes by their length.
+template <int NR> __device__ __forceinline__ int overhead(int units, int nseg) {
+    return NR == 1 ? 8 : min(24, max(8, (int)((uint32_t)units / (4u * (uint32_t)nseg))));
+}
 
-// One pass over the segments of a CTA's share, in order.
-struct Walk {
+// One pass over the segments of a CTA's share, in order.  A segment is ov units,
+// then w for each granule; a granule is the share's that has its first unit.
+template <int NR> struct Walk {
     int b, seg;              // request, segment in the request
-    int at;                  // place in the segment, of its ov + rq.ng
+    int at;                  // place in the segment, of its ov + w rq.ng
     int left;                // of the share
-    int ov;
+    int ov, w;
     Req rq;
-    __device__ __forceinline__ int take() const { return min(ov + rq.ng - at, left); }
+    __device__ __forceinline__ int size() const { return NR == 1 ? ov + rq.ng : ov + w * rq.ng; }
+    __device__ __forceinline__ int take() const { return min(size() - at, left); }
+    __device__ __forceinline__ int granule(int unit) const {
+        const int x = max(0, unit - ov);
+        return NR == 1 || w == 1 ? x : (int)((uint32_t)(x + w - 1) / (uint32_t)w);
+    }
     // the granules of this portion: [pos, pos + count)
-    __device__ __forceinline__ int pos() const { return max(0, at - ov); }
-    __device__ __forceinline__ int count() const { return max(0, at + take() - ov) - pos(); }
+    __device__ __forceinline__ int pos() const { return granule(at); }
+    __device__ __forceinline__ int count() const { return granule(at + take()) - pos(); }
     __device__ __forceinline__ void next(const AttnParams& p, int hr) {
         const int c = take();
         left -= c;
         at += c;
-        if (at < ov + rq.ng || left <= 0) return;
+        if (at < size() || left <= 0) return;
         at = 0;
         if (++seg == hr) {
             seg = 0;
             ++b;
             uint32_t bits = 0;
             rq = request(p, b, bits);
+            w = p.template weight<NR>(rq.n);
         }
     }
 };
@@ -275,8 +301,8 @@ struct Deal {
 
 // CTAs to deal to: as many as there are, but a segment is not cut to less than
 // twice its overhead.
-__device__ __forceinline__ int cta_count(int units, int nseg, int most) {
-    return min(most, max(nseg, units / (2 * OVERHEAD)));
+__device__ __forceinline__ int cta_count(int units, int ov, int nseg, int most) {
+    return min(most, max(nseg, (int)((uint32_t)units / (2u * (uint32_t)ov))));
 }
 
 // A segment that this CTA shares with others: what joining its parts needs.
@@ -287,17 +313,17 @@ struct Pend {
 };
 
 // NR column tiles of 8 rows per warp; W key warps times row tiles; QS: Q in shared
-// memory instead of registers
-template <int IO, int KV, int D, int NR, int W, bool QS>
-__global__ void __launch_bounds__(32 * (W + 1), 1)
+// memory instead of registers; NP producer warps
+template <int IO, int KV, int D, int NR, int W, bool QS, int NP>
+__global__ void __launch_bounds__(32 * (W + NP), 1)
 attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
            const __grid_constant__ AttnParams p) {
     using A = At<IO, KV, D, NR>;
-    constexpr int NTH = 32 * (W + 1);
+    constexpr int NTH = 32 * (W + NP);
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[MAX_SLOTS], empty[MAX_SLOTS];
     __shared__ uint32_t flags[MAX_SLOTS];
-    __shared__ int wsum[W + 1];
+    __shared__ int wsum[W + NP];
     __shared__ int first_off, first_b;
     __shared__ Req first_rq;
     __shared__ volatile int abort_flag;
@@ -317,7 +343,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     }
     if (warp == W && lane < 2) tc::tma_prefetch_desc(lane ? &mv : &mk);
     for (int s = tid; s < p.slots; s += NTH) {
-        tc::mbar_init(&full[s], 1);
+        tc::mbar_init(&full[s], NP);
         tc::mbar_init(&empty[s], p.rtc);
         tc::fence_mbar_init();
     }
@@ -336,7 +362,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     //   aligned: few long segments: each gets CTAs of its own, by its length
     //            (no CTA then works, and joins, in two segments);
     //   else     the row of all segments, overheads included, is cut evenly.
-    Walk wk;
+    Walk<NR> wk;
     Deal deal;
     int g0 = 0, n_cta, units;
     int own_c0 = -1, own_c1 = -1;        // aligned: the segment's CTAs
@@ -345,18 +371,20 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     if (p.B <= 32) {
         Req rq{0, 0, 0};
         if (lane < p.B) rq = request(p, lane, bits);
-        const int granules = __reduce_add_sync(0xffffffffu, rq.ng) * hr;
+        const int cost = rq.ng * p.template weight<NR>(rq.n);
+        const int granules = __reduce_add_sync(0xffffffffu, cost) * hr;
         const int longest = __reduce_max_sync(0xffffffffu, rq.ng);
         const bool whole = nseg <= (int)gridDim.x && longest <= 64 / GK * (W / p.rtc);
         n_cta = min((int)gridDim.x, (granules + (1 << p.min_sh) - 1) >> p.min_sh);
         const bool aligned = !whole && 4 * nseg <= n_cta && granules < (1 << 22);
-        units = granules + nseg * OVERHEAD;
+        const int ov = overhead<NR>(granules, nseg);
+        units = granules + nseg * ov;
         // CTAs per segment of the lane's request, or its segment's units
-        int k = whole ? 1 : rq.ng + OVERHEAD;
+        int k = whole ? 1 : cost + ov;
         if (aligned)
-            k = 1 + (n_cta - nseg) * rq.ng / granules;
+            k = 1 + (n_cta - nseg) * cost / granules;
         else
-            n_cta = whole ? nseg : cta_count(units, nseg, gridDim.x);
+            n_cta = whole ? nseg : cta_count(units, ov, nseg, gridDim.x);
         if (lane >= p.B) k = 0;
         int incl = k * hr;
 #pragma unroll
@@ -378,7 +406,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const int off = want - (__shfl_sync(0xffffffffu, incl, b) - k * hr);
         wk.seg = (int)((uint32_t)off / (uint32_t)k);
         const int rest = off - wk.seg * k;
-        wk.ov = whole || aligned ? 0 : OVERHEAD;
+        wk.ov = whole || aligned ? 0 : ov;
+        wk.w = whole || aligned ? 1 : p.template weight<NR>(wk.rq.n);
         if (whole) {
             wk.at = 0;
             wk.left = wk.rq.ng;
@@ -399,7 +428,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         Req rq0{};
         for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
             rq0 = request(p, b, bits);
-            mine += (rq0.ng + OVERHEAD) * hr;
+            mine += rq0.ng * p.template weight<NR>(rq0.n) * hr;
         }
         int incl = mine;
 #pragma unroll
@@ -412,22 +441,26 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         int before = 0;
         units = 0;
 #pragma unroll
-        for (int w = 0; w <= W; ++w) {
+        for (int w = 0; w < W + NP; ++w) {
             const int x = wsum[w];
             if (w < warp) before += x;
             units += x;
         }
-        n_cta = cta_count(units, nseg, gridDim.x);
+        const int ov = overhead<NR>(units, nseg);
+        units += nseg * ov;
+        n_cta = cta_count(units, ov, nseg, gridDim.x);
         if (cta >= n_cta) return;
         deal = Deal(units, n_cta);
         g0 = deal.start(cta);
-        const int lo = before + incl - mine;
+        const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        const int lo = before + incl - mine + b0 * hr * ov;
+        mine += (b1 - b0) * hr * ov;
         if (g0 >= lo && g0 < lo + mine) {
             int at = lo;
             for (int b = tid * per;; ++b) {
                 uint32_t ignore = 0;
                 if (per > 1) rq0 = request(p, b, ignore);
-                const int c = (rq0.ng + OVERHEAD) * hr;
+                const int c = (rq0.ng * p.template weight<NR>(rq0.n) + ov) * hr;
                 if (g0 < at + c) {
                     first_b = b;
                     first_off = g0 - at;
@@ -441,22 +474,25 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         wk.b = first_b;
         wk.rq = first_rq;
         wk.left = deal.start(cta + 1) - g0;
-        wk.ov = OVERHEAD;
-        wk.seg = (int)((uint32_t)first_off / (uint32_t)(wk.rq.ng + OVERHEAD));
-        wk.at = first_off - wk.seg * (wk.rq.ng + OVERHEAD);
+        wk.ov = ov;
+        wk.w = p.template weight<NR>(wk.rq.n);
+        wk.seg = (int)((uint32_t)first_off / (uint32_t)wk.size());
+        wk.at = first_off - wk.seg * wk.size();
     }
     if (bits && cta == 0) raise_status(p.ws, bits);
     const int rows_tile = 8 * NR;
     const int cap = p.pm.cap();
 
-    if (warp == W) {
+    if (warp >= W) {
         // ---- producer: one granule per lane, SB lanes at a time; the page ids of 32
-        // granules are fetched at once.  Issuing costs this warp some 200 cycles
-        // a group and 40 a copy; a large group waits for as many free slots.
+        // granules are fetched at once.  Issuing costs this warp some 400 cycles
+        // a group and 85 a copy; a large group waits for as many free slots.
         // (2.2 GB of 8-bit cache: 32 keys a granule, groups of 1, 2, 4, 8: 621,
         // 452, 366, 334 us; 64 keys, groups of 1, 2, 4: 391, 329, 342.  bf16, 24
-        // requests, groups of 1, 2, 4, 8: 79, 77, 75.8, 78.8 us.)
-        constexpr int SB = A::Q8 ? 2 : 4;
+        // requests, groups of 1, 2, 4, 8: 79, 77, 75.8, 78.8 us.)  Of two
+        // producers one copies K, the other V.
+        constexpr int SB = A::Q8 && A::GK == 64 ? 2 : 4;
+        const bool do_k = NP == 1 || warp == W, do_v = NP == 1 || warp == W + 1;
         int slot0 = 0, use0 = 0;         // of the batch's first granule
         bool ok = true;
         uint32_t bad = 0;
@@ -503,10 +539,10 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     ok = __all_sync(0xffffffffu, got);
                     if (!ok) break;
                     if (turn) {
-                        flags[slot] = have;
+                        if (do_k) flags[slot] = have;
                         tc::mbar_arrive_expect_tx(
                             &full[slot],
-                            __popc(have) * (A::SLOT / A::NSUB + (A::Q8 ? 8 * SUB : 0)));
+                            __popc(have) * (A::SLOT / A::NSUB + (A::Q8 ? 8 * SUB : 0)) / NP);
 #pragma unroll
                         for (int h = 0; h < A::NSUB; ++h) {
                             if (page[h] < 0 || (h * SUB) % p.box != 0) continue;
@@ -515,10 +551,12 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                             uint8_t* kd = ring + (size_t)slot * A::SLOT + h * SUB * A::SW;
 #pragma unroll
                             for (int nb = 0; nb < A::NB; ++nb) {
-                                tc::tma_load_3d(kd + nb * GK * A::SW, &mk, &full[slot], nb * A::SW,
-                                                prow, page[h]);
-                                tc::tma_load_3d(kd + A::SLOT_KV + nb * GK * A::SW, &mv, &full[slot],
-                                                nb * A::SW, prow, page[h]);
+                                if (do_k)
+                                    tc::tma_load_3d(kd + nb * GK * A::SW, &mk, &full[slot],
+                                                    nb * A::SW, prow, page[h]);
+                                if (do_v)
+                                    tc::tma_load_3d(kd + A::SLOT_KV + nb * GK * A::SW, &mv,
+                                                    &full[slot], nb * A::SW, prow, page[h]);
                             }
                             if constexpr (A::Q8) {
                                 const int64_t row =
@@ -526,7 +564,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                                 float* sd = scales + slot * 2 * GK + h * SUB;
 #pragma unroll
                                 for (int v = 0; v < 2; ++v)
-                                    asm volatile(
+                                    if (v ? do_v : do_k) asm volatile(
                                         "cp.async.bulk.shared::cluster.global.mbarrier::"
                                         "complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                             smem_u32(sd + v * GK)),
@@ -569,8 +607,17 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     }
 
     // ---- consumers
-    // key warp kw of KW, row tile rt; warps beyond KW rtc only keep the barriers
-    const int rt = warp % p.rtc, kw = warp / p.rtc, KW = W / p.rtc;
+    // Key warp kw of KW, row tile rt: the segment's `live` tiles with rows share the
+    // warps.  Warps beyond KW live only keep the barriers.
+    int live = 1, rt = 0, kw = warp, KW = W;
+    auto roles = [&](int n, int seg) {
+        if constexpr (NR > 1) {
+            live = p.template live<NR>(n, seg);
+            rt = live == 1 ? 0 : warp % live;
+            kw = live == 1 ? warp : warp / live;
+            KW = W / live;
+        }
+    };
     const int g = lane / 4, t = lane % 4;
     const int kr = g ^ ((g & 1) << 2);                       // key row of fragment row g
     const int va = 2 * t, vb = (2 * t + 1) ^ 4;              // of fragment columns 2t, 2t + 1
@@ -619,11 +666,11 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
         bar();
 #pragma unroll 1
-        for (int task = warp; task < p.rtc * TPR; task += W) {
+        for (int task = warp; task < live * TPR; task += W) {
             const int rt2 = task / TPR, nr = task % TPR / (A::NT / 2);
             const int i = task % (A::NT / 2) * 2;
             const float4* s = buf + rt2 * JW + nr * (A::NT + 1) * 32 + lane;
-            const int step = p.rtc * JW;
+            const int step = live * JW;
             float4 x[W];
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
@@ -696,6 +743,17 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 }
             }
             if (bad) raise_status(p.ws, SPEC_DEV_RANGE);
+        }
+        if (NR > 1 && whole && live < p.rtc) {           // tiles without rows: zeros
+            constexpr int CH = D * (IO == SPEC_IO_F32 ? 4 : 2) / 16;
+            const int r0 = (p.rg(seg) * p.rtc + live) * rows_tile;
+            for (int x = tid; x < (p.rtc - live) * rows_tile * CH; x += 32 * W) {
+                const int r = r0 + x / CH, tok = p.tok(r);
+                if (tok >= p.T) break;
+                reinterpret_cast<uint4*>(p.o)[(((size_t)b * p.T + tok) * p.Hq + p.hk(seg) * p.G +
+                                               r - tok * p.G) * CH + x % CH] =
+                    make_uint4(0, 0, 0, 0);
+            }
         }
     };
 
@@ -1052,7 +1110,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     // 16 bytes at a time (rows the step does not have: zeros)
     constexpr int QB = IO == SPEC_IO_F32 ? 4 : 2;
     constexpr int RAW = D * QB / 64;                     // 16-byte pieces of a row per lane
-    auto load_q = [&](const Walk& w, int tile, uint4 (&raw)[RAW]) {
+    auto load_q = [&](const Walk<NR>& w, int tile, uint4 (&raw)[RAW]) {
         const int r = (p.rg(w.seg) * p.rtc * NR + tile) * 8 + g, i = p.tok(r);
         const bool real = i < p.T;
         const uint4* qp = reinterpret_cast<const uint4*>(
@@ -1143,9 +1201,10 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         size_t at = 0;
         clear();
         if (wk.left > 0) {
+            roles(wk.rq.n, wk.seg);
             const int row0 = (p.rg(wk.seg) * p.rtc + rt) * rows_tile;
             const int first = wk.pos(), cnt = wk.count();
-            if (cnt == 0) {                      // a segment's overhead alone
+            if (cnt == 0) {                      // units that are no granule's first
                 gpos += wk.take();
                 wk.next(p, hr);
                 if (AHEAD && wk.left > 0) load_q(wk, rt, raw);
@@ -1161,7 +1220,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             if constexpr (QS) {
                 // the warps make a column tile each (they are past the last
                 // segment's products: its joining had barriers)
-                for (int tile = warp; tile < p.rtc * NR; tile += W) {
+                for (int tile = warp; tile < live * NR; tile += W) {
                     float row;
                     uint32_t qt[A::QT][A::KCH][A::QR];
                     load_q(wk, tile, raw);
@@ -1186,7 +1245,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     rowf[nr][1] = __shfl_sync(0xffffffffu, row, 8 * t + 4);
                 }
             }
-            Walk nx = wk;
+            Walk<NR> nx = wk;
             nx.next(p, hr);
             if (AHEAD && nx.left > 0) load_q(nx, rt, raw);
             // ---- the granules: every KW-th one
@@ -1213,7 +1272,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 for (int h0 = 0; h0 < A::NSUB; h0 += NS)
                     products(kb, h0, slot, have, lim_min, lim_max);
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&empty[slot]);
+                // a slot is free after rtc arrivals, however many tiles are live
+                if (lane == 0) arrive_n(&empty[slot], rt == 0 ? p.rtc - live + 1 : 1);
             }
             slot0 += cnt % p.slots;
             use0 += cnt / p.slots;
@@ -1232,7 +1292,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 if (c0 < 0) {
                     const int s0 = gpos - wk.at;
                     c0 = deal.owner(s0 + wk.ov);
-                    c1 = deal.owner(s0 + wk.ov + wk.rq.ng - 1);
+                    c1 = deal.owner(s0 + wk.ov + (wk.rq.ng - 1) * (NR == 1 ? 1 : wk.w));
                     shift = s0 > deal.start(c0);
                 }
                 at = 2 * cta + (cta == c0 ? shift : 0);
@@ -1261,6 +1321,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             b = pe.b;
             seg = pe.seg;
             n = pe.n;
+            roles(n, seg);
             const int row0 = (p.rg(seg) * p.rtc + rt) * rows_tile;
             constexpr int STEP = NR == 1 ? 3 : 1;        // parts under way at once
 #pragma unroll 1
@@ -1313,7 +1374,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         finish(b, seg, n, whole, at);
-        if (!whole && warp < min(W, p.rtc * TPR)) {
+        if (!whole && warp < min(W, live * TPR)) {
             // each warp that wrote of the part counts itself in; the segment is
             // joined, when its CTA has no more granules, by who comes last.  (A
             // CTA's first part is counted in while it works on: the neighbour
@@ -1322,7 +1383,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             __syncwarp();
             if (lane == 0) {
                 uint32_t* tk = p.tickets + (size_t)b * hr + seg;
-                const uint32_t all = (uint32_t)(c1 - c0 + 1) * min(W, p.rtc * TPR);
+                const uint32_t all = (uint32_t)(c1 - c0 + 1) * min(W, live * TPR);
                 if (atomicAdd(tk, 1u) == all - 1) {
                     *tk = 0;                             // for the next call
                     pend[which].last = 1;
@@ -1370,7 +1431,7 @@ template <class A> bool pool_map(CUtensorMap* m, const spec_paged_cfg& c, const 
 
 constexpr int SMEM_MAX = 225 * 1024;     // of 227 KB, beside the static variables
 
-template <int IO, int KV, int D, int NR, int W, bool QS>
+template <int IO, int KV, int D, int NR, int W, bool QS, int NP>
 cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
                         const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
     using A = At<IO, KV, D, NR>;
@@ -1411,7 +1472,7 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     static_assert(fit >= W && fit >= 4, "the ring's waits need a slot per key warp");
     p.slots = fit < MAX_SLOTS ? fit : MAX_SLOTS;
     const int smem = fixed + p.slots * per_slot;
-    auto kern = attn_paged<IO, KV, D, NR, W, QS>;
+    auto kern = attn_paged<IO, KV, D, NR, W, QS, NP>;
     // once per device and kernel (the size is a constant of the kernel)
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
@@ -1427,7 +1488,7 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     const int64_t per_seg = ((int64_t)c.max_pages * c.page + A::GK - 1) / A::GK;
     const int64_t most = (int64_t)c.B * c.Hkv * w.rtg * per_seg;
     const int grid = (int)(most < sms ? most : sms);
-    return launch_k(false, kern, dim3(grid), dim3(32 * (W + 1)), smem, st, mk, mv, p);
+    return launch_k(false, kern, dim3(grid), dim3(32 * (W + NP)), smem, st, mk, mv, p);
 }
 
 template <int IO, int KV, int D>
@@ -1439,12 +1500,12 @@ cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void*
     // KB, and the ring must have a slot per key warp.
     constexpr bool big = At<IO, KV, D, 1>::SLOT > 16384;
     if (paged_row_tiles(c).nr == 1)
-        return attn_launch<IO, KV, D, 1, big ? 6 : 7, false>(c, kv, q, n_new, o, ws, st);
-    if constexpr (IO == SPEC_IO_BF16)
-        return attn_launch<IO, KV, D, 2, At<IO, KV, D, 2>::SLOT < 16384 ? 10 : 7, true>(
-            c, kv, q, n_new, o, ws, st);
+        return attn_launch<IO, KV, D, 1, big ? 6 : 7, false, 1>(c, kv, q, n_new, o, ws, st);
+    if constexpr (IO == SPEC_IO_BF16 && At<IO, KV, D, 2>::SLOT < 16384)
+        return attn_launch<IO, KV, D, 2, 10, true, 2>(c, kv, q, n_new, o, ws, st);
     else
-        return attn_launch<IO, KV, D, 2, big ? 5 : 7, false>(c, kv, q, n_new, o, ws, st);
+        return attn_launch<IO, KV, D, 2, big ? 5 : 7, IO == SPEC_IO_BF16, 1>(c, kv, q, n_new, o, ws,
+                                                                            st);
 }
 
 }  // namespace

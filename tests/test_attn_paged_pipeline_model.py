@@ -1,7 +1,9 @@
 """A CPU model of the ring protocol of the decode attention (csrc/attn_paged.cu):
-one producer that issues granule copies in order, a few at a time, into a ring
-of slots, and key warps that take the granules in turn (granule i of a segment
-portion by warp i mod KW; with several row tiles, one warp of each).  Copies
+a producer (or two, one for K and one for V) that issues granule copies in order,
+a few at a time, into a ring of slots, and key warps that take the granules in turn (granule i of a segment
+portion by warp i mod KW; with several row tiles, one warp of each).  A portion's
+tiles may be fewer than the CTA's: the warps are then shared out to those, and
+the first tile's warp arrives for the missing ones.  Copies
 land and warps work for random times, and mbarrier waits have the hardware's
 parity semantics.
 
@@ -27,10 +29,10 @@ class Bar:
     def __init__(self, count):
         self.count, self.pending, self.tx, self.n = count, count, 0, 0
 
-    def arrive(self, tx=0):
-        if self.pending == 0:
+    def arrive(self, tx=0, n=1):
+        if self.pending < n:
             raise Broken("an arrival more than the phase expects")
-        self.pending -= 1
+        self.pending -= n
         self.tx += tx
         self.check()
 
@@ -47,10 +49,11 @@ class Bar:
         return ok
 
 
-def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1, group=4):
+def run(portions, slots, warps, rtc, seed, guard=True, slow=0.1, group=4, producers=1):
+    """portions: (granules, row tiles with rows)"""
     rnd = random.Random(seed)
-    full, empty = [Bar(1) for _ in range(slots)], [Bar(rtc) for _ in range(slots)]
-    content, readers = [None] * slots, [0] * slots
+    full, empty = [Bar(producers) for _ in range(slots)], [Bar(rtc) for _ in range(slots)]
+    content, readers = [[None] * producers for _ in range(slots)], [0] * slots
     time, order, heap = 0, 0, []
 
     def at(dt, fn):
@@ -61,9 +64,9 @@ def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1, group=4):
     def latency(base):
         return base * (20 if rnd.random() < slow else 1) * rnd.uniform(0.5, 1.5)
 
-    def producer():
+    def producer(which):
         i = 0
-        for cnt in portions:
+        for cnt, _ in portions:
             for b in range(0, cnt, group):
                 batch = range(i + b, i + min(b + group, cnt))
                 for k in batch:
@@ -77,7 +80,7 @@ def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1, group=4):
                     full[s].arrive(tx=1)
 
                     def land(k=k, s=s):
-                        content[s] = k
+                        content[s][which] = k
                         full[s].tx -= 1
                         full[s].check()
                     at(latency(60), land)
@@ -86,10 +89,11 @@ def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1, group=4):
 
     arrived = [0] * len(portions)                # warps at each portion's end
 
-    def consumer(kw):
+    def consumer(warp):
         base = 0
-        for pn, cnt in enumerate(portions):
-            for gi in range(kw, cnt, kws):
+        for pn, (cnt, live) in enumerate(portions):
+            rt, kw, kws = warp % live, warp // live, warps // live
+            for gi in range(kw, cnt if kw < kws else 0, kws):
                 k = base + gi
                 s, use = k % slots, k // slots
                 if guard and use > 0:
@@ -97,20 +101,20 @@ def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1, group=4):
                         yield 1
                 while not full[s].passed(use):
                     yield 1
-                if content[s] != k:
+                if content[s] != [k] * producers:
                     raise Broken("another granule than the expected one")
                 readers[s] += 1
                 yield latency(40)
-                if content[s] != k:
+                if content[s] != [k] * producers:
                     raise Broken("a slot changed while it was read")
                 readers[s] -= 1
-                empty[s].arrive()
+                empty[s].arrive(n=rtc - live + 1 if rt == 0 else 1)
             base += cnt
             arrived[pn] += 1                     # the joining barrier of the segment
-            while arrived[pn] < kws * rtc:
+            while arrived[pn] < warps:
                 yield 1
 
-    roles = [producer()] + [consumer(kw) for kw in range(kws) for _ in range(rtc)]
+    roles = [producer(i) for i in range(producers)] + [consumer(w) for w in range(warps)]
     alive = len(roles)
 
     def step(r):
@@ -133,23 +137,26 @@ def run(portions, slots, kws, rtc, seed, guard=True, slow=0.1, group=4):
         raise Broken("deadlock")
 
 
-def portions_of(rnd):
-    return [rnd.choice([1, 3, 7, 17, 40, 70]) for _ in range(rnd.randint(1, 4))]
+def portions_of(rnd, rtc):
+    return [(rnd.choice([1, 3, 7, 17, 40, 70]), rnd.randint(1, rtc))
+            for _ in range(rnd.randint(1, 4))]
 
 
-@pytest.mark.parametrize("slots,kws,rtc,group", [
-    (12, 7, 1, 4), (11, 7, 1, 2), (23, 7, 1, 2), (24, 7, 1, 4), (6, 6, 1, 4), (10, 10, 1, 2),
-    (10, 5, 2, 2), (10, 3, 3, 4), (13, 3, 2, 4)])
-def test_ring(slots, kws, rtc, group):
+@pytest.mark.parametrize("slots,warps,rtc,group,producers", [
+    (12, 7, 1, 4, 1), (11, 7, 1, 2, 1), (23, 7, 1, 2, 1), (24, 7, 1, 4, 1), (6, 6, 1, 4, 1),
+    (10, 10, 1, 2, 1), (10, 10, 2, 2, 2), (10, 10, 3, 4, 2), (13, 7, 2, 4, 1), (11, 7, 3, 4, 1),
+    (14, 10, 3, 4, 2), (14, 10, 2, 4, 2)])
+def test_ring(slots, warps, rtc, group, producers):
     for seed in range(25):
-        run(portions_of(random.Random(seed)), slots, kws, rtc, seed, group=group)
+        run(portions_of(random.Random(seed), rtc), slots, warps, rtc, seed, group=group,
+            producers=producers)
 
 
 def test_a_wait_for_the_copy_alone_is_caught():
     caught = 0
     for seed in range(40):
         try:
-            run([200], 24, 15, 1, seed, guard=False, slow=0.2)
+            run([(200, 1)], 24, 15, 1, seed, guard=False, slow=0.2)
         except Broken:
             caught += 1
     assert caught > 0

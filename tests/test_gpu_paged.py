@@ -283,6 +283,20 @@ def test_many_requests(B, kv):
     assert x.status() == 0
 
 
+@pytest.mark.parametrize("io,kv,T,Hq,Hkv,D", [("bf16", "e4m3", 12, 8, 2, 128), ("bf16", "io", 8, 16, 4, 64),
+                                              ("f32", "io", 9, 8, 2, 64), ("bf16", "e4m3", 30, 8, 2, 64)])
+@pytest.mark.parametrize("B", [2, 12, 40])
+def test_requests_with_few_and_many_new_tokens(io, kv, T, Hq, Hkv, D, B):
+    """Row tiles without rows leave their warps to the others; requests are
+    dealt out by what they cost, in CTAs of their own, evenly cut, and beyond 32."""
+    rng = np.random.default_rng(B + T)
+    lens = rng.integers(0, 2500 if B < 40 else 500, B).tolist()
+    n = [T, 1] + rng.integers(0, T + 1, B - 2).tolist()
+    x = Case(lens, T=T, Hq=Hq, Hkv=Hkv, D=D, page=32, io=io, kv=kv, seed=B, n_new=n)
+    x.check(x.attend())
+    assert x.status() == 0
+
+
 def test_the_most_new_tokens_and_the_largest_pages():
     x = Case([900, 3], T=128, Hq=6, Hkv=2, D=64, page=1024, kv="e4m3", seed=63, n_new=[128, 100])
     x.check(x.attend())
