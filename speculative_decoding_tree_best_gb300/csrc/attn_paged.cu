@@ -39,10 +39,12 @@
 //
 // Measured (graph replays, bytes of K, V and scales over time): 8 x 131072 keys,
 // 8 kv-heads, 8 bits 326 us, 6.8 TB/s, the rate of a plain copy; 24 requests of
-// 1024-8192 keys bf16 72 us (6.2 TB/s), 8 bits 47 us (4.9 TB/s: two or three
-// segments a CTA, some 5000 cycles each of ends, joins and imbalance); one
-// request of 4096 keys bf16 10 us, of which reading is 2.5: launch, lengths,
-// page ids and copies follow one another, then parts are joined.
+// 1024-8192 keys bf16 72 us (6.2 TB/s), 8 bits 46 us (5.0 TB/s: two or three
+// segments a CTA, whose ends the ring does not hide); one request of 4096 keys
+// bf16 10 us, of which reading is 2.5: lengths, page ids and copies follow one
+// another (3000 cycles), then parts are counted in (2700) and joined (5500).  8
+// requests of 4096-8192 keys and 1-8 new tokens, 8 bits: 41 us (2.4 TB/s), by the
+// conversions and products, done for each 16 rows.
 #include <cuda.h>
 #include <math.h>
 
@@ -170,7 +172,7 @@ template <int IO, int KV, int D, int NR> struct At {
     static constexpr int QR = EPC / 2;                  // Q registers per chunk and part
     static constexpr int PT = F32 ? 3 : (Q8 && IO == SPEC_IO_BF16 ? 1 : 2); // parts of a weight
     // Keys per granule.  With few rows memory is the bound: 64 keys in 8 bits, so
-    // that issuing a granule's copies (about 40 cycles each, four of them) keeps
+    // that issuing a granule's copies (four of them, see the producer) keeps
     // ahead of it.  With more rows the products are, and 32 keys spread better.
     static constexpr int GK = Q8 && NR == 1 ? 64 : 32;
     static constexpr int NSUB = GK / SUB;
@@ -1495,8 +1497,10 @@ template <int IO, int KV, int D>
 cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* q,
                    const int32_t* n_new, void* o, void* ws, cudaStream_t st) {
     // Up to eight rows: seven key warps and the producer with up to 255 registers
-    // each.  More: ten with 168, Q in shared memory (8 requests x 32 rows, 8-bit
-    // cache: 49.7 us; seven with 255: 59.9).  In fp32 a granule at D = 128 is 32
+    // each (eight leave 168: 24 requests, 8-bit cache, 48.4 us against 46.4).  More:
+    // ten with 168, Q in shared memory (8 requests x 32 rows, 8-bit cache: 49.7
+    // us; seven with 255: 59.9), and a second producer, which the warps' number
+    // leaves registers for (43.8 -> 42.6 us).  In fp32 a granule at D = 128 is 32
     // KB, and the ring must have a slot per key warp.
     constexpr bool big = At<IO, KV, D, 1>::SLOT > 16384;
     if (paged_row_tiles(c).nr == 1)

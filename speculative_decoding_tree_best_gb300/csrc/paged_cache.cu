@@ -9,6 +9,12 @@
 // mantissa bits; a rounding is at most 2^-4 of a value (2^-10 scale below the
 // normal range).  The floor keeps 1 / scale in fp32's range.  Rows of zeros
 // take scale 1, rows with a non-finite value a NaN scale and NaN codes.
+//
+// What bounds it: reading or writing the flat tensors (2 bytes a value in bf16)
+// and the codes (1).  Measured (graph replays, D = 128, 8 kv-heads, bf16 and
+// 8-bit codes): 8 requests of 1024-8192 rows read back 33.9 us, 6.0 TB/s; 4
+// prompts of 1-4000 tokens written 13.1 us, 3.9 TB/s, bound by instructions
+// (exact quotients, maxima, packing); 24 single tokens 2.1 us, latency.
 #include <math.h>
 
 #include "paged.cuh"
