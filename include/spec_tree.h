@@ -609,7 +609,7 @@ size_t spec_draft_workspace_bytes(const spec_draft_cfg *cfg, int num_sms);
  *   [B][N][V] float >= 0, u [B][N] float (these may be NULL when N = 0);
  *   n_draft NULL (N each) or [B], in [0, N] (else clamped, SPEC_DEV_BADREQ);
  *   logits [B][N+1][V] io (rows beyond n_draft are not read);
- *   e [B][V] float > 0;
+ *   e [B][V] float > 0 (scores beyond fp32's range tie);
  *   kv_len, root_tok  NULL, or [B]: advanced by tau / replaced by the drawn token.
  * A draft outside [0, V) is refused (SPEC_DEV_BADTOK).  A row whose
  * probabilities are not finite (NaN or +inf logits, or all -inf) refuses its

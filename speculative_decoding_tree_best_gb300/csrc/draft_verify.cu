@@ -294,7 +294,9 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     // exponential of its best, and where two scores are nearer than that
     // reciprocal tells apart, the quotients decide.  (A division per token made
     // the race 45 instructions a token.)
-    float top_lo = 0.0f, top_hi = 0.0f, top_w = 0.0f, top_e = 1.0f;
+    // (top_lo is never 0: tokens without weight take no quotient.)  An exponential
+    // below 2^-126 has an infinite approximate score; quotients decide there too.
+    float top_lo = 0x1p-149f, top_hi = 0.0f, top_w = 0.0f, top_e = 1.0f;
     int top_i = NONE;
     auto score = [&](float x, float q, float ex, int v) {
         const float w = fmaf(ex2((x - m) * a.k), inv, -q);
@@ -302,7 +304,7 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex));
         const float s = w * r;
         bool more = s > top_hi;
-        if (!more && s > top_lo) more = w / ex > top_w / top_e;      // seldom
+        if (!more && s >= top_lo) more = w / ex > top_w / top_e;     // seldom
         if (more) {
             top_lo = s * (1.0f - 0x1p-20f);
             top_hi = s * (1.0f + 0x1p-20f);

@@ -139,10 +139,6 @@ cudaError_t launch_draft_verify(const spec_draft_cfg& c, const int32_t* draft_to
 
 // ---- device side ------------------------------------------------------------------
 
-// Element of a cache row: the I/O type, or an e4m3 code.
-template <int IO, int KV> struct kv_t { using T = typename io_t<IO>::T; };
-template <int IO> struct kv_t<IO, SPEC_KV_E4M3> { using T = uint8_t; };
-
 // What a paged kernel needs to find a row, by value.
 struct PageMap {
     const int32_t* table;
@@ -171,11 +167,6 @@ __device__ __forceinline__ int new_rows(const int32_t* n_new, int b, int T, uint
     const int n = n_new[b];
     if (n < 0 || n > T) bits |= SPEC_DEV_BADREQ;
     return n < 0 ? 0 : (n > T ? T : n);
-}
-
-__device__ __forceinline__ float e4m3_to_float(uint8_t x) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(x, __NV_E4M3);
-    return __half2float(__half(h));
 }
 
 }  // namespace spec

@@ -178,6 +178,24 @@ def test_ties_go_to_the_lowest_token():
     assert run(x)[0].out_tok.item() == 77
 
 
+def test_exponentials_below_the_normal_range():
+    """Scores of 2^110 and more, whose exponentials have no finite approximate
+    reciprocal, are told apart; equal ones go to the lowest token."""
+    x = make(3, 1, 4000, seed=14, spread=0.5)
+    x["e"][:] = 1.0
+    x["u"][:] = 1.0                                        # the draft is refused
+    x["q"][:] = 0.0
+    x["q"][:, 0, 0] = 1.0
+    x["toks"][:] = 0
+    pairs = [(8, 9), (100, 3000), (17, 2049)]
+    for b, at in enumerate(pairs):
+        x["e"][b, list(at)] = 2.0 ** -128
+        x["logits"][b, 0, list(at)] = (0.25, 1.5 if b < 2 else 0.25)
+    out, _ = run(x)
+    assert out.accept_len.tolist() == [1, 1, 1]
+    assert out.out_tok[:, 0].tolist() == [9, 3000, 17]
+
+
 def test_drafters_that_equal_the_target_at_the_draft():
     """Residuals that vanish: a refusal by u q = p exactly, with q = p
     everywhere but for the roundings, falls back to a token of p."""
