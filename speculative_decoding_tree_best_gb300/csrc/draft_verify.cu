@@ -110,6 +110,7 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
     const int row = blockIdx.x / splits, seg = blockIdx.x % splits;
     const int b = row / (c.N + 1), i = row % (c.N + 1);
     uint32_t ignore = 0;
+    pdl_wait();
     // the second launch may start: it waits for this one's results
     pdl_trigger();
     if (i > new_rows(n_draft, b, c.N, ignore)) return;
@@ -394,7 +395,7 @@ cudaError_t verify_t(const spec_draft_cfg& c, const int32_t* n_draft, const void
                      RaceArgs a, const DraftWs& w, cudaStream_t st) {
     const int64_t ctas = (int64_t)c.B * (c.N + 1) * w.splits;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch_k(false, row_mass<IO>, dim3((unsigned)ctas), dim3(NT), 0, st, c,
+    cudaError_t e = launch_k(true, row_mass<IO>, dim3((unsigned)ctas), dim3(NT), 0, st, c,
                              n_draft, static_cast<const typename io_t<IO>::T*>(logits), a.k,
                              ws_ptr<float2>(a.ws, w.part_off), w.splits);
     if (e != cudaSuccess) return e;

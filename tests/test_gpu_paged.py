@@ -431,6 +431,72 @@ def test_another_stream_and_a_captured_graph():
     x.check(o)
 
 
+@pytest.mark.parametrize("before", ["nothing", "copy", "fill", "kernel", "join"])
+def test_each_call_waits_for_what_comes_before(before):
+    """The launches may start before the one ahead of them ends: a chain of append,
+    attention and read-back follows copies, fills, kernels and other streams, in a
+    graph and out of it, and sees their results."""
+    x = Case([300, 70], T=2, Hq=8, Hkv=2, D=128, page=16, kv="e4m3", seed=31)
+    want = x.attend()
+    new = {n: torch.stack([torch.from_numpy(x.raw[n][b, L:L + 2]) for b, L in enumerate(x.lens)])
+           .to(torch.bfloat16).cuda() for n in ("k", "v")}
+    Lmax = 302
+    q, ns = x.dev(x.q), x.n_dev()
+    k, v, o = torch.zeros_like(new["k"]), torch.zeros_like(new["v"]), torch.zeros_like(want)
+    out = [torch.zeros((2, Lmax, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kept = [torch.zeros_like(out[0]) for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def chain():
+        cur = torch.cuda.current_stream()
+        if before == "copy":
+            k.copy_(new["k"]), v.copy_(new["v"])
+        elif before == "fill":
+            k.copy_(new["k"]), v.copy_(new["v"]), o.zero_()
+        elif before == "kernel":
+            torch.mul(new["k"], 1, out=k), torch.mul(new["v"], 1, out=v)
+        elif before == "join":
+            side.wait_stream(cur)
+            with torch.cuda.stream(side):
+                k.copy_(new["k"])
+            v.copy_(new["v"])
+            cur.wait_stream(side)
+        src = (new["k"], new["v"]) if before == "nothing" else (k, v)
+        binding.kv_page_append(x.cfg, x.kv, *src, x.ws, n_new=ns)
+        binding.attn_decode_paged(x.cfg, x.kv, q, o, x.ws, n_new=ns)
+        binding.kv_page_read(x.cfg, x.kv, *out, x.ws)
+        kept[0].copy_(out[0]), kept[1].copy_(out[1])
+
+    def spoil():
+        for t in (k, v, o, *out, *kept):
+            t.zero_()
+        for b, L in enumerate(x.lens):                     # the rows that append writes
+            for r in (L, L + 1):
+                pg = int(x.table[b][r // 16])
+                for pool in x.pools:
+                    pool.view(torch.uint8)[pg, :, r % 16] = 0x7f
+        torch.cuda.synchronize()
+
+    chain()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
+    read = [t.clone() for t in kept]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain()
+        chain()
+    for _ in range(5):
+        spoil()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and all(torch.equal(a, b) for a, b in zip(kept, read))
+        spoil()
+        chain()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and all(torch.equal(a, b) for a, b in zip(kept, read))
+    assert x.status() == 0
+
+
 def test_a_pool_beyond_32_bit_offsets():
     page, Hkv, D = 64, 8, 128
     n_pages = (1 << 32) // (page * Hkv * D) + 8            # more than 2^32 codes a pool
