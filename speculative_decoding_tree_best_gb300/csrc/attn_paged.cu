@@ -62,6 +62,9 @@ using tc::smem_u32;
 
 constexpr int SUB = 16;                // keys per product tile: the smallest page
 constexpr int MAX_RTC = 3;             // row tiles per CTA, at most (paged_row_tiles)
+// log2 of how far a weight may be above 1 (8 requests of drafts 40.6 -> 39.6 us, 24
+// requests e4m3 45.4 -> 45.1, 8 x 131072 keys 327.3 -> 325.8 against none)
+constexpr float SLACK = 8.0f;
 constexpr int MAX_SLOTS = 64;          // granules in a CTA's ring, at most
 
 // ---- instruction wrappers -------------------------------------------------------------
@@ -890,7 +893,10 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                             !((have >> (h0 + h)) & 1u))
                             x[nr][h][e] = -INFINITY;
         }
-        // the running maximum of what the V weights go by (fmaxf passes over a NaN)
+        // The running maximum of what the V weights go by (fmaxf passes over a NaN).
+        // It is brought up to date when a lane is above it by more than SLACK: the
+        // weights are then at most 2^SLACK, which fp16 holds, and most granules do
+        // without the shuffles.
         bool grow = false;
         float nm[NR][2];
 #pragma unroll
@@ -905,16 +911,17 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     else
                         y = fmaxf(y, fmaxf(x[nr][h][e], x[nr][h][2 + e]));
                 }
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
                 nm[nr][e] = fmaxf(m[nr][e], y);
-                grow |= nm[nr][e] > m[nr][e];
+                grow |= nm[nr][e] > m[nr][e] + SLACK;
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        nm[nr][e] = fmaxf(nm[nr][e], __shfl_xor_sync(0xffffffffu, nm[nr][e], d));
                     const float f = ex2(m[nr][e] - (nm[nr][e] == -INFINITY ? 0.0f : nm[nr][e]));
                     m[nr][e] = nm[nr][e];
                     l[nr][e] *= f;
