@@ -68,14 +68,14 @@ __device__ __forceinline__ float2 quotients(float2 x, float y, float r) {
 }
 
 // The rows of one request, (token, head) in memory order, are cut into blocks of
-// RPC rows, one to a CTA; a thread has UNR rows of its block, all under way
-// at once.
-constexpr int UNR = 4;
-
-template <int IO, int D> struct rows_of {
+// RPC rows, one to a CTA; a thread has R rows of its block, all under way at
+// once: writing, two of the keys' with the same two of the values' (a place is
+// looked up once for both); reading back, four of one of them.
+template <int IO, int D, int R> struct rows_of {
     static constexpr int PER = NT / geo<IO, D>::LPR;     // rows per pass of the block
-    static constexpr int RPC = UNR * PER;
+    static constexpr int RPC = R * PER;
 };
+constexpr int APPEND_ROWS = 2, READ_ROWS = 4;
 
 struct RowArgs {
     PageMap pm;
@@ -92,12 +92,11 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
             const uint4* __restrict__ v_new, const int32_t* __restrict__ n_new, void* k_pages,
             void* v_pages, float* k_scale, float* v_scale, void* ws) {
     using G = geo<IO, D>;
-    using R = rows_of<IO, D>;
+    using R = rows_of<IO, D, APPEND_ROWS>;
     const PageMap& pm = a.pm;
     pdl_wait();
     const int b = blockIdx.x / a.blocks, row0 = (blockIdx.x - b * a.blocks) * R::RPC;
     const int lane = threadIdx.x % G::LPR, mine = threadIdx.x / G::LPR;
-    const bool is_v = blockIdx.y != 0;
     const int tok0 = row0 / pm.Hkv, h0 = row0 - tok0 * pm.Hkv;
     uint32_t bits = 0;
     const int n = new_rows(n_new, b, a.T, bits);
@@ -105,32 +104,35 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
     if (L < 0 || L > pm.cap() - n) bits |= SPEC_DEV_OVERFLOW;
     if (bits && row0 == 0 && threadIdx.x == 0) raise_status(ws, bits);
     if ((bits & SPEC_DEV_OVERFLOW) || tok0 >= n) return;
-    const uint4* src = (is_v ? v_new : k_new) + ((size_t)b * a.T * pm.Hkv + row0) * G::LPR;
-    uint4 u[UNR];
-    int64_t dst[UNR];
+    const size_t base = ((size_t)b * a.T * pm.Hkv + row0) * G::LPR + lane;
+    uint4 u[4];                                          // key and value of a row in turn
+    int64_t dst[2];
 #pragma unroll
-    for (int j = 0; j < UNR; ++j) {
+    for (int j = 0; j < 2; ++j) {
         const int r = j * R::PER + mine, dt = a.token(h0 + r);
         const int i = tok0 + dt, h = h0 + r - dt * pm.Hkv;
         dst[j] = -1;
-        u[j] = make_uint4(0, 0, 0, 0);
+        u[2 * j] = u[2 * j + 1] = make_uint4(0, 0, 0, 0);
         if (i < n) {
-            u[j] = __ldg(src + r * G::LPR + lane);
+            u[2 * j] = __ldg(k_new + base + r * G::LPR);
+            u[2 * j + 1] = __ldg(v_new + base + r * G::LPR);
             dst[j] = pm.row(b, L + i, h);
             if (dst[j] < 0 && lane == 0) raise_status(ws, SPEC_DEV_BADPAGE);
         }
     }
-    void* pages = is_v ? v_pages : k_pages;
     if constexpr (KV == SPEC_KV_IO) {
 #pragma unroll
-        for (int j = 0; j < UNR; ++j)
-            if (dst[j] >= 0) reinterpret_cast<uint4*>(pages)[dst[j] * G::LPR + lane] = u[j];
+        for (int j = 0; j < 2; ++j)
+            if (dst[j] >= 0) {
+                reinterpret_cast<uint4*>(k_pages)[dst[j] * G::LPR + lane] = u[2 * j];
+                reinterpret_cast<uint4*>(v_pages)[dst[j] * G::LPR + lane] = u[2 * j + 1];
+            }
     } else {
         // the largest magnitudes as integers: bit patterns of magnitudes order
         // like the numbers, infinities and NaN on top
-        uint32_t top[UNR];
+        uint32_t top[4];
 #pragma unroll
-        for (int j = 0; j < UNR; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
             if constexpr (IO == SPEC_IO_F32) {
                 top[j] = max(max(w[0] & 0x7fffffffu, w[1] & 0x7fffffffu),
@@ -141,10 +143,9 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
                 top[j] = max(y << 16, y & 0xffff0000u);
             }
         }
-        // The thread's four rows are reduced together: lanes whose number ends in
-        // binary 00, 10, 01, 11 keep rows 0 to 3, so that one exchange serves two
-        // rows and every lane makes one scale instead of four.
-        static_assert(UNR == 4);
+        // The four are reduced together: lanes whose number ends in binary 00, 10,
+        // 01, 11 keep 0 to 3, so that one exchange serves two of them and every
+        // lane makes one scale instead of four.
         const bool o1 = lane & 1, o2 = lane & 2;
         uint32_t k0 = o1 ? top[2] : top[0], k1 = o1 ? top[3] : top[1];
         k0 = max(k0, __shfl_xor_sync(0xffffffffu, o1 ? top[0] : top[2], 1));
@@ -157,12 +158,12 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
         float scale = fmaxf(quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-100f);
         if (most == 0u) scale = 1.0f;
         if (most >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
-        const int64_t at = o1 ? (o2 ? dst[3] : dst[2]) : (o2 ? dst[1] : dst[0]);
-        if (lane < 4 && at >= 0) (is_v ? v_scale : k_scale)[at] = scale;
+        const int64_t at = o1 ? dst[1] : dst[0];
+        if (lane < 4 && at >= 0) (o2 ? v_scale : k_scale)[at] = scale;
         // where the remainder underflows the code is 0 whatever it is
         const float inv = __frcp_rn(scale);
 #pragma unroll
-        for (int j = 0; j < UNR; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const int from = 2 * (j & 1) + j / 2;
             const float sj = __shfl_sync(0xffffffffu, scale, from, G::LPR);
             const float rj = __shfl_sync(0xffffffffu, inv, from, G::LPR);
@@ -176,12 +177,13 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
                 c[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
                        ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
             }
-            if (dst[j] >= 0) {
+            if (dst[j / 2] >= 0) {
+                void* pages = j & 1 ? v_pages : k_pages;
                 if constexpr (G::VEC == 8)
-                    reinterpret_cast<uint2*>(pages)[dst[j] * G::LPR + lane] =
+                    reinterpret_cast<uint2*>(pages)[dst[j / 2] * G::LPR + lane] =
                         make_uint2(c[0], c[1]);
                 else
-                    reinterpret_cast<uint32_t*>(pages)[dst[j] * G::LPR + lane] = c[0];
+                    reinterpret_cast<uint32_t*>(pages)[dst[j / 2] * G::LPR + lane] = c[0];
             }
         }
     }
@@ -194,7 +196,7 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
           const float* __restrict__ v_scale, uint4* __restrict__ k_out, uint4* __restrict__ v_out,
           void* ws) {
     using G = geo<IO, D>;
-    using R = rows_of<IO, D>;
+    using R = rows_of<IO, D, READ_ROWS>;
     const PageMap& pm = a.pm;
     pdl_wait();
     const int b = blockIdx.x / a.blocks, row0 = (blockIdx.x - b * a.blocks) * R::RPC;
@@ -210,11 +212,11 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
     if (tok0 >= L) return;
     const void* pages = is_v ? v_pages : k_pages;
     constexpr int NW = KV == SPEC_KV_E4M3 ? G::VEC / 4 : 4;   // 32-bit words of a lane's piece
-    uint32_t w[UNR][NW];
-    float scale[UNR];
-    bool have[UNR];
+    uint32_t w[READ_ROWS][NW];
+    float scale[READ_ROWS];
+    bool have[READ_ROWS];
 #pragma unroll
-    for (int j = 0; j < UNR; ++j) {
+    for (int j = 0; j < READ_ROWS; ++j) {
         const int r = j * R::PER + mine, dt = a.token(h0 + r);
         const int i = tok0 + dt, h = h0 + r - dt * pm.Hkv;
         have[j] = i < L;
@@ -244,7 +246,7 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
     }
     uint4* dst = (is_v ? v_out : k_out) + ((size_t)b * a.T * pm.Hkv + row0) * G::LPR + lane;
 #pragma unroll
-    for (int j = 0; j < UNR; ++j) {
+    for (int j = 0; j < READ_ROWS; ++j) {
         if (!have[j]) continue;
         uint4 u;
         if constexpr (KV == SPEC_KV_IO) {
@@ -276,10 +278,11 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
 // any access to memory, and there is no early trigger, so that what follows needs
 // no such care.
 // cudaErrorInvalidConfiguration when the launch would need too many CTAs.
-template <int IO, int D>
+template <int IO, int D, int R>
 cudaError_t row_args(const spec_paged_cfg& c, const spec_paged_kv& kv, int64_t T, RowArgs& a) {
     const int64_t rows = T * c.Hkv;
-    const int64_t blocks = (rows + rows_of<IO, D>::RPC - 1) / rows_of<IO, D>::RPC;
+    const int rpc = rows_of<IO, D, R>::RPC;
+    const int64_t blocks = (rows + rpc - 1) / rpc;
     if (rows > 0x7fffffff - 4096 || blocks * c.B > 0x7fffffff) return cudaErrorInvalidConfiguration;
     a.pm = page_map(c, kv);
     a.T = (int)T;
@@ -292,9 +295,9 @@ template <int IO, int KV, int D>
 cudaError_t append_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* k_new,
                      const void* v_new, const int32_t* n_new, void* ws, cudaStream_t st) {
     RowArgs a;
-    const cudaError_t e = row_args<IO, D>(c, kv, c.T, a);
+    const cudaError_t e = row_args<IO, D, APPEND_ROWS>(c, kv, c.T, a);
     if (e != cudaSuccess) return e;
-    return launch_k(true, append_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT),
+    return launch_k(true, append_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B)), dim3(NT),
                     0, st, a, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
                     n_new, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, ws);
 }
@@ -303,7 +306,7 @@ template <int IO, int KV, int D>
 cudaError_t read_t(const spec_paged_cfg& c, const spec_paged_kv& kv, int Lmax, void* k_out,
                    void* v_out, void* ws, cudaStream_t st) {
     RowArgs a;
-    const cudaError_t e = row_args<IO, D>(c, kv, Lmax, a);
+    const cudaError_t e = row_args<IO, D, READ_ROWS>(c, kv, Lmax, a);
     if (e != cudaSuccess) return e;
     return launch_k(true, read_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT), 0,
                     st, a, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, static_cast<uint4*>(k_out),
