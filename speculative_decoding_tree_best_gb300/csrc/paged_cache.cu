@@ -13,8 +13,8 @@
 // What bounds it: reading or writing the flat tensors (2 bytes a value in bf16)
 // and the codes (1).  Measured (graph replays, D = 128, 8 kv-heads, bf16 and
 // 8-bit codes): 8 requests of 1024-8192 rows read back 33.9 us, 6.0 TB/s; 4
-// prompts of 1-4000 tokens written 13.1 us, 3.9 TB/s, bound by instructions
-// (exact quotients, maxima, packing); 24 single tokens 2.1 us, latency.
+// prompts of 1-4000 tokens written 11.6 us, 4.4 TB/s, bound by instructions
+// (exact quotients, maxima, packing); 24 single tokens 1.8 us, latency.
 #include <math.h>
 
 #include "paged.cuh"
@@ -68,14 +68,17 @@ __device__ __forceinline__ float2 quotients(float2 x, float y, float r) {
 }
 
 // The rows of one request, (token, head) in memory order, are cut into blocks of
-// RPC rows, one to a CTA; a thread has R rows of its block, all under way at
-// once: writing, two of the keys' with the same two of the values' (a place is
-// looked up once for both); reading back, four of one of them.
-template <int IO, int D, int R> struct rows_of {
+// RPC rows, one to a CTA; a thread has UNR rows of its block, of the keys and of
+// the values, all under way at once, and looks a row's place up once for both.
+// (Prompts written, 4 rows of one of them, 2 and 4 of both: 12.8, 11.6, 11.3 us;
+// single tokens 1.78, 1.76, 2.1; read back, one request of 4095 rows in bf16 5.4,
+// 5.2, 5.5, 8 requests in 8 bits 33.8, 33.9, 33.3, and with 1 of both 44.)
+constexpr int UNR = 2;
+
+template <int IO, int D> struct rows_of {
     static constexpr int PER = NT / geo<IO, D>::LPR;     // rows per pass of the block
-    static constexpr int RPC = R * PER;
+    static constexpr int RPC = UNR * PER;
 };
-constexpr int APPEND_ROWS = 2, READ_ROWS = 4;
 
 struct RowArgs {
     PageMap pm;
@@ -92,7 +95,7 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
             const uint4* __restrict__ v_new, const int32_t* __restrict__ n_new, void* k_pages,
             void* v_pages, float* k_scale, float* v_scale, void* ws) {
     using G = geo<IO, D>;
-    using R = rows_of<IO, D, APPEND_ROWS>;
+    using R = rows_of<IO, D>;
     const PageMap& pm = a.pm;
     pdl_wait();
     const int b = blockIdx.x / a.blocks, row0 = (blockIdx.x - b * a.blocks) * R::RPC;
@@ -105,10 +108,10 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
     if (bits && row0 == 0 && threadIdx.x == 0) raise_status(ws, bits);
     if ((bits & SPEC_DEV_OVERFLOW) || tok0 >= n) return;
     const size_t base = ((size_t)b * a.T * pm.Hkv + row0) * G::LPR + lane;
-    uint4 u[4];                                          // key and value of a row in turn
-    int64_t dst[2];
+    uint4 u[2 * UNR];                                          // key and value of a row in turn
+    int64_t dst[UNR];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < UNR; ++j) {
         const int r = j * R::PER + mine, dt = a.token(h0 + r);
         const int i = tok0 + dt, h = h0 + r - dt * pm.Hkv;
         dst[j] = -1;
@@ -122,7 +125,7 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
     }
     if constexpr (KV == SPEC_KV_IO) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < UNR; ++j)
             if (dst[j] >= 0) {
                 reinterpret_cast<uint4*>(k_pages)[dst[j] * G::LPR + lane] = u[2 * j];
                 reinterpret_cast<uint4*>(v_pages)[dst[j] * G::LPR + lane] = u[2 * j + 1];
@@ -143,6 +146,7 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
                 top[j] = max(y << 16, y & 0xffff0000u);
             }
         }
+        static_assert(UNR == 2);
         // The four are reduced together: lanes whose number ends in binary 00, 10,
         // 01, 11 keep 0 to 3, so that one exchange serves two of them and every
         // lane makes one scale instead of four.
@@ -196,12 +200,11 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
           const float* __restrict__ v_scale, uint4* __restrict__ k_out, uint4* __restrict__ v_out,
           void* ws) {
     using G = geo<IO, D>;
-    using R = rows_of<IO, D, READ_ROWS>;
+    using R = rows_of<IO, D>;
     const PageMap& pm = a.pm;
     pdl_wait();
     const int b = blockIdx.x / a.blocks, row0 = (blockIdx.x - b * a.blocks) * R::RPC;
     const int lane = threadIdx.x % G::LPR, mine = threadIdx.x / G::LPR;
-    const bool is_v = blockIdx.y != 0;
     const int tok0 = row0 / pm.Hkv, h0 = row0 - tok0 * pm.Hkv;
     int L = pm.kv_len[b];
     const int most = min(a.T, pm.cap());
@@ -210,13 +213,12 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
         L = L < 0 ? 0 : most;
     }
     if (tok0 >= L) return;
-    const void* pages = is_v ? v_pages : k_pages;
     constexpr int NW = KV == SPEC_KV_E4M3 ? G::VEC / 4 : 4;   // 32-bit words of a lane's piece
-    uint32_t w[READ_ROWS][NW];
-    float scale[READ_ROWS];
-    bool have[READ_ROWS];
+    uint32_t w[2 * UNR][NW];                       // key and value of a row in turn
+    float scale[2 * UNR];
+    bool have[UNR];
 #pragma unroll
-    for (int j = 0; j < READ_ROWS; ++j) {
+    for (int j = 0; j < UNR; ++j) {
         const int r = j * R::PER + mine, dt = a.token(h0 + r);
         const int i = tok0 + dt, h = h0 + r - dt * pm.Hkv;
         have[j] = i < L;
@@ -227,27 +229,33 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
             if (lane == 0) raise_status(ws, SPEC_DEV_BADPAGE);
             continue;
         }
-        if constexpr (KV == SPEC_KV_E4M3) {
-            scale[j] = __ldg((is_v ? v_scale : k_scale) + src);
-            if constexpr (NW == 2) {
-                const uint2 y = __ldg(reinterpret_cast<const uint2*>(pages) + src * G::LPR + lane);
-                w[j][0] = y.x;
-                w[j][1] = y.y;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const void* pages = v ? v_pages : k_pages;
+            uint32_t(&y)[NW] = w[2 * j + v];
+            if constexpr (KV == SPEC_KV_E4M3) {
+                scale[2 * j + v] = __ldg((v ? v_scale : k_scale) + src);
+                if constexpr (NW == 2) {
+                    const uint2 x =
+                        __ldg(reinterpret_cast<const uint2*>(pages) + src * G::LPR + lane);
+                    y[0] = x.x;
+                    y[1] = x.y;
+                } else {
+                    y[0] = __ldg(reinterpret_cast<const uint32_t*>(pages) + src * G::LPR + lane);
+                }
             } else {
-                w[j][0] = __ldg(reinterpret_cast<const uint32_t*>(pages) + src * G::LPR + lane);
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(pages) + src * G::LPR + lane);
+                y[0] = x.x;
+                y[1] = x.y;
+                y[NW - 2] = x.z;
+                y[NW - 1] = x.w;
             }
-        } else {
-            const uint4 y = __ldg(reinterpret_cast<const uint4*>(pages) + src * G::LPR + lane);
-            w[j][0] = y.x;
-            w[j][1] = y.y;
-            w[j][NW - 2] = y.z;
-            w[j][NW - 1] = y.w;
         }
     }
-    uint4* dst = (is_v ? v_out : k_out) + ((size_t)b * a.T * pm.Hkv + row0) * G::LPR + lane;
+    const size_t base = ((size_t)b * a.T * pm.Hkv + row0) * G::LPR + lane;
 #pragma unroll
-    for (int j = 0; j < READ_ROWS; ++j) {
-        if (!have[j]) continue;
+    for (int j = 0; j < 2 * UNR; ++j) {
+        if (!have[j / 2]) continue;
         uint4 u;
         if constexpr (KV == SPEC_KV_IO) {
             u = make_uint4(w[j][0], w[j][1], w[j][NW - 2], w[j][NW - 1]);
@@ -269,7 +277,7 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
                                pack_bf16(x[G::VEC - 4], x[G::VEC - 3]),
                                pack_bf16(x[G::VEC - 2], x[G::VEC - 1]));
         }
-        dst[(j * R::PER + mine) * G::LPR] = u;
+        (j & 1 ? v_out : k_out)[base + (j / 2 * R::PER + mine) * G::LPR] = u;
     }
 }
 
@@ -278,10 +286,10 @@ read_rows(const __grid_constant__ RowArgs a, const void* __restrict__ k_pages,
 // any access to memory, and there is no early trigger, so that what follows needs
 // no such care.
 // cudaErrorInvalidConfiguration when the launch would need too many CTAs.
-template <int IO, int D, int R>
+template <int IO, int D>
 cudaError_t row_args(const spec_paged_cfg& c, const spec_paged_kv& kv, int64_t T, RowArgs& a) {
     const int64_t rows = T * c.Hkv;
-    const int rpc = rows_of<IO, D, R>::RPC;
+    const int rpc = rows_of<IO, D>::RPC;
     const int64_t blocks = (rows + rpc - 1) / rpc;
     if (rows > 0x7fffffff - 4096 || blocks * c.B > 0x7fffffff) return cudaErrorInvalidConfiguration;
     a.pm = page_map(c, kv);
@@ -295,7 +303,7 @@ template <int IO, int KV, int D>
 cudaError_t append_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void* k_new,
                      const void* v_new, const int32_t* n_new, void* ws, cudaStream_t st) {
     RowArgs a;
-    const cudaError_t e = row_args<IO, D, APPEND_ROWS>(c, kv, c.T, a);
+    const cudaError_t e = row_args<IO, D>(c, kv, c.T, a);
     if (e != cudaSuccess) return e;
     return launch_k(true, append_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B)), dim3(NT),
                     0, st, a, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
@@ -306,9 +314,9 @@ template <int IO, int KV, int D>
 cudaError_t read_t(const spec_paged_cfg& c, const spec_paged_kv& kv, int Lmax, void* k_out,
                    void* v_out, void* ws, cudaStream_t st) {
     RowArgs a;
-    const cudaError_t e = row_args<IO, D, READ_ROWS>(c, kv, Lmax, a);
+    const cudaError_t e = row_args<IO, D>(c, kv, Lmax, a);
     if (e != cudaSuccess) return e;
-    return launch_k(true, read_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B), 2), dim3(NT), 0,
+    return launch_k(true, read_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B)), dim3(NT), 0,
                     st, a, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, static_cast<uint4*>(k_out),
                     static_cast<uint4*>(v_out), ws);
 }
