@@ -7,8 +7,9 @@
 // two parts a, b join as m = max(m_a, m_b), o = o_a 2^(m_a - m) + o_b 2^(m_b - m)).
 // In an 8-bit cache a value is code * scale per row: the key's scale multiplies
 // the score; the value's scale goes into the weight's exponent,
-// w'_k = 2^(x_k + log2 scale_k - m) with m the maximum over x_k + log2 scale_k,
-// so that the weights that meet the codes are at most 1 whatever the scales.
+// w'_k = 2^(x_k + log2 scale_k - m) with m the maximum over x_k + log2 scale_k
+// (up to a factor of 2^SLACK, below), so that the weights that meet the codes are
+// at most 2^SLACK whatever the scales.
 //
 // What bounds it: reading the cache, 2 D values a key and kv-head against
 // 4 D G T flops (G = Hq / Hkv), 2 G T flops a byte in bf16: far below the
@@ -33,17 +34,17 @@
 // Rounding.  Scores, weights, sums and outputs are fp32.  What the tensor cores
 // take is exact (cached values; bf16 q) or in parts: weights as two bf16 parts
 // (2^-16) over a bf16 cache, as one fp16 part over an 8-bit cache with bf16
-// outputs (2^-11, an eighth of the output's own rounding; they are at most 1),
+// outputs (2^-11, an eighth of the output's own rounding; they are at most 2^SLACK),
 // two fp16 parts with fp32 outputs (2^-22), and an fp32 cache, q and weights as
 // three bf16 parts each (2^-24).
 //
 // Measured (graph replays, bytes of K, V and scales over time): 8 x 131072 keys,
 // 8 kv-heads, 8 bits 326 us, 6.8 TB/s, the rate of a plain copy; 24 requests of
-// 1024-8192 keys bf16 72 us (6.2 TB/s), 8 bits 46 us (5.0 TB/s: two or three
+// 1024-8192 keys bf16 72 us (6.2 TB/s), 8 bits 45 us (5.1 TB/s: two or three
 // segments a CTA, whose ends the ring does not hide); one request of 4096 keys
-// bf16 10 us, of which reading is 2.5: lengths, page ids and copies follow one
+// bf16 9.3 us, of which reading is 2.5: lengths, page ids and copies follow one
 // another (3000 cycles), then parts are counted in (2700) and joined (5500).  8
-// requests of 4096-8192 keys and 1-8 new tokens, 8 bits: 41 us (2.4 TB/s), by the
+// requests of 4096-8192 keys and 1-8 new tokens, 8 bits: 40 us (2.5 TB/s), by the
 // conversions and products, done for each 16 rows.
 #include <cuda.h>
 #include <math.h>
@@ -571,14 +572,16 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                                     (((int64_t)page[h] * p.pm.Hkv) << p.pm.sh) + prow;
                                 float* sd = scales + slot * 2 * GK + h * SUB;
 #pragma unroll
-                                for (int v = 0; v < 2; ++v)
-                                    if (v ? do_v : do_k) asm volatile(
+                                for (int v = 0; v < 2; ++v) {
+                                    if (!(v ? do_v : do_k)) continue;
+                                    asm volatile(
                                         "cp.async.bulk.shared::cluster.global.mbarrier::"
                                         "complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                             smem_u32(sd + v * GK)),
                                         "l"((v ? p.v_scale : p.k_scale) + row), "r"(4 * p.box),
                                         "r"(smem_u32(&full[slot]))
                                         : "memory");
+                                }
                             }
                         }
                     }

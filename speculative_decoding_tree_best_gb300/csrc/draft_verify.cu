@@ -22,7 +22,7 @@
 //      the chain ended; the request's last CTA (a ticket) joins the slices and
 //      writes the outputs.
 // Measured (graph replays, V = 151936, bf16, a drafter's rows in fp32): one request
-// of 8 drafts 9.3 us, two launches' latency; 24 requests of up to 8 drafts 20.7 us,
+// of 8 drafts 9.2 us, two launches' latency; 24 requests of up to 8 drafts 20.6 us,
 // 65 MB at 3.2 TB/s: each launch is a chain (loads, block reduction; masses,
 // decision, loads, reduction, ticket) of which reading is about half.
 #include <math.h>

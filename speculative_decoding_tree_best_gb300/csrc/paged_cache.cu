@@ -317,8 +317,8 @@ cudaError_t read_t(const spec_paged_cfg& c, const spec_paged_kv& kv, int Lmax, v
     const cudaError_t e = row_args<IO, D>(c, kv, Lmax, a);
     if (e != cudaSuccess) return e;
     return launch_k(true, read_rows<IO, KV, D>, dim3((unsigned)(a.blocks * c.B)), dim3(NT), 0,
-                    st, a, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale, static_cast<uint4*>(k_out),
-                    static_cast<uint4*>(v_out), ws);
+                    st, a, kv.k_pages, kv.v_pages, kv.k_scale, kv.v_scale,
+                    static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), ws);
 }
 
 }  // namespace
