@@ -515,13 +515,16 @@ def _arg(t, dtype, shape, name, device):
 
 
 def _workspace(ws, need, device):
+    try:
+        if ws.get_device() == device and ws.nbytes >= need and ws.is_contiguous():
+            return ws.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
         raise TypeError("ws must be a contiguous CUDA tensor")
     if ws.get_device() != device:
         raise ValueError(f"ws is on cuda:{ws.get_device()}, the current device is cuda:{device}")
-    if ws.nbytes < need:
-        raise ValueError(f"ws holds {ws.nbytes} bytes, {need} are needed")
-    return ws.data_ptr()
+    raise ValueError(f"ws holds {ws.nbytes} bytes, {need} are needed")
 
 
 class _Plan:
@@ -543,22 +546,25 @@ class _Plan:
 
 
 _plans = {}
+# what a call asks of torch, looked up once
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _plan(cfg, device) -> _Plan:
-    key = (type(cfg), bytes(cfg), device)
-    p = _plans.get(key)
+def _plan(cfg, raw, device) -> _Plan:
+    """raw: bytes(cfg) (the two configurations differ in length)."""
+    p = _plans.get((raw, device))
     if p is None:
         if len(_plans) >= 1024:
             _plans.clear()
-        p = _plans[key] = _Plan(cfg)
+        p = _plans[raw, device] = _Plan(cfg)
     return p
 
 
 def _raw_stream(stream, device):
     """_stream as an integer; the current stream without making an object."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _get_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -622,6 +628,7 @@ class PagedKV:
             _arg(_required(page_table, "page_table"), i32, (cfg.B, cfg.max_pages), "page_table",
                  dev),
             _arg(_required(kv_len, "kv_len"), i32, (cfg.B,), "kv_len", dev))
+        self._ref = ctypes.byref(self._c)
         self._t = (k_pages, v_pages, k_scale, v_scale, page_table, kv_len)
         self.key = (pool, cfg.B, cfg.max_pages, cfg.kv_dtype, dt, dev)
         self._fits = set()
@@ -642,54 +649,60 @@ class PagedKV:
                    torch.full((cfg.B, cfg.max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros((cfg.B,), dtype=torch.int32, device=device), *sc)
 
-    def c(self, cfg: SpecPagedCfg, device: int) -> SpecPagedKV:
+    def ref(self, cfg: SpecPagedCfg, raw: bytes, device: int):
+        """The cache as an argument of a call with that configuration (raw: its bytes)."""
         if device != self.key[5]:
             raise ValueError(f"the cache is on cuda:{self.key[5]}, the current device is "
                              f"cuda:{device}")
-        fits = bytes(cfg)
-        if fits not in self._fits:                 # T and Hq may differ from call to call
+        if raw not in self._fits:                  # T and Hq may differ from call to call
             pool = (cfg.n_pages, cfg.Hkv, cfg.page, cfg.D)
             if self.key[:4] != (pool, cfg.B, cfg.max_pages, cfg.kv_dtype) or (
                     cfg.kv_dtype == SPEC_KV_IO and self.key[4] != _io_dtype(cfg)):
                 raise ValueError("the cache was made for another configuration")
             if len(self._fits) >= 64:
                 self._fits.clear()
-            self._fits.add(fits)
-        return self._c
+            self._fits.add(raw)
+        return self._ref
 
 
 def kv_page_append(cfg: SpecPagedCfg, kv: PagedKV, k_new, v_new, ws, n_new=None, stream=None):
     """Write the new tokens' rows (k_new, v_new [B][T][Hkv][D] io) behind the
     committed ones; n_new: None or CUDA int32 [B]."""
-    dev = torch.cuda.current_device()
-    p = _plan(cfg, dev)
-    _check("kv_page_append", (_lib or load()).kv_page_append(
-        ctypes.byref(cfg), ctypes.byref(kv.c(cfg, dev)), _arg(k_new, p.dt, p.new, "k_new", dev),
+    dev, raw = _get_device(), bytes(cfg)
+    p = _plan(cfg, raw, dev)
+    rc = (_lib or load()).kv_page_append(
+        ctypes.byref(cfg), kv.ref(cfg, raw, dev), _arg(k_new, p.dt, p.new, "k_new", dev),
         _arg(v_new, p.dt, p.new, "v_new", dev), _arg(n_new, torch.int32, p.b, "n_new", dev),
-        _workspace(ws, _STATUS_BYTES, dev), _raw_stream(stream, dev)))
+        _workspace(ws, _STATUS_BYTES, dev), _raw_stream(stream, dev))
+    if rc:
+        _check("kv_page_append", rc)
 
 
 def kv_page_read(cfg: SpecPagedCfg, kv: PagedKV, k_out, v_out, ws, stream=None):
     """The committed rows as a contiguous cache [B][Lmax][Hkv][D] io (rows at
     or past kv_len are left as they were)."""
-    dev = torch.cuda.current_device()
-    p = _plan(cfg, dev)
+    dev, raw = _get_device(), bytes(cfg)
+    p = _plan(cfg, raw, dev)
     Lmax = k_out.shape[1] if isinstance(k_out, torch.Tensor) and k_out.dim() == 4 else 0
     shape = (cfg.B, Lmax, cfg.Hkv, cfg.D)
-    _check("kv_page_read", (_lib or load()).kv_page_read(
-        ctypes.byref(cfg), ctypes.byref(kv.c(cfg, dev)), Lmax, _arg(k_out, p.dt, shape, "k_out", dev),
+    rc = (_lib or load()).kv_page_read(
+        ctypes.byref(cfg), kv.ref(cfg, raw, dev), Lmax, _arg(k_out, p.dt, shape, "k_out", dev),
         _arg(v_out, p.dt, shape, "v_out", dev), _workspace(ws, _STATUS_BYTES, dev),
-        _raw_stream(stream, dev)))
+        _raw_stream(stream, dev))
+    if rc:
+        _check("kv_page_read", rc)
 
 
 def attn_decode_paged(cfg: SpecPagedCfg, kv: PagedKV, q, o, ws, n_new=None, stream=None):
     """Attention of the new tokens (q, o [B][T][Hq][D] io) over the paged cache."""
-    dev = torch.cuda.current_device()
-    p = _plan(cfg, dev)
-    _check("attn_decode_paged", (_lib or load()).attn_decode_paged(
-        ctypes.byref(cfg), ctypes.byref(kv.c(cfg, dev)), _arg(q, p.dt, p.q, "q", dev),
+    dev, raw = _get_device(), bytes(cfg)
+    p = _plan(cfg, raw, dev)
+    rc = (_lib or load()).attn_decode_paged(
+        ctypes.byref(cfg), kv.ref(cfg, raw, dev), _arg(q, p.dt, p.q, "q", dev),
         _arg(n_new, torch.int32, p.b, "n_new", dev), _arg(o, p.dt, p.q, "o", dev),
-        _workspace(ws, p.need, dev), _raw_stream(stream, dev)))
+        _workspace(ws, p.need, dev), _raw_stream(stream, dev))
+    if rc:
+        _check("attn_decode_paged", rc)
 
 
 class DraftBuffers:
@@ -709,19 +722,21 @@ def draft_verify_sampled(cfg: SpecDraftCfg, draft_tok, draft_prob, logits, u, e,
     draft_prob f32 [B][N][V] or None (point masses), logits io [B][N+1][V], u
     f32 [B][N], e f32 [B][V]; kv_len / root_tok are advanced when given.  With
     N = 0 (plain sampling) draft_tok, draft_prob and u are not read."""
-    dev, f32, i32 = torch.cuda.current_device(), torch.float32, torch.int32
-    p = _plan(cfg, dev)
+    dev, f32, i32 = _get_device(), torch.float32, torch.int32
+    p = _plan(cfg, bytes(cfg), dev)
     N, V = p.new[1], p.q[2]
     if N == 0:
         draft_tok = draft_prob = u = None
     co = SpecDraftOut(_arg(out.accept_len, i32, p.b, "accept_len", dev),
                       _arg(out.out_tok, i32, p.q[:2], "out_tok", dev),
                       _arg(out.target_prob, f32, p.new, "target_prob", dev) if N else None)
-    _check("draft_verify_sampled", (_lib or load()).draft_verify_sampled(
+    rc = (_lib or load()).draft_verify_sampled(
         ctypes.byref(cfg), _arg(draft_tok, i32, p.new, "draft_tok", dev),
         _arg(n_draft, i32, p.b, "n_draft", dev),
         _arg(draft_prob, f32, p.new + (V,), "draft_prob", dev),
         _arg(logits, p.dt, p.q, "logits", dev), _arg(u, f32, p.new, "u", dev),
         _arg(e, f32, p.b + (V,), "e", dev), ctypes.byref(co), _arg(kv_len, i32, p.b, "kv_len", dev),
         _arg(root_tok, i32, p.b, "root_tok", dev), _workspace(ws, p.need, dev),
-        _raw_stream(stream, dev)))
+        _raw_stream(stream, dev))
+    if rc:
+        _check("draft_verify_sampled", rc)
