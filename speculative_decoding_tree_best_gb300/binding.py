@@ -530,7 +530,7 @@ def _workspace(ws, need, device):
 class _Plan:
     """What the calls of one configuration on one device need to know: the
     shapes and types of their arguments and the workspace's size."""
-    __slots__ = ("new", "q", "b", "dt", "need")
+    __slots__ = ("new", "q", "b", "dt", "need", "rows", "probs", "e")
 
     def __init__(self, cfg):
         if isinstance(cfg, SpecPagedCfg):
@@ -540,6 +540,9 @@ class _Plan:
         else:
             self.new = (cfg.B, cfg.N)
             self.q = (cfg.B, cfg.N + 1, cfg.V)
+            self.rows = self.q[:2]
+            self.probs = self.new + (cfg.V,)
+            self.e = (cfg.B, cfg.V)
             self.need = int(load().spec_draft_workspace_bytes(ctypes.byref(cfg), 0))
         self.b = (cfg.B,)
         self.dt = _io_dtype(cfg)
@@ -706,13 +709,26 @@ def attn_decode_paged(cfg: SpecPagedCfg, kv: PagedKV, q, o, ws, n_new=None, stre
 
 
 class DraftBuffers:
-    """Outputs of draft_verify_sampled."""
+    """Outputs of draft_verify_sampled: accept_len [B], out_tok [B][N+1] int32 and
+    target_prob [B][N] fp32.  The tensors are fixed for the object's life."""
 
     def __init__(self, cfg: SpecDraftCfg, device="cuda"):
         B, N = cfg.B, cfg.N
-        self.accept_len = torch.empty((B,), dtype=torch.int32, device=device)
-        self.out_tok = torch.empty((B, N + 1), dtype=torch.int32, device=device)
-        self.target_prob = torch.empty((B, N), dtype=torch.float32, device=device)
+        self._t = (torch.empty((B,), dtype=torch.int32, device=device),
+                   torch.empty((B, N + 1), dtype=torch.int32, device=device),
+                   torch.empty((B, N), dtype=torch.float32, device=device))
+        self.key = ((B, N + 1), self._t[0].get_device())
+        self._c = SpecDraftOut(*(t.data_ptr() if t.numel() else None for t in self._t))
+        self._ref = ctypes.byref(self._c)
+
+    accept_len, out_tok, target_prob = (property(lambda self, i=i: self._t[i]) for i in range(3))
+
+    def ref(self, rows, device: int):
+        """The outputs as an argument of a call with (B, N + 1) rows."""
+        if self.key != (rows, device):
+            _arg(self.accept_len, torch.int32, rows[:1], "accept_len", device)
+            _arg(self.out_tok, torch.int32, rows, "out_tok", device)
+        return self._ref
 
 
 def draft_verify_sampled(cfg: SpecDraftCfg, draft_tok, draft_prob, logits, u, e,
@@ -724,18 +740,14 @@ def draft_verify_sampled(cfg: SpecDraftCfg, draft_tok, draft_prob, logits, u, e,
     N = 0 (plain sampling) draft_tok, draft_prob and u are not read."""
     dev, f32, i32 = _get_device(), torch.float32, torch.int32
     p = _plan(cfg, bytes(cfg), dev)
-    N, V = p.new[1], p.q[2]
-    if N == 0:
+    if cfg.N == 0:
         draft_tok = draft_prob = u = None
-    co = SpecDraftOut(_arg(out.accept_len, i32, p.b, "accept_len", dev),
-                      _arg(out.out_tok, i32, p.q[:2], "out_tok", dev),
-                      _arg(out.target_prob, f32, p.new, "target_prob", dev) if N else None)
     rc = (_lib or load()).draft_verify_sampled(
         ctypes.byref(cfg), _arg(draft_tok, i32, p.new, "draft_tok", dev),
         _arg(n_draft, i32, p.b, "n_draft", dev),
-        _arg(draft_prob, f32, p.new + (V,), "draft_prob", dev),
+        _arg(draft_prob, f32, p.probs, "draft_prob", dev),
         _arg(logits, p.dt, p.q, "logits", dev), _arg(u, f32, p.new, "u", dev),
-        _arg(e, f32, p.b + (V,), "e", dev), ctypes.byref(co), _arg(kv_len, i32, p.b, "kv_len", dev),
+        _arg(e, f32, p.e, "e", dev), out.ref(p.rows, dev), _arg(kv_len, i32, p.b, "kv_len", dev),
         _arg(root_tok, i32, p.b, "root_tok", dev), _workspace(ws, p.need, dev),
         _raw_stream(stream, dev))
     if rc:

@@ -237,6 +237,22 @@ def test_graph_and_stream():
     assert torch.equal(out.target_prob, want.target_prob)
 
 
+def test_outputs_and_workspaces_of_another_shape_are_refused():
+    x = make(3, 2, 100, seed=15)
+    cfg = binding.draft_cfg(B=3, N=2, V=100)
+    for B, N in ((2, 2), (3, 1)):
+        with pytest.raises(ValueError):
+            run(x, out=binding.DraftBuffers(binding.draft_cfg(B=B, N=N, V=100)))
+    with pytest.raises((TypeError, ValueError)):
+        run(x, out=binding.DraftBuffers(cfg, device="cpu"))
+    for ws in (binding.alloc_draft_workspace(cfg)[:256], [0]):
+        with pytest.raises((TypeError, ValueError)):
+            run(x, ws=ws)
+    with pytest.raises(TypeError):
+        run(x, ws=torch.zeros(1 << 20, dtype=torch.uint8))
+    check(x, run(x)[0])
+
+
 def test_frequencies_follow_the_target():
     """4000 independent requests at once: the first emitted token of a chain of
     one draft follows p (chi-square over 6 tokens, 5 degrees: 99.9% is 20.5)."""
