@@ -525,6 +525,8 @@ typedef struct spec_paged_kv {
 /* Bytes of workspace of the paged calls (0 on an invalid cfg), zero-filled once
  * like the tree calls' workspace, which it does not replace.  num_sms: the SM
  * count to lay it out for; 0 asks the current device (0 when there is none).
+ * One workspace that is large enough for each of them serves calls of any
+ * configurations, of draft_verify_sampled too, that follow one another.
  * Calls that may run at the same time (streams, replayed graphs) need one each;
  * after SPEC_DEV_TIMEOUT it is to be zero-filled again. */
 size_t spec_paged_workspace_bytes(const spec_paged_cfg *cfg, int num_sms);

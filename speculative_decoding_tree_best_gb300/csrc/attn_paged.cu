@@ -1397,7 +1397,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             fence_gpu();
             __syncwarp();
             if (lane == 0) {
-                uint32_t* tk = p.tickets + (size_t)b * hr + seg;
+                uint32_t* tk = p.tickets + c0;
                 const uint32_t all = (uint32_t)(c1 - c0 + 1) * min(W, live * TPR);
                 if (atomicAdd(tk, 1u) == all - 1) {
                     *tk = 0;                             // for the next call
@@ -1464,7 +1464,7 @@ cudaError_t attn_launch(const spec_paged_cfg& c, const spec_paged_kv& kv, const 
     p.n_new = n_new;
     p.o = o;
     p.ws = ws;
-    p.tickets = ws_ptr<uint32_t>(ws, w.ticket_off);
+    p.tickets = ws_ptr<uint32_t>(ws, kTicketOff);
     p.part_o = ws_ptr<float4>(ws, w.part_o_off);
     p.part_ml = ws_ptr<float4>(ws, w.part_ml_off);
     p.B = c.B;

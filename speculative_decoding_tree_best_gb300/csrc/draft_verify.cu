@@ -205,7 +205,7 @@ struct RaceArgs {
     void* ws;
     const float2* part;
     float2* cand;            // [B][slices]: (score, token)
-    uint32_t* tickets;       // [B]
+    uint32_t* tickets;       // [B] where there is more than one slice
     int splits, slices, per; // per: tokens of a slice
     float k;                 // log2(e) / temperature
 };
@@ -354,21 +354,23 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     }
     Cand best{top_i == NONE ? -INFINITY : top_w / top_e, top_i};
     best = block_best(best, sh);
-    if (tid == 0) {
-        __stcg(a.cand + (size_t)b * a.slices + blockIdx.x,
-               make_float2(best.s, __int_as_float(best.i)));
-        asm volatile("fence.acq_rel.gpu;" ::: "memory");
-        last_cta = atomicAdd(a.tickets + b, 1u) == (uint32_t)a.slices - 1;
-        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+    if (a.slices > 1) {
+        if (tid == 0) {
+            __stcg(a.cand + (size_t)b * a.slices + blockIdx.x,
+                   make_float2(best.s, __int_as_float(best.i)));
+            asm volatile("fence.acq_rel.gpu;" ::: "memory");
+            last_cta = atomicAdd(a.tickets + b, 1u) == (uint32_t)a.slices - 1;
+            asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        }
+        __syncthreads();
+        if (!last_cta) return;
+        best = Cand{-INFINITY, NONE};
+        for (int k = tid; k < a.slices; k += NT) {
+            const float2 x = __ldcg(a.cand + (size_t)b * a.slices + k);
+            take(best, x.x, __float_as_int(x.y));
+        }
+        best = block_best(best, sh);
     }
-    __syncthreads();
-    if (!last_cta) return;
-    best = Cand{-INFINITY, NONE};
-    for (int k = tid; k < a.slices; k += NT) {
-        const float2 x = __ldcg(a.cand + (size_t)b * a.slices + k);
-        take(best, x.x, __float_as_int(x.y));
-    }
-    best = block_best(best, sh);
     if (best.i == NONE && s > 0.0f && kept < n) {
         // p <= q everywhere in fp32 (a refusal at a rounding's distance): p decides
         Cand again{-INFINITY, NONE};
@@ -382,7 +384,7 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     for (int j = tid; j <= N; j += NT)
         a.out.out_tok[(size_t)b * (N + 1) + j] = j < kept ? draft[j] : (j == kept ? tok : -1);
     if (tid == 0) {
-        a.tickets[b] = 0;                                // for the next call
+        if (a.slices > 1) a.tickets[b] = 0;              // for the next call
         a.out.accept_len[b] = kept + 1;
         if (a.kv_len) a.kv_len[b] += kept + 1;
         if (a.root_tok) a.root_tok[b] = tok;
@@ -414,7 +416,7 @@ cudaError_t launch_draft_verify(const spec_draft_cfg& c, const int32_t* draft_to
     const DraftWs w = draft_ws_layout(c, sms);
     RaceArgs a{draft_tok, n_draft, draft_prob, logits, u, e, out, kv_len, root_tok, ws,
                ws_ptr<const float2>(ws, w.part_off), ws_ptr<float2>(ws, w.cand_off),
-               ws_ptr<uint32_t>(ws, w.ticket_off), w.splits, w.slices, w.per,
+               ws_ptr<uint32_t>(ws, draft_ticket_off(sms)), w.splits, w.slices, w.per,
                1.4426950408889634f / c.temperature};
     return c.io_dtype == SPEC_IO_BF16 ? verify_t<SPEC_IO_BF16>(c, n_draft, logits, a, w, st)
                                       : verify_t<SPEC_IO_F32>(c, n_draft, logits, a, w, st);

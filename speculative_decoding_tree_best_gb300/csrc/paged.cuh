@@ -58,35 +58,52 @@ inline RowTiles paged_row_tiles(const spec_paged_cfg& c) {
     return r;
 }
 
-// Status word; a ticket per (request, kv-head, row group); two parts per CTA
-// (a CTA's first and last segment may be shared with its neighbours):
-// fp32 outputs in the warps' register order, and (max, max, sum, sum) per lane.
+// The head of a workspace of the paged calls and of the chain verification:
+// status word, then the tickets of both, which every call finds at zero and
+// leaves at zero.  Their places and their number go by the SMs alone, so that no
+// configuration has data where another has tickets, and one workspace serves any
+// of them in turn.
+//   attention      a ticket per CTA: a segment cut between CTAs counts in that of
+//                  the CTA with its first granule (no two cut ones begin in a CTA)
+//   verification   a ticket per request whose race is cut into slices: fewer
+//                  requests than kRaceCtas per SM (draft_ws_layout)
+constexpr int kRaceCtas = 3;
+constexpr size_t kTicketOff = 256;
+inline size_t draft_ticket_off(int num_sms) {
+    return kTicketOff + sizeof(uint32_t) * (size_t)num_sms;
+}
+inline size_t ws_data_off(int num_sms) {
+    return align_up(draft_ticket_off(num_sms) + sizeof(uint32_t) * kRaceCtas * (size_t)num_sms, 256);
+}
+
+// Attention: two parts per CTA (its first and last segment may be shared with its
+// neighbours): fp32 outputs in the warps' register order, and (max, max, sum, sum)
+// per lane.
 struct PagedWs {
-    size_t ticket_off, part_o_off, part_ml_off, total;
+    size_t part_o_off, part_ml_off, total;
     int rtc, rtg;
 };
 
 inline PagedWs paged_ws_layout(const spec_paged_cfg& c, int num_sms) {
     PagedWs w{};
-    w.total = 256;
-    w.ticket_off = w.total;
+    w.total = ws_data_off(num_sms);
     if (c.T > SPEC_MAX_ROWS) return w;       // no attention with so many rows
     const RowTiles r = paged_row_tiles(c);
     w.rtc = r.rtc;
     w.rtg = r.rtg;
     const size_t tiles = (size_t)2 * num_sms * r.rtc * r.nr;
-    w.part_o_off = align_up(w.ticket_off + sizeof(uint32_t) * (size_t)c.B * c.Hkv * r.rtg, 256);
+    w.part_o_off = w.total;
     w.part_ml_off = align_up(w.part_o_off + tiles * 8 * c.D * sizeof(float), 256);
     w.total = align_up(w.part_ml_off + tiles * 32 * 16, 256);
     return w;
 }
 
 // How the verification is split: `splits` segments per logits row, `slices` of
-// `per` tokens for the race.  About eight CTAs per SM over all rows, and three
+// `per` tokens for the race.  About eight CTAs per SM over all rows, and kRaceCtas
 // over the requests' races, but no segment under 4096 and no slice under 2048
 // tokens (a load per thread).
 struct DraftWs {
-    size_t part_off, cand_off, ticket_off, total;
+    size_t part_off, cand_off, total;
     int splits, slices, per;
 };
 
@@ -97,13 +114,12 @@ inline DraftWs draft_ws_layout(const spec_draft_cfg& c, int num_sms) {
         return (int)(want < 1 ? 1 : (want > most ? most : want));
     };
     w.splits = clamp((8LL * num_sms + rows - 1) / rows, ((int64_t)c.V + 4095) / 4096);
-    w.slices = clamp((3LL * num_sms + c.B - 1) / c.B, ((int64_t)c.V + 2047) / 2048);
+    w.slices = clamp(((int64_t)kRaceCtas * num_sms + c.B - 1) / c.B, ((int64_t)c.V + 2047) / 2048);
     w.per = (int)((((int64_t)c.V + w.slices - 1) / w.slices + 7) / 8 * 8);
     w.slices = (int)(((int64_t)c.V + w.per - 1) / w.per);
-    w.part_off = 256;
+    w.part_off = ws_data_off(num_sms);
     w.cand_off = align_up(w.part_off + sizeof(float) * 2 * rows * w.splits, 256);
-    w.ticket_off = align_up(w.cand_off + sizeof(float) * 2 * (size_t)c.B * w.slices, 256);
-    w.total = align_up(w.ticket_off + sizeof(uint32_t) * c.B, 256);
+    w.total = align_up(w.cand_off + sizeof(float) * 2 * (size_t)c.B * w.slices, 256);
     return w;
 }
 

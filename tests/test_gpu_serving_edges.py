@@ -1,0 +1,81 @@
+"""The serving operators at the edges of what their calls accept: one workspace
+for many shapes in turn, and inputs far from the ordinary ones."""
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_tree_best_gb300 import binding
+from tests import test_gpu_chain as chain
+from tests.test_gpu_paged import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_tree_best_gb300 import build
+    build.build()
+    binding.load()
+
+
+# ------------------------------------------------- one workspace for many shapes
+
+def one_workspace(needs):
+    return torch.zeros(max(needs), dtype=torch.uint8, device="cuda")
+
+
+def test_attention_of_many_shapes_on_one_workspace():
+    """Shapes whose parts, row groups and tickets differ, in turn and back again:
+    each call finds the counters at zero wherever the one before had its data."""
+    rng = np.random.default_rng(1)
+    shapes = [dict(lens=[9000], Hq=32, Hkv=8, D=128, page=64),
+              dict(lens=rng.integers(3000, 6000, 24).tolist(), Hq=32, Hkv=8, D=128, page=64),
+              dict(lens=[4000, 3100], T=33, Hq=8, Hkv=2, D=64, page=16),
+              dict(lens=rng.integers(0, 900, 40).tolist(), T=2, Hq=8, Hkv=8, D=64, page=32)]
+    xs = [Case(io="bf16", kv="e4m3", seed=i, **s) for i, s in enumerate(shapes)]
+    want = [x.attend() for x in xs]                        # each on its own workspace
+    for x, w in zip(xs, want):
+        x.check(w)
+    ws = one_workspace([binding.spec_paged_workspace_bytes(x.cfg) for x in xs])
+    for i in (0, 1, 2, 3, 1, 0, 3, 2, 0, 1):
+        xs[i].ws = ws
+        assert torch.equal(xs[i].attend(), want[i]), i
+    assert binding.spec_status_read(ws) == 0
+
+
+def test_verifications_of_many_shapes_on_one_workspace():
+    """Also beyond the number of requests whose races are cut into slices."""
+    xs = [chain.make(B, N, V, seed=B + N) for B, N, V in
+          ((24, 8, 30000), (24, 4, 30000), (8, 8, 30000), (1, 2, 100003), (700, 1, 50))]
+    cfgs = [binding.draft_cfg(B=x["logits"].shape[0], N=x["toks"].shape[1], V=x["logits"].shape[2],
+                              temperature=x["t"]) for x in xs]
+    want = [chain.run(x)[0] for x in xs]
+    for x, w in zip(xs, want):
+        chain.check(x, w)
+    ws = one_workspace([binding.spec_draft_workspace_bytes(c) for c in cfgs])
+    for i in (0, 1, 0, 2, 0, 3, 4, 2, 1, 3, 0):
+        out = binding.DraftBuffers(cfgs[i])
+        for t in (out.accept_len, out.out_tok):
+            t.fill_(-7)
+        chain.run(xs[i], ws=ws, out=out)
+        for name in ("accept_len", "out_tok", "target_prob"):
+            assert torch.equal(getattr(out, name), getattr(want[i], name)), (i, name)
+    assert binding.spec_status_read(ws) == 0
+
+
+def test_attention_and_verification_share_a_workspace():
+    x = Case([9000, 70], T=3, Hq=16, Hkv=4, D=128, page=64, kv="e4m3", seed=5)
+    y = chain.make(6, 2, 40000, seed=6)
+    want_o, want_t = x.attend(), chain.run(y)[0]
+    cfg = binding.draft_cfg(B=6, N=2, V=40000)
+    ws = one_workspace([binding.spec_paged_workspace_bytes(x.cfg),
+                        binding.spec_draft_workspace_bytes(cfg)])
+    x.ws = ws
+    for _ in range(3):
+        assert torch.equal(x.attend(), want_o)
+        out = binding.DraftBuffers(cfg)
+        out.out_tok.fill_(-7)
+        chain.run(y, ws=ws, out=out)
+        assert torch.equal(out.out_tok, want_t.out_tok)
