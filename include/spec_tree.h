@@ -577,8 +577,10 @@ int kv_page_read(const spec_paged_cfg *cfg, const spec_paged_kv *kv, int Lmax, v
 int attn_decode_paged(const spec_paged_cfg *cfg, const spec_paged_kv *kv, const void *q,
                       const int32_t *n_new, void *o, void *ws, void *stream);
 
-/* Shape of the chain verification: N drafts per request in [0, 127], V >= 1,
- * 1 <= B <= 65535, temperature > 0 and finite, reserved 0 (else ST_EINVAL). */
+#define SPEC_MAX_DRAFT_V (1 << 30)
+
+/* Shape of the chain verification: N drafts per request in [0, 127],
+ * 1 <= V <= 2^30, 1 <= B <= 65535, temperature > 0 and finite, reserved 0 (else ST_EINVAL). */
 typedef struct spec_draft_cfg {
     int32_t B, N, V;
     int32_t io_dtype;        /* of the logits */

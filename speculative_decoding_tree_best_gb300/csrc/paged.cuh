@@ -34,8 +34,10 @@ inline int check_paged_kv(const spec_paged_cfg& c, const spec_paged_kv* kv) {
 
 inline int check_draft_cfg(const spec_draft_cfg* c) {
     if (!c) return ST_EINVAL;
-    if (c->B < 1 || c->B > 65535 || c->N < 0 || c->N + 1 > SPEC_MAX_ROWS || c->V < 1)
+    if (c->B < 1 || c->B > 65535 || c->N < 0 || c->N + 1 > SPEC_MAX_ROWS)
         return ST_EINVAL;
+    // the kernels step over a row in 32 bits, some thousands of tokens past its end
+    if (c->V < 1 || c->V > SPEC_MAX_DRAFT_V) return ST_EINVAL;
     if (!(c->temperature > 0.0f && c->temperature <= 3.0e38f) || c->reserved != 0u)
         return ST_EINVAL;
     if (c->io_dtype != SPEC_IO_F32 && c->io_dtype != SPEC_IO_BF16) return ST_EUNSUPPORTED;
