@@ -35,6 +35,7 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int NONE = 0x7fffffff;
+constexpr float FOLD = 0x1p20f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -154,19 +155,31 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
         m = nm;
         // 2^((x - base) k) as 2^(x k - c), c = fl(base k): the sum of a product
         // and a constant is rounded once, and what c is off by, base k - c (a
-        // fused multiply-add gives it exactly), is the same factor for all
+        // fused multiply-add gives it exactly), is the same factor for all.  It
+        // is at most FOLD 2^-25 there; beyond (a small temperature, or nothing
+        // but masks of the type's lowest value) that factor, and base k itself,
+        // leave fp32's range: there x - base comes first.
         const float base = m == -INFINITY ? 0.0f : m;      // a NaN beside -inf stays
         const float c0 = -base * k;
         float ps[4] = {};
+        auto add = [&](auto&& term) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (at + j * NT >= left) break;                // the same for all threads
-            float x[VEC];
-            grp<IO>::unpack(u[j], x);
+            for (int j = 0; j < U; ++j) {
+                if (at + j * NT >= left) break;            // the same for all threads
+                float x[VEC];
+                grp<IO>::unpack(u[j], x);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) ps[v % 4] += ex2(fmaf(x[v], k, c0));
+                for (int v = 0; v < VEC; ++v) ps[v % 4] += term(x[v]);
+            }
+        };
+        float rest = 1.0f;
+        if (fabsf(c0) <= FOLD) {
+            add([&](float x) { return ex2(fmaf(x, k, c0)); });
+            rest = ex2(-fmaf(base, k, c0));
+        } else {
+            add([&](float x) { return ex2((x - base) * k); });
         }
-        s += ((ps[0] + ps[1]) + (ps[2] + ps[3])) * ex2(-fmaf(base, k, c0));
+        s += ((ps[0] + ps[1]) + (ps[2] + ps[3])) * rest;
     }
     if (seg == 0) {
         // the elements of the row in groups that it shares with its neighbours
@@ -417,7 +430,7 @@ cudaError_t launch_draft_verify(const spec_draft_cfg& c, const int32_t* draft_to
     RaceArgs a{draft_tok, n_draft, draft_prob, logits, u, e, out, kv_len, root_tok, ws,
                ws_ptr<const float2>(ws, w.part_off), ws_ptr<float2>(ws, w.cand_off),
                ws_ptr<uint32_t>(ws, draft_ticket_off(sms)), w.splits, w.slices, w.per,
-               1.4426950408889634f / c.temperature};
+               fminf(1.4426950408889634f / c.temperature, 3.4028234663852886e38f)};
     return c.io_dtype == SPEC_IO_BF16 ? verify_t<SPEC_IO_BF16>(c, n_draft, logits, a, w, st)
                                       : verify_t<SPEC_IO_F32>(c, n_draft, logits, a, w, st);
 }

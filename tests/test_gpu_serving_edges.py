@@ -79,3 +79,46 @@ def test_attention_and_verification_share_a_workspace():
         out.out_tok.fill_(-7)
         chain.run(y, ws=ws, out=out)
         assert torch.equal(out.out_tok, want_t.out_tok)
+
+
+# ---------------------------------------------------------- verification: row masses
+
+@pytest.mark.parametrize("io,V", [("bf16", 4099), ("f32", 4099), ("bf16", 32768), ("f32", 1000)])
+@pytest.mark.parametrize("t,at", [(1e-6, 15.0), (3e-9, 15.0), (1e-10, 1000.0), (1e-30, 20.0), (1e-44, 20.0)])
+def test_small_temperatures(io, V, t, at):
+    """Logits over the temperature far beyond 2^31: the largest logit, or the
+    largest few that are equal, have all of the mass."""
+    x = chain.make(24, 3, V, io, seed=V, spread=0.05 * at)
+    x["t"] = float(np.float32(t))
+    x["toks"][::2, :2] = x["logits"][::2, :2].argmax(-1)
+    out, ws = chain.run(x)
+    kepts = chain.check(x, out)
+    assert binding.spec_status_read(ws) == 0
+    assert max(kepts) >= 2
+
+
+def test_logits_that_differ_by_a_small_temperature():
+    """fp32 logits a few roundings apart at a temperature of that size."""
+    x = chain.make(12, 2, 5000, "f32", seed=2)
+    x["logits"] = (np.float32(15) + np.float32(2.0 ** -20) * np.random.default_rng(3).integers(
+        -20, 20, x["logits"].shape)).astype(np.float32)
+    x["t"] = float(np.float32(1e-6))
+    out, ws = chain.run(x)
+    chain.check(x, out)
+    assert binding.spec_status_read(ws) == 0
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [0.5, 1.0])
+def test_masks_of_the_lowest_value(io, t):
+    """All but a few tokens at the type's lowest value, in one row all of them."""
+    lowest = np.float32(torch.finfo(chain.DT[io]).min)
+    x = chain.make(8, 2, 5003, io, t=t, seed=4)
+    x["logits"][:, :, 20:] = lowest
+    x["q"][:, :, 20:] = 0
+    x["q"] /= x["q"].sum(-1, keepdims=True)
+    x["toks"] %= 20
+    x["logits"][3] = lowest
+    out, ws = chain.run(x)
+    chain.check(x, out)
+    assert binding.spec_status_read(ws) == 0
