@@ -309,7 +309,9 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     // reciprocal tells apart, the quotients decide.  (A division per token made
     // the race 45 instructions a token.)
     // (top_lo is never 0: tokens without weight take no quotient.)  An exponential
-    // below 2^-126 has an infinite approximate score; quotients decide there too.
+    // below 2^-126 has an infinite approximate score, which makes top_hi infinite
+    // for good: then the thread goes over its tokens again.  One from 2^126 on has
+    // none: if that is all there is, the request's last CTA sees to it.
     float top_lo = 0x1p-149f, top_hi = 0.0f, top_w = 0.0f, top_e = 1.0f;
     int top_i = NONE;
     auto score = [&](float x, float q, float ex, int v) {
@@ -326,6 +328,12 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
             top_e = ex;
             top_i = v;
         }
+    };
+    // a token by its quotient (res: by the residual, where there is one)
+    auto take_quotient = [&](Cand& c, int v, bool res) {
+        const float q = !res ? 0.0f : (qp ? qp[v] : (v == point ? 1.0f : 0.0f));
+        const float w = fmaf(ex2((io_t<IO>::ld(lp, v) - m) * a.k), inv, -q);
+        if (w > 0.0f) take(c, w / e[v], v);
     };
     if (s > 0.0f && vec) {
         for (int v0 = first; v0 < hi; v0 += U * NT * VEC) {
@@ -366,6 +374,12 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
             score(io_t<IO>::ld(lp, v), qp ? qp[v] : (v == point ? 1.0f : 0.0f), e[v], v);
     }
     Cand best{top_i == NONE ? -INFINITY : top_w / top_e, top_i};
+    if (!(top_hi < INFINITY)) {
+        best = Cand{-INFINITY, NONE};
+        const int len = vec ? VEC : 1;
+        for (int v0 = lo + tid * len; v0 < hi; v0 += NT * len)
+            for (int v = v0; v < v0 + len; ++v) take_quotient(best, v, true);
+    }
     best = block_best(best, sh);
     if (a.slices > 1) {
         if (tid == 0) {
@@ -384,14 +398,16 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
         }
         best = block_best(best, sh);
     }
-    if (best.i == NONE && s > 0.0f && kept < n) {
-        // p <= q everywhere in fp32 (a refusal at a rounding's distance): p decides
-        Cand again{-INFINITY, NONE};
-        for (int v = tid; v < V; v += NT) {
-            const float w = ex2((io_t<IO>::ld(lp, v) - m) * a.k) * inv;
-            if (w > 0.0f) take(again, w / e[v], v);
+    if (s > 0.0f && !(best.s >= 0x1p-100f)) {
+        // No token, or scores where approximate ones lose bits or vanish: the
+        // quotients of all.  Where p <= q everywhere in fp32 (a refusal at a
+        // rounding's distance) p decides.
+        for (int pass = 0; pass < 2; ++pass) {
+            Cand again{-INFINITY, NONE};
+            for (int v = tid; v < V; v += NT) take_quotient(again, v, pass == 0);
+            best = block_best(again, sh);
+            if (best.i != NONE) break;
         }
-        best = block_best(again, sh);
     }
     const int tok = best.i != NONE ? best.i : 0;
     for (int j = tid; j <= N; j += NT)

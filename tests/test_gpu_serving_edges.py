@@ -122,3 +122,44 @@ def test_masks_of_the_lowest_value(io, t):
     out, ws = chain.run(x)
     chain.check(x, out)
     assert binding.spec_status_read(ws) == 0
+
+
+# ------------------------------------------------ verification: ends of the scores' range
+
+@pytest.mark.parametrize("V", [4000, 4003])
+@pytest.mark.parametrize("small", [2.0 ** -128, 2.0 ** -140, 2.0 ** -149])
+def test_an_exponential_below_the_normal_range_beside_a_larger_score(V, small):
+    """A token of little weight and a subnormal exponential, before and behind one
+    whose score is larger, the same thread's or another's; and the other way round."""
+    x = chain.make(8, 0, V, io="f32", seed=20, spread=0.1)
+    x["e"][:] = 1.0
+    pairs = [(8, 9), (9, 8), (8, 8 + 256), (264, 8), (100, 3000), (3000, 100), (16, 17), (17, 16)]
+    for b, (i, j) in enumerate(pairs):                     # i has the small exponential
+        x["e"][b, i] = small
+        x["logits"][b, 0, i] = -14.0                       # weight about 2^-32
+        x["e"][b, j] = small * (2.0 ** 20 if b < 6 else 2.0 ** 40)
+        x["logits"][b, 0, j] = 0.5                         # 21 log2 units more
+    out, ws = chain.run(x)
+    chain.check(x, out)
+    assert out.out_tok[:, 0].tolist() == [j for _, j in pairs[:6]] + [i for i, _ in pairs[6:]]
+
+
+@pytest.mark.parametrize("V", [40, 43, 2600])
+@pytest.mark.parametrize("N", [0, 2])
+def test_exponentials_whose_reciprocal_vanishes(V, N):
+    """All of them from 2^126 on: scores below the normal range, told apart."""
+    x = chain.make(12, N, V, io="f32", seed=V + N, spread=4.0)
+    x["e"] = (2.0 ** 126 * (1 + 0.99 * np.random.default_rng(V).random(x["e"].shape))).astype(np.float32)
+    out, ws = chain.run(x)
+    chain.check(x, out)
+    assert binding.spec_status_read(ws) == 0
+
+
+def test_drafts_of_point_masses_whose_reciprocals_vanish():
+    """A refused draft is not drawn again there either."""
+    x = chain.make(6, 1, 24, io="f32", seed=9, point=True, spread=4.0)
+    x["toks"] = x["logits"][:, :1].argmax(-1).astype(np.int32)
+    x["u"][:] = np.float32(1 - 2 ** -24)
+    x["e"] = (2.0 ** 126 * (1 + 0.99 * np.random.default_rng(9).random(x["e"].shape))).astype(np.float32)
+    out, _ = chain.run(x)
+    assert chain.check(x, out) and (out.out_tok[:, 0].cpu().numpy() != x["toks"][:, 0]).all()
