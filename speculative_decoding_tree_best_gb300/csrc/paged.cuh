@@ -38,7 +38,7 @@ inline int check_draft_cfg(const spec_draft_cfg* c) {
         return ST_EINVAL;
     // the kernels step over a row in 32 bits, some thousands of tokens past its end
     if (c->V < 1 || c->V > SPEC_MAX_DRAFT_V) return ST_EINVAL;
-    if (!(c->temperature > 0.0f && c->temperature <= 3.0e38f) || c->reserved != 0u)
+    if (!(c->temperature > 0.0f && c->temperature <= 3.4028234663852886e38f) || c->reserved != 0u)
         return ST_EINVAL;
     if (c->io_dtype != SPEC_IO_F32 && c->io_dtype != SPEC_IO_BF16) return ST_EUNSUPPORTED;
     return ST_OK;

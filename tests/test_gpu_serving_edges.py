@@ -163,3 +163,14 @@ def test_drafts_of_point_masses_whose_reciprocals_vanish():
     x["e"] = (2.0 ** 126 * (1 + 0.99 * np.random.default_rng(9).random(x["e"].shape))).astype(np.float32)
     out, _ = chain.run(x)
     assert chain.check(x, out) and (out.out_tok[:, 0].cpu().numpy() != x["toks"][:, 0]).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_large_temperatures(io):
+    """Probabilities that are all but equal, up to the largest finite temperature."""
+    for t in (1e6, 3.4028234663852886e38):
+        x = chain.make(6, 2, 999, io, seed=21)
+        x["t"] = float(np.float32(t))
+        out, ws = chain.run(x)
+        chain.check(x, out)
+        assert binding.spec_status_read(ws) == 0

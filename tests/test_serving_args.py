@@ -14,3 +14,9 @@ def test_vocabularies_beyond_the_kernels_indices_are_refused(lib, V):  # noqa: F
     assert draft(lib, cfg) == binding.ST_EINVAL
     assert lib.spec_draft_workspace_bytes(ctypes.byref(cfg), 152) == 0
     assert lib.spec_draft_workspace_bytes(ctypes.byref(binding.draft_cfg(B=1, N=1, V=1 << 30)), 152) > 0
+
+
+def test_every_finite_temperature_is_accepted(lib):  # noqa: F811
+    for t in (3.4028234663852886e38, 3.1e38, 1e-45):
+        cfg = binding.draft_cfg(B=1, N=1, V=10, temperature=t)
+        assert lib.spec_draft_workspace_bytes(ctypes.byref(cfg), 152) > 0
