@@ -9,7 +9,7 @@
 // the score; the value's scale goes into the weight's exponent,
 // w'_k = 2^(x_k + log2 scale_k - m) with m the maximum over x_k + log2 scale_k
 // (up to a factor of 2^SLACK, below), so that the weights that meet the codes are
-// at most 2^SLACK whatever the scales.
+// at most 2^(SLACK + LIFT) whatever the scales.
 //
 // What bounds it: reading the cache, 2 D values a key and kv-head against
 // 4 D G T flops (G = Hq / Hkv), 2 G T flops a byte in bf16: far below the
@@ -33,9 +33,11 @@
 //
 // Rounding.  Scores, weights, sums and outputs are fp32.  What the tensor cores
 // take is exact (cached values; bf16 q) or in parts: weights as two bf16 parts
-// (2^-16) over a bf16 cache, as one fp16 part over an 8-bit cache with bf16
-// outputs (2^-11, an eighth of the output's own rounding; they are at most 2^SLACK),
-// two fp16 parts with fp32 outputs (2^-22), and an fp32 cache, q and weights as
+// (2^-16) over a bf16 cache; over an 8-bit cache in fp16, times 2^LIFT: one part
+// with bf16 outputs (2^-11, an eighth of the output's own rounding) unless a tile
+// has weights below fp16's normal range (2^-25 of the largest so far), two parts
+// there and with fp32 outputs (2^-22), the second REST times as large, so that what
+// is left of a weight is at most 2^-48 of the largest; and an fp32 cache, q and weights as
 // three bf16 parts each (2^-24).
 //
 // Measured (graph replays, bytes of K, V and scales over time): 8 x 131072 keys,
@@ -63,9 +65,17 @@ using tc::smem_u32;
 
 constexpr int SUB = 16;                // keys per product tile: the smallest page
 constexpr int MAX_RTC = 3;             // row tiles per CTA, at most (paged_row_tiles)
-// log2 of how far a weight may be above 1 (8 requests of drafts 40.6 -> 39.6 us, 24
-// requests e4m3 45.4 -> 45.1, 8 x 131072 keys 327.3 -> 325.8 against none)
-constexpr float SLACK = 8.0f;
+// log2 of how far a weight may be above that of the maximum (0 to 4: 8 requests of
+// drafts about 1 us less)
+constexpr float SLACK = 4.0f;
+// fp16 weights: 2^LIFT times as large, up to 2^(SLACK + LIFT) = 2^15, so that fewer
+// of them fall below fp16's normal range (with 8 and 7, drafts 40.8 us instead of
+// 40.7, 8 x 131072 keys 336 instead of 328; without the second part for those that
+// do, 39.6 and 327, but long flat tails are lost).  What a weight's fp16 part
+// leaves goes times REST, against codes, or into outputs, that are scaled to match
+// (exact: codes are multiples of 2^-9).
+constexpr float LIFT = 11.0f;
+constexpr float REST = 0x1p12f;
 constexpr int MAX_SLOTS = 64;          // granules in a CTA's ring, at most
 
 // ---- instruction wrappers -------------------------------------------------------------
@@ -129,6 +139,12 @@ __device__ __forceinline__ float log2_scale(float x) {
 }
 __device__ __forceinline__ uint32_t packh(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// both halves over REST
+__device__ __forceinline__ uint32_t scale_f16(uint32_t x) {
+    const __half2 f = __floats2half2_rn(1.0f / REST, 1.0f / REST);
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&x), f);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t packb(float lo, float hi) {
@@ -898,7 +914,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
         // The running maximum of what the V weights go by (fmaxf passes over a NaN).
         // It is brought up to date when a lane is above it by more than SLACK: the
-        // weights are then at most 2^SLACK, which fp16 holds, and most granules do
+        // weights are then at most 2^(SLACK + LIFT), which fp16 holds, and most granules do
         // without the shuffles.
         bool grow = false;
         float nm[NR][2];
@@ -937,10 +953,11 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
         }
         // the weights, in place of the scores, and their sum
+        uint32_t least = 0xffffffffu;                    // the least weight's bits
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            const float b0 = m[nr][0] == -INFINITY ? 0.0f : m[nr][0];
-            const float b1 = m[nr][1] == -INFINITY ? 0.0f : m[nr][1];
+            const float b0 = m[nr][0] == -INFINITY ? 0.0f : m[nr][0] - (A::Q8 ? LIFT : 0.0f);
+            const float b1 = m[nr][1] == -INFINITY ? 0.0f : m[nr][1] - (A::Q8 ? LIFT : 0.0f);
 #pragma unroll
             for (int h = 0; h < NS; ++h)
 #pragma unroll
@@ -953,7 +970,24 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                         x[nr][h][e] = 0.0f;
                     else
                         x[nr][h][e] = A::Q8 ? ex2(d + lv[h][e >> 1]) : pl;
+                    least = min(least, __float_as_uint(x[nr][h][e]));
                 }
+        }
+        // One fp16 part is not enough for weights below its normal range, 2^-14:
+        // there may be more of them than the few large ones outweigh.
+        bool rest = false;
+        if constexpr (A::Q8 && A::PT == 1) {
+            if (masked) {                                // but for the zeros
+                least = 0xffffffffu;
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int h = 0; h < NS; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            least = min(least, __float_as_uint(x[nr][h][e]) - 1u);
+            }
+            rest = __any_sync(0xffffffffu, least < 0x38800000u - 1u);
         }
         // Keys that no row sees must not reach O (their weights are 0, but
         // 0 x inf is not): their V counts as zeros.  Of the keys that some rows
@@ -983,6 +1017,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             slow = __any_sync(0xffffffffu, bad);
         }
         int cut = slow ? lim_min : lim_max;
+        bool again = false;                              // with what the first part left
 #pragma unroll 1
         for (;;) {
             // volatile: in local memory, not in registers that the usual way needs
@@ -1015,7 +1050,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                             if constexpr (A::PT == 2) {
                                 const float2 b =
                                     __half22float2(*reinterpret_cast<const __half2*>(&c));
-                                wb[nr][A::PT - 1][k] = movm(packh(u - b.x, v - b.y));
+                                wb[nr][A::PT - 1][k] = movm(packh((u - b.x) * REST, (v - b.y) * REST));
                             }
                         } else {
                             const uint32_t c = packb(u, v);
@@ -1085,11 +1120,20 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                                 e4m3x4(__byte_perm(v[2][i], v[3][i], sel), a[y][2], a[y][3]);
                             }
 #pragma unroll
-                            for (int q = 0; q < A::PT; ++q)
+                            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) mma_o(nr, 2 * i + y, a[y], 0);
+                            if constexpr (A::PT == 2) {
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) a[y][k] = scale_f16(a[y][k]);
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                    for (int y = 0; y < 2; ++y) mma_o(nr, 2 * i + y, a[y], q);
+                                    for (int y = 0; y < 2; ++y)
+                                        mma_o(nr, 2 * i + y, a[y], A::PT - 1);
+                            }
                         }
                     } else {
                         uint32_t a[4][4];
@@ -1109,15 +1153,38 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                     }
                 }
             }
-            if (!slow) break;
+            if (slow) {
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int i = 0; i < A::NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (limit(nr, e & 1) != cut) o[nr][i][e] = keep[nr][i][e];
+                if (++cut <= lim_max) continue;
+            }
+            if (!rest) break;
+            // once more with what the weights' fp16 part left, REST times as large,
+            // into outputs as many times as large
+            const float f = again ? 1.0f / REST : REST;
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int i = 0; i < A::NT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (limit(nr, e & 1) != cut) o[nr][i][e] = keep[nr][i][e];
-            if (++cut > lim_max) break;
+                    for (int e = 0; e < 4; ++e) o[nr][i][e] *= f;
+            if (again) break;
+            again = true;
+            cut = slow ? lim_min : lim_max;
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int h = 0; h < NS; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float u = x[nr][h][e];
+                        x[nr][h][e] = (u - __half2float(__float2half_rn(u))) * REST;
+                    }
         }
     };
 

@@ -174,3 +174,82 @@ def test_large_temperatures(io):
         out, ws = chain.run(x)
         chain.check(x, out)
         assert binding.spec_status_read(ws) == 0
+
+
+# --------------------------------------------- attention: a few keys against very many
+
+def long_request(L, T, sink, tail, first, io="bf16", kv="e4m3", Hq=4, D=128, page=256, seed=0):
+    """One request whose first key has a score of log(L) + sink over the others'
+    (equal ones, or normal ones of standard deviation 2 nats), and a first value of
+    zeros, of one large element, or like the others; page table in order."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = L + T
+    cols = -(-n // page)
+    cfg = binding.paged_cfg(B=1, T=T, Hq=Hq, Hkv=1, D=D, page=page, n_pages=cols, max_pages=cols,
+                            io=io, kv=kv)
+    rows = cols * page
+    k = torch.zeros(rows, D, device="cuda")
+    a = float(torch.tensor(2.0 * D ** 0.5).bfloat16())     # q = a on the first element: 2 nats a unit
+    if tail == "normal":
+        k[:, 0] = torch.randn(rows, generator=g, device="cuda").to(torch.float8_e4m3fn).float()
+    k[0, 0] = float(torch.tensor((np.log(L) + sink) / 2).to(torch.float8_e4m3fn))
+    v = torch.randn(rows, D, generator=g, device="cuda")
+    v[0] *= {"zeros": 0, "one": 0, "like": 1}[first]
+    if first == "one":
+        v[0, 3] = 2000.0
+    c = dict(cfg=cfg)
+    if kv == "e4m3":
+        scale = torch.where(v.abs().amax(-1) == 0, 1.0, v.abs().amax(-1) / 448)
+        vc = (v / scale[:, None]).to(torch.float8_e4m3fn)
+        pools, scales = [k.to(torch.float8_e4m3fn), vc], [torch.ones(rows, device="cuda"), scale]
+        c["k"], c["v"] = k.double(), vc.double() * scale.double()[:, None]
+        scales = [s.view(cols, 1, page).contiguous() for s in scales]
+    else:
+        pools, scales = [x.to(chain.DT[io]) for x in (k, v)], [None, None]
+        c["k"], c["v"] = (p.double() for p in pools)
+    q = torch.zeros(1, T, Hq, D, device="cuda")
+    q[..., 0] = a
+    c["q"] = q.to(chain.DT[io])
+    c["kv"] = binding.PagedKV(cfg, *(p.view(cols, 1, page, D).contiguous() for p in pools),
+                              torch.arange(cols, dtype=torch.int32, device="cuda").view(1, cols),
+                              torch.full((1,), L, dtype=torch.int32, device="cuda"), *scales)
+    c["L"] = L
+    return c
+
+
+def attend_and_bound(c, sums):
+    """The library's output, the 64-bit one, and the bound of their difference:
+    the terms of tests/test_gpu_paged.py, but for `sums` roundings of 2^-23 on the
+    way of a weight or product through the fp32 sums."""
+    cfg = c["cfg"]
+    o = torch.full_like(c["q"], 7.0)
+    ws = binding.alloc_paged_workspace(cfg)
+    binding.attn_decode_paged(cfg, c["kv"], c["q"], o, ws)
+    assert binding.spec_status_read(ws) == 0
+    want, A = torch.zeros_like(o, dtype=torch.float64), torch.zeros_like(o, dtype=torch.float64)
+    z = 0.0
+    for i in range(cfg.T):
+        n = c["L"] + i + 1
+        k, v, q = c["k"][:n], c["v"][:n], c["q"][0, i].double()
+        w = torch.softmax(q @ k.T / cfg.D ** 0.5, -1)
+        want[0, i], A[0, i] = w @ v, w @ v.abs()
+        z = max(z, float((q.abs() @ k.abs().T).max()) / cfg.D ** 0.5)
+    d = (32 * 2.0 ** -23 + 2 * 2.0 ** -21) * z + 2.0 ** -20
+    q8, bf = cfg.kv_dtype == binding.SPEC_KV_E4M3, cfg.io_dtype == binding.SPEC_IO_BF16
+    cw = (2.0 ** -11 if q8 else 2.0 ** -16) if bf else 2.0 ** -20
+    tol = (2.0 ** -8 if bf else 2.0 ** -24) * want.abs() + (cw + 2 * d + sums * 2.0 ** -23) * A + 1e-37
+    return o.double(), want, tol
+
+
+@pytest.mark.parametrize("io,kv", [("bf16", "e4m3"), ("f32", "e4m3"), ("bf16", "io")])
+@pytest.mark.parametrize("L,T", [(8192, 1), (8191, 4), (32768, 1), (131071, 1), (131070, 5)])
+@pytest.mark.parametrize("sink,tail,first", [(0.0, "equal", "zeros"), (5.0, "equal", "zeros"),
+                                             (0.0, "equal", "one"), (0.0, "equal", "like"),
+                                             (2.0, "normal", "zeros"), (2.0, "normal", "one")])
+def test_one_key_against_all_others(L, T, sink, tail, first, io, kv):
+    """Weights far below the largest one count by their sum.  (A weight goes into
+    a sum with each 16 keys of its warp, one key warp of seven or more having at
+    most every 8th part of a CTA's, and is joined over at most 200 parts.)"""
+    got, want, tol = attend_and_bound(long_request(L, T, sink, tail, first, io, kv), L / 16 + 200)
+    bad = (got - want).abs() > tol
+    assert not bad.any(), float(((got - want).abs() / tol).max())
