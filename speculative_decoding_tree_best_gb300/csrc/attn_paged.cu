@@ -6,9 +6,8 @@
 // pass, kept per warp and joined at the end (the maxima, sums and outputs of
 // two parts a, b join as m = max(m_a, m_b), o = o_a 2^(m_a - m) + o_b 2^(m_b - m)).
 // In an 8-bit cache a value is code * scale per row: the key's scale multiplies
-// the score; the value's scale goes into the weight's exponent,
-// w'_k = 2^(x_k + log2 scale_k - m) with m the maximum over x_k + log2 scale_k
-// (up to a factor of 2^SLACK, below), so that the weights that meet the codes are
+// the score, the value's the weight, w'_k = 2^(x_k - m) scale_k with m the maximum
+// over x_k + log2 scale_k, scales below 2^LOW counting as that there (up to a factor of 2^SLACK, below), so that the weights that meet the codes are
 // at most 2^(SLACK + LIFT) whatever the scales.
 //
 // What bounds it: reading the cache, 2 D values a key and kv-head against
@@ -65,8 +64,8 @@ using tc::smem_u32;
 
 constexpr int SUB = 16;                // keys per product tile: the smallest page
 constexpr int MAX_RTC = 3;             // row tiles per CTA, at most (paged_row_tiles)
-// log2 of how far a weight may be above that of the maximum (0 to 4: 8 requests of
-// drafts about 1 us less)
+// log2 of how far a weight may be above that of the maximum: few granules then
+// change the maximum (8 instead of 0 gave 8 requests of drafts 40.6 -> 39.6 us)
 constexpr float SLACK = 4.0f;
 // fp16 weights: 2^LIFT times as large, up to 2^(SLACK + LIFT) = 2^15, so that fewer
 // of them fall below fp16's normal range (with 8 and 7, drafts 40.8 us instead of
@@ -74,8 +73,12 @@ constexpr float SLACK = 4.0f;
 // do, 39.6 and 327, but long flat tails are lost).  What a weight's fp16 part
 // leaves goes times REST, against codes, or into outputs, that are scaled to match
 // (exact: codes are multiples of 2^-9).
-constexpr float LIFT = 11.0f;
+constexpr float LIFT = 11.0f, LIFT_INV = 0x1p-11f;
 constexpr float REST = 0x1p12f;
+// log2 of the least scale that the maximum goes by (the least that kv_page_append
+// writes): a weight in the softmax's sum is at most 2^(SLACK - LOW), of which 2^23
+// are within fp32's range, also where all values so far are zeros by a scale of 0
+constexpr float LOW = -100.0f;
 constexpr int MAX_SLOTS = 64;          // granules in a CTA's ring, at most
 
 // ---- instruction wrappers -------------------------------------------------------------
@@ -131,10 +134,9 @@ __device__ __forceinline__ void arrive_n(uint64_t* bar, int n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
                  : "memory");
 }
-// log2 of a scale; 0 counts as 2^-126, a NaN stays
 __device__ __forceinline__ float log2_scale(float x) {
     float y;
-    asm("max.NaN.f32 %0, %1, 0f00800000;\n\tlg2.approx.f32 %0, %0;" : "=f"(y) : "f"(x));
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t packh(float lo, float hi) {
@@ -752,7 +754,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 if (tok >= p.T) continue;
                 const float sum = e ? l1 : l0;
                 const bool real = tok < n && sum != 0.0f;
-                const float inv = real ? 1.0f / sum : 0.0f;
+                const float inv = real ? (A::Q8 ? LIFT_INV : 1.0f) / sum : 0.0f;
                 T* dst = static_cast<T*>(p.o) +
                          (((size_t)b * p.T + tok) * p.Hq + hk * p.G + r0 + e - tok * p.G) * D;
 #pragma unroll
@@ -884,7 +886,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
         // scores in log2 units, -inf where the row does not see the key
         const bool masked = kb + (h0 + NS) * SUB > lim_min || part != (1u << NS) - 1u;
-        float lv[NS][2];
+        float sv[NS][2];                                 // the values' scales
 #pragma unroll
         for (int h = 0; h < NS; ++h) {
             float kf[2] = {1.0f, 1.0f};
@@ -892,8 +894,8 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 const float* sc = scales + slot * 2 * GK + (h0 + h) * SUB + kr;
                 kf[0] = sc[0];
                 kf[1] = sc[8];
-                lv[h][0] = log2_scale(sc[GK]);
-                lv[h][1] = log2_scale(sc[GK + 8]);
+                sv[h][0] = sc[GK];
+                sv[h][1] = sc[GK + 8];
             }
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
@@ -917,7 +919,13 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         // weights are then at most 2^(SLACK + LIFT), which fp16 holds, and most granules do
         // without the shuffles.
         bool grow = false;
-        float nm[NR][2];
+        float nm[NR][2], lv[NS][2];
+        if constexpr (A::Q8) {
+#pragma unroll
+            for (int h = 0; h < NS; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) lv[h][k] = fmaxf(log2_scale(sv[h][k]), LOW);
+        }
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -964,12 +972,12 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 for (int e = 0; e < 4; ++e) {
                     const float d = x[nr][h][e] - ((e & 1) ? b1 : b0);
                     const float pl = ex2(d);
-                    l[nr][e & 1] += pl;
+                    l[nr][e & 1] = A::Q8 ? fmaf(pl, LIFT_INV, l[nr][e & 1]) : l[nr][e & 1] + pl;
                     // the scale of a key that is not seen may be anything
                     if (A::Q8 && masked && x[nr][h][e] == -INFINITY)
                         x[nr][h][e] = 0.0f;
                     else
-                        x[nr][h][e] = A::Q8 ? ex2(d + lv[h][e >> 1]) : pl;
+                        x[nr][h][e] = A::Q8 ? pl * sv[h][e >> 1] : pl;
                     least = min(least, __float_as_uint(x[nr][h][e]));
                 }
         }

@@ -253,3 +253,32 @@ def test_one_key_against_all_others(L, T, sink, tail, first, io, kv):
     got, want, tol = attend_and_bound(long_request(L, T, sink, tail, first, io, kv), L / 16 + 200)
     bad = (got - want).abs() > tol
     assert not bad.any(), float(((got - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("least", [0.0, 2.0 ** -120])
+def test_values_of_zeros_by_their_scale(io, T, least):
+    """A scale of 0 (or next to it) stands for a row of zeros: it counts in the
+    softmax's sum, before and behind values of ordinary size, and alone."""
+    lens = [700, 700, 700, 9000, 60]
+    x = Case(lens, T=T, Hq=8, Hkv=2, D=128, page=32, io=io, kv="e4m3", seed=41)
+    for b, zero in enumerate((slice(0, 690), slice(10, 700 + T), slice(0, 700 + T, 2), slice(0, 8000),
+                              slice(0, 60 + T))):
+        x.scale["v"][b, zero] = least
+    x.upload()
+    o = x.attend()
+    x.check(o)
+    assert (o[4] == 0).all() or least > 0
+    assert x.status() == 0
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -60, 2.0 ** 60, 2.0 ** 100])
+def test_values_all_very_small_or_very_large(io, T, scale):
+    x = Case([300, 5000], T=T, Hq=8, Hkv=2, D=64, page=16, io=io, kv="e4m3", seed=42)
+    x.scale["v"] = (x.scale["v"] / x.scale["v"].max() * np.float32(scale)).astype(np.float32)
+    x.upload()
+    x.check(x.attend())
+    assert x.status() == 0
