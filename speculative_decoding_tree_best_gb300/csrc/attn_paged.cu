@@ -36,8 +36,14 @@
 // with bf16 outputs (2^-11, an eighth of the output's own rounding) unless a tile
 // has weights below fp16's normal range (2^-25 of the largest so far), two parts
 // there and with fp32 outputs (2^-22), the second REST times as large, so that what
-// is left of a weight is at most 2^-48 of the largest; and an fp32 cache, q and weights as
-// three bf16 parts each (2^-24).
+// is left of a weight is at most 2^-48 of the largest; and an fp32 cache, q and
+// weights as three bf16 parts each, without the products of parts beyond 2^-24.
+// The tensor cores cut a sum off at its last bit, towards 0.  With bf16 outputs
+// that is let be (131072 keys in one CTA: 1200 steps a warp, 2^-24 each on average,
+// under a twentieth of the output's rounding).  With fp32 outputs each 16 keys' or
+// elements' products start at 0 and are added to the rest in fp32: over 8192 keys
+// 2.8e-7 of the output is lost instead of 6.9e-6 (all errors 5.2e-7 instead of
+// 7.7e-6), for 2 to 3 % of the time, 10 to 17 % with more than eight rows.
 //
 // Measured (graph replays, bytes of K, V and scales over time): 8 x 131072 keys,
 // 8 kv-heads, 8 bits 326 us, 6.8 TB/s, the rate of a plain copy; 24 requests of
@@ -839,36 +845,54 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                         e4m3x4(w0[h][i], a[h][0], a[h][2]);
                         e4m3x4(w1[h][i], a[h][1], a[h][3]);
                     }
-#pragma unroll
-                    for (int q = 0; q < A::QT; ++q)
+                    if constexpr (A::QT == 1) {
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr) {
-                            const uint2 b = q_of(nr, q, j, i);
+                            const uint2 b = q_of(nr, 0, j, i);
 #pragma unroll
                             for (int h = 0; h < NS; ++h) mma_f16_16816(x[nr][h], a[h], b.x, b.y);
                         }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < NS; ++h)
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr) {
+                                float y[4] = {};
+#pragma unroll
+                                for (int q = A::QT - 1; q >= 0; --q) {
+                                    const uint2 b = q_of(nr, q, j, i);
+                                    mma_f16_16816(y, a[h], b.x, b.y);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) x[nr][h][e] += y[e];
+                            }
+                    }
                 }
             } else if constexpr (A::F32) {
-                uint32_t a[NS][3][4];
 #pragma unroll
-                for (int h = 0; h < NS; ++h)
+                for (int h = 0; h < NS; ++h) {
+                    uint32_t a[3][4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t* w = k % 2 ? w1[h] : w0[h];
                         split3x2(__uint_as_float(w[k / 2 * 2]), __uint_as_float(w[k / 2 * 2 + 1]),
-                                 a[h][0][k], a[h][1][k], a[h][2][k]);
+                                 a[0][k], a[1][k], a[2][k]);
                     }
+                    float y[NR][4] = {};
 #pragma unroll
-                for (int q = 2; q >= 0; --q)                  // parts i + q <= 2: 2^-24 is left
+                    for (int q = 2; q >= 0; --q)              // parts i + q <= 2: 2^-24 is left
 #pragma unroll
-                    for (int i = 2 - q; i >= 0; --i)
+                        for (int i = 2 - q; i >= 0; --i)
 #pragma unroll
-                        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                            for (int h = 0; h < NS; ++h) {
+                            for (int nr = 0; nr < NR; ++nr) {
                                 const uint2 b = q_of(nr, q, j, 0);
-                                mma_bf16_16816(x[nr][h], a[h][i], b.x, b.y);
+                                mma_bf16_16816(y[nr], a[i], b.x, b.y);
                             }
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[nr][h][e] += y[nr][e];
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -1108,6 +1132,7 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                                 split3x2(__uint_as_float(v[i / 2 * 2][2 * r + i % 2]),
                                          __uint_as_float(v[i / 2 * 2 + 1][2 * r + i % 2]),
                                          a[r][0][i], a[r][1][i], a[r][2][i]);
+                        float y[NR][2][4] = {};
 #pragma unroll
                         for (int q = 2; q >= 0; --q)
 #pragma unroll
@@ -1115,7 +1140,15 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                    for (int r = 0; r < 2; ++r) mma_o(nr, j * 2 + r, a[r][i], q);
+                                    for (int r = 0; r < 2; ++r)
+                                        mma_bf16_16816(y[nr][r], a[r][i], wb[nr][q][0],
+                                                       wb[nr][q][1]);
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[nr][j * 2 + r][e] += y[nr][r][e];
                     } else if constexpr (A::Q8) {
                         constexpr int NW = A::ROWB == 64 ? 2 : 4;
 #pragma unroll
@@ -1127,20 +1160,30 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                                 e4m3x4(__byte_perm(v[0][i], v[1][i], sel), a[y][0], a[y][1]);
                                 e4m3x4(__byte_perm(v[2][i], v[3][i], sel), a[y][2], a[y][3]);
                             }
-#pragma unroll
-                            for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) mma_o(nr, 2 * i + y, a[y], 0);
-                            if constexpr (A::PT == 2) {
-#pragma unroll
-                                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) a[y][k] = scale_f16(a[y][k]);
+                            if constexpr (A::PT == 1) {
 #pragma unroll
                                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                                    for (int y = 0; y < 2; ++y)
-                                        mma_o(nr, 2 * i + y, a[y], A::PT - 1);
+                                    for (int y = 0; y < 2; ++y) mma_o(nr, 2 * i + y, a[y], 0);
+                            } else {
+                                // (the small part last: the codes are scaled in place)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    float z[NR][4] = {};
+#pragma unroll
+                                    for (int nr = 0; nr < NR; ++nr)
+                                        mma_f16_16816(z[nr], a[y], wb[nr][0][0], wb[nr][0][1]);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) a[y][k] = scale_f16(a[y][k]);
+#pragma unroll
+                                    for (int nr = 0; nr < NR; ++nr) {
+                                        mma_f16_16816(z[nr], a[y], wb[nr][A::PT - 1][0],
+                                                      wb[nr][A::PT - 1][1]);
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            o[nr][2 * i + y][e] += z[nr][e];
+                                    }
+                                }
                             }
                         }
                     } else {

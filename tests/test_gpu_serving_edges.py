@@ -282,3 +282,42 @@ def test_values_all_very_small_or_very_large(io, T, scale):
     x.upload()
     x.check(x.attend())
     assert x.status() == 0
+
+
+@pytest.mark.parametrize("kv", ["io", "e4m3"])
+@pytest.mark.parametrize("T,D", [(1, 64), (1, 128), (4, 64), (4, 128)])
+def test_nothing_systematic_is_lost_in_fp32(kv, T, D):
+    """The part of the error that goes with the output itself: sum of error x output
+    over sum of output squared.  Roundings to nearest have no such part.  What has:
+    an accumulator cut off by 2^-23 at most once per chunk of products, and products
+    of third parts left out, on average below 2^-23 of a product: together 2^-22 of
+    the output, and as much of each score, which moves weights by 2^-22 times the
+    largest score."""
+    B, L, Hkv, G, page = 6, 9000, 8, 4, 64
+    g = torch.Generator(device="cuda").manual_seed(D + T)
+    cols = -(-(L + T) // page)
+    cfg = binding.paged_cfg(B=B, T=T, Hq=Hkv * G, Hkv=Hkv, D=D, page=page, n_pages=B * cols,
+                            max_pages=cols, io="f32", kv=kv)
+    pools = [torch.randn(B * cols, Hkv, page, D, generator=g, device="cuda") for _ in range(2)]
+    scales = [None, None]
+    if kv == "e4m3":
+        scales = [p.abs().amax(-1) / 448 for p in pools]
+        pools = [(p / s[..., None]).to(torch.float8_e4m3fn) for p, s in zip(pools, scales)]
+    cache = binding.PagedKV(cfg, *pools, torch.arange(B * cols, dtype=torch.int32, device="cuda").view(B, cols),
+                            torch.full((B,), L, dtype=torch.int32, device="cuda"), *scales)
+    q = 2 * torch.randn(B, T, Hkv * G, D, generator=g, device="cuda")
+    o = torch.empty_like(q)
+    binding.attn_decode_paged(cfg, cache, q, o, binding.alloc_paged_workspace(cfg))
+    along, square, z = 0.0, 0.0, 0.0
+    for b in range(B):
+        for h in range(Hkv):
+            k, v = (p[b * cols:(b + 1) * cols, h].double() * (1 if s is None else
+                    s[b * cols:(b + 1) * cols, h].double()[..., None]) for p, s in zip(pools, scales))
+            k, v = k.reshape(-1, D), v.reshape(-1, D)
+            for i in range(T):
+                s = q[b, i, h * G:(h + 1) * G].double() @ k[:L + i + 1].T / D ** 0.5
+                want = torch.softmax(s, -1) @ v[:L + i + 1]
+                along += float(((o[b, i, h * G:(h + 1) * G].double() - want) * want).sum())
+                square += float((want * want).sum())
+                z = max(z, float(s.abs().max()))
+    assert abs(along / square) <= (1 + z) * 2.0 ** -22, (along / square, z)
