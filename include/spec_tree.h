@@ -589,7 +589,7 @@ typedef struct spec_draft_cfg {
 } spec_draft_cfg;
 
 typedef struct spec_draft_out {
-    int32_t *accept_len;     /* [B] tau in [1, n_draft + 1]: drafts kept + 1 */
+    int32_t *accept_len;     /* [B] tau in [1, n_draft + 1]: drafts kept + 1; 0: no request */
     int32_t *out_tok;        /* [B][N+1] kept drafts, then the drawn token, -1 beyond tau */
     float *target_prob;      /* [B][N] p_i of draft i (0 beyond n_draft); NULL when N = 0 */
 } spec_draft_out;
@@ -613,7 +613,9 @@ size_t spec_draft_workspace_bytes(const spec_draft_cfg *cfg, int num_sms);
  * draws v with its weight's share.  N = 0 is plain sampling of one token.
  *   draft_tok [B][N] int32, draft_prob NULL (drafts are point masses, q = 1) or
  *   [B][N][V] float >= 0, u [B][N] float (these may be NULL when N = 0);
- *   n_draft NULL (N each) or [B], in [0, N] (else clamped, SPEC_DEV_BADREQ);
+ *   n_draft NULL (N each) or [B], in [0, N], or -1: no request in that slot
+ *   (accept_len 0, out_tok -1, kv_len and root_tok as they were; its inputs do
+ *   not count) (else clamped, SPEC_DEV_BADREQ);
  *   logits [B][N+1][V] io (rows beyond n_draft are not read);
  *   e [B][V] float > 0 (scores beyond fp32's range tie);
  *   kv_len, root_tok  NULL, or [B]: advanced by tau / replaced by the drawn token.

@@ -736,8 +736,9 @@ def draft_verify_sampled(cfg: SpecDraftCfg, draft_tok, draft_prob, logits, u, e,
                          stream=None):
     """Verify drafted chains from given random numbers: draft_tok int32 [B][N],
     draft_prob f32 [B][N][V] or None (point masses), logits io [B][N+1][V], u
-    f32 [B][N], e f32 [B][V]; kv_len / root_tok are advanced when given.  With
-    N = 0 (plain sampling) draft_tok, draft_prob and u are not read."""
+    f32 [B][N], e f32 [B][V]; kv_len / root_tok are advanced when given.  n_draft
+    int32 [B], -1 where a slot has no request, or None (N each).  With N = 0
+    (plain sampling) draft_tok, draft_prob and u are not read."""
     dev, f32, i32 = _get_device(), torch.float32, torch.int32
     p = _plan(cfg, bytes(cfg), dev)
     if cfg.N == 0:

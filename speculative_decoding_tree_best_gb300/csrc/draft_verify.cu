@@ -102,6 +102,11 @@ template <int IO> struct grp {
     }
 };
 
+// Drafts of request b; -1 where there is no request.
+__device__ __forceinline__ int drafts(const int32_t* n_draft, int b, int N, uint32_t& bits) {
+    return n_draft && n_draft[b] == -1 ? -1 : new_rows(n_draft, b, N, bits);
+}
+
 template <int IO>
 __global__ void __launch_bounds__(NT)
 row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
@@ -114,7 +119,7 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
     pdl_wait();
     // the second launch may start: it waits for this one's results
     pdl_trigger();
-    if (i > new_rows(n_draft, b, c.N, ignore)) return;
+    if (i > drafts(n_draft, b, c.N, ignore)) return;
     // the row's own 16-byte groups [g0, g1), and the elements beside them
     const int64_t r0 = (int64_t)row * c.V, r1 = r0 + c.V;
     const int64_t g0 = (r0 + VEC - 1) / VEC, g1 = r1 / VEC;
@@ -258,7 +263,7 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     const int first = lo + tid * VEC;
     if (vec) load_e(first);
     uint32_t bits = 0;
-    const int n = new_rows(a.n_draft, b, N, bits);
+    const int n = drafts(a.n_draft, b, N, bits);
     if (tid < n) {
         const int x = a.draft_tok[(size_t)b * N + tid];
         const bool in = x >= 0 && x < V;
@@ -270,6 +275,13 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     }
     if (bits && blockIdx.x == 0) raise_status(a.ws, bits);
     pdl_wait();
+    if (n < 0) {                                         // no request
+        if (blockIdx.x > 0) return;
+        if (tid <= N) a.out.out_tok[(size_t)b * (N + 1) + tid] = -1;
+        if (tid < N) a.out.target_prob[(size_t)b * N + tid] = 0.0f;
+        if (tid == 0) a.out.accept_len[b] = 0;
+        return;
+    }
 
     // ---- the rows' masses (a warp per row) and the chain
     for (int i = warp; i <= n; i += NT / 32) {

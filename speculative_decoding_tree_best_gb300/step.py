@@ -250,7 +250,8 @@ class ChainStep:
     drafts: per attention layer the new tokens' rows are appended and attended
     from (attend), then the drafts are verified (verify), which advances kv_len
     over what was kept.  A step of request b has n_draft[b] + 1 new tokens: the
-    pending token and its drafts; with n_draft 0 it is a plain decode step.
+    pending token and its drafts; with n_draft 0 it is a plain decode step, and
+    with n_draft -1 the slot has no request: it is neither written nor advanced.
 
     The layers share one page table, kv_len and root_tok, which the caller
     owns the contents of (page_table names the pages of each request; a page

@@ -321,3 +321,79 @@ def test_nothing_systematic_is_lost_in_fp32(kv, T, D):
                 square += float((want * want).sum())
                 z = max(z, float(s.abs().max()))
     assert abs(along / square) <= (1 + z) * 2.0 ** -22, (along / square, z)
+
+
+# ------------------------------------------------------------ slots without a request
+
+@pytest.mark.parametrize("V", [997, 40000])
+@pytest.mark.parametrize("N", [0, 3])
+def test_verification_leaves_slots_without_a_request_out(N, V):
+    x = chain.make(6, N, V, seed=30)
+    x["n"] = np.array([N, -1, 0, -1, N, -1], np.int32)
+    x["logits"][1::2] = np.nan
+    kv = torch.arange(6, dtype=torch.int32, device="cuda")
+    root = torch.full((6,), 77, dtype=torch.int32, device="cuda")
+    ws = None
+    for _ in range(2):                                     # counters are at zero again
+        out, ws = chain.run(x, kv_len=kv, root=root, ws=ws)
+    assert binding.spec_status_read(ws) == 0
+    assert out.accept_len[1::2].tolist() == [0, 0, 0]
+    assert (out.out_tok[1::2] == -1).all() and (out.target_prob[1::2] == 0).all()
+    assert kv[1::2].tolist() == [1, 3, 5] and root[1::2].tolist() == [77] * 3
+    live = dict(x, logits=x["logits"][::2], q=x["q"][::2], toks=x["toks"][::2], u=x["u"][::2],
+                e=x["e"][::2], n=x["n"][::2])
+    got = binding.DraftBuffers(binding.draft_cfg(B=3, N=N, V=V))
+    for name in ("accept_len", "out_tok", "target_prob"):
+        getattr(got, name).copy_(getattr(out, name)[::2])
+    chain.check(live, got)
+    assert kv[::2].tolist() == [2 * i + 2 * int(a) for i, a in enumerate(got.accept_len)]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_with_slots_without_a_request(captured):
+    """A request joins a batch whose other slots are empty and own no page; whole
+    steps run eagerly or as one replayed graph."""
+    from speculative_decoding_tree_best_gb300 import step
+    B, N, V, Hq, Hkv, D, layers = 4, 2, 3001, 8, 2, 64, 2
+    pc = binding.paged_cfg(B=B, T=N + 1, Hq=Hq, Hkv=Hkv, D=D, page=16, n_pages=8, max_pages=4, kv="e4m3")
+    st = step.ChainStep(pc, binding.draft_cfg(B=B, N=N, V=V), layers)
+    st.n_draft.fill_(-1)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    f = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    rows = [[f(B, N + 1, h, D) for h in (Hq, Hkv, Hkv)] for _ in range(layers)]
+    x = chain.make(B, N, V, seed=31)
+    logits = torch.from_numpy(x["logits"]).bfloat16().cuda()
+    d = [torch.from_numpy(x[c]).cuda() for c in ("toks", "q", "u", "e")]
+
+    def run():
+        o = [st.attend(i, *r) for i, r in enumerate(rows)]
+        st.verify(logits, *d)
+        return o
+    run()
+    assert st.kv_len.tolist() == [0] * B and st.status() == 0
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o = run()
+        go = graph.replay
+    else:
+        go = run
+    at = 0
+    for s in range(5):
+        if s == 2:                                         # slot 1 gets a request and two pages
+            st.page_table[1, :2] = torch.tensor([5, 2], dtype=torch.int32)
+            st.n_draft[1] = N
+        before = [c.k_pages.view(torch.uint8).clone() for c in st.caches]
+        r = go()
+        o = r if r is not None else o
+        torch.cuda.synchronize()
+        assert st.status() == 0
+        lens = st.out.accept_len.tolist()
+        at += lens[1]
+        assert [lens[i] for i in (0, 2, 3)] == [0, 0, 0] and (lens[1] > 0) == (s >= 2)
+        assert st.kv_len.tolist() == [0, at, 0, 0]
+        for i in range(layers):
+            assert (o[i][[0, 2, 3]] == 0).all() and bool((o[i][1] != 0).any()) == (s >= 2)
+            changed = (st.caches[i].k_pages.view(torch.uint8) != before[i]).flatten(1).any(1)
+            assert set(changed.nonzero().flatten().tolist()) <= ({5, 2} if s >= 2 else set())
