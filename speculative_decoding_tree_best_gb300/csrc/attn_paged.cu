@@ -769,8 +769,9 @@ attn_paged(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                                    2 * ((i + k) % (A::RL / 2));
                     const float u = real ? (e ? y[k].y : y[k].x) * inv : 0.0f;
                     const float v = real ? (e ? y[k].w : y[k].z) * inv : 0.0f;
-                    bad |= !(fabsf(u) <= 3.4028234663852886e38f &&
-                             fabsf(v) <= 3.4028234663852886e38f);
+                    // from MOST on the output's type has no finite number
+                    constexpr float MOST = IO == SPEC_IO_F32 ? INFINITY : 0x1.ffp127f;
+                    bad |= !(fabsf(u) < MOST && fabsf(v) < MOST);
                     if constexpr (IO == SPEC_IO_F32)
                         *reinterpret_cast<float2*>(dst + d0) = make_float2(u, v);
                     else

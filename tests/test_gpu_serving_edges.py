@@ -397,3 +397,17 @@ def test_steps_with_slots_without_a_request(captured):
             assert (o[i][[0, 2, 3]] == 0).all() and bool((o[i][1] != 0).any()) == (s >= 2)
             changed = (st.caches[i].k_pages.view(torch.uint8) != before[i]).flatten(1).any(1)
             assert set(changed.nonzero().flatten().tolist()) <= ({5, 2} if s >= 2 else set())
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_outputs_that_round_to_infinity_are_reported(T):
+    """448 x 7.59e35 is finite in fp32 and beyond bf16's largest number."""
+    x = Case([40], T=T, Hq=4, Hkv=1, D=64, page=16, kv="e4m3", seed=50)
+    x.vals["v"][:] = 448.0
+    x.scale["v"][:] = np.float32(7.59e35)
+    x.upload()
+    assert torch.isinf(x.attend()).all()
+    assert x.status() == binding.SPEC_DEV_RANGE
+    x.scale["v"][:] = np.float32(7.56e35)
+    x.upload()
+    assert torch.isfinite(x.attend()).all() and x.status() == 0
