@@ -46,13 +46,14 @@
 // 7.7e-6), for 2 to 3 % of the time, 10 to 17 % with more than eight rows.
 //
 // Measured (graph replays, bytes of K, V and scales over time): 8 x 131072 keys,
-// 8 kv-heads, 8 bits 326 us, 6.8 TB/s, the rate of a plain copy; 24 requests of
+// 8 kv-heads, 8 bits 323-328 us, 6.8 TB/s, the rate of a plain copy; 24 requests of
 // 1024-8192 keys bf16 72 us (6.2 TB/s), 8 bits 45 us (5.1 TB/s: two or three
 // segments a CTA, whose ends the ring does not hide); one request of 4096 keys
 // bf16 9.3 us, of which reading is 2.5: lengths, page ids and copies follow one
 // another (3000 cycles), then parts are counted in (2700) and joined (5500).  8
-// requests of 4096-8192 keys and 1-8 new tokens, 8 bits: 40 us (2.5 TB/s), by the
-// conversions and products, done for each 16 rows.
+// requests of 4096-8192 keys and 1-8 new tokens, 8 bits: 41 us (2.4 TB/s), by the
+// conversions and products, done for each 16 rows; 16, 32, 128 new tokens each, 82,
+// 181, 647 us: beyond 48 rows a kv-head the cache is read again for each 48.
 #include <cuda.h>
 #include <math.h>
 
@@ -1633,7 +1634,9 @@ cudaError_t attn_t(const spec_paged_cfg& c, const spec_paged_kv& kv, const void*
     // ten with 168, Q in shared memory (8 requests x 32 rows, 8-bit cache: 49.7
     // us; seven with 255: 59.9), and a second producer, which the warps' number
     // leaves registers for (43.8 -> 42.6 us).  In fp32 a granule at D = 128 is 32
-    // KB, and the ring must have a slot per key warp.
+    // KB, and the ring must have a slot per key warp; more than eight rows there take
+    // 255 registers and spill 384 bytes (8 requests of 4096-8192 keys, 8 tokens: 315 us
+    // over 57 of reading; fp32 over 8 bits spills 276 bytes: 83 us over 15).
     constexpr bool big = At<IO, KV, D, 1>::SLOT > 16384;
     if (paged_row_tiles(c).nr == 1)
         return attn_launch<IO, KV, D, 1, big ? 6 : 7, false, 1>(c, kv, q, n_new, o, ws, st);

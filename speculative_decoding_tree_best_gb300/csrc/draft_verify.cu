@@ -22,7 +22,7 @@
 //      the chain ended; the request's last CTA (a ticket) joins the slices and
 //      writes the outputs.
 // Measured (graph replays, V = 151936, bf16, a drafter's rows in fp32): one request
-// of 8 drafts 9.2 us, two launches' latency; 24 requests of up to 8 drafts 20.6 us,
+// of 8 drafts 9.2 us, two launches' latency; 24 requests of up to 8 drafts 20.9 us,
 // 65 MB at 3.2 TB/s: each launch is a chain (loads, block reduction; masses,
 // decision, loads, reduction, ticket) of which reading is about half.
 #include <math.h>
@@ -117,7 +117,9 @@ row_mass(spec_draft_cfg c, const int32_t* __restrict__ n_draft,
     const int b = row / (c.N + 1), i = row % (c.N + 1);
     uint32_t ignore = 0;
     pdl_wait();
-    // the second launch may start: it waits for this one's results
+    // The second launch may start: it waits for this one's results.  It reads the
+    // caller's inputs before, which is sound because this wait comes first in every
+    // CTA: whatever wrote them has ended by then.
     pdl_trigger();
     if (i > drafts(n_draft, b, c.N, ignore)) return;
     // the row's own 16-byte groups [g0, g1), and the elements beside them
@@ -232,7 +234,7 @@ template <int IO>
 __global__ void __launch_bounds__(NT)
 race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     using T = typename io_t<IO>::T;
-    // tokens per group, groups under way at once: 2 and 70 registers, so that
+    // tokens per group, groups under way at once: 2 and 72 registers, so that
     // three CTAs share an SM (before the scores below, 24 requests 22.1 us; 1:
     // 23.4, 4 on two CTAs: 28)
     constexpr int VEC = 8, U = 2;
@@ -322,7 +324,8 @@ race(spec_draft_cfg c, const __grid_constant__ RaceArgs a) {
     // the race 45 instructions a token.)
     // (top_lo is never 0: tokens without weight take no quotient.)  An exponential
     // below 2^-126 has an infinite approximate score, which makes top_hi infinite
-    // for good: then the thread goes over its tokens again.  One from 2^126 on has
+    // for good: then the thread goes over its tokens again.  (Told apart here, it
+    // made 24 requests 22.1 us instead of 20.9.)  One from 2^126 on has
     // none: if that is all there is, the request's last CTA sees to it.
     float top_lo = 0x1p-149f, top_hi = 0.0f, top_w = 0.0f, top_e = 1.0f;
     int top_i = NONE;

@@ -101,8 +101,8 @@ inline PagedWs paged_ws_layout(const spec_paged_cfg& c, int num_sms) {
 }
 
 // How the verification is split: `splits` segments per logits row, `slices` of
-// `per` tokens for the race.  About eight CTAs per SM over all rows, and kRaceCtas
-// over the requests' races, but no segment under 4096 and no slice under 2048
+// `per` tokens for the race.  About eight CTAs per SM over all rows (five are
+// resident at once: 1.7 waves), and kRaceCtas over the requests' races, but no segment under 4096 and no slice under 2048
 // tokens (a load per thread).
 struct DraftWs {
     size_t part_off, cand_off, total;
