@@ -411,3 +411,25 @@ def test_outputs_that_round_to_infinity_are_reported(T):
     x.scale["v"][:] = np.float32(7.56e35)
     x.upload()
     assert torch.isfinite(x.attend()).all() and x.status() == 0
+
+
+@pytest.mark.parametrize("io,kv", [("bf16", "e4m3"), ("f32", "e4m3"), ("f32", "io")])
+@pytest.mark.parametrize("L", [20, 31, 8190])
+@pytest.mark.parametrize("sink,first", [(5.0, "zeros"), (9.0, "one")])
+def test_small_weights_beside_a_later_row_that_is_not_finite(io, kv, L, sink, first):
+    """The fourth new row is NaN: the three before it keep their values, small
+    weights and all, those from it on have none."""
+    T = 6
+    c = long_request(L, T, sink, "equal", first, io, kv)
+    for pool in (c["kv"].k_pages, c["kv"].v_pages):
+        raw = pool.view(torch.uint8) if kv == "e4m3" else pool
+        raw[(L + 3) // 256, 0, (L + 3) % 256] = 0x7f if kv == "e4m3" else float("nan")
+    cfg, o = c["cfg"], torch.full_like(c["q"], 7.0)
+    ws = binding.alloc_paged_workspace(cfg)
+    binding.attn_decode_paged(cfg, c["kv"], c["q"], o, ws)
+    assert binding.spec_status_read(ws) == binding.SPEC_DEV_RANGE
+    assert not torch.isfinite(o[0, 3:]).any()
+    clean = long_request(L, T, sink, "equal", first, io, kv)
+    got, want, tol = attend_and_bound(clean, L / 16 + 200)
+    assert ((got - want).abs() <= tol).all()
+    assert ((o.double() - want).abs() <= tol)[0, :3].all()
