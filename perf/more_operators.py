@@ -257,9 +257,8 @@ def prepare(case, seed):
         if c["op"] != "pages":
             s["rope"] = binding.rope_table(c["rot"], base=c["base"], scaling=c["scaling"],
                                            factor=c["factor"], orig_len=c["orig"])
-            strides = (dict(zip(("q_stride", "k_stride", "v_stride"),
-                                (s[n].stride(1) for n in ("q", "k_new", "v_new"))))
-                       if c["op"] == "append" else {})
+            wide = (c["Hq"] + 2 * c["Hkv"]) * c["D"] if c.get("fused") else 0
+            strides = dict(q_stride=wide, k_stride=wide, v_stride=wide)
             s["rcfg"] = binding.rope_cfg(rows=c["rows"] if c["op"] == "rope" else c["B"] * c["T"],
                                          Hq=c["Hq"], Hkv=c["Hkv"], D=c["D"], rot=c["rot"],
                                          layout=c["layout"], io=c["io"],
