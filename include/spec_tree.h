@@ -83,6 +83,7 @@ enum {
                                    ancestors) gives this, as do non-finite inputs there. */
 #define SPEC_DEV_BADPAGE  0x40u /* a page table entry that was needed is outside [0, n_pages) */
 #define SPEC_DEV_BADTOK   0x80u /* a drafted token is outside [0, V) (it is refused) */
+#define SPEC_DEV_NOPAGE   0x100u /* a request got no pages: the free list does not reach */
 
 enum { SPEC_IO_F32 = 0, SPEC_IO_BF16 = 1 };
 
@@ -628,6 +629,182 @@ int draft_verify_sampled(const spec_draft_cfg *cfg, const int32_t *draft_tok,
                          const int32_t *n_draft, const float *draft_prob, const void *logits,
                          const float *u, const float *e, const spec_draft_out *out,
                          int32_t *kv_len, int32_t *root_tok, void *ws, void *stream);
+
+/* ------------------------------------------------------------------------------
+ * Around a serving step: the page tables' growth, rotary positions, and sampling
+ * with filters.  The paged calls' workspace serves the page-table calls and
+ * rope_page_append too, token_sample's is its own or any larger one.
+ */
+
+/* Page tables and the pages that nobody holds.  Request b holds the pages of
+ * its table's first n_held[b] columns; the free list's first n_free entries are
+ * free.  One set serves all layers whose pools number their pages alike. */
+typedef struct spec_page_pool {
+    int32_t *page_table;    /* [B][max_pages] */
+    int32_t *kv_len;        /* [B] committed rows */
+    int32_t *free_list;     /* [n_pages] */
+    int32_t *n_free;        /* [1] in [0, n_pages] (else clamped, SPEC_DEV_BADREQ) */
+    int32_t *n_held;        /* [B] in [0, max_pages] */
+} spec_page_pool;
+
+/*
+ * page_tables_extend -- pages for the new tokens' rows, and where each row goes.
+ * Request b with n_new[b] > 0 needs ceil((kv_len + n_new) / page) pages; what it
+ * lacks is taken from the end of the free list (entry n_free - 1 first), in the
+ * order (request, column).  A request that lacks pages gets none when the
+ * running total of what is lacking, its own included, exceeds n_free
+ * (SPEC_DEV_NOPAGE): the list serves the first requests.  So does one with
+ * kv_len < 0 or kv_len + n_new > max_pages * page (SPEC_DEV_OVERFLOW), or n_held
+ * outside [0, max_pages] (SPEC_DEV_BADREQ).
+ *   n_new  NULL (T each) or [B], in [0, T] (else clamped, SPEC_DEV_BADREQ)
+ *   slots  [B][T] int64: page * cfg->page + row of the page of new row i, -1 for
+ *          i >= n_ok[b] and where the page is not in the pool (SPEC_DEV_BADPAGE)
+ *   n_ok   [B]: n_new[b], or 0 for a request that got no pages
+ * page_table, n_held and n_free are updated, kv_len and free_list are not.
+ * Of cfg, B, T, page, n_pages and max_pages are used.
+ */
+int page_tables_extend(const spec_paged_cfg *cfg, const spec_page_pool *pool,
+                       const int32_t *n_new, int64_t *slots, int32_t *n_ok, void *ws,
+                       void *stream);
+
+/*
+ * page_tables_trim -- pages of rows that are not kept go back to the free list.
+ * Request b keeps its first min(n_held, ceil(keep / page)) columns; the others'
+ * pages are appended to the free list in the order (request, column), their
+ * columns become -1, and kv_len becomes min(kv_len, keep).  keep[b] = kv_len[b]
+ * gives back the pages of refused drafts, 0 those of a request that ended, -1
+ * leaves a request as it is (so does a smaller value, and n_held outside
+ * [0, max_pages]: SPEC_DEV_BADREQ).  A page that requests share must not be
+ * given back; a list that would grow past n_pages keeps its first n_pages
+ * entries (SPEC_DEV_BADREQ).
+ *   keep [B]; it may be kv_len itself.
+ */
+int page_tables_trim(const spec_paged_cfg *cfg, const spec_page_pool *pool, const int32_t *keep,
+                     void *ws, void *stream);
+
+enum { SPEC_ROPE_HALF = 0, SPEC_ROPE_INTERLEAVED = 1 };
+enum {
+    SPEC_ROPE_NONE = 0,
+    SPEC_ROPE_LINEAR = 1,    /* positions divided by factor */
+    SPEC_ROPE_NTK = 2,       /* base times factor^(rot / (rot - 2)) */
+    SPEC_ROPE_YARN = 3       /* Peng et al. 2023: by the turns over orig_len */
+};
+
+/* How a rotation's frequencies f_j = base^(-2 j / rot), j < rot / 2, are scaled
+ * for contexts beyond the trained length.  YARN: f_j becomes
+ * (1 - g) f_j / factor + g f_j, g = (orig_len f_j / 2 pi - beta_slow) /
+ * (beta_fast - beta_slow) held to [0, 1], and the rotated values are multiplied
+ * by amp = 0.1 ln(factor) + 1 (1 otherwise). */
+typedef struct spec_rope_scaling {
+    double base;            /* >= 1 */
+    double factor;          /* >= 1 (read unless NONE) */
+    double beta_fast, beta_slow;   /* YARN: beta_fast > beta_slow >= 0 */
+    int32_t orig_len;       /* YARN: >= 1 */
+    int32_t kind;
+} spec_rope_scaling;
+
+/* Host: turns[j] = f_j / 2 pi in units of 2^-64 turns (host, [rot / 2]) and amp
+ * (host), the table that the calls below take as a device copy.  rot a multiple
+ * of 16 in [16, 128]. */
+int spec_rope_turns(int rot, const spec_rope_scaling *scaling, uint64_t *turns, float *amp);
+
+/* Shape of the rotations.  Limits (else ST_EINVAL): 1 <= rows < 2^31; 1 <= Hq,
+ * 0 <= Hkv (1 <= Hkv for rope_page_append), Hq + 2 Hkv <= 2^16; D in {64, 128};
+ * rot a multiple of 16 in [16, D]; strides 0 or >= H * D and of a multiple of 16
+ * bytes; the heads to be turned, rows (Hq + 2 Hkv), below 2^37. */
+typedef struct spec_rope_cfg {
+    int32_t rows;            /* tokens */
+    int32_t Hq, Hkv, D;
+    int32_t rot;             /* values of a head that are rotated: its first */
+    int32_t layout;          /* pairs (j, j + rot/2): HALF, or (2 j, 2 j + 1): INTERLEAVED */
+    int32_t io_dtype;
+    int32_t inverse;         /* 0, or 1: by the negative angle */
+    int64_t q_stride, k_stride, v_stride;   /* elements from token to token of the inputs
+                                               (slices of a wider row); 0: contiguous */
+} spec_rope_cfg;
+
+/*
+ * rope_apply -- rotary positions of queries and keys.  A pair (a, b) at position
+ * p becomes amp (a cos t - b sin t, a sin t + b cos t), t = p f_j, in fp32; values
+ * past `rot` are copied.  The angle is exact to 2^-32 turns at every position
+ * (integer arithmetic modulo a turn).  The inverse is also the gradient with
+ * respect to the inputs.
+ *   turns [rot/2] uint64   pos [rows] int32 (any value)
+ *   q [rows][Hq][D] io, k [rows][Hkv][D] io (NULL with Hkv = 0), tokens
+ *   q_stride / k_stride elements apart; q_out, k_out contiguous (in place is
+ *   fine where the input is contiguous too)
+ */
+int rope_apply(const spec_rope_cfg *cfg, const uint64_t *turns, float amp, const int32_t *pos,
+               const void *q, const void *k, void *q_out, void *k_out, void *stream);
+
+/*
+ * rope_page_append -- rope_apply and kv_page_append in one pass: the rows of a
+ * step's new tokens (rows = B * T of `pcfg`) at positions kv_len[b] + i, the keys
+ * and values into the cache's slots (page_tables_extend).  With SPEC_KV_E4M3 a
+ * row is brought to 8 bits from the rotated fp32 values by kv_page_append's rule,
+ * else rounded to io once.  A slot < 0 is a token without a row: nothing of it is
+ * read or written.  A slot past the pool is not written (SPEC_DEV_BADPAGE).  Two
+ * tokens of one call must not share a slot.  Of `kv` the page table is not used.
+ *   slots [B][T] int64;  q, q_out [B][T][Hq][D], k_new, v_new [B][T][Hkv][D] io,
+ *   tokens *_stride elements apart (q_out contiguous)
+ */
+int rope_page_append(const spec_rope_cfg *cfg, const spec_paged_cfg *pcfg,
+                     const spec_paged_kv *kv, const uint64_t *turns, float amp,
+                     const int64_t *slots, const void *q, const void *k_new, const void *v_new,
+                     void *q_out, void *ws, void *stream);
+
+#define SPEC_MAX_SAMPLE_V (1 << 20)
+
+/* Shape of token_sample: 1 <= R <= 2^20 rows, 1 <= V <= 2^20, per >= 1 (else ST_EINVAL). */
+typedef struct spec_sample_cfg {
+    int32_t R, V;
+    int32_t per;             /* consecutive rows that share a request's parameters */
+    int32_t io_dtype;        /* of the logits */
+} spec_sample_cfg;
+
+/* Parameters of the requests, [ceil(R / per)] each; NULL: off for all rows. */
+typedef struct spec_sample_params {
+    const float *temperature;   /* >= 0 (off: 1); 0 keeps the first maximum alone */
+    const int32_t *top_k;       /* <= 0: off */
+    const float *top_p;         /* >= 1: off; <= 0 keeps one token */
+    const float *min_p;         /* <= 0: off; above 1 as 1 */
+} spec_sample_params;
+
+typedef struct spec_sample_out {
+    int32_t *tok;            /* [R] drawn token */
+    float *tok_prob;         /* [R] its probability among what stays */
+    float *prob;             /* [R][V] the probabilities, 0 for what does not stay */
+    void *logits;            /* [R][V] io: the logits, -inf for what does not stay */
+} spec_sample_out;
+
+/* Workspace of token_sample, as spec_paged_workspace_bytes. */
+size_t spec_sample_workspace_bytes(const spec_sample_cfg *cfg, int num_sms);
+
+/*
+ * token_sample -- sampling with temperature, min-p, top-k and top-p from given
+ * random numbers: a drafter's token with the distribution it was drawn from
+ * (draft_verify_sampled's draft_prob), a plain token, or the target's logits
+ * without what a request's filters remove, for draft_verify_sampled.
+ *   w = exp((x - max) / temperature); of the tokens with x > -inf
+ *   min_p  keeps those with x >= max + temperature ln(min_p),
+ *   top_k  of these the first k in the order (x descending, index ascending),
+ *   top_p  of these, in that order, those with less than top_p of their sum of w
+ *          before them,
+ *   and the first one always stays; p = w / sum of w over what stays;
+ *   tok = argmax p / e  (lowest index on ties).
+ * Borders are decided on masses of 2^-30 relative accuracy in integers (weights
+ * below about 2^-43 of the largest, 2^-(62 - ceil(log2 V)), count as nothing
+ * there), so that the result does not depend on the order of summation.
+ *   logits [R][V] io; e [R][V] float > 0 (NULL: no token is drawn, out->tok and
+ *   out->tok_prob are NULL too); of `out` any may be NULL (tok with tok_prob);
+ *   out->logits may be `logits` itself.
+ * A temperature that is NaN or negative counts as 0, another parameter that is
+ * NaN as off (SPEC_DEV_BADREQ).  A row with a NaN or +inf logit, or with -inf alone, gives token 0,
+ * probabilities 0 and its logits as they are (SPEC_DEV_BADLOGIT).  The race is in
+ * fp32: scores nearer than its rounding can fall either way.
+ */
+int token_sample(const spec_sample_cfg *cfg, const void *logits, const spec_sample_params *params,
+                 const float *e, const spec_sample_out *out, void *ws, void *stream);
 
 #ifdef __cplusplus
 }

@@ -22,7 +22,7 @@ ST_OK, ST_EINVAL, ST_EUNSUPPORTED, ST_ECUDA, ST_EOVERFLOW, ST_TIMEOUT, ST_ESCRAT
 NOALLOC_SCRATCH_BYTES = 8 << 20
 SPEC_DEV_OVERFLOW, SPEC_DEV_BADLAT, SPEC_DEV_TIMEOUT, SPEC_DEV_BADREQ = 0x1, 0x2, 0x4, 0x8
 SPEC_DEV_BADLOGIT, SPEC_DEV_RANGE = 0x10, 0x20
-SPEC_DEV_BADPAGE, SPEC_DEV_BADTOK = 0x40, 0x80
+SPEC_DEV_BADPAGE, SPEC_DEV_BADTOK, SPEC_DEV_NOPAGE = 0x40, 0x80, 0x100
 SPEC_IO_F32, SPEC_IO_BF16 = 0, 1
 SPEC_KV_IO, SPEC_KV_E4M3 = 0, 1
 EXPORTS = ("spec_workspace_bytes", "spec_workspace_bytes_for_sms", "spec_tree_build", "gdn_tree_verify", "attn_tree_verify",
@@ -33,9 +33,12 @@ EXPORTS = ("spec_workspace_bytes", "spec_workspace_bytes_for_sms", "spec_tree_bu
            "accept_and_commit_sampled", "spec_verify_step_sampled",
            "spec_verify_step_persistent", "spec_step_launches_persistent",
            "spec_paged_workspace_bytes", "kv_page_append", "kv_page_read", "attn_decode_paged",
-           "spec_draft_workspace_bytes", "draft_verify_sampled")
+           "spec_draft_workspace_bytes", "draft_verify_sampled",
+           "page_tables_extend", "page_tables_trim", "spec_rope_turns", "rope_apply",
+           "rope_page_append", "spec_sample_workspace_bytes", "token_sample")
 SAMPLE_CHUNK = 4096
 _STATUS_BYTES = 256          # the status word and its reserve, at the head of a workspace
+_TICKET_BYTES = 512          # with the first tickets behind it
 
 _lock = threading.Lock()
 _lib = None
@@ -94,6 +97,34 @@ class SpecDraftCfg(ctypes.Structure):
 
 class SpecDraftOut(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("accept_len", "out_tok", "target_prob")]
+
+
+class SpecPagePool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "page_table", "kv_len", "free_list", "n_free", "n_held")]
+
+
+class SpecRopeScaling(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("base", "factor", "beta_fast", "beta_slow")] + [
+        ("orig_len", ctypes.c_int32), ("kind", ctypes.c_int32)]
+
+
+class SpecRopeCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "rows", "Hq", "Hkv", "D", "rot", "layout", "io_dtype", "inverse")] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class SpecSampleCfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "V", "per", "io_dtype")]
+
+
+class SpecSampleParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p")]
+
+
+class SpecSampleOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("tok", "tok_prob", "prob", "logits")]
 
 
 def load(path: Optional[str] = None) -> ctypes.CDLL:
@@ -163,8 +194,21 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
             lib.attn_decode_paged.argtypes = [pcfgp, pkvp] + [vp] * 5
             lib.draft_verify_sampled.argtypes = [dcfgp] + [vp] * 6 + [
                 ctypes.POINTER(SpecDraftOut)] + [vp] * 4
+            poolp, ropep = ctypes.POINTER(SpecPagePool), ctypes.POINTER(SpecRopeCfg)
+            scfgp = ctypes.POINTER(SpecSampleCfg)
+            lib.page_tables_extend.argtypes = [pcfgp, poolp] + [vp] * 5
+            lib.page_tables_trim.argtypes = [pcfgp, poolp] + [vp] * 3
+            lib.spec_rope_turns.argtypes = [ctypes.c_int, ctypes.POINTER(SpecRopeScaling), vp,
+                                            ctypes.POINTER(ctypes.c_float)]
+            lib.rope_apply.argtypes = [ropep, vp, ctypes.c_float] + [vp] * 6
+            lib.rope_page_append.argtypes = [ropep, pcfgp, pkvp, vp, ctypes.c_float] + [vp] * 7
+            lib.spec_sample_workspace_bytes.argtypes = [scfgp, ctypes.c_int]
+            lib.spec_sample_workspace_bytes.restype = ctypes.c_size_t
+            lib.token_sample.argtypes = [scfgp, vp, ctypes.POINTER(SpecSampleParams), vp,
+                                         ctypes.POINTER(SpecSampleOut), vp, vp]
             for n in ("kv_page_append", "kv_page_read", "attn_decode_paged",
-                      "draft_verify_sampled"):
+                      "draft_verify_sampled", "page_tables_extend", "page_tables_trim",
+                      "spec_rope_turns", "rope_apply", "rope_page_append", "token_sample"):
                 getattr(lib, n).restype = ctypes.c_int
             for n in ("spec_tree_build", "gdn_tree_verify", "attn_tree_verify",
                       "attn_tree_verify_noalloc", "spec_wait_probe", "spec_step_launches",
@@ -753,3 +797,258 @@ def draft_verify_sampled(cfg: SpecDraftCfg, draft_tok, draft_prob, logits, u, e,
         _raw_stream(stream, dev))
     if rc:
         _check("draft_verify_sampled", rc)
+
+
+# ------------------------------- page tables, rotary positions, filtered sampling
+
+class PagePool:
+    """Page tables and the pages that nobody holds: page_table [B][max_pages],
+    kv_len [B], free_list [n_pages], n_free [1], n_held [B], all int32.  The first
+    two may be those of a PagedKV (all layers' caches share them).  The tensors
+    are fixed for the object's life; their contents are the caller's."""
+
+    def __init__(self, cfg: SpecPagedCfg, page_table, kv_len, free_list, n_free, n_held):
+        dev, i32 = torch.cuda.current_device(), torch.int32
+        self._t = (page_table, kv_len, free_list, n_free, n_held)
+        self._c = SpecPagePool(*(
+            _arg(_required(t, n), i32, shape, n, dev) for t, n, shape in zip(
+                self._t, ("page_table", "kv_len", "free_list", "n_free", "n_held"),
+                ((cfg.B, cfg.max_pages), (cfg.B,), (cfg.n_pages,), (1,), (cfg.B,)))))
+        self._ref = ctypes.byref(self._c)
+        self.key = (cfg.B, cfg.max_pages, cfg.n_pages, dev)
+
+    page_table, kv_len, free_list, n_free, n_held = (
+        property(lambda self, i=i: self._t[i]) for i in range(5))
+
+    @classmethod
+    def empty(cls, cfg: SpecPagedCfg, page_table=None, kv_len=None, device="cuda") -> "PagePool":
+        """All pages free, handed out in the order 0, 1, ...; tables of -1."""
+        i32 = dict(dtype=torch.int32, device=device)
+        if page_table is None:
+            page_table = torch.full((cfg.B, cfg.max_pages), -1, **i32)
+        if kv_len is None:
+            kv_len = torch.zeros((cfg.B,), **i32)
+        return cls(cfg, page_table, kv_len, torch.arange(cfg.n_pages - 1, -1, -1, **i32),
+                   torch.full((1,), cfg.n_pages, **i32), torch.zeros((cfg.B,), **i32))
+
+    def ref(self, cfg: SpecPagedCfg, device: int):
+        """The pool as an argument of a call with that configuration."""
+        if self.key != (cfg.B, cfg.max_pages, cfg.n_pages, device):
+            if device != self.key[3]:
+                raise ValueError(f"the pool is on cuda:{self.key[3]}, the current device is "
+                                 f"cuda:{device}")
+            raise ValueError("the pool was made for another configuration")
+        return self._ref
+
+
+def page_tables_extend(cfg: SpecPagedCfg, pool: PagePool, slots, n_ok, ws, n_new=None,
+                       stream=None):
+    """Pages for the new tokens' rows: slots int64 [B][T] receives where each row
+    goes (-1: nowhere), n_ok int32 [B] the rows that each request may write."""
+    dev, i32 = _get_device(), torch.int32
+    b = (cfg.B,)
+    rc = (_lib or load()).page_tables_extend(
+        ctypes.byref(cfg), pool.ref(cfg, dev), _arg(n_new, i32, b, "n_new", dev),
+        _arg(_required(slots, "slots"), torch.int64, (cfg.B, cfg.T), "slots", dev),
+        _arg(_required(n_ok, "n_ok"), i32, b, "n_ok", dev), _workspace(ws, _TICKET_BYTES, dev),
+        _raw_stream(stream, dev))
+    if rc:
+        _check("page_tables_extend", rc)
+
+
+def page_tables_trim(cfg: SpecPagedCfg, pool: PagePool, keep, ws, stream=None):
+    """Pages past the rows that are kept (keep int32 [B], -1: all) go back to the
+    free list; kv_len is held to keep."""
+    dev = _get_device()
+    rc = (_lib or load()).page_tables_trim(
+        ctypes.byref(cfg), pool.ref(cfg, dev),
+        _arg(_required(keep, "keep"), torch.int32, (cfg.B,), "keep", dev),
+        _workspace(ws, _TICKET_BYTES, dev), _raw_stream(stream, dev))
+    if rc:
+        _check("page_tables_trim", rc)
+
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class RopeTable:
+    """A rotation's frequencies on the device (turns int64 [rot/2]: units of 2^-64
+    turns a position) and the factor of the rotated values (amp)."""
+    __slots__ = ("turns", "amp", "rot", "_ptr", "_dev")
+
+    def __init__(self, turns: torch.Tensor, amp: float):
+        self.rot = 2 * turns.numel()
+        self._dev = turns.get_device()
+        self._ptr = _arg(turns, torch.int64, (turns.numel(),), "turns", self._dev)
+        self.turns, self.amp = turns, float(amp)
+
+    def ptr(self, rot: int, device: int) -> int:
+        if rot != self.rot:
+            raise ValueError(f"the table is for {self.rot} rotated values, {rot} are asked for")
+        if device != self._dev:
+            raise ValueError(f"the table is on cuda:{self._dev}, the current device is "
+                             f"cuda:{device}")
+        return self._ptr
+
+
+def spec_rope_turns(rot: int, base: float = 1e4, scaling: str = "none", factor: float = 1.0,
+                    orig_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(turns, amp) on the host: a list of rot/2 integers in units of 2^-64 turns."""
+    turns = (ctypes.c_uint64 * max(1, rot // 2))()
+    amp = ctypes.c_float(0.0)
+    s = SpecRopeScaling(float(base), float(factor), float(beta_fast), float(beta_slow),
+                        int(orig_len), _SCALINGS[scaling])
+    _check("spec_rope_turns", load().spec_rope_turns(int(rot), ctypes.byref(s), turns,
+                                                     ctypes.byref(amp)))
+    return list(turns), float(amp.value)
+
+
+def rope_table(rot: int, device="cuda", **scaling) -> RopeTable:
+    """The table of spec_rope_turns(rot, **scaling) on the device."""
+    turns, amp = spec_rope_turns(rot, **scaling)
+    signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+    return RopeTable(torch.tensor(signed, dtype=torch.int64, device=device), amp)
+
+
+def rope_cfg(rows, Hq, Hkv, D, rot=None, layout="half", io="bf16", inverse=False, q_stride=0,
+             k_stride=0, v_stride=0) -> SpecRopeCfg:
+    """Shape of the rotations; layout "half" or "interleaved", rot None: all of D.
+    The strides are elements from token to token (0: contiguous)."""
+    return SpecRopeCfg(rows, Hq, Hkv, D, D if rot is None else rot, _LAYOUTS[layout],
+                       _IO[io][0], int(bool(inverse)), q_stride, k_stride, v_stride)
+
+
+def _tokens(t, dtype, tokens, H, D, stride, name, device):
+    """Data pointer of `tokens` (a shape) tokens of [H][D], `stride` elements apart
+    (0: contiguous)."""
+    shape = tokens + (H, D)
+    step = stride or H * D
+    if step == H * D:
+        return _arg(_required(t, name), dtype, shape, name, device)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    want = (step, D, 1) if len(tokens) == 1 else (tokens[1] * step, step, D, 1)
+    if (t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and all(s == w or n == 1 for s, w, n in zip(t.stride(), want, shape))):
+        return t.data_ptr()
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    raise ValueError(f"{name} must have strides {want}, got {t.stride()}")
+
+
+def rope_apply(cfg: SpecRopeCfg, table: RopeTable, pos, q, k, q_out, k_out, stream=None):
+    """Rotary positions of q [rows][Hq][D] and k [rows][Hkv][D] io (k and k_out
+    None with Hkv = 0) at pos int32 [rows]; q_out and k_out are contiguous."""
+    dev, dt, rows = _get_device(), _io_dtype(cfg), (cfg.rows,)
+    if cfg.Hkv == 0:
+        k = k_out = None
+    rc = (_lib or load()).rope_apply(
+        ctypes.byref(cfg), table.ptr(cfg.rot, dev), table.amp,
+        _arg(_required(pos, "pos"), torch.int32, rows, "pos", dev),
+        _tokens(q, dt, rows, cfg.Hq, cfg.D, cfg.q_stride, "q", dev),
+        _tokens(k, dt, rows, cfg.Hkv, cfg.D, cfg.k_stride, "k", dev) if cfg.Hkv else None,
+        _arg(_required(q_out, "q_out"), dt, (cfg.rows, cfg.Hq, cfg.D), "q_out", dev),
+        _arg(_required(k_out, "k_out"), dt, (cfg.rows, cfg.Hkv, cfg.D), "k_out", dev)
+        if cfg.Hkv else None, _raw_stream(stream, dev))
+    if rc:
+        _check("rope_apply", rc)
+
+
+def rope_page_append(cfg: SpecRopeCfg, pcfg: SpecPagedCfg, kv: PagedKV, table: RopeTable, slots,
+                     q, k_new, v_new, q_out, ws, stream=None):
+    """The new tokens' queries and keys rotated at kv_len + i, q [B][T][Hq][D] into
+    q_out, the rows of k_new and v_new [B][T][Hkv][D] into the cache's slots
+    (int64 [B][T], -1: no row), in one pass."""
+    dev, dt = _get_device(), _io_dtype(pcfg)
+    bt, D, Hkv = (pcfg.B, pcfg.T), pcfg.D, pcfg.Hkv
+    rc = (_lib or load()).rope_page_append(
+        ctypes.byref(cfg), ctypes.byref(pcfg), kv.ref(pcfg, bytes(pcfg), dev),
+        table.ptr(cfg.rot, dev), table.amp,
+        _arg(_required(slots, "slots"), torch.int64, bt, "slots", dev),
+        _tokens(q, dt, bt, pcfg.Hq, D, cfg.q_stride, "q", dev),
+        _tokens(k_new, dt, bt, Hkv, D, cfg.k_stride, "k_new", dev),
+        _tokens(v_new, dt, bt, Hkv, D, cfg.v_stride, "v_new", dev),
+        _arg(_required(q_out, "q_out"), dt, bt + (pcfg.Hq, D), "q_out", dev),
+        _workspace(ws, _STATUS_BYTES, dev), _raw_stream(stream, dev))
+    if rc:
+        _check("rope_page_append", rc)
+
+
+def sample_cfg(R, V, per=1, io="bf16") -> SpecSampleCfg:
+    """Shape of token_sample: R rows, `per` of them to a set of parameters."""
+    return SpecSampleCfg(R, V, per, _IO[io][0])
+
+
+def spec_sample_workspace_bytes(cfg: SpecSampleCfg, num_sms: int = 0) -> int:
+    """Workspace bytes of token_sample (num_sms 0: the current device's)."""
+    n = load().spec_sample_workspace_bytes(ctypes.byref(cfg), int(num_sms))
+    if n == 0:
+        raise SpecError("spec_sample_workspace_bytes", ST_EINVAL,
+                        "invalid configuration (or no CUDA device visible)")
+    return int(n)
+
+
+def alloc_sample_workspace(cfg: SpecSampleCfg, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of spec_sample_workspace_bytes(cfg) bytes."""
+    return torch.zeros((spec_sample_workspace_bytes(cfg),), dtype=torch.uint8, device=device)
+
+
+class SampleBuffers:
+    """Outputs of token_sample: tok [R] int32 and tok_prob [R] fp32 (draw), prob
+    [R][V] fp32 (prob), logits [R][V] io (logits: True, or the tensor to write,
+    which may be the input); None where not asked for.  The tensors are fixed for
+    the object's life."""
+
+    def __init__(self, cfg: SpecSampleCfg, draw=True, prob=False, logits=False, device="cuda"):
+        R, V, f32 = cfg.R, cfg.V, torch.float32
+        if logits is True:
+            logits = torch.empty((R, V), dtype=_io_dtype(cfg), device=device)
+        elif logits is False:
+            logits = None
+        else:
+            _arg(logits, _io_dtype(cfg), (R, V), "logits", torch.cuda.current_device())
+        if isinstance(prob, torch.Tensor):
+            _arg(prob, f32, (R, V), "prob", torch.cuda.current_device())
+        else:
+            prob = torch.empty((R, V), dtype=f32, device=device) if prob else None
+        self.tok = torch.empty((R,), dtype=torch.int32, device=device) if draw else None
+        self.tok_prob = torch.empty((R,), dtype=f32, device=device) if draw else None
+        self.prob, self.logits = prob, logits
+        got = [t for t in (self.tok, prob, logits) if t is not None]
+        if not got:
+            raise ValueError("no output is asked for")
+        self.key = (R, V, cfg.io_dtype, got[0].get_device())
+        self._c = SpecSampleOut(*(None if t is None else t.data_ptr() for t in (
+            self.tok, self.tok_prob, prob, logits)))
+        self._ref = ctypes.byref(self._c)
+
+    def ref(self, cfg: SpecSampleCfg, device: int):
+        """The outputs as an argument of a call with that configuration."""
+        if self.key != (cfg.R, cfg.V, cfg.io_dtype, device):
+            raise ValueError("the outputs were made for another configuration or device")
+        return self._ref
+
+
+def token_sample(cfg: SpecSampleCfg, logits, e, out: SampleBuffers, ws, temperature=None,
+                 top_k=None, top_p=None, min_p=None, stream=None):
+    """Sample from logits io [R][V] with e f32 [R][V] (None where `out` draws no
+    token); temperature, top_p, min_p f32 and top_k int32 [ceil(R / per)], or None:
+    off."""
+    dev, f32 = _get_device(), torch.float32
+    RV, n = (cfg.R, cfg.V), (-(-cfg.R // max(cfg.per, 1)),)
+    if (e is None) != (out.tok is None):
+        raise ValueError("e goes with outputs that draw a token, and only with them")
+    params = SpecSampleParams(_arg(temperature, f32, n, "temperature", dev),
+                              _arg(top_k, torch.int32, n, "top_k", dev),
+                              _arg(top_p, f32, n, "top_p", dev), _arg(min_p, f32, n, "min_p", dev))
+    rc = (_lib or load()).token_sample(
+        ctypes.byref(cfg), _arg(_required(logits, "logits"), _io_dtype(cfg), RV, "logits", dev),
+        ctypes.byref(params), _arg(e, f32, RV, "e", dev), out.ref(cfg, dev),
+        _workspace(ws, _STATUS_BYTES, dev), _raw_stream(stream, dev))
+    if rc:
+        _check("token_sample", rc)

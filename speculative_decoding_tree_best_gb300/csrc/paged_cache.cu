@@ -17,6 +17,7 @@
 // (exact quotients, maxima, packing); 24 single tokens 1.8 us, latency.
 #include <math.h>
 
+#include "cache_rows.cuh"
 #include "paged.cuh"
 
 namespace spec {
@@ -24,48 +25,6 @@ namespace spec {
 namespace {
 
 constexpr int NT = 256;
-
-// lanes per row and values per lane: 16 bytes of the I/O type each
-template <int IO, int D> struct geo {
-    static constexpr int VEC = 16 / sizeof(typename io_t<IO>::T);
-    static constexpr int LPR = D / VEC;
-};
-
-template <int IO>
-__device__ __forceinline__ void unpack(const uint4& u,
-                                       float (&x)[16 / sizeof(typename io_t<IO>::T)]) {
-    if constexpr (IO == SPEC_IO_F32) {
-        x[0] = __uint_as_float(u.x);
-        x[1] = __uint_as_float(u.y);
-        x[2] = __uint_as_float(u.z);
-        x[3] = __uint_as_float(u.w);
-    } else {
-        const uint32_t r[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(r[i] << 16);
-            x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-        }
-    }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// x / y from r, 1 / y rounded: one Newton step on the quotient's remainder, which
-// rounds it correctly (Markstein 1990).
-__device__ __forceinline__ float quotient(float x, float y, float r) {
-    const float q = x * r;
-    return fmaf(fmaf(-q, y, x), r, q);
-}
-
-// two quotients by the same y
-__device__ __forceinline__ float2 quotients(float2 x, float y, float r) {
-    const float2 r2 = make_float2(r, r), q = __fmul2_rn(x, r2);
-    return __ffma2_rn(__ffma2_rn(q, make_float2(-y, -y), x), r2, q);
-}
 
 // The rows of one request, (token, head) in memory order, are cut into blocks of
 // RPC rows, one to a CTA; a thread has UNR rows of its block, of the keys and of
@@ -158,13 +117,9 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
 #pragma unroll
         for (int o = 4; o < G::LPR; o <<= 1)
             most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const float amax = __uint_as_float(most);
-        float scale = fmaxf(quotient(amax, 448.0f, 1.0f / 448.0f), 0x1p-100f);
-        if (most == 0u) scale = 1.0f;
-        if (most >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);
+        const float scale = row_scale(most);
         const int64_t at = o1 ? dst[1] : dst[0];
         if (lane < 4 && at >= 0) (o2 ? v_scale : k_scale)[at] = scale;
-        // where the remainder underflows the code is 0 whatever it is
         const float inv = __frcp_rn(scale);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -175,12 +130,8 @@ append_rows(const __grid_constant__ RowArgs a, const uint4* __restrict__ k_new,
             unpack<IO>(u[j], x);
             uint32_t c[G::VEC / 4];
 #pragma unroll
-            for (int k = 0; k < G::VEC / 4; ++k) {
-                const float2 lo = quotients(make_float2(x[4 * k], x[4 * k + 1]), sj, rj);
-                const float2 hi = quotients(make_float2(x[4 * k + 2], x[4 * k + 3]), sj, rj);
-                c[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
-                       ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
-            }
+            for (int k = 0; k < G::VEC / 4; ++k)
+                c[k] = codes4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3], sj, rj);
             if (dst[j / 2] >= 0) {
                 void* pages = j & 1 ? v_pages : k_pages;
                 if constexpr (G::VEC == 8)
