@@ -2,13 +2,10 @@
 // random numbers.
 //
 // Mathematics.  What stays is a prefix of the order (logit descending, index
-// ascending), so it is {K >= t} of the key K = (logit's bits, made to order like
-// the number; index, falling): one 52-bit integer, different for every token.
-// min-p gives t directly.  top-k and top-p ask for the largest t with
-// F(t) = sum of f over {K >= t} >= target: f = 1 and the count k, or f = the
-// token's weight and top_p times the sum over what top-k left.  That is a radix
-// selection: a histogram of f over the top bits of K - lo names the bin that the
-// border is in, which becomes the next range.
+// ascending): all tokens above a border value and those at it up to a border index.
+// min-p gives the value directly.  top-k and top-p ask for the shortest prefix with
+// F >= target: F = its length and the count k, or F = the sum of its weights and
+// top_p times that of what top-k left.
 //   Weights are integers, 2^-(62 - lg V) of the largest one, from an exponential
 // of 2^-30 relative accuracy (a table of 2^(-j/64) and a cubic): sums of them are
 // exact in 64 bits, so the border depends neither on the order of summation nor
@@ -16,10 +13,25 @@
 //   The draw: argmin e / w over independent exponentials e is token v with
 // probability w_v / sum w.
 //
+// The border, by what it takes:
+//   top_k small   The k-th largest of the threads' own maxima is not above the k-th
+//                 largest logit.  So the logits from there on (few more than k) are
+//                 gathered in one CTA, sorted, and all filters and the draw decided
+//                 on the sorted list.
+//   bf16          Logits take few values: a histogram of counts over the values
+//                 (8192 of them from the maximum down, those within 2^-24 of 0 as
+//                 one) holds all that the masses need, a weight a value; what is
+//                 left is how many of the tokens at the border value stay, the
+//                 first ones.
+//   else          A radix selection on the key K = (logit's bits, made to order like
+//                 the number; index, falling), one 52-bit integer, different for
+//                 every token: a histogram of F over the top bits of K names the
+//                 bin that the border is in, which becomes the next range.
+//
 // Data flow.  A cluster of CTAs owns a row.  It reads the row once, into shared
 // memory (what does not fit is read again from L2), and each pass goes over that
-// copy; histograms are added up in the cluster's first CTA, which finds the border
-// bin and tells the others.
+// copy.  Histograms are added up by parts: each CTA takes a part of the bins from
+// all (reading the others' shared memory), and tells the others its total.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -32,7 +44,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int NT = 512;
-constexpr int NB = 2048;                 // bins of a pass
+constexpr int NBIN = 8192;               // bins of counts
+constexpr int NMASS = 4096;              // bins of masses (as many bytes)
+constexpr int LIST = 2048;               // tokens that the sorted list holds
 constexpr int IDX_BITS = 20;             // of a key: V <= 2^20
 constexpr uint32_t IDX_MAX = (1u << IDX_BITS) - 1;
 constexpr int MAX_CLUSTER = 16;
@@ -54,21 +68,25 @@ struct SampleArgs {
     u64 pow2[64];            // 2^(62 - j/64)
 };
 
-// What one CTA tells the others.
+// What a selection finds, told to all CTAs.
 struct Border {
-    u64 lo, hi;              // the next range
-    u64 above;               // F over the keys past hi; where lo = hi, that key too
+    u64 from;                // what stays: keys from here on
+    u64 sum;                 // sum of weights of that (where weights were asked for)
+    u64 lo, hi;              // radix: the next range; values: the bin's number, tokens of it
     u64 target;
-    int found;               // 0: F never reaches the target
+    int state;
 };
+enum { NOT_FOUND = 0, FOUND = 1, NARROWED = 2 };
 
 struct Cand {
-    float s, x;
+    float w, e, x;           // the score is w / e
     int i;
 };
 
+// The better one: by cross products, lowest index on ties.
 __device__ __forceinline__ void take(Cand& a, const Cand& b) {
-    if (b.s > a.s || (b.s == a.s && b.i < a.i)) a = b;
+    const float p = b.w * a.e, q = a.w * b.e;
+    if (p > q || (p == q && b.i < a.i)) a = b;
 }
 
 // A request's parameters, made by one thread (64-bit floating point is slow here).
@@ -83,17 +101,25 @@ struct Params {
 };
 
 struct Shared {
-    u64 mass[NB];
-    uint32_t count[NB];
+    union {
+        uint32_t count[NBIN];
+        struct {
+            uint32_t lo[NMASS], hi[NMASS];
+        } mass;
+        u64 list[LIST];
+    };
     u64 pow2[64];
     u64 part[NT / 32];
+    u64 cta_sum[MAX_CLUSTER];
     Border border;
-    float cta_max[MAX_CLUSTER];
+    Params prm;
     Cand cand[MAX_CLUSTER];
     Cand warp_cand[NT / 32];
+    float cta_max[MAX_CLUSTER];
     float warp_max[NT / 32];
-    u64 cta_mass[MAX_CLUSTER];
-    Params prm;
+    uint32_t ties[MAX_CLUSTER];
+    uint32_t listed;
+    int border_index;
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -195,29 +221,24 @@ template <int IO> struct Row {
             }
         }
     }
-    // f(x, index in the row) for all of this CTA's elements (-inf beside the row)
-    template <typename F> __device__ __forceinline__ void each(F&& f) const {
-        for (int g = lo + threadIdx.x; g < hi; g += NT) {
+    __device__ __forceinline__ int index(int g) const { return (int)((g0 + g) * VEC - r0); }
+    // f(x, index in the row) for the elements of groups [from, to), `step` apart (-inf
+    // beside the row)
+    template <typename F>
+    __device__ __forceinline__ void range(int from, int to, F&& f, int step = 1) const {
+        for (int g = from; g < to; g += step) {
             float x[VEC];
             unpack(get(g), x);
-            const int i = (int)((g0 + g) * VEC - r0);
+            const int i = index(g);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) f(x[v], i + v);
         }
     }
+    // the same for all of this CTA's elements, a thread's own groups
+    template <typename F> __device__ __forceinline__ void each(F&& f) const {
+        range(lo + threadIdx.x, hi, f, NT);
+    }
 };
-
-__device__ __forceinline__ u64 block_sum(u64 x, u64* part) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = x;
-    __syncthreads();
-    x = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) x += part[w];
-    return x;
-}
 
 // Exclusive prefix of x over the block.
 __device__ __forceinline__ u64 block_prefix(u64 x, u64* part, u64& total) {
@@ -241,87 +262,364 @@ __device__ __forceinline__ u64 block_prefix(u64 x, u64* part, u64& total) {
     return before + s - x;
 }
 
-// The largest t in [lo, hi] with F(t) >= target; `lo` where F never reaches it
-// (no key is above hi).  MASS: f = weights, the target want 2^-64 of F(lo), and F(t)
-// is left in `sum`; else f = 1 and the target `want`.
-template <bool MASS, int IO>
-__device__ u64 select(cg::cluster_group& cl, Shared& sh, const Row<IO>& row, const Weights& wt,
-                      u64 lo, u64 hi, u64 want, u64& sum) {
-    const int rank = cl.block_rank(), C = cl.num_blocks(), tid = threadIdx.x;
-    const u64 first = lo;
-    u64 above = 0, target = want;
-    for (int pass = 0;; ++pass) {
-        const u64 span = hi - lo;
-        const int bits = 64 - __clzll((long long)span);
-        const int shift = max(0, bits - 11);                   // span >> shift < NB
-        row.each([&](float x, int i) {
-            const u64 k = key_of(x, i);
-            if (k < lo || k > hi || i < 0) return;
-            const int bin = (int)((hi - k) >> shift);
-            if (MASS) atomicAdd(&sh.mass[bin], wt.fixed<IO>(x));
-            else atomicAdd(&sh.count[bin], 1u);
-        });
-        __syncthreads();
-        if (rank != 0) {
-            for (int b = tid; b < NB; b += NT) {
-                if (MASS) {
-                    if (sh.mass[b]) atomicAdd(cl.map_shared_rank(&sh.mass[b], 0), sh.mass[b]);
-                    sh.mass[b] = 0;
-                } else {
-                    if (sh.count[b]) atomicAdd(cl.map_shared_rank(&sh.count[b], 0), sh.count[b]);
-                    sh.count[b] = 0;
-                }
-            }
-        }
+// What stays of a CTA's slice: logits above v, and those at v up to index `last`.
+struct Kept {
+    float v;
+    int last;
+    __device__ __forceinline__ bool has(float x, int i) const {
+        return x > v || (x == v && i <= last);
+    }
+};
+
+__device__ __forceinline__ float value_of(u64 key) {
+    const uint32_t k = (uint32_t)(key >> IDX_BITS);
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ int index_of(u64 key) { return IDX_MAX - ((uint32_t)key & IDX_MAX); }
+
+struct Ctx {
+    cg::cluster_group& cl;
+    Shared& sh;
+    int rank, C, tid;
+    Weights wt;
+
+    // x of this CTA and the others', and their sum before this one and in all
+    __device__ __forceinline__ void totals(u64 x, u64& before, u64& all) {
+        if (tid < C) *cl.map_shared_rank(&sh.cta_sum[rank], tid) = x;
         cl.sync();
-        if (rank == 0) {
-            constexpr int RUN = NB / NT;
-            u64 f[RUN], s = 0, total;
-#pragma unroll
-            for (int j = 0; j < RUN; ++j) {
-                f[j] = MASS ? sh.mass[tid * RUN + j] : sh.count[tid * RUN + j];
-                s += f[j];
-            }
-            u64 before = block_prefix(s, sh.part, total) + above;
-            total += above;
-            if (MASS && pass == 0) {
-                target = __umul64hi(total, want) + (total * want != 0);    // rounded up
-                target = max(target, (u64)1);
-            }
-            if (tid == 0 && total < target) sh.border = Border{lo, hi, above, target, 0};
-            if (before < target && target <= before + s) {     // one thread, or none
-                int j = 0;
-#pragma unroll
-                for (int k = 0; k < RUN - 1; ++k)
-                    if (j == k && before + f[k] < target) {
-                        before += f[k];
-                        ++j;
-                    }
-                const u64 top = hi - ((u64)(tid * RUN + j) << shift);
-                const u64 width = 1ull << shift;
-                const u64 low = top - lo < width ? lo : top - width + 1;
-                sh.border = Border{low, top, low == top ? before + f[j] : before, target, 1};
-            }
-#pragma unroll
-            for (int j = 0; j < RUN; ++j) {
-                sh.mass[tid * RUN + j] = 0;
-                sh.count[tid * RUN + j] = 0;
-            }
-            __syncthreads();
-            if (tid > 0 && tid < C) *cl.map_shared_rank(&sh.border, tid) = sh.border;
-        }
-        cl.sync();
-        const Border b = sh.border;
-        if (!b.found) return first;
-        above = b.above;
-        target = b.target;
-        lo = b.lo;
-        hi = b.hi;
-        if (lo == hi) {
-            if (MASS) sum = above;
-            return lo;
+        before = all = 0;
+        for (int c = 0; c < C; ++c) {
+            const u64 y = sh.cta_sum[c];
+            before += c < rank ? y : 0;
+            all += y;
         }
     }
+    __device__ __forceinline__ void tell(const Border& b) {
+        for (int c = 0; c < C; ++c) *cl.map_shared_rank(&sh.border, c) = b;
+    }
+};
+
+// The target of a prefix's F: `want`, or that many 2^-64 of `all`, rounded up.
+template <bool MASS> __device__ __forceinline__ u64 target_of(u64 want, u64 all) {
+    if (!MASS) return want;
+    return max(__umul64hi(all, want) + (all * want != 0), (u64)1);
+}
+
+// ---- bins of bf16's values: signed steps from 0, the smallest magnitudes as 0
+
+constexpr int NEAR_0 = (127 - 24) << 7;                  // 2^-24
+constexpr int FARTHEST = 0x7f80 - NEAR_0;                // infinity
+
+__device__ __forceinline__ int step_of(float x) {
+    const int i = __float_as_int(x) >> 16;
+    const int s = max((i & 0x7fff) - NEAR_0, 0);
+    return i < 0 ? -s : s;
+}
+__device__ __forceinline__ float step_value(int s) {
+    const uint32_t b = (uint32_t)(abs(s) + NEAR_0) << 16;
+    return s == 0 ? 0.0f : __uint_as_float(s < 0 ? b | 0x80000000u : b);
+}
+// the least fp32 number with that step
+__device__ __forceinline__ float step_least(int s) {
+    const uint32_t b = (uint32_t)(abs(s) + NEAR_0) << 16;
+    return __uint_as_float(s > 0 ? b : b | 0x8000ffffu);
+}
+
+// The border bin of counts that every CTA has in sh.count, bin 0 the maximum's
+// (`top` its step): tells all `lo` = the bin, `hi` = its tokens, target = how many
+// of them (in units of F) are still wanted, and (MASS) sum = F before them.
+// The cluster has not synchronised since the counts were made.
+template <bool MASS, int IO>
+__device__ void border_bin(Ctx& k, u64 want, int top) {
+    Shared& sh = k.sh;
+    k.cl.sync();
+    // bins [from, from + run) are this thread's: 16-byte pieces of four
+    const int part = NBIN / k.C, run = max(4, part / NT);
+    const bool mine = k.tid * run < part;
+    const int from = k.rank * part + k.tid * run;
+    uint4 n[NBIN / NT / 4];
+    u64 s = 0;
+#pragma unroll
+    for (int j = 0; j < NBIN / NT / 4; ++j) {
+        n[j] = make_uint4(0, 0, 0, 0);
+        if (!mine || 4 * j >= run) continue;
+        for (int c = 0; c < k.C; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(
+                k.cl.map_shared_rank(&sh.count[from + 4 * j], (k.rank + c) % k.C));
+            n[j].x += x.x;
+            n[j].y += x.y;
+            n[j].z += x.z;
+            n[j].w += x.w;
+        }
+    }
+    auto f = [&](uint32_t count, int bin) -> u64 {
+        if (count == 0) return 0;
+        return MASS ? count * k.wt.template fixed<IO>(step_value(top - bin)) : (u64)count;
+    };
+#pragma unroll
+    for (int j = 0; j < NBIN / NT / 4; ++j)
+        s += f(n[j].x, from + 4 * j) + f(n[j].y, from + 4 * j + 1) + f(n[j].z, from + 4 * j + 2) +
+             f(n[j].w, from + 4 * j + 3);
+    u64 mine_all, before_me, all;
+    u64 at = block_prefix(s, sh.part, mine_all);
+    k.totals(mine_all, before_me, all);
+    at += before_me;
+    const u64 target = target_of<MASS>(want, all);
+    if (k.tid == 0 && k.rank == 0 && all < target) k.tell(Border{0, 0, 0, 0, 0, NOT_FOUND});
+    if (at < target && target <= at + s) {               // one thread of the cluster, or none
+#pragma unroll
+        for (int j = 0; j < NBIN / NT / 4; ++j) {
+            const uint32_t c4[4] = {n[j].x, n[j].y, n[j].z, n[j].w};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const u64 g = f(c4[b], from + 4 * j + b);
+                if (at < target && target <= at + g)
+                    k.tell(Border{0, at, (u64)(from + 4 * j + b), c4[b], target - at, NARROWED});
+                at += g;
+            }
+        }
+    }
+    k.cl.sync();
+}
+
+// Radix selection: the largest key t of `kept` such that F over its {K >= t} reaches
+// the target; NOT_FOUND where it does not.
+template <bool MASS, int IO>
+__device__ Border radix(Ctx& k, const Row<IO>& row, const Kept& kept, u64 want) {
+    Shared& sh = k.sh;
+    const int tid = k.tid;
+    u64 lo = (u64)key_of(kept.v) << IDX_BITS, hi = (u64)key_of(k.wt.m) << IDX_BITS | IDX_MAX;
+    u64 above = 0, target = want;
+    for (int pass = 0;; ++pass) {
+        for (int b = tid; b < NBIN; b += NT) sh.count[b] = 0;
+        __syncthreads();
+        const u64 span = hi - lo;
+        const int shift = max(0, 64 - __clzll((long long)span) - 12);     // span >> shift < NMASS
+        row.each([&](float x, int i) {
+            const u64 key = key_of(x, i);
+            if (key < lo || key > hi || !kept.has(x, i)) return;
+            const int bin = (int)((hi - key) >> shift);
+            if (MASS) {
+                const u64 w = k.wt.template fixed<IO>(x);
+                const uint32_t wl = (uint32_t)w;
+                const uint32_t old = atomicAdd(&sh.mass.lo[bin], wl);
+                const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
+                if (wh) atomicAdd(&sh.mass.hi[bin], wh);
+            } else {
+                atomicAdd(&sh.count[bin], 1u);
+            }
+        });
+        k.cl.sync();
+        const int part = NMASS / k.C, run = max(1, part / NT);
+        const int from = k.rank * part + tid * run;
+        u64 f[NMASS / NT], s = 0;
+#pragma unroll
+        for (int j = 0; j < NMASS / NT; ++j) {
+            f[j] = 0;
+            if (j >= run || tid * run >= part) continue;
+            for (int c = 0; c < k.C; ++c) {
+                if (MASS)
+                    f[j] += (u64)*k.cl.map_shared_rank(&sh.mass.hi[from + j], c) << 32;
+                f[j] += *k.cl.map_shared_rank(&sh.count[from + j], c);   // mass.lo is count's first half
+            }
+            s += f[j];
+        }
+        u64 mine_all, before_me, all;
+        u64 at = block_prefix(s, sh.part, mine_all);
+        k.totals(mine_all, before_me, all);
+        at += before_me + above;
+        if (pass == 0) target = target_of<MASS>(want, all);
+        if (tid == 0 && k.rank == 0 && above + all < target)
+            k.tell(Border{0, 0, 0, 0, 0, NOT_FOUND});
+        if (at < target && target <= at + s) {
+#pragma unroll
+            for (int j = 0; j < NMASS / NT; ++j) {
+                if (at < target && target <= at + f[j]) {
+                    const u64 top = hi - ((u64)(from + j) << shift), width = 1ull << shift;
+                    const u64 low = top - lo < width ? lo : top - width + 1;
+                    k.tell(Border{low, low == top ? at + f[j] : at, low, top, target,
+                                  low == top ? FOUND : NARROWED});
+                }
+                at += f[j];
+            }
+        }
+        k.cl.sync();
+        const Border b = sh.border;
+        if (b.state != NARROWED) return b;
+        above = b.sum;
+        lo = b.lo;
+        hi = b.hi;
+    }
+}
+
+// How many of this CTA's tokens at value v stay when the first `want` of all do, as
+// the last index that stays.  `mine`: the CTA's number of them.
+template <int IO>
+__device__ int last_tie(Ctx& k, const Row<IO>& row, const Kept& in, float v, u64 want, uint32_t mine) {
+    Shared& sh = k.sh;
+    if (k.tid < k.C) *k.cl.map_shared_rank(&sh.ties[k.rank], k.tid) = mine;
+    k.cl.sync();
+    u64 before = 0;
+    for (int c = 0; c < k.rank; ++c) before += sh.ties[c];
+    if (want <= before) return -1;
+    if (want >= before + mine) return in.v == v ? in.last : (int)IDX_MAX;
+    // the border is here: a run of groups a thread, in order
+    const uint32_t left = (uint32_t)(want - before);
+    const int n = row.hi - row.lo, run = (n + NT - 1) / NT;
+    const int g0 = min(row.hi, row.lo + k.tid * run), g1 = min(row.hi, g0 + run);
+    uint32_t count = 0;
+    row.range(g0, g1, [&](float x, int i) { count += x == v && in.has(x, i); });
+    u64 all;
+    uint32_t at = (uint32_t)block_prefix(count, sh.part, all);
+    if (at < left && left <= at + count)
+        row.range(g0, g1, [&](float x, int i) {
+            if (x == v && in.has(x, i) && ++at == left) sh.border_index = i;
+        });
+    __syncthreads();
+    return sh.border_index;
+}
+
+// Narrows `kept` to its shortest prefix whose F reaches the target; it stays as it is
+// where F never does.  MASS leaves the sum of its weights in `sum`.
+template <bool MASS, int IO>
+__device__ void select(Ctx& k, const Row<IO>& row, Kept& kept, u64 want, u64& sum) {
+    Shared& sh = k.sh;
+    if constexpr (IO == SPEC_IO_BF16) {
+        const int top = step_of(k.wt.m), least = top - (NBIN - 1);
+        // whether everything, or all that has weight, is in the bins
+        const float end = least <= -FARTHEST ? -INFINITY : step_value(least);
+        const bool whole = kept.v >= end || (MASS && k.wt.m - end > k.wt.far);
+        if (whole || !MASS) {
+            for (int b = k.tid; b < NBIN; b += NT) sh.count[b] = 0;
+            __syncthreads();
+            row.each([&](float x, int i) {
+                const int bin = top - step_of(x);
+                if (bin < NBIN && kept.has(x, i)) atomicAdd(&sh.count[bin], 1u);
+            });
+            border_bin<MASS, IO>(k, want, top);
+            const Border b = sh.border;
+            if (b.state == NOT_FOUND && whole) return;
+            const int s = top - (int)b.lo;
+            if (b.state != NOT_FOUND && s != 0) {
+                const float v = step_value(s);
+                const u64 w = MASS ? k.wt.template fixed<IO>(v) : 1;
+                const u64 n = (b.target + w - 1) / w;
+                if (MASS) sum = b.sum + n * w;
+                int last = kept.v == v ? kept.last : (int)IDX_MAX;
+                if (n < b.hi) last = last_tie<IO>(k, row, kept, v, n, sh.count[b.lo]);
+                kept = Kept{v, last};
+                return;
+            }
+        }
+    }
+    const Border b = radix<MASS, IO>(k, row, kept, want);
+    if (b.state == NOT_FOUND) return;
+    if (MASS) sum = b.sum;
+    kept = Kept{value_of(b.from), index_of(b.from)};
+}
+
+// Sorts n keys (n <= LIST), the largest first; `list` has room for the next power of two.
+__device__ void sort_list(u64* list, int n) {
+    int size = 32;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += NT) list[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            for (int t = threadIdx.x; t < size / 2; t += NT) {
+                const int a = 2 * t - (t & (j - 1)), b = a + j;
+                const u64 x = list[a], y = list[b];
+                if ((x < y) == ((a & k) == 0)) {
+                    list[a] = y;
+                    list[b] = x;
+                }
+            }
+            __syncthreads();
+        }
+}
+
+// The block's best candidate, in thread 0.
+__device__ __forceinline__ void block_best(Cand& best, Shared& sh) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        take(best, Cand{__shfl_xor_sync(0xffffffffu, best.w, o),
+                        __shfl_xor_sync(0xffffffffu, best.e, o),
+                        __shfl_xor_sync(0xffffffffu, best.x, o),
+                        __shfl_xor_sync(0xffffffffu, best.i, o)});
+    if (threadIdx.x % 32 == 0) sh.warp_cand[threadIdx.x / 32] = best;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < NT / 32; ++w) take(best, sh.warp_cand[w]);
+}
+
+constexpr int SMALL_K = 1024;
+
+// The filters with a top_k of at most SMALL_K, on the sorted list of the logits that
+// can be among them; the first CTA draws the token too.  false: the list is too
+// short for them (or the border below the bins), and nothing has changed.
+template <int IO>
+__device__ bool short_list(Ctx& k, const Row<IO>& row, Kept& kept, float thread_max,
+                           const float* e, u64& sum, Cand& best) {
+    Shared& sh = k.sh;
+    const int top = step_of(k.wt.m), tid = k.tid;
+    const Params& prm = sh.prm;
+    for (int b = tid; b < NBIN; b += NT) sh.count[b] = 0;
+    __syncthreads();
+    {
+        const int bin = top - step_of(thread_max);
+        if (bin < NBIN && thread_max > -INFINITY) atomicAdd(&sh.count[bin], 1u);
+    }
+    border_bin<false, IO>(k, prm.top_k, top);
+    if (sh.border.state == NOT_FOUND) return false;
+    const float cut = fmaxf(step_least(top - (int)sh.border.lo), kept.v);
+    if (thread_max >= cut)
+        row.each([&](float x, int i) {
+            if (!(x >= cut)) return;
+            const uint32_t at = atomicAdd(k.cl.map_shared_rank(&sh.listed, 0), 1u);
+            if (at < LIST) *k.cl.map_shared_rank(&sh.list[at], 0) = key_of(x, i);
+        });
+    k.cl.sync();
+    if (k.rank == 0) {
+        const int n = (int)min(sh.listed, (uint32_t)LIST + 1);
+        if (n > LIST) {
+            if (tid == 0) k.tell(Border{0, 0, 0, 0, 0, NOT_FOUND});
+        } else {
+            sort_list(sh.list, n);
+            const int all = min(n, prm.top_k);
+            constexpr int RUN = LIST / NT;
+            u64 w[RUN], s = 0, total;
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                const int at = tid * RUN + j;
+                w[j] = at < all ? k.wt.template fixed<IO>(value_of(sh.list[at])) : 0;
+                s += w[j];
+            }
+            u64 before = block_prefix(s, sh.part, total);
+            const u64 target = prm.top_p ? target_of<true>(prm.top_p, total) : total;
+            // the prefix ends where it reaches the target; without a top_p at `all`
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                const int at = tid * RUN + j;
+                const bool ends = prm.top_p ? before < target && target <= before + w[j]
+                                            : at == all - 1;
+                if (ends) k.tell(Border{sh.list[at], prm.top_p ? before + w[j] : total, 0, 0,
+                                        (u64)(at + 1), FOUND});
+                before += w[j];
+            }
+        }
+    }
+    k.cl.sync();
+    const Border b = sh.border;
+    if (b.state == NOT_FOUND) return false;
+    if (k.rank == 0 && e)
+        for (int at = tid; at < (int)b.target; at += NT) {
+            const float x = value_of(sh.list[at]);
+            const int i = index_of(sh.list[at]);
+            take(best, Cand{k.wt.template value<IO>(x), e[row.r0 + i], x, i});
+        }
+    sum = b.sum;
+    kept = Kept{value_of(b.from), index_of(b.from)};
+    return true;
 }
 
 __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req) {
@@ -346,7 +644,7 @@ __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req
 }
 
 template <int IO>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 2)
 sample_rows(const __grid_constant__ SampleArgs a) {
     using T = typename io_t<IO>::T;
     constexpr int VEC = Row<IO>::VEC;
@@ -356,10 +654,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     const int rank = cl.block_rank(), C = cl.num_blocks(), tid = threadIdx.x;
     const int lane = tid % 32, warp = tid / 32;
     const int r = blockIdx.x / C, V = a.V;
-    for (int b = tid; b < NB; b += NT) {
-        sh.mass[b] = 0;
-        sh.count[b] = 0;
-    }
+    if (tid == 0) sh.listed = 0;
     if (tid < 64) sh.pow2[tid] = a.pow2[tid];
     Row<IO> row;
     row.logits = static_cast<const T*>(a.logits);
@@ -385,6 +680,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) m = max_nan(m, x[v]);
     }
+    const float thread_max = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) sh.warp_max[warp] = m;
@@ -409,89 +705,156 @@ sample_rows(const __grid_constant__ SampleArgs a) {
         if (bits && rank == 0) raise_status(a.ws, bits);
     }
     __syncthreads();
-    const Weights wt{m, prm.c, prm.c_lo, prm.far, a.lg, sh.pow2};
+    Ctx k{cl, sh, rank, C, tid, Weights{m, prm.c, prm.c_lo, prm.far, a.lg, sh.pow2}};
+    const Weights& wt = k.wt;
 
     // ---- the border
-    u64 keep_from = ~0ull, sum = 0;
-    if (!bad) {
-        keep_from = (u64)key_of(prm.low) << IDX_BITS;
-        const u64 most = (u64)key_of(m) << IDX_BITS | IDX_MAX;
-        if (prm.top_k > 0 && prm.top_k < V)
-            keep_from = select<false, IO>(cl, sh, row, wt, keep_from, most, prm.top_k, sum);
-        if (prm.top_p != 0) {
-            keep_from = select<true, IO>(cl, sh, row, wt, keep_from, most, prm.top_p, sum);
-        } else if (a.out.tok_prob || a.out.prob) {
+    const float* e = a.e;
+    float* prob = a.out.prob;
+    T* out = static_cast<T*>(a.out.logits);
+    Kept kept{prm.low, (int)IDX_MAX};
+    u64 sum = 0;
+    bool summed = false, drawn = false;
+    Cand best{-1.0f, 1.0f, 0.0f, NO_TOK};
+    if (bad) {
+        kept.v = __int_as_float(0x7fffffff);             // NaN: nothing
+    } else {
+        const bool some = prm.top_k > 0 && prm.top_k < V;
+        if (some && prm.top_k <= min(SMALL_K, C * NT / 2))
+            summed = drawn = short_list<IO>(k, row, kept, thread_max, e, sum, best);
+        if (!drawn) {
+            if (some) select<false, IO>(k, row, kept, prm.top_k, sum);
+            if (prm.top_p != 0) {
+                select<true, IO>(k, row, kept, prm.top_p, sum);
+                summed = true;
+            }
+        }
+        if (!summed && prob) {
             row.each([&](float x, int i) {
-                if (key_of(x, i) >= keep_from) sum += wt.fixed<IO>(x);
+                if (kept.has(x, i)) sum += wt.template fixed<IO>(x);
             });
-            sum = block_sum(sum, sh.part);
-            if (tid < C) *cl.map_shared_rank(&sh.cta_mass[rank], tid) = sum;
-            cl.sync();
-            sum = 0;
-            for (int c = 0; c < C; ++c) sum += sh.cta_mass[c];
+            u64 all, before;
+            block_prefix(sum, sh.part, all);
+            k.totals(all, before, sum);
+            summed = true;
         }
     }
 
-    // ---- what stays: the race and the outputs
-    const float inv =
-        bad || sum == 0 ? 0.0f : 1.0f / (__ull2float_rn(sum) * (1.0f / (float)(1ull << (62 - a.lg))));
-    Cand best{-1.0f, 0.0f, NO_TOK};
-    float* prob = a.out.prob;
-    T* kept = static_cast<T*>(a.out.logits);
-    for (int g = row.lo + tid; g < row.hi; g += NT) {
-        const uint4 u = row.get(g);
-        float x[VEC];
-        Row<IO>::unpack(u, x);
-        const int64_t e0 = (row.g0 + g) * VEC;
-        const int i = (int)(e0 - row.r0);
-        const bool whole = i >= 0 && i + VEC <= V;
+    // ---- what stays: the draw and the outputs
+    auto inverse = [&](u64 s) {
+        return s == 0 ? 0.0f : 1.0f / (__ull2float_rn(s) * (1.0f / (float)(1ull << (62 - a.lg))));
+    };
+    float inv = inverse(sum);
+    const bool race = e && !drawn && !bad, tally = !summed && a.out.tok_prob && !bad;
+    if (race || prob || out) {
+        for (int g = row.lo + tid; g < row.hi; g += NT) {
+            const uint4 u = row.get(g);
+            float x[VEC];
+            Row<IO>::unpack(u, x);
+            const int64_t e0 = (row.g0 + g) * VEC;
+            const int i = row.index(g);
+            const bool whole = i >= 0 && i + VEC <= V;
+            float most = x[0];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            if (!whole && (i + v < 0 || i + v >= V)) continue;
-            const bool in = !bad && key_of(x[v], i + v) >= keep_from;
-            const float w = in && (prob || a.e) ? wt.value<IO>(x[v]) : 0.0f;
-            if (in && a.e) take(best, Cand{w / a.e[e0 + v], x[v], i + v});
-            if (prob) prob[e0 + v] = w * inv;
-            if (kept && (!in || kept != a.logits))
-                kept[e0 + v] = in || bad ? (T)x[v] : (T)-INFINITY;
+            for (int v = 1; v < VEC; ++v) most = fmaxf(most, x[v]);
+            const bool any = most >= kept.v;             // (never in a bad row)
+            float w[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) w[v] = 0.0f;
+            if (any) {
+                float ex[VEC];
+                if (race) {
+#pragma unroll
+                    for (int v = 0; v < VEC; v += 4) {
+                        if (whole) {
+                            const float4 y = __ldg(reinterpret_cast<const float4*>(e + e0 + v));
+                            ex[v] = y.x;
+                            ex[v + 1] = y.y;
+                            ex[v + 2] = y.z;
+                            ex[v + 3] = y.w;
+                        } else {
+#pragma unroll
+                            for (int j = v; j < v + 4; ++j)
+                                ex[j] = i + j >= 0 && i + j < V ? e[e0 + j] : 1.0f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    if (!kept.has(x[v], i + v)) continue;
+                    w[v] = wt.template value<IO>(x[v]);
+                    if (race) take(best, Cand{w[v], ex[v], x[v], i + v});
+                    if (tally) sum += wt.template fixed<IO>(x[v]);
+                }
+            }
+            if (prob) {
+#pragma unroll
+                for (int v = 0; v < VEC; v += 4) {
+                    if (whole) {
+                        *reinterpret_cast<float4*>(prob + e0 + v) =
+                            make_float4(w[v] * inv, w[v + 1] * inv, w[v + 2] * inv, w[v + 3] * inv);
+                    } else {
+#pragma unroll
+                        for (int j = v; j < v + 4; ++j)
+                            if (i + j >= 0 && i + j < V) prob[e0 + j] = w[j] * inv;
+                    }
+                }
+            }
+            if (out) {
+                alignas(16) T y[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    y[v] = (T)(bad || kept.has(x[v], i + v) ? x[v] : -INFINITY);
+                if (whole) {
+                    reinterpret_cast<uint4*>(out)[row.g0 + g] = *reinterpret_cast<const uint4*>(y);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v)
+                        if (i + v >= 0 && i + v < V) out[e0 + v] = y[v];
+                }
+            }
         }
     }
-    if (!a.e) return;                                    // no CTA reads another's memory past here
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        take(best, Cand{__shfl_xor_sync(0xffffffffu, best.s, o),
-                        __shfl_xor_sync(0xffffffffu, best.x, o),
-                        __shfl_xor_sync(0xffffffffu, best.i, o)});
-    if (lane == 0) sh.warp_cand[warp] = best;
-    __syncthreads();
+    if (!e) return;                              // no CTA reads another's memory past here
+    block_best(best, sh);
+    if (tally) {
+        u64 all;
+        block_prefix(sum, sh.part, all);
+        sum = all;
+    }
     if (tid == 0) {
-        for (int w = 1; w < NT / 32; ++w) take(best, sh.warp_cand[w]);
         *cl.map_shared_rank(&sh.cand[rank], 0) = best;
+        if (tally) *cl.map_shared_rank(&sh.cta_sum[rank], 0) = sum;
     }
     cl.sync();
     if (rank == 0 && tid == 0) {
         best = sh.cand[0];
         for (int c = 1; c < C; ++c) take(best, sh.cand[c]);
-        const bool none = bad || best.i == NO_TOK;
+        if (tally) {
+            sum = 0;
+            for (int c = 0; c < C; ++c) sum += sh.cta_sum[c];
+            inv = inverse(sum);
+        }
+        const bool none = best.i == NO_TOK;
         a.out.tok[r] = none ? 0 : best.i;
-        if (a.out.tok_prob) a.out.tok_prob[r] = none ? 0.0f : wt.value<IO>(best.x) * inv;
+        if (a.out.tok_prob) a.out.tok_prob[r] = none ? 0.0f : wt.template value<IO>(best.x) * inv;
     }
 }
 
-// CTAs per row: the more the fewer rows, and as many as hold the row in shared memory
-// where 16 do.
+// CTAs per row: as many as it takes for two CTAs' slices to share an SM, and more
+// while the rows leave SMs idle (no slice under 64 groups).
 template <int IO>
 cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
     constexpr int VEC = Row<IO>::VEC;
-    const int most = 160 * 1024;
+    const int two = 78 * 1024, most = 180 * 1024;        // bytes of a slice, two and one to an SM
     const int64_t groups = ((int64_t)c.V + VEC - 1) / VEC + 1;
     int sms = device_sm_count();
     if (sms < 1) sms = 1;
     int C = 1;
-    while (C < MAX_CLUSTER && ((int64_t)c.R * C * 2 <= sms || (groups + C - 1) / C * 16 > most) &&
-           (groups / C) > 64)
+    while (C < MAX_CLUSTER && groups / C > 64 &&
+           ((int64_t)c.R * C <= sms || (groups + C - 1) / C * 16 > two))
         C *= 2;
-    int64_t share = (groups + C - 1) / C;
+    const int64_t share = (groups + C - 1) / C;
     a.resident = (int)(share * 16 > most ? most / 16 : share);
     const size_t smem = (size_t)a.resident * 16;
     cudaError_t e = cudaFuncSetAttribute(sample_rows<IO>,
