@@ -14,10 +14,10 @@
 // probability w_v / sum w.
 //
 // The border, by what it takes:
-//   top_k small   The k-th largest of the threads' own maxima is not above the k-th
-//                 largest logit.  So the logits from there on (few more than k) are
-//                 gathered in one CTA, sorted, and all filters and the draw decided
-//                 on the sorted list.
+//   top_k small   Each CTA of C finds a value that k / C of its threads' maxima reach.
+//                 The least of these values is not above the k-th largest logit: the
+//                 logits from there on (few more than k) are gathered in one CTA,
+//                 sorted, and all filters and the draw decided on the sorted list.
 //   bf16          Logits take few values: a histogram of counts over the values
 //                 (8192 of them from the maximum down, those within 2^-24 of 0 as
 //                 one) holds all that the masses need, a weight a value; what is
@@ -51,6 +51,7 @@ constexpr int IDX_BITS = 20;             // of a key: V <= 2^20
 constexpr uint32_t IDX_MAX = (1u << IDX_BITS) - 1;
 constexpr int MAX_CLUSTER = 16;
 constexpr int NO_TOK = 0x7fffffff;
+constexpr float LOWEST = -3.4028234663852886e38f;
 // weights below 2^-CUT of the largest are 0 in the sums
 constexpr float CUT = 43.0f;
 
@@ -69,11 +70,11 @@ struct SampleArgs {
 };
 
 // What a selection finds, told to all CTAs.
-struct Border {
-    u64 from;                // what stays: keys from here on
-    u64 sum;                 // sum of weights of that (where weights were asked for)
-    u64 lo, hi;              // radix: the next range; values: the bin's number, tokens of it
-    u64 target;
+struct alignas(16) Border {
+    u64 from;                // the border's key, or its bin
+    u64 sum;                 // F up to there, the border's own included (a bin's: before it)
+    u64 target;              // what F is to reach (a bin's: what is wanted of it)
+    uint32_t tokens;         // of the bin
     int state;
 };
 enum { NOT_FOUND = 0, FOUND = 1, NARROWED = 2 };
@@ -115,7 +116,7 @@ struct Shared {
     Params prm;
     Cand cand[MAX_CLUSTER];
     Cand warp_cand[NT / 32];
-    float cta_max[MAX_CLUSTER];
+    float2 cta_max[MAX_CLUSTER];         // and the value that enough of its threads reach
     float warp_max[NT / 32];
     uint32_t ties[MAX_CLUSTER];
     uint32_t listed;
@@ -221,6 +222,18 @@ template <int IO> struct Row {
             }
         }
     }
+    // the largest of a group, NaN where there is one
+    static __device__ __forceinline__ float most(const uint4& u) {
+        if constexpr (IO == SPEC_IO_F32) {
+            return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
+                           max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+        } else {
+            const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+            const float2 y = __bfloat1622float2(
+                __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
+            return max_nan(y.x, y.y);
+        }
+    }
     __device__ __forceinline__ int index(int g) const { return (int)((g0 + g) * VEC - r0); }
     // f(x, index in the row) for the elements of groups [from, to), `step` apart (-inf
     // beside the row)
@@ -277,17 +290,18 @@ __device__ __forceinline__ float value_of(u64 key) {
 }
 __device__ __forceinline__ int index_of(u64 key) { return IDX_MAX - ((uint32_t)key & IDX_MAX); }
 
-struct Ctx {
+template <int C> struct Ctx {
     cg::cluster_group& cl;
     Shared& sh;
-    int rank, C, tid;
+    int rank, tid;
     Weights wt;
 
-    // x of this CTA and the others', and their sum before this one and in all
+    // the sum of the CTAs' x before this one, and of all
     __device__ __forceinline__ void totals(u64 x, u64& before, u64& all) {
         if (tid < C) *cl.map_shared_rank(&sh.cta_sum[rank], tid) = x;
         cl.sync();
         before = all = 0;
+#pragma unroll
         for (int c = 0; c < C; ++c) {
             const u64 y = sh.cta_sum[c];
             before += c < rank ? y : 0;
@@ -295,7 +309,14 @@ struct Ctx {
         }
     }
     __device__ __forceinline__ void tell(const Border& b) {
-        for (int c = 0; c < C; ++c) *cl.map_shared_rank(&sh.border, c) = b;
+        const uint4* src = reinterpret_cast<const uint4*>(&b);
+        const uint4 lo = src[0], hi = src[1];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            uint4* to = reinterpret_cast<uint4*>(cl.map_shared_rank(&sh.border, c));
+            to[0] = lo;
+            to[1] = hi;
+        }
     }
 };
 
@@ -326,66 +347,68 @@ __device__ __forceinline__ float step_least(int s) {
 }
 
 // The border bin of counts that every CTA has in sh.count, bin 0 the maximum's
-// (`top` its step): tells all `lo` = the bin, `hi` = its tokens, target = how many
-// of them (in units of F) are still wanted, and (MASS) sum = F before them.
-// The cluster has not synchronised since the counts were made.
-template <bool MASS, int IO>
-__device__ void border_bin(Ctx& k, u64 want, int top) {
+// (`top` its step): tells all the bin and its tokens, `sum` = F before it and
+// `target` = what is wanted of it.  The cluster has not synchronised since the
+// counts were made.
+template <bool MASS, int IO, int C>
+__device__ __forceinline__ void border_bin(Ctx<C>& k, u64 want, int top) {
     Shared& sh = k.sh;
     k.cl.sync();
-    // bins [from, from + run) are this thread's: 16-byte pieces of four
-    const int part = NBIN / k.C, run = max(4, part / NT);
-    const bool mine = k.tid * run < part;
-    const int from = k.rank * part + k.tid * run;
-    uint4 n[NBIN / NT / 4];
-    u64 s = 0;
+    // bins [from, from + RUN) are this thread's: 16-byte pieces of four
+    constexpr int PART = NBIN / C, RUN = PART / NT < 4 ? 4 : PART / NT;
+    const bool mine = k.tid * RUN < PART;
+    const int from = k.rank * PART + k.tid * RUN;
+    uint32_t n[RUN];
+    u64 f[RUN], s = 0;
 #pragma unroll
-    for (int j = 0; j < NBIN / NT / 4; ++j) {
-        n[j] = make_uint4(0, 0, 0, 0);
-        if (!mine || 4 * j >= run) continue;
-        for (int c = 0; c < k.C; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(
-                k.cl.map_shared_rank(&sh.count[from + 4 * j], (k.rank + c) % k.C));
-            n[j].x += x.x;
-            n[j].y += x.y;
-            n[j].z += x.z;
-            n[j].w += x.w;
+    for (int j = 0; j < RUN; j += 4) {
+        uint4 x[C], t = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            x[c] = mine ? *reinterpret_cast<const uint4*>(
+                              k.cl.map_shared_rank(&sh.count[from + j], (k.rank + c) % C))
+                        : t;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            t.x += x[c].x;
+            t.y += x[c].y;
+            t.z += x[c].z;
+            t.w += x[c].w;
         }
+        n[j] = t.x;
+        n[j + 1] = t.y;
+        n[j + 2] = t.z;
+        n[j + 3] = t.w;
     }
-    auto f = [&](uint32_t count, int bin) -> u64 {
-        if (count == 0) return 0;
-        return MASS ? count * k.wt.template fixed<IO>(step_value(top - bin)) : (u64)count;
-    };
 #pragma unroll
-    for (int j = 0; j < NBIN / NT / 4; ++j)
-        s += f(n[j].x, from + 4 * j) + f(n[j].y, from + 4 * j + 1) + f(n[j].z, from + 4 * j + 2) +
-             f(n[j].w, from + 4 * j + 3);
+    for (int j = 0; j < RUN; ++j) {
+        f[j] = n[j];
+        if (MASS && n[j]) f[j] *= k.wt.template fixed<IO>(step_value(top - from - j));
+        s += f[j];
+    }
     u64 mine_all, before_me, all;
     u64 at = block_prefix(s, sh.part, mine_all);
     k.totals(mine_all, before_me, all);
     at += before_me;
     const u64 target = target_of<MASS>(want, all);
-    if (k.tid == 0 && k.rank == 0 && all < target) k.tell(Border{0, 0, 0, 0, 0, NOT_FOUND});
+    if (k.tid == 0 && k.rank == 0 && all < target) k.tell(Border{0, 0, 0, 0, NOT_FOUND});
     if (at < target && target <= at + s) {               // one thread of the cluster, or none
+        Border b{};
 #pragma unroll
-        for (int j = 0; j < NBIN / NT / 4; ++j) {
-            const uint32_t c4[4] = {n[j].x, n[j].y, n[j].z, n[j].w};
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const u64 g = f(c4[b], from + 4 * j + b);
-                if (at < target && target <= at + g)
-                    k.tell(Border{0, at, (u64)(from + 4 * j + b), c4[b], target - at, NARROWED});
-                at += g;
-            }
+        for (int j = 0; j < RUN; ++j) {
+            if (at < target && target <= at + f[j])
+                b = Border{(u64)(from + j), at, target - at, n[j], NARROWED};
+            at += f[j];
         }
+        k.tell(b);
     }
     k.cl.sync();
 }
 
 // Radix selection: the largest key t of `kept` such that F over its {K >= t} reaches
 // the target; NOT_FOUND where it does not.
-template <bool MASS, int IO>
-__device__ Border radix(Ctx& k, const Row<IO>& row, const Kept& kept, u64 want) {
+template <bool MASS, int IO, int C>
+__device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 want) {
     Shared& sh = k.sh;
     const int tid = k.tid;
     u64 lo = (u64)key_of(kept.v) << IDX_BITS, hi = (u64)key_of(k.wt.m) << IDX_BITS | IDX_MAX;
@@ -410,17 +433,19 @@ __device__ Border radix(Ctx& k, const Row<IO>& row, const Kept& kept, u64 want) 
             }
         });
         k.cl.sync();
-        const int part = NMASS / k.C, run = max(1, part / NT);
-        const int from = k.rank * part + tid * run;
-        u64 f[NMASS / NT], s = 0;
+        constexpr int PART = NMASS / C, RUN = PART / NT < 1 ? 1 : PART / NT;
+        const int from = k.rank * PART + tid * RUN;
+        u64 f[RUN], s = 0;
 #pragma unroll
-        for (int j = 0; j < NMASS / NT; ++j) {
+        for (int j = 0; j < RUN; ++j) {
             f[j] = 0;
-            if (j >= run || tid * run >= part) continue;
-            for (int c = 0; c < k.C; ++c) {
-                if (MASS)
-                    f[j] += (u64)*k.cl.map_shared_rank(&sh.mass.hi[from + j], c) << 32;
-                f[j] += *k.cl.map_shared_rank(&sh.count[from + j], c);   // mass.lo is count's first half
+            if (tid * RUN < PART) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    // (mass.lo lies where count does)
+                    f[j] += *k.cl.map_shared_rank(&sh.count[from + j], c);
+                    if (MASS) f[j] += (u64)*k.cl.map_shared_rank(&sh.mass.hi[from + j], c) << 32;
+                }
             }
             s += f[j];
         }
@@ -430,34 +455,33 @@ __device__ Border radix(Ctx& k, const Row<IO>& row, const Kept& kept, u64 want) 
         at += before_me + above;
         if (pass == 0) target = target_of<MASS>(want, all);
         if (tid == 0 && k.rank == 0 && above + all < target)
-            k.tell(Border{0, 0, 0, 0, 0, NOT_FOUND});
+            k.tell(Border{0, 0, 0, 0, NOT_FOUND});
         if (at < target && target <= at + s) {
+            Border b{};
 #pragma unroll
-            for (int j = 0; j < NMASS / NT; ++j) {
-                if (at < target && target <= at + f[j]) {
-                    const u64 top = hi - ((u64)(from + j) << shift), width = 1ull << shift;
-                    const u64 low = top - lo < width ? lo : top - width + 1;
-                    k.tell(Border{low, low == top ? at + f[j] : at, low, top, target,
-                                  low == top ? FOUND : NARROWED});
-                }
+            for (int j = 0; j < RUN; ++j) {
+                if (at < target && target <= at + f[j])
+                    b = Border{(u64)(from + j), at, f[j], 0, NARROWED};
                 at += f[j];
             }
+            k.tell(b);
         }
         k.cl.sync();
-        const Border b = sh.border;
-        if (b.state != NARROWED) return b;
+        Border b = sh.border;
+        if (b.state == NOT_FOUND) return b;
         above = b.sum;
-        lo = b.lo;
-        hi = b.hi;
+        hi -= b.from << shift;
+        if (hi - lo >= 1ull << shift) lo = hi - (1ull << shift) + 1;
+        if (lo == hi) return Border{lo, b.sum + b.target, 0, 0, FOUND};
     }
 }
 
 // How many of this CTA's tokens at value v stay when the first `want` of all do, as
 // the last index that stays.  `mine`: the CTA's number of them.
-template <int IO>
-__device__ int last_tie(Ctx& k, const Row<IO>& row, const Kept& in, float v, u64 want, uint32_t mine) {
+template <int IO, int C>
+__device__ __forceinline__ int last_tie(Ctx<C>& k, const Row<IO>& row, const Kept& in, float v, u64 want, uint32_t mine) {
     Shared& sh = k.sh;
-    if (k.tid < k.C) *k.cl.map_shared_rank(&sh.ties[k.rank], k.tid) = mine;
+    if (k.tid < C) *k.cl.map_shared_rank(&sh.ties[k.rank], k.tid) = mine;
     k.cl.sync();
     u64 before = 0;
     for (int c = 0; c < k.rank; ++c) before += sh.ties[c];
@@ -481,8 +505,8 @@ __device__ int last_tie(Ctx& k, const Row<IO>& row, const Kept& in, float v, u64
 
 // Narrows `kept` to its shortest prefix whose F reaches the target; it stays as it is
 // where F never does.  MASS leaves the sum of its weights in `sum`.
-template <bool MASS, int IO>
-__device__ void select(Ctx& k, const Row<IO>& row, Kept& kept, u64 want, u64& sum) {
+template <bool MASS, int IO, int C>
+__device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept, u64 want, u64& sum) {
     Shared& sh = k.sh;
     if constexpr (IO == SPEC_IO_BF16) {
         const int top = step_of(k.wt.m), least = top - (NBIN - 1);
@@ -492,21 +516,31 @@ __device__ void select(Ctx& k, const Row<IO>& row, Kept& kept, u64 want, u64& su
         if (whole || !MASS) {
             for (int b = k.tid; b < NBIN; b += NT) sh.count[b] = 0;
             __syncthreads();
-            row.each([&](float x, int i) {
-                const int bin = top - step_of(x);
-                if (bin < NBIN && kept.has(x, i)) atomicAdd(&sh.count[bin], 1u);
-            });
+            // (bins that weigh nothing stay empty; without a border value so far only
+            // -inf has to be kept out, which the bins do unless they reach it)
+            const int bins = !MASS || k.wt.far >= 3.0e38f
+                                 ? NBIN : min(NBIN, top - step_of(k.wt.m - k.wt.far) + 2);
+            if (least > -FARTHEST && kept.v == LOWEST && kept.last == (int)IDX_MAX)
+                row.each([&](float x, int) {
+                    const int bin = top - step_of(x);
+                    if (bin < bins) atomicAdd(&sh.count[bin], 1u);
+                });
+            else
+                row.each([&](float x, int i) {
+                    const int bin = top - step_of(x);
+                    if (bin < bins && kept.has(x, i)) atomicAdd(&sh.count[bin], 1u);
+                });
             border_bin<MASS, IO>(k, want, top);
             const Border b = sh.border;
             if (b.state == NOT_FOUND && whole) return;
-            const int s = top - (int)b.lo;
+            const int s = top - (int)b.from;
             if (b.state != NOT_FOUND && s != 0) {
                 const float v = step_value(s);
                 const u64 w = MASS ? k.wt.template fixed<IO>(v) : 1;
                 const u64 n = (b.target + w - 1) / w;
                 if (MASS) sum = b.sum + n * w;
                 int last = kept.v == v ? kept.last : (int)IDX_MAX;
-                if (n < b.hi) last = last_tie<IO>(k, row, kept, v, n, sh.count[b.lo]);
+                if (n < b.tokens) last = last_tie<IO>(k, row, kept, v, n, sh.count[b.from]);
                 kept = Kept{v, last};
                 return;
             }
@@ -518,9 +552,27 @@ __device__ void select(Ctx& k, const Row<IO>& row, Kept& kept, u64 want, u64& su
     kept = Kept{value_of(b.from), index_of(b.from)};
 }
 
-// Sorts n keys (n <= LIST), the largest first; `list` has room for the next power of two.
-__device__ void sort_list(u64* list, int n) {
-    int size = 32;
+// Sorts n keys (1 <= n <= LIST), the largest first, and returns where they are in `list`
+// (which has room for the next power of two).  Up to RANKED keys by counting how many
+// are larger, the threads shared out over the keys; more in a bitonic network.
+constexpr int RANKED = 512;
+static_assert(RANKED <= NT && 2 * RANKED <= LIST);
+
+__device__ __forceinline__ u64* sort_list(u64* list, int n) {
+    if (n <= RANKED) {
+        int sh = 0;                                      // 2^sh threads to a key
+        while (n << (sh + 1) <= NT && sh < 3) ++sh;
+        const int at = threadIdx.x >> sh, part = threadIdx.x & ((1 << sh) - 1);
+        const u64 x = at < n ? list[at] : 0;
+        int above = 0;
+#pragma unroll 4
+        for (int i = part; i < n; i += 1 << sh) above += list[i] > x;
+        for (int o = 1; o < 1 << sh; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
+        if (at < n && part == 0) list[RANKED + above] = x;
+        __syncthreads();
+        return list + RANKED;
+    }
+    int size = RANKED;
     while (size < n) size *= 2;
     for (int i = n + threadIdx.x; i < size; i += NT) list[i] = 0;
     __syncthreads();
@@ -536,6 +588,7 @@ __device__ void sort_list(u64* list, int n) {
             }
             __syncthreads();
         }
+    return list;
 }
 
 // The block's best candidate, in thread 0.
@@ -554,24 +607,29 @@ __device__ __forceinline__ void block_best(Cand& best, Shared& sh) {
 
 constexpr int SMALL_K = 1024;
 
-// The filters with a top_k of at most SMALL_K, on the sorted list of the logits that
-// can be among them; the first CTA draws the token too.  false: the list is too
-// short for them (or the border below the bins), and nothing has changed.
-template <int IO>
-__device__ bool short_list(Ctx& k, const Row<IO>& row, Kept& kept, float thread_max,
-                           const float* e, u64& sum, Cand& best) {
-    Shared& sh = k.sh;
-    const int top = step_of(k.wt.m), tid = k.tid;
-    const Params& prm = sh.prm;
-    for (int b = tid; b < NBIN; b += NT) sh.count[b] = 0;
-    __syncthreads();
-    {
-        const int bin = top - step_of(thread_max);
-        if (bin < NBIN && thread_max > -INFINITY) atomicAdd(&sh.count[bin], 1u);
+// The least fp32 number that `want` threads' maxima reach, to the accuracy of a step
+// (-FLT_MAX or -inf where fewer have one).
+__device__ __forceinline__ float reached(float thread_max, int want) {
+    const int mine = step_of(thread_max);
+    int lo = -FARTHEST, hi = FARTHEST;                   // `want` of them reach lo
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (__syncthreads_count(mine >= mid) >= want) lo = mid;
+        else hi = mid - 1;
     }
-    border_bin<false, IO>(k, prm.top_k, top);
-    if (sh.border.state == NOT_FOUND) return false;
-    const float cut = fmaxf(step_least(top - (int)sh.border.lo), kept.v);
+    return lo == -FARTHEST ? -INFINITY : step_least(lo);
+}
+
+// The filters with a small top_k, on the sorted list of the logits from `cut` on,
+// which are top_k or more; the first CTA draws the token too.  false: the list is
+// too short for them, and nothing has changed.
+template <int IO, int C>
+__device__ __forceinline__ bool short_list(Ctx<C>& k, const Row<IO>& row, Kept& kept,
+                                           float thread_max, float cut, const float* e, u64& sum,
+                                           Cand& best) {
+    Shared& sh = k.sh;
+    const int tid = k.tid;
+    const Params& prm = sh.prm;
     if (thread_max >= cut)
         row.each([&](float x, int i) {
             if (!(x >= cut)) return;
@@ -582,28 +640,37 @@ __device__ bool short_list(Ctx& k, const Row<IO>& row, Kept& kept, float thread_
     if (k.rank == 0) {
         const int n = (int)min(sh.listed, (uint32_t)LIST + 1);
         if (n > LIST) {
-            if (tid == 0) k.tell(Border{0, 0, 0, 0, 0, NOT_FOUND});
+            if (tid == 0) k.tell(Border{0, 0, 0, 0, NOT_FOUND});
         } else {
-            sort_list(sh.list, n);
-            const int all = min(n, prm.top_k);
-            constexpr int RUN = LIST / NT;
-            u64 w[RUN], s = 0, total;
+            const u64* list = sort_list(sh.list, n);
+            // a run of keys a thread; their random numbers on their way meanwhile
+            const int all = min(n, prm.top_k), run = n <= NT ? 1 : LIST / NT;
+            u64 w[LIST / NT], s = 0, total;
+            float ex[LIST / NT], x[LIST / NT];
+            int i[LIST / NT];
 #pragma unroll
-            for (int j = 0; j < RUN; ++j) {
-                const int at = tid * RUN + j;
-                w[j] = at < all ? k.wt.template fixed<IO>(value_of(sh.list[at])) : 0;
+            for (int j = 0; j < LIST / NT; ++j) {
+                const int at = tid * run + j;
+                w[j] = 0;
+                if (j >= run || at >= all) continue;
+                x[j] = value_of(list[at]);
+                i[j] = index_of(list[at]);
+                if (e) ex[j] = e[row.r0 + i[j]];
+                w[j] = k.wt.template fixed<IO>(x[j]);
                 s += w[j];
             }
-            u64 before = block_prefix(s, sh.part, total);
-            const u64 target = prm.top_p ? target_of<true>(prm.top_p, total) : total;
+            const u64 start = block_prefix(s, sh.part, total);
             // the prefix ends where it reaches the target; without a top_p at `all`
+            const u64 target = prm.top_p ? target_of<true>(prm.top_p, total) : total;
+            u64 before = start;
 #pragma unroll
-            for (int j = 0; j < RUN; ++j) {
-                const int at = tid * RUN + j;
-                const bool ends = prm.top_p ? before < target && target <= before + w[j]
-                                            : at == all - 1;
-                if (ends) k.tell(Border{sh.list[at], prm.top_p ? before + w[j] : total, 0, 0,
-                                        (u64)(at + 1), FOUND});
+            for (int j = 0; j < LIST / NT; ++j) {
+                const int at = tid * run + j;
+                if (j >= run || at >= all) continue;
+                const bool in = !prm.top_p || before < target;
+                if (in && (prm.top_p ? target <= before + w[j] : at == all - 1))
+                    k.tell(Border{list[at], before + w[j], 0, 0, FOUND});
+                if (in && e) take(best, Cand{k.wt.template value<IO>(x[j]), ex[j], x[j], i[j]});
                 before += w[j];
             }
         }
@@ -611,12 +678,6 @@ __device__ bool short_list(Ctx& k, const Row<IO>& row, Kept& kept, float thread_
     k.cl.sync();
     const Border b = sh.border;
     if (b.state == NOT_FOUND) return false;
-    if (k.rank == 0 && e)
-        for (int at = tid; at < (int)b.target; at += NT) {
-            const float x = value_of(sh.list[at]);
-            const int i = index_of(sh.list[at]);
-            take(best, Cand{k.wt.template value<IO>(x), e[row.r0 + i], x, i});
-        }
     sum = b.sum;
     kept = Kept{value_of(b.from), index_of(b.from)};
     return true;
@@ -643,7 +704,7 @@ __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req
     return y;
 }
 
-template <int IO>
+template <int IO, int C>
 __global__ void __launch_bounds__(NT, 2)
 sample_rows(const __grid_constant__ SampleArgs a) {
     using T = typename io_t<IO>::T;
@@ -651,7 +712,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     extern __shared__ uint4 slice[];
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
-    const int rank = cl.block_rank(), C = cl.num_blocks(), tid = threadIdx.x;
+    const int rank = cl.block_rank(), tid = threadIdx.x;
     const int lane = tid % 32, warp = tid / 32;
     const int r = blockIdx.x / C, V = a.V;
     if (tid == 0) sh.listed = 0;
@@ -666,19 +727,26 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     row.hi = min(groups, row.lo + share);
     row.smem = slice;
     row.resident = a.resident;
+    cl.barrier_arrive();
     pdl_wait();
-    if (tid == 0) sh.prm = params_of(a.p, r / a.per);
 
-    // ---- the row, and its maximum
+    // ---- the row, and its maximum; the last thread, while its loads are under way,
+    // makes the request's parameters
+    constexpr int U = 4;
     float m = -INFINITY;
-#pragma unroll 4
-    for (int g = row.lo + tid; g < row.hi; g += NT) {
-        const uint4 u = row.load(g);
-        if (g - row.lo < a.resident) slice[g - row.lo] = u;
-        float x[VEC];
-        Row<IO>::unpack(u, x);
+    for (int g = row.lo + tid, first = true; first || g < row.hi; g += U * NT, first = false) {
+        uint4 u[U];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) m = max_nan(m, x[v]);
+        for (int j = 0; j < U; ++j)
+            if (g + j * NT < row.hi) u[j] = row.load(g + j * NT);
+        if (first && tid == NT - 1) sh.prm = params_of(a.p, r / a.per);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int at = g + j * NT - row.lo;
+            if (g + j * NT >= row.hi) continue;
+            if (at < a.resident) slice[at] = u[j];
+            m = max_nan(m, Row<IO>::most(u[j]));
+        }
     }
     const float thread_max = m;
 #pragma unroll
@@ -687,17 +755,25 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     __syncthreads();
     m = sh.warp_max[lane % (NT / 32)];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    cl.sync();                                           // everyone has started
-    if (tid < C) *cl.map_shared_rank(&sh.cta_max[rank], tid) = m;
+    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    static_assert(NT / 32 == 16);
+    const bool small_k = sh.prm.top_k > 0 && sh.prm.top_k < V &&
+                         sh.prm.top_k <= min(SMALL_K, C * NT / 2);
+    float cut = 0.0f;
+    if (small_k) cut = reached(thread_max, (sh.prm.top_k + C - 1) / C);
+    cl.barrier_wait();                                   // everyone has started
+    if (tid < C) *cl.map_shared_rank(&sh.cta_max[rank], tid) = make_float2(m, cut);
     cl.sync();
-    m = -INFINITY;
-    for (int c = 0; c < C; ++c) m = max_nan(m, sh.cta_max[c]);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        m = max_nan(m, sh.cta_max[c].x);
+        cut = fminf(cut, sh.cta_max[c].y);
+    }
 
     const Params& prm = sh.prm;
     const bool bad = !(fabsf(m) < INFINITY);
     if (tid == 0) {
-        float low = -3.4028234663852886e38f;
+        float low = LOWEST;
         if (prm.min_p >= 1.0f) low = m;
         else if (prm.min_p > 0.0f) low = fmaxf(low, __double2float_ru((double)m + prm.min_low));
         sh.prm.low = low;
@@ -705,7 +781,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
         if (bits && rank == 0) raise_status(a.ws, bits);
     }
     __syncthreads();
-    Ctx k{cl, sh, rank, C, tid, Weights{m, prm.c, prm.c_lo, prm.far, a.lg, sh.pow2}};
+    Ctx<C> k{cl, sh, rank, tid, Weights{m, prm.c, prm.c_lo, prm.far, a.lg, sh.pow2}};
     const Weights& wt = k.wt;
 
     // ---- the border
@@ -719,11 +795,10 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     if (bad) {
         kept.v = __int_as_float(0x7fffffff);             // NaN: nothing
     } else {
-        const bool some = prm.top_k > 0 && prm.top_k < V;
-        if (some && prm.top_k <= min(SMALL_K, C * NT / 2))
-            summed = drawn = short_list<IO>(k, row, kept, thread_max, e, sum, best);
+        if (small_k)
+            summed = drawn = short_list<IO>(k, row, kept, thread_max, fmaxf(cut, kept.v), e, sum, best);
         if (!drawn) {
-            if (some) select<false, IO>(k, row, kept, prm.top_k, sum);
+            if (prm.top_k > 0 && prm.top_k < V) select<false, IO>(k, row, kept, prm.top_k, sum);
             if (prm.top_p != 0) {
                 select<true, IO>(k, row, kept, prm.top_p, sum);
                 summed = true;
@@ -741,80 +816,88 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     }
 
     // ---- what stays: the draw and the outputs
+    constexpr int F = IO == SPEC_IO_F32 ? 4 : 2;
     auto inverse = [&](u64 s) {
         return s == 0 ? 0.0f : 1.0f / (__ull2float_rn(s) * (1.0f / (float)(1ull << (62 - a.lg))));
     };
     float inv = inverse(sum);
     const bool race = e && !drawn && !bad, tally = !summed && a.out.tok_prob && !bad;
-    if (race || prob || out) {
-        for (int g = row.lo + tid; g < row.hi; g += NT) {
-            const uint4 u = row.get(g);
-            float x[VEC];
-            Row<IO>::unpack(u, x);
-            const int64_t e0 = (row.g0 + g) * VEC;
-            const int i = row.index(g);
-            const bool whole = i >= 0 && i + VEC <= V;
-            float most = x[0];
+    // F groups at once, so that their random numbers' loads are under way together
+    if (race || prob || out)
+        for (int g = row.lo + tid; g < row.hi; g += F * NT) {
+            uint4 u[F];
+            float ex[F][VEC];
+            bool any[F], whole[F];
 #pragma unroll
-            for (int v = 1; v < VEC; ++v) most = fmaxf(most, x[v]);
-            const bool any = most >= kept.v;             // (never in a bad row)
-            float w[VEC];
+            for (int j = 0; j < F; ++j) {
+                const int at = g + j * NT, i = row.index(at);
+                any[j] = whole[j] = false;
+                if (at >= row.hi) continue;
+                u[j] = row.get(at);
+                whole[j] = i >= 0 && i + VEC <= V;
+                any[j] = Row<IO>::most(u[j]) >= kept.v;  // (never in a bad row)
+                if (!race || !any[j]) continue;
+                const float* src = e + (row.g0 + at) * VEC;
+                if (whole[j]) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) w[v] = 0.0f;
-            if (any) {
-                float ex[VEC];
-                if (race) {
-#pragma unroll
-                    for (int v = 0; v < VEC; v += 4) {
-                        if (whole) {
-                            const float4 y = __ldg(reinterpret_cast<const float4*>(e + e0 + v));
-                            ex[v] = y.x;
-                            ex[v + 1] = y.y;
-                            ex[v + 2] = y.z;
-                            ex[v + 3] = y.w;
-                        } else {
-#pragma unroll
-                            for (int j = v; j < v + 4; ++j)
-                                ex[j] = i + j >= 0 && i + j < V ? e[e0 + j] : 1.0f;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    if (!kept.has(x[v], i + v)) continue;
-                    w[v] = wt.template value<IO>(x[v]);
-                    if (race) take(best, Cand{w[v], ex[v], x[v], i + v});
-                    if (tally) sum += wt.template fixed<IO>(x[v]);
-                }
-            }
-            if (prob) {
-#pragma unroll
-                for (int v = 0; v < VEC; v += 4) {
-                    if (whole) {
-                        *reinterpret_cast<float4*>(prob + e0 + v) =
-                            make_float4(w[v] * inv, w[v + 1] * inv, w[v + 2] * inv, w[v + 3] * inv);
-                    } else {
-#pragma unroll
-                        for (int j = v; j < v + 4; ++j)
-                            if (i + j >= 0 && i + j < V) prob[e0 + j] = w[j] * inv;
-                    }
-                }
-            }
-            if (out) {
-                alignas(16) T y[VEC];
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    y[v] = (T)(bad || kept.has(x[v], i + v) ? x[v] : -INFINITY);
-                if (whole) {
-                    reinterpret_cast<uint4*>(out)[row.g0 + g] = *reinterpret_cast<const uint4*>(y);
+                    for (int v = 0; v < VEC; v += 4)
+                        *reinterpret_cast<float4*>(&ex[j][v]) =
+                            __ldg(reinterpret_cast<const float4*>(src + v));
                 } else {
 #pragma unroll
+                    for (int v = 0; v < VEC; ++v) ex[j][v] = i + v >= 0 && i + v < V ? src[v] : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < F; ++j) {
+                const int at = g + j * NT, i = row.index(at);
+                if (at >= row.hi) continue;
+                const int64_t e0 = (row.g0 + at) * VEC;
+                float x[VEC];
+                Row<IO>::unpack(u[j], x);
+                if (race && any[j]) {
+#pragma unroll
                     for (int v = 0; v < VEC; ++v)
-                        if (i + v >= 0 && i + v < V) out[e0 + v] = y[v];
+                        if (kept.has(x[v], i + v)) {
+                            const float w = ex2((x[v] - m) * wt.c);
+                            if (w * best.e > best.w * ex[j][v])
+                                best = Cand{w, ex[j][v], x[v], i + v};
+                            if (tally) sum += wt.template fixed<IO>(x[v]);
+                        }
+                }
+                if (prob) {
+                    float w[VEC];
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v)
+                        w[v] = any[j] && kept.has(x[v], i + v) ? wt.template value<IO>(x[v]) * inv
+                                                               : 0.0f;
+                    if (whole[j]) {
+#pragma unroll
+                        for (int v = 0; v < VEC; v += 4)
+                            *reinterpret_cast<float4*>(prob + e0 + v) =
+                                make_float4(w[v], w[v + 1], w[v + 2], w[v + 3]);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v)
+                            if (i + v >= 0 && i + v < V) prob[e0 + v] = w[v];
+                    }
+                }
+                if (out) {
+                    alignas(16) T y[VEC];
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v)
+                        y[v] = (T)(bad || (any[j] && kept.has(x[v], i + v)) ? x[v] : -INFINITY);
+                    if (whole[j]) {
+                        reinterpret_cast<uint4*>(out)[row.g0 + at] =
+                            *reinterpret_cast<const uint4*>(y);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v)
+                            if (i + v >= 0 && i + v < V) out[e0 + v] = y[v];
+                    }
                 }
             }
         }
-    }
     if (!e) return;                              // no CTA reads another's memory past here
     block_best(best, sh);
     if (tally) {
@@ -841,31 +924,21 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     }
 }
 
-// CTAs per row: as many as it takes for two CTAs' slices to share an SM, and more
-// while the rows leave SMs idle (no slice under 64 groups).
-template <int IO>
-cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
-    constexpr int VEC = Row<IO>::VEC;
-    const int two = 78 * 1024, most = 180 * 1024;        // bytes of a slice, two and one to an SM
-    const int64_t groups = ((int64_t)c.V + VEC - 1) / VEC + 1;
-    int sms = device_sm_count();
-    if (sms < 1) sms = 1;
-    int C = 1;
-    while (C < MAX_CLUSTER && groups / C > 64 &&
-           ((int64_t)c.R * C <= sms || (groups + C - 1) / C * 16 > two))
-        C *= 2;
+template <int IO, int C>
+cudaError_t launch_c(const spec_sample_cfg& c, SampleArgs& a, int64_t groups, cudaStream_t st) {
+    const int most = 180 * 1024;                         // a slice, with one CTA to an SM
     const int64_t share = (groups + C - 1) / C;
     a.resident = (int)(share * 16 > most ? most / 16 : share);
-    const size_t smem = (size_t)a.resident * 16;
-    cudaError_t e = cudaFuncSetAttribute(sample_rows<IO>,
+    cudaError_t e = cudaFuncSetAttribute(sample_rows<IO, C>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(sample_rows<IO>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && C > 8)
+        e = cudaFuncSetAttribute(sample_rows<IO, C>,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(c.R * C));
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = (size_t)a.resident * 16;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -875,7 +948,29 @@ cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_rows<IO>, a);
+    return cudaLaunchKernelEx(&cfg, sample_rows<IO, C>, a);
+}
+
+// CTAs per row: as many as it takes for two CTAs' slices to share an SM, and more
+// while the rows leave SMs idle (no slice under 64 groups).
+template <int IO>
+cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
+    constexpr int VEC = Row<IO>::VEC;
+    const int two = 78 * 1024;                           // a slice, with two CTAs to an SM
+    const int64_t groups = ((int64_t)c.V + VEC - 1) / VEC + 1;
+    int sms = device_sm_count();
+    if (sms < 1) sms = 1;
+    int C = 1;
+    while (C < MAX_CLUSTER && groups / C > 64 &&
+           ((int64_t)c.R * C <= sms || (groups + C - 1) / C * 16 > two))
+        C *= 2;
+    switch (C) {
+        case 1: return launch_c<IO, 1>(c, a, groups, st);
+        case 2: return launch_c<IO, 2>(c, a, groups, st);
+        case 4: return launch_c<IO, 4>(c, a, groups, st);
+        case 8: return launch_c<IO, 8>(c, a, groups, st);
+        default: return launch_c<IO, 16>(c, a, groups, st);
+    }
 }
 
 }  // namespace
