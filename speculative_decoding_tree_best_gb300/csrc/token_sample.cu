@@ -18,12 +18,14 @@
 //                 The least of these values is not above the k-th largest logit: the
 //                 logits from there on (few more than k) are gathered in one CTA,
 //                 sorted, and all filters and the draw decided on the sorted list.
-//   bf16          Logits take few values: a histogram of counts over the values
-//                 (8192 of them from the maximum down, those within 2^-24 of 0 as
-//                 one) holds all that the masses need, a weight a value; what is
-//                 left is how many of the tokens at the border value stay, the
-//                 first ones.
-//   else          A radix selection on the key K = (logit's bits, made to order like
+//   else          A histogram over bins of 2^-7 of a value's binade, from the maximum
+//                 down, names the bin that the border is in.  bf16 logits take one
+//                 value in a bin: counts are all that masses need, a weight a bin, and
+//                 the tokens at the border value stay from the first on.  fp32 logits'
+//                 masses are added up themselves, and the bin's tokens gathered and
+//                 sorted.  What lies below the bins counts in the totals.
+//   and where that is not enough (a bin too full for the list, a border below the bins)
+//                 a radix selection on the key K = (logit's bits, made to order like
 //                 the number; index, falling), one 52-bit integer, different for
 //                 every token: a histogram of F over the top bits of K names the
 //                 bin that the border is in, which becomes the next range.
@@ -44,9 +46,12 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int NT = 512;
-constexpr int NBIN = 8192;               // bins of counts
-constexpr int NMASS = 4096;              // bins of masses (as many bytes)
+constexpr int NBIN = 4096;               // bins of counts
+constexpr int NMASS = NBIN / 2;          // bins of masses (as many bytes)
 constexpr int LIST = 2048;               // tokens that the sorted list holds
+constexpr int ODD = 256;                 // tokens beside the bins that are noted down
+constexpr int SOME = 64;                 // of a CTA, and
+constexpr int POOL = 256;                // of a cluster: maxima that the k-th largest is bounded by
 constexpr int IDX_BITS = 20;             // of a key: V <= 2^20
 constexpr uint32_t IDX_MAX = (1u << IDX_BITS) - 1;
 constexpr int MAX_CLUSTER = 16;
@@ -77,7 +82,7 @@ struct alignas(16) Border {
     uint32_t tokens;         // of the bin
     int state;
 };
-enum { NOT_FOUND = 0, FOUND = 1, NARROWED = 2 };
+enum { NOT_FOUND = 0, FOUND = 1, NARROWED = 2, BELOW = 3 };
 
 struct Cand {
     float w, e, x;           // the score is w / e
@@ -102,7 +107,7 @@ struct Params {
 };
 
 struct Shared {
-    union {
+    union alignas(16) {
         uint32_t count[NBIN];
         struct {
             uint32_t lo[NMASS], hi[NMASS];
@@ -111,15 +116,20 @@ struct Shared {
     };
     u64 pow2[64];
     u64 part[NT / 32];
-    u64 cta_sum[MAX_CLUSTER];
+    u64 cta_sum[MAX_CLUSTER], cta_rest[MAX_CLUSTER];
+    u64 near_0, rest;                    // F of what the bins do not hold: see bins()
+    uint32_t odd_ones;
+    float odd[ODD];
     Border border;
     Params prm;
     Cand cand[MAX_CLUSTER];
     Cand warp_cand[NT / 32];
     float2 cta_max[MAX_CLUSTER];         // and the value that enough of its threads reach
     float warp_max[NT / 32];
+    float some[SOME], pool[NT], bound;   // for the bound on the top_k-th: see the kernel
     uint32_t ties[MAX_CLUSTER];
-    uint32_t listed;
+    uint32_t listed[MAX_CLUSTER];        // tokens in the list, by the CTA they came from
+    uint32_t my_listed;
     int border_index;
 };
 
@@ -282,11 +292,17 @@ struct Kept {
     __device__ __forceinline__ bool has(float x, int i) const {
         return x > v || (x == v && i <= last);
     }
+    // whether x alone says: all of the logits at v stay
+    __device__ __forceinline__ bool by_value() const { return last == (int)IDX_MAX; }
 };
 
 __device__ __forceinline__ float value_of(u64 key) {
     const uint32_t k = (uint32_t)(key >> IDX_BITS);
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+// what stays when of those at v none do: the numbers above v
+__device__ __forceinline__ Kept above_value(float v) {
+    return Kept{value_of((u64)(key_of(v) + 1) << IDX_BITS), (int)IDX_MAX};
 }
 __device__ __forceinline__ int index_of(u64 key) { return IDX_MAX - ((uint32_t)key & IDX_MAX); }
 
@@ -296,16 +312,20 @@ template <int C> struct Ctx {
     int rank, tid;
     Weights wt;
 
-    // the sum of the CTAs' x before this one, and of all
-    __device__ __forceinline__ void totals(u64 x, u64& before, u64& all) {
-        if (tid < C) *cl.map_shared_rank(&sh.cta_sum[rank], tid) = x;
+    // the sum of the CTAs' x before this one, and of all; of their `rest`
+    __device__ __forceinline__ void totals(u64 x, u64& before, u64& all, u64 mine_rest, u64& rest) {
+        if (tid < C) {
+            *cl.map_shared_rank(&sh.cta_sum[rank], tid) = x;
+            *cl.map_shared_rank(&sh.cta_rest[rank], tid) = mine_rest;
+        }
         cl.sync();
-        before = all = 0;
+        before = all = rest = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const u64 y = sh.cta_sum[c];
             before += c < rank ? y : 0;
             all += y;
+            rest += sh.cta_rest[c];
         }
     }
     __device__ __forceinline__ void tell(const Border& b) {
@@ -326,9 +346,10 @@ template <bool MASS> __device__ __forceinline__ u64 target_of(u64 want, u64 all)
     return max(__umul64hi(all, want) + (all * want != 0), (u64)1);
 }
 
-// ---- bins of bf16's values: signed steps from 0, the smallest magnitudes as 0
+// ---- bins: signed steps of 2^-7 of a binade from 0 (bf16's values), the smallest
+// magnitudes as 0
 
-constexpr int NEAR_0 = (127 - 24) << 7;                  // 2^-24
+constexpr int NEAR_0 = (127 - 12) << 7;                  // 2^-12
 constexpr int FARTHEST = 0x7f80 - NEAR_0;                // infinity
 
 __device__ __forceinline__ int step_of(float x) {
@@ -346,52 +367,143 @@ __device__ __forceinline__ float step_least(int s) {
     return __uint_as_float(s > 0 ? b : b | 0x8000ffffu);
 }
 
-// The border bin of counts that every CTA has in sh.count, bin 0 the maximum's
-// (`top` its step): tells all the bin and its tokens, `sum` = F before it and
-// `target` = what is wanted of it.  The cluster has not synchronised since the
-// counts were made.
-template <bool MASS, int IO, int C>
+// What the bins hold: the tokens' number (top_k), the number at a bf16 value, which
+// its weight makes a mass, or fp32 logits' masses, two steps to a bin.
+enum { COUNTS, VALUES, MASSES };
+
+template <int KIND> __device__ __forceinline__ int bin_of(int top, float x) {
+    const int d = top - step_of(x);
+    return KIND == MASSES ? d >> 1 : d;
+}
+
+// Adds to bin `b` of masses, in two words: 64-bit atomics on shared memory are loops.
+__device__ __forceinline__ void add_mass(Shared& sh, int b, u64 w) {
+    const uint32_t lo = (uint32_t)w, old = atomicAdd(&sh.mass.lo[b], lo);
+    const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old);
+    if (hi) atomicAdd(&sh.mass.hi[b], hi);
+}
+
+// This CTA's histogram of `kept`, bin 0 the maximum's (`top` its step).  Beside it
+// sh.rest has F of what lies below the bins, and with VALUES sh.near_0 that of the
+// numbers in the bin of 0 that are not 0.
+template <int KIND, int IO, int C>
+__device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& kept, int top) {
+    Shared& sh = k.sh;
+    for (int b = k.tid; b < NBIN; b += NT) sh.count[b] = 0;
+    if (k.tid == 0) {
+        sh.near_0 = sh.rest = 0;
+        sh.odd_ones = 0;
+    }
+    __syncthreads();
+    constexpr int END = KIND == MASSES ? NMASS : NBIN;
+    const float m = k.wt.m, far = k.wt.far;
+    // Odd ones, seldom there, are noted down for later: below the bins, or near 0
+    // (where a bin holds more than one value).  Taken as they came, they made the pass
+    // twice as long: the block waits for the warp with most of them.
+    auto odd_one = [&](int b, float x) {
+        return b >= END ? KIND == COUNTS || m - x <= far : KIND == VALUES && b == top;
+    };
+    auto one = [&](float x, bool in) {
+        const int b = bin_of<KIND>(top, x);
+        if (!in) return;
+        if (b >= END || (KIND == VALUES && b == top)) {
+            if (!odd_one(b, x)) return;
+            const uint32_t at = atomicAdd(&sh.odd_ones, 1u);
+            if (at < ODD) sh.odd[at] = x;
+        } else if (KIND != MASSES) {
+            atomicAdd(&sh.count[b], 1u);
+        } else if (m - x <= far) {
+            add_mass(sh, b, k.wt.template fixed<IO>(x));
+        }
+    };
+    if (kept.by_value())
+        row.each([&](float x, int) { one(x, x >= kept.v); });
+    else
+        row.each([&](float x, int i) { one(x, kept.has(x, i)); });
+    u64 near = 0, rest = 0;
+    auto look = [&](float x) {
+        const int b = bin_of<KIND>(top, x);
+        if (b < END && x == 0.0f) atomicAdd(&sh.count[b], 1u);
+        else if (KIND == COUNTS) ++rest;
+        else (b < END ? near : rest) += k.wt.template fixed<IO>(x);
+    };
+    __syncthreads();
+    if (sh.odd_ones <= ODD) {
+        for (int j = k.tid; j < (int)sh.odd_ones; j += NT) look(sh.odd[j]);
+    } else {
+        row.each([&](float x, int i) {
+            if (kept.has(x, i) && odd_one(bin_of<KIND>(top, x), x)) look(x);
+        });
+    }
+    if (sh.odd_ones) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            near += __shfl_xor_sync(0xffffffffu, near, o);
+            rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        }
+        if (k.tid % 32 == 0) {
+            if (near) atomicAdd(&sh.near_0, near);
+            if (rest) atomicAdd(&sh.rest, rest);
+        }
+    }
+}
+
+// The border bin of all CTAs' histograms: tells them the bin and its tokens (but with
+// MASSES), `sum` = F before it and `target` = what is wanted of it (BELOW: the border
+// is below the bins).  The cluster has not synchronised since bins().
+template <int KIND, int IO, int C>
 __device__ __forceinline__ void border_bin(Ctx<C>& k, u64 want, int top) {
     Shared& sh = k.sh;
     k.cl.sync();
     // bins [from, from + RUN) are this thread's: 16-byte pieces of four
-    constexpr int PART = NBIN / C, RUN = PART / NT < 4 ? 4 : PART / NT;
+    constexpr int N = KIND == MASSES ? NMASS : NBIN;
+    constexpr int PART = N / C, RUN = PART / NT < 4 ? 4 : PART / NT;
     const bool mine = k.tid * RUN < PART;
     const int from = k.rank * PART + k.tid * RUN;
     uint32_t n[RUN];
     u64 f[RUN], s = 0;
 #pragma unroll
     for (int j = 0; j < RUN; j += 4) {
-        uint4 x[C], t = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            x[c] = mine ? *reinterpret_cast<const uint4*>(
-                              k.cl.map_shared_rank(&sh.count[from + j], (k.rank + c) % C))
-                        : t;
+        uint4 x[C], y[C];
+        const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            t.x += x[c].x;
-            t.y += x[c].y;
-            t.z += x[c].z;
-            t.w += x[c].w;
+            x[c] = y[c] = none;
+            if (!mine) continue;
+            const uint32_t* src = k.cl.map_shared_rank(&sh.count[from + j], (k.rank + c) % C);
+            x[c] = *reinterpret_cast<const uint4*>(src);
+            if (KIND == MASSES) y[c] = *reinterpret_cast<const uint4*>(src + NMASS);
         }
-        n[j] = t.x;
-        n[j + 1] = t.y;
-        n[j + 2] = t.z;
-        n[j + 3] = t.w;
+        n[j] = n[j + 1] = n[j + 2] = n[j + 3] = 0;
+        f[j] = f[j + 1] = f[j + 2] = f[j + 3] = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const uint32_t lo[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+            const uint32_t hi[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (KIND == MASSES) f[j + i] += (u64)hi[i] << 32 | lo[i];
+                else n[j + i] += lo[i];
+            }
+        }
     }
 #pragma unroll
     for (int j = 0; j < RUN; ++j) {
-        f[j] = n[j];
-        if (MASS && n[j]) f[j] *= k.wt.template fixed<IO>(step_value(top - from - j));
+        if (KIND != MASSES) f[j] = n[j];
+        if (KIND == VALUES) {
+            if (n[j]) f[j] *= k.wt.template fixed<IO>(step_value(top - from - j));
+            if (mine && from + j == top)
+                for (int c = 0; c < C; ++c) f[j] += *k.cl.map_shared_rank(&sh.near_0, c);
+        }
         s += f[j];
     }
-    u64 mine_all, before_me, all;
+    u64 mine_all, before_me, all, rest;
     u64 at = block_prefix(s, sh.part, mine_all);
-    k.totals(mine_all, before_me, all);
+    k.totals(mine_all, before_me, all, sh.rest, rest);
     at += before_me;
-    const u64 target = target_of<MASS>(want, all);
-    if (k.tid == 0 && k.rank == 0 && all < target) k.tell(Border{0, 0, 0, 0, NOT_FOUND});
+    const u64 target = target_of<KIND != COUNTS>(want, all + rest);
+    if (k.tid == 0 && k.rank == 0 && all < target)
+        k.tell(Border{0, 0, 0, 0, all + rest < target ? NOT_FOUND : BELOW});
     if (at < target && target <= at + s) {               // one thread of the cluster, or none
         Border b{};
 #pragma unroll
@@ -417,17 +529,13 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
         for (int b = tid; b < NBIN; b += NT) sh.count[b] = 0;
         __syncthreads();
         const u64 span = hi - lo;
-        const int shift = max(0, 64 - __clzll((long long)span) - 12);     // span >> shift < NMASS
+        const int shift = max(0, 64 - __clzll((long long)span) - 11);     // span >> shift < NMASS
         row.each([&](float x, int i) {
             const u64 key = key_of(x, i);
             if (key < lo || key > hi || !kept.has(x, i)) return;
             const int bin = (int)((hi - key) >> shift);
             if (MASS) {
-                const u64 w = k.wt.template fixed<IO>(x);
-                const uint32_t wl = (uint32_t)w;
-                const uint32_t old = atomicAdd(&sh.mass.lo[bin], wl);
-                const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
-                if (wh) atomicAdd(&sh.mass.hi[bin], wh);
+                add_mass(sh, bin, k.wt.template fixed<IO>(x));
             } else {
                 atomicAdd(&sh.count[bin], 1u);
             }
@@ -449,9 +557,9 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
             }
             s += f[j];
         }
-        u64 mine_all, before_me, all;
+        u64 mine_all, before_me, all, rest;
         u64 at = block_prefix(s, sh.part, mine_all);
-        k.totals(mine_all, before_me, all);
+        k.totals(mine_all, before_me, all, 0, rest);
         at += before_me + above;
         if (pass == 0) target = target_of<MASS>(want, all);
         if (tid == 0 && k.rank == 0 && above + all < target)
@@ -476,17 +584,17 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
     }
 }
 
-// How many of this CTA's tokens at value v stay when the first `want` of all do, as
-// the last index that stays.  `mine`: the CTA's number of them.
+// What stays of this CTA's when of the tokens at value v the first `want` of all do.
+// `mine`: the CTA's number of them.
 template <int IO, int C>
-__device__ __forceinline__ int last_tie(Ctx<C>& k, const Row<IO>& row, const Kept& in, float v, u64 want, uint32_t mine) {
+__device__ __forceinline__ Kept first_ties(Ctx<C>& k, const Row<IO>& row, const Kept& in, float v, u64 want, uint32_t mine) {
     Shared& sh = k.sh;
     if (k.tid < C) *k.cl.map_shared_rank(&sh.ties[k.rank], k.tid) = mine;
     k.cl.sync();
     u64 before = 0;
     for (int c = 0; c < k.rank; ++c) before += sh.ties[c];
-    if (want <= before) return -1;
-    if (want >= before + mine) return in.v == v ? in.last : (int)IDX_MAX;
+    if (want <= before) return above_value(v);
+    if (want >= before + mine) return Kept{v, in.v == v ? in.last : (int)IDX_MAX};
     // the border is here: a run of groups a thread, in order
     const uint32_t left = (uint32_t)(want - before);
     const int n = row.hi - row.lo, run = (n + NT - 1) / NT;
@@ -500,63 +608,14 @@ __device__ __forceinline__ int last_tie(Ctx<C>& k, const Row<IO>& row, const Kep
             if (x == v && in.has(x, i) && ++at == left) sh.border_index = i;
         });
     __syncthreads();
-    return sh.border_index;
-}
-
-// Narrows `kept` to its shortest prefix whose F reaches the target; it stays as it is
-// where F never does.  MASS leaves the sum of its weights in `sum`.
-template <bool MASS, int IO, int C>
-__device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept, u64 want, u64& sum) {
-    Shared& sh = k.sh;
-    if constexpr (IO == SPEC_IO_BF16) {
-        const int top = step_of(k.wt.m), least = top - (NBIN - 1);
-        // whether everything, or all that has weight, is in the bins
-        const float end = least <= -FARTHEST ? -INFINITY : step_value(least);
-        const bool whole = kept.v >= end || (MASS && k.wt.m - end > k.wt.far);
-        if (whole || !MASS) {
-            for (int b = k.tid; b < NBIN; b += NT) sh.count[b] = 0;
-            __syncthreads();
-            // (bins that weigh nothing stay empty; without a border value so far only
-            // -inf has to be kept out, which the bins do unless they reach it)
-            const int bins = !MASS || k.wt.far >= 3.0e38f
-                                 ? NBIN : min(NBIN, top - step_of(k.wt.m - k.wt.far) + 2);
-            if (least > -FARTHEST && kept.v == LOWEST && kept.last == (int)IDX_MAX)
-                row.each([&](float x, int) {
-                    const int bin = top - step_of(x);
-                    if (bin < bins) atomicAdd(&sh.count[bin], 1u);
-                });
-            else
-                row.each([&](float x, int i) {
-                    const int bin = top - step_of(x);
-                    if (bin < bins && kept.has(x, i)) atomicAdd(&sh.count[bin], 1u);
-                });
-            border_bin<MASS, IO>(k, want, top);
-            const Border b = sh.border;
-            if (b.state == NOT_FOUND && whole) return;
-            const int s = top - (int)b.from;
-            if (b.state != NOT_FOUND && s != 0) {
-                const float v = step_value(s);
-                const u64 w = MASS ? k.wt.template fixed<IO>(v) : 1;
-                const u64 n = (b.target + w - 1) / w;
-                if (MASS) sum = b.sum + n * w;
-                int last = kept.v == v ? kept.last : (int)IDX_MAX;
-                if (n < b.tokens) last = last_tie<IO>(k, row, kept, v, n, sh.count[b.from]);
-                kept = Kept{v, last};
-                return;
-            }
-        }
-    }
-    const Border b = radix<MASS, IO>(k, row, kept, want);
-    if (b.state == NOT_FOUND) return;
-    if (MASS) sum = b.sum;
-    kept = Kept{value_of(b.from), index_of(b.from)};
+    return Kept{v, sh.border_index};
 }
 
 // Sorts n keys (1 <= n <= LIST), the largest first, and returns where they are in `list`
 // (which has room for the next power of two).  Up to RANKED keys by counting how many
 // are larger, the threads shared out over the keys; more in a bitonic network.
-constexpr int RANKED = 512;
-static_assert(RANKED <= NT && 2 * RANKED <= LIST);
+constexpr int RANKED = NT;
+static_assert(2 * RANKED <= LIST);
 
 __device__ __forceinline__ u64* sort_list(u64* list, int n) {
     if (n <= RANKED) {
@@ -564,9 +623,15 @@ __device__ __forceinline__ u64* sort_list(u64* list, int n) {
         while (n << (sh + 1) <= NT && sh < 3) ++sh;
         const int at = threadIdx.x >> sh, part = threadIdx.x & ((1 << sh) - 1);
         const u64 x = at < n ? list[at] : 0;
+        if (threadIdx.x == 0 && n % 2) list[n] = 0;      // keys are read in pairs
+        __syncthreads();
+        const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(list);
         int above = 0;
 #pragma unroll 4
-        for (int i = part; i < n; i += 1 << sh) above += list[i] > x;
+        for (int i = part; 2 * i < n; i += 1 << sh) {
+            const ulonglong2 y = pairs[i];
+            above += (y.x > x) + (y.y > x);
+        }
         for (int o = 1; o < 1 << sh; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
         if (at < n && part == 0) list[RANKED + above] = x;
         __syncthreads();
@@ -607,17 +672,163 @@ __device__ __forceinline__ void block_best(Cand& best, Shared& sh) {
 
 constexpr int SMALL_K = 1024;
 
-// The least fp32 number that `want` threads' maxima reach, to the accuracy of a step
-// (-FLT_MAX or -inf where fewer have one).
-__device__ __forceinline__ float reached(float thread_max, int want) {
-    const int mine = step_of(thread_max);
-    int lo = -FARTHEST, hi = FARTHEST;                   // `want` of them reach lo
+// The least fp32 number that `want` of the n values in v reach, to the accuracy of a
+// step (-inf where fewer are above -inf).  For one warp; n <= NT.
+__device__ __forceinline__ float reached(const float* v, int n, int want) {
+    const int lane = threadIdx.x % 32;
+    int s[NT / 32];
+    int lo = FARTHEST, hi = -FARTHEST;
+#pragma unroll
+    for (int j = 0; j < NT / 32; ++j) {
+        s[j] = -FARTHEST - 1;
+        if (lane + 32 * j < n) {
+            s[j] = step_of(v[lane + 32 * j]);
+            lo = min(lo, s[j]);
+            hi = max(hi, s[j]);
+        }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);              // all of them reach lo
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (want > n) lo = hi = -FARTHEST;
     while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
-        if (__syncthreads_count(mine >= mid) >= want) lo = mid;
+        unsigned count = 0;
+#pragma unroll
+        for (int j = 0; j < NT / 32; ++j) count += s[j] >= mid;
+        if ((int)__reduce_add_sync(0xffffffffu, count) >= want) lo = mid;
         else hi = mid - 1;
     }
-    return lo == -FARTHEST ? -INFINITY : step_least(lo);
+    return lo <= -FARTHEST ? -INFINITY : step_least(lo);
+}
+
+// n values in `v` (n a power of two, at most NT / 2), and which of them is how many below
+// the largest: f(that number, value), once for each, in the threads that have it.
+template <int N, typename P> __device__ __forceinline__ void ranked(const float* v, P&& f) {
+    constexpr int PER = NT / N < 8 ? NT / N : 8;         // threads to a value
+    const int at = threadIdx.x / PER, part = threadIdx.x % PER;
+    if (threadIdx.x >= N * PER) return;
+    const float x = v[at];
+    int above = 0;
+#pragma unroll
+    for (int i = part; i < N; i += PER) above += v[i] > x || (v[i] == x && i < at);
+#pragma unroll
+    for (int o = 1; o < PER; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (part == 0) f(above, x);
+}
+
+// The logits x of the CTA's slice with f(x, i) into its part of the first CTA's list,
+// of LIST / C keys.
+template <int IO, int C, typename P>
+__device__ __forceinline__ void gather(Ctx<C>& k, const Row<IO>& row, bool any, P&& f) {
+    Shared& sh = k.sh;
+    if (any)
+        row.each([&](float x, int i) {
+            if (!f(x, i)) return;
+            const uint32_t at = atomicAdd(&sh.my_listed, 1u);
+            if (at < LIST / C)
+                *k.cl.map_shared_rank(&sh.list[k.rank * (LIST / C) + at], 0) = key_of(x, i);
+        });
+    __syncthreads();
+    if (k.tid == 0) {
+        *k.cl.map_shared_rank(&sh.listed[k.rank], 0) = sh.my_listed;
+        sh.my_listed = 0;
+    }
+    k.cl.sync();
+}
+
+// The border in the first CTA's list (its threads call this): the
+// shortest prefix whose mass reaches `target` (0: top_p of that of the first `limit`),
+// without both the first `limit`.  Tells all the border with `above` added to its
+// sum (NOT_FOUND: the list did not hold them), and with e makes the draw.
+template <int IO, int C>
+__device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int limit, u64 top_p,
+                                           u64 target, u64 above, const float* e, Cand& best) {
+    Shared& sh = k.sh;
+    const int tid = k.tid;
+    // the parts moved together
+    int n = 0;
+    {
+        constexpr int PART = LIST / C, PER = NT / C;     // threads to a part
+        const int part = tid / PER;
+        bool over = false;
+        int to = 0;
+        u64 key[PART / PER];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int y = (int)sh.listed[c];
+            over |= y > PART;
+            if (c < part) to += y;
+            n += y;
+        }
+        if (over) {
+            if (tid == 0) k.tell(Border{0, 0, 0, 0, NOT_FOUND});
+            return;
+        }
+        const int mine = (int)sh.listed[part];
+#pragma unroll
+        for (int j = 0; j < PART / PER; ++j)
+            if (tid % PER + j * PER < mine) key[j] = sh.list[part * PART + tid % PER + j * PER];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < PART / PER; ++j)
+            if (tid % PER + j * PER < mine) sh.list[to + tid % PER + j * PER] = key[j];
+        __syncthreads();
+    }
+    limit = min(n, limit);
+    if (n <= NT && n > 2 * limit) {
+        // most are not among the first `limit`: those below the limit's step leave
+        const u64 key = tid < n ? sh.list[tid] : 0;
+        sh.pool[tid] = tid < n ? value_of(key) : -INFINITY;
+        __syncthreads();
+        if (tid < 32) {
+            const float x = reached(sh.pool, n, limit);
+            if (tid == 0) sh.bound = x;
+        }
+        __syncthreads();
+        const bool stay = tid < n && value_of(key) >= sh.bound;
+        const unsigned mask = __ballot_sync(0xffffffffu, stay);
+        if (tid % 32 == 0) sh.part[tid / 32] = __popc(mask);
+        __syncthreads();
+        int at = __popc(mask & ((1u << (tid % 32)) - 1));
+        n = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < tid / 32) at += (int)sh.part[w];
+            n += (int)sh.part[w];
+        }
+        if (stay) sh.list[at] = key;
+        __syncthreads();
+    }
+    const u64* list = sort_list(sh.list, n);
+    // a run of keys a thread; their random numbers on their way meanwhile
+    const int run = n <= NT ? 1 : LIST / NT;
+    u64 w[LIST / NT], s = 0, total;
+    float ex[LIST / NT], x[LIST / NT];
+    int i[LIST / NT];
+#pragma unroll
+    for (int j = 0; j < LIST / NT; ++j) {
+        const int at = tid * run + j;
+        w[j] = 0;
+        if (j >= run || at >= limit) continue;
+        x[j] = value_of(list[at]);
+        i[j] = index_of(list[at]);
+        if (e) ex[j] = e[row.r0 + i[j]];
+        w[j] = k.wt.template fixed<IO>(x[j]);
+        s += w[j];
+    }
+    u64 before = block_prefix(s, sh.part, total);
+    const bool by_mass = target || top_p;
+    if (top_p) target = target_of<true>(top_p, total);
+#pragma unroll
+    for (int j = 0; j < LIST / NT; ++j) {
+        const int at = tid * run + j;
+        if (j >= run || at >= limit) continue;
+        const bool in = !by_mass || before < target;
+        if (in && (by_mass ? target <= before + w[j] : at == limit - 1))
+            k.tell(Border{list[at], above + before + w[j], 0, 0, FOUND});
+        if (in && e) take(best, Cand{k.wt.template value<IO>(x[j]), ex[j], x[j], i[j]});
+        before += w[j];
+    }
 }
 
 // The filters with a small top_k, on the sorted list of the logits from `cut` on,
@@ -627,60 +838,54 @@ template <int IO, int C>
 __device__ __forceinline__ bool short_list(Ctx<C>& k, const Row<IO>& row, Kept& kept,
                                            float thread_max, float cut, const float* e, u64& sum,
                                            Cand& best) {
-    Shared& sh = k.sh;
-    const int tid = k.tid;
-    const Params& prm = sh.prm;
-    if (thread_max >= cut)
-        row.each([&](float x, int i) {
-            if (!(x >= cut)) return;
-            const uint32_t at = atomicAdd(k.cl.map_shared_rank(&sh.listed, 0), 1u);
-            if (at < LIST) *k.cl.map_shared_rank(&sh.list[at], 0) = key_of(x, i);
-        });
+    gather<IO>(k, row, thread_max >= cut, [&](float x, int) { return x >= cut; });
+    if (k.rank == 0)
+        solve_list<IO>(k, row, k.sh.prm.top_k, k.sh.prm.top_p, 0, 0, e, best);
     k.cl.sync();
-    if (k.rank == 0) {
-        const int n = (int)min(sh.listed, (uint32_t)LIST + 1);
-        if (n > LIST) {
-            if (tid == 0) k.tell(Border{0, 0, 0, 0, NOT_FOUND});
-        } else {
-            const u64* list = sort_list(sh.list, n);
-            // a run of keys a thread; their random numbers on their way meanwhile
-            const int all = min(n, prm.top_k), run = n <= NT ? 1 : LIST / NT;
-            u64 w[LIST / NT], s = 0, total;
-            float ex[LIST / NT], x[LIST / NT];
-            int i[LIST / NT];
-#pragma unroll
-            for (int j = 0; j < LIST / NT; ++j) {
-                const int at = tid * run + j;
-                w[j] = 0;
-                if (j >= run || at >= all) continue;
-                x[j] = value_of(list[at]);
-                i[j] = index_of(list[at]);
-                if (e) ex[j] = e[row.r0 + i[j]];
-                w[j] = k.wt.template fixed<IO>(x[j]);
-                s += w[j];
-            }
-            const u64 start = block_prefix(s, sh.part, total);
-            // the prefix ends where it reaches the target; without a top_p at `all`
-            const u64 target = prm.top_p ? target_of<true>(prm.top_p, total) : total;
-            u64 before = start;
-#pragma unroll
-            for (int j = 0; j < LIST / NT; ++j) {
-                const int at = tid * run + j;
-                if (j >= run || at >= all) continue;
-                const bool in = !prm.top_p || before < target;
-                if (in && (prm.top_p ? target <= before + w[j] : at == all - 1))
-                    k.tell(Border{list[at], before + w[j], 0, 0, FOUND});
-                if (in && e) take(best, Cand{k.wt.template value<IO>(x[j]), ex[j], x[j], i[j]});
-                before += w[j];
-            }
-        }
-    }
-    k.cl.sync();
-    const Border b = sh.border;
+    const Border b = k.sh.border;
     if (b.state == NOT_FOUND) return false;
     sum = b.sum;
     kept = Kept{value_of(b.from), index_of(b.from)};
     return true;
+}
+
+// Narrows `kept` to its shortest prefix whose F reaches the target; it stays as it is
+// where F never does.  MASS leaves the sum of its weights in `sum`.
+template <bool MASS, int IO, int C>
+__device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept, u64 want,
+                                       u64& sum) {
+    constexpr int KIND = !MASS ? COUNTS : (IO == SPEC_IO_BF16 ? VALUES : MASSES);
+    Shared& sh = k.sh;
+    const int top = step_of(k.wt.m);
+    bins<KIND, IO>(k, row, kept, top);
+    border_bin<KIND, IO>(k, want, top);
+    Border b = sh.border;
+    if (b.state == NOT_FOUND) return;
+    if (b.state == NARROWED) {
+        const int bin = (int)b.from, s = top - bin;
+        if (IO == SPEC_IO_BF16 && s != 0) {              // one value
+            const float v = step_value(s);
+            const u64 w = MASS ? k.wt.template fixed<IO>(v) : 1;
+            const u64 n = (b.target + w - 1) / w;
+            if (MASS) sum = b.sum + n * w;
+            if (n < b.tokens) kept = first_ties<IO>(k, row, kept, v, n, sh.count[bin]);
+            else kept = Kept{v, kept.v == v ? kept.last : (int)IDX_MAX};
+            return;
+        }
+        gather<IO>(k, row, true, [&](float x, int i) {
+            return bin_of<KIND>(top, x) == bin && kept.has(x, i);
+        });
+        Cand none;
+        if (k.rank == 0)
+            solve_list<IO>(k, row, MASS ? LIST : (int)b.target, 0, MASS ? b.target : 0, b.sum,
+                           nullptr, none);
+        k.cl.sync();
+        b = sh.border;
+    }
+    if (b.state != FOUND) b = radix<MASS, IO>(k, row, kept, want);
+    if (b.state == NOT_FOUND) return;
+    if (MASS) sum = b.sum;
+    kept = Kept{value_of(b.from), index_of(b.from)};
 }
 
 __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req) {
@@ -697,10 +902,11 @@ __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req
     y.top_p = top_p >= 1.0f ? 0 : max((u64)(fmaxf(top_p, 0.0f) * 0x1p64f), (u64)1);
     y.min_p = min_p;
     if (min_p > 0.0f && min_p < 1.0f) y.min_low = (double)t * log((double)min_p);
-    const double c = t > 0.0f ? fmin(1.4426950408889634 / (double)t, 1e38) : 0.0;
-    y.c = (float)c;
-    y.c_lo = (float)(c - (double)y.c);
-    y.far = c > 0.0 ? (float)fmin((double)CUT / c, 3.0e38) : 3.4028234663852886e38f;
+    // log2(e) / t to 2^-46: the quotient's remainder, divided again
+    y.c = fminf(1.4426950216293335f / t, 1e38f);
+    y.c_lo = y.c < 1e38f && t < INFINITY ? (fmaf(-y.c, t, 1.4426950216293335f) + 1.925963033500011e-8f) / t : 0.0f;
+    if (t == 0.0f) y.c = y.c_lo = 0.0f;
+    y.far = y.c > 0.0f ? fminf(CUT / y.c, 3.0e38f) : 3.4028234663852886e38f;
     return y;
 }
 
@@ -715,7 +921,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     const int rank = cl.block_rank(), tid = threadIdx.x;
     const int lane = tid % 32, warp = tid / 32;
     const int r = blockIdx.x / C, V = a.V;
-    if (tid == 0) sh.listed = 0;
+    if (tid == 0) sh.my_listed = 0;
     if (tid < 64) sh.pow2[tid] = a.pow2[tid];
     Row<IO> row;
     row.logits = static_cast<const T*>(a.logits);
@@ -750,24 +956,46 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     }
     const float thread_max = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < 32; o *= 2) {
+        if (o == NT / SOME && lane % o == 0) sh.some[tid / o] = m;
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
     if (lane == 0) sh.warp_max[warp] = m;
     __syncthreads();
     m = sh.warp_max[lane % (NT / 32)];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    static_assert(NT / 32 == 16);
-    const bool small_k = sh.prm.top_k > 0 && sh.prm.top_k < V &&
-                         sh.prm.top_k <= min(SMALL_K, C * NT / 2);
+    for (int o = NT / 64; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // A lower bound of the k-th largest logit: the k-th of a pool of maxima of threads'
+    // shares, of each CTA its largest ones; or, where k is too large for that, the least
+    // of what k / C of each CTA's threads reach.
+    const int top_k = sh.prm.top_k < V ? sh.prm.top_k : 0;
+    constexpr int EACH = POOL / C < SOME ? POOL / C : SOME;
+    const bool pooled = top_k > 0 && top_k <= EACH * C * 3 / 4;
+    const bool small_k = pooled || (top_k > 0 && top_k <= min(SMALL_K, C * NT / 2));
     float cut = 0.0f;
-    if (small_k) cut = reached(thread_max, (sh.prm.top_k + C - 1) / C);
+    if (small_k && !pooled) {
+        sh.pool[tid] = thread_max;
+        __syncthreads();
+        if (tid < 32) cut = reached(sh.pool, NT, (top_k + C - 1) / C);
+        __syncthreads();                                 // (the pool is written again below)
+    }
     cl.barrier_wait();                                   // everyone has started
+    if (pooled)
+        ranked<SOME>(sh.some, [&](int n, float x) {
+            if (n < EACH)
+#pragma unroll
+                for (int c = 0; c < C; ++c) *cl.map_shared_rank(&sh.pool[rank * EACH + n], c) = x;
+        });
     if (tid < C) *cl.map_shared_rank(&sh.cta_max[rank], tid) = make_float2(m, cut);
     cl.sync();
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         m = max_nan(m, sh.cta_max[c].x);
         cut = fminf(cut, sh.cta_max[c].y);
+    }
+    if (pooled && tid < 32) {
+        const float x = reached(sh.pool, EACH * C, top_k);
+        if (tid == 0) sh.bound = x;
     }
 
     const Params& prm = sh.prm;
@@ -796,9 +1024,10 @@ sample_rows(const __grid_constant__ SampleArgs a) {
         kept.v = __int_as_float(0x7fffffff);             // NaN: nothing
     } else {
         if (small_k)
-            summed = drawn = short_list<IO>(k, row, kept, thread_max, fmaxf(cut, kept.v), e, sum, best);
+            summed = drawn = short_list<IO>(k, row, kept, thread_max,
+                                            fmaxf(pooled ? sh.bound : cut, kept.v), e, sum, best);
         if (!drawn) {
-            if (prm.top_k > 0 && prm.top_k < V) select<false, IO>(k, row, kept, prm.top_k, sum);
+            if (top_k > 0) select<false, IO>(k, row, kept, top_k, sum);
             if (prm.top_p != 0) {
                 select<true, IO>(k, row, kept, prm.top_p, sum);
                 summed = true;
@@ -808,37 +1037,37 @@ sample_rows(const __grid_constant__ SampleArgs a) {
             row.each([&](float x, int i) {
                 if (kept.has(x, i)) sum += wt.template fixed<IO>(x);
             });
-            u64 all, before;
+            u64 all, before, rest;
             block_prefix(sum, sh.part, all);
-            k.totals(all, before, sum);
+            k.totals(all, before, sum, 0, rest);
             summed = true;
         }
     }
 
-    // ---- what stays: the draw and the outputs
+    // ---- what stays: the draw and the outputs (other CTAs' memory is written up to the
+    // next barrier, where there is one, and not read)
     constexpr int F = IO == SPEC_IO_F32 ? 4 : 2;
     auto inverse = [&](u64 s) {
         return s == 0 ? 0.0f : 1.0f / (__ull2float_rn(s) * (1.0f / (float)(1ull << (62 - a.lg))));
     };
     float inv = inverse(sum);
     const bool race = e && !drawn && !bad, tally = !summed && a.out.tok_prob && !bad;
-    // F groups at once, so that their random numbers' loads are under way together
-    if (race || prob || out)
+    // the draw: F groups at once, so that their random numbers' loads are under way together
+    if (race)
         for (int g = row.lo + tid; g < row.hi; g += F * NT) {
             uint4 u[F];
             float ex[F][VEC];
-            bool any[F], whole[F];
+            bool any[F];
 #pragma unroll
             for (int j = 0; j < F; ++j) {
                 const int at = g + j * NT, i = row.index(at);
-                any[j] = whole[j] = false;
+                any[j] = false;
                 if (at >= row.hi) continue;
                 u[j] = row.get(at);
-                whole[j] = i >= 0 && i + VEC <= V;
-                any[j] = Row<IO>::most(u[j]) >= kept.v;  // (never in a bad row)
-                if (!race || !any[j]) continue;
+                any[j] = Row<IO>::most(u[j]) >= kept.v;
+                if (!any[j]) continue;
                 const float* src = e + (row.g0 + at) * VEC;
-                if (whole[j]) {
+                if (i >= 0 && i + VEC <= V) {
 #pragma unroll
                     for (int v = 0; v < VEC; v += 4)
                         *reinterpret_cast<float4*>(&ex[j][v]) =
@@ -848,71 +1077,88 @@ sample_rows(const __grid_constant__ SampleArgs a) {
                     for (int v = 0; v < VEC; ++v) ex[j][v] = i + v >= 0 && i + v < V ? src[v] : 1.0f;
                 }
             }
+            auto draw = [&](auto&& in) {
 #pragma unroll
-            for (int j = 0; j < F; ++j) {
-                const int at = g + j * NT, i = row.index(at);
-                if (at >= row.hi) continue;
-                const int64_t e0 = (row.g0 + at) * VEC;
-                float x[VEC];
-                Row<IO>::unpack(u[j], x);
-                if (race && any[j]) {
+                for (int j = 0; j < F; ++j) {
+                    if (!any[j]) continue;
+                    const int i = row.index(g + j * NT);
+                    float x[VEC];
+                    Row<IO>::unpack(u[j], x);
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v)
-                        if (kept.has(x[v], i + v)) {
-                            const float w = ex2((x[v] - m) * wt.c);
-                            if (w * best.e > best.w * ex[j][v])
-                                best = Cand{w, ex[j][v], x[v], i + v};
-                            if (tally) sum += wt.template fixed<IO>(x[v]);
-                        }
-                }
-                if (prob) {
-                    float w[VEC];
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v)
-                        w[v] = any[j] && kept.has(x[v], i + v) ? wt.template value<IO>(x[v]) * inv
-                                                               : 0.0f;
-                    if (whole[j]) {
-#pragma unroll
-                        for (int v = 0; v < VEC; v += 4)
-                            *reinterpret_cast<float4*>(prob + e0 + v) =
-                                make_float4(w[v], w[v + 1], w[v + 2], w[v + 3]);
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v)
-                            if (i + v >= 0 && i + v < V) prob[e0 + v] = w[v];
+                    for (int v = 0; v < VEC; ++v) {
+                        const float w = ex2((x[v] - m) * wt.c);
+                        if (in(x[v], i + v) && w * best.e > best.w * ex[j][v])
+                            best = Cand{w, ex[j][v], x[v], i + v};
                     }
                 }
-                if (out) {
-                    alignas(16) T y[VEC];
+            };
+            if (kept.by_value()) draw([&](float x, int) { return x >= kept.v; });
+            else draw([&](float x, int i) { return kept.has(x, i); });
+        }
+    if (tally)
+        row.each([&](float x, int i) {
+            if (kept.has(x, i)) sum += wt.template fixed<IO>(x);
+        });
+    if (prob || out)
+        for (int g = row.lo + tid; g < row.hi; g += NT) {
+            const uint4 u = row.get(g);
+            const int64_t e0 = (row.g0 + g) * VEC;
+            const int i = row.index(g);
+            const bool whole = i >= 0 && i + VEC <= V;
+            const bool any = Row<IO>::most(u) >= kept.v;          // (never in a bad row)
+            float x[VEC];
+            Row<IO>::unpack(u, x);
+            if (prob) {
+                float w[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) w[v] = 0.0f;
+                if (any) {
 #pragma unroll
                     for (int v = 0; v < VEC; ++v)
-                        y[v] = (T)(bad || (any[j] && kept.has(x[v], i + v)) ? x[v] : -INFINITY);
-                    if (whole[j]) {
-                        reinterpret_cast<uint4*>(out)[row.g0 + at] =
-                            *reinterpret_cast<const uint4*>(y);
-                    } else {
+                        if (kept.has(x[v], i + v)) w[v] = wt.template value<IO>(x[v]) * inv;
+                }
+                if (whole) {
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v)
-                            if (i + v >= 0 && i + v < V) out[e0 + v] = y[v];
-                    }
+                    for (int v = 0; v < VEC; v += 4)
+                        *reinterpret_cast<float4*>(prob + e0 + v) =
+                            make_float4(w[v], w[v + 1], w[v + 2], w[v + 3]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v)
+                        if (i + v >= 0 && i + v < V) prob[e0 + v] = w[v];
+                }
+            }
+            if (out) {
+                alignas(16) T y[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    y[v] = (T)(bad || (any && kept.has(x[v], i + v)) ? x[v] : -INFINITY);
+                if (whole) {
+                    reinterpret_cast<uint4*>(out)[row.g0 + g] = *reinterpret_cast<const uint4*>(y);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v)
+                        if (i + v >= 0 && i + v < V) out[e0 + v] = y[v];
                 }
             }
         }
-    if (!e) return;                              // no CTA reads another's memory past here
+    if (!e || (drawn && rank != 0)) return;
     block_best(best, sh);
     if (tally) {
         u64 all;
         block_prefix(sum, sh.part, all);
         sum = all;
     }
-    if (tid == 0) {
-        *cl.map_shared_rank(&sh.cand[rank], 0) = best;
-        if (tally) *cl.map_shared_rank(&sh.cta_sum[rank], 0) = sum;
+    if (!drawn) {
+        if (tid == 0) {
+            *cl.map_shared_rank(&sh.cand[rank], 0) = best;
+            if (tally) *cl.map_shared_rank(&sh.cta_sum[rank], 0) = sum;
+        }
+        cl.sync();
     }
-    cl.sync();
     if (rank == 0 && tid == 0) {
-        best = sh.cand[0];
-        for (int c = 1; c < C; ++c) take(best, sh.cand[c]);
+        if (!drawn)
+            for (int c = 0; c < C; ++c) take(best, sh.cand[c]);
         if (tally) {
             sum = 0;
             for (int c = 0; c < C; ++c) sum += sh.cta_sum[c];
