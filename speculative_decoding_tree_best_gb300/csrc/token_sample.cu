@@ -245,6 +245,14 @@ template <int IO> struct Row {
         }
     }
     __device__ __forceinline__ int index(int g) const { return (int)((g0 + g) * VEC - r0); }
+    // f(the group's elements, index of the first in the row) for this thread's groups
+    template <typename F> __device__ __forceinline__ void groups(F&& f) const {
+        for (int g = lo + threadIdx.x; g < hi; g += NT) {
+            float x[VEC];
+            unpack(get(g), x);
+            f(x, index(g));
+        }
+    }
     // f(x, index in the row) for the elements of groups [from, to), `step` apart (-inf
     // beside the row)
     template <typename F>
@@ -353,9 +361,8 @@ constexpr int NEAR_0 = (127 - 12) << 7;                  // 2^-12
 constexpr int FARTHEST = 0x7f80 - NEAR_0;                // infinity
 
 __device__ __forceinline__ int step_of(float x) {
-    const int i = __float_as_int(x) >> 16;
-    const int s = max((i & 0x7fff) - NEAR_0, 0);
-    return i < 0 ? -s : s;
+    const int i = __float_as_int(x) >> 16, sign = i >> 31;
+    return (max((i & 0x7fff) - NEAR_0, 0) ^ sign) - sign;
 }
 __device__ __forceinline__ float step_value(int s) {
     const uint32_t b = (uint32_t)(abs(s) + NEAR_0) << 16;
@@ -385,7 +392,7 @@ __device__ __forceinline__ void add_mass(Shared& sh, int b, u64 w) {
 
 // This CTA's histogram of `kept`, bin 0 the maximum's (`top` its step).  Beside it
 // sh.rest has F of what lies below the bins, and with VALUES sh.near_0 that of the
-// numbers in the bin of 0 that are not 0.
+// bin of 0, whose count says nothing of its weights.
 template <int KIND, int IO, int C>
 __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& kept, int top) {
     Shared& sh = k.sh;
@@ -395,44 +402,55 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
         sh.odd_ones = 0;
     }
     __syncthreads();
-    constexpr int END = KIND == MASSES ? NMASS : NBIN;
+    constexpr int END = KIND == MASSES ? NMASS : NBIN, VEC = Row<IO>::VEC;
     const float m = k.wt.m, far = k.wt.far;
     // Odd ones, seldom there, are noted down for later: below the bins, or near 0
     // (where a bin holds more than one value).  Taken as they came, they made the pass
     // twice as long: the block waits for the warp with most of them.
-    auto odd_one = [&](int b, float x) {
-        return b >= END ? KIND == COUNTS || m - x <= far : KIND == VALUES && b == top;
+    auto beside = [&](int b) { return b >= END || (KIND == VALUES && b == top); };
+    auto note = [&](float x) {
+        if (KIND != COUNTS && !(m - x <= far)) return;   // weighs nothing
+        const uint32_t at = atomicAdd(&sh.odd_ones, 1u);
+        if (at < ODD) sh.odd[at] = x;
     };
-    auto one = [&](float x, bool in) {
-        const int b = bin_of<KIND>(top, x);
-        if (!in) return;
-        if (b >= END || (KIND == VALUES && b == top)) {
-            if (!odd_one(b, x)) return;
-            const uint32_t at = atomicAdd(&sh.odd_ones, 1u);
-            if (at < ODD) sh.odd[at] = x;
-        } else if (KIND != MASSES) {
-            atomicAdd(&sh.count[b], 1u);
-        } else if (m - x <= far) {
-            add_mass(sh, b, k.wt.template fixed<IO>(x));
+    row.groups([&](const float (&x)[VEC], int i) {
+        bool odd = false;
+        if (KIND != MASSES && kept.by_value()) {
+            // (what weighs nothing is counted, and weighs nothing)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const int b = bin_of<KIND>(top, x[v]);
+                const bool in = x[v] >= kept.v;
+                odd |= in && beside(b);
+                if (in && b < END) atomicAdd(&sh.count[b], 1u);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const int b = bin_of<KIND>(top, x[v]);
+                const bool in = kept.has(x[v], i + v);
+                odd |= in && beside(b);
+                if (!in || b >= END) continue;
+                if (KIND != MASSES) atomicAdd(&sh.count[b], 1u);
+                else if (m - x[v] <= far) add_mass(sh, b, k.wt.template fixed<IO>(x[v]));
+            }
         }
-    };
-    if (kept.by_value())
-        row.each([&](float x, int) { one(x, x >= kept.v); });
-    else
-        row.each([&](float x, int i) { one(x, kept.has(x, i)); });
+        if (odd)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                if (beside(bin_of<KIND>(top, x[v])) && kept.has(x[v], i + v)) note(x[v]);
+    });
     u64 near = 0, rest = 0;
     auto look = [&](float x) {
-        const int b = bin_of<KIND>(top, x);
-        if (b < END && x == 0.0f) atomicAdd(&sh.count[b], 1u);
-        else if (KIND == COUNTS) ++rest;
-        else (b < END ? near : rest) += k.wt.template fixed<IO>(x);
+        if (KIND == COUNTS) ++rest;
+        else (bin_of<KIND>(top, x) < END ? near : rest) += k.wt.template fixed<IO>(x);
     };
     __syncthreads();
     if (sh.odd_ones <= ODD) {
         for (int j = k.tid; j < (int)sh.odd_ones; j += NT) look(sh.odd[j]);
     } else {
         row.each([&](float x, int i) {
-            if (kept.has(x, i) && odd_one(bin_of<KIND>(top, x), x)) look(x);
+            if (beside(bin_of<KIND>(top, x)) && kept.has(x, i)) look(x);
         });
     }
     if (sh.odd_ones) {
@@ -491,7 +509,8 @@ __device__ __forceinline__ void border_bin(Ctx<C>& k, u64 want, int top) {
     for (int j = 0; j < RUN; ++j) {
         if (KIND != MASSES) f[j] = n[j];
         if (KIND == VALUES) {
-            if (n[j]) f[j] *= k.wt.template fixed<IO>(step_value(top - from - j));
+            if (from + j == top) f[j] = 0;
+            else if (n[j]) f[j] *= k.wt.template fixed<IO>(step_value(top - from - j));
             if (mine && from + j == top)
                 for (int c = 0; c < C; ++c) f[j] += *k.cl.map_shared_rank(&sh.near_0, c);
         }
@@ -656,14 +675,17 @@ __device__ __forceinline__ u64* sort_list(u64* list, int n) {
     return list;
 }
 
+__device__ __forceinline__ void take_across(Cand& best, int o) {
+    take(best, Cand{__shfl_xor_sync(0xffffffffu, best.w, o),
+                    __shfl_xor_sync(0xffffffffu, best.e, o),
+                    __shfl_xor_sync(0xffffffffu, best.x, o),
+                    __shfl_xor_sync(0xffffffffu, best.i, o)});
+}
+
 // The block's best candidate, in thread 0.
 __device__ __forceinline__ void block_best(Cand& best, Shared& sh) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        take(best, Cand{__shfl_xor_sync(0xffffffffu, best.w, o),
-                        __shfl_xor_sync(0xffffffffu, best.e, o),
-                        __shfl_xor_sync(0xffffffffu, best.x, o),
-                        __shfl_xor_sync(0xffffffffu, best.i, o)});
+    for (int o = 16; o > 0; o >>= 1) take_across(best, o);
     if (threadIdx.x % 32 == 0) sh.warp_cand[threadIdx.x / 32] = best;
     __syncthreads();
     if (threadIdx.x == 0)
@@ -888,6 +910,71 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
     kept = Kept{value_of(b.from), index_of(b.from)};
 }
 
+// The race over what stays of this CTA's slice: `best` is the warp's best candidate
+// in all its lanes.
+//   A token is looked at where w / e can be above the best so far, that is
+// log2 e < log2 w + log2(best.e / best.w); and bits(e) 2^-23 - 127 is at most log2 e
+// (the chord is below the logarithm), which makes the test a multiply-add and an
+// integer comparison, in units of 2^-7.  With a best per warp a group passes it
+// seldom after the first few (a division, or two products, and an exponential for
+// every token made 256 rows' draws 40 us longer).
+template <int IO, int C>
+__device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const Kept& kept,
+                                     const float* e, Cand& best) {
+    constexpr int VEC = Row<IO>::VEC;
+    constexpr float MAGIC = 12582912.0f;                 // 1.5 2^23: integers in the low bits
+    const float m = k.wt.m, c = k.wt.c, c7 = fminf(c * 128.0f, 3.0e38f);
+    const int V = (int)(row.r1 - row.r0);
+    const bool by_value = kept.by_value();
+    float bar = 3.0e38f;                                 // everything passes
+    for (int g = row.lo + k.tid - k.tid % 32; g < row.hi; g += NT) {     // the same for the warp
+        const int at = g + k.tid % 32;
+        bool look = false;
+        uint4 u;
+        float ex[VEC];
+        const int i = row.index(at);
+        if (at < row.hi) {
+            u = row.get(at);
+            look = Row<IO>::most(u) >= kept.v;
+        }
+        if (look) {
+            const float* src = e + (row.g0 + at) * VEC;
+            if (i >= 0 && i + VEC <= V) {
+#pragma unroll
+                for (int v = 0; v < VEC; v += 4)
+                    *reinterpret_cast<float4*>(&ex[v]) =
+                        __ldg(reinterpret_cast<const float4*>(src + v));
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) ex[v] = i + v >= 0 && i + v < V ? src[v] : 1.0f;
+            }
+            float x[VEC];
+            Row<IO>::unpack(u, x);
+            look = false;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                look |= x[v] >= kept.v && (__float_as_int(ex[v]) >> 16) + 0x4b400000 <=
+                                              __float_as_int(fmaf(x[v] - m, c7, bar));
+        }
+        if (!__any_sync(0xffffffffu, look)) continue;
+        if (look) {
+            float x[VEC];
+            Row<IO>::unpack(u, x);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                if (!(by_value ? x[v] >= kept.v : kept.has(x[v], i + v))) continue;
+                const float w = ex2((x[v] - m) * c);
+                take(best, Cand{w, ex[v], x[v], i + v});
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) take_across(best, o);
+        // two units above, for the roundings of the test
+        bar = best.w > 0.0f && best.e > 0.0f
+                  ? (__log2f(best.e) - __log2f(best.w) + 127.0f) * 128.0f + 2.0f + MAGIC : 3.0e38f;
+    }
+}
+
 __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req) {
     Params y{};
     float t = p.temperature ? p.temperature[req] : 1.0f;
@@ -1046,55 +1133,12 @@ sample_rows(const __grid_constant__ SampleArgs a) {
 
     // ---- what stays: the draw and the outputs (other CTAs' memory is written up to the
     // next barrier, where there is one, and not read)
-    constexpr int F = IO == SPEC_IO_F32 ? 4 : 2;
     auto inverse = [&](u64 s) {
         return s == 0 ? 0.0f : 1.0f / (__ull2float_rn(s) * (1.0f / (float)(1ull << (62 - a.lg))));
     };
     float inv = inverse(sum);
     const bool race = e && !drawn && !bad, tally = !summed && a.out.tok_prob && !bad;
-    // the draw: F groups at once, so that their random numbers' loads are under way together
-    if (race)
-        for (int g = row.lo + tid; g < row.hi; g += F * NT) {
-            uint4 u[F];
-            float ex[F][VEC];
-            bool any[F];
-#pragma unroll
-            for (int j = 0; j < F; ++j) {
-                const int at = g + j * NT, i = row.index(at);
-                any[j] = false;
-                if (at >= row.hi) continue;
-                u[j] = row.get(at);
-                any[j] = Row<IO>::most(u[j]) >= kept.v;
-                if (!any[j]) continue;
-                const float* src = e + (row.g0 + at) * VEC;
-                if (i >= 0 && i + VEC <= V) {
-#pragma unroll
-                    for (int v = 0; v < VEC; v += 4)
-                        *reinterpret_cast<float4*>(&ex[j][v]) =
-                            __ldg(reinterpret_cast<const float4*>(src + v));
-                } else {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) ex[j][v] = i + v >= 0 && i + v < V ? src[v] : 1.0f;
-                }
-            }
-            auto draw = [&](auto&& in) {
-#pragma unroll
-                for (int j = 0; j < F; ++j) {
-                    if (!any[j]) continue;
-                    const int i = row.index(g + j * NT);
-                    float x[VEC];
-                    Row<IO>::unpack(u[j], x);
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        const float w = ex2((x[v] - m) * wt.c);
-                        if (in(x[v], i + v) && w * best.e > best.w * ex[j][v])
-                            best = Cand{w, ex[j][v], x[v], i + v};
-                    }
-                }
-            };
-            if (kept.by_value()) draw([&](float x, int) { return x >= kept.v; });
-            else draw([&](float x, int i) { return kept.has(x, i); });
-        }
+    if (race) draw(k, row, kept, e, best);
     if (tally)
         row.each([&](float x, int i) {
             if (kept.has(x, i)) sum += wt.template fixed<IO>(x);
