@@ -24,7 +24,7 @@ namespace spec {
 
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 128;
 constexpr int UNR = 2;
 
 // sine and cosine of `turn` 2^-32 turns, times amp
@@ -44,6 +44,12 @@ __device__ __forceinline__ void sincos_turn(uint32_t turn, float amp, float& s, 
     const bool swap = quarter & 1;
     s = (swap ? pc : ps) * (quarter & 2 ? -amp : amp);
     c = (swap ? ps : pc) * ((quarter + 1) & 2 ? -amp : amp);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
 
 struct RopeArgs {
@@ -76,7 +82,7 @@ struct Item {
 };
 
 template <int IO, int KV, int D, int LAYOUT, bool APPEND>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 6)
 rope_rows(const __grid_constant__ RopeArgs a) {
     constexpr int VEC = 16 / sizeof(typename io_t<IO>::T);
     constexpr int PPR = D / VEC, LPR = PPR / 2;        // pieces and lanes of a row
@@ -104,6 +110,7 @@ rope_rows(const __grid_constant__ RopeArgs a) {
     } else if (live) {
         pos = a.pos[row];
     }
+    if (!__any_sync(0xffffffffu, live)) return;          // padding
     auto item = [&](int at) {
         Item x{nullptr, nullptr, 0, -1};
         if (!live || at >= a.items) return x;
@@ -168,11 +175,11 @@ rope_rows(const __grid_constant__ RopeArgs a) {
                            (slot & ((1 << a.sh) - 1))) * PPR;
             if constexpr (APPEND && KV == SPEC_KV_E4M3) {
                 if (__any_sync(0xffffffffu, cached)) {
-                    uint32_t most = 0;
+                    float top = 0.0f;                    // NaN where there is one
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
-                        most = max(most, max(__float_as_uint(x[0][i]) & 0x7fffffffu,
-                                             __float_as_uint(x[1][i]) & 0x7fffffffu));
+                        top = max_nan(max_nan(top, fabsf(x[0][i])), fabsf(x[1][i]));
+                    uint32_t most = __float_as_uint(top);
 #pragma unroll
                     for (int o = 1; o < LPR; o <<= 1)
                         most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -211,7 +218,7 @@ rope_rows(const __grid_constant__ RopeArgs a) {
 // How the heads of a token are shared out: about two loads' worth of threads on
 // every SM before a group takes a second head, at most MOST heads a group (the
 // sines and cosines of eight pairs cost about as much as three heads).
-constexpr int MOST = 8;
+constexpr int MOST = 12;
 
 template <int IO, int KV, int D, int LAYOUT, bool APPEND>
 cudaError_t launch_t(RopeArgs& a, int64_t rows, cudaStream_t st) {
