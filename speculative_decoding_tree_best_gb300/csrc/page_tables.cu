@@ -20,8 +20,8 @@ namespace spec {
 
 namespace {
 
-constexpr int NT = 512;
-// slots per CTA: four 16-byte stores a thread
+constexpr int NT = 256;
+// slots per CTA: four 16-byte stores a thread (512 threads: 11.9 us instead of 10.1 for prompts)
 constexpr int SLOTS = NT * 8;
 
 struct PoolArgs {
@@ -286,12 +286,12 @@ cudaError_t launch_pages_trim(const spec_paged_cfg& c, const spec_page_pool& p,
     size_t smem;
     const cudaError_t e = req_bytes(trim_tables, c.B, smem);
     if (e != cudaSuccess) return e;
-    // no more pages change hands than there are: about eight a thread, a CTA an SM
+    // no more pages change hands than there are: one a thread, a CTA an SM
     const int64_t most = c.n_pages < (int64_t)c.B * c.max_pages ? c.n_pages
                                                                 : (int64_t)c.B * c.max_pages;
     int sms = device_sm_count();
     if (sms < 1) sms = 1;
-    int64_t ctas = (most + 8 * NT - 1) / (8 * NT);
+    int64_t ctas = (most + NT - 1) / NT;
     if (ctas > sms) ctas = sms;
     return launch_k(true, trim_tables, dim3((unsigned)ctas), dim3(NT), smem, st, pool_args(c, p),
                     keep, ws);
