@@ -792,8 +792,8 @@ size_t spec_sample_workspace_bytes(const spec_sample_cfg *cfg, int num_sms);
  *          before them,
  *   and the first one always stays; p = w / sum of w over what stays;
  *   tok = argmax p / e  (lowest index on ties).
- * Borders are decided on masses of 2^-30 relative accuracy in integers (weights
- * below about 2^-43 of the largest, 2^-(62 - ceil(log2 V)), count as nothing
+ * Borders are decided on masses of 2^-29 relative accuracy in integers (weights
+ * below about 2^-42 of the largest, 2^-(61 - ceil(log2 V)), count as nothing
  * there), so that the result does not depend on the order of summation.
  *   logits [R][V] io; e [R][V] float > 0 (NULL: no token is drawn, out->tok and
  *   out->tok_prob are NULL too); of `out` any may be NULL (tok with tok_prob);

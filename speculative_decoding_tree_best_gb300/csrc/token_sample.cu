@@ -6,8 +6,8 @@
 // min-p gives the value directly.  top-k and top-p ask for the shortest prefix with
 // F >= target: F = its length and the count k, or F = the sum of its weights and
 // top_p times that of what top-k left.
-//   Weights are integers, 2^-(62 - lg V) of the largest one, from an exponential
-// of 2^-30 relative accuracy (a table of 2^(-j/64) and a cubic): sums of them are
+//   Weights are integers, 2^-(61 - lg V) of the largest one, from an exponential
+// of 2^-29 relative accuracy (a table of 2^(-j/64) and a cubic): sums of them are
 // exact in 64 bits, so the border depends neither on the order of summation nor
 // on fp32's rounding of long sums.
 //   The draw: argmin e / w over independent exponentials e is token v with
@@ -47,7 +47,7 @@ namespace cg = cooperative_groups;
 
 constexpr int NT = 512;
 constexpr int NBIN = 4096;               // bins of counts
-constexpr int NMASS = NBIN / 2;          // bins of masses (as many bytes)
+constexpr int NMASS = NBIN / 2;          // bins of masses
 constexpr int LIST = 2048;               // tokens that the sorted list holds
 constexpr int ODD = 256;                 // tokens beside the bins that are noted down
 constexpr int SOME = 64;                 // of a CTA, and
@@ -57,8 +57,8 @@ constexpr uint32_t IDX_MAX = (1u << IDX_BITS) - 1;
 constexpr int MAX_CLUSTER = 16;
 constexpr int NO_TOK = 0x7fffffff;
 constexpr float LOWEST = -3.4028234663852886e38f;
-// weights below 2^-CUT of the largest are 0 in the sums
-constexpr float CUT = 43.0f;
+// weights below 2^-CUT of the largest are 0 in the sums (CUT + lg <= 63)
+constexpr float CUT = 42.0f;
 
 typedef unsigned long long u64;
 
@@ -69,9 +69,9 @@ struct SampleArgs {
     spec_sample_out out;
     void* ws;
     int R, V, per;
-    int lg;                  // ceil(log2 V)
+    int lg;                  // ceil(log2 V) + 1: sums of weights are at most 2^61
     int resident;            // 16-byte groups of a CTA's slice kept in shared memory
-    u64 pow2[64];            // 2^(62 - j/64)
+    uint32_t pow2[64];       // 2^(29 - j/64)
 };
 
 // What a selection finds, told to all CTAs.
@@ -109,12 +109,10 @@ struct Params {
 struct Shared {
     union alignas(16) {
         uint32_t count[NBIN];
-        struct {
-            uint32_t lo[NMASS], hi[NMASS];
-        } mass;
+        uint32_t mass[3][NMASS];         // three parts of 15 bits and more
         u64 list[LIST];
     };
-    u64 pow2[64];
+    uint2 pow2[64];
     u64 part[NT / 32];
     u64 cta_sum[MAX_CLUSTER], cta_rest[MAX_CLUSTER];
     u64 near_0, rest;                    // F of what the bins do not hold: see bins()
@@ -155,12 +153,16 @@ __device__ __forceinline__ u64 key_of(float x, int i) {
     return (u64)key_of(x) << IDX_BITS | (IDX_MAX - (uint32_t)i);
 }
 
+// added to a float under 2^22, leaves it rounded to an integer in the low bits
+constexpr float MAGIC = 12582912.0f;
+constexpr int MAGIC_BITS = 0x4b400000;
+
 // The softmax's weights of a row: 2^-((m - x) c), c = log2(e) / temperature in two
 // parts.
 struct Weights {
     float m, c, c_lo, far;       // far: weights beyond it are 0 in the sums
     int lg;
-    const u64* pow2;
+    const uint2* pow2;           // (2^(29 - j/64) - MAGIC_BITS, 2^(29 - j/64) as a float)
 
     // the exponent's (m - x) c and what its rounding leaves
     template <int IO> __device__ __forceinline__ float exponent(float x, float& rest) const {
@@ -174,19 +176,24 @@ struct Weights {
         }
         return y;
     }
-    // as an integer, of 2^(62 - lg) for the largest
+    // as an integer, of 2^(62 - lg) for the largest, rounded down; without branches, so
+    // that several are under way at once.  The exponent's multiple of 1/64 is looked up
+    // (2^(29 - j/64), rounded) and the rest, under 0.0055, is a cubic whose product with
+    // that is rounded by the magic number: 30 bits in all.  (With the 62-bit product
+    // and a rounded shift twice the instructions.)
     template <int IO> __device__ __forceinline__ u64 fixed(float x) const {
-        if (!(fminf(m - x, 3.4028234663852886e38f) <= far)) return 0;
+        const bool some = m - x <= far;
         float rest;
-        const float y = exponent<IO>(x, rest);
-        const float n = fmaf(y, 64.0f, 12582912.0f);           // rounded to an integer
-        const int k = __float_as_int(n) - 0x4b400000;
-        const float r = (fmaf(n - 12582912.0f, -0x1p-6f, y) + rest) * -0.6931471805599453f;
-        const float p = r * fmaf(r, fmaf(r, 1.0f / 6.0f, 0.5f), 1.0f);      // e^r - 1, |r| < 0.0055
-        const u64 t = pow2[k & 63];
-        const u64 w = t + (((int64_t)__float2int_rn(p * 0x1p38f) * (int32_t)(t >> 32)) >> 6);
-        const int s = (k >> 6) + lg;
-        return (w + ((1ull << s) >> 1)) >> s;
+        const float y = exponent<IO>(some ? x : m, rest);
+        const float n = fmaf(y, 64.0f, MAGIC);                 // rounded to an integer
+        const float r = fmaf(n - MAGIC, -0x1p-6f, y) + rest;
+        // 2^-r - 1
+        const float q = r * fmaf(r, fmaf(r, -0.05550410866482158f, 0.2402265069591007f),
+                                 -0.6931471805599453f);
+        const uint2 t = pow2[__float_as_int(n) & 63];
+        const uint32_t w = t.x + (uint32_t)__float_as_int(fmaf(q, __uint_as_float(t.y), MAGIC));
+        const int s = (__float_as_int(n) >> 6) + (lg - (MAGIC_BITS >> 6));
+        return some ? (u64)w << 33 >> s : 0;
     }
     // as a float (1 for the largest)
     template <int IO> __device__ __forceinline__ float value(float x) const {
@@ -383,11 +390,13 @@ template <int KIND> __device__ __forceinline__ int bin_of(int top, float x) {
     return KIND == MASSES ? d >> 1 : d;
 }
 
-// Adds to bin `b` of masses, in two words: 64-bit atomics on shared memory are loops.
+// Adds to bin `b` of masses, in three parts of the weight (at most 2^62 / V), each of
+// which so many tokens cannot overflow: 64-bit atomics on shared memory are loops (24
+// fp32 rows XX us), and with two parts and a carry the first has to be waited for.
 __device__ __forceinline__ void add_mass(Shared& sh, int b, u64 w) {
-    const uint32_t lo = (uint32_t)w, old = atomicAdd(&sh.mass.lo[b], lo);
-    const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old);
-    if (hi) atomicAdd(&sh.mass.hi[b], hi);
+    atomicAdd(&sh.mass[0][b], (uint32_t)w & 0x7fffu);
+    atomicAdd(&sh.mass[1][b], (uint32_t)(w >> 15) & 0x7fffu);
+    if (w >> 30) atomicAdd(&sh.mass[2][b], (uint32_t)(w >> 30));
 }
 
 // This CTA's histogram of `kept`, bin 0 the maximum's (`top` its step).  Beside it
@@ -396,7 +405,7 @@ __device__ __forceinline__ void add_mass(Shared& sh, int b, u64 w) {
 template <int KIND, int IO, int C>
 __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& kept, int top) {
     Shared& sh = k.sh;
-    for (int b = k.tid; b < NBIN; b += NT) sh.count[b] = 0;
+    for (int b = k.tid; b < 3 * NMASS; b += NT) sh.mass[0][b] = 0;
     if (k.tid == 0) {
         sh.near_0 = sh.rest = 0;
         sh.odd_ones = 0;
@@ -425,6 +434,10 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
                 if (in && b < END) atomicAdd(&sh.count[b], 1u);
             }
         } else {
+            u64 w[VEC];
+            if (KIND == MASSES)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) w[v] = k.wt.template fixed<IO>(x[v]);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const int b = bin_of<KIND>(top, x[v]);
@@ -432,7 +445,7 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
                 odd |= in && beside(b);
                 if (!in || b >= END) continue;
                 if (KIND != MASSES) atomicAdd(&sh.count[b], 1u);
-                else if (m - x[v] <= far) add_mass(sh, b, k.wt.template fixed<IO>(x[v]));
+                else if (w[v]) add_mass(sh, b, w[v]);
             }
         }
         if (odd)
@@ -482,26 +495,26 @@ __device__ __forceinline__ void border_bin(Ctx<C>& k, u64 want, int top) {
     u64 f[RUN], s = 0;
 #pragma unroll
     for (int j = 0; j < RUN; j += 4) {
-        uint4 x[C], y[C];
-        const uint4 none = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            x[c] = y[c] = none;
-            if (!mine) continue;
-            const uint32_t* src = k.cl.map_shared_rank(&sh.count[from + j], (k.rank + c) % C);
-            x[c] = *reinterpret_cast<const uint4*>(src);
-            if (KIND == MASSES) y[c] = *reinterpret_cast<const uint4*>(src + NMASS);
-        }
-        n[j] = n[j + 1] = n[j + 2] = n[j + 3] = 0;
         f[j] = f[j + 1] = f[j + 2] = f[j + 3] = 0;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const uint32_t lo[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-            const uint32_t hi[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+        for (int part = 0; part < (KIND == MASSES ? 3 : 1); ++part) {
+            uint4 x[C];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (KIND == MASSES) f[j + i] += (u64)hi[i] << 32 | lo[i];
-                else n[j + i] += lo[i];
+            for (int c = 0; c < C; ++c) {
+                x[c] = make_uint4(0, 0, 0, 0);
+                if (mine)
+                    x[c] = *reinterpret_cast<const uint4*>(k.cl.map_shared_rank(
+                        &sh.mass[0][part * NMASS + from + j], (k.rank + c) % C));
+            }
+            n[j] = n[j + 1] = n[j + 2] = n[j + 3] = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (KIND == MASSES) f[j + i] += (u64)y[i] << (15 * part);
+                    else n[j + i] += y[i];
+                }
             }
         }
     }
@@ -545,7 +558,7 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
     u64 lo = (u64)key_of(kept.v) << IDX_BITS, hi = (u64)key_of(k.wt.m) << IDX_BITS | IDX_MAX;
     u64 above = 0, target = want;
     for (int pass = 0;; ++pass) {
-        for (int b = tid; b < NBIN; b += NT) sh.count[b] = 0;
+        for (int b = tid; b < 3 * NMASS; b += NT) sh.mass[0][b] = 0;
         __syncthreads();
         const u64 span = hi - lo;
         const int shift = max(0, 64 - __clzll((long long)span) - 11);     // span >> shift < NMASS
@@ -569,9 +582,11 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
             if (tid * RUN < PART) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    // (mass.lo lies where count does)
-                    f[j] += *k.cl.map_shared_rank(&sh.count[from + j], c);
-                    if (MASS) f[j] += (u64)*k.cl.map_shared_rank(&sh.mass.hi[from + j], c) << 32;
+                    // (the counts lie where the first part does)
+#pragma unroll
+                    for (int part = 0; part < (MASS ? 3 : 1); ++part)
+                        f[j] += (u64)*k.cl.map_shared_rank(&sh.mass[part][from + j], c)
+                                << (15 * part);
                 }
             }
             s += f[j];
@@ -738,18 +753,28 @@ template <int N, typename P> __device__ __forceinline__ void ranked(const float*
     if (part == 0) f(above, x);
 }
 
-// The logits x of the CTA's slice with f(x, i) into its part of the first CTA's list,
-// of LIST / C keys.
+// The logits x of the CTA's slice with f(x, i), all of them `least` or more, into its
+// part of the first CTA's list, of LIST / C keys.
 template <int IO, int C, typename P>
-__device__ __forceinline__ void gather(Ctx<C>& k, const Row<IO>& row, bool any, P&& f) {
+__device__ __forceinline__ void gather(Ctx<C>& k, const Row<IO>& row, bool any, float least,
+                                       P&& f) {
     Shared& sh = k.sh;
     if (any)
-        row.each([&](float x, int i) {
-            if (!f(x, i)) return;
-            const uint32_t at = atomicAdd(&sh.my_listed, 1u);
-            if (at < LIST / C)
-                *k.cl.map_shared_rank(&sh.list[k.rank * (LIST / C) + at], 0) = key_of(x, i);
-        });
+        for (int g = row.lo + k.tid; g < row.hi; g += NT) {
+            const uint4 u = row.get(g);
+            if (!(Row<IO>::most(u) >= least)) continue;
+            float x[Row<IO>::VEC];
+            Row<IO>::unpack(u, x);
+            const int i = row.index(g);
+#pragma unroll
+            for (int v = 0; v < Row<IO>::VEC; ++v) {
+                if (!f(x[v], i + v)) continue;
+                const uint32_t at = atomicAdd(&sh.my_listed, 1u);
+                if (at < LIST / C)
+                    *k.cl.map_shared_rank(&sh.list[k.rank * (LIST / C) + at], 0) =
+                        key_of(x[v], i + v);
+            }
+        }
     __syncthreads();
     if (k.tid == 0) {
         *k.cl.map_shared_rank(&sh.listed[k.rank], 0) = sh.my_listed;
@@ -860,7 +885,7 @@ template <int IO, int C>
 __device__ __forceinline__ bool short_list(Ctx<C>& k, const Row<IO>& row, Kept& kept,
                                            float thread_max, float cut, const float* e, u64& sum,
                                            Cand& best) {
-    gather<IO>(k, row, thread_max >= cut, [&](float x, int) { return x >= cut; });
+    gather<IO>(k, row, thread_max >= cut, cut, [&](float x, int) { return x >= cut; });
     if (k.rank == 0)
         solve_list<IO>(k, row, k.sh.prm.top_k, k.sh.prm.top_p, 0, 0, e, best);
     k.cl.sync();
@@ -894,7 +919,7 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
             else kept = Kept{v, kept.v == v ? kept.last : (int)IDX_MAX};
             return;
         }
-        gather<IO>(k, row, true, [&](float x, int i) {
+        gather<IO>(k, row, true, kept.v, [&](float x, int i) {
             return bin_of<KIND>(top, x) == bin && kept.has(x, i);
         });
         Cand none;
@@ -922,7 +947,6 @@ template <int IO, int C>
 __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const Kept& kept,
                                      const float* e, Cand& best) {
     constexpr int VEC = Row<IO>::VEC;
-    constexpr float MAGIC = 12582912.0f;                 // 1.5 2^23: integers in the low bits
     const float m = k.wt.m, c = k.wt.c, c7 = fminf(c * 128.0f, 3.0e38f);
     const int V = (int)(row.r1 - row.r0);
     const bool by_value = kept.by_value();
@@ -953,7 +977,7 @@ __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const 
             look = false;
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
-                look |= x[v] >= kept.v && (__float_as_int(ex[v]) >> 16) + 0x4b400000 <=
+                look |= x[v] >= kept.v && (__float_as_int(ex[v]) >> 16) + MAGIC_BITS <=
                                               __float_as_int(fmaf(x[v] - m, c7, bar));
         }
         if (!__any_sync(0xffffffffu, look)) continue;
@@ -1009,7 +1033,8 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     const int lane = tid % 32, warp = tid / 32;
     const int r = blockIdx.x / C, V = a.V;
     if (tid == 0) sh.my_listed = 0;
-    if (tid < 64) sh.pow2[tid] = a.pow2[tid];
+    if (tid < 64)
+        sh.pow2[tid] = make_uint2(a.pow2[tid] - MAGIC_BITS, __float_as_uint((float)a.pow2[tid]));
     Row<IO> row;
     row.logits = static_cast<const T*>(a.logits);
     row.r0 = (int64_t)r * V;
@@ -1269,9 +1294,9 @@ cudaError_t launch_token_sample(const spec_sample_cfg& c, const void* logits,
                                 const spec_sample_params& p, const float* e,
                                 const spec_sample_out& out, void* ws, cudaStream_t st) {
     static const struct Pow2 {
-        u64 t[64];
+        uint32_t t[64];
         Pow2() {
-            for (int j = 0; j < 64; ++j) t[j] = (u64)(exp2(-j / 64.0) * 4611686018427387904.0);
+            for (int j = 0; j < 64; ++j) t[j] = (uint32_t)(exp2(29 - j / 64.0) + 0.5);
         }
     } pow2;
     SampleArgs a{};
@@ -1283,7 +1308,7 @@ cudaError_t launch_token_sample(const spec_sample_cfg& c, const void* logits,
     a.R = c.R;
     a.V = c.V;
     a.per = c.per;
-    while ((1 << a.lg) < c.V) ++a.lg;
+    while ((1 << a.lg) < 2 * c.V) ++a.lg;
     for (int j = 0; j < 64; ++j) a.pow2[j] = pow2.t[j];
     return c.io_dtype == SPEC_IO_BF16 ? sample_t<SPEC_IO_BF16>(c, a, st)
                                       : sample_t<SPEC_IO_F32>(c, a, st);

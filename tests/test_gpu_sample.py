@@ -1,9 +1,9 @@
 """Filtered sampling against the definition in 64 bits.
 
 What stays compares exactly where the nearest border of top_p is further than
-2^-26 of the mass from top_p: weights are integers of 2^-44 of the largest (for
+2^-26 of the mass from top_p: weights are integers of 2^-43 of the largest (for
 V <= 2^18) from an exponential within 2^-29, so a sum of n of them is within
-2^-29 + n 2^-45 of itself.  Probabilities: the exponent is taken in two parts, 2^-22
+2^-29 + n 2^-44 of itself.  Probabilities: the exponent is taken in two parts, 2^-22
 of the exponential, a division and a few roundings of 2^-24: within 2^-20.  Tokens
 compare exactly where no other score comes within 2^-16 of the best."""
 import math
