@@ -108,7 +108,7 @@ struct Params {
 
 struct Shared {
     union alignas(16) {
-        uint32_t count[NBIN];
+        uint32_t count[NBIN + 32];       // the last ones take what belongs nowhere
         uint32_t mass[3][NMASS];         // three parts of 15 bits and more
         u64 list[LIST];
     };
@@ -207,21 +207,42 @@ struct Weights {
 template <int IO> struct Row {
     using T = typename io_t<IO>::T;
     static constexpr int VEC = 16 / sizeof(T);
-    const T* logits;
-    int64_t r0, r1, end;         // the row's elements, the tensor's end
-    int64_t g0;                  // first 16-byte group with one of them
-    int lo, hi;                  // this CTA's groups, from g0
+    const T* logits;             // the row's first element, which may stand inside a
+    const uint4* first;          // 16-byte group: the group
+    int V, off;                  // and its place there
+    int whole_lo, whole_n;       // groups of the row's elements only: [whole_lo, + whole_n)
+    int64_t r0;                  // the row's first element in the tensor
+    int lo, hi;                  // this CTA's groups, from `first`
     const uint4* smem;
     int resident;
 
+    __device__ __forceinline__ Row(const T* tensor, int row, int vocab) : V(vocab) {
+        r0 = (int64_t)row * vocab;
+        logits = tensor + r0;
+        off = (int)(r0 % VEC);
+        first = reinterpret_cast<const uint4*>(logits - off);
+        whole_lo = off != 0;
+        whole_n = (off + V) / VEC - whole_lo;
+    }
+    __device__ __forceinline__ int groups() const { return (off + V + VEC - 1) / VEC; }
+    __device__ __forceinline__ bool whole(int g) const {
+        return (unsigned)(g - whole_lo) < (unsigned)whole_n;
+    }
+    // where in the row the group begins
+    __device__ __forceinline__ int index(int g) const { return g * VEC - off; }
     // group g from memory, with what is not the row's as -inf
     __device__ __forceinline__ uint4 load(int g) const {
-        const int64_t e0 = (g0 + g) * VEC;
+        if (whole(g)) return first[g];
+        return load_edge(g);
+    }
+    __device__ __noinline__ uint4 load_edge(int g) const {
         const T low = IO == SPEC_IO_F32 ? (T)-INFINITY : (T)__uint_as_float(0xff800000u);
-        if (e0 >= r0 && e0 + VEC <= r1) return reinterpret_cast<const uint4*>(logits)[g0 + g];
         alignas(16) T x[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) x[v] = e0 + v >= r0 && e0 + v < r1 ? logits[e0 + v] : low;
+        for (int v = 0; v < VEC; ++v) {
+            const int i = index(g) + v;
+            x[v] = i >= 0 && i < V ? logits[i] : low;
+        }
         return *reinterpret_cast<const uint4*>(x);
     }
     __device__ __forceinline__ uint4 get(int g) const {
@@ -249,15 +270,6 @@ template <int IO> struct Row {
             const float2 y = __bfloat1622float2(
                 __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
             return max_nan(y.x, y.y);
-        }
-    }
-    __device__ __forceinline__ int index(int g) const { return (int)((g0 + g) * VEC - r0); }
-    // f(the group's elements, index of the first in the row) for this thread's groups
-    template <typename F> __device__ __forceinline__ void groups(F&& f) const {
-        for (int g = lo + threadIdx.x; g < hi; g += NT) {
-            float x[VEC];
-            unpack(get(g), x);
-            f(x, index(g));
         }
     }
     // f(x, index in the row) for the elements of groups [from, to), `step` apart (-inf
@@ -305,7 +317,7 @@ struct Kept {
     float v;
     int last;
     __device__ __forceinline__ bool has(float x, int i) const {
-        return x > v || (x == v && i <= last);
+        return (x > v) | ((x == v) & (i <= last));       // without branches
     }
     // whether x alone says: all of the logits at v stay
     __device__ __forceinline__ bool by_value() const { return last == (int)IDX_MAX; }
@@ -320,6 +332,40 @@ __device__ __forceinline__ Kept above_value(float v) {
     return Kept{value_of((u64)(key_of(v) + 1) << IDX_BITS), (int)IDX_MAX};
 }
 __device__ __forceinline__ int index_of(u64 key) { return IDX_MAX - ((uint32_t)key & IDX_MAX); }
+
+// A group with -inf for what does not stay.  Two bf16 values at a time where the value
+// alone says; the least bf16 value that stays is rounded up.
+template <int IO> struct Filter {
+    Kept kept;
+    uint32_t v2;
+    __device__ __forceinline__ Filter(const Kept& k) : kept(k), v2(0) {
+        if (IO == SPEC_IO_BF16) {
+            const __nv_bfloat162 h = __bfloat162bfloat162(__float2bfloat16_ru(k.v));
+            v2 = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    __device__ __forceinline__ uint32_t two(uint32_t w, int i) const {
+        uint32_t mask;
+        if (kept.by_value()) {
+            mask = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w),
+                               *reinterpret_cast<const __nv_bfloat162*>(&v2));
+        } else {
+            mask = (kept.has(__uint_as_float(w << 16), i) ? 0xffffu : 0u) |
+                   (kept.has(__uint_as_float(w & 0xffff0000u), i + 1) ? 0xffff0000u : 0u);
+        }
+        return (w & mask) | (0xff80ff80u & ~mask);
+    }
+    __device__ __forceinline__ uint32_t one(uint32_t w, int i) const {
+        return kept.has(__uint_as_float(w), i) ? w : 0xff800000u;
+    }
+    // u: the group, i: the index of its first
+    __device__ __forceinline__ uint4 operator()(const uint4& u, int i) const {
+        if constexpr (IO == SPEC_IO_BF16)
+            return make_uint4(two(u.x, i), two(u.y, i + 2), two(u.z, i + 4), two(u.w, i + 6));
+        else
+            return make_uint4(one(u.x, i), one(u.y, i + 1), one(u.z, i + 2), one(u.w, i + 3));
+    }
+};
 
 template <int C> struct Ctx {
     cg::cluster_group& cl;
@@ -396,7 +442,7 @@ template <int KIND> __device__ __forceinline__ int bin_of(int top, float x) {
 __device__ __forceinline__ void add_mass(Shared& sh, int b, u64 w) {
     atomicAdd(&sh.mass[0][b], (uint32_t)w & 0x7fffu);
     atomicAdd(&sh.mass[1][b], (uint32_t)(w >> 15) & 0x7fffu);
-    if (w >> 30) atomicAdd(&sh.mass[2][b], (uint32_t)(w >> 30));
+    atomicAdd(&sh.mass[2][b], (uint32_t)(w >> 30));
 }
 
 // This CTA's histogram of `kept`, bin 0 the maximum's (`top` its step).  Beside it
@@ -416,43 +462,40 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
     // Odd ones, seldom there, are noted down for later: below the bins, or near 0
     // (where a bin holds more than one value).  Taken as they came, they made the pass
     // twice as long: the block waits for the warp with most of them.
-    auto beside = [&](int b) { return b >= END || (KIND == VALUES && b == top); };
-    auto note = [&](float x) {
-        if (KIND != COUNTS && !(m - x <= far)) return;   // weighs nothing
-        const uint32_t at = atomicAdd(&sh.odd_ones, 1u);
-        if (at < ODD) sh.odd[at] = x;
-    };
-    row.groups([&](const float (&x)[VEC], int i) {
+    // (conditions of a token are joined without branches)
+    auto beside = [&](int b) { return (b >= END) | (KIND == VALUES ? b == top : false); };
+    // What does not stay is -inf, and below the bins; where what stays reaches there too
+    // (deep), those found there are told apart later.
+    const bool deep = bin_of<KIND>(top, kept.v) >= END;
+    const Filter<IO> filter(kept);
+    const int trash = (KIND == MASSES ? 0 : NBIN) + k.tid % 32;     // (nothing added to masses)
+    for (int g = row.lo + k.tid; g < row.hi; g += NT) {
+        const uint4 u = filter(row.get(g), row.index(g));
+        float x[VEC];
+        Row<IO>::unpack(u, x);
         bool odd = false;
-        if (KIND != MASSES && kept.by_value()) {
-            // (what weighs nothing is counted, and weighs nothing)
+        u64 w[VEC];
+        if (KIND == MASSES)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const int b = bin_of<KIND>(top, x[v]);
-                const bool in = x[v] >= kept.v;
-                odd |= in && beside(b);
-                if (in && b < END) atomicAdd(&sh.count[b], 1u);
-            }
-        } else {
-            u64 w[VEC];
-            if (KIND == MASSES)
+            for (int v = 0; v < VEC; ++v) w[v] = k.wt.template fixed<IO>(x[v]);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) w[v] = k.wt.template fixed<IO>(x[v]);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const int b = bin_of<KIND>(top, x[v]);
-                const bool in = kept.has(x[v], i + v);
-                odd |= in && beside(b);
-                if (!in || b >= END) continue;
-                if (KIND != MASSES) atomicAdd(&sh.count[b], 1u);
-                else if (w[v]) add_mass(sh, b, w[v]);
-            }
+        for (int v = 0; v < VEC; ++v) {
+            const int b = bin_of<KIND>(top, x[v]);
+            odd |= KIND == VALUES ? b == top : false;
+            if (deep) odd |= b >= END;
+            // (a branch for each token costs more than an addition for nothing)
+            if (KIND == MASSES) add_mass(sh, b < END ? b : trash, b < END ? w[v] : 0);
+            else atomicAdd(&sh.count[b < END ? b : trash], 1u);
         }
         if (odd)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (beside(bin_of<KIND>(top, x[v])) && kept.has(x[v], i + v)) note(x[v]);
-    });
+            for (int v = 0; v < VEC; ++v) {
+                if (!(x[v] > -INFINITY) || !beside(bin_of<KIND>(top, x[v]))) continue;
+                if (KIND != COUNTS && !(m - x[v] <= far)) continue;      // weighs nothing
+                const uint32_t at = atomicAdd(&sh.odd_ones, 1u);
+                if (at < ODD) sh.odd[at] = x[v];
+            }
+    }
     u64 near = 0, rest = 0;
     auto look = [&](float x) {
         if (KIND == COUNTS) ++rest;
@@ -747,7 +790,7 @@ template <int N, typename P> __device__ __forceinline__ void ranked(const float*
     const float x = v[at];
     int above = 0;
 #pragma unroll
-    for (int i = part; i < N; i += PER) above += v[i] > x || (v[i] == x && i < at);
+    for (int i = part; i < N; i += PER) above += (v[i] > x) | ((v[i] == x) & (i < at));
 #pragma unroll
     for (int o = 1; o < PER; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
     if (part == 0) f(above, x);
@@ -859,7 +902,7 @@ __device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int li
         if (j >= run || at >= limit) continue;
         x[j] = value_of(list[at]);
         i[j] = index_of(list[at]);
-        if (e) ex[j] = e[row.r0 + i[j]];
+        if (e) ex[j] = e[i[j]];
         w[j] = k.wt.template fixed<IO>(x[j]);
         s += w[j];
     }
@@ -904,10 +947,13 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
     constexpr int KIND = !MASS ? COUNTS : (IO == SPEC_IO_BF16 ? VALUES : MASSES);
     Shared& sh = k.sh;
     const int top = step_of(k.wt.m);
-    bins<KIND, IO>(k, row, kept, top);
-    border_bin<KIND, IO>(k, want, top);
-    Border b = sh.border;
-    if (b.state == NOT_FOUND) return;
+    Border b{0, 0, 0, 0, BELOW};
+    if (top + FARTHEST >= NBIN) {                        // -inf is below the bins
+        bins<KIND, IO>(k, row, kept, top);
+        border_bin<KIND, IO>(k, want, top);
+        b = sh.border;
+        if (b.state == NOT_FOUND) return;
+    }
     if (b.state == NARROWED) {
         const int bin = (int)b.from, s = top - bin;
         if (IO == SPEC_IO_BF16 && s != 0) {              // one value
@@ -948,54 +994,69 @@ __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const 
                                      const float* e, Cand& best) {
     constexpr int VEC = Row<IO>::VEC;
     const float m = k.wt.m, c = k.wt.c, c7 = fminf(c * 128.0f, 3.0e38f);
-    const int V = (int)(row.r1 - row.r0);
-    const bool by_value = kept.by_value();
+    const Filter<IO> filter(kept);
     float bar = 3.0e38f;                                 // everything passes
-    for (int g = row.lo + k.tid - k.tid % 32; g < row.hi; g += NT) {     // the same for the warp
-        const int at = g + k.tid % 32;
+    // two units above, for the roundings of the test
+    auto raise_bar = [&]() {
+        bar = (best.w > 0.0f) & (best.e > 0.0f)
+                  ? (__log2f(best.e) - __log2f(best.w) + 127.0f) * 128.0f + 2.0f + MAGIC : 3.0e38f;
+    };
+    bool shared_best = false;
+    for (int g = row.lo + k.tid - k.tid % 32;; g += NT) {              // the same for the warp
+        const int at = g + k.tid % 32, i = row.index(at);
         bool look = false;
         uint4 u;
         float ex[VEC];
-        const int i = row.index(at);
         if (at < row.hi) {
             u = row.get(at);
             look = Row<IO>::most(u) >= kept.v;
         }
         if (look) {
-            const float* src = e + (row.g0 + at) * VEC;
-            if (i >= 0 && i + VEC <= V) {
+            u = filter(u, i);
+            if (row.whole(at)) {
 #pragma unroll
                 for (int v = 0; v < VEC; v += 4)
                     *reinterpret_cast<float4*>(&ex[v]) =
-                        __ldg(reinterpret_cast<const float4*>(src + v));
+                        __ldg(reinterpret_cast<const float4*>(e + i + v));
             } else {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) ex[v] = i + v >= 0 && i + v < V ? src[v] : 1.0f;
+                for (int v = 0; v < VEC; ++v) ex[v] = i + v >= 0 && i + v < row.V ? e[i + v] : 1.0f;
             }
             float x[VEC];
             Row<IO>::unpack(u, x);
             look = false;
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
-                look |= x[v] >= kept.v && (__float_as_int(ex[v]) >> 16) + MAGIC_BITS <=
-                                              __float_as_int(fmaf(x[v] - m, c7, bar));
+                look |= (__float_as_int(ex[v]) >> 16) + MAGIC_BITS <=
+                        __float_as_int(fmaf(x[v] - m, c7, bar));
         }
-        if (!__any_sync(0xffffffffu, look)) continue;
-        if (look) {
-            float x[VEC];
-            Row<IO>::unpack(u, x);
+        if (__any_sync(0xffffffffu, look)) {
+            if (look) {
+                float x[VEC];
+                Row<IO>::unpack(u, x);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                if (!(by_value ? x[v] >= kept.v : kept.has(x[v], i + v))) continue;
-                const float w = ex2((x[v] - m) * c);
-                take(best, Cand{w, ex[v], x[v], i + v});
+                for (int v = 0; v < VEC; ++v) {
+                    if (!(x[v] > -INFINITY)) continue;
+                    take(best, Cand{ex2((x[v] - m) * c), ex[v], x[v], i + v});
+                }
             }
-        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) take_across(best, o);
-        // two units above, for the roundings of the test
-        bar = best.w > 0.0f && best.e > 0.0f
-                  ? (__log2f(best.e) - __log2f(best.w) + 127.0f) * 128.0f + 2.0f + MAGIC : 3.0e38f;
+            for (int o = 16; o > 0; o >>= 1) take_across(best, o);
+            raise_bar();
+        }
+        if (!shared_best) {
+            // the warps go on from the best of their first groups
+            shared_best = true;
+            if (k.tid % 32 == 0) k.sh.warp_cand[k.tid / 32] = best;
+            __syncthreads();
+            const Cand other = k.sh.warp_cand[k.tid % (NT / 32)];
+            take(best, other);
+#pragma unroll
+            for (int o = NT / 64; o > 0; o >>= 1) take_across(best, o);
+            raise_bar();
+            __syncthreads();                             // (warp_cand is written again later)
+        }
+        if (g + NT >= row.hi) break;
     }
 }
 
@@ -1035,12 +1096,8 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     if (tid == 0) sh.my_listed = 0;
     if (tid < 64)
         sh.pow2[tid] = make_uint2(a.pow2[tid] - MAGIC_BITS, __float_as_uint((float)a.pow2[tid]));
-    Row<IO> row;
-    row.logits = static_cast<const T*>(a.logits);
-    row.r0 = (int64_t)r * V;
-    row.r1 = row.r0 + V;
-    row.g0 = row.r0 / VEC;
-    const int groups = (int)((row.r1 + VEC - 1) / VEC - row.g0), share = (groups + C - 1) / C;
+    Row<IO> row(static_cast<const T*>(a.logits), r, V);
+    const int groups = row.groups(), share = (groups + C - 1) / C;
     row.lo = min(groups, rank * share);
     row.hi = min(groups, row.lo + share);
     row.smem = slice;
@@ -1125,9 +1182,9 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     const Weights& wt = k.wt;
 
     // ---- the border
-    const float* e = a.e;
-    float* prob = a.out.prob;
-    T* out = static_cast<T*>(a.out.logits);
+    const float* e = a.e ? a.e + row.r0 : nullptr;
+    float* prob = a.out.prob ? a.out.prob + row.r0 : nullptr;
+    T* out = a.out.logits ? static_cast<T*>(a.out.logits) + row.r0 : nullptr;
     Kept kept{prm.low, (int)IDX_MAX};
     u64 sum = 0;
     bool summed = false, drawn = false;
@@ -1145,94 +1202,88 @@ sample_rows(const __grid_constant__ SampleArgs a) {
                 summed = true;
             }
         }
-        if (!summed && prob) {
-            row.each([&](float x, int i) {
-                if (kept.has(x, i)) sum += wt.template fixed<IO>(x);
-            });
-            u64 all, before, rest;
-            block_prefix(sum, sh.part, all);
-            k.totals(all, before, sum, 0, rest);
-            summed = true;
-        }
     }
 
     // ---- what stays: the draw and the outputs (other CTAs' memory is written up to the
     // next barrier, where there is one, and not read)
-    auto inverse = [&](u64 s) {
-        return s == 0 ? 0.0f : 1.0f / (__ull2float_rn(s) * (1.0f / (float)(1ull << (62 - a.lg))));
-    };
-    float inv = inverse(sum);
-    const bool race = e && !drawn && !bad, tally = !summed && a.out.tok_prob && !bad;
+    const Filter<IO> filter(kept);
+    // probabilities are w / z.  Where a border was found by mass, z is its sum; else it
+    // only scales, and is summed up in fp32.
+    float z = __ull2float_rn(sum) * (1.0f / (float)(1ull << (62 - a.lg)));
+    if (!summed && !bad && (prob || a.out.tok_prob)) {
+        z = 0.0f;
+        for (int g = row.lo + tid; g < row.hi; g += NT) {
+            float x[VEC];
+            Row<IO>::unpack(filter(row.get(g), row.index(g)), x);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                z += x[v] > -INFINITY ? ex2((x[v] - m) * wt.c) : 0.0f;
+        }
+        z = warp_sum(z);
+        __syncthreads();
+        if (lane == 0) sh.warp_max[warp] = z;
+        __syncthreads();
+        z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) z += sh.warp_max[w];
+        if (tid < C) *cl.map_shared_rank(&sh.cta_max[rank], tid) = make_float2(z, 0.0f);
+        cl.sync();
+        z = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) z += sh.cta_max[c].x;
+    }
+    const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+    const bool race = e && !drawn && !bad;
     if (race) draw(k, row, kept, e, best);
-    if (tally)
-        row.each([&](float x, int i) {
-            if (kept.has(x, i)) sum += wt.template fixed<IO>(x);
-        });
     if (prob || out)
         for (int g = row.lo + tid; g < row.hi; g += NT) {
-            const uint4 u = row.get(g);
-            const int64_t e0 = (row.g0 + g) * VEC;
             const int i = row.index(g);
-            const bool whole = i >= 0 && i + VEC <= V;
-            const bool any = Row<IO>::most(u) >= kept.v;          // (never in a bad row)
-            float x[VEC];
-            Row<IO>::unpack(u, x);
+            const bool whole = row.whole(g);
+            uint4 u = row.get(g);
+            if (!bad) u = filter(u, i);
+            if (out) {
+                if (whole) {
+                    *reinterpret_cast<uint4*>(out + i) = u;
+                } else {
+                    alignas(16) T y[VEC];
+                    *reinterpret_cast<uint4*>(y) = u;
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v)
+                        if (i + v >= 0 && i + v < V) out[i + v] = y[v];
+                }
+            }
             if (prob) {
-                float w[VEC];
+                float x[VEC], w[VEC];
+                Row<IO>::unpack(u, x);
+                const bool any = Row<IO>::most(u) >= kept.v;     // (never in a bad row)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) w[v] = 0.0f;
                 if (any) {
 #pragma unroll
                     for (int v = 0; v < VEC; ++v)
-                        if (kept.has(x[v], i + v)) w[v] = wt.template value<IO>(x[v]) * inv;
+                        w[v] = x[v] > -INFINITY ? wt.template value<IO>(x[v]) * inv : 0.0f;
                 }
                 if (whole) {
 #pragma unroll
                     for (int v = 0; v < VEC; v += 4)
-                        *reinterpret_cast<float4*>(prob + e0 + v) =
+                        *reinterpret_cast<float4*>(prob + i + v) =
                             make_float4(w[v], w[v + 1], w[v + 2], w[v + 3]);
                 } else {
 #pragma unroll
                     for (int v = 0; v < VEC; ++v)
-                        if (i + v >= 0 && i + v < V) prob[e0 + v] = w[v];
-                }
-            }
-            if (out) {
-                alignas(16) T y[VEC];
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    y[v] = (T)(bad || (any && kept.has(x[v], i + v)) ? x[v] : -INFINITY);
-                if (whole) {
-                    reinterpret_cast<uint4*>(out)[row.g0 + g] = *reinterpret_cast<const uint4*>(y);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v)
-                        if (i + v >= 0 && i + v < V) out[e0 + v] = y[v];
+                        if (i + v >= 0 && i + v < V) prob[i + v] = w[v];
                 }
             }
         }
     if (!e || (drawn && rank != 0)) return;
     block_best(best, sh);
-    if (tally) {
-        u64 all;
-        block_prefix(sum, sh.part, all);
-        sum = all;
-    }
     if (!drawn) {
-        if (tid == 0) {
-            *cl.map_shared_rank(&sh.cand[rank], 0) = best;
-            if (tally) *cl.map_shared_rank(&sh.cta_sum[rank], 0) = sum;
-        }
+        if (tid == 0) *cl.map_shared_rank(&sh.cand[rank], 0) = best;
         cl.sync();
     }
     if (rank == 0 && tid == 0) {
         if (!drawn)
             for (int c = 0; c < C; ++c) take(best, sh.cand[c]);
-        if (tally) {
-            sum = 0;
-            for (int c = 0; c < C; ++c) sum += sh.cta_sum[c];
-            inv = inverse(sum);
-        }
         const bool none = best.i == NO_TOK;
         a.out.tok[r] = none ? 0 : best.i;
         if (a.out.tok_prob) a.out.tok_prob[r] = none ? 0.0f : wt.template value<IO>(best.x) * inv;
