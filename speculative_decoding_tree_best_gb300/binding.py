@@ -919,19 +919,43 @@ def rope_cfg(rows, Hq, Hkv, D, rot=None, layout="half", io="bf16", inverse=False
                        _IO[io][0], int(bool(inverse)), q_stride, k_stride, v_stride)
 
 
-def _tokens(t, dtype, tokens, H, D, stride, name, device):
-    """Data pointer of `tokens` (a shape) tokens of [H][D], `stride` elements apart
-    (0: contiguous)."""
-    shape = tokens + (H, D)
-    step = stride or H * D
-    if step == H * D:
-        return _arg(_required(t, name), dtype, shape, name, device)
+class _RopePlan:
+    """What the calls of one rotation need to know: the type, and the shapes and
+    strides of q, k, v and the outputs, for tokens of the given shape."""
+    __slots__ = ("dt", "rows", "q", "k", "v", "q_out", "k_out")
+
+    def __init__(self, cfg, tokens):
+        def side(H, stride):
+            step = stride or H * cfg.D
+            return tokens + (H, cfg.D), (tokens[-1] * step,) * (len(tokens) - 1) + (step, cfg.D, 1)
+        self.dt, self.rows = _io_dtype(cfg), (cfg.rows,)
+        self.q, self.k, self.v = (side(H, s) for H, s in (
+            (cfg.Hq, cfg.q_stride), (cfg.Hkv, cfg.k_stride), (cfg.Hkv, cfg.v_stride)))
+        self.q_out, self.k_out = self.q[0], self.k[0]
+
+
+def _rope_plan(cfg, tokens) -> _RopePlan:
+    key = (bytes(cfg), tokens)
+    p = _plans.get(key)
+    if p is None:
+        if len(_plans) >= 1024:
+            _plans.clear()
+        p = _plans[key] = _RopePlan(cfg, tokens)
+    return p
+
+
+def _tokens(t, dtype, side, name, device):
+    """Data pointer of tokens of [H][D], a stride apart (side: shape, strides)."""
+    shape, want = side
+    try:
+        if (t.dtype is dtype and t.get_device() == device and t.shape == shape
+                and (t.stride() == want
+                     or all(s == w or n == 1 for s, w, n in zip(t.stride(), want, shape)))):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    want = (step, D, 1) if len(tokens) == 1 else (tokens[1] * step, step, D, 1)
-    if (t.dtype is dtype and t.get_device() == device and t.shape == shape
-            and all(s == w or n == 1 for s, w, n in zip(t.stride(), want, shape))):
-        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -944,17 +968,15 @@ def _tokens(t, dtype, tokens, H, D, stride, name, device):
 def rope_apply(cfg: SpecRopeCfg, table: RopeTable, pos, q, k, q_out, k_out, stream=None):
     """Rotary positions of q [rows][Hq][D] and k [rows][Hkv][D] io (k and k_out
     None with Hkv = 0) at pos int32 [rows]; q_out and k_out are contiguous."""
-    dev, dt, rows = _get_device(), _io_dtype(cfg), (cfg.rows,)
-    if cfg.Hkv == 0:
-        k = k_out = None
+    dev, p = _get_device(), _rope_plan(cfg, (cfg.rows,))
+    keys = cfg.Hkv > 0
     rc = (_lib or load()).rope_apply(
         ctypes.byref(cfg), table.ptr(cfg.rot, dev), table.amp,
-        _arg(_required(pos, "pos"), torch.int32, rows, "pos", dev),
-        _tokens(q, dt, rows, cfg.Hq, cfg.D, cfg.q_stride, "q", dev),
-        _tokens(k, dt, rows, cfg.Hkv, cfg.D, cfg.k_stride, "k", dev) if cfg.Hkv else None,
-        _arg(_required(q_out, "q_out"), dt, (cfg.rows, cfg.Hq, cfg.D), "q_out", dev),
-        _arg(_required(k_out, "k_out"), dt, (cfg.rows, cfg.Hkv, cfg.D), "k_out", dev)
-        if cfg.Hkv else None, _raw_stream(stream, dev))
+        _arg(_required(pos, "pos"), torch.int32, p.rows, "pos", dev),
+        _tokens(q, p.dt, p.q, "q", dev), _tokens(k, p.dt, p.k, "k", dev) if keys else None,
+        _arg(_required(q_out, "q_out"), p.dt, p.q_out, "q_out", dev),
+        _arg(_required(k_out, "k_out"), p.dt, p.k_out, "k_out", dev) if keys else None,
+        _raw_stream(stream, dev))
     if rc:
         _check("rope_apply", rc)
 
@@ -964,16 +986,15 @@ def rope_page_append(cfg: SpecRopeCfg, pcfg: SpecPagedCfg, kv: PagedKV, table: R
     """The new tokens' queries and keys rotated at kv_len + i, q [B][T][Hq][D] into
     q_out, the rows of k_new and v_new [B][T][Hkv][D] into the cache's slots
     (int64 [B][T], -1: no row), in one pass."""
-    dev, dt = _get_device(), _io_dtype(pcfg)
-    bt, D, Hkv = (pcfg.B, pcfg.T), pcfg.D, pcfg.Hkv
+    dev, bt = _get_device(), (pcfg.B, pcfg.T)
+    p = _rope_plan(cfg, bt)
     rc = (_lib or load()).rope_page_append(
         ctypes.byref(cfg), ctypes.byref(pcfg), kv.ref(pcfg, bytes(pcfg), dev),
         table.ptr(cfg.rot, dev), table.amp,
         _arg(_required(slots, "slots"), torch.int64, bt, "slots", dev),
-        _tokens(q, dt, bt, pcfg.Hq, D, cfg.q_stride, "q", dev),
-        _tokens(k_new, dt, bt, Hkv, D, cfg.k_stride, "k_new", dev),
-        _tokens(v_new, dt, bt, Hkv, D, cfg.v_stride, "v_new", dev),
-        _arg(_required(q_out, "q_out"), dt, bt + (pcfg.Hq, D), "q_out", dev),
+        _tokens(q, p.dt, p.q, "q", dev), _tokens(k_new, p.dt, p.k, "k_new", dev),
+        _tokens(v_new, p.dt, p.v, "v_new", dev),
+        _arg(_required(q_out, "q_out"), p.dt, p.q_out, "q_out", dev),
         _workspace(ws, _STATUS_BYTES, dev), _raw_stream(stream, dev))
     if rc:
         _check("rope_page_append", rc)

@@ -37,6 +37,8 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "serving.cuh"
 
 namespace spec {
@@ -1162,7 +1164,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     constexpr int EACH = POOL / C < SOME ? POOL / C : SOME;
     const bool pooled = top_k > 0 && top_k <= EACH * C * 3 / 4;
     const bool small_k = pooled || (top_k > 0 && top_k <= min(SMALL_K, C * NT / 2));
-    float cut = 0.0f;
+    float cut = INFINITY;
     if (small_k && !pooled) {
         sh.pool[tid] = thread_max;
         __syncthreads();
@@ -1316,12 +1318,21 @@ cudaError_t launch_c(const spec_sample_cfg& c, SampleArgs& a, int64_t groups, cu
     const int most = 180 * 1024;                         // a slice, with one CTA to an SM
     const int64_t share = (groups + C - 1) / C;
     a.resident = (int)(share * 16 > most ? most / 16 : share);
-    cudaError_t e = cudaFuncSetAttribute(sample_rows<IO, C>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess && C > 8)
-        e = cudaFuncSetAttribute(sample_rows<IO, C>,
-                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    // once per device and kernel
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(sample_rows<IO, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 most);
+        if (e == cudaSuccess && C > 8)
+            e = cudaFuncSetAttribute(sample_rows<IO, C>,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(c.R * C));
     cfg.blockDim = dim3(NT);

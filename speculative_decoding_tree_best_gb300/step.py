@@ -257,6 +257,12 @@ class ChainStep:
     owns the contents of (page_table names the pages of each request; a page
     id is good for every layer's pool).  Rows of refused drafts are written
     over by the next step.
+
+    The page table can be left to the step: begin() takes the pages that the new
+    tokens' rows need from `pool`, attend_rope() rotates and appends by the slots
+    that it found, and release() gives pages back.  A request that got no pages
+    has no request in its slot (n_draft -1) for that step.  draft() draws a
+    drafter's tokens, and verify() can filter the target's logits.
     """
 
     def __init__(self, pcfg: binding.SpecPagedCfg, dcfg: binding.SpecDraftCfg, n_layers: int,
@@ -281,6 +287,38 @@ class ChainStep:
         self.out = binding.DraftBuffers(dcfg, device)
         self.paged_ws = binding.alloc_paged_workspace(pcfg, device)
         self.draft_ws = binding.alloc_draft_workspace(dcfg, device)
+        self.pool = binding.PagePool.empty(pcfg, self.page_table, self.kv_len, device)
+        self.slots = torch.full((pcfg.B, pcfg.T), -1, dtype=torch.int64, device=device)
+        self._keep = torch.empty((pcfg.B,), **i32)
+        self._q = torch.empty((pcfg.B, pcfg.T, pcfg.Hq, pcfg.D), dtype=dt, device=device)
+        self._drafter = self._filtered = None
+
+    def begin(self):
+        """Pages for this step's new tokens (n_draft + 1 each); requests that get
+        none have n_draft -1 afterwards."""
+        torch.add(self.n_draft, 1, out=self._n_new)
+        binding.page_tables_extend(self.pcfg, self.pool, self.slots, self._keep, self.paged_ws,
+                                   n_new=self._n_new)
+        torch.sub(self._keep, 1, out=self.n_draft)
+
+    def attend_rope(self, layer: int, rcfg: binding.SpecRopeCfg, table: binding.RopeTable, q,
+                    k_new, v_new):
+        """attend() of queries and keys that are not rotated yet, after begin()."""
+        torch.add(self.n_draft, 1, out=self._n_new)
+        o, kv = self.attn_o[layer], self.caches[layer]
+        binding.rope_page_append(rcfg, self.pcfg, kv, table, self.slots, q, k_new, v_new, self._q,
+                                 self.paged_ws)
+        binding.attn_decode_paged(self.pcfg, kv, self._q, o, self.paged_ws, n_new=self._n_new)
+        return o
+
+    def release(self, ended=None):
+        """Pages past the committed rows go back to the pool, and all pages of the
+        requests where `ended` (bool [B]) is set."""
+        if ended is None:
+            self._keep.copy_(self.kv_len)
+        else:
+            torch.where(ended, torch.zeros_like(self.kv_len), self.kv_len, out=self._keep)
+        binding.page_tables_trim(self.pcfg, self.pool, self._keep, self.paged_ws)
 
     def attend(self, layer: int, q, k_new, v_new):
         """Append layer `layer`'s rows and attend from them: [B][T][Hq][D]."""
@@ -291,8 +329,39 @@ class ChainStep:
         binding.attn_decode_paged(self.pcfg, kv, q, o, self.paged_ws, n_new=self._n_new)
         return o
 
-    def verify(self, logits, draft_tok, draft_prob, u, e) -> binding.DraftBuffers:
-        """Verify the drafts, advance kv_len and root_tok."""
+    def draft(self, i: int, logits, e, draft_tok, draft_prob, **filters):
+        """Draft i of every request from a drafter's logits io [B][V] and e f32
+        [B][V]: draft_tok [B][N] and draft_prob [B][N][V], as verify() takes them,
+        receive the token and the distribution that it was drawn from.  filters:
+        temperature, top_k, top_p, min_p [B] as token_sample's."""
+        d = self.dcfg
+        key = binding.sample_cfg(d.B, d.V, io="bf16" if d.io_dtype else "f32")
+        if self._drafter is None:
+            self._drafter = (key, binding.SampleBuffers(key, prob=True),
+                             binding.alloc_sample_workspace(key))
+        cfg, out, ws = self._drafter
+        binding.token_sample(cfg, logits, e, out, ws, **filters)
+        draft_tok[:, i].copy_(out.tok)
+        draft_prob[:, i].copy_(out.prob)
+
+    def verify(self, logits, draft_tok, draft_prob, u, e, **filters) -> binding.DraftBuffers:
+        """Verify the drafts, advance kv_len and root_tok.  filters: top_k, top_p,
+        min_p [B] as token_sample's, applied to each of a request's rows at the
+        step's temperature."""
+        if filters:
+            d = self.dcfg
+            if self._filtered is None:
+                cfg = binding.sample_cfg(d.B * (d.N + 1), d.V, per=d.N + 1,
+                                         io="bf16" if d.io_dtype else "f32")
+                dev = self.kv_len.device
+                t = torch.full((d.B,), d.temperature, dtype=torch.float32, device=dev)
+                self._filtered = (cfg, binding.SampleBuffers(cfg, draw=False, logits=True,
+                                                             device=dev),
+                                  binding.alloc_sample_workspace(cfg, dev), t)
+            cfg, out, ws, t = self._filtered
+            binding.token_sample(cfg, logits.view(cfg.R, cfg.V), None, out, ws, temperature=t,
+                                 **filters)
+            logits = out.logits.view(logits.shape)
         binding.draft_verify_sampled(self.dcfg, draft_tok, draft_prob, logits, u, e, self.out,
                                      self.draft_ws, n_draft=self.n_draft, kv_len=self.kv_len,
                                      root_tok=self.root_tok)
@@ -300,5 +369,8 @@ class ChainStep:
 
     def status(self) -> int:
         """SPEC_DEV_* bits of the calls so far."""
-        return (binding.spec_status_read(self.paged_ws)
-                | binding.spec_status_read(self.draft_ws))
+        bits = binding.spec_status_read(self.paged_ws) | binding.spec_status_read(self.draft_ws)
+        for made in (self._drafter, self._filtered):
+            if made is not None:
+                bits |= binding.spec_status_read(made[2])
+        return bits
