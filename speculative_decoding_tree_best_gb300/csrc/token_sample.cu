@@ -14,10 +14,11 @@
 // probability w_v / sum w.
 //
 // The border, by what it takes:
-//   top_k small   Each CTA of C finds a value that k / C of its threads' maxima reach.
-//                 The least of these values is not above the k-th largest logit: the
-//                 logits from there on (few more than k) are gathered in one CTA,
-//                 sorted, and all filters and the draw decided on the sorted list.
+//   top_k small   A lower bound of the k-th largest logit: the k-th of a pool of maxima
+//                 of threads' shares, or (top_k above 3/4 of the pool) the least of the
+//                 values that k / C of each CTA's threads reach.  The logits from there
+//                 on, few more than k, are gathered in one CTA, sorted, and all filters
+//                 and the draw decided on the sorted list.
 //   else          A histogram over bins of 2^-7 of a value's binade, from the maximum
 //                 down, names the bin that the border is in.  bf16 logits take one
 //                 value in a bin: counts are all that masses need, a weight a bin, and
@@ -34,6 +35,15 @@
 // memory (what does not fit is read again from L2), and each pass goes over that
 // copy.  Histograms are added up by parts: each CTA takes a part of the bins from
 // all (reading the others' shared memory), and tells the others its total.
+//
+// What bounds it: reading the logits (2 or 4 bytes a token), the random numbers of what
+// stays, writing what is asked for.  Measured (graph replays, V = 151936): one bf16 row
+// 10.7 us, a chain of six exchanges and a sort; 24 fp32 rows with their probabilities
+// 43 us, most of it the rows with a top_p alone (some 60 instructions a token in their
+// histogram, and only their clusters' SMs at work); 216 bf16 rows filtered and written
+// back 75 us, 131 MB at 1.7 TB/s; 256 bf16 rows' nucleus 146 us.  The last two are bound by instructions (35 a
+// token, at 40 to 50 % of the issue slots: the CTAs of a cluster wait for one another,
+// and 256 rows are 3.4 rounds of the 76 clusters that fit).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -47,6 +57,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// Two CTAs of 512 threads to an SM, 64 registers each.  (256 rows' nucleus, then in 149
+// us: four of 256 threads and clusters twice as large 179, one of 1024 and half as
+// large 160; one row 10.6, 11.7 and 12.8.)
 constexpr int NT = 512;
 constexpr int NBIN = 4096;               // bins of counts
 constexpr int NMASS = NBIN / 2;          // bins of masses
@@ -197,8 +210,8 @@ struct Weights {
     // as an integer, of 2^(62 - lg) for the largest, rounded down; without branches, so
     // that several are under way at once.  The exponent's multiple of 1/64 is looked up
     // (2^(29 - j/64), rounded) and the rest, under 0.0055, is a cubic whose product with
-    // that is rounded by the magic number: 30 bits in all.  (With the 62-bit product
-    // and a rounded shift twice the instructions.)
+    // that is rounded by the magic number: 30 bits in all.  (A 62-bit product and a
+    // rounded shift: 24 fp32 rows 48.5 us instead of 45.3.)
     template <int IO> __device__ __forceinline__ u64 fixed(float x) const {
         const bool some = m - x <= far;
         float rest;
@@ -407,7 +420,11 @@ template <int C> struct Ctx {
             rest += sh.cta_rest[c];
         }
     }
-    __device__ __forceinline__ void tell(const Border& b) {
+    __device__ __forceinline__ void tell(const Border& b, bool all = true) {
+        if (!all) {                                      // this CTA alone
+            sh.border = b;
+            return;
+        }
         const uint4* src = reinterpret_cast<const uint4*>(&b);
         const uint4 lo = src[0], hi = src[1];
 #pragma unroll
@@ -454,9 +471,10 @@ template <int KIND> __device__ __forceinline__ int bin_of(int top, float x) {
     return KIND == MASSES ? d >> 1 : d;
 }
 
-// Adds to bin `b` of masses, in three parts of the weight (at most 2^62 / V), each of
-// which so many tokens cannot overflow: 64-bit atomics on shared memory are loops (24
-// fp32 rows XX us), and with two parts and a carry the first has to be waited for.
+// Adds to bin `b` of masses, in three parts of the weight (at most 2^61 / V): the first
+// two of 15 bits, so that a CTA's 2^16 tokens do not overflow them, nor V tokens the
+// third.  (64-bit atomics on shared memory are loops: 6 to 28 times as long as 32-bit
+// ones, 1000 a thread of two CTAs an SM in 300 to 1380 us instead of 49.)
 __device__ __forceinline__ void add_mass(Shared& sh, int b, u64 w) {
     atomicAdd(&sh.mass[0][b], (uint32_t)w & 0x7fffu);
     atomicAdd(&sh.mass[1][b], (uint32_t)(w >> 15) & 0x7fffu);
@@ -815,9 +833,10 @@ template <int N, typename P> __device__ __forceinline__ void ranked(const float*
 }
 
 // The logits x of the CTA's slice with f(x, i), all of them `least` or more, into its
-// part of the first CTA's list, of LIST / C keys.
+// part of the first CTA's list, of LIST / C keys.  false: a part is too short for them
+// (the same for all CTAs).
 template <int IO, int C, typename P>
-__device__ __forceinline__ void gather(Ctx<C>& k, const Row<IO>& row, bool any, float least,
+__device__ __forceinline__ bool gather(Ctx<C>& k, const Row<IO>& row, bool any, float least,
                                        P&& f) {
     Shared& sh = k.sh;
     if (any)
@@ -837,20 +856,24 @@ __device__ __forceinline__ void gather(Ctx<C>& k, const Row<IO>& row, bool any, 
             }
         }
     __syncthreads();
-    if (k.tid == 0) {
-        *k.cl.map_shared_rank(&sh.listed[k.rank], 0) = sh.my_listed;
-        sh.my_listed = 0;
-    }
+    const uint32_t mine = sh.my_listed;
+    if (k.tid < C) *k.cl.map_shared_rank(&sh.listed[k.rank], k.tid) = mine;
     cluster_sync();
+    if (k.tid == 0) sh.my_listed = 0;                    // (all have read it)
+    bool fits = true;
+#pragma unroll
+    for (int c = 0; c < C; ++c) fits &= sh.listed[c] <= LIST / C;
+    return fits;
 }
 
 // The border in the first CTA's list (its threads call this): the
 // shortest prefix whose mass reaches `target` (0: top_p of that of the first `limit`),
-// without both the first `limit`.  Tells all the border with `above` added to its
-// sum (NOT_FOUND: the list did not hold them), and with e makes the draw.
+// without both the first `limit`.  Tells all CTAs, or this one alone, the border with
+// `above` added to its sum, and with e makes the draw.
 template <int IO, int C>
 __device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int limit, u64 top_p,
-                                           u64 target, u64 above, const float* e, Cand& best) {
+                                           u64 target, u64 above, bool all, const float* e,
+                                           Cand& best) {
     Shared& sh = k.sh;
     const int tid = k.tid;
     // the parts moved together
@@ -858,19 +881,13 @@ __device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int li
     {
         constexpr int PART = LIST / C, PER = NT / C;     // threads to a part
         const int part = tid / PER;
-        bool over = false;
         int to = 0;
         u64 key[PART / PER];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int y = (int)sh.listed[c];
-            over |= y > PART;
             if (c < part) to += y;
             n += y;
-        }
-        if (over) {
-            if (tid == 0) k.tell(Border{0, 0, 0, 0, NOT_FOUND});
-            return;
         }
         const int mine = (int)sh.listed[part];
 #pragma unroll
@@ -933,28 +950,10 @@ __device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int li
         if (j >= run || at >= limit) continue;
         const bool in = !by_mass || before < target;
         if (in && (by_mass ? target <= before + w[j] : at == limit - 1))
-            k.tell(Border{list[at], above + before + w[j], 0, 0, FOUND});
+            k.tell(Border{list[at], above + before + w[j], 0, 0, FOUND}, all);
         if (in && e) take(best, Cand{k.wt.template value<IO>(x[j]), ex[j], x[j], i[j]});
         before += w[j];
     }
-}
-
-// The filters with a small top_k, on the sorted list of the logits from `cut` on,
-// which are top_k or more; the first CTA draws the token too.  false: the list is
-// too short for them, and nothing has changed.
-template <int IO, int C>
-__device__ __forceinline__ bool short_list(Ctx<C>& k, const Row<IO>& row, Kept& kept,
-                                           float thread_max, float cut, const float* e, u64& sum,
-                                           Cand& best) {
-    gather<IO>(k, row, thread_max >= cut, cut, [&](float x, int) { return x >= cut; });
-    if (k.rank == 0)
-        solve_list<IO>(k, row, k.sh.prm.top_k, k.sh.prm.top_p, 0, 0, e, best);
-    cluster_sync();
-    const Border b = k.sh.border;
-    if (b.state == NOT_FOUND) return false;
-    sum = b.sum;
-    kept = Kept{value_of(b.from), index_of(b.from)};
-    return true;
 }
 
 // Narrows `kept` to its shortest prefix whose F reaches the target; it stays as it is
@@ -983,15 +982,17 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
             else kept = Kept{v, kept.v == v ? kept.last : (int)IDX_MAX};
             return;
         }
-        gather<IO>(k, row, true, kept.v, [&](float x, int i) {
-            return bin_of<KIND>(top, x) == bin && kept.has(x, i);
-        });
-        Cand none;
-        if (k.rank == 0)
-            solve_list<IO>(k, row, MASS ? LIST : (int)b.target, 0, MASS ? b.target : 0, b.sum,
-                           nullptr, none);
-        cluster_sync();
-        b = sh.border;
+        b.state = BELOW;
+        if (gather<IO>(k, row, true, kept.v, [&](float x, int i) {
+                return bin_of<KIND>(top, x) == bin && kept.has(x, i);
+            })) {
+            Cand none;
+            if (k.rank == 0)
+                solve_list<IO>(k, row, MASS ? LIST : (int)b.target, 0, MASS ? b.target : 0, b.sum,
+                               true, nullptr, none);
+            cluster_sync();
+            b = sh.border;
+        }
     }
     if (b.state != FOUND) b = radix<MASS, IO>(k, row, kept, want);
     if (b.state == NOT_FOUND) return;
@@ -1004,9 +1005,10 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
 //   A token is looked at where w / e can be above the best so far, that is
 // log2 e < log2 w + log2(best.e / best.w); and bits(e) 2^-23 - 127 is at most log2 e
 // (the chord is below the logarithm), which makes the test a multiply-add and an
-// integer comparison, in units of 2^-7.  With a best per warp a group passes it
-// seldom after the first few (a division, or two products, and an exponential for
-// every token made 256 rows' draws 40 us longer).
+// integer comparison, in units of 2^-7.  A group passes it seldom after the first.
+// (256 rows without a filter: 67 million instructions with two products and an
+// exponential a token, 38 million with this test and the filter on two values at once;
+// 103 and 88 us.)
 template <int IO, int C>
 __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const Kept& kept,
                                      const float* e, Cand& best) {
@@ -1215,9 +1217,23 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     if (bad) {
         kept.v = __int_as_float(0x7fffffff);             // NaN: nothing
     } else {
-        if (small_k)
-            summed = drawn = short_list<IO>(k, row, kept, thread_max,
-                                            fmaxf(pooled ? sh.bound : cut, kept.v), e, sum, best);
+        if (small_k) {
+            const float from = fmaxf(pooled ? sh.bound : cut, kept.v);
+            if (gather<IO>(k, row, thread_max >= from, from, [&](float x, int) { return x >= from; })) {
+                // without more to write the first CTA ends it alone (all waiting, 256 rows' 10 to
+                // 200 best 70 us instead of 62)
+                const bool alone = !prob && !out;
+                if (alone && rank != 0) return;
+                if (rank == 0)
+                    solve_list<IO>(k, row, top_k, prm.top_p, 0, 0, !alone, e, best);
+                if (alone) __syncthreads();
+                else cluster_sync();
+                const Border b = sh.border;
+                sum = b.sum;
+                kept = Kept{value_of(b.from), index_of(b.from)};
+                summed = drawn = true;
+            }
+        }
         if (!drawn) {
             if (top_k > 0) select<false, IO>(k, row, kept, top_k, sum);
             if (prm.top_p != 0) {
