@@ -815,7 +815,7 @@ class PagePool:
                 self._t, ("page_table", "kv_len", "free_list", "n_free", "n_held"),
                 ((cfg.B, cfg.max_pages), (cfg.B,), (cfg.n_pages,), (1,), (cfg.B,)))))
         self._ref = ctypes.byref(self._c)
-        self.key = (cfg.B, cfg.max_pages, cfg.n_pages, dev)
+        self.key = (cfg.B, cfg.max_pages, cfg.n_pages, cfg.page, dev)
 
     page_table, kv_len, free_list, n_free, n_held = (
         property(lambda self, i=i: self._t[i]) for i in range(5))
@@ -833,9 +833,9 @@ class PagePool:
 
     def ref(self, cfg: SpecPagedCfg, device: int):
         """The pool as an argument of a call with that configuration."""
-        if self.key != (cfg.B, cfg.max_pages, cfg.n_pages, device):
-            if device != self.key[3]:
-                raise ValueError(f"the pool is on cuda:{self.key[3]}, the current device is "
+        if self.key != (cfg.B, cfg.max_pages, cfg.n_pages, cfg.page, device):
+            if device != self.key[4]:
+                raise ValueError(f"the pool is on cuda:{self.key[4]}, the current device is "
                                  f"cuda:{device}")
             raise ValueError("the pool was made for another configuration")
         return self._ref

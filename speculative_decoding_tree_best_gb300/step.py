@@ -337,8 +337,9 @@ class ChainStep:
         d = self.dcfg
         key = binding.sample_cfg(d.B, d.V, io="bf16" if d.io_dtype else "f32")
         if self._drafter is None:
-            self._drafter = (key, binding.SampleBuffers(key, prob=True),
-                             binding.alloc_sample_workspace(key))
+            dev = self.kv_len.device
+            self._drafter = (key, binding.SampleBuffers(key, prob=True, device=dev),
+                             binding.alloc_sample_workspace(key, dev))
         cfg, out, ws = self._drafter
         binding.token_sample(cfg, logits, e, out, ws, **filters)
         draft_tok[:, i].copy_(out.tok)

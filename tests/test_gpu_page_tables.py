@@ -195,3 +195,24 @@ def test_kv_len_itself_as_what_is_kept_and_captured():
         torch.cuda.synchronize()
         same(pool, s)
         np.testing.assert_array_equal(slots.cpu().numpy(), want)
+
+
+def test_pools_and_arguments_of_another_shape_are_refused():
+    cfg = config(3, 4, 16, 5, 20)
+    pool, ws = binding.PagePool.empty(cfg), binding.alloc_paged_workspace(cfg)
+    slots = torch.empty((3, 4), dtype=torch.int64, device="cuda")
+    n_ok = torch.empty((3,), dtype=torch.int32, device="cuda")
+    for other in (config(2, 4, 16, 5, 20), config(3, 4, 16, 6, 20), config(3, 4, 16, 5, 21),
+                  config(3, 4, 32, 5, 20)):
+        with pytest.raises(ValueError):
+            binding.page_tables_extend(other, pool, slots, n_ok, ws)
+        with pytest.raises(ValueError):
+            binding.page_tables_trim(other, pool, n_ok, ws)
+    for bad in (slots[:, :3], slots.int(), slots.cpu(), None):
+        with pytest.raises((TypeError, ValueError)):
+            binding.page_tables_extend(cfg, pool, bad, n_ok, ws)
+    with pytest.raises(ValueError):
+        binding.page_tables_trim(cfg, pool, n_ok, ws[:256])
+    with pytest.raises(TypeError):
+        binding.PagePool(cfg, pool.page_table.long(), pool.kv_len, pool.free_list, pool.n_free,
+                         pool.n_held)

@@ -1,10 +1,9 @@
 """Rotary positions against the rotation in 64 bits, and the pass that writes the
 cache against the separate calls.
 
-Tolerance.  The angle is off by at most 2^-32 turns (1.5e-9) and the rounding of
-its rest in [-pi/4, pi/4], 2^-25 pi/4... half a step of the largest, 2^-25; the
-Taylor sums by 1.8e-9 and some roundings of 2^-25: sine and cosine are within
-2^-23.  A value is two products and a sum of them in fp32: within
+Tolerance.  The angle is off by at most 2^-32 turns (1.5e-9) and by the roundings of
+its rest in [-pi/4, pi/4], half a step of a number below 1 each (2^-25); the Taylor
+sums by 1.8e-9 and some roundings of 2^-25: sine and cosine are within 2^-23.  A value is two products and a sum of them in fp32: within
 (|a| + |b|) amp (2^-23 + 2 * 2^-24) < (|a| + |b|) amp 2^-22, then half a step of the
 I/O type.  Positions above 2^20 add the 64-bit product's own 2^-53 p."""
 import numpy as np

@@ -157,6 +157,43 @@ def test_masks_and_extremes(io):
     check(x, io, m=[0.01, 0.5, 0.1, 1.0, 0.3, 0.5, 0.5, 2.0])
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [1, 30])
+def test_sorted_rows(io, R):
+    """All of a row's largest logits in one part of it: the bounds that each part
+    gives are far below, and the short list overflows."""
+    V = 60013
+    x = np.sort(rows(R, V, 12), 1)
+    x[::2] = x[::2, ::-1]
+    for k in (40, 300, 900):
+        check(x, io, k=[k] * R, p=[0.97] * R)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_borders_below_the_bins(io):
+    """A few logits far above the others: the bins, which go down from the largest,
+    do not reach the border."""
+    V = 9001
+    x = rows(6, V, 13) - 2000.0
+    x[:, 5000:5003] = [[3.0, 1.0, 2.0]]
+    check(x, io, k=[3000, 2, 1500, 4, 3, 8999], t=[1.0, 1.0, 900.0, 1e4, 2.0, 50.0])
+    check(x, io, p=[0.9, 0.99, 0.8, 0.5, 0.3, 0.97], t=[900.0, 1.0, 2000.0, 1e4, 500.0, 3000.0])
+    x = -(10.0 ** np.random.default_rng(14).uniform(33, 37, (3, V)))      # nothing near 0
+    check(x, io, k=[2000, 7, 100], t=[1e33, 1e35, 1e36])
+    check(x, io, p=[0.6, 0.9, 0.8], t=[1e35, 1e36, 1e37])
+
+
+def test_small_magnitudes():
+    """Most logits within 2^-12 of 0, many of them 0: one bin holds them."""
+    x = rows(4, 20011, 15, 1e-5)
+    x[1, ::3] = 0.0
+    x[2, ::2] *= 1e5
+    x[3, 100:] = -0.0
+    for io in ("bf16", "f32"):
+        check(x, io, p=[0.5, 0.7, 0.9, 0.3], t=[1e-5, 0.7, 1.0, 2.0])
+        check(x, io, k=[5000, 12000, 1500, 60], p=[0.5, 0.7, 0.9, 0.35], t=[1e-5, 2e-5, 1.0, 2.0])
+
+
 def test_temperatures_at_the_ends():
     x = rows(7, 999, 6)
     x[1, 500] = x[1, 300] = x[1].max() + 1                # greedy with a tie
