@@ -1164,7 +1164,9 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     // of what k / C of each CTA's threads reach.
     const int top_k = sh.prm.top_k < V ? sh.prm.top_k : 0;
     constexpr int EACH = POOL / C < SOME ? POOL / C : SOME;
-    const bool pooled = top_k > 0 && top_k <= EACH * C * 3 / 4;
+    // (a share is 8 threads' groups; the last CTA's slice may be shorter)
+    const int shares = min(EACH, share / (NT / SOME));
+    const bool pooled = top_k > 0 && top_k <= shares * C * 3 / 4;
     const bool small_k = pooled || (top_k > 0 && top_k <= min(SMALL_K, C * NT / 2));
     float cut = INFINITY;
     if (small_k && !pooled) {
@@ -1366,7 +1368,8 @@ cudaError_t launch_c(const spec_sample_cfg& c, SampleArgs& a, int64_t groups, cu
 }
 
 // CTAs per row: as many as it takes for two CTAs' slices to share an SM, and more
-// while the rows leave SMs idle (no slice under 64 groups).
+// while the rows leave SMs idle and a thread has a group (smaller slices give the
+// bounds for top_k too few maxima: one row of 5000 tokens 18.6 us instead of 10.5).
 template <int IO>
 cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
     constexpr int VEC = Row<IO>::VEC;
@@ -1375,7 +1378,7 @@ cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
     int sms = device_sm_count();
     if (sms < 1) sms = 1;
     int C = 1;
-    while (C < MAX_CLUSTER && groups / C > 64 &&
+    while (C < MAX_CLUSTER && groups / C >= 2 * NT &&
            ((int64_t)c.R * C <= sms || (groups + C - 1) / C * 16 > two))
         C *= 2;
     switch (C) {
