@@ -645,11 +645,8 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
             const u64 key = key_of(x, i);
             if (key < lo || key > hi || !kept.has(x, i)) return;
             const int bin = (int)((hi - key) >> shift);
-            if (MASS) {
-                add_mass(sh, bin, k.wt.template fixed<IO>(x));
-            } else {
-                atomicAdd(&sh.count[bin], 1u);
-            }
+            if (MASS) add_mass(sh, bin, k.wt.template fixed<IO>(x));
+            else atomicAdd(&sh.count[bin], 1u);
         });
         cluster_sync();
         constexpr int PART = NMASS / C, RUN = PART / NT < 1 ? 1 : PART / NT;
@@ -700,7 +697,8 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
 // What stays of this CTA's when of the tokens at value v the first `want` of all do.
 // `mine`: the CTA's number of them.
 template <int IO, int C>
-__device__ __forceinline__ Kept first_ties(Ctx<C>& k, const Row<IO>& row, const Kept& in, float v, u64 want, uint32_t mine) {
+__device__ __forceinline__ Kept first_ties(Ctx<C>& k, const Row<IO>& row, const Kept& in, float v,
+                                           u64 want, uint32_t mine) {
     Shared& sh = k.sh;
     if (k.tid < C) *k.cl.map_shared_rank(&sh.ties[k.rank], k.tid) = mine;
     cluster_sync();
@@ -1101,7 +1099,8 @@ __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req
     if (min_p > 0.0f && min_p < 1.0f) y.min_low = (double)t * log((double)min_p);
     // log2(e) / t to 2^-46: the quotient's remainder, divided again
     y.c = fminf(1.4426950216293335f / t, 1e38f);
-    y.c_lo = y.c < 1e38f && t < INFINITY ? (fmaf(-y.c, t, 1.4426950216293335f) + 1.925963033500011e-8f) / t : 0.0f;
+    y.c_lo = y.c < 1e38f && t < INFINITY
+                 ? (fmaf(-y.c, t, 1.4426950216293335f) + 1.925963033500011e-8f) / t : 0.0f;
     if (t == 0.0f) y.c = y.c_lo = 0.0f;
     y.far = y.c > 0.0f ? fminf(CUT / y.c, 3.0e38f) : 3.4028234663852886e38f;
     return y;
@@ -1221,7 +1220,8 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     } else {
         if (small_k) {
             const float from = fmaxf(pooled ? sh.bound : cut, kept.v);
-            if (gather<IO>(k, row, thread_max >= from, from, [&](float x, int) { return x >= from; })) {
+            if (gather<IO>(k, row, thread_max >= from, from,
+                           [&](float x, int) { return x >= from; })) {
                 // without more to write the first CTA ends it alone (all waiting, 256 rows' 10 to
                 // 200 best 70 us instead of 62)
                 const bool alone = !prob && !out;
