@@ -38,7 +38,7 @@
 //
 // What bounds it: reading the logits (2 or 4 bytes a token), the random numbers of what
 // stays, writing what is asked for.  Measured (graph replays, V = 151936): one bf16 row
-// 10.7 us, a chain of six exchanges and a sort; 24 fp32 rows with their probabilities
+// 10.3 us, a chain of five exchanges and a sort; 24 fp32 rows with their probabilities
 // 43 us, most of it the rows with a top_p alone (some 60 instructions a token in their
 // histogram, and only their clusters' SMs at work); 216 bf16 rows filtered and written
 // back 75 us, 131 MB at 1.7 TB/s; 256 bf16 rows' nucleus 146 us.  The last two are bound by instructions (35 a
@@ -1370,6 +1370,10 @@ cudaError_t launch_c(const spec_sample_cfg& c, SampleArgs& a, int64_t groups, cu
 // CTAs per row: as many as it takes for two CTAs' slices to share an SM, and more
 // while the rows leave SMs idle and a thread has a group (smaller slices give the
 // bounds for top_k too few maxima: one row of 5000 tokens 18.6 us instead of 10.5).
+//   Idle: with twice as many there were not more than 8/5 of the SMs' number, for
+// clusters of 16 not more than that, since a GPC holds one of those at a CTA an SM.
+// (Nucleus of 16 / 24 / 38 rows of 151936, up to twice the number: 37.3, 29.0, 42.1 us;
+// up to once: 26.3, 29.6, 40.8; like this 26.3, 29.0, 40.8.)
 template <int IO>
 cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
     constexpr int VEC = Row<IO>::VEC;
@@ -1379,7 +1383,8 @@ cudaError_t sample_t(const spec_sample_cfg& c, SampleArgs& a, cudaStream_t st) {
     if (sms < 1) sms = 1;
     int C = 1;
     while (C < MAX_CLUSTER && groups / C >= 2 * NT &&
-           ((int64_t)c.R * C <= sms || (groups + C - 1) / C * 16 > two))
+           ((int64_t)c.R * 2 * C * 5 <= (2 * C == MAX_CLUSTER ? 5 : 8) * (int64_t)sms ||
+            (groups + C - 1) / C * 16 > two))
         C *= 2;
     switch (C) {
         case 1: return launch_c<IO, 1>(c, a, groups, st);
