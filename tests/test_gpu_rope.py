@@ -232,3 +232,29 @@ def test_append_rows_that_are_not_finite_zeros_and_bad_slots():
     assert (c.k_pages[0, 0, 0].float() == 0).all() and c.v_pages[0, 0, 2].float().isnan().all()
     assert (c.k_pages.view(torch.uint8)[0, 0, 3:] == 0x2b).all()
     assert (c.k_pages.view(torch.uint8)[1] == 0x2b).all() and (q_out[0, 3:] != 0).any()
+
+
+def test_captured_steps_follow_their_inputs():
+    """rope_page_append in a graph: replays read the lengths, slots and rows of their time."""
+    B, T, Hq, Hkv, D = 3, 2, 4, 2, 64
+    pcfg = binding.paged_cfg(B=B, T=T, Hq=Hq, Hkv=Hkv, D=D, page=16, n_pages=12, max_pages=4)
+    c, d, ws = cache(pcfg), cache(pcfg), binding.alloc_paged_workspace(pcfg)
+    rc, table = binding.rope_cfg(B * T, Hq, Hkv, D), binding.rope_table(D)
+    q, k, v = (randn((B, T, h, D), "bf16", s) for s, h in ((1, Hq), (2, Hkv), (3, Hkv)))
+    slots = torch.arange(B * T, device="cuda").view(B, T) * 17
+    q_out, now = torch.zeros_like(q), torch.zeros_like(q)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            binding.rope_page_append(rc, pcfg, c, table, slots, q, k, v, q_out, ws)
+    for step in range(3):
+        for kv in (c, d):
+            kv.kv_len.copy_(torch.tensor([5, 0, 40], dtype=torch.int32) + step)
+        slots.add_(1)
+        k.copy_(randn((B, T, Hkv, D), "bf16", 10 + step))
+        graph.replay()
+        binding.rope_page_append(rc, pcfg, d, table, slots, q, k, v, now, ws)
+        assert torch.equal(q_out, now)
+        for a, b in ((c.k_pages, d.k_pages), (c.v_pages, d.v_pages)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

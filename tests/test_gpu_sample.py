@@ -313,3 +313,33 @@ def test_captured_on_another_stream():
         graph.replay()
         binding.token_sample(cfg, x, e, now, ws, top_p=p)
         assert torch.equal(out.tok, now.tok) and torch.equal(out.prob, now.prob)
+
+
+def test_two_streams_at_once():
+    """Calls of two streams, with outputs and workspaces of their own, beside one
+    another: the same results as one after the other."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    jobs = []
+    for R, V, io in ((40, 30000, "bf16"), (7, 60000, "f32")):
+        cfg = binding.sample_cfg(R, V, io=io)
+        x = (3 * torch.randn((R, V), generator=g, device="cuda")).to(DT[io])
+        e = torch.rand((R, V), generator=g, device="cuda") + 1e-6
+        p = 0.3 + 0.69 * torch.rand((R,), generator=g, device="cuda")
+        k = torch.randint(0, 2000, (R,), generator=g, device="cuda", dtype=torch.int32)
+        for kw in (dict(top_p=p), dict(top_k=k), dict(top_k=k, top_p=p)):
+            want = binding.SampleBuffers(cfg, prob=True)
+            binding.token_sample(cfg, x, e, want, binding.alloc_sample_workspace(cfg), **kw)
+            jobs.append((cfg, x, e, kw, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for i, (cfg, x, e, kw, want) in enumerate(jobs):
+            out, ws = binding.SampleBuffers(cfg, prob=True), binding.alloc_sample_workspace(cfg)
+            got.append((out, ws))
+        torch.cuda.synchronize()
+        for i, (cfg, x, e, kw, want) in enumerate(jobs):
+            binding.token_sample(cfg, x, e, *got[i], stream=streams[i % 2], **kw)
+        torch.cuda.synchronize()
+        for (out, _), (_, _, _, _, want) in zip(got, jobs):
+            assert torch.equal(out.tok, want.tok) and torch.equal(out.prob, want.prob)
