@@ -704,6 +704,7 @@ __device__ __forceinline__ Kept first_ties(Ctx<C>& k, const Row<IO>& row, const 
     cluster_sync();
     u64 before = 0;
     for (int c = 0; c < k.rank; ++c) before += sh.ties[c];
+    if (in.v > v) return in;                             // its ties left before
     if (want <= before) return above_value(v);
     if (want >= before + mine) return Kept{v, in.v == v ? in.last : (int)IDX_MAX};
     // the border is here: a run of groups a thread, in order
@@ -977,8 +978,8 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
             const u64 n = (b.target + w - 1) / w;
             if (MASS) sum = b.sum + n * w;
             if (n < b.tokens) kept = first_ties<IO>(k, row, kept, v, n, sh.count[bin]);
-            else kept = Kept{v, kept.v == v ? kept.last : (int)IDX_MAX};
-            return;
+            else if (!(kept.v > v)) kept = Kept{v, kept.v == v ? kept.last : (int)IDX_MAX};
+            return;                                      // (above v: its ties left before)
         }
         b.state = BELOW;
         if (gather<IO>(k, row, true, kept.v, [&](float x, int i) {

@@ -140,6 +140,20 @@ def test_ties_go_to_the_lowest_index(io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_ties_that_both_borders_meet(io):
+    """top_k leaves 2000 of 3000 equal logits, and top_p's border is among them or at
+    their end: those that top_k removed stay removed.  (In the last row one weighs
+    e^2 times the others: the sum is 1 + 1999 e^-2 = 271.5, 0.6 of it 162.9, and before
+    the token j there is 1 + (j - 1) e^-2, which is less up to j = 1197: 1198 tokens.
+    0.75 of 2000 equal ones is on a border, and not compared.)"""
+    x = np.full((4, 60000), -5.0)
+    x[:, 7::20] = 2.0
+    x[2:, 11] = 4.0
+    p = [0.9999, 0.75, 0.9999, 0.6]
+    assert check(x, io, k=[2000] * 4, p=p) == [2000, 2000, 1198]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_masks_and_extremes(io):
     V = 5003
     low = float(torch.finfo(DT[io]).min)
