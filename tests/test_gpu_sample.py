@@ -357,3 +357,24 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for (out, _), (_, _, _, _, want) in zip(got, jobs):
             assert torch.equal(out.tok, want.tok) and torch.equal(out.prob, want.prob)
+
+
+def test_cold_caches():
+    """Calls whose instructions and inputs come from memory, so that the warps of the
+    CTAs that share a row are far apart: the same borders each time."""
+    R, V = 30, 60013
+    x = torch.from_numpy(rows(R, V, 24).astype(np.float32)).cuda()
+    p = np.random.default_rng(1).uniform(0.3, 0.999, R).astype(np.float32)
+    want = [ref.sample(y, 1.0, 0, float(q), 0.0)[1:] for y, q in zip(x.cpu().numpy(), p)]
+    sure = torch.tensor([m >= NEAR for _, m in want])
+    n = torch.tensor([n for n, _ in want])
+    assert int(sure.sum()) >= R - 2
+    cfg = binding.sample_cfg(R, V, io="f32")
+    ws, e, top_p = binding.alloc_sample_workspace(cfg), torch.ones_like(x), torch.from_numpy(p).cuda()
+    out = binding.SampleBuffers(cfg, logits=True)
+    flush = torch.empty(400 << 20, dtype=torch.uint8, device="cuda")         # more than L2
+    for i in range(200):
+        flush.fill_(i)
+        binding.token_sample(cfg, x, e, out, ws, top_p=top_p)
+        got = (out.logits > -math.inf).sum(1).cpu()
+        assert got[sure].tolist() == n[sure].tolist()
