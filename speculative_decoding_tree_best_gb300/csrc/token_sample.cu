@@ -38,11 +38,11 @@
 //
 // What bounds it: reading the logits (2 or 4 bytes a token), the random numbers of what
 // stays, writing what is asked for.  Measured (graph replays, V = 151936): one bf16 row
-// 10.3 us, a chain of five exchanges and a sort; 24 fp32 rows with their probabilities
-// 43 us, most of it the rows with a top_p alone (some 60 instructions a token in their
+// 10.5 us, a chain of five exchanges and a sort; 24 fp32 rows with their probabilities
+// 44 us, most of it the rows with a top_p alone (some 60 instructions a token in their
 // histogram, and only their clusters' SMs at work); 216 bf16 rows filtered and written
-// back 75 us, 131 MB at 1.7 TB/s; 256 bf16 rows' nucleus 146 us.  The last two are bound by instructions (35 a
-// token, at 40 to 50 % of the issue slots: the CTAs of a cluster wait for one another,
+// back 76 us, 131 MB at 1.7 TB/s; 256 bf16 rows' nucleus 148 us.
+// The last two are bound by instructions (35 a token, at 40 to 50 % of the issue slots: the CTAs of a cluster wait for one another,
 // and 256 rows are 3.4 rounds of the 76 clusters that fit).
 #include <cooperative_groups.h>
 #include <math.h>
