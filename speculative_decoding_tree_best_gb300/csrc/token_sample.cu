@@ -635,7 +635,8 @@ template <bool MASS, int IO, int C>
 __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 want) {
     Shared& sh = k.sh;
     const int tid = k.tid;
-    u64 lo = (u64)key_of(kept.v) << IDX_BITS, hi = (u64)key_of(k.wt.m) << IDX_BITS | IDX_MAX;
+    // the range is the same in all CTAs (kept.v need not be: see first_ties)
+    u64 lo = (u64)key_of(sh.prm.low) << IDX_BITS, hi = (u64)key_of(k.wt.m) << IDX_BITS | IDX_MAX;
     u64 above = 0, target = want;
     for (int pass = 0;; ++pass) {
         for (int b = tid; b < 3 * NMASS; b += NT) sh.mass[0][b] = 0;
