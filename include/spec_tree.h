@@ -703,8 +703,8 @@ typedef struct spec_rope_scaling {
     int32_t kind;
 } spec_rope_scaling;
 
-/* Host: turns[j] = f_j / 2 pi in units of 2^-64 turns (host, [rot / 2]) and amp
- * (host), the table that the calls below take as a device copy.  rot a multiple
+/* Host: turns[j] = f_j / 2 pi in units of 2^-64 turns, to the nearest one (host,
+ * [rot / 2]), and amp (host), the table that the calls below take as a device copy.  rot a multiple
  * of 16 in [16, 128]. */
 int spec_rope_turns(int rot, const spec_rope_scaling *scaling, uint64_t *turns, float *amp);
 
@@ -726,8 +726,9 @@ typedef struct spec_rope_cfg {
 /*
  * rope_apply -- rotary positions of queries and keys.  A pair (a, b) at position
  * p becomes amp (a cos t - b sin t, a sin t + b cos t), t = p f_j, in fp32; values
- * past `rot` are copied.  The angle is exact to 2^-32 turns at every position
- * (integer arithmetic modulo a turn).  The inverse is also the gradient with
+ * past `rot` are copied.  The angle is within 2^-31 turns of t at every position
+ * (integer arithmetic modulo a turn: half a unit of the table at 2^31 is 2^-34, and
+ * the upper 32 bits count).  The inverse is also the gradient with
  * respect to the inputs.
  *   turns [rot/2] uint64   pos [rows] int32 (any value)
  *   q [rows][Hq][D] io, k [rows][Hkv][D] io (NULL with Hkv = 0), tokens

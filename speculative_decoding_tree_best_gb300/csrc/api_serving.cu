@@ -20,6 +20,53 @@ bool al16_or_null(const void* p) { return !p || al16(p); }
 
 bool is_finite(double x) { return x - x == 0.0; }
 
+// ---- a rotation's frequencies, in pairs of doubles (the sum of both, some 100 bits).
+// A table of 64-bit numbers needs more than a double's 53: at position 2^31 a relative
+// error of 2^-53 is 2^-25 turns.
+
+struct Two {
+    double hi, lo;
+};
+
+Two joined(double a, double b) {                         // |a| >= |b|
+    const double s = a + b;
+    return Two{s, b - (s - a)};
+}
+
+Two add(Two a, Two b) {
+    const double s = a.hi + b.hi, v = s - a.hi;
+    return joined(s, (a.hi - (s - v)) + (b.hi - v) + (a.lo + b.lo));
+}
+
+Two mul(Two a, Two b) {
+    volatile double p = a.hi * b.hi;                     // rounded by itself on every machine
+    return joined(p, fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+
+Two neg(Two a) { return Two{-a.hi, -a.lo}; }
+
+Two div(Two a, Two b) {
+    const double x = a.hi / b.hi;
+    Two r = add(a, neg(mul(Two{x, 0.0}, b)));
+    const double y = r.hi / b.hi;
+    r = add(r, neg(mul(Two{y, 0.0}, b)));
+    return add(joined(x, y), Two{r.hi / b.hi, 0.0});
+}
+
+// base^(-j / n): a Newton step from the rounded power, whose n-th power times base^j is
+// multiplied up in an order that stays near 1
+Two root(double base, int j, int n) {
+    const double f = pow(base, -(double)j / n);
+    if (f == 0.0) return Two{0.0, 0.0};
+    Two t{1.0, 0.0};
+    for (int fs = n, bases = j; fs + bases > 0;) {
+        const bool down = bases == 0 || (fs > 0 && t.hi >= 1.0);
+        t = mul(t, Two{down ? f : base, 0.0});
+        --(down ? fs : bases);
+    }
+    return joined(f, -f * ((t.hi - 1.0) + t.lo) / n);
+}
+
 }  // namespace
 
 extern "C" {
@@ -56,20 +103,27 @@ int spec_rope_turns(int rot, const spec_rope_scaling* s, uint64_t* turns, float*
     if (yarn && (s->orig_len < 1 || !(s->beta_slow >= 0.0) || !(s->beta_fast > s->beta_slow) ||
                  !is_finite(s->beta_fast)))
         return ST_EINVAL;
-    double base = s->base;
-    if (s->kind == SPEC_ROPE_NTK) base *= pow(s->factor, (double)rot / (rot - 2));
-    if (!is_finite(base)) return ST_EINVAL;
-    const double two_pi = 6.283185307179586476925;
-    for (int j = 0; j < rot / 2; ++j) {
-        double f = pow(base, -2.0 * j / rot);
-        if (s->kind == SPEC_ROPE_LINEAR) f /= s->factor;
+    const int n = rot / 2;
+    const bool ntk = s->kind == SPEC_ROPE_NTK;
+    if (ntk && !is_finite(s->base * pow(s->factor, (double)n / (n - 1)))) return ST_EINVAL;
+    const Two two_pi{6.283185307179586, 2.4492935982947064e-16}, factor{s->factor, 0.0};
+    for (int j = 0; j < n; ++j) {
+        Two f = root(s->base, j, n);
+        if (ntk) f = mul(f, root(s->factor, j, n - 1));  // (factor^(n / (n - 1)))^(-j / n)
+        if (s->kind == SPEC_ROPE_LINEAR) f = div(f, factor);
         if (yarn) {
-            double g = (s->orig_len * f / two_pi - s->beta_slow) / (s->beta_fast - s->beta_slow);
-            g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
-            f = (1.0 - g) * f / s->factor + g * f;
+            const Two slow{-s->beta_slow, 0.0};
+            const Two over = div(mul(Two{(double)s->orig_len, 0.0}, f), two_pi);
+            Two g = div(add(over, slow), add(Two{s->beta_fast, 0.0}, slow));
+            if (g.hi <= 0.0) g = Two{0.0, 0.0};
+            if (g.hi >= 1.0) g = Two{1.0, 0.0};
+            f = add(div(mul(add(Two{1.0, 0.0}, neg(g)), f), factor), mul(g, f));
         }
         // f <= 1: under 0.16 turns a position
-        turns[j] = (uint64_t)(f / two_pi * 18446744073709551616.0 + 0.5);
+        const Two t = div(f, two_pi);
+        const double hi = t.hi * 18446744073709551616.0, whole = floor(hi);
+        const double rest = (hi - whole) + t.lo * 18446744073709551616.0;
+        turns[j] = (uint64_t)whole + (uint64_t)(int64_t)floor(rest + 0.5);
     }
     *amp = yarn ? (float)(0.1 * log(s->factor) + 1.0) : 1.0f;
     return ST_OK;

@@ -2,13 +2,12 @@
 // write of a step's new rows into the cache's pages.
 //
 // Mathematics.  The pair j of a head at position p turns by p f_j.  The angle is
-// taken in turns, modulo one, in integers: the table holds f_j / 2 pi in units of
-// 2^-64 turns, and p times that, modulo 2^64, is the fraction of a turn to the
-// last bit at any position (a table error of 2^-54 of f_j is 2^-24 turns at
-// p = 2^30).  Its upper 32 bits are split into a quarter turn and a rest in
-// [-pi/4, pi/4], whose sine and cosine are Taylor sums to x^9 and x^10 (the next
-// terms: 1.8e-9, 1.1e-10).  No position needs more than fp32, and none loses
-// accuracy to its size.
+// taken in turns, modulo one, in integers: the table holds f_j / 2 pi in whole units
+// of 2^-64 turns, and p times that, modulo 2^64, is the fraction of a turn, at most
+// 2^-34 off at the farthest position (half a unit times 2^31).  Its upper 32 bits are
+// split into a quarter turn and a rest in [-pi/4, pi/4], whose sine and cosine are
+// Taylor sums to x^9 and x^10 (the next terms: 1.8e-9, 1.1e-10).  No position needs
+// more than fp32, and none loses accuracy to its size.
 //
 // Data flow.  A head's row belongs to D / 16 (bf16) or D / 8 (fp32) lanes; a lane
 // holds two 16-byte pieces that are each other's partners (elements v and
