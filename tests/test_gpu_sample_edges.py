@@ -7,7 +7,7 @@ import torch
 
 from speculative_decoding_tree_best_gb300 import binding
 from tests import indep_serving as ref
-from tests.test_gpu_sample import NEAR, check
+from tests.test_gpu_sample import DT, NEAR, check, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,50 @@ def test_a_border_near_zero_after_ties(io, R, V, low):
     assert ref.sample(x[0], 1.0, k, float(np.float32(0.3)))[2] >= NEAR
     n = check(x, io, k=[k] * R, p=[0.3] * R)
     assert len(n) == R and abs(n[0] - 0.3 * k) < 0.01 * k
+
+
+# how a border is found, with the I/O type, rows, vocabulary, spread, top_k and top_p
+# (cluster sizes from 1 to 16 CTAs)
+BORDERS = {
+    "masses and a list": ("f32", 30, 60013, 3.0, 0, 1),
+    "masses, 16 CTAs": ("f32", 1, 151936, 3.0, 0, 1),
+    "masses, few CTAs": ("f32", 150, 20011, 3.0, 0, 1),
+    "counts of values": ("bf16", 30, 60013, 3.0, 0, 1),
+    "counts of values, many rows": ("bf16", 256, 60013, 3.0, 0, 1),
+    "counts, ties by value": ("bf16", 30, 60013, 3.0, 3000, 0),
+    "counts and a list": ("f32", 30, 60013, 3.0, 3000, 0),
+    "both in the histogram": ("bf16", 9, 120011, 3.0, 5000, 1),
+    "both in the histogram, fp32": ("f32", 9, 120011, 3.0, 5000, 1),
+    "radix": ("f32", 6, 60013, 1e-5, 30000, 1),
+    "radix after ties": ("bf16", 6, 60013, 1e-5, 30000, 1),
+    "short list": ("bf16", 30, 60013, 3.0, 40, 1),
+    "short list by the threads' maxima": ("f32", 30, 60013, 3.0, 900, 1),
+    "short list, 16 CTAs": ("bf16", 1, 151936, 3.0, 200, 1),
+}
+
+
+def test_cold_caches_of_all_borders():
+    """Each way to a border in turn with the others, L2 overwritten before each call,
+    so that instructions and inputs come from memory: the same borders each time."""
+    jobs = []
+    for i, (name, (io, R, V, spread, k, p)) in enumerate(BORDERS.items()):
+        x = torch.from_numpy(rows(R, V, 40 + i, spread).astype(np.float32)).cuda().to(DT[io])
+        p = np.random.default_rng(i).uniform(0.3, 0.999, R).astype(np.float32) if p else None
+        some = range(0, R, max(1, R // 30))
+        want = [ref.sample(x[r].float().cpu().numpy(), 1.0, k, 1.0 if p is None else float(p[r]))[1:]
+                for r in some]
+        sure = [m >= NEAR for _, m in want]
+        assert sum(sure) >= len(want) - 2
+        cfg = binding.sample_cfg(R, V, io=io)
+        kw = dict(top_k=torch.full((R,), k, dtype=torch.int32, device="cuda") if k else None,
+                  top_p=None if p is None else torch.from_numpy(p).cuda())
+        jobs.append((name, cfg, x, binding.alloc_sample_workspace(cfg), kw,
+                     binding.SampleBuffers(cfg, draw=False, logits=True),
+                     [(r, n) for r, (n, _), ok in zip(some, want, sure) if ok]))
+    flush = torch.empty(400 << 20, dtype=torch.uint8, device="cuda")         # more than L2
+    for i in range(50):
+        for name, cfg, x, ws, kw, out, want in jobs:
+            flush.fill_(i % 100)
+            binding.token_sample(cfg, x, None, out, ws, **kw)
+            n = (out.logits > -np.inf).sum(1).cpu()
+            assert [int(n[r]) for r, _ in want] == [w for _, w in want], name
