@@ -763,12 +763,22 @@ typedef struct spec_sample_cfg {
     int32_t io_dtype;        /* of the logits */
 } spec_sample_cfg;
 
+/* What becomes of rows that do not count. */
+enum {
+    SPEC_IDLE_SKIP = 0,      /* nothing of them is read, written or raised */
+    SPEC_IDLE_QUIET = 1      /* as the others, but they raise nothing */
+};
+
 /* Parameters of the requests, [ceil(R / per)] each; NULL: off for all rows. */
 typedef struct spec_sample_params {
     const float *temperature;   /* >= 0 (off: 1); 0 keeps the first maximum alone */
     const int32_t *top_k;       /* <= 0: off */
     const float *top_p;         /* >= 1: off; <= 0 keeps one token */
     const float *min_p;         /* <= 0: off; above 1 as 1 */
+    const int32_t *last_row;    /* of a request's `per` rows, the last that counts (-1: none
+                                   do, else held to [0, per - 1]; off: all do).  n_draft is
+                                   that for the N + 1 rows of draft_verify_sampled. */
+    int32_t idle;               /* SPEC_IDLE_*, for the rows that do not count */
 } spec_sample_params;
 
 typedef struct spec_sample_out {

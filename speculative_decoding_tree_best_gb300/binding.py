@@ -120,7 +120,8 @@ class SpecSampleCfg(ctypes.Structure):
 
 
 class SpecSampleParams(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p")]
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "temperature", "top_k", "top_p", "min_p", "last_row")] + [("idle", ctypes.c_int32)]
 
 
 class SpecSampleOut(ctypes.Structure):
@@ -1055,18 +1056,24 @@ class SampleBuffers:
         return self._ref
 
 
+_IDLE = {"skip": 0, "quiet": 1}
+
+
 def token_sample(cfg: SpecSampleCfg, logits, e, out: SampleBuffers, ws, temperature=None,
-                 top_k=None, top_p=None, min_p=None, stream=None):
+                 top_k=None, top_p=None, min_p=None, stream=None, last_row=None, idle="skip"):
     """Sample from logits io [R][V] with e f32 [R][V] (None where `out` draws no
     token); temperature, top_p, min_p f32 and top_k int32 [ceil(R / per)], or None:
-    off."""
+    off.  last_row int32 [ceil(R / per)] (None: all rows count): of a request's rows
+    the last that counts, -1: none; the rows after it are left out ("skip": their
+    outputs stay as they were) or treated as the others but raise nothing ("quiet")."""
     dev, f32 = _get_device(), torch.float32
     RV, n = (cfg.R, cfg.V), (-(-cfg.R // max(cfg.per, 1)),)
     if (e is None) != (out.tok is None):
         raise ValueError("e goes with outputs that draw a token, and only with them")
     params = SpecSampleParams(_arg(temperature, f32, n, "temperature", dev),
                               _arg(top_k, torch.int32, n, "top_k", dev),
-                              _arg(top_p, f32, n, "top_p", dev), _arg(min_p, f32, n, "min_p", dev))
+                              _arg(top_p, f32, n, "top_p", dev), _arg(min_p, f32, n, "min_p", dev),
+                              _arg(last_row, torch.int32, n, "last_row", dev), _IDLE[idle])
     rc = (_lib or load()).token_sample(
         ctypes.byref(cfg), _arg(_required(logits, "logits"), _io_dtype(cfg), RV, "logits", dev),
         ctypes.byref(params), _arg(e, f32, RV, "e", dev), out.ref(cfg, dev),

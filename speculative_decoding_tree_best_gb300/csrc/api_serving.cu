@@ -169,8 +169,10 @@ int token_sample(const spec_sample_cfg* cfg, const void* logits, const spec_samp
     if (rc) return rc;
     if (!params || !out || !al16(logits) || !al16(ws) || !al16_or_null(e)) return ST_EINVAL;
     if (!al16_or_null(params->temperature) || !al16_or_null(params->top_k) ||
-        !al16_or_null(params->top_p) || !al16_or_null(params->min_p))
+        !al16_or_null(params->top_p) || !al16_or_null(params->min_p) ||
+        !al16_or_null(params->last_row))
         return ST_EINVAL;
+    if (params->idle != SPEC_IDLE_SKIP && params->idle != SPEC_IDLE_QUIET) return ST_EINVAL;
     if (!al16_or_null(out->tok) || !al16_or_null(out->tok_prob) || !al16_or_null(out->prob) ||
         !al16_or_null(out->logits))
         return ST_EINVAL;

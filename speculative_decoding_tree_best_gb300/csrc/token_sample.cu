@@ -1134,6 +1134,15 @@ sample_rows(const __grid_constant__ SampleArgs a) {
     row.resident = a.resident;
     cluster_arrive();
     pdl_wait();
+    bool idle = false;                                   // the same for the whole cluster
+    if (a.p.last_row) {
+        const int last = a.p.last_row[r / a.per];
+        idle = last == -1 || r % a.per > max(last, 0);
+        if (idle && a.p.idle == SPEC_IDLE_SKIP) {
+            cluster_wait();
+            return;
+        }
+    }
 
     // ---- the row, and its maximum; the last thread, while its loads are under way,
     // makes the request's parameters
@@ -1207,7 +1216,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
         else if (prm.min_p > 0.0f) low = fmaxf(low, __double2float_ru((double)m + prm.min_low));
         sh.prm.low = low;
         const uint32_t bits = prm.bits | (bad ? SPEC_DEV_BADLOGIT : 0u);
-        if (bits && rank == 0) raise_status(a.ws, bits);
+        if (bits && rank == 0 && !idle) raise_status(a.ws, bits);
     }
     __syncthreads();
     Ctx<C> k{cl, sh, rank, tid, Weights{m, prm.c, prm.c_lo, prm.far, a.lg, sh.pow2}};

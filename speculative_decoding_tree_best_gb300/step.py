@@ -333,7 +333,8 @@ class ChainStep:
         """Draft i of every request from a drafter's logits io [B][V] and e f32
         [B][V]: draft_tok [B][N] and draft_prob [B][N][V], as verify() takes them,
         receive the token and the distribution that it was drawn from.  filters:
-        temperature, top_k, top_p, min_p [B] as token_sample's."""
+        temperature, top_k, top_p, min_p [B] as token_sample's.  A slot with n_draft
+        -1 is sampled too, since n_draft may be set later, but raises nothing."""
         d = self.dcfg
         key = binding.sample_cfg(d.B, d.V, io="bf16" if d.io_dtype else "f32")
         if self._drafter is None:
@@ -341,14 +342,15 @@ class ChainStep:
             self._drafter = (key, binding.SampleBuffers(key, prob=True, device=dev),
                              binding.alloc_sample_workspace(key, dev))
         cfg, out, ws = self._drafter
-        binding.token_sample(cfg, logits, e, out, ws, **filters)
+        binding.token_sample(cfg, logits, e, out, ws, last_row=self.n_draft, idle="quiet",
+                             **filters)
         draft_tok[:, i].copy_(out.tok)
         draft_prob[:, i].copy_(out.prob)
 
     def verify(self, logits, draft_tok, draft_prob, u, e, **filters) -> binding.DraftBuffers:
         """Verify the drafts, advance kv_len and root_tok.  filters: top_k, top_p,
-        min_p [B] as token_sample's, applied to each of a request's rows at the
-        step's temperature."""
+        min_p [B] as token_sample's, applied to those of a request's rows that count
+        (the first n_draft + 1) at the step's temperature."""
         if filters:
             d = self.dcfg
             if self._filtered is None:
@@ -361,7 +363,7 @@ class ChainStep:
                                   binding.alloc_sample_workspace(cfg, dev), t)
             cfg, out, ws, t = self._filtered
             binding.token_sample(cfg, logits.view(cfg.R, cfg.V), None, out, ws, temperature=t,
-                                 **filters)
+                                 last_row=self.n_draft, **filters)
             logits = out.logits.view(logits.shape)
         binding.draft_verify_sampled(self.dcfg, draft_tok, draft_prob, logits, u, e, self.out,
                                      self.draft_ws, n_draft=self.n_draft, kv_len=self.kv_len,
