@@ -350,18 +350,20 @@ class ChainStep:
     def verify(self, logits, draft_tok, draft_prob, u, e, **filters) -> binding.DraftBuffers:
         """Verify the drafts, advance kv_len and root_tok.  filters: top_k, top_p,
         min_p [B] as token_sample's, applied to those of a request's rows that count
-        (the first n_draft + 1) at the step's temperature."""
+        (the first n_draft + 1) at dcfg's temperature."""
         if filters:
             d = self.dcfg
             if self._filtered is None:
                 cfg = binding.sample_cfg(d.B * (d.N + 1), d.V, per=d.N + 1,
                                          io="bf16" if d.io_dtype else "f32")
                 dev = self.kv_len.device
-                t = torch.full((d.B,), d.temperature, dtype=torch.float32, device=dev)
+                t = torch.empty((d.B,), dtype=torch.float32, device=dev)
                 self._filtered = (cfg, binding.SampleBuffers(cfg, draw=False, logits=True,
                                                              device=dev),
                                   binding.alloc_sample_workspace(cfg, dev), t)
             cfg, out, ws, t = self._filtered
+            # by every call, so that a captured step and others each have their own
+            t.fill_(d.temperature)
             binding.token_sample(cfg, logits.view(cfg.R, cfg.V), None, out, ws, temperature=t,
                                  last_row=self.n_draft, **filters)
             logits = out.logits.view(logits.shape)

@@ -1,4 +1,5 @@
-"""Filters in a serving step: rows and slots that do not count."""
+"""Filters in a serving step: rows and slots that do not count, temperatures that
+change."""
 import numpy as np
 import pytest
 import torch
@@ -122,3 +123,19 @@ def test_slots_without_a_request_draft_quietly():
     logits[4, 9] = float("nan")
     st.draft(1, logits, x["e"], x["draft_tok"], x["draft_prob"], **filters())
     assert st.status() == binding.SPEC_DEV_BADLOGIT
+
+
+def kept_at(x, temperature):
+    st = chain_step(temperature)
+    out = result(st.verify(**x, **filters()))
+    return out, (st._filtered[1].logits > -np.inf).sum(1).tolist()
+
+
+def test_the_temperature_changes_between_steps():
+    x = inputs(3)
+    st = chain_step(0.4)
+    for t in (0.4, 1.7, 0.4):
+        st.dcfg.temperature = t
+        got = result(st.verify(**x, **filters()))
+        assert (got, (st._filtered[1].logits > -np.inf).sum(1).tolist()) == kept_at(x, t)
+    assert kept_at(x, 0.4)[1] != kept_at(x, 1.7)[1]
