@@ -291,6 +291,8 @@ class ChainStep:
         self.slots = torch.full((pcfg.B, pcfg.T), -1, dtype=torch.int64, device=device)
         self._keep = torch.empty((pcfg.B,), **i32)
         self._q = torch.empty((pcfg.B, pcfg.T, pcfg.Hq, pcfg.D), dtype=dt, device=device)
+        self._temperature = torch.empty((pcfg.B,), dtype=torch.float32, device=device)
+        # outputs of token_sample, made by the first call that needs them
         self._drafter = self._filtered = None
 
     def begin(self):
@@ -336,14 +338,12 @@ class ChainStep:
         temperature, top_k, top_p, min_p [B] as token_sample's.  A slot with n_draft
         -1 is sampled too, since n_draft may be set later, but raises nothing."""
         d = self.dcfg
-        key = binding.sample_cfg(d.B, d.V, io="bf16" if d.io_dtype else "f32")
+        cfg = binding.sample_cfg(d.B, d.V, io="bf16" if d.io_dtype else "f32")
         if self._drafter is None:
-            dev = self.kv_len.device
-            self._drafter = (key, binding.SampleBuffers(key, prob=True, device=dev),
-                             binding.alloc_sample_workspace(key, dev))
-        cfg, out, ws = self._drafter
-        binding.token_sample(cfg, logits, e, out, ws, last_row=self.n_draft, idle="quiet",
-                             **filters)
+            self._drafter = binding.SampleBuffers(cfg, prob=True, device=self.kv_len.device)
+        out = self._drafter
+        binding.token_sample(cfg, logits, e, out, self.draft_ws, last_row=self.n_draft,
+                             idle="quiet", **filters)
         draft_tok[:, i].copy_(out.tok)
         draft_prob[:, i].copy_(out.prob)
 
@@ -353,19 +353,16 @@ class ChainStep:
         (the first n_draft + 1) at dcfg's temperature."""
         if filters:
             d = self.dcfg
+            cfg = binding.sample_cfg(d.B * (d.N + 1), d.V, per=d.N + 1,
+                                     io="bf16" if d.io_dtype else "f32")
             if self._filtered is None:
-                cfg = binding.sample_cfg(d.B * (d.N + 1), d.V, per=d.N + 1,
-                                         io="bf16" if d.io_dtype else "f32")
-                dev = self.kv_len.device
-                t = torch.empty((d.B,), dtype=torch.float32, device=dev)
-                self._filtered = (cfg, binding.SampleBuffers(cfg, draw=False, logits=True,
-                                                             device=dev),
-                                  binding.alloc_sample_workspace(cfg, dev), t)
-            cfg, out, ws, t = self._filtered
+                self._filtered = binding.SampleBuffers(cfg, draw=False, logits=True,
+                                                       device=self.kv_len.device)
+            out = self._filtered
             # by every call, so that a captured step and others each have their own
-            t.fill_(d.temperature)
-            binding.token_sample(cfg, logits.view(cfg.R, cfg.V), None, out, ws, temperature=t,
-                                 last_row=self.n_draft, **filters)
+            self._temperature.fill_(d.temperature)
+            binding.token_sample(cfg, logits.view(cfg.R, cfg.V), None, out, self.draft_ws,
+                                 temperature=self._temperature, last_row=self.n_draft, **filters)
             logits = out.logits.view(logits.shape)
         binding.draft_verify_sampled(self.dcfg, draft_tok, draft_prob, logits, u, e, self.out,
                                      self.draft_ws, n_draft=self.n_draft, kv_len=self.kv_len,
@@ -374,8 +371,5 @@ class ChainStep:
 
     def status(self) -> int:
         """SPEC_DEV_* bits of the calls so far."""
-        bits = binding.spec_status_read(self.paged_ws) | binding.spec_status_read(self.draft_ws)
-        for made in (self._drafter, self._filtered):
-            if made is not None:
-                bits |= binding.spec_status_read(made[2])
-        return bits
+        return (binding.spec_status_read(self.paged_ws)
+                | binding.spec_status_read(self.draft_ws))

@@ -1,5 +1,5 @@
 """Filters in a serving step: rows and slots that do not count, temperatures that
-change."""
+change, steps captured before anything ran."""
 import numpy as np
 import pytest
 import torch
@@ -128,7 +128,7 @@ def test_slots_without_a_request_draft_quietly():
 def kept_at(x, temperature):
     st = chain_step(temperature)
     out = result(st.verify(**x, **filters()))
-    return out, (st._filtered[1].logits > -np.inf).sum(1).tolist()
+    return out, (st._filtered.logits > -np.inf).sum(1).tolist()
 
 
 def test_the_temperature_changes_between_steps():
@@ -137,5 +137,31 @@ def test_the_temperature_changes_between_steps():
     for t in (0.4, 1.7, 0.4):
         st.dcfg.temperature = t
         got = result(st.verify(**x, **filters()))
-        assert (got, (st._filtered[1].logits > -np.inf).sum(1).tolist()) == kept_at(x, t)
+        assert (got, (st._filtered.logits > -np.inf).sum(1).tolist()) == kept_at(x, t)
     assert kept_at(x, 0.4)[1] != kept_at(x, 1.7)[1]
+
+
+def test_steps_captured_before_anything_ran():
+    """draft and verify captured as the step's first calls; calls outside the graph,
+    at another temperature, before and between its replays."""
+    x = inputs(4)
+    z = x["logits"][:, 1].contiguous()
+    toks, probs = x["draft_tok"].clone(), x["draft_prob"].clone()
+    fresh = chain_step(0.5)
+    fresh.draft(2, z, x["e"], toks, probs, temperature=torch.full((B,), 0.6, device="cuda"))
+    want = result(fresh.verify(**dict(x, draft_tok=toks, draft_prob=probs), **filters()))
+    st, f, t = chain_step(0.5), filters(), torch.full((B,), 0.6, device="cuda")
+    toks2, probs2 = x["draft_tok"].clone(), x["draft_prob"].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.draft(2, z, x["e"], toks2, probs2, temperature=t)
+        st.verify(**dict(x, draft_tok=toks2, draft_prob=probs2), **f)
+    assert st.status() == 0
+    for _ in range(2):
+        st.dcfg.temperature = 1.7
+        assert result(st.verify(**x, **f)) == kept_at(x, 1.7)[0]
+        graph.replay()
+        assert result(st.out) == want
+        assert torch.equal(toks2, toks) and torch.equal(probs2, probs)
+    assert st.status() == 0
