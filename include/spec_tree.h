@@ -806,13 +806,14 @@ size_t spec_sample_workspace_bytes(const spec_sample_cfg *cfg, int num_sms);
  * Borders are decided on masses of 2^-29 relative accuracy in integers (weights
  * below about 2^-42 of the largest, 2^-(61 - ceil(log2 V)), count as nothing
  * there), so that the result does not depend on the order of summation.
- *   logits [R][V] io; e [R][V] float > 0 (NULL: no token is drawn, out->tok and
- *   out->tok_prob are NULL too); of `out` any may be NULL (tok with tok_prob);
+ *   logits [R][V] io; e [R][V] normal floats > 0 (NULL: no token is drawn, out->tok
+ *   and out->tok_prob are NULL too); of `out` any may be NULL (tok with tok_prob);
  *   out->logits may be `logits` itself.
  * A temperature that is NaN or negative counts as 0, another parameter that is
  * NaN as off (SPEC_DEV_BADREQ).  A row with a NaN or +inf logit, or with -inf alone, gives token 0,
  * probabilities 0 and its logits as they are (SPEC_DEV_BADLOGIT).  The race is in
- * fp32: scores nearer than its rounding can fall either way.
+ * fp32: scores nearer than its rounding can fall either way, scores beyond its range
+ * tie, and a weight below 2^-126 of the largest is 0.
  */
 int token_sample(const spec_sample_cfg *cfg, const void *logits, const spec_sample_params *params,
                  const float *e, const spec_sample_out *out, void *ws, void *stream);

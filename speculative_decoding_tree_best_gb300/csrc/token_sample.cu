@@ -100,9 +100,16 @@ struct alignas(16) Border {
 enum { NOT_FOUND = 0, FOUND = 1, NARROWED = 2, BELOW = 3 };
 
 struct Cand {
-    float w, e, x;           // the score is w / e
+    float w, e, x;           // the score is w / e, w and e times the same power of two
     int i;
 };
+
+// e is brought to [1, 2) or near it, so that no product of take() leaves fp32's range
+// where the scores are within it (the weights may go down to 2^-126, and e as far)
+__device__ __forceinline__ Cand cand_of(float w, float e, float x, int i) {
+    const float f = __uint_as_float((254u - min(__float_as_uint(e) >> 23, 253u)) << 23);
+    return Cand{w * f, e * f, x, i};
+}
 
 // The better one: by cross products, lowest index on ties.
 __device__ __forceinline__ void take(Cand& a, const Cand& b) {
@@ -955,7 +962,7 @@ __device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int li
         const bool in = !by_mass || before < target;
         if (in && (by_mass ? target <= before + w[j] : at == limit - 1))
             k.tell(Border{list[at], above + before + w[j], 0, 0, FOUND}, all);
-        if (in && e) take(best, Cand{k.wt.template value<IO>(x[j]), ex[j], x[j], i[j]});
+        if (in && e) take(best, cand_of(k.wt.template value<IO>(x[j]), ex[j], x[j], i[j]));
         before += w[j];
     }
 }
@@ -1066,7 +1073,7 @@ __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const 
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     if (!(x[v] > -INFINITY)) continue;
-                    take(best, Cand{ex2((x[v] - m) * c), ex[v], x[v], i + v});
+                    take(best, cand_of(ex2((x[v] - m) * c), ex[v], x[v], i + v));
                 }
             }
 #pragma unroll

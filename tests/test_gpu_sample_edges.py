@@ -1,6 +1,8 @@
 """Filtered sampling where the filters' passes hand borders on to one another, and
 for rows and numbers at the ends of what the calls accept.  Tolerances are those of
 test_gpu_sample.py."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -81,3 +83,32 @@ def test_cold_caches_of_all_borders():
             binding.token_sample(cfg, x, None, out, ws, **kw)
             n = (out.logits > -np.inf).sum(1).cpu()
             assert [int(n[r]) for r, _ in want] == [w for _, w in want], name
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1000, 60013])
+@pytest.mark.parametrize("k", [0, 100])
+def test_races_between_small_weights(io, V, k):
+    """Tokens whose weights and random numbers are both far below 1: scores 2^20, 2^10
+    and 1, while weight times random number is below fp32's range.  (bf16 rounds the
+    exponents 60 and 100 by at most 2^-9: the scores stay 2^9 apart.)"""
+    x = torch.full((4, V), -150.0)
+    e = torch.ones((4, V))
+    order = [(7, 300, 500), (500, 300, 7), (V - 1, 8, V - 9), (400, V - 2, 3)]
+    for r, (top, low, best) in enumerate(order):
+        x[r, top] = 0.0
+        x[r, best], e[r, best] = -60 * math.log(2.0), 2.0 ** -80
+        x[r, low], e[r, low] = -100 * math.log(2.0), 2.0 ** -110
+    cfg = binding.sample_cfg(4, V, io=io)
+    out, ws = binding.SampleBuffers(cfg), binding.alloc_sample_workspace(cfg)
+    top_k = torch.full((4,), k, dtype=torch.int32, device="cuda")
+    binding.token_sample(cfg, x.cuda().to(DT[io]), e.cuda(), out, ws, top_k=top_k)
+    assert out.tok.tolist() == [best for _, _, best in order]
+    # and at the ends of the range that random numbers have: the largest score wins
+    e = torch.full((4, V), 2.0 ** 126)
+    e[0, 5], e[1, V // 2], e[2, V - 1] = 2.0 ** -126, 2.0 ** -126, float(2.0 ** 125)
+    e[3, :] = float("inf")
+    e[3, 4] = 2.0 ** 127
+    x = torch.zeros((4, V))
+    binding.token_sample(cfg, x.cuda().to(DT[io]), e.cuda(), out, ws, top_k=None)
+    assert out.tok.tolist() == [5, V // 2, V - 1, 4]
