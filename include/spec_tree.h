@@ -694,7 +694,10 @@ enum {
  * for contexts beyond the trained length.  YARN: f_j becomes
  * (1 - g) f_j / factor + g f_j, g = (orig_len f_j / 2 pi - beta_slow) /
  * (beta_fast - beta_slow) held to [0, 1], and the rotated values are multiplied
- * by amp = 0.1 ln(factor) + 1 (1 otherwise). */
+ * by amp = 0.1 ln(factor) + 1 (1 otherwise).  That ramp is the paper's, by the turns
+ * over orig_len; serving code that ramps over j, between the rounded dimensions of
+ * beta_fast and beta_slow, turns by other angles.  For these, and any other scaling,
+ * the table is the caller's: turns[j] = f_j / 2 pi 2^64, modulo 2^64. */
 typedef struct spec_rope_scaling {
     double base;            /* >= 1 */
     double factor;          /* >= 1 (read unless NONE) */

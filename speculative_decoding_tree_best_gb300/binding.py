@@ -9,6 +9,7 @@ fallback, and loading fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import fractions
 import os
 import threading
 from typing import Optional
@@ -873,10 +874,27 @@ _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
+_TWO_PI = fractions.Fraction(62831853071795864769252867665590057683943388, 10 ** 43)
+
+
+def rope_turns_of(frequencies):
+    """The entries of a table (host): radians a position in units of 2^-64 turns, to the
+    nearest one, modulo a turn."""
+    return [round(fractions.Fraction(float(f)) * 2 ** 64 / _TWO_PI) % 2 ** 64
+            for f in frequencies]
+
+
 class RopeTable:
     """A rotation's frequencies on the device (turns int64 [rot/2]: units of 2^-64
     turns a position) and the factor of the rotated values (amp)."""
     __slots__ = ("turns", "amp", "rot", "_ptr", "_dev")
+
+    @classmethod
+    def from_frequencies(cls, frequencies, amp: float = 1.0, device="cuda") -> "RopeTable":
+        """A table of any frequencies f_j (radians a position, rot/2 finite numbers):
+        a model's own list, or a scaling that rope_table does not have."""
+        turns = [t - (1 << 64) if t >> 63 else t for t in rope_turns_of(frequencies)]
+        return cls(torch.tensor(turns, dtype=torch.int64, device=device), amp)
 
     def __init__(self, turns: torch.Tensor, amp: float):
         self.rot = 2 * turns.numel()
@@ -895,7 +913,11 @@ class RopeTable:
 
 def spec_rope_turns(rot: int, base: float = 1e4, scaling: str = "none", factor: float = 1.0,
                     orig_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
-    """(turns, amp) on the host: a list of rot/2 integers in units of 2^-64 turns."""
+    """(turns, amp) on the host: a list of rot/2 integers in units of 2^-64 turns.
+    scaling "none", "linear", "ntk" or "yarn": the paper's, whose ramp goes by the turns
+    over orig_len.  Models whose serving code ramps over the pair's index (between the
+    two dimensions that beta_fast and beta_slow give, rounded) have other angles: give
+    their frequencies to RopeTable.from_frequencies."""
     turns = (ctypes.c_uint64 * max(1, rot // 2))()
     amp = ctypes.c_float(0.0)
     s = SpecRopeScaling(float(base), float(factor), float(beta_fast), float(beta_slow),

@@ -54,3 +54,17 @@ def test_the_farthest_position(lib):  # noqa: F811
             angle = Decimal(((p * got) % 2 ** 64) >> 32) / 2 ** 32
             off = (angle - (p * want / 2 ** 64) % 1 + Decimal("0.5")) % 1 - Decimal("0.5")
             assert -(Decimal(2) ** -32 + Decimal(2) ** -34) <= off <= Decimal(2) ** -34
+
+
+def test_entries_of_given_frequencies(lib):  # noqa: F811
+    """A caller's own frequencies: to the nearest unit, modulo a turn."""
+    f = [1.0, 0.1, 1e4 ** (-31 / 32), -0.1, 0.1 + 40.0, 0.0, 5e-20]
+    with localcontext() as ctx:
+        ctx.prec = 60
+        for got, x in zip(binding.rope_turns_of(f), f):
+            off = (got - Decimal(x) / TWO_PI * 2 ** 64) % 2 ** 64
+            assert min(off, 2 ** 64 - off) <= Decimal("0.50001") and 0 <= got < 2 ** 64
+    # those of a scaling that the library has, up to the rounding of their doubles
+    mine, _ = binding.spec_rope_turns(64, 1e4)
+    for a, b in zip(binding.rope_turns_of([1e4 ** (-j / 32) for j in range(32)]), mine):
+        assert abs(a - b) <= 2 ** 10
