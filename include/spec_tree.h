@@ -806,9 +806,11 @@ size_t spec_sample_workspace_bytes(const spec_sample_cfg *cfg, int num_sms);
  *          before them,
  *   and the first one always stays; p = w / sum of w over what stays;
  *   tok = argmax p / e  (lowest index on ties).
- * Borders are decided on masses of 2^-29 relative accuracy in integers (weights
- * below about 2^-42 of the largest, 2^-(61 - ceil(log2 V)), count as nothing
- * there), so that the result does not depend on the order of summation.
+ * Borders are decided on masses in integers, so that the result does not depend on
+ * the order of summation: a weight is within 2^-29 of itself, rounded down to a
+ * unit of 2^-(61 - ceil(log2 V)) of the largest, and 0 below 2^-42 of that.  A sum
+ * is within 2^-29 of itself and V 2^-min(42, 61 - ceil(log2 V)) of the largest
+ * weight: 2^-24 for V = 2^18, 2^-21 for V = 2^20.
  *   logits [R][V] io; e [R][V] normal floats > 0 (NULL: no token is drawn, out->tok
  *   and out->tok_prob are NULL too); of `out` any may be NULL (tok with tok_prob);
  *   out->logits may be `logits` itself.

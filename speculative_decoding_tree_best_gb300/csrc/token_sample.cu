@@ -39,11 +39,14 @@
 // What bounds it: reading the logits (2 or 4 bytes a token), the random numbers of what
 // stays, writing what is asked for.  Measured (graph replays, V = 151936): one bf16 row
 // 10.5 us, a chain of five exchanges and a sort; 24 fp32 rows with their probabilities
-// 44 us, most of it the rows with a top_p alone (some 60 instructions a token in their
-// histogram, and only their clusters' SMs at work); 216 bf16 rows filtered and written
-// back 76 us, 131 MB at 1.7 TB/s; 256 bf16 rows' nucleus 148 us.
-// The last two are bound by instructions (35 a token, at 40 to 50 % of the issue slots: the CTAs of a cluster wait for one another,
-// and 256 rows are 3.4 rounds of the 76 clusters that fit).
+// 44.5 us, most of it the rows with a top_p alone (one such row 30.8 us; 73 instructions a
+// token over all rows, and only their clusters' SMs at work at the end); 216 bf16 rows
+// filtered and written back 76 us, 131 MB at 1.7 TB/s; 256 bf16 rows without a filter 90
+// us, their nucleus 149.  The last three are bound by instructions (34, 46 and 66 warp
+// instructions for 32 tokens) and by the CTAs of a cluster that wait for one another; 256
+// rows are 3.4 rounds of the 76 clusters that fit.  Every instantiation spills at its 64
+// registers: 136 to 188 bytes stored for clusters of one to four CTAs, 404 and 452 (bf16,
+// fp32) for eight, 800 and 848 for sixteen, most of it border_bin's 16 bytes from each CTA.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -1017,9 +1020,8 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
 // log2 e < log2 w + log2(best.e / best.w); and bits(e) 2^-23 - 127 is at most log2 e
 // (the chord is below the logarithm), which makes the test a multiply-add and an
 // integer comparison, in units of 2^-7.  A group passes it seldom after the first.
-// (256 rows without a filter: 67 million instructions with two products and an
-// exponential a token, 38 million with this test and the filter on two values at once;
-// 103 and 88 us.)
+// (256 rows without a filter: 103 us with two products and an exponential a token, 90
+// with this test and the filter on two values at once, 56 million instructions.)
 template <int IO, int C>
 __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const Kept& kept,
                                      const float* e, Cand& best) {
