@@ -209,16 +209,12 @@ struct Weights {
     int lg;
     const uint2* pow2;           // (2^(29 - j/64) - MAGIC_BITS, 2^(29 - j/64) as a float)
 
-    // the exponent's (m - x) c and what its rounding leaves
-    template <int IO> __device__ __forceinline__ float exponent(float x, float& rest) const {
-        const float d = fminf(m - x, 3.4028234663852886e38f), y = d * c;
+    // the exponent's (m - x) c and what the roundings of both leave (bf16 values too: a
+    // difference of numbers more than 2^16 apart is rounded)
+    __device__ __forceinline__ float exponent(float x, float& rest) const {
+        const float d = fminf(m - x, 3.4028234663852886e38f), y = d * c, b = d - m;
         rest = fmaf(d, c_lo, fmaf(d, c, -y));
-        // bf16 values lie on a coarse grid: their difference is exact where the
-        // smaller is above 2^-16 of the larger, else 2^-24 of it off
-        if constexpr (IO == SPEC_IO_F32) {
-            const float b = d - m;
-            rest = fmaf((m - (d - b)) - (x + b), c, rest);
-        }
+        rest = fmaf((m - (d - b)) - (x + b), c, rest);
         return y;
     }
     // as an integer, of 2^(62 - lg) for the largest, rounded down; without branches, so
@@ -226,10 +222,10 @@ struct Weights {
     // (2^(29 - j/64), rounded) and the rest, under 0.0055, is a cubic whose product with
     // that is rounded by the magic number: 30 bits in all.  (A 62-bit product and a
     // rounded shift: 24 fp32 rows 48.5 us instead of 45.3.)
-    template <int IO> __device__ __forceinline__ u64 fixed(float x) const {
+    __device__ __forceinline__ u64 fixed(float x) const {
         const bool some = m - x <= far;
         float rest;
-        const float y = exponent<IO>(some ? x : m, rest);
+        const float y = exponent(some ? x : m, rest);
         const float n = fmaf(y, 64.0f, MAGIC);                 // rounded to an integer
         const float r = fmaf(n - MAGIC, -0x1p-6f, y) + rest;
         // 2^-r - 1
@@ -241,9 +237,9 @@ struct Weights {
         return some ? (u64)w << 33 >> s : 0;
     }
     // as a float (1 for the largest)
-    template <int IO> __device__ __forceinline__ float value(float x) const {
+    __device__ __forceinline__ float value(float x) const {
         float rest;
-        const float y = exponent<IO>(x, rest);
+        const float y = exponent(x, rest);
         if (!(y < 200.0f)) return 0.0f;
         return ex2(-y) * fmaf(rest, -0.6931471805599453f, 1.0f);
     }
@@ -527,7 +523,7 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
         u64 w[VEC];
         if (KIND == MASSES)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) w[v] = k.wt.template fixed<IO>(x[v]);
+            for (int v = 0; v < VEC; ++v) w[v] = k.wt.fixed(x[v]);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const int b = bin_of<KIND>(top, x[v]);
@@ -549,7 +545,7 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
     u64 near = 0, rest = 0;
     auto look = [&](float x) {
         if (KIND == COUNTS) ++rest;
-        else (bin_of<KIND>(top, x) < END ? near : rest) += k.wt.template fixed<IO>(x);
+        else (bin_of<KIND>(top, x) < END ? near : rest) += k.wt.fixed(x);
     };
     __syncthreads();
     if (sh.odd_ones <= ODD) {
@@ -616,7 +612,7 @@ __device__ __forceinline__ void border_bin(Ctx<C>& k, u64 want, int top) {
         if (KIND != MASSES) f[j] = n[j];
         if (KIND == VALUES) {
             if (from + j == top) f[j] = 0;
-            else if (n[j]) f[j] *= k.wt.template fixed<IO>(step_value(top - from - j));
+            else if (n[j]) f[j] *= k.wt.fixed(step_value(top - from - j));
             if (mine && from + j == top)
                 for (int c = 0; c < C; ++c) f[j] += *k.cl.map_shared_rank(&sh.near_0, c);
         }
@@ -660,7 +656,7 @@ __device__ Border radix(Ctx<C>& k, const Row<IO>& row, const Kept& kept, u64 wan
             const u64 key = key_of(x, i);
             if (key < lo || key > hi || !kept.has(x, i)) return;
             const int bin = (int)((hi - key) >> shift);
-            if (MASS) add_mass(sh, bin, k.wt.template fixed<IO>(x));
+            if (MASS) add_mass(sh, bin, k.wt.fixed(x));
             else atomicAdd(&sh.count[bin], 1u);
         });
         cluster_sync();
@@ -952,7 +948,7 @@ __device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int li
         x[j] = value_of(list[at]);
         i[j] = index_of(list[at]);
         if (e) ex[j] = e[i[j]];
-        w[j] = k.wt.template fixed<IO>(x[j]);
+        w[j] = k.wt.fixed(x[j]);
         s += w[j];
     }
     u64 before = block_prefix(s, sh.part, total);
@@ -965,7 +961,7 @@ __device__ __forceinline__ void solve_list(Ctx<C>& k, const Row<IO>& row, int li
         const bool in = !by_mass || before < target;
         if (in && (by_mass ? target <= before + w[j] : at == limit - 1))
             k.tell(Border{list[at], above + before + w[j], 0, 0, FOUND}, all);
-        if (in && e) take(best, cand_of(k.wt.template value<IO>(x[j]), ex[j], x[j], i[j]));
+        if (in && e) take(best, cand_of(k.wt.value(x[j]), ex[j], x[j], i[j]));
         before += w[j];
     }
 }
@@ -989,7 +985,7 @@ __device__ __forceinline__ void select(Ctx<C>& k, const Row<IO>& row, Kept& kept
         const int bin = (int)b.from, s = top - bin;
         if (IO == SPEC_IO_BF16 && s != 0) {              // one value
             const float v = step_value(s);
-            const u64 w = MASS ? k.wt.template fixed<IO>(v) : 1;
+            const u64 w = MASS ? k.wt.fixed(v) : 1;
             const u64 n = (b.target + w - 1) / w;
             if (MASS) sum = b.sum + n * w;
             if (n < b.tokens) kept = first_ties<IO>(k, row, kept, v, n, sh.count[bin]);
@@ -1326,7 +1322,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
                 if (any) {
 #pragma unroll
                     for (int v = 0; v < VEC; ++v)
-                        w[v] = x[v] > -INFINITY ? wt.template value<IO>(x[v]) * inv : 0.0f;
+                        w[v] = x[v] > -INFINITY ? wt.value(x[v]) * inv : 0.0f;
                 }
                 if (whole) {
 #pragma unroll
@@ -1351,7 +1347,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
             for (int c = 0; c < C; ++c) take(best, sh.cand[c]);
         const bool none = best.i == NO_TOK;
         a.out.tok[r] = none ? 0 : best.i;
-        if (a.out.tok_prob) a.out.tok_prob[r] = none ? 0.0f : wt.template value<IO>(best.x) * inv;
+        if (a.out.tok_prob) a.out.tok_prob[r] = none ? 0.0f : wt.value(best.x) * inv;
     }
 }
 

@@ -112,3 +112,17 @@ def test_races_between_small_weights(io, V, k):
     x = torch.zeros((4, V))
     binding.token_sample(cfg, x.cuda().to(DT[io]), e.cuda(), out, ws, top_k=None)
     assert out.tok.tolist() == [5, V // 2, V - 1, 4]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_logits_far_below_the_largest_in_magnitude(io):
+    """Differences from the largest that round even between bf16 values (22 and
+    numbers of 2^-8 to 2^-20), at temperatures where the exponent is up to 120: a
+    rounding of the difference alone would be 2^-25 of that."""
+    rng = np.random.default_rng(50)
+    V = 5003
+    x = np.exp2(rng.uniform(-20, -8, (5, V))) * rng.choice([-1, 1], (5, V))
+    x[:, 77] = [22.0, 5.5, 21.75, 30.0, 17.0]
+    t = [0.3, 0.1, 0.27, 0.5, 9.0]
+    check(x, io, t=t)
+    check(x, io, t=t, k=[0, 40, 3000, 0, 0], p=[0.9999, 1.0, 1.0, 1.0, 0.7])
