@@ -39,14 +39,14 @@
 // What bounds it: reading the logits (2 or 4 bytes a token), the random numbers of what
 // stays, writing what is asked for.  Measured (graph replays, V = 151936): one bf16 row
 // 10.5 us, a chain of five exchanges and a sort; 24 fp32 rows with their probabilities
-// 44.5 us, most of it the rows with a top_p alone (one such row 30.8 us; 73 instructions a
+// 44 us, most of it the rows with a top_p alone (one such row 30.3 us; 73 instructions a
 // token over all rows, and only their clusters' SMs at work at the end); 216 bf16 rows
 // filtered and written back 76 us, 131 MB at 1.7 TB/s; 256 bf16 rows without a filter 90
-// us, their nucleus 149.  The last three are bound by instructions (34, 46 and 66 warp
+// us, their nucleus 148.  The last three are bound by instructions (34, 46 and 66 warp
 // instructions for 32 tokens) and by the CTAs of a cluster that wait for one another; 256
 // rows are 3.4 rounds of the 76 clusters that fit.  Every instantiation spills at its 64
-// registers: 136 to 188 bytes stored for clusters of one to four CTAs, 404 and 452 (bf16,
-// fp32) for eight, 800 and 848 for sixteen, most of it border_bin's 16 bytes from each CTA.
+// registers: 120 to 176 bytes stored for clusters of one to four CTAs, 432 and 452 (bf16,
+// fp32) for eight, 872 and 860 for sixteen, most of it border_bin's 16 bytes from each CTA.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -122,7 +122,7 @@ __device__ __forceinline__ void take(Cand& a, const Cand& b) {
 
 // A request's parameters, made by one thread (64-bit floating point is slow here).
 struct Params {
-    float c, c_lo, far;      // log2(e) / temperature; see Weights
+    float c, c_lo, far;      // 2 log2(e) / temperature; see Weights
     float min_p;
     double min_low;          // temperature ln(min_p)
     u64 top_p;               // in units of 2^-64; 0: off
@@ -203,19 +203,21 @@ __device__ __forceinline__ u64 key_of(float x, int i) {
 constexpr float MAGIC = 12582912.0f;
 constexpr int MAGIC_BITS = 0x4b400000;
 
-// The softmax's weights of a row: 2^-((m - x) c), c = log2(e) / temperature in two
-// parts.
+// The softmax's weights of a row: 2^-((m - x) / 2 c), c = 2 log2(e) / temperature in two
+// parts.  (Halves, since m - x can leave fp32's range where m and x do not.)
 struct Weights {
-    float m, c, c_lo, far;       // far: weights beyond it are 0 in the sums
+    float m, h, c, c_lo, far;    // h = m / 2; far: weights beyond it are 0 in the sums
     int lg;
     const uint2* pow2;           // (2^(29 - j/64) - MAGIC_BITS, 2^(29 - j/64) as a float)
 
-    // the exponent's (m - x) c and what the roundings of both leave (bf16 values too: a
+    // (m - x) / 2
+    __device__ __forceinline__ float below(float x) const { return fmaf(-0.5f, x, h); }
+    // the exponent below(x) c and what the roundings of both leave (of bf16 values too: a
     // difference of numbers more than 2^16 apart is rounded)
-    __device__ __forceinline__ float exponent(float x, float& rest) const {
-        const float d = fminf(m - x, 3.4028234663852886e38f), y = d * c, b = d - m;
+    __device__ __forceinline__ float exponent(float x, float d, float& rest) const {
+        const float y = d * c, b = d - h;
         rest = fmaf(d, c_lo, fmaf(d, c, -y));
-        rest = fmaf((m - (d - b)) - (x + b), c, rest);
+        rest = fmaf((h - (d - b)) - fmaf(0.5f, x, b), c, rest);
         return y;
     }
     // as an integer, of 2^(62 - lg) for the largest, rounded down; without branches, so
@@ -224,9 +226,10 @@ struct Weights {
     // that is rounded by the magic number: 30 bits in all.  (A 62-bit product and a
     // rounded shift: 24 fp32 rows 48.5 us instead of 45.3.)
     __device__ __forceinline__ u64 fixed(float x) const {
-        const bool some = m - x <= far;
+        const float d = below(x);
+        const bool some = d <= far;
         float rest;
-        const float y = exponent(some ? x : m, rest);
+        const float y = exponent(some ? x : m, some ? d : 0.0f, rest);
         const float n = fmaf(y, 64.0f, MAGIC);                 // rounded to an integer
         const float r = fmaf(n - MAGIC, -0x1p-6f, y) + rest;
         // 2^-r - 1
@@ -240,7 +243,7 @@ struct Weights {
     // as a float (1 for the largest)
     __device__ __forceinline__ float value(float x) const {
         float rest;
-        const float y = exponent(x, rest);
+        const float y = exponent(x, below(x), rest);
         if (!(y < 200.0f)) return 0.0f;
         return ex2(-y) * fmaf(rest, -0.6931471805599453f, 1.0f);
     }
@@ -505,7 +508,7 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
     }
     __syncthreads();
     constexpr int END = KIND == MASSES ? NMASS : NBIN, VEC = Row<IO>::VEC;
-    const float m = k.wt.m, far = k.wt.far;
+    const float far = k.wt.far;
     // Odd ones, seldom there, are noted down for later: below the bins, or near 0
     // (where a bin holds more than one value).  Taken as they came, they made the pass
     // twice as long: the block waits for the warp with most of them.
@@ -538,7 +541,7 @@ __device__ __forceinline__ void bins(Ctx<C>& k, const Row<IO>& row, const Kept& 
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 if (!(x[v] > -INFINITY) || !beside(bin_of<KIND>(top, x[v]))) continue;
-                if (KIND != COUNTS && !(m - x[v] <= far)) continue;      // weighs nothing
+                if (KIND != COUNTS && !(k.wt.below(x[v]) <= far)) continue;      // weighs nothing
                 const uint32_t at = atomicAdd(&sh.odd_ones, 1u);
                 if (at < ODD) sh.odd[at] = x[v];
             }
@@ -1023,7 +1026,7 @@ template <int IO, int C>
 __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const Kept& kept,
                                      const float* e, Cand& best) {
     constexpr int VEC = Row<IO>::VEC;
-    const float m = k.wt.m, c = k.wt.c, c7 = fminf(c * 128.0f, 3.0e38f);
+    const float c = k.wt.c, c7 = fminf(c * 128.0f, 3.0e38f);
     const Filter<IO> filter(kept);
     float bar = 3.0e38f;                                 // everything passes
     // two units above, for the roundings of the test
@@ -1063,7 +1066,7 @@ __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const 
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
                 look |= (__float_as_int(ex[v]) >> 16) + MAGIC_BITS <=
-                        __float_as_int(fmaf(x[v] - m, c7, bar));
+                        __float_as_int(fmaf(-k.wt.below(x[v]), c7, bar));
         }
         if (__any_sync(0xffffffffu, look)) {
             if (look) {
@@ -1072,7 +1075,7 @@ __device__ __forceinline__ void draw(const Ctx<C>& k, const Row<IO>& row, const 
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     if (!(x[v] > -INFINITY)) continue;
-                    take(best, cand_of(ex2((x[v] - m) * c), ex[v], x[v], i + v));
+                    take(best, cand_of(ex2(-k.wt.below(x[v]) * c), ex[v], x[v], i + v));
                 }
             }
 #pragma unroll
@@ -1109,12 +1112,12 @@ __device__ __forceinline__ Params params_of(const spec_sample_params& p, int req
     y.top_p = top_p >= 1.0f ? 0 : max((u64)(fmaxf(top_p, 0.0f) * 0x1p64f), (u64)1);
     y.min_p = min_p;
     if (min_p > 0.0f && min_p < 1.0f) y.min_low = (double)t * log((double)min_p);
-    // log2(e) / t to 2^-46: the quotient's remainder, divided again
-    y.c = fminf(1.4426950216293335f / t, 1e38f);
-    y.c_lo = y.c < 1e38f && t < INFINITY
-                 ? (fmaf(-y.c, t, 1.4426950216293335f) + 1.925963033500011e-8f) / t : 0.0f;
+    // 2 log2(e) / t to 2^-46: the quotient's remainder, divided again
+    y.c = fminf(2.885390043258667f / t, 2e38f);
+    y.c_lo = y.c < 2e38f && t < INFINITY
+                 ? (fmaf(-y.c, t, 2.885390043258667f) + 3.851926067000022e-8f) / t : 0.0f;
     if (t == 0.0f) y.c = y.c_lo = 0.0f;
-    y.far = y.c > 0.0f ? fminf(CUT / y.c, 3.0e38f) : 3.4028234663852886e38f;
+    y.far = y.c > 0.0f ? fminf(CUT / y.c, 3.4028234663852886e38f) : 3.4028234663852886e38f;
     return y;
 }
 
@@ -1225,7 +1228,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
         if (bits && rank == 0 && !idle) raise_status(a.ws, bits);
     }
     __syncthreads();
-    Ctx<C> k{cl, sh, rank, tid, Weights{m, prm.c, prm.c_lo, prm.far, a.lg, sh.pow2}};
+    Ctx<C> k{cl, sh, rank, tid, Weights{m, 0.5f * m, prm.c, prm.c_lo, prm.far, a.lg, sh.pow2}};
     const Weights& wt = k.wt;
 
     // ---- the border
@@ -1279,7 +1282,7 @@ sample_rows(const __grid_constant__ SampleArgs a) {
             Row<IO>::unpack(filter(row.get(g), row.index(g)), x);
 #pragma unroll
             for (int v = 0; v < VEC; ++v)
-                z += x[v] > -INFINITY ? ex2((x[v] - m) * wt.c) : 0.0f;
+                z += x[v] > -INFINITY ? ex2(-wt.below(x[v]) * wt.c) : 0.0f;
         }
         z = warp_sum(z);
         __syncthreads();

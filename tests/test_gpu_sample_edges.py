@@ -126,3 +126,16 @@ def test_logits_far_below_the_largest_in_magnitude(io):
     t = [0.3, 0.1, 0.27, 0.5, 9.0]
     check(x, io, t=t)
     check(x, io, t=t, k=[0, 40, 3000, 0, 0], p=[0.9999, 1.0, 1.0, 1.0, 0.7])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_logits_as_far_apart_as_numbers_go(io):
+    """The largest and the least logit further apart than fp32's largest number, at
+    temperatures of their size: no probability is lost, negative or not a number."""
+    rng = np.random.default_rng(51)
+    V = 1003
+    x = rng.uniform(-3.3e38, 3.3e38, (6, V))
+    x[:, 5], x[:, 700] = 3.38e38, -3.38e38
+    t = [1e37, 5e36, 3.3e38, float("inf"), 1e38, 2e37]
+    check(x, io, t=t)
+    check(x, io, t=t, k=[0, 300, 0, 900, 1000, 2], p=[0.9, 0.97, 0.6, 0.371, 1.0, 0.5])
